@@ -47,7 +47,7 @@ def listed():
         # the same in float32 at odd sizes, with capped logits and a temperature
         _lp("logprobs-train-odd-f32", True, "f32", 257, 515, 5003, 3, 30.0, 1.3, 0.1, "uniform"),
         # the same on a large head
-        _lp("logprobs-train-large", True, "bf16", 4096, 4096, 131072, 0, 0.0, 1.0, 0.25, "zipf"),
+        _lp("logprobs-train-large", True, "bf16", 4096, 4096, 131072, 0, 0.0, 1.0, 0.1, "zipf"),
         # the final norm of one decoding step of 16 sequences
         _norm("norm-decode-16", False, "bf16", 16, 4096, True, 0.0),
         # the final norm of a training batch, forward and backward
