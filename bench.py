@@ -40,7 +40,9 @@ TRAFFIC_FILE = os.path.join(ROOT, "profiles", "hbm_traffic_large_vocab.txt")
 KERNEL_SOURCES = [os.path.join(ROOT, "lm_head_linear_amd", "csrc", f)
                   for f in ("kernels_bf16.hip", "kernels_common.hip", "kernels_f32.hip",
                             "flce_api.hip", "flce_check.cpp", "flce_plan.h", "flce_internal.h",
-                            "gemm_index.h")]
+                            "gemm_index.h", "gemm_bf16.h", "api_util.h", "ops_api.hip",
+                            "ops_check.cpp", "ops_plan.h", "row_io.h", "kernels_norm.hip",
+                            "kernels_embed.hip")]
 
 
 def log(*a):

@@ -385,6 +385,119 @@ int flce_forward_logits(const void* h, const void* W, const int64_t* labels, int
                         void* workspace, size_t workspace_bytes, int32_t* status,
                         float* lse_out, void* logits, int64_t ld_logits, int logits_dtype);
 
+/*
+ * ---- The operators around the head ------------------------------------------
+ * The table W [V,H] that the head multiplies by is also, in a model with tied
+ * embeddings, what its tokens are looked up in, and a norm stands in front of
+ * the head. The following entry points share the conventions above (device
+ * pointers, the caller's stream and workspace, status codes, no allocation, no
+ * wait, capturable). Matrices may have a row stride: ld_x elements between the
+ * rows of x (ld_x >= H). Pointers need the alignment of one element only.
+ */
+
+/*
+ * flce_rms_norm -- root-mean-square norm of N rows of H values, with the
+ * residual's addition:
+ *   s    = round(x + residual)            (residual NULL: s is x, not written)
+ *   rstd = 1 / sqrt(mean_h(s^2) + eps)
+ *   y    = round(s * rstd * (weight + weight_offset))
+ * Sums are float32; x + residual is rounded to the type of the rows once (the
+ * residual stream that the next layer reads), and the norm is of that value.
+ * weight_offset 1 serves weights stored as their distance from one.
+ * x, residual, y, s are of `dtype`; weight is of `weight_dtype`: `dtype`, or
+ * float32 with bf16 rows. rstd [N] (float32, what the backward reads) may be
+ * NULL. In place: y may be x, s may be the residual or x (same pointer and
+ * stride); any other overlap of an output is FLCE_ERR_ARG. N = 0 does nothing.
+ * flce_rms_norm_check_args: FLCE_ERR_ARG for N < 0 or N >= 2^31, H <= 0 or
+ * H > 2^24, unknown types, eps negative or not finite, weight_offset not
+ * finite, a NULL x, y or weight, residual without s or s without residual, a
+ * row stride below H or above 2^31, an overlap; FLCE_ERR_UNSUPPORTED for
+ * float32 rows with bf16 weights, or a pointer not aligned to its elements.
+ */
+int flce_rms_norm_check_args(const void* x, int64_t ld_x, const void* residual, int64_t ld_res,
+                             const void* weight, int64_t N, int64_t H, float eps,
+                             float weight_offset, const void* y, int64_t ld_y, const void* s,
+                             int64_t ld_s, const float* rstd, const void* stream, int dtype,
+                             int weight_dtype);
+int flce_rms_norm(const void* x, int64_t ld_x, const void* residual, int64_t ld_res,
+                  const void* weight, int64_t N, int64_t H, float eps, float weight_offset,
+                  void* y, int64_t ld_y, void* s, int64_t ld_s, float* rstd, void* stream,
+                  int dtype, int weight_dtype);
+
+/*
+ * flce_rms_norm_backward -- with n = s * rstd and g = dy * (weight + offset):
+ *   dx      = round(ds + rstd * (g - n * mean_h(g * n)))
+ *   dweight = round(sum over rows of dy * n)
+ * dx is the gradient of x and of the residual. ds (the gradient that reaches s
+ * itself, from the residual stream) may be NULL: 0. dweight [H] of
+ * weight_dtype may be NULL (not wanted; then no workspace is needed either);
+ * with accumulate_dweight it is added to what is there. dweight is summed in
+ * float32 in a fixed order: the same bits on every run. N = 0 zeroes dweight
+ * unless it accumulates. In place: dx may be dy or ds.
+ * The workspace (256-byte aligned) is flce_rms_norm_backward_workspace_size
+ * bytes, which is 0 for invalid sizes. Errors as flce_rms_norm_check_args, and
+ * FLCE_ERR_WORKSPACE.
+ */
+size_t flce_rms_norm_backward_workspace_size(int64_t N, int64_t H);
+int flce_rms_norm_backward_check_args(const void* dy, int64_t ld_dy, const void* ds, int64_t ld_ds,
+                                      const void* s, int64_t ld_s, const void* weight,
+                                      const float* rstd, int64_t N, int64_t H,
+                                      float weight_offset, const void* dx, int64_t ld_dx,
+                                      const void* dweight, int accumulate_dweight,
+                                      const void* stream, int dtype, int weight_dtype,
+                                      const void* workspace, size_t workspace_bytes);
+int flce_rms_norm_backward(const void* dy, int64_t ld_dy, const void* ds, int64_t ld_ds,
+                           const void* s, int64_t ld_s, const void* weight, const float* rstd,
+                           int64_t N, int64_t H, float weight_offset, void* dx, int64_t ld_dx,
+                           void* dweight, int accumulate_dweight, void* stream, int dtype,
+                           int weight_dtype, void* workspace, size_t workspace_bytes);
+
+/*
+ * flce_embedding -- out[i] = round(scale * W[tokens[i]]) for N token ids; W
+ * [V,H] dense, out [N,H] of the same type. A token equal to padding_index
+ * (which may or may not be an id of the table) gives a row of zeros. A token
+ * that is neither that nor in [0, V) gives a row of NaN and FLCE_ERR_LABEL in
+ * *status (device; NULL = not written); nothing is read out of bounds.
+ * flce_embedding_check_args: FLCE_ERR_ARG for N < 0, N or V > 2^31, H <= 0 or
+ * > 2^24, V <= 0, an unknown type, a scale that is not finite, a NULL W,
+ * tokens or out, a bad row stride, an output that overlaps anything;
+ * FLCE_ERR_UNSUPPORTED for a misaligned pointer or sizes beyond one grid.
+ */
+int flce_embedding_check_args(const int64_t* tokens, const void* W, int64_t N, int64_t H,
+                              int64_t V, int64_t padding_index, float scale, const void* out,
+                              int64_t ld_out, const void* stream, int dtype,
+                              const int32_t* status);
+int flce_embedding(const int64_t* tokens, const void* W, int64_t N, int64_t H, int64_t V,
+                   int64_t padding_index, float scale, void* out, int64_t ld_out, void* stream,
+                   int dtype, int32_t* status);
+
+/*
+ * flce_embedding_backward -- dW[v] (+)= round(scale * sum of dout[i] over the i
+ * with tokens[i] = v). The tokens are sorted (equal ids keep their order) and
+ * each id's rows are summed in float32 in that fixed order: the same bits on
+ * every run. accumulate_dW 0: every row of dW is written (zeros where no token
+ * points); 1: only the rows of tokens that occur are read, added to and
+ * written, at a cost that does not depend on V -- a tied table's gradient,
+ * after the head's. dout is of `dtype`, dW of `grad_dtype`: `dtype`, or float32
+ * with bf16 rows. Tokens equal to padding_index and tokens outside [0, V) add
+ * nothing; the latter also set *status to FLCE_ERR_LABEL. N = 0 zeroes dW
+ * unless it accumulates. The workspace (256-byte aligned) is
+ * flce_embedding_backward_workspace_size bytes (0 for invalid sizes). Errors as
+ * flce_embedding_check_args, and FLCE_ERR_WORKSPACE; float32 rows with a bf16
+ * gradient are FLCE_ERR_UNSUPPORTED.
+ */
+size_t flce_embedding_backward_workspace_size(int64_t N, int64_t H, int64_t V);
+int flce_embedding_backward_check_args(const int64_t* tokens, const void* dout, int64_t ld_dout,
+                                       int64_t N, int64_t H, int64_t V, int64_t padding_index,
+                                       float scale, const void* dW, int accumulate_dW,
+                                       const void* stream, int dtype, int grad_dtype,
+                                       const void* workspace, size_t workspace_bytes,
+                                       const int32_t* status);
+int flce_embedding_backward(const int64_t* tokens, const void* dout, int64_t ld_dout, int64_t N,
+                            int64_t H, int64_t V, int64_t padding_index, float scale, void* dW,
+                            int accumulate_dW, void* stream, int dtype, int grad_dtype,
+                            void* workspace, size_t workspace_bytes, int32_t* status);
+
 /* flce_status_string -- a static, human-readable name for a status code
  * (this library's own addition; no page defines status codes). */
 const char* flce_status_string(int status);

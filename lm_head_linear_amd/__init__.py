@@ -33,6 +33,13 @@ from typing import Optional
 import torch
 
 from . import _lib
+from ._ops import (  # noqa: F401
+    flce_embedding, flce_embedding_backward, flce_embedding_backward_check_args,
+    flce_embedding_backward_workspace_size, flce_embedding_check_args, flce_rms_norm,
+    flce_rms_norm_backward, flce_rms_norm_backward_check_args,
+    flce_rms_norm_backward_workspace_size, flce_rms_norm_check_args, fused_embedding,
+    fused_rms_norm)
+from ._util import FlceError, _check_tensor, _dtype_code, _ptr, flce_status_string
 
 __all__ = [
     "flce_workspace_size",
@@ -52,6 +59,18 @@ __all__ = [
     "flce_forward_logits",
     "flce_forward_logits_check_args",
     "flce_forward_noalloc",
+    "flce_rms_norm",
+    "flce_rms_norm_check_args",
+    "flce_rms_norm_backward",
+    "flce_rms_norm_backward_check_args",
+    "flce_rms_norm_backward_workspace_size",
+    "flce_embedding",
+    "flce_embedding_check_args",
+    "flce_embedding_backward",
+    "flce_embedding_backward_check_args",
+    "flce_embedding_backward_workspace_size",
+    "fused_rms_norm",
+    "fused_embedding",
     "flce_status_string",
     "flce_vocab_chunk",
     "flce_kept_chunks",
@@ -69,34 +88,12 @@ __all__ = [
 ]
 
 
-class FlceError(RuntimeError):
-    def __init__(self, code: int, where: str = ""):
-        self.code = code
-        super().__init__(f"{where}: {flce_status_string(code)}" if where else flce_status_string(code))
-
-
-def _dtype_code(dt: torch.dtype) -> int:
-    if dt == torch.bfloat16:
-        return _lib.BF16
-    if dt == torch.float32:
-        return _lib.F32
-    raise ValueError(f"unsupported dtype {dt}; use torch.bfloat16 or torch.float32")
-
-
 def _red_code(reduction: str) -> int:
     if reduction == "sum":
         return _lib.SUM
     if reduction == "mean":
         return _lib.MEAN
     raise ValueError(f"reduction must be 'sum' or 'mean', got {reduction!r}")
-
-
-def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
-    return None if t is None else t.data_ptr()
-
-
-def flce_status_string(code: int) -> str:
-    return _lib.load().flce_status_string(int(code)).decode()
 
 
 def flce_workspace_size(N: int, H: int, V: int, dtype: torch.dtype,
@@ -212,17 +209,6 @@ def flce_forward_logits_check_args(h, W, labels, *, N, H, V, logits, ld_logits=N
     ld = V if ld_logits is None else int(ld_logits)
     return int(_lib.load().flce_forward_logits_check_args(*args, _ptr(logits), ld,
                                                           _dtype_code(logits_dtype)))
-
-
-def _check_tensor(name, t, shape, dtype, device):
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
 
 
 def flce_forward_backward(h: torch.Tensor, W: torch.Tensor, labels: torch.Tensor, *,

@@ -20,6 +20,13 @@ _FB_ARGS = [_vp, _vp, _vp, _i64, _i64, _i64, _i64, _f32, _i32, _i64, _vp, _vp, _
             _vp, _i32, _f32, _i32, _vp, _sz, _vp, _vp]
 _F_ARGS = [_vp, _vp, _vp, _i64, _i64, _i64, _i64, _f32, _i32, _i64, _vp, _vp, _vp, _i32,
            _f32, _vp, _sz, _vp, _vp]
+_NORM = [_vp, _i64, _vp, _i64, _vp, _i64, _i64, _f32, _f32, _vp, _i64, _vp, _i64, _vp, _vp,
+         _i32, _i32]
+_NORM_BWD = [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _f32, _vp, _i64, _vp, _i32,
+             _vp, _i32, _i32, _vp, _sz]
+_EMBED = [_vp, _vp, _i64, _i64, _i64, _i64, _f32, _vp, _i64, _vp, _i32, _vp]
+_EMBED_BWD = [_vp, _vp, _i64, _i64, _i64, _i64, _i64, _f32, _vp, _i32, _vp, _i32, _i32, _vp, _sz,
+              _vp]
 SIGNATURES = {
     "flce_workspace_size": (_sz, [_i64, _i64, _i64, _i32]),
     "flce_check_args": (_i32, _FB_ARGS),
@@ -39,6 +46,16 @@ SIGNATURES = {
                                     _vp, _vp, _vp, _i32, _f32, _vp, _vp]),
     "flce_forward_logits_check_args": (_i32, _F_ARGS + [_vp, _i64, _i32]),
     "flce_forward_logits": (_i32, _F_ARGS + [_vp, _i64, _i32]),
+    "flce_rms_norm_check_args": (_i32, _NORM),
+    "flce_rms_norm": (_i32, _NORM),
+    "flce_rms_norm_backward_workspace_size": (_sz, [_i64, _i64]),
+    "flce_rms_norm_backward_check_args": (_i32, _NORM_BWD),
+    "flce_rms_norm_backward": (_i32, _NORM_BWD),
+    "flce_embedding_check_args": (_i32, _EMBED),
+    "flce_embedding": (_i32, _EMBED),
+    "flce_embedding_backward_workspace_size": (_sz, [_i64, _i64, _i64]),
+    "flce_embedding_backward_check_args": (_i32, _EMBED_BWD),
+    "flce_embedding_backward": (_i32, _EMBED_BWD),
     "flce_status_string": (_c.c_char_p, [_i32]),
     "flce_vocab_chunk": (_i64, [_i64, _i64, _i64, _i32]),
     "flce_kept_chunks": (_i64, [_i64, _i64, _i64, _i32, _i32]),

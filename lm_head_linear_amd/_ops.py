@@ -1,0 +1,317 @@
+"""The operators around the head: the norm in front of it and the lookup in the
+table it shares with the embedding (see include/flce.h for the contracts).
+
+Like the head's own bindings these only marshal arguments. Matrices may be views
+with a row stride (unit stride along a row); outputs and workspaces may be passed
+in, so that a call allocates nothing.
+"""
+from __future__ import annotations
+
+from typing import Optional
+
+import torch
+
+from . import _lib
+from ._util import FlceError, _check_tensor, _dtype_code, _ptr
+
+
+def _rows(name, t, N, H, dtype, dev):
+    """Checks an [N, H] matrix with unit stride along its rows; its row stride."""
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 2 or t.shape[0] != N or t.shape[1] != H:
+        raise ValueError(f"{name} must have shape {(N, H)}, got {tuple(t.shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    if N == 0 or (H == 1 and N == 1):
+        return H
+    if H > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have unit stride along its rows")
+    if N == 1:
+        return H
+    if t.stride(0) < H:
+        raise ValueError(f"{name} must not have overlapping rows (row stride {t.stride(0)})")
+    return t.stride(0)
+
+
+def _on_gpu(where, dev):
+    if dev.type != "cuda":
+        raise ValueError(f"{where} runs on a GPU; tensors are on {dev}")
+
+
+def _run(where, dev, fn, *args):
+    with torch.cuda.device(dev):
+        rc = fn(*args)
+    if rc != _lib.OK:
+        raise FlceError(rc, where)
+
+
+def _bytes(t):
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def _workspace(ws, need, dev):
+    return torch.empty(need, dtype=torch.uint8, device=dev) if _bytes(ws) < need else ws
+
+
+# ---- root-mean-square norm -----------------------------------------------------------
+
+
+def flce_rms_norm_check_args(x, weight, residual=None, *, N, H, ld_x=None, ld_res=None, eps=1e-6,
+                             weight_offset=0.0, y=None, ld_y=None, s=None, ld_s=None, rstd=None,
+                             dtype=torch.bfloat16, weight_dtype=None) -> int:
+    """The norm's synchronous checks (no GPU work); a status code."""
+    ld = lambda v: H if v is None else int(v)  # noqa: E731
+    return int(_lib.load().flce_rms_norm_check_args(
+        _ptr(x), ld(ld_x), _ptr(residual), ld(ld_res), _ptr(weight), N, H, float(eps),
+        float(weight_offset), _ptr(y), ld(ld_y), _ptr(s), ld(ld_s), _ptr(rstd), None,
+        _dtype_code(dtype), _dtype_code(weight_dtype or dtype)))
+
+
+def flce_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None,
+                  *, eps: float = 1e-6, weight_offset: float = 0.0,
+                  y: Optional[torch.Tensor] = None, s: Optional[torch.Tensor] = None,
+                  rstd: Optional[torch.Tensor] = None):
+    """RMS norm of the rows of x [N, H], after adding the residual: (y, s, rstd).
+
+    s = x + residual rounded to the rows' type (x itself without a residual),
+    y = s * rstd * (weight + weight_offset). weight [H] has the rows' type, or
+    float32 with bf16 rows. ``y`` may be x and ``s`` the residual (in place).
+    """
+    if x.dim() != 2:
+        raise ValueError("x must be [N, H]")
+    N, H = x.shape
+    dev, dt = x.device, x.dtype
+    _on_gpu("flce_rms_norm", dev)
+    code, wcode = _dtype_code(dt), _dtype_code(weight.dtype)
+    _check_tensor("weight", weight, (H,), weight.dtype, dev)
+    ld_x, ld_r, ld_s = _rows("x", x, N, H, dt, dev), H, H
+    if y is None:
+        y = torch.empty(N, H, dtype=dt, device=dev)
+    if rstd is None:
+        rstd = torch.empty(N, dtype=torch.float32, device=dev)
+    else:
+        _check_tensor("rstd", rstd, (N,), torch.float32, dev)
+    if residual is not None:
+        ld_r = _rows("residual", residual, N, H, dt, dev)
+        if s is None:
+            s = torch.empty(N, H, dtype=dt, device=dev)
+        ld_s = _rows("s", s, N, H, dt, dev)
+    elif s is not None:
+        raise ValueError("s is written only with a residual")
+    _run("flce_rms_norm", dev, _lib.load().flce_rms_norm, x.data_ptr(), ld_x, _ptr(residual), ld_r,
+         weight.data_ptr(), N, H, float(eps), float(weight_offset), y.data_ptr(),
+         _rows("y", y, N, H, dt, dev), _ptr(s), ld_s, rstd.data_ptr(),
+         torch.cuda.current_stream(dev).cuda_stream, code, wcode)
+    return y, x if residual is None else s, rstd
+
+
+def flce_rms_norm_backward_workspace_size(N: int, H: int) -> int:
+    return int(_lib.load().flce_rms_norm_backward_workspace_size(N, H))
+
+
+def flce_rms_norm_backward_check_args(dy, s, weight, rstd, ds=None, *, N, H, ld_dy=None,
+                                      ld_ds=None, ld_s=None, weight_offset=0.0, dx=None,
+                                      ld_dx=None, dweight=None, accumulate_dweight=False,
+                                      dtype=torch.bfloat16, weight_dtype=None,
+                                      workspace=None) -> int:
+    """The norm's backward's synchronous checks (no GPU work); a status code."""
+    ld = lambda v: H if v is None else int(v)  # noqa: E731
+    return int(_lib.load().flce_rms_norm_backward_check_args(
+        _ptr(dy), ld(ld_dy), _ptr(ds), ld(ld_ds), _ptr(s), ld(ld_s), _ptr(weight), _ptr(rstd), N,
+        H, float(weight_offset), _ptr(dx), ld(ld_dx), _ptr(dweight), int(bool(accumulate_dweight)),
+        None, _dtype_code(dtype), _dtype_code(weight_dtype or dtype), _ptr(workspace),
+        _bytes(workspace)))
+
+
+def flce_rms_norm_backward(dy: torch.Tensor, s: torch.Tensor, weight: torch.Tensor,
+                           rstd: torch.Tensor, ds: Optional[torch.Tensor] = None, *,
+                           weight_offset: float = 0.0, dx: Optional[torch.Tensor] = None,
+                           dweight: Optional[torch.Tensor] = None, want_dweight: bool = True,
+                           accumulate_dweight: bool = False,
+                           workspace: Optional[torch.Tensor] = None):
+    """Gradients of :func:`flce_rms_norm`: (dx, dweight).
+
+    dx is the gradient of x and of the residual alike; ``ds`` is the gradient
+    that reaches s itself. dweight is None unless wanted (``want_dweight``) and
+    is added to the tensor passed in with ``accumulate_dweight``.
+    """
+    if dy.dim() != 2:
+        raise ValueError("dy must be [N, H]")
+    N, H = dy.shape
+    dev, dt = dy.device, dy.dtype
+    _on_gpu("flce_rms_norm_backward", dev)
+    code, wcode = _dtype_code(dt), _dtype_code(weight.dtype)
+    _check_tensor("weight", weight, (H,), weight.dtype, dev)
+    _check_tensor("rstd", rstd, (N,), torch.float32, dev)
+    ld_dy, ld_s = _rows("dy", dy, N, H, dt, dev), _rows("s", s, N, H, dt, dev)
+    ld_ds = H if ds is None else _rows("ds", ds, N, H, dt, dev)
+    if dx is None:
+        dx = torch.empty(N, H, dtype=dt, device=dev)
+    if accumulate_dweight and dweight is None:
+        raise ValueError("accumulate_dweight needs the dweight tensor to add to")
+    if dweight is not None:
+        _check_tensor("dweight", dweight, (H,), weight.dtype, dev)
+    elif want_dweight:
+        dweight = torch.empty(H, dtype=weight.dtype, device=dev)
+    if dweight is not None:
+        workspace = _workspace(workspace, flce_rms_norm_backward_workspace_size(N, H), dev)
+    _run("flce_rms_norm_backward", dev, _lib.load().flce_rms_norm_backward, dy.data_ptr(), ld_dy,
+         _ptr(ds), ld_ds, s.data_ptr(), ld_s, weight.data_ptr(), rstd.data_ptr(), N, H,
+         float(weight_offset), dx.data_ptr(), _rows("dx", dx, N, H, dt, dev), _ptr(dweight),
+         int(bool(accumulate_dweight)), torch.cuda.current_stream(dev).cuda_stream, code, wcode,
+         _ptr(workspace), _bytes(workspace))
+    return dx, dweight
+
+
+class _RMSNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, residual, eps, weight_offset):
+        shape = x.shape
+        flat = lambda t: None if t is None else t.reshape(-1, shape[-1])  # noqa: E731
+        y, s, rstd = flce_rms_norm(flat(x), weight, flat(residual), eps=eps,
+                                   weight_offset=weight_offset)
+        ctx.save_for_backward(s, weight, rstd)
+        ctx.weight_offset = weight_offset
+        ctx.has_residual = residual is not None
+        ctx.set_materialize_grads(False)
+        if residual is None:
+            return y.view(shape)
+        return y.view(shape), s.view(shape)
+
+    @staticmethod
+    def backward(ctx, dy, ds=None):
+        s, weight, rstd = ctx.saved_tensors
+        if dy is None:                       # only the sum was used
+            return ds, None, ds if ctx.has_residual else None, None, None
+        shape = dy.shape
+        rows = lambda t: t.contiguous().view(-1, shape[-1])  # noqa: E731
+        dx, dw = flce_rms_norm_backward(
+            rows(dy), s, weight, rstd, None if ds is None else rows(ds),
+            weight_offset=ctx.weight_offset, want_dweight=ctx.needs_input_grad[1])
+        dx = dx.view(shape)
+        return dx, dw, dx if ctx.has_residual else None, None, None
+
+
+def fused_rms_norm(x: torch.Tensor, weight: torch.Tensor,
+                   residual: Optional[torch.Tensor] = None, *, eps: float = 1e-6,
+                   weight_offset: float = 0.0):
+    """RMS norm of x [..., H] with gradients; with a residual, (y, x + residual).
+
+    The gradients of x and of the residual are the same tensor of values: both
+    inputs enter through their sum.
+    """
+    return _RMSNorm.apply(x, weight.contiguous(), residual, float(eps), float(weight_offset))
+
+
+# ---- embedding -----------------------------------------------------------------------
+
+
+def flce_embedding_check_args(tokens, W, *, N, H, V, padding_index=-100, scale=1.0, out=None,
+                              ld_out=None, dtype=torch.bfloat16, status=None) -> int:
+    """The lookup's synchronous checks (no GPU work); a status code."""
+    return int(_lib.load().flce_embedding_check_args(
+        _ptr(tokens), _ptr(W), N, H, V, int(padding_index), float(scale), _ptr(out),
+        H if ld_out is None else int(ld_out), None, _dtype_code(dtype), _ptr(status)))
+
+
+def flce_embedding(tokens: torch.Tensor, W: torch.Tensor, *, scale: float = 1.0,
+                   padding_index: int = -100, out: Optional[torch.Tensor] = None,
+                   status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """out[i] = scale * W[tokens[i]] (rounded once) for int64 tokens [N], W [V, H].
+
+    A token equal to ``padding_index`` gives zeros; one outside [0, V) gives NaN
+    (and FLCE_ERR_LABEL in ``status``, a device int32).
+    """
+    if W.dim() != 2 or tokens.dim() != 1:
+        raise ValueError("tokens must be [N] and W [V, H]")
+    (V, H), N = W.shape, tokens.shape[0]
+    dev = W.device
+    _on_gpu("flce_embedding", dev)
+    code = _dtype_code(W.dtype)
+    _check_tensor("tokens", tokens, (N,), torch.int64, dev)
+    _check_tensor("W", W, (V, H), W.dtype, dev)
+    if status is not None:
+        _check_tensor("status", status, (), torch.int32, dev)
+    if out is None:
+        out = torch.empty(N, H, dtype=W.dtype, device=dev)
+    _run("flce_embedding", dev, _lib.load().flce_embedding, tokens.data_ptr(), W.data_ptr(), N, H,
+         V, int(padding_index), float(scale), out.data_ptr(), _rows("out", out, N, H, W.dtype, dev),
+         torch.cuda.current_stream(dev).cuda_stream, code, _ptr(status))
+    return out
+
+
+def flce_embedding_backward_workspace_size(N: int, H: int, V: int) -> int:
+    return int(_lib.load().flce_embedding_backward_workspace_size(N, H, V))
+
+
+def flce_embedding_backward_check_args(tokens, dout, *, N, H, V, dW, ld_dout=None,
+                                       padding_index=-100, scale=1.0, accumulate_dW=False,
+                                       dtype=torch.bfloat16, grad_dtype=None, workspace=None,
+                                       status=None) -> int:
+    """The lookup's gradient's synchronous checks (no GPU work); a status code."""
+    return int(_lib.load().flce_embedding_backward_check_args(
+        _ptr(tokens), _ptr(dout), H if ld_dout is None else int(ld_dout), N, H, V,
+        int(padding_index), float(scale), _ptr(dW), int(bool(accumulate_dW)), None,
+        _dtype_code(dtype), _dtype_code(grad_dtype or dtype), _ptr(workspace), _bytes(workspace),
+        _ptr(status)))
+
+
+def flce_embedding_backward(tokens: torch.Tensor, dout: torch.Tensor, V: int, *,
+                            scale: float = 1.0, padding_index: int = -100,
+                            dW: Optional[torch.Tensor] = None, accumulate_dW: bool = False,
+                            grad_dtype: Optional[torch.dtype] = None,
+                            workspace: Optional[torch.Tensor] = None,
+                            status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The table's gradient of :func:`flce_embedding`: dW [V, H].
+
+    dW[v] = scale * (sum of dout[i] over tokens[i] == v), summed in float32 in the
+    tokens' order. With ``accumulate_dW`` it is added to the dW passed in (the
+    head's gradient of a tied table): only the rows of the tokens are touched.
+    """
+    if dout.dim() != 2 or tokens.dim() != 1:
+        raise ValueError("tokens must be [N] and dout [N, H]")
+    N, H = dout.shape
+    dev, dt = dout.device, dout.dtype
+    _on_gpu("flce_embedding_backward", dev)
+    gdt = grad_dtype if grad_dtype is not None else dt if dW is None else dW.dtype
+    code, gcode = _dtype_code(dt), _dtype_code(gdt)
+    _check_tensor("tokens", tokens, (N,), torch.int64, dev)
+    ld = _rows("dout", dout, N, H, dt, dev)
+    if dW is None:
+        if accumulate_dW:
+            raise ValueError("accumulate_dW needs the dW tensor to add to")
+        dW = torch.empty(V, H, dtype=gdt, device=dev)
+    _check_tensor("dW", dW, (V, H), gdt, dev)
+    if status is not None:
+        _check_tensor("status", status, (), torch.int32, dev)
+    workspace = _workspace(workspace, flce_embedding_backward_workspace_size(N, H, V), dev)
+    _run("flce_embedding_backward", dev, _lib.load().flce_embedding_backward, tokens.data_ptr(),
+         dout.data_ptr(), ld, N, H, V, int(padding_index), float(scale), dW.data_ptr(),
+         int(bool(accumulate_dW)), torch.cuda.current_stream(dev).cuda_stream, code, gcode,
+         workspace.data_ptr(), _bytes(workspace), _ptr(status))
+    return dW
+
+
+class _Embedding(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, tokens, W, scale, padding_index):
+        flat = tokens.reshape(-1).contiguous()
+        out = flce_embedding(flat, W, scale=scale, padding_index=padding_index)
+        ctx.save_for_backward(flat)
+        ctx.args = (W.shape[0], scale, padding_index)
+        return out.view(*tokens.shape, W.shape[1])
+
+    @staticmethod
+    def backward(ctx, dout):
+        (tokens,) = ctx.saved_tensors
+        V, scale, padding_index = ctx.args
+        dW = flce_embedding_backward(tokens, dout.contiguous().view(-1, dout.shape[-1]), V,
+                                     scale=scale, padding_index=padding_index)
+        return None, dW, None, None
+
+
+def fused_embedding(tokens: torch.Tensor, W: torch.Tensor, *, scale: float = 1.0,
+                    padding_index: int = -100) -> torch.Tensor:
+    """scale * W[tokens] for tokens of any shape, with the table's gradient."""
+    return _Embedding.apply(tokens, W.contiguous(), float(scale), int(padding_index))

@@ -12,8 +12,9 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libflce.so")
 
-HIP_SOURCES = ["flce_api.hip", "kernels_common.hip", "kernels_bf16.hip", "kernels_f32.hip"]
-CXX_SOURCES = ["flce_check.cpp"]
+HIP_SOURCES = ["flce_api.hip", "kernels_common.hip", "kernels_bf16.hip", "kernels_f32.hip",
+               "ops_api.hip", "kernels_norm.hip", "kernels_embed.hip"]
+CXX_SOURCES = ["flce_check.cpp", "ops_check.cpp"]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [

@@ -1,30 +1,20 @@
 // C-ABI entry points: argument checks, workspace carving, launch sequence,
 // optional per-kernel timing.
 #include <hip/hip_runtime.h>
-#include <rocprofiler-sdk-roctx/roctx.h>
 
 #include <cstdint>
 #include <mutex>
 #include <vector>
 
 #include "../../include/flce.h"
+#include "api_util.h"
 #include "flce_internal.h"
 #include "flce_plan.h"
 #include "gemm_index.h"
 
 namespace {
 
-// ---- ROCTX ranges -------------------------------------------------------------
-// A named range around each entry point's call and each pass it enqueues
-// (forward, merge, one per backward chunk or token chunk), for a profiler's
-// marker trace (rocprofv3 --marker-trace). They span the host-side enqueue of
-// the pass; the kernel trace gives the device times.
-struct Range {
-  explicit Range(const char* name) { roctxRangePushA(name); }
-  ~Range() { roctxRangePop(); }
-  Range(const Range&) = delete;
-  Range& operator=(const Range&) = delete;
-};
+using flce::Range;
 
 // ---- per-kernel timing ------------------------------------------------------
 struct Rec {
@@ -71,7 +61,9 @@ void prof_after(int kind, hipStream_t s) {
 const char* kKindNames[flce::kNumKinds] = {"label_scan", "lse_fwd_gemm", "lse_merge",
                                            "loss_final", "grad_logits_gemm", "dW_gemm",
                                            "dH_gemm", "fill", "probs_to_grad", "dH_reduce",
-                                           "gather", "dH_dW_gemm", "pad_copy"};
+                                           "gather", "dH_dW_gemm", "pad_copy", "rms_norm",
+                                           "rms_norm_bwd", "embed", "embed_sort",
+                                           "embed_grad"};
 
 // ---- scratch of flce_forward_noalloc ---------------------------------------
 // One copy on every GPU the library runs on, held until the process ends. In
@@ -162,8 +154,7 @@ int run_nr(const void* h, const void* W, const int64_t* labels, int64_t N, int64
            int64_t token_chunk) {
   flce::Plan p;
   if (!flce::make_plan_nr(N, H, V, dtype, token_chunk, &p)) return FLCE_ERR_UNSUPPORTED;
-  flce::Launcher L{static_cast<hipStream_t>(stream), nullptr, nullptr};
-  if (g_prof.on) { L.before = prof_before; L.after = prof_after; }
+  const flce::Launcher L = flce::make_launcher(stream);
   char* ws = static_cast<char*>(workspace);
   flce::Args a{};
   a.h = h; a.W = W; a.labels = labels;
@@ -229,8 +220,7 @@ int run(const void* h, const void* W, const int64_t* labels, int64_t N, int64_t 
   flce::Plan p;
   if (!flce::make_plan(N, H, V, dtype, &p, backward, grad_dtype, gather)) return FLCE_ERR_ARG;
 
-  flce::Launcher L{static_cast<hipStream_t>(stream), nullptr, nullptr};
-  if (g_prof.on) { L.before = prof_before; L.after = prof_after; }
+  const flce::Launcher L = flce::make_launcher(stream);
 
   char* ws = static_cast<char*>(workspace);
   flce::Args a{};
@@ -293,6 +283,12 @@ int run(const void* h, const void* W, const int64_t* labels, int64_t N, int64_t 
 }
 
 }  // namespace
+
+flce::Launcher flce::make_launcher(void* stream) {
+  Launcher L{static_cast<hipStream_t>(stream), nullptr, nullptr};
+  if (g_prof.on) { L.before = prof_before; L.after = prof_after; }
+  return L;
+}
 
 extern "C" {
 

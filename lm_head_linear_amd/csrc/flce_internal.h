@@ -24,7 +24,12 @@ enum Kind : int {
   kGather = 10,
   kGemmDWDH = 11,     // dH's tiles and then dW's, in one grid
   kPadCopy = 12,      // row copies of a call at a padded hidden width
-  kNumKinds = 13,
+  kNorm = 13,
+  kNormBwd = 14,
+  kEmbed = 15,
+  kEmbedSort = 16,
+  kEmbedGrad = 17,
+  kNumKinds = 18,
 };
 
 // Everything one call needs on the device side.
@@ -108,6 +113,9 @@ hipError_t launch_merge_gathered(const Plan& p, const Args& a, int64_t t0, int64
 // bf16 MFMA path.
 hipError_t bf16_forward(const Plan& p, const Args& a, const Launcher& L);
 hipError_t bf16_backward_chunk(const Plan& p, const Args& a, int64_t chunk, const Launcher& L);
+// The products of vocabulary chunk `chunk` of a compact plan once its G (a.g)
+// is formed: dW[chunk] and the chunk's share of dH.
+hipError_t bf16_chunk_products(const Plan& p, const Args& a, int64_t chunk, const Launcher& L);
 // No-recompute variant, token chunk c: the forward that keeps the
 // probabilities, then (after the chunk's merge) G in place and dW, dH.
 hipError_t bf16_nr_forward_chunk(const Plan& p, const Args& a, int64_t c, const Launcher& L);

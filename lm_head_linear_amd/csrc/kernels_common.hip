@@ -509,18 +509,20 @@ hipError_t launch_copy_rows(const void* src, int64_t ld_src, void* dst, int64_t 
 
 hipError_t launch_zero_bytes(void* ptr, size_t bytes, const Launcher& L) {
   if (bytes == 0) return hipSuccess;
+  // 16-byte stores for an aligned buffer, its last bytes one by one
+  const bool aligned = (reinterpret_cast<uintptr_t>(ptr) & 15u) == 0;
+  const int64_t n16 = aligned ? int64_t(bytes / 16) : 0;
+  const int64_t rest = int64_t(bytes) - n16 * 16;
   L.pre(kFill);
-  if ((reinterpret_cast<uintptr_t>(ptr) & 15u) == 0 && (bytes & 15u) == 0) {
-    const int64_t n16 = int64_t(bytes / 16);
-    int64_t blocks = (n16 + 255) / 256;
-    if (blocks > 4096) blocks = 4096;
-    hipLaunchKernelGGL(k_zero16, dim3(unsigned(blocks)), dim3(256), 0, L.stream,
-                       reinterpret_cast<uint4*>(ptr), n16);
-  } else {
-    int64_t blocks = (int64_t(bytes) + 255) / 256;
-    if (blocks > 4096) blocks = 4096;
-    hipLaunchKernelGGL(k_zero1, dim3(unsigned(blocks)), dim3(256), 0, L.stream,
-                       reinterpret_cast<unsigned char*>(ptr), int64_t(bytes));
+  if (n16 > 0) {
+    const int64_t blocks = (n16 + 255) / 256;
+    hipLaunchKernelGGL(k_zero16, dim3(unsigned(blocks < 4096 ? blocks : 4096)), dim3(256), 0,
+                       L.stream, reinterpret_cast<uint4*>(ptr), n16);
+  }
+  if (rest > 0) {
+    const int64_t blocks = (rest + 255) / 256;
+    hipLaunchKernelGGL(k_zero1, dim3(unsigned(blocks < 4096 ? blocks : 4096)), dim3(256), 0,
+                       L.stream, static_cast<unsigned char*>(ptr) + n16 * 16, rest);
   }
   L.post(kFill);
   return hipGetLastError();

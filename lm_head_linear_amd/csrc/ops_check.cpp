@@ -1,0 +1,208 @@
+// Synchronous argument checks and workspace plans of the operators around the
+// head's loss (no HIP calls).
+#include "ops_plan.h"
+
+#include <cmath>
+#include <initializer_list>
+
+#include "../../include/flce.h"
+
+namespace flce {
+namespace {
+
+constexpr int64_t kMaxRows = int64_t(1) << 31, kMaxWidth = int64_t(1) << 24;
+constexpr int64_t kMaxGrid = (int64_t(1) << 31) - 1;
+
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+bool is_dtype(int d) { return d == FLCE_F32 || d == FLCE_BF16; }
+size_t esize(int d) { return d == FLCE_BF16 ? 2 : 4; }
+
+// A buffer of a call: [rows][cols] elements of es bytes, ld apart.
+struct Buf {
+  const void* p;
+  int64_t rows, cols, ld;
+  size_t es;
+  bool none() const { return !p || rows <= 0 || cols <= 0; }
+  uintptr_t begin() const { return reinterpret_cast<uintptr_t>(p); }
+  uintptr_t end() const { return begin() + (size_t(rows - 1) * size_t(ld) + size_t(cols)) * es; }
+};
+Buf matrix(const void* p, int64_t rows, int64_t cols, int64_t ld, size_t es) {
+  return Buf{p, rows, cols, ld, es};
+}
+Buf vec(const void* p, int64_t n, size_t es) { return Buf{p, 1, n, n, es}; }
+
+bool overlap(const Buf& a, const Buf& b) {
+  return !a.none() && !b.none() && a.begin() < b.end() && b.begin() < a.end();
+}
+bool same(const Buf& a, const Buf& b) {
+  return a.p == b.p && a.ld == b.ld && a.es == b.es;
+}
+// Row strides: at least a row, and no size that leaves 64 bits.
+bool bad_ld(int64_t ld, int64_t cols) { return ld < cols || ld > (int64_t(1) << 31); }
+bool misaligned(const Buf& b) { return !b.none() && b.begin() % b.es != 0; }
+
+// The outputs overlap neither each other nor an input.
+bool clash(std::initializer_list<Buf> outs, std::initializer_list<Buf> ins) {
+  for (const Buf* a = outs.begin(); a != outs.end(); ++a) {
+    for (const Buf* b = a + 1; b != outs.end(); ++b)
+      if (overlap(*a, *b)) return true;
+    for (const Buf& b : ins)
+      if (overlap(*a, b)) return true;
+  }
+  return false;
+}
+
+}  // namespace
+
+bool make_embed_plan(int64_t N, int64_t H, int64_t V, EmbedPlan* p) {
+  if (N < 0 || H <= 0 || V <= 0) return false;
+  if (N > kMaxRows || H > kMaxWidth || V > kMaxRows) return false;
+  EmbedPlan q;
+  // 32 sorted tokens a wave; more for very many tokens, so that an id that
+  // fills many windows leaves at most about as many partial rows as a window
+  // has tokens
+  q.window = 32;
+  while (q.window < 4096 && q.window * q.window * 32 < N) q.window *= 2;
+  const int64_t windows = ceil_div(N, q.window), blocks = ceil_div(N, kSortBlock);
+  const size_t list = align256(size_t(N) * sizeof(uint32_t));
+  const int lists = N <= kSortLocal ? 1 : 2;
+  size_t off = 0;
+  for (int i = 0; i < lists; ++i) {
+    q.off_key[i] = off; off += list;
+    q.off_pos[i] = off; off += list;
+  }
+  if (lists == 2) { q.off_hist = off; off = align256(off + size_t(256 * blocks) * 4); }
+  if (windows > 1) { q.off_part = off; off = align256(off + size_t(2 * windows) * H * 4); }
+  q.total = off > 0 ? off : 256;
+  *p = q;
+  return true;
+}
+
+}  // namespace flce
+
+using namespace flce;
+
+extern "C" {
+
+int flce_rms_norm_check_args(const void* x, int64_t ld_x, const void* residual, int64_t ld_res,
+                             const void* weight, int64_t N, int64_t H, float eps,
+                             float weight_offset, const void* y, int64_t ld_y, const void* s,
+                             int64_t ld_s, const float* rstd, const void* stream, int dtype,
+                             int weight_dtype) {
+  (void)stream;
+  if (N < 0 || H <= 0 || !is_dtype(dtype) || !is_dtype(weight_dtype)) return FLCE_ERR_ARG;
+  if (N > kMaxGrid || H > kMaxWidth) return FLCE_ERR_ARG;
+  if (!(eps >= 0.f) || !std::isfinite(eps) || !std::isfinite(weight_offset)) return FLCE_ERR_ARG;
+  if (!weight || (N > 0 && (!x || !y))) return FLCE_ERR_ARG;
+  if ((residual != nullptr) != (s != nullptr) && N > 0) return FLCE_ERR_ARG;
+  if (bad_ld(ld_x, H) || bad_ld(ld_y, H)) return FLCE_ERR_ARG;
+  if (residual && (bad_ld(ld_res, H) || bad_ld(ld_s, H))) return FLCE_ERR_ARG;
+  const size_t es = esize(dtype), ws = esize(weight_dtype);
+  const Buf bx = matrix(x, N, H, ld_x, es), by = matrix(y, N, H, ld_y, es),
+            br = matrix(residual, N, H, ld_res, es), bs = matrix(s, N, H, ld_s, es),
+            bw = vec(weight, H, ws), bq = vec(rstd, N, 4);
+  // in place: y may be x (then s may not), s may be the residual or x
+  if (overlap(by, bx) && !same(by, bx)) return FLCE_ERR_ARG;
+  if (overlap(bs, bx) && !same(bs, bx)) return FLCE_ERR_ARG;
+  if (overlap(bs, br) && !same(bs, br)) return FLCE_ERR_ARG;
+  if (overlap(by, br) || overlap(by, bs)) return FLCE_ERR_ARG;
+  if (overlap(bw, by) || overlap(bw, bs)) return FLCE_ERR_ARG;
+  if (clash({bq}, {bx, br, by, bs, bw})) return FLCE_ERR_ARG;
+  if (dtype == FLCE_F32 && weight_dtype != FLCE_F32) return FLCE_ERR_UNSUPPORTED;
+  for (const Buf& b : {bx, by, br, bs, bw, bq})
+    if (misaligned(b)) return FLCE_ERR_UNSUPPORTED;
+  return FLCE_OK;
+}
+
+size_t flce_rms_norm_backward_workspace_size(int64_t N, int64_t H) {
+  if (N < 0 || H <= 0 || N > kMaxGrid || H > kMaxWidth) return 0;
+  const size_t n = align256(size_t(norm_shares(N)) * size_t(H) * 4);
+  return n ? n : 256;
+}
+
+int flce_rms_norm_backward_check_args(const void* dy, int64_t ld_dy, const void* ds, int64_t ld_ds,
+                                      const void* s, int64_t ld_s, const void* weight,
+                                      const float* rstd, int64_t N, int64_t H,
+                                      float weight_offset, const void* dx, int64_t ld_dx,
+                                      const void* dweight, int accumulate_dweight,
+                                      const void* stream, int dtype, int weight_dtype,
+                                      const void* workspace, size_t workspace_bytes) {
+  (void)stream; (void)accumulate_dweight;
+  if (N < 0 || H <= 0 || !is_dtype(dtype) || !is_dtype(weight_dtype)) return FLCE_ERR_ARG;
+  if (N > kMaxGrid || H > kMaxWidth || !std::isfinite(weight_offset)) return FLCE_ERR_ARG;
+  if (!weight || (N > 0 && (!dy || !s || !rstd || !dx))) return FLCE_ERR_ARG;
+  if (bad_ld(ld_dy, H) || bad_ld(ld_s, H) || bad_ld(ld_dx, H)) return FLCE_ERR_ARG;
+  if (ds && bad_ld(ld_ds, H)) return FLCE_ERR_ARG;
+  const size_t es = esize(dtype), ws = esize(weight_dtype);
+  const Buf by = matrix(dy, N, H, ld_dy, es), bd = matrix(ds, N, H, ld_ds, es),
+            bs = matrix(s, N, H, ld_s, es), bw = vec(weight, H, ws), bq = vec(rstd, N, 4),
+            bx = matrix(dx, N, H, ld_dx, es), bdw = vec(dweight, H, ws),
+            wk = vec(dweight ? workspace : nullptr, int64_t(workspace_bytes), 1);
+  // in place: dx may be dy or ds
+  if (overlap(bx, by) && !same(bx, by)) return FLCE_ERR_ARG;
+  if (overlap(bx, bd) && !same(bx, bd)) return FLCE_ERR_ARG;
+  if (clash({bx}, {bs, bw, bq, bdw, wk})) return FLCE_ERR_ARG;
+  if (clash({bdw}, {by, bd, bs, bw, bq, wk})) return FLCE_ERR_ARG;
+  if (clash({wk}, {by, bd, bs, bw, bq})) return FLCE_ERR_ARG;
+  if (dtype == FLCE_F32 && weight_dtype != FLCE_F32) return FLCE_ERR_UNSUPPORTED;
+  for (const Buf& b : {by, bd, bs, bw, bq, bx, bdw})
+    if (misaligned(b)) return FLCE_ERR_UNSUPPORTED;
+  if (dweight) {
+    if (!workspace || wk.begin() % 256 != 0) return FLCE_ERR_WORKSPACE;
+    if (workspace_bytes < flce_rms_norm_backward_workspace_size(N, H)) return FLCE_ERR_WORKSPACE;
+  }
+  return FLCE_OK;
+}
+
+int flce_embedding_check_args(const int64_t* tokens, const void* W, int64_t N, int64_t H,
+                              int64_t V, int64_t padding_index, float scale, const void* out,
+                              int64_t ld_out, const void* stream, int dtype,
+                              const int32_t* status) {
+  (void)stream; (void)padding_index;
+  if (N < 0 || H <= 0 || V <= 0 || !is_dtype(dtype) || !std::isfinite(scale)) return FLCE_ERR_ARG;
+  EmbedPlan p;
+  if (!make_embed_plan(N, H, V, &p) || bad_ld(ld_out, H)) return FLCE_ERR_ARG;
+  if (!W || (N > 0 && (!tokens || !out))) return FLCE_ERR_ARG;
+  const size_t es = esize(dtype);
+  const Buf bt = vec(tokens, N, 8), bw = matrix(W, V, H, H, es),
+            bo = matrix(out, N, H, ld_out, es), bst = vec(status, 1, 4);
+  if (clash({bo, bst}, {bt, bw})) return FLCE_ERR_ARG;
+  if (ceil_div(N * ceil_div(H * int64_t(es), 2048), 4) > kMaxGrid) return FLCE_ERR_UNSUPPORTED;
+  for (const Buf& b : {bt, bw, bo, bst})
+    if (misaligned(b)) return FLCE_ERR_UNSUPPORTED;
+  return FLCE_OK;
+}
+
+size_t flce_embedding_backward_workspace_size(int64_t N, int64_t H, int64_t V) {
+  EmbedPlan p;
+  return make_embed_plan(N, H, V, &p) ? p.total : 0;
+}
+
+int flce_embedding_backward_check_args(const int64_t* tokens, const void* dout, int64_t ld_dout,
+                                       int64_t N, int64_t H, int64_t V, int64_t padding_index,
+                                       float scale, const void* dW, int accumulate_dW,
+                                       const void* stream, int dtype, int grad_dtype,
+                                       const void* workspace, size_t workspace_bytes,
+                                       const int32_t* status) {
+  (void)stream; (void)padding_index; (void)accumulate_dW;
+  if (N < 0 || H <= 0 || V <= 0 || !is_dtype(dtype) || !is_dtype(grad_dtype)) return FLCE_ERR_ARG;
+  EmbedPlan p;
+  if (!std::isfinite(scale) || !make_embed_plan(N, H, V, &p) || bad_ld(ld_dout, H))
+    return FLCE_ERR_ARG;
+  if (!dW || (N > 0 && (!tokens || !dout))) return FLCE_ERR_ARG;
+  const Buf bt = vec(tokens, N, 8), bd = matrix(dout, N, H, ld_dout, esize(dtype)),
+            bw = matrix(dW, V, H, H, esize(grad_dtype)), bst = vec(status, 1, 4),
+            wk = vec(workspace, int64_t(workspace_bytes), 1);
+  if (clash({bw, bst, wk}, {bt, bd})) return FLCE_ERR_ARG;
+  if (dtype == FLCE_F32 && grad_dtype == FLCE_BF16) return FLCE_ERR_UNSUPPORTED;
+  if (ceil_div(ceil_div(N, p.window) * ceil_div(H, 512), 4) > kMaxGrid)
+    return FLCE_ERR_UNSUPPORTED;
+  for (const Buf& b : {bt, bd, bw, bst})
+    if (misaligned(b)) return FLCE_ERR_UNSUPPORTED;
+  if (!workspace || wk.begin() % 256 != 0 || workspace_bytes < p.total) return FLCE_ERR_WORKSPACE;
+  return FLCE_OK;
+}
+
+}  // extern "C"
