@@ -498,6 +498,86 @@ int flce_embedding_backward(const int64_t* tokens, const void* dout, int64_t ld_
                             int accumulate_dW, void* stream, int dtype, int grad_dtype,
                             void* workspace, size_t workspace_bytes, int32_t* status);
 
+/*
+ * flce_logprobs -- log probabilities of given tokens under the head, with the
+ * entropy and the top alternatives of each position, for scoring, policy
+ * gradients and serving. With z = h . W^T, z' the softcapped logit and
+ * x = z' / temperature:
+ *   lse_i     = log sum_v exp(x_iv)
+ *   logp_i    = x_{i,tokens_i} - lse_i
+ *   entropy_i = -sum_v p_iv log p_iv,  p = exp(x - lse)      (in nats)
+ *   top_ids[i][k], top_logp[i][k]: the top_k tokens of highest logit, best
+ *     first, equal logits by lowest id, and their log probabilities
+ * Everything is float32 (ids int64) [N] or [N][top_k]; sums and logits are
+ * float32 and no logit is stored in device memory. Alternatives are ranked by z
+ * (the order of x without ties made by rounding); where fewer than top_k logits
+ * exist above -inf the rest is id -1, value -inf. NaN logits are not ranked.
+ * tokens [N] int64 may be NULL (no given tokens: logp must be NULL too);
+ * entropy, lse, status may be NULL; top_logp and top_ids are NULL exactly when
+ * top_k is 0 (at most FLCE_MAX_TOP).
+ * A row whose token equals ignore_index is left out of the work: logp, entropy
+ * and lse 0, ids -1, top_logp -inf. A row whose token is neither that nor in
+ * [0, V) gets logp NaN and sets *status to FLCE_ERR_LABEL; its other outputs do
+ * not depend on the token.
+ * bf16 inputs with N <= 64 run a kernel that reads W once at the memory's rate;
+ * more run the head's matrix-core tiles over the live rows.
+ * The workspace (256-byte aligned) is flce_logprobs_workspace_size bytes: the
+ * partials and candidates of up to 8192 tokens at a time, the gathered rows, and
+ * padded copies for a bf16 H that is not a multiple of 8 and N > 64.
+ * flce_logprobs_check_args: FLCE_ERR_ARG for sizes as in flce_check_args, top_k
+ * outside [0, FLCE_MAX_TOP], softcap negative or not finite, temperature not
+ * positive, not finite or without a finite inverse, a missing or contradicting
+ * pointer, an output that overlaps an input, another output or the workspace;
+ * FLCE_ERR_UNSUPPORTED for a bf16 matrix that is not 16-byte aligned (any other
+ * pointer: its element), FLCE_ERR_WORKSPACE.
+ */
+#define FLCE_MAX_TOP 32
+size_t flce_logprobs_workspace_size(int64_t N, int64_t H, int64_t V, int dtype, int top_k);
+int flce_logprobs_check_args(const void* h, const void* W, const int64_t* tokens, int64_t N,
+                             int64_t H, int64_t V, int64_t ignore_index, float softcap,
+                             float temperature, int top_k, const float* logp,
+                             const float* entropy, const float* lse, const float* top_logp,
+                             const int64_t* top_ids, const void* stream, int dtype,
+                             const void* workspace, size_t workspace_bytes,
+                             const int32_t* status);
+int flce_logprobs(const void* h, const void* W, const int64_t* tokens, int64_t N, int64_t H,
+                  int64_t V, int64_t ignore_index, float softcap, float temperature, int top_k,
+                  float* logp, float* entropy, float* lse, float* top_logp, int64_t* top_ids,
+                  void* stream, int dtype, void* workspace, size_t workspace_bytes,
+                  int32_t* status);
+
+/*
+ * flce_logprobs_backward -- dH and dW for upstream gradients a = grad_logp and
+ * b = grad_entropy ([N] float32, either may be NULL: zero; not both):
+ *   dL/dx_iv = a_i ([v = tokens_i] - p_iv) - b_i p_iv (log p_iv + entropy_i)
+ *   G = dL/dx * dz'/dz / temperature,  dH = G . W,  dW (+)= G^T . h
+ * from the lse and (with grad_entropy) the entropy that flce_logprobs returned
+ * for the same h, W, softcap and temperature. The logits are recomputed chunk by
+ * chunk; G is rounded to bf16 once for bf16 inputs (kept as a bf16 pair with
+ * grad_dtype FLCE_F32), the products are those of flce_forward_backward, and so
+ * are accumulate_dW and grad_dtype. Ignored rows give dH rows of zeros; a token
+ * outside [0, V) gives NaN in its dH row and in dW, and FLCE_ERR_LABEL in
+ * *status. The same bits on every run. N = 0 zeroes dW unless it accumulates.
+ * The workspace (256-byte aligned) is flce_logprobs_backward_workspace_size
+ * bytes (0 for invalid sizes). Errors as flce_logprobs_check_args.
+ */
+size_t flce_logprobs_backward_workspace_size(int64_t N, int64_t H, int64_t V, int dtype,
+                                             int grad_dtype);
+int flce_logprobs_backward_check_args(const void* h, const void* W, const int64_t* tokens,
+                                      const float* lse, const float* entropy,
+                                      const float* grad_logp, const float* grad_entropy,
+                                      int64_t N, int64_t H, int64_t V, int64_t ignore_index,
+                                      float softcap, float temperature, const void* dH,
+                                      const void* dW, int accumulate_dW, const void* stream,
+                                      int dtype, int grad_dtype, const void* workspace,
+                                      size_t workspace_bytes, const int32_t* status);
+int flce_logprobs_backward(const void* h, const void* W, const int64_t* tokens, const float* lse,
+                           const float* entropy, const float* grad_logp,
+                           const float* grad_entropy, int64_t N, int64_t H, int64_t V,
+                           int64_t ignore_index, float softcap, float temperature, void* dH,
+                           void* dW, int accumulate_dW, void* stream, int dtype, int grad_dtype,
+                           void* workspace, size_t workspace_bytes, int32_t* status);
+
 /* flce_status_string -- a static, human-readable name for a status code
  * (this library's own addition; no page defines status codes). */
 const char* flce_status_string(int status);

@@ -34,11 +34,15 @@ import torch
 
 from . import _lib
 from ._ops import (  # noqa: F401
+    TokenLogprobs,
     flce_embedding, flce_embedding_backward, flce_embedding_backward_check_args,
-    flce_embedding_backward_workspace_size, flce_embedding_check_args, flce_rms_norm,
+    flce_embedding_backward_workspace_size, flce_embedding_check_args, flce_logprobs,
+    flce_logprobs_backward, flce_logprobs_backward_check_args,
+    flce_logprobs_backward_workspace_size, flce_logprobs_check_args,
+    flce_logprobs_workspace_size, flce_rms_norm,
     flce_rms_norm_backward, flce_rms_norm_backward_check_args,
     flce_rms_norm_backward_workspace_size, flce_rms_norm_check_args, fused_embedding,
-    fused_rms_norm)
+    fused_rms_norm, token_logprobs)
 from ._util import FlceError, _check_tensor, _dtype_code, _ptr, flce_status_string
 
 __all__ = [
@@ -59,6 +63,15 @@ __all__ = [
     "flce_forward_logits",
     "flce_forward_logits_check_args",
     "flce_forward_noalloc",
+    "flce_logprobs",
+    "flce_logprobs_check_args",
+    "flce_logprobs_workspace_size",
+    "flce_logprobs_backward",
+    "flce_logprobs_backward_check_args",
+    "flce_logprobs_backward_workspace_size",
+    "token_logprobs",
+    "TokenLogprobs",
+    "TiedLMHead",
     "flce_rms_norm",
     "flce_rms_norm_check_args",
     "flce_rms_norm_backward",
@@ -562,3 +575,51 @@ class FusedLinearCrossEntropy(torch.nn.Module):
             num_label_tokens=num_label_tokens, mb_scale=mb_scale)
         self.num_tokens = n
         return loss
+
+
+class TiedLMHead(torch.nn.Module):
+    """The two ends of a language model around one table W [V, H]: the embedding
+    of its tokens, the final norm, and the head's loss or log probabilities.
+
+    ``embed(tokens)`` looks tokens up (times ``embed_scale``); the model's layers
+    run between; ``loss(x, labels, residual)`` and ``logprobs(x, tokens,
+    residual)`` add the residual, normalise (norm_eps, norm_weight + weight_offset)
+    and run the head. W's gradient is the sum of the embedding's and the head's.
+    """
+
+    def __init__(self, vocab_size: int, hidden_size: int, *, ignore_index: int = -100,
+                 logit_softcapping: float = 0.0, reduction: str = "sum", embed_scale: float = 1.0,
+                 norm_eps: float = 1e-6, weight_offset: float = 0.0, device=None, dtype=None):
+        super().__init__()
+        kw = dict(device=device, dtype=dtype)
+        self.weight = torch.nn.Parameter(torch.randn(vocab_size, hidden_size, **kw) * 0.02)
+        self.norm_weight = torch.nn.Parameter(
+            torch.full((hidden_size,), 1.0 - weight_offset, **kw))
+        self.criterion = FusedLinearCrossEntropy(ignore_index, logit_softcapping, reduction)
+        self.embed_scale = float(embed_scale)
+        self.norm_eps = float(norm_eps)
+        self.weight_offset = float(weight_offset)
+
+    def embed(self, tokens: torch.Tensor) -> torch.Tensor:
+        """embed_scale * W[tokens]; a token equal to ignore_index gives zeros."""
+        return fused_embedding(tokens, self.weight, scale=self.embed_scale,
+                               padding_index=self.criterion.ignore_index)
+
+    def norm(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None) -> torch.Tensor:
+        out = fused_rms_norm(x, self.norm_weight, residual, eps=self.norm_eps,
+                             weight_offset=self.weight_offset)
+        return out if residual is None else out[0]
+
+    def loss(self, x: torch.Tensor, labels: torch.Tensor,
+             residual: Optional[torch.Tensor] = None, **kw) -> torch.Tensor:
+        """The head's loss (:class:`FusedLinearCrossEntropy`) of the normalised rows."""
+        return self.criterion(self.norm(x, residual), labels, self.weight, **kw)
+
+    def logprobs(self, x: torch.Tensor, tokens: Optional[torch.Tensor] = None,
+                 residual: Optional[torch.Tensor] = None, *, temperature: float = 1.0,
+                 top_k: int = 0) -> TokenLogprobs:
+        """:func:`token_logprobs` of the normalised rows."""
+        return token_logprobs(self.norm(x, residual), tokens, self.weight,
+                              ignore_index=self.criterion.ignore_index,
+                              softcap=self.criterion.logit_softcapping, temperature=temperature,
+                              top_k=top_k)

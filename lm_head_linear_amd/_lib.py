@@ -12,6 +12,8 @@ SUM, MEAN = 0, 1
 OK, ERR_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_HIP, ERR_LABEL, ERR_SCRATCH = range(7)
 # bytes of the fixed scratch array behind flce_forward_noalloc (FLCE_NOALLOC_SCRATCH_BYTES)
 NOALLOC_SCRATCH_BYTES = 96 << 20
+# most alternatives of flce_logprobs (FLCE_MAX_TOP)
+MAX_TOP = 32
 
 # Every symbol the header declares, with its ctypes signature.
 _c = ctypes
@@ -27,6 +29,10 @@ _NORM_BWD = [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _f32, _vp, _
 _EMBED = [_vp, _vp, _i64, _i64, _i64, _i64, _f32, _vp, _i64, _vp, _i32, _vp]
 _EMBED_BWD = [_vp, _vp, _i64, _i64, _i64, _i64, _i64, _f32, _vp, _i32, _vp, _i32, _i32, _vp, _sz,
               _vp]
+_LP = [_vp, _vp, _vp, _i64, _i64, _i64, _i64, _f32, _f32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _i32,
+       _vp, _sz, _vp]
+_LP_BWD = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _f32, _f32, _vp, _vp, _i32,
+           _vp, _i32, _i32, _vp, _sz, _vp]
 SIGNATURES = {
     "flce_workspace_size": (_sz, [_i64, _i64, _i64, _i32]),
     "flce_check_args": (_i32, _FB_ARGS),
@@ -56,6 +62,12 @@ SIGNATURES = {
     "flce_embedding_backward_workspace_size": (_sz, [_i64, _i64, _i64]),
     "flce_embedding_backward_check_args": (_i32, _EMBED_BWD),
     "flce_embedding_backward": (_i32, _EMBED_BWD),
+    "flce_logprobs_workspace_size": (_sz, [_i64, _i64, _i64, _i32, _i32]),
+    "flce_logprobs_check_args": (_i32, _LP),
+    "flce_logprobs": (_i32, _LP),
+    "flce_logprobs_backward_workspace_size": (_sz, [_i64, _i64, _i64, _i32, _i32]),
+    "flce_logprobs_backward_check_args": (_i32, _LP_BWD),
+    "flce_logprobs_backward": (_i32, _LP_BWD),
     "flce_status_string": (_c.c_char_p, [_i32]),
     "flce_vocab_chunk": (_i64, [_i64, _i64, _i64, _i32]),
     "flce_kept_chunks": (_i64, [_i64, _i64, _i64, _i32, _i32]),

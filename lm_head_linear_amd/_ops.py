@@ -7,7 +7,7 @@ in, so that a call allocates nothing.
 """
 from __future__ import annotations
 
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -315,3 +315,199 @@ def fused_embedding(tokens: torch.Tensor, W: torch.Tensor, *, scale: float = 1.0
                     padding_index: int = -100) -> torch.Tensor:
     """scale * W[tokens] for tokens of any shape, with the table's gradient."""
     return _Embedding.apply(tokens, W.contiguous(), float(scale), int(padding_index))
+
+
+# ---- token log probabilities ---------------------------------------------------------
+
+
+class TokenLogprobs(NamedTuple):
+    """What :func:`flce_logprobs` returns; logp is None without given tokens, the
+    alternatives are [N, 0] with top_k = 0."""
+    logp: Optional[torch.Tensor]
+    entropy: torch.Tensor
+    lse: torch.Tensor
+    top_logp: torch.Tensor
+    top_ids: torch.Tensor
+
+
+def flce_logprobs_workspace_size(N: int, H: int, V: int, dtype: torch.dtype,
+                                 top_k: int = 0) -> int:
+    return int(_lib.load().flce_logprobs_workspace_size(N, H, V, _dtype_code(dtype), int(top_k)))
+
+
+def flce_logprobs_check_args(h, W, tokens=None, *, N, H, V, ignore_index=-100, softcap=0.0,
+                             temperature=1.0, top_k=0, logp=None, entropy=None, lse=None,
+                             top_logp=None, top_ids=None, dtype=torch.bfloat16, workspace=None,
+                             status=None) -> int:
+    """The log probabilities' synchronous checks (no GPU work); a status code."""
+    return int(_lib.load().flce_logprobs_check_args(
+        _ptr(h), _ptr(W), _ptr(tokens), N, H, V, int(ignore_index), float(softcap),
+        float(temperature), int(top_k), _ptr(logp), _ptr(entropy), _ptr(lse), _ptr(top_logp),
+        _ptr(top_ids), None, _dtype_code(dtype), _ptr(workspace), _bytes(workspace),
+        _ptr(status)))
+
+
+def _out(name, t, shape, dtype, dev):
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _check_tensor(name, t, shape, dtype, dev)
+    return t
+
+
+def flce_logprobs(h: torch.Tensor, W: torch.Tensor, tokens: Optional[torch.Tensor] = None, *,
+                  ignore_index: int = -100, softcap: float = 0.0, temperature: float = 1.0,
+                  top_k: int = 0, logp: Optional[torch.Tensor] = None,
+                  entropy: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                  top_logp: Optional[torch.Tensor] = None,
+                  top_ids: Optional[torch.Tensor] = None,
+                  workspace: Optional[torch.Tensor] = None,
+                  status: Optional[torch.Tensor] = None) -> TokenLogprobs:
+    """Log probabilities of tokens [N] under the head W [V, H] at h [N, H].
+
+    Also each position's entropy (nats), log-sum-exp and ``top_k`` (at most 32)
+    best alternatives, by logit and then by lowest id. Rows whose token is
+    ``ignore_index`` are left out: 0, and ids -1 with -inf. Without ``tokens``
+    every row counts and ``logp`` is None. Nothing is synchronised.
+    """
+    if h.dim() != 2 or W.dim() != 2:
+        raise ValueError("h must be [N, H] and W [V, H]")
+    (N, H), V = h.shape, W.shape[0]
+    dev = W.device
+    _on_gpu("flce_logprobs", dev)
+    code, f32 = _dtype_code(W.dtype), torch.float32
+    _check_tensor("h", h, (N, H), W.dtype, dev)
+    _check_tensor("W", W, (V, H), W.dtype, dev)
+    top_k = int(top_k)
+    if not 0 <= top_k <= _lib.MAX_TOP:
+        raise ValueError(f"top_k must be 0 to {_lib.MAX_TOP}, got {top_k}")
+    if tokens is not None:
+        _check_tensor("tokens", tokens, (N,), torch.int64, dev)
+        logp = _out("logp", logp, (N,), f32, dev)
+    elif logp is not None:
+        raise ValueError("logp needs tokens")
+    entropy = _out("entropy", entropy, (N,), f32, dev)
+    lse = _out("lse", lse, (N,), f32, dev)
+    top_logp = _out("top_logp", top_logp, (N, top_k), f32, dev)
+    top_ids = _out("top_ids", top_ids, (N, top_k), torch.int64, dev)
+    if status is not None:
+        _check_tensor("status", status, (), torch.int32, dev)
+    lib = _lib.load()
+    need = lib.flce_logprobs_workspace_size(N, H, V, code, top_k)
+    workspace = _workspace(workspace, need, dev)
+    _run("flce_logprobs", dev, lib.flce_logprobs, h.data_ptr(), W.data_ptr(), _ptr(tokens), N, H,
+         V, int(ignore_index), float(softcap), float(temperature), top_k, _ptr(logp),
+         entropy.data_ptr(), lse.data_ptr(), top_logp.data_ptr() if top_k else None,
+         top_ids.data_ptr() if top_k else None, torch.cuda.current_stream(dev).cuda_stream, code,
+         workspace.data_ptr(), _bytes(workspace), _ptr(status))
+    return TokenLogprobs(logp, entropy, lse, top_logp, top_ids)
+
+
+def flce_logprobs_backward_workspace_size(N: int, H: int, V: int, dtype: torch.dtype,
+                                          grad_dtype: Optional[torch.dtype] = None) -> int:
+    return int(_lib.load().flce_logprobs_backward_workspace_size(
+        N, H, V, _dtype_code(dtype), _dtype_code(grad_dtype or dtype)))
+
+
+def flce_logprobs_backward_check_args(h, W, tokens, lse, entropy=None, grad_logp=None,
+                                      grad_entropy=None, *, N, H, V, ignore_index=-100,
+                                      softcap=0.0, temperature=1.0, dH=None, dW=None,
+                                      accumulate_dW=False, dtype=torch.bfloat16, grad_dtype=None,
+                                      workspace=None, status=None) -> int:
+    """The log probabilities' backward's synchronous checks; a status code."""
+    return int(_lib.load().flce_logprobs_backward_check_args(
+        _ptr(h), _ptr(W), _ptr(tokens), _ptr(lse), _ptr(entropy), _ptr(grad_logp),
+        _ptr(grad_entropy), N, H, V, int(ignore_index), float(softcap), float(temperature),
+        _ptr(dH), _ptr(dW), int(bool(accumulate_dW)), None, _dtype_code(dtype),
+        _dtype_code(grad_dtype or dtype), _ptr(workspace), _bytes(workspace), _ptr(status)))
+
+
+def flce_logprobs_backward(h: torch.Tensor, W: torch.Tensor, tokens: torch.Tensor,
+                           lse: torch.Tensor, entropy: Optional[torch.Tensor],
+                           grad_logp: Optional[torch.Tensor],
+                           grad_entropy: Optional[torch.Tensor] = None, *,
+                           ignore_index: int = -100, softcap: float = 0.0,
+                           temperature: float = 1.0, dH: Optional[torch.Tensor] = None,
+                           dW: Optional[torch.Tensor] = None, accumulate_dW: bool = False,
+                           grad_dtype: Optional[torch.dtype] = None,
+                           workspace: Optional[torch.Tensor] = None,
+                           status: Optional[torch.Tensor] = None):
+    """(dH, dW) of :func:`flce_logprobs` for the gradients of logp and entropy.
+
+    ``lse`` and (with ``grad_entropy``) ``entropy`` are what the forward returned
+    for the same inputs and options.
+    """
+    if h.dim() != 2 or W.dim() != 2:
+        raise ValueError("h must be [N, H] and W [V, H]")
+    (N, H), V = h.shape, W.shape[0]
+    dev = W.device
+    _on_gpu("flce_logprobs_backward", dev)
+    gdt = W.dtype if grad_dtype is None else grad_dtype
+    code, gcode = _dtype_code(W.dtype), _dtype_code(gdt)
+    _check_tensor("h", h, (N, H), W.dtype, dev)
+    _check_tensor("W", W, (V, H), W.dtype, dev)
+    _check_tensor("tokens", tokens, (N,), torch.int64, dev)
+    for name, t in (("lse", lse), ("entropy", entropy), ("grad_logp", grad_logp),
+                    ("grad_entropy", grad_entropy)):
+        if t is not None:
+            _check_tensor(name, t, (N,), torch.float32, dev)
+    dH = _out("dH", dH, (N, H), gdt, dev)
+    if dW is None and accumulate_dW:
+        raise ValueError("accumulate_dW needs the dW tensor to add to")
+    dW = _out("dW", dW, (V, H), gdt, dev)
+    if status is not None:
+        _check_tensor("status", status, (), torch.int32, dev)
+    lib = _lib.load()
+    need = lib.flce_logprobs_backward_workspace_size(N, H, V, code, gcode)
+    if need == 0:
+        raise FlceError(_lib.ERR_UNSUPPORTED if W.dtype == torch.float32 else _lib.ERR_ARG,
+                        "flce_logprobs_backward_workspace_size")
+    workspace = _workspace(workspace, need, dev)
+    _run("flce_logprobs_backward", dev, lib.flce_logprobs_backward, h.data_ptr(), W.data_ptr(),
+         tokens.data_ptr(), lse.data_ptr(), _ptr(entropy), _ptr(grad_logp), _ptr(grad_entropy), N,
+         H, V, int(ignore_index), float(softcap), float(temperature), dH.data_ptr(),
+         dW.data_ptr(), int(bool(accumulate_dW)), torch.cuda.current_stream(dev).cuda_stream, code,
+         gcode, workspace.data_ptr(), _bytes(workspace), _ptr(status))
+    return dH, dW
+
+
+class _TokenLogprobs(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, h, W, tokens, ignore_index, softcap, temperature, top_k):
+        out = flce_logprobs(h, W, tokens, ignore_index=ignore_index, softcap=softcap,
+                            temperature=temperature, top_k=top_k)
+        ctx.save_for_backward(h, W, tokens, out.lse, out.entropy)
+        ctx.kw = dict(ignore_index=ignore_index, softcap=softcap, temperature=temperature)
+        ctx.set_materialize_grads(False)
+        ctx.mark_non_differentiable(out.lse, out.top_logp, out.top_ids)
+        return tuple(out)
+
+    @staticmethod
+    def backward(ctx, grad_logp, grad_entropy, *_):
+        h, W, tokens, lse, entropy = ctx.saved_tensors
+        if grad_logp is None and grad_entropy is None:
+            return (None,) * 7
+        flat = lambda g: None if g is None else g.contiguous()  # noqa: E731
+        dH, dW = flce_logprobs_backward(h, W, tokens, lse, entropy, flat(grad_logp),
+                                        flat(grad_entropy), **ctx.kw)
+        return dH, dW, None, None, None, None, None
+
+
+def token_logprobs(hidden_states: torch.Tensor, tokens: Optional[torch.Tensor],
+                   lm_weight: torch.Tensor, *, ignore_index: int = -100, softcap: float = 0.0,
+                   temperature: float = 1.0, top_k: int = 0) -> TokenLogprobs:
+    """:func:`flce_logprobs` for hidden_states [..., H] and tokens [...], with the
+    gradients of logp and entropy (the other outputs have none). Without tokens
+    there are no gradients."""
+    lead, H = hidden_states.shape[:-1], hidden_states.shape[-1]
+    h, W = hidden_states.reshape(-1, H).contiguous(), lm_weight.contiguous()
+    y = None if tokens is None else tokens.reshape(-1).contiguous()
+    if y is None or not torch.is_grad_enabled() or not (h.requires_grad or W.requires_grad):
+        out = flce_logprobs(h.detach(), W.detach(), y, ignore_index=ignore_index, softcap=softcap,
+                            temperature=temperature, top_k=top_k)
+    else:
+        out = _TokenLogprobs.apply(h, W, y, ignore_index, float(softcap), float(temperature),
+                                   int(top_k))
+    logp, entropy, lse, top_logp, top_ids = out
+    return TokenLogprobs(None if logp is None else logp.view(lead), entropy.view(lead),
+                         lse.view(lead), top_logp.view(*lead, int(top_k)),
+                         top_ids.view(*lead, int(top_k)))

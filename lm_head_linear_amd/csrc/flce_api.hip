@@ -12,6 +12,44 @@
 #include "flce_plan.h"
 #include "gemm_index.h"
 
+namespace flce {
+
+// A call whose bf16 rows are padded (Plan::pad_h) runs at the padded width on
+// the workspace's copies: W padded, dW padded from the caller's when it is
+// added to, dH and dW written there and copied out at the end. The gather
+// pads the hidden rows it copies; a call without it reads a padded copy of h.
+hipError_t pad_inputs(const Plan& p, Args& a, char* ws, bool backward, const Launcher& L) {
+  if (!p.pad_h) return hipSuccess;
+  void* wp = ws + p.off_wp;
+  hipError_t e = launch_copy_rows(a.W, p.h_in, wp, p.H, p.V, p.h_in, p.H, p.elem, L);
+  a.W = wp;
+  a.H = p.H;
+  if (e == hipSuccess && !p.compact) {
+    void* hp = ws + p.off_hp;
+    e = launch_copy_rows(a.h, p.h_in, hp, p.H, p.N, p.h_in, p.H, p.elem, L);
+    a.h = hp;
+  }
+  if (!backward) return e;
+  void* dwp = ws + p.off_dwp;
+  if (e == hipSuccess && a.accumulate_dW)
+    e = launch_copy_rows(a.dW, p.h_in, dwp, p.H, p.V, p.h_in, p.H, p.grad_elem, L);
+  a.dW = dwp;
+  a.dH = ws + p.off_dhp;
+  return e;
+}
+
+hipError_t crop_outputs(const Plan& p, const char* ws, void* dH, void* dW, const Launcher& L) {
+  if (!p.pad_h) return hipSuccess;
+  hipError_t e = launch_copy_rows(ws + p.off_dwp, p.H, dW, p.h_in, p.V, p.h_in, p.h_in,
+                                        p.grad_elem, L);
+  if (e == hipSuccess)
+    e = launch_copy_rows(ws + p.off_dhp, p.H, dH, p.h_in, p.N, p.h_in, p.h_in,
+                               p.grad_elem, L);
+  return e;
+}
+
+}  // namespace flce
+
 namespace {
 
 using flce::Range;
@@ -63,7 +101,7 @@ const char* kKindNames[flce::kNumKinds] = {"label_scan", "lse_fwd_gemm", "lse_me
                                            "dH_gemm", "fill", "probs_to_grad", "dH_reduce",
                                            "gather", "dH_dW_gemm", "pad_copy", "rms_norm",
                                            "rms_norm_bwd", "embed", "embed_sort",
-                                           "embed_grad"};
+                                           "embed_grad", "logprobs_tiles", "logprobs_join"};
 
 // ---- scratch of flce_forward_noalloc ---------------------------------------
 // One copy on every GPU the library runs on, held until the process ends. In
@@ -106,42 +144,6 @@ hipError_t scratch_address(hipStream_t stream, void** out) {
   }
   *out = g_scratch_ptr[dev];
   return hipSuccess;
-}
-
-// A call whose bf16 rows are padded (Plan::pad_h) runs at the padded width on
-// the workspace's copies: W padded, dW padded from the caller's when it is
-// added to, dH and dW written there and copied out at the end. The gather
-// pads the hidden rows it copies; a call without it reads a padded copy of h.
-hipError_t pad_inputs(const flce::Plan& p, flce::Args& a, char* ws, bool backward,
-                      const flce::Launcher& L) {
-  if (!p.pad_h) return hipSuccess;
-  void* wp = ws + p.off_wp;
-  hipError_t e = flce::launch_copy_rows(a.W, p.h_in, wp, p.H, p.V, p.h_in, p.H, p.elem, L);
-  a.W = wp;
-  a.H = p.H;
-  if (e == hipSuccess && !p.compact) {
-    void* hp = ws + p.off_hp;
-    e = flce::launch_copy_rows(a.h, p.h_in, hp, p.H, p.N, p.h_in, p.H, p.elem, L);
-    a.h = hp;
-  }
-  if (!backward) return e;
-  void* dwp = ws + p.off_dwp;
-  if (e == hipSuccess && a.accumulate_dW)
-    e = flce::launch_copy_rows(a.dW, p.h_in, dwp, p.H, p.V, p.h_in, p.H, p.grad_elem, L);
-  a.dW = dwp;
-  a.dH = ws + p.off_dhp;
-  return e;
-}
-
-hipError_t crop_outputs(const flce::Plan& p, const char* ws, void* dH, void* dW,
-                        const flce::Launcher& L) {
-  if (!p.pad_h) return hipSuccess;
-  hipError_t e = flce::launch_copy_rows(ws + p.off_dwp, p.H, dW, p.h_in, p.V, p.h_in, p.h_in,
-                                        p.grad_elem, L);
-  if (e == hipSuccess)
-    e = flce::launch_copy_rows(ws + p.off_dhp, p.H, dH, p.h_in, p.N, p.h_in, p.h_in,
-                               p.grad_elem, L);
-  return e;
 }
 
 // The no-recompute variant (arguments already checked): token chunk by chunk,
@@ -187,7 +189,7 @@ int run_nr(const void* h, const void* W, const int64_t* labels, int64_t N, int64
   a.hc = ws + p.off_hc;
   {
     Range r("flce.setup");
-    e = pad_inputs(p, a, ws, true, L);
+    e = flce::pad_inputs(p, a, ws, true, L);
     // the labels scanned and the tokens gathered, the kept ones first; the
     // chunks run over that order (the ignored tokens only for their lse, when
     // it is asked for)
@@ -204,7 +206,7 @@ int run_nr(const void* h, const void* W, const int64_t* labels, int64_t N, int64
   }
   Range r("flce.finish");
   if (e == hipSuccess) e = flce::launch_loss_final(p, a, L);
-  if (e == hipSuccess) e = crop_outputs(p, ws, dH, dW, L);
+  if (e == hipSuccess) e = flce::crop_outputs(p, ws, dH, dW, L);
   return e == hipSuccess ? FLCE_OK : FLCE_ERR_HIP;
 }
 
@@ -258,7 +260,7 @@ int run(const void* h, const void* W, const int64_t* labels, int64_t N, int64_t 
   const bool bf16 = dtype == FLCE_BF16;
   {
     Range r("flce.setup");
-    e = pad_inputs(p, a, ws, backward, L);
+    e = flce::pad_inputs(p, a, ws, backward, L);
     // a compact plan gathers the tokens with the label scan, the kept ones in
     // front; the forward then skips the ignored ones unless their lse is asked
     // for
@@ -277,7 +279,7 @@ int run(const void* h, const void* W, const int64_t* labels, int64_t N, int64_t 
   }
   if (e == hipSuccess && backward && p.pad_h) {
     Range r("flce.copy_out");
-    e = crop_outputs(p, ws, dH, dW, L);
+    e = flce::crop_outputs(p, ws, dH, dW, L);
   }
   return e == hipSuccess ? FLCE_OK : FLCE_ERR_HIP;
 }

@@ -29,7 +29,9 @@ enum Kind : int {
   kEmbed = 15,
   kEmbedSort = 16,
   kEmbedGrad = 17,
-  kNumKinds = 18,
+  kLpTiles = 18,
+  kLpJoin = 19,
+  kNumKinds = 20,
 };
 
 // Everything one call needs on the device side.
@@ -110,6 +112,11 @@ hipError_t launch_chunk_counts(const Plan& p, const Args& a, bool all_rows, cons
 hipError_t launch_merge_gathered(const Plan& p, const Args& a, int64_t t0, int64_t nt,
                                  const int64_t* count, const Launcher& L);
 
+// A padded call's copies (Plan::pad_h): the inputs before its launches (a then
+// points at them), the gradients out of them at its end. Nothing otherwise.
+hipError_t pad_inputs(const Plan& p, Args& a, char* ws, bool backward, const Launcher& L);
+hipError_t crop_outputs(const Plan& p, const char* ws, void* dH, void* dW, const Launcher& L);
+
 // bf16 MFMA path.
 hipError_t bf16_forward(const Plan& p, const Args& a, const Launcher& L);
 hipError_t bf16_backward_chunk(const Plan& p, const Args& a, int64_t chunk, const Launcher& L);
@@ -124,5 +131,7 @@ hipError_t bf16_nr_backward_chunk(const Plan& p, const Args& a, int64_t c, const
 // float32 path.
 hipError_t f32_forward(const Plan& p, const Args& a, const Launcher& L);
 hipError_t f32_backward_chunk(const Plan& p, const Args& a, int64_t chunk, const Launcher& L);
+// The products of vocabulary chunk `chunk` once G^T (a.g) is formed.
+hipError_t f32_chunk_products(const Plan& p, const Args& a, int64_t chunk, const Launcher& L);
 
 }  // namespace flce

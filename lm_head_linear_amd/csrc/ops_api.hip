@@ -102,4 +102,94 @@ int flce_embedding_backward(const int64_t* tokens, const void* dout, int64_t ld_
   return status_of(flce::launch_embedding_backward(a, L));
 }
 
+int flce_logprobs(const void* h, const void* W, const int64_t* tokens, int64_t N, int64_t H,
+                  int64_t V, int64_t ignore_index, float softcap, float temperature, int top_k,
+                  float* logp, float* entropy, float* lse, float* top_logp, int64_t* top_ids,
+                  void* stream, int dtype, void* workspace, size_t workspace_bytes,
+                  int32_t* status) {
+  const int st = flce_logprobs_check_args(h, W, tokens, N, H, V, ignore_index, softcap,
+                                          temperature, top_k, logp, entropy, lse, top_logp,
+                                          top_ids, stream, dtype, workspace, workspace_bytes,
+                                          status);
+  if (st != FLCE_OK) return st;
+  Range r("flce_logprobs");
+  const Launcher L = flce::make_launcher(stream);
+  if (N == 0)
+    return status ? status_of(flce::launch_token_status(nullptr, 0, V, ignore_index, status, L))
+                  : FLCE_OK;
+  flce::LpPlan q;
+  if (!flce::make_lp_plan(N, H, V, dtype, top_k, tokens != nullptr, &q)) return FLCE_ERR_ARG;
+  const flce::LpArgs a{h, W, tokens, N, H, V, ignore_index, softcap, temperature, top_k,
+                       logp, entropy, lse, top_logp, top_ids, dtype, status};
+  return status_of(flce::launch_logprobs(q, a, static_cast<char*>(workspace), L));
+}
+
+int flce_logprobs_backward(const void* h, const void* W, const int64_t* tokens, const float* lse,
+                           const float* entropy, const float* grad_logp,
+                           const float* grad_entropy, int64_t N, int64_t H, int64_t V,
+                           int64_t ignore_index, float softcap, float temperature, void* dH,
+                           void* dW, int accumulate_dW, void* stream, int dtype, int grad_dtype,
+                           void* workspace, size_t workspace_bytes, int32_t* status) {
+  const int st = flce_logprobs_backward_check_args(
+      h, W, tokens, lse, entropy, grad_logp, grad_entropy, N, H, V, ignore_index, softcap,
+      temperature, dH, dW, accumulate_dW, stream, dtype, grad_dtype, workspace, workspace_bytes,
+      status);
+  if (st != FLCE_OK) return st;
+  Range r("flce_logprobs_backward");
+  const Launcher L = flce::make_launcher(stream);
+  flce::Plan p;
+  if (!flce::make_plan(N, H, V, dtype, &p, true, grad_dtype)) return FLCE_ERR_ARG;
+  hipError_t e = hipSuccess;
+  if (N == 0) {
+    if (!accumulate_dW) e = flce::launch_zero_bytes(dW, size_t(V) * H * p.grad_elem, L);
+    if (e == hipSuccess && status)
+      e = flce::launch_token_status(nullptr, 0, V, ignore_index, status, L);
+    return status_of(e);
+  }
+  char* ws = static_cast<char*>(workspace);
+  char* own = ws + p.total;                         // behind the head's own workspace
+  const size_t arr = (size_t(p.ld_part) * sizeof(float) + 255) & ~size_t(255);
+  flce::Args a{};
+  a.h = h; a.W = W; a.labels = tokens;
+  a.N = N; a.H = H; a.V = V;
+  a.ignore_index = ignore_index; a.softcap = softcap;
+  a.num_tokens = reinterpret_cast<int64_t*>(own);
+  a.dH = dH; a.dW = dW;
+  a.mb_scale = 1.f; a.accumulate_dW = accumulate_dW ? 1 : 0;
+  a.status = status;
+  a.sc = reinterpret_cast<flce::Scalars*>(ws + p.off_scalars);
+  a.tok_loss = reinterpret_cast<double*>(ws + p.off_tokloss);
+  a.g = ws + p.off_g;
+  a.dh_acc = p.need_dh_acc ? reinterpret_cast<float*>(ws + p.off_dhacc) : nullptr;
+  a.dh_part = p.dh_kseg ? reinterpret_cast<float*>(ws + p.off_dhpart) : nullptr;
+  if (p.compact) {
+    a.idx = reinterpret_cast<int32_t*>(ws + p.off_idx);
+    a.yc = reinterpret_cast<int64_t*>(ws + p.off_yc);
+    a.bcnt = reinterpret_cast<int32_t*>(ws + p.off_bcnt);
+    a.hc = ws + p.off_hc;
+  }
+  own += 256;
+  const flce::LpGradArgs g{lse, entropy, grad_logp, grad_entropy, temperature,
+                           reinterpret_cast<float*>(own), reinterpret_cast<float*>(own + arr),
+                           reinterpret_cast<float*>(own + 2 * arr),
+                           reinterpret_cast<float*>(own + 3 * arr)};
+  {
+    Range s("flce.setup");
+    e = flce::pad_inputs(p, a, ws, true, L);
+    if (e == hipSuccess && p.compact) e = flce::launch_scan_gather(p, a, false, L);
+    if (e == hipSuccess && !p.compact && status)
+      e = flce::launch_token_status(tokens, N, V, ignore_index, status, L);
+    if (e == hipSuccess) e = flce::launch_lp_coefficients(p, a, g, L);
+  }
+  for (int64_t c = 0; e == hipSuccess && c < p.n_chunks; ++c) {
+    Range s("flce.backward_chunk");
+    e = flce::launch_lp_gradient(p, a, g, c, L);
+    if (e == hipSuccess)
+      e = dtype == FLCE_BF16 ? flce::bf16_chunk_products(p, a, c, L)
+                             : flce::f32_chunk_products(p, a, c, L);
+  }
+  if (e == hipSuccess) e = flce::crop_outputs(p, ws, dH, dW, L);
+  return status_of(e);
+}
+
 }  // extern "C"

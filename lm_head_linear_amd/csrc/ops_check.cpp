@@ -80,6 +80,66 @@ bool make_embed_plan(int64_t N, int64_t H, int64_t V, EmbedPlan* p) {
   return true;
 }
 
+bool make_lp_plan(int64_t N, int64_t H, int64_t V, int dtype, int top_k, bool tokens, LpPlan* out) {
+  LpPlan q;
+  if (top_k < 0 || top_k > FLCE_MAX_TOP) return false;
+  if (!make_plan(N, H, V, dtype, &q.p, false, -1, 0)) return false;
+  const bool bf16 = dtype == FLCE_BF16;
+  q.top_k = top_k;
+  q.few = bf16 && N <= kFewTokens && ceil_div(V, kLpRows) <= kFewMaxLists;
+  const bool tiles = bf16 && !q.few;
+  q.gather = tiles && tokens;
+  q.p.compact = q.gather;
+  q.part_rows = tiles ? kTileBF16 : kLpRows;
+  q.list_rows = tiles ? kTileBF16 / 2 : kLpRows;
+  q.parts = ceil_div(V, q.part_rows);
+  q.lists = ceil_div(V, q.list_rows);
+  q.kc = top_k < q.list_rows ? top_k : q.list_rows;
+  const int64_t step = tiles ? kTileBF16 : kLpRows;      // tokens per tile
+  const int64_t nmax = ceil_div(N > 0 ? N : 1, step) * step;
+  int64_t nc = nmax < kLpMaxChunk ? nmax : kLpMaxChunk;
+  if (q.kc > 0) {
+    const int64_t fit = kLpListBytes / (q.lists * q.kc * 5) / step * step;
+    if (nc > fit) nc = fit > step ? fit : step;
+  }
+  q.nc = nc;
+  q.n_chunks = ceil_div(N, nc);
+  if (q.few || (!bf16 && nc <= kFewTokens && q.lists <= kFewMaxLists)) {
+    q.sp = 1; q.st = q.parts;
+    q.ck = 1; q.cl = q.kc; q.ct = q.lists * q.kc;
+  } else {
+    q.sp = nc; q.st = 1;
+    q.ct = 1; q.ck = nc; q.cl = q.kc * nc;
+  }
+  size_t off = 0;
+  auto take = [&](size_t bytes) { const size_t at = off; off = align256(off + bytes); return at; };
+  q.off_sc = take(sizeof(Scalars));
+  q.off_nt = take(sizeof(int64_t));
+  if (N > 0) {
+    if (q.gather) {
+      q.p.n_gather_blocks = ceil_div(N, kGatherBlock);
+      q.off_tokloss = take(size_t(N) * sizeof(double));
+      q.off_idx = take(size_t(N) * sizeof(int32_t));
+      q.off_yc = take(size_t(N) * sizeof(int64_t));
+      q.off_bcnt = take(size_t(q.p.n_gather_blocks) * sizeof(int32_t));
+      q.off_ccnt = take(size_t(2 * q.n_chunks) * sizeof(int64_t));
+    }
+    if (q.gather || (tiles && q.p.pad_h)) q.off_h = take(size_t(N) * q.p.H * 2);
+    if (tiles && q.p.pad_h) q.off_wp = take(size_t(V) * q.p.H * 2);
+    q.off_part = take(size_t(q.parts) * nc * 2 * sizeof(float));
+    q.off_pd = take(size_t(q.parts) * nc * sizeof(float));
+    q.off_zt = take(size_t(nc) * sizeof(float));
+    if (top_k > 0) {
+      q.off_tau = take(size_t(nc) * sizeof(float));
+      q.off_cv = take(size_t(q.lists) * q.kc * nc * sizeof(float));
+      q.off_ci = take(size_t(q.lists) * q.kc * nc);
+    }
+  }
+  q.total = off;
+  *out = q;
+  return true;
+}
+
 }  // namespace flce
 
 using namespace flce;
@@ -202,6 +262,95 @@ int flce_embedding_backward_check_args(const int64_t* tokens, const void* dout, 
   for (const Buf& b : {bt, bd, bw, bst})
     if (misaligned(b)) return FLCE_ERR_UNSUPPORTED;
   if (!workspace || wk.begin() % 256 != 0 || workspace_bytes < p.total) return FLCE_ERR_WORKSPACE;
+  return FLCE_OK;
+}
+
+size_t flce_logprobs_workspace_size(int64_t N, int64_t H, int64_t V, int dtype, int top_k) {
+  LpPlan a, b;
+  if (!make_lp_plan(N, H, V, dtype, top_k, true, &a) ||
+      !make_lp_plan(N, H, V, dtype, top_k, false, &b))
+    return 0;
+  return a.total > b.total ? a.total : b.total;
+}
+
+int flce_logprobs_check_args(const void* h, const void* W, const int64_t* tokens, int64_t N,
+                             int64_t H, int64_t V, int64_t ignore_index, float softcap,
+                             float temperature, int top_k, const float* logp,
+                             const float* entropy, const float* lse, const float* top_logp,
+                             const int64_t* top_ids, const void* stream, int dtype,
+                             const void* workspace, size_t workspace_bytes,
+                             const int32_t* status) {
+  (void)ignore_index; (void)stream;
+  if (!is_dtype(dtype)) return FLCE_ERR_ARG;
+  if (!(softcap >= 0.f) || !std::isfinite(softcap)) return FLCE_ERR_ARG;
+  if (!(temperature > 0.f) || !std::isfinite(temperature) || !std::isfinite(1.f / temperature))
+    return FLCE_ERR_ARG;
+  LpPlan p;
+  if (!make_lp_plan(N, H, V, dtype, top_k, tokens != nullptr, &p)) return FLCE_ERR_ARG;
+  if (!W || (N > 0 && !h)) return FLCE_ERR_ARG;
+  if (N > 0 && ((tokens != nullptr) != (logp != nullptr))) return FLCE_ERR_ARG;
+  if (N > 0 && top_k > 0 && (!top_logp || !top_ids)) return FLCE_ERR_ARG;
+  if (top_k == 0 && (top_logp || top_ids)) return FLCE_ERR_ARG;
+  const size_t es = esize(dtype);
+  const Buf bh = matrix(h, N, H, H, es), bw = matrix(W, V, H, H, es), bt = vec(tokens, N, 8),
+            bl = vec(logp, N, 4), be = vec(entropy, N, 4), bz = vec(lse, N, 4),
+            bv = vec(top_logp, N * top_k, 4), bi = vec(top_ids, N * top_k, 8),
+            bs = vec(status, 1, 4), wk = vec(workspace, int64_t(workspace_bytes), 1);
+  if (clash({bl, be, bz, bv, bi, bs, wk}, {bh, bw, bt})) return FLCE_ERR_ARG;
+  if (dtype == FLCE_BF16 && !bf16_shape_ok(N, p.p.H, V)) return FLCE_ERR_UNSUPPORTED;
+  const uintptr_t mask = dtype == FLCE_BF16 ? 15u : 3u;
+  if ((bw.begin() & mask) || (N > 0 && (bh.begin() & mask))) return FLCE_ERR_UNSUPPORTED;
+  for (const Buf& b : {bt, bl, be, bz, bv, bi, bs})
+    if (misaligned(b)) return FLCE_ERR_UNSUPPORTED;
+  if (!workspace || wk.begin() % 256 != 0) return FLCE_ERR_WORKSPACE;
+  if (workspace_bytes < flce_logprobs_workspace_size(N, H, V, dtype, top_k))
+    return FLCE_ERR_WORKSPACE;
+  return FLCE_OK;
+}
+
+size_t flce_logprobs_backward_workspace_size(int64_t N, int64_t H, int64_t V, int dtype,
+                                             int grad_dtype) {
+  Plan p;
+  if (!make_plan(N, H, V, dtype, &p, true, grad_dtype)) return 0;
+  // the head's backward, its dummy count, and the token coefficients
+  return p.total + 256 + 4 * align256(size_t(p.ld_part) * sizeof(float));
+}
+
+int flce_logprobs_backward_check_args(const void* h, const void* W, const int64_t* tokens,
+                                      const float* lse, const float* entropy,
+                                      const float* grad_logp, const float* grad_entropy,
+                                      int64_t N, int64_t H, int64_t V, int64_t ignore_index,
+                                      float softcap, float temperature, const void* dH,
+                                      const void* dW, int accumulate_dW, const void* stream,
+                                      int dtype, int grad_dtype, const void* workspace,
+                                      size_t workspace_bytes, const int32_t* status) {
+  (void)ignore_index; (void)stream; (void)accumulate_dW;
+  if (!is_dtype(dtype) || !is_dtype(grad_dtype)) return FLCE_ERR_ARG;
+  if (!(softcap >= 0.f) || !std::isfinite(softcap)) return FLCE_ERR_ARG;
+  if (!(temperature > 0.f) || !std::isfinite(temperature) || !std::isfinite(1.f / temperature))
+    return FLCE_ERR_ARG;
+  if (dtype == FLCE_F32 && grad_dtype == FLCE_BF16) return FLCE_ERR_UNSUPPORTED;
+  Plan p;
+  if (!make_plan(N, H, V, dtype, &p, true, grad_dtype)) return FLCE_ERR_ARG;
+  if (!W || !dW || (N > 0 && (!h || !dH || !tokens || !lse))) return FLCE_ERR_ARG;
+  if (N > 0 && !grad_logp && !grad_entropy) return FLCE_ERR_ARG;
+  if (N > 0 && grad_entropy && !entropy) return FLCE_ERR_ARG;
+  const size_t es = esize(dtype), gs = esize(grad_dtype);
+  const Buf bh = matrix(h, N, H, H, es), bw = matrix(W, V, H, H, es), bt = vec(tokens, N, 8),
+            bz = vec(lse, N, 4), be = vec(entropy, N, 4), ga = vec(grad_logp, N, 4),
+            gb = vec(grad_entropy, N, 4), dh = matrix(dH, N, H, H, gs),
+            dw = matrix(dW, V, H, H, gs), bs = vec(status, 1, 4),
+            wk = vec(workspace, int64_t(workspace_bytes), 1);
+  if (clash({dh, dw, bs, wk}, {bh, bw, bt, bz, be, ga, gb})) return FLCE_ERR_ARG;
+  if (dtype == FLCE_BF16 && !bf16_shape_ok(N, p.H, V)) return FLCE_ERR_UNSUPPORTED;
+  const uintptr_t mask = dtype == FLCE_BF16 ? 15u : 3u;
+  if (((bw.begin() | dw.begin()) & mask) || (N > 0 && ((bh.begin() | dh.begin()) & mask)))
+    return FLCE_ERR_UNSUPPORTED;
+  for (const Buf& b : {bt, bz, be, ga, gb, bs})
+    if (misaligned(b)) return FLCE_ERR_UNSUPPORTED;
+  if (!workspace || wk.begin() % 256 != 0) return FLCE_ERR_WORKSPACE;
+  if (workspace_bytes < flce_logprobs_backward_workspace_size(N, H, V, dtype, grad_dtype))
+    return FLCE_ERR_WORKSPACE;
   return FLCE_OK;
 }
 

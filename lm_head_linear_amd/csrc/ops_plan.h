@@ -6,6 +6,8 @@
 #include <cstddef>
 #include <cstdint>
 
+#include "flce_plan.h"
+
 namespace flce {
 
 // ---- root-mean-square norm ---------------------------------------------------------
@@ -89,6 +91,67 @@ struct EmbedPlan {
 // False for sizes that are not valid.
 bool make_embed_plan(int64_t N, int64_t H, int64_t V, EmbedPlan* p);
 
+// ---- token log probabilities -------------------------------------------------------
+// Tokens up to which a bf16 call streams W once through the few-token kernel
+// instead of the 256 x 256 tiles (see kernels_logprobs.hip for both sides).
+constexpr int64_t kFewTokens = 64;
+// Vocabulary rows per workgroup of the few-token and float32 kernels.
+constexpr int64_t kLpRows = 64;
+// The join of few tokens keeps up to 8 lists a thread.
+constexpr int64_t kFewMaxLists = 8 * 1024;
+// Bytes of candidate lists per token chunk, and tokens per chunk.
+constexpr int64_t kLpListBytes = int64_t(1) << 30;
+constexpr int64_t kLpMaxChunk = 8192;
+
+struct LpPlan {
+  Plan p;                     // sizes (H padded), the gather's blocks; its offsets are not used
+  bool few = false;           // the few-token kernel
+  bool gather = false;        // live tokens first (bf16 tiles with tokens given)
+  int top_k = 0;
+  // Partials: per part_rows vocabulary rows and token the max, sum and weighted
+  // sum; candidates: per list_rows rows and token the kc largest logits, sorted.
+  int64_t part_rows = 0, parts = 0, list_rows = 0, lists = 0, kc = 0;
+  int64_t nc = 0, n_chunks = 0;   // tokens per chunk
+  // Elements between parts / tokens, and between lists / candidates / tokens:
+  // token-major for few tokens (a workgroup joins one token), otherwise tokens
+  // adjacent (a workgroup joins 32).
+  int64_t sp = 0, st = 0, cl = 0, ck = 0, ct = 0;
+  size_t off_sc = 0, off_nt = 0, off_tokloss = 0, off_idx = 0, off_yc = 0, off_bcnt = 0,
+         off_ccnt = 0, off_h = 0, off_wp = 0, off_part = 0, off_pd = 0, off_zt = 0, off_tau = 0,
+         off_cv = 0, off_ci = 0, total = 0;
+};
+
+bool make_lp_plan(int64_t N, int64_t H, int64_t V, int dtype, int top_k, bool tokens, LpPlan* p);
+
+struct LpArgs {
+  const void* h;
+  const void* W;
+  const int64_t* tokens;      // may be null: no given tokens
+  int64_t N, H, V, ignore_index;
+  float softcap, temperature;
+  int top_k;
+  float* logp;
+  float* entropy;
+  float* lse;
+  float* top_logp;
+  int64_t* top_ids;
+  int dtype;
+  int32_t* status;
+};
+
+struct LpGradArgs {
+  const float* lse;
+  const float* entropy;       // null without grad_entropy
+  const float* grad_logp;     // may be null
+  const float* grad_entropy;  // may be null
+  float temperature;
+  // gathered order: the lse and the gradient's coefficients
+  float* lse_g;
+  float* c0;
+  float* c1;
+  float* ca;
+};
+
 }  // namespace flce
 
 #if defined(__HIPCC__)
@@ -102,6 +165,13 @@ hipError_t launch_rms_norm(const NormArgs& a, const Launcher& L);
 hipError_t launch_rms_norm_backward(const NormBwdArgs& a, const Launcher& L);
 hipError_t launch_embedding(const EmbedArgs& a, const Launcher& L);
 hipError_t launch_embedding_backward(const EmbedGradArgs& a, const Launcher& L);
+hipError_t launch_logprobs(const LpPlan& q, const LpArgs& a, char* ws, const Launcher& L);
+// The logit gradient of vocabulary chunk `chunk` (a.g) from the coefficients,
+// and the kernel that forms those.
+hipError_t launch_lp_coefficients(const Plan& p, const Args& a, const LpGradArgs& g,
+                                  const Launcher& L);
+hipError_t launch_lp_gradient(const Plan& p, const Args& a, const LpGradArgs& g, int64_t chunk,
+                              const Launcher& L);
 hipError_t launch_token_status(const int64_t* tokens, int64_t N, int64_t V, int64_t padding,
                                int32_t* status, const Launcher& L);
 

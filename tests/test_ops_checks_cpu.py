@@ -143,10 +143,92 @@ def test_embedding_workspace():
     assert size(1 << 20, 64, 100) < 4 * (1 << 20) * 4 + 256 * 128 * 4 + 2 * 8192 * 64 * 4 + 1
 
 
+def lp(**kw):
+    a = dict(h=Buf(M), W=Buf(2 * M), tokens=Buf(3 * M), N=4, H=24, V=100, top_k=3,
+             logp=Buf(4 * M), entropy=Buf(5 * M), lse=Buf(6 * M), top_logp=Buf(7 * M),
+             top_ids=Buf(8 * M), status=Buf(9 * M))
+    a.update(kw)
+    if "workspace" not in a:
+        a["workspace"] = Buf(64 * M, max(1, m.flce_logprobs_workspace_size(
+            a["N"], a["H"], a["V"], a.get("dtype", torch.bfloat16), a["top_k"])))
+    return m.flce_logprobs_check_args(**a)
+
+
+NOTOP = dict(top_k=0, top_logp=None, top_ids=None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    ({}, OK), (NOTOP, OK), (dict(entropy=None, lse=None, status=None), OK),
+    (dict(tokens=None, logp=None), OK), (dict(N=1000), OK), (dict(dtype=torch.float32), OK),
+    (dict(N=0, h=None, tokens=None, logp=None), OK), (dict(H=7), OK), (dict(V=1), OK),
+    (dict(top_k=32), OK), (dict(temperature=0.01, softcap=30.0), OK),
+    (dict(N=-1), ARG), (dict(H=0), ARG), (dict(V=0), ARG), (dict(top_k=-1), ARG),
+    (dict(top_k=33), ARG), (dict(softcap=-1.0), ARG), (dict(softcap=float("inf")), ARG),
+    (dict(temperature=0.0), ARG), (dict(temperature=-1.0), ARG),
+    (dict(temperature=float("nan")), ARG), (dict(temperature=1e-39), ARG),
+    (dict(h=None), ARG), (dict(W=None), ARG), (dict(tokens=None), ARG), (dict(logp=None), ARG),
+    (dict(top_ids=None), ARG), (dict(top_logp=None), ARG), (dict(top_k=0), ARG),
+    (dict(logp=Buf(5 * M)), ARG), (dict(lse=Buf(M)), ARG), (dict(top_ids=Buf(2 * M + 16)), ARG),
+    (dict(status=Buf(3 * M + 4)), ARG), (dict(workspace=Buf(M, 1 << 20)), ARG),
+    (dict(h=Buf(M + 8)), UNSUP), (dict(W=Buf(2 * M + 2)), UNSUP), (dict(logp=Buf(4 * M + 2)), UNSUP),
+    (dict(dtype=torch.float32, h=Buf(M + 8)), OK), (dict(top_ids=Buf(8 * M + 4)), UNSUP),
+    (dict(workspace=None), WS), (dict(workspace=Buf(64 * M, 1024)), WS),
+    (dict(workspace=Buf(64 * M + 64, 1 << 24)), WS),
+])
+def test_logprobs(kw, want):
+    assert lp(**kw) == want
+
+
+def lp_bwd(**kw):
+    a = dict(h=Buf(M), W=Buf(2 * M), tokens=Buf(3 * M), lse=Buf(4 * M), entropy=Buf(5 * M),
+             grad_logp=Buf(6 * M), grad_entropy=Buf(7 * M), N=4, H=24, V=100, dH=Buf(8 * M),
+             dW=Buf(9 * M), status=Buf(10 * M))
+    a.update(kw)
+    if "workspace" not in a:
+        a["workspace"] = Buf(64 * M, max(1, m.flce_logprobs_backward_workspace_size(
+            a["N"], a["H"], a["V"], a.get("dtype", torch.bfloat16), a.get("grad_dtype"))))
+    return m.flce_logprobs_backward_check_args(**a)
+
+
+@pytest.mark.parametrize("kw,want", [
+    ({}, OK), (dict(grad_logp=None), OK), (dict(grad_entropy=None, entropy=None), OK),
+    (dict(grad_dtype=torch.float32), OK), (dict(dtype=torch.float32), OK), (dict(H=13), OK),
+    (dict(N=0, h=None, dH=None, tokens=None, lse=None, entropy=None, grad_logp=None,
+          grad_entropy=None), OK),
+    (dict(grad_logp=None, grad_entropy=None), ARG), (dict(entropy=None), ARG),
+    (dict(lse=None), ARG), (dict(tokens=None), ARG), (dict(dH=None), ARG), (dict(dW=None), ARG),
+    (dict(dW=Buf(2 * M)), ARG), (dict(dH=Buf(9 * M)), ARG), (dict(dW=Buf(6 * M)), ARG),
+    (dict(dH=Buf(4 * M)), ARG), (dict(workspace=Buf(9 * M, 1 << 24)), ARG),
+    (dict(temperature=0.0), ARG), (dict(softcap=float("nan")), ARG), (dict(N=-2), ARG),
+    (dict(dH=Buf(8 * M + 8)), UNSUP), (dict(grad_logp=Buf(6 * M + 1)), UNSUP),
+    (dict(workspace=None), WS), (dict(workspace=Buf(64 * M, 4096)), WS),
+])
+def test_logprobs_backward(kw, want):
+    assert lp_bwd(**kw) == want
+
+
+def test_float32_inputs_take_no_bf16_gradients():
+    assert lp_bwd(dtype=torch.float32, grad_dtype=torch.bfloat16,
+                  workspace=Buf(64 * M, 1 << 24)) == UNSUP
+
+
+def test_logprobs_workspace():
+    size = m.flce_logprobs_workspace_size
+    bf = torch.bfloat16
+    assert size(4, 8, 8, bf, 33) == 0 and size(4, 0, 8, bf, 0) == 0 and size(0, 8, 8, bf, 4) == 512
+    # one token: three partials and 8 candidates of 5 bytes for each 64 vocabulary
+    # rows, held for 64 tokens
+    assert size(1, 4096, 131072, bf, 8) < 64 * 2048 * (12 + 8 * 5) + 4096
+    # the candidates of a chunk of tokens stay below 1 GiB, whatever N is
+    a, b = size(1 << 17, 64, 256000, bf, 32), size(1 << 18, 64, 256000, bf, 32)
+    assert b - a < (1 << 17) * (64 * 2 + 32) and a < (1 << 30) + (1 << 17) * 256 + (1 << 25)
+
+
 def test_cpu_tensors_are_refused():
     t, W = torch.zeros(3, dtype=torch.int64), torch.zeros(5, 8)
     for call in (lambda: m.flce_embedding(t, W), lambda: m.flce_rms_norm(W, torch.ones(8)),
                  lambda: m.flce_embedding_backward(t, torch.zeros(3, 8), 5),
+                 lambda: m.flce_logprobs(torch.zeros(3, 8), W, t),
                  lambda: m.flce_rms_norm_backward(W, W, torch.ones(8), torch.ones(5))):
         with pytest.raises(ValueError, match="runs on a GPU"):
             call()
