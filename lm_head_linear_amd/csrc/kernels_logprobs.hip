@@ -160,7 +160,7 @@ struct EpiLp {
       mx[j] = m;
       sm[j] = col_sum4(s);
       dm[j] = col_sum4(d);
-      if (TOPK) {
+      if (TOPK && live > 0) {                      // rows past V have no list
         const float th = tau ? tau_t[acc_col(wn, j, lane)] : -INFINITY;
         float z[8][4];
 #pragma unroll
