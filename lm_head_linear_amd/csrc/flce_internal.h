@@ -131,7 +131,5 @@ hipError_t bf16_nr_backward_chunk(const Plan& p, const Args& a, int64_t c, const
 // float32 path.
 hipError_t f32_forward(const Plan& p, const Args& a, const Launcher& L);
 hipError_t f32_backward_chunk(const Plan& p, const Args& a, int64_t chunk, const Launcher& L);
-// The products of vocabulary chunk `chunk` once G^T (a.g) is formed.
-hipError_t f32_chunk_products(const Plan& p, const Args& a, int64_t chunk, const Launcher& L);
 
 }  // namespace flce

@@ -3,9 +3,9 @@
 //
 // The lookup reads and writes a row per token and is bound by that.
 //
-// The gradient sorts the tokens (stable, so equal ids keep their order), and a
-// wave then adds up the rows of a window of sorted tokens over a slice of
-// columns, one id after another: each row of dout is read once, a dW row whose
+// The gradient sorts the tokens (stable, so equal ids keep their order), and the
+// rows of kEmbedWindow sorted tokens are then added up over a slice of columns by
+// a workgroup, one id after another: each row of dout is read once, a dW row whose
 // tokens lie in one window is written once, and the sums are float32 in a fixed
 // order. An id whose tokens reach past a window leaves a float32 partial row per
 // window; a second pass adds those up in window order. Atomic adds would need
@@ -13,9 +13,12 @@
 //
 // The sort: least significant digit first, 8 bits a pass. A wave ranks 64 keys
 // at a time by ballots over the digit's bits, counting in a table of its own,
-// so equal digits keep their order. Up to kSortLocal tokens one workgroup sorts
-// in LDS; more go through one histogram, scan and scatter pass per digit over
-// many workgroups.
+// so equal digits keep their order. A workgroup sorts a chunk of kSortChunk
+// tokens in LDS. Up to kSortMerge tokens the sorted chunks are merged in one
+// step: a key's place is its place in its chunk plus, found by bisection in LDS,
+// the keys of each other chunk that go before it. More tokens go through one
+// histogram, scan and scatter pass per digit over many workgroups. (One
+// workgroup sorting 16384 tokens in LDS by itself took 163 us.)
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -131,58 +134,81 @@ __device__ __forceinline__ void digit_offsets(uint32_t (*cnt)[256], uint32_t* ws
   __syncthreads();
 }
 
-// Up to kSortLocal tokens, in one workgroup: R keys a thread.
-template <int R>
-__global__ __launch_bounds__(kSortThreads) void k_sort_local(
+// Chunk blockIdx.x of kSortChunk tokens, a key a thread.
+__global__ __launch_bounds__(kSortThreads) void k_sort_chunks(
     const int64_t* __restrict__ tokens, int64_t N, int64_t V, int64_t padding, int bits,
-    uint32_t* __restrict__ skey, uint32_t* __restrict__ spos, int32_t* __restrict__ status) {
-  __shared__ uint32_t key[kSortThreads * R];
-  __shared__ uint16_t pos[kSortThreads * R];
+    uint32_t* __restrict__ skey, uint32_t* __restrict__ spos) {
+  static_assert(kSortThreads == kSortChunk, "a key a thread");
+  __shared__ uint32_t key[kSortThreads], pos[kSortThreads];
   __shared__ uint32_t cnt[kSortWaves][256];
   __shared__ uint32_t wsum[kSortWaves];
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-  uint32_t k[R], p[R], dest[R];
-  int bad = 0;
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const int i = (w * R + r) * 64 + lane;         // wave w: R consecutive runs of 64
-    p[r] = uint32_t(i);
-    k[r] = 0;
-    if (i < N) {
-      const int64_t t = tokens[i];
-      k[r] = token_key(t, V, padding);
-      bad |= t != padding && k[r] == uint32_t(V);
-    }
-  }
-  bad = __syncthreads_or(bad);
-  if (status && tid == 0) *status = bad ? FLCE_ERR_LABEL : FLCE_OK;
+  const int64_t i0 = int64_t(blockIdx.x) * kSortChunk;
+  const bool live = i0 + tid < N;
+  uint32_t k = live ? token_key(tokens[i0 + tid], V, padding) : 0, p = uint32_t(i0 + tid);
   for (int shift = 0; shift < bits; shift += 8) {
     for (int i = tid; i < kSortWaves * 256; i += kSortThreads) (&cnt[0][0])[i] = 0;
     __syncthreads();
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-      dest[r] = wave_rank((k[r] >> shift) & 255, (w * R + r) * 64 + lane < N, cnt[w], lane);
+    const uint32_t rank = wave_rank((k >> shift) & 255, live, cnt[w], lane);
     __syncthreads();
     digit_offsets(cnt, wsum, nullptr);
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-      if ((w * R + r) * 64 + lane < N) {
-        const uint32_t to = cnt[w][(k[r] >> shift) & 255] + dest[r];
-        key[to] = k[r];
-        pos[to] = uint16_t(p[r]);
-      }
-    __syncthreads();
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int i = (w * R + r) * 64 + lane;
-      if (i < N) { k[r] = key[i]; p[r] = pos[i]; }
+    if (live) {
+      const uint32_t to = cnt[w][(k >> shift) & 255] + rank;
+      key[to] = k;
+      pos[to] = p;
     }
+    __syncthreads();
+    if (live) { k = key[tid]; p = pos[tid]; }
   }
+  if (live) { skey[i0 + tid] = k; spos[i0 + tid] = p; }
+}
+
+// The sorted chunks merged: 256 keys of chunk blockIdx.x / 4 a workgroup. Equal keys
+// of an earlier chunk go before, those of a later one behind. C: chunks held, in LDS;
+// places past the last key hold the largest value.
+template <int C>
+__global__ __launch_bounds__(256) void k_sort_merge(
+    const uint32_t* __restrict__ ikey, const uint32_t* __restrict__ ipos, int64_t N,
+    uint32_t* __restrict__ okey, uint32_t* __restrict__ opos) {
+  __shared__ __attribute__((aligned(16))) uint32_t key[C * kSortChunk];
+  const int chunks = int((N + kSortChunk - 1) / kSortChunk);
+#pragma unroll 16
+  for (int i = 4 * threadIdx.x; i < (chunks + 3) / 4 * 4 * int(kSortChunk); i += 1024) {
+    uint4 v = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+    if (i + 4 <= N) {
+      v = *reinterpret_cast<const uint4*>(ikey + i);
+    } else {
+      if (i < N) v.x = ikey[i];
+      if (i + 1 < N) v.y = ikey[i + 1];
+      if (i + 2 < N) v.z = ikey[i + 2];
+    }
+    *reinterpret_cast<uint4*>(key + i) = v;
+  }
+  __syncthreads();
+  const int c = blockIdx.x >> 2;
+  const int64_t at = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  if (at >= N) return;
+  const uint32_t k = key[at];
+  uint32_t place = uint32_t(at - c * kSortChunk);
+  for (int b = 0; b < chunks; b += 4) {            // four bisections at a time
+    uint32_t lo[4], less[4];
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const int i = (w * R + r) * 64 + lane;
-    if (i < N) { skey[i] = k[r]; spos[i] = p[r]; }
+    for (int u = 0; u < 4; ++u) {
+      lo[u] = 0;
+      less[u] = b + u < c ? k + 1 : k;             // keys below this go before
+    }
+#pragma unroll
+    for (int step = int(kSortChunk); step > 0; step >>= 1)
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const uint32_t m = lo[u] + step;
+        if (m <= kSortChunk && key[(b + u) * kSortChunk + m - 1] < less[u]) lo[u] = m;
+      }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) place += b + u == c ? 0 : lo[u];
   }
+  okey[place] = k;
+  opos[place] = ipos[at];
 }
 
 // Many workgroups, kSortBlock keys each (kSortRounds a thread). `first`: the keys
@@ -321,48 +347,56 @@ __device__ __forceinline__ void write_row(G* dW, int64_t v, int64_t H, int64_t c
   store_cols(dW + v * H, c, H, f);
 }
 
-// A wave: the sorted tokens [w win, w win + win) over kSliceCols columns. The
-// partial rows of window w: part[2 w] of an id that reaches into it from the
-// window before, part[2 w + 1] of one that starts in it and reaches past it.
+// A workgroup: 256 sorted tokens over kSliceCols columns, 32 of them a wave, in
+// order. A wave writes the rows of the ids that begin and end in its 32; its first
+// run, if the id began before, and its last, if the id goes on, stay in LDS, where
+// the wave in which an id began adds up what the others left of it. What reaches past
+// the workgroup's tokens goes to memory: part[2 w] of an id that began before
+// workgroup w's tokens, part[2 w + 1] of one that begins there and goes on.
+constexpr int kSumWaves = 8, kSumWave = 32;
+static_assert(kSumWaves * kSumWave == kEmbedWindow, "tokens per workgroup");
 constexpr int kInFlight = 8;                       // rows loaded before they are added
 
 template <class T, class G>
-__global__ __launch_bounds__(256) void k_embed_sum(
+__global__ __launch_bounds__(64 * kSumWaves) void k_embed_sum(
     const uint32_t* __restrict__ skey, const uint32_t* __restrict__ spos,
-    const T* __restrict__ dout, int64_t ldd, int64_t N, int64_t H, int64_t V, int win,
-    int64_t slices, float scale, int accumulate, G* __restrict__ dW, float* __restrict__ part) {
+    const T* __restrict__ dout, int64_t ldd, int64_t N, int64_t H, int64_t V, int64_t slices,
+    float scale, int accumulate, G* __restrict__ dW, float* __restrict__ part) {
+  __shared__ float edge[2][kSumWaves][kSliceCols];           // first runs, last runs
+  __shared__ uint32_t end_key[kSumWaves];          // the id that goes on behind a wave, or V
+  __shared__ int whole[kSumWaves];                 // its 32 are one run of an id begun before
   const int lane = threadIdx.x & 63;
-  const int64_t u = int64_t(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t wd = u / slices, c = (u - wd * slices) * kSliceCols + lane * kLaneCols;
-  const int64_t i0 = wd * win;
-  if (i0 >= N) return;
-  const int n = int(N - i0 < win ? N - i0 : win);
-  // an id that reaches in from the window before: its first run is a partial row
-  auto key_at = [&](int64_t i) -> uint32_t { return __builtin_amdgcn_readfirstlane(skey[i]); };
-  uint32_t cur = key_at(i0);
-  bool head = i0 > 0 && key_at(i0 - 1) == cur;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t wd = blockIdx.x / slices;
+  const int64_t cl = lane * kLaneCols, c = (blockIdx.x - wd * slices) * kSliceCols + cl;
+  const int64_t i0 = wd * kEmbedWindow + w * kSumWave;
+  const int n = i0 >= N ? 0 : int(N - i0 < kSumWave ? N - i0 : kSumWave);
+  const uint32_t none = uint32_t(V);
+  // the wave's keys and positions in its lanes; the keys beside them
+  const int64_t il = n > 0 ? i0 + ((lane & 31) < n ? (lane & 31) : n - 1) : 0;
+  const uint32_t keys = n > 0 ? skey[il] : none, poss = n > 0 ? spos[il] : 0;
+  const uint32_t before = i0 > 0 && n > 0 ? skey[i0 - 1] : none;
+  const uint32_t behind = n == kSumWave && i0 + n < N ? skey[i0 + n] : none;
+  auto uni = [](uint32_t x) -> uint32_t { return __builtin_amdgcn_readfirstlane(x); };
+  auto key_of = [&](int q) -> uint32_t { return __builtin_amdgcn_readlane(keys, q); };
+  uint32_t cur = key_of(0);
+  bool head = cur < none && uni(before) == cur;
+  const uint32_t last = n > 0 ? key_of(31) : none;
+  const bool tail = last < none && uni(behind) == last;
   float acc[8] = {};
-  auto flush = [&](bool tail) {
-    if (cur >= uint32_t(V)) return;                // no row: padding, or a bad id
-    if (head || tail) store_cols(part + (2 * wd + (head ? 0 : 1)) * H, c, H, acc);
-    else write_row(dW, int64_t(cur), H, c, scale, accumulate, acc);
+  auto leave = [&](int which) {                    // the run so far, to LDS
+#pragma unroll
+    for (int e = 0; e < 8; ++e) edge[which][w][cl + e] = acc[e];
   };
-  for (int b = 0; b < n; b += kInFlight) {
-    float f[kInFlight][8];
-    uint32_t key[kInFlight];
+  auto add_rows = [&](int q, const float (&f)[kInFlight][8]) {
 #pragma unroll
     for (int r = 0; r < kInFlight; ++r) {
-      const int64_t i = i0 + (b + r < n ? b + r : n - 1);
-      key[r] = key_at(i);
-      if (key[r] >= uint32_t(V)) continue;         // the rows behind the last id
-      load_cols(dout + int64_t(__builtin_amdgcn_readfirstlane(spos[i])) * ldd, c, H, f[r]);
-    }
-#pragma unroll
-    for (int r = 0; r < kInFlight; ++r) {
-      if (b + r >= n || key[r] >= uint32_t(V)) continue;
-      if (key[r] != cur) {
-        flush(false);
-        cur = key[r];
+      const uint32_t key = key_of(q + r);
+      if (q + r >= n || key >= none) continue;
+      if (key != cur) {
+        if (head) leave(0);
+        else write_row(dW, int64_t(cur), H, c, scale, accumulate, acc);
+        cur = key;
         head = false;
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[e] = 0.f;
@@ -370,19 +404,57 @@ __global__ __launch_bounds__(256) void k_embed_sum(
 #pragma unroll
       for (int e = 0; e < 8; ++e) acc[e] += f[r][e];
     }
-    if (key[kInFlight - 1] >= uint32_t(V)) break;  // nothing but such rows from here on
+  };
+#pragma unroll
+  for (int q = 0; q < kSumWave; q += kInFlight) {
+    if (q >= n || key_of(q) >= none) break;        // the rest has no rows
+    float f[kInFlight][8];
+#pragma unroll
+    for (int r = 0; r < kInFlight; ++r)
+      load_cols(dout + int64_t(uint32_t(__builtin_amdgcn_readlane(poss, q + r))) * ldd, c, H, f[r]);
+    add_rows(q, f);
   }
-  flush(i0 + n < N && key_at(i0 + n) == cur);
+  if (cur < none) {
+    if (head) leave(0);
+    else if (tail) leave(1);
+    else write_row(dW, int64_t(cur), H, c, scale, accumulate, acc);
+  }
+  if (lane == 0) {
+    end_key[w] = tail ? last : none;
+    whole[w] = tail && head;                       // head still set: no other id came
+  }
+  __syncthreads();
+  // wave w: the id that began in it and goes on; wave 0 also the one begun before
+  auto join = [&](int from, bool began) {
+    int x = began ? from + 1 : 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] = began ? edge[1][from][cl + e] : 0.f;
+    for (; x < kSumWaves; ++x) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] += edge[0][x][cl + e];
+      if (!whole[x]) break;
+    }
+    return x == kSumWaves;                         // it goes on past the workgroup
+  };
+  if (w == 0 && uni(before) < none && uni(before) == key_of(0) && n > 0) {
+    join(0, false);
+    store_cols(part + 2 * wd * H, c, H, acc);
+  }
+  if (tail && !whole[w]) {
+    if (join(w, true)) store_cols(part + (2 * wd + 1) * H, c, H, acc);
+    else write_row(dW, int64_t(last), H, c, scale, accumulate, acc);
+  }
 }
 
-// The ids that reach past the window they start in: their partial rows added up
-// in window order. A wave per window and slice; most have none and leave.
+// The ids that reach past the workgroup's tokens they begin in: their partial rows
+// added up in order. A wave per kEmbedWindow tokens and slice; most have none.
 template <class G>
 __global__ __launch_bounds__(256) void k_embed_join(const uint32_t* __restrict__ skey, int64_t N,
-                                                    int64_t H, int64_t V, int win, int64_t slices,
+                                                    int64_t H, int64_t V, int64_t slices,
                                                     float scale, int accumulate,
                                                     G* __restrict__ dW,
                                                     const float* __restrict__ part) {
+  constexpr int64_t win = kEmbedWindow;
   const int lane = threadIdx.x & 63;
   const int64_t u = int64_t(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t wd = u / slices, c = (u - wd * slices) * kSliceCols + lane * kLaneCols;
@@ -390,43 +462,51 @@ __global__ __launch_bounds__(256) void k_embed_join(const uint32_t* __restrict__
   if (i1 >= N) return;                             // the last window: nothing behind it
   const uint32_t key = skey[i1 - 1];
   if (key >= uint32_t(V) || skey[i1] != key) return;
-  if (skey[i0] == key && i0 > 0 && skey[i0 - 1] == key) return;   // it started earlier
+  if (skey[i0] == key && i0 > 0 && skey[i0 - 1] == key) return;   // it began earlier
   float acc[8];
   load_cols(part + (2 * wd + 1) * H, c, H, acc);
-  for (int64_t x = wd + 1;; ++x) {
-    float f[8];
-    load_cols(part + 2 * x * H, c, H, f);
+  // the windows behind that begin with this id, their rows loaded eight at a time
+  const int64_t windows = (N + win - 1) / win;
+  bool more = true;
+  for (int64_t x = wd + 1; more; x += kInFlight) {
+    float f[kInFlight][8];
+    uint32_t first[kInFlight];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] += f[e];
-    const int64_t end = (x + 1) * win;
-    if (end >= N || skey[end] != key) break;
+    for (int r = 0; r < kInFlight; ++r) {
+      first[r] = uint32_t(V);
+      if (x + r < windows) {
+        first[r] = skey[(x + r) * win];
+        load_cols(part + 2 * (x + r) * H, c, H, f[r]);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < kInFlight; ++r) {
+      more = more && first[r] == key;
+      if (more) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] += f[r][e];
+      }
+    }
   }
   write_row(dW, int64_t(key), H, c, scale, accumulate, acc);
-}
-
-template <int R>
-void sort_local(const EmbedGradArgs& a, int bits, const Launcher& L) {
-  hipLaunchKernelGGL(k_sort_local<R>, dim3(1), dim3(kSortThreads), 0, L.stream, a.tokens, a.N, a.V,
-                     a.padding, bits, a.key[0], a.pos[0], a.status);
 }
 
 template <class T, class G>
 hipError_t sums(const EmbedGradArgs& a, const uint32_t* key, const uint32_t* pos,
                 const Launcher& L) {
   const int64_t slices = (a.H + kSliceCols - 1) / kSliceCols;
-  const int64_t waves = (a.N + a.window - 1) / a.window * slices;
-  const dim3 grid(unsigned((waves + 3) / 4));
+  const int64_t windows = (a.N + kEmbedWindow - 1) / kEmbedWindow;
   G* dW = static_cast<G*>(a.dW);
   L.pre(kEmbedGrad);
-  hipLaunchKernelGGL((k_embed_sum<T, G>), grid, dim3(256), 0, L.stream, key, pos,
-                     static_cast<const T*>(a.dout), a.ld_dout, a.N, a.H, a.V, int(a.window),
+  hipLaunchKernelGGL((k_embed_sum<T, G>), dim3(unsigned(windows * slices)), dim3(64 * kSumWaves), 0,
+                     L.stream, key, pos, static_cast<const T*>(a.dout), a.ld_dout, a.N, a.H, a.V,
                      slices, a.scale, a.accumulate, dW, a.part);
   L.post(kEmbedGrad);
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess || a.N <= a.window) return e;
+  if (e != hipSuccess || windows == 1) return e;
   L.pre(kEmbedGrad);
-  hipLaunchKernelGGL(k_embed_join<G>, grid, dim3(256), 0, L.stream, key, a.N, a.H, a.V,
-                     int(a.window), slices, a.scale, a.accumulate, dW, a.part);
+  hipLaunchKernelGGL(k_embed_join<G>, dim3(unsigned((windows * slices + 3) / 4)), dim3(256), 0,
+                     L.stream, key, a.N, a.H, a.V, slices, a.scale, a.accumulate, dW, a.part);
   L.post(kEmbedGrad);
   return hipGetLastError();
 }
@@ -470,16 +550,27 @@ hipError_t launch_embedding_backward(const EmbedGradArgs& a, const Launcher& L) 
   }
   int bits = 1;
   while (bits < 32 && (int64_t(1) << bits) <= a.V) ++bits;   // keys 0 .. V
+  if (a.status) e = launch_token_status(a.tokens, a.N, a.V, a.padding, a.status, L);
+  if (e != hipSuccess) return e;
   int at = 0;
-  if (a.N <= kSortLocal) {
+  if (a.N <= kSortMerge) {
+    const int64_t chunks = (a.N + kSortChunk - 1) / kSortChunk;
     L.pre(kEmbedSort);
-    if (a.N <= kSortThreads) sort_local<1>(a, bits, L);
-    else if (a.N <= 4 * kSortThreads) sort_local<4>(a, bits, L);
-    else sort_local<16>(a, bits, L);
+    hipLaunchKernelGGL(k_sort_chunks, dim3(unsigned(chunks)), dim3(kSortThreads), 0, L.stream,
+                       a.tokens, a.N, a.V, a.padding, bits, a.key[0], a.pos[0]);
+    auto merge = [&](auto c) {
+      hipLaunchKernelGGL(k_sort_merge<decltype(c)::value>, dim3(unsigned(4 * chunks)), dim3(256), 0,
+                         L.stream, a.key[0], a.pos[0], a.N, a.key[1], a.pos[1]);
+    };
+    if (chunks > 1) {
+      if (chunks <= 4) merge(std::integral_constant<int, 4>{});
+      else if (chunks <= 16) merge(std::integral_constant<int, 16>{});
+      else merge(std::integral_constant<int, 32>{});
+      at = 1;
+    }
     L.post(kEmbedSort);
     e = hipGetLastError();
   } else {
-    if (a.status) e = launch_token_status(a.tokens, a.N, a.V, a.padding, a.status, L);
     const int64_t nb = (a.N + kSortBlock - 1) / kSortBlock;
     const dim3 grid{unsigned(nb)};
     for (int shift = 0; e == hipSuccess && shift < bits; shift += 8) {

@@ -233,21 +233,14 @@ hipError_t f32_backward_chunk(const Plan& p, const Args& a, int64_t chunk, const
                      static_cast<const float*>(a.W), static_cast<const float*>(a.h), a.labels,
                      a.lse, a.sc, p.N, p.H, p.V, a.ignore_index, a.softcap, v0, vcur, p.ldg, gt);
   L.post(kGradLogits);
-  const hipError_t e = hipGetLastError();
+  hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  return f32_chunk_products(p, a, chunk, L);
-}
-
-hipError_t f32_chunk_products(const Plan& p, const Args& a, int64_t chunk, const Launcher& L) {
-  const int64_t v0 = chunk * p.vchunk;
-  const int64_t vcur = (p.V - v0) < p.vchunk ? (p.V - v0) : p.vchunk;
-  const float* gt = static_cast<const float*>(a.g);
   L.pre(kGemmDW);
   hipLaunchKernelGGL(k_f32_dw, dim3(cdiv(vcur, kT), cdiv(p.H, kT)), dim3(256), 0, L.stream, gt,
                      static_cast<const float*>(a.h), p.N, p.H, p.ldg, v0, vcur, a.accumulate_dW,
                      static_cast<float*>(a.dW));
   L.post(kGemmDW);
-  const hipError_t e = hipGetLastError();
+  e = hipGetLastError();
   if (e != hipSuccess) return e;
   L.pre(kGemmDH);
   hipLaunchKernelGGL(k_f32_dh, dim3(cdiv(p.N, kT), cdiv(p.H, kT)), dim3(256), 0, L.stream, gt,

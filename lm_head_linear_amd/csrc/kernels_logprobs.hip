@@ -9,8 +9,7 @@
 // so that  lse = M + log S,  log p_y = (x_y - M) - log S,  entropy = log S - D / S.
 // log S is taken apart from M: a token that holds nearly all of the probability
 // keeps its small log probability. Alternatives are ranked by the raw logit z (the
-// order of x, without the ties that rounding x makes), equal ones by lowest id:
-// each tile leaves its kc largest, sorted, and the join merges the lists.
+// order of x, without the ties that rounding x makes), equal ones by lowest id.
 //
 // Three kernels compute logits:
 //  - the 256 x 256 bf16 tiles of the head's own forward (gemm_bf16.h), live tokens
@@ -18,7 +17,11 @@
 //  - few bf16 tokens: 64 vocabulary rows a workgroup, W streamed from memory
 //    straight into the matrix cores' operand registers: bound by reading W once;
 //  - float32: 64 x 64 tiles on the float32 matrix instruction.
-// Logits are never stored in device memory.
+// The 256 x 256 tiles never store a logit; each leaves its top_k largest logits
+// that could still be listed, sorted, and the join merges those lists. The two
+// kernels of 64 vocabulary rows store the logits of their few tokens (N V 4 bytes
+// next to the V H 2 of W) and each tile's largest; the join then looks only into
+// the top_k tiles of the largest, which hold all top_k alternatives.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -29,6 +32,7 @@
 #include "gemm_bf16.h"
 #include "ops_plan.h"
 #include "row_io.h"
+#include "wave_ops.h"
 
 namespace flce {
 namespace {
@@ -61,31 +65,35 @@ struct LpOut {
   float2* part;               // m, s
   float* pd;                  // d
   float* zt;                  // x of the given token, one writer per token
-  float* cv;                  // candidates: raw logit, -inf behind the last
-  uint8_t* ci;                //   and its row within the list
+  float* cv;                  // 256 x 256 tiles: candidates, -inf behind the last,
+  uint8_t* ci;                //   and their rows within the list
+  float* zmax;                // 64-row tiles: the largest raw logit
+  float* z;                   //   and all of them, [token][vocabulary]; null: not wanted
   int64_t sp, st, cl, ck, ct;
   int kc;
 };
 
-__device__ __forceinline__ uint32_t min4(uint32_t x) {
-  // min over the four lanes of an accumulator column (see col_max4)
+// x summed over the lanes of this column with a smaller g (lane / 16).
+__device__ __forceinline__ int before_rows(int x, int g) {
+  int at = 0;
 #if defined(__HIP_DEVICE_COMPILE__)
-  const auto a = __builtin_amdgcn_permlane16_swap(x, x, false, false);
-  x = a[0] < a[1] ? a[0] : a[1];
-  const auto b = __builtin_amdgcn_permlane32_swap(x, x, false, false);
-  x = b[0] < b[1] ? b[0] : b[1];
+  const auto a = __builtin_amdgcn_permlane16_swap(uint32_t(x), uint32_t(x), false, false);
+  const uint32_t pair = a[0] + a[1];
+  const auto b = __builtin_amdgcn_permlane32_swap(pair, pair, false, false);
+  at = int(((g & 1) ? a[0] : 0u) + ((g & 2) ? b[0] : 0u));
 #endif
-  return x;
+  return at;
 }
 
 // ---- epilogue of the 256 x 256 tiles ----------------------------------------------
 // The accumulators are raw logits, tile rows vocabulary ids, columns tokens (see
 // EpiLse for the layout). The two waves of a column join their (m, s, d) through
 // LDS; each wave leaves candidates of its own 128 rows. A candidate has to exceed
-// tau, the token's kc-th largest logit among lower ids (-inf before any are known):
-// an equal one with a higher id could not be listed either. Each round takes the
-// column's largest logit left, lowest row first, in the four lanes that hold the
-// column; a wave stops when none of its 16 columns has one left.
+// tau, the token's kc-th largest logit among lower ids: an equal one with a higher
+// id could not be listed either. Few do, so the wave counts them and stores them in
+// any order. Without a tau yet, or with more of them than the list holds, a column's
+// kc largest are taken in rounds: the largest logit left, lowest row first, in the
+// four lanes that hold the column; a wave stops when none of its 16 columns has one.
 template <bool SOFTCAP, bool TOPK>
 struct EpiLp {
   const int64_t* labels;      // null: no given tokens
@@ -162,36 +170,66 @@ struct EpiLp {
       dm[j] = col_sum4(d);
       if (TOPK && live > 0) {                      // rows past V have no list
         const float th = tau ? tau_t[acc_col(wn, j, lane)] : -INFINITY;
-        float z[8][4];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) z[i][r] = in(i, r) ? acc[i][j][r] : -INFINITY;
         const int64_t list = (vbase >> 7) * out.cl + t * out.ct;
         int n = 0;
-        for (; n < out.kc; ++n) {
-          float b = -INFINITY;
+        bool rounds = tau == nullptr;
+        // x rises with z: no x as large as that of tau, no logit above tau
+        if (tau && (SOFTCAP || __ballot(t < N && m >= th * warp.inv_t) != 0)) {
+          int own = 0;                               // this lane's logits above tau
 #pragma unroll
           for (int i = 0; i < 8; ++i)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) b = fmaxf(b, z[i][r]);
-          b = col_max4(b);
-          const bool go = b > th && t < N;
-          if (__ballot(go) == 0) break;
-          uint32_t row = 255;
+            for (int r = 0; r < 4; ++r) own += in(i, r) && acc[i][j][r] > th ? 1 : 0;
+          own = t < N ? own : 0;
+          int at = before_rows(own, g);
+          n = rows_all(own, AddOp());
+          rounds = __ballot(n > out.kc) != 0;
+          if (!rounds && own > 0) {
 #pragma unroll
-          for (int i = 7; i >= 0; --i)
+            for (int i = 0; i < 8; ++i)
 #pragma unroll
-            for (int r = 3; r >= 0; --r) row = z[i][r] == b ? uint32_t(i * 16 + 4 * g + r) : row;
-          row = min4(row);
-          const int mine = int(row) - 4 * g;         // the lane's register of that row
+              for (int r = 0; r < 4; ++r)
+                if (in(i, r) && acc[i][j][r] > th) {
+                  out.cv[list + at * out.ck] = acc[i][j][r];
+                  out.ci[list + at * out.ck] = uint8_t(i * 16 + 4 * g + r);
+                  ++at;
+                }
+          }
+        }
+        if (rounds) {
+          float z[8][4];
 #pragma unroll
           for (int i = 0; i < 8; ++i)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) z[i][r] = mine == i * 16 + r ? -INFINITY : z[i][r];
-          if (g == 0 && t < N) {
-            out.cv[list + n * out.ck] = go ? b : -INFINITY;
-            out.ci[list + n * out.ck] = uint8_t(row);
+            for (int r = 0; r < 4; ++r) z[i][r] = in(i, r) ? acc[i][j][r] : -INFINITY;
+          for (n = 0; n < out.kc; ++n) {
+            float bq[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              bq[r] = z[0][r];
+#pragma unroll
+              for (int i = 1; i < 8; ++i) bq[r] = fmaxf(bq[r], z[i][r]);
+            }
+            const float b = col_max4(fmaxf(fmaxf(bq[0], bq[1]), fmaxf(bq[2], bq[3])));
+            const bool go = b > th && t < N;
+            if (__ballot(go) == 0) break;
+            uint32_t rq[4] = {255, 255, 255, 255};
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+              for (int i = 7; i >= 0; --i)
+                rq[r] = z[i][r] == b ? uint32_t(i * 16 + 4 * g + r) : rq[r];
+            MinOp least;
+            const uint32_t row = rows_all(least(least(rq[0], rq[1]), least(rq[2], rq[3])), least);
+            const int mine = int(row) - 4 * g;       // the lane's register of that row
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+              for (int r = 0; r < 4; ++r) z[i][r] = mine == i * 16 + r ? -INFINITY : z[i][r];
+            if (g == 0 && t < N) {
+              out.cv[list + n * out.ck] = go ? b : -INFINITY;
+              out.ci[list + n * out.ck] = uint8_t(row);
+            }
           }
         }
         if (n < out.kc && g == 0 && t < N) out.cv[list + n * out.ck] = -INFINITY;
@@ -238,81 +276,67 @@ struct EpiLp {
 };
 
 // ---- epilogue of the 64-row tiles ---------------------------------------------------
-// z[e] is the raw logit of row e TPT + q (q = this lane's place among the TPT
-// adjacent lanes of token t) of the 64 vocabulary rows from v0; `live` of them exist.
+// z[e] is the raw logit of row q E + e (q = this lane's place among the TPT adjacent
+// lanes of token t, E = 64 / TPT) of the 64 vocabulary rows from v0; `live` exist.
 template <int TPT, bool SOFTCAP>
-__device__ __forceinline__ void tile_epilogue(float (&z)[64 / TPT], int q, int64_t t, int64_t N,
-                                              const int64_t* labels, int64_t v0, int live,
-                                              const Warp& warp, const LpOut& out) {
+__device__ __forceinline__ void tile_epilogue(const float (&z)[64 / TPT], int q, int64_t t,
+                                              int64_t N, const int64_t* labels, int64_t v0,
+                                              int live, int64_t V, const Warp& warp,
+                                              const LpOut& out) {
   constexpr int E = 64 / TPT;
-  const int64_t list = v0 / 64;
   const bool tok = t < N;
+  const int n = live - q * E;                      // rows of this lane that exist
   float x[E];
-  float m = -INFINITY;
+  float m = -INFINITY, zm = -INFINITY;
 #pragma unroll
   for (int e = 0; e < E; ++e) {
     x[e] = warp_logit<SOFTCAP>(warp, z[e]);
-    if (e * TPT + q < live) m = fmaxf(m, x[e]);
-    else z[e] = -INFINITY;
+    m = fmaxf(m, e < n ? x[e] : -INFINITY);
+    zm = fmaxf(zm, e < n ? z[e] : -INFINITY);
   }
-#pragma unroll
-  for (int o = TPT / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+  m = group_all<TPT>(m, MaxOp());
   float s = 0.f, d = 0.f;
   const float mb = m * kLog2e;
 #pragma unroll
   for (int e = 0; e < E; ++e) {
     float u = fmaf(x[e], kLog2e, -mb);
-    u = (e * TPT + q < live && m != -INFINITY && u != -INFINITY) ? u : -200.f;
+    u = (e < n && m != -INFINITY && u != -INFINITY) ? u : -200.f;
     const float p = __builtin_amdgcn_exp2f(u);
     s += p;
     d = fmaf(p, u, d);
   }
-  d *= kLn2;
-#pragma unroll
-  for (int o = TPT / 2; o > 0; o >>= 1) {
-    s += __shfl_xor(s, o);
-    d += __shfl_xor(d, o);
-  }
+  s = group_all<TPT>(s, AddOp());
+  d = group_all<TPT>(d * kLn2, AddOp());
+  const int64_t at = (v0 / 64) * out.sp + t * out.st;
   if (tok && q == 0) {
-    out.part[list * out.sp + t * out.st] = make_float2(m, s);
-    out.pd[list * out.sp + t * out.st] = d;
+    out.part[at] = make_float2(m, s);
+    out.pd[at] = d;
   }
   if (labels && tok) {
     const int64_t y = labels[t] - v0;
-    if (y >= 0 && y < live && int(y) % TPT == q) {
+    if (y >= 0 && y < live && int(y) / E == q) {
       float val = 0.f;
 #pragma unroll
-      for (int e = 0; e < E; ++e) val = int(y) / TPT == e ? x[e] : val;
+      for (int e = 0; e < E; ++e) val = int(y) % E == e ? x[e] : val;
       out.zt[t] = val;
     }
   }
-  if (out.kc == 0) return;
-  const int64_t at = list * out.cl + t * out.ct;
-  int n = 0;
-  for (; n < out.kc; ++n) {
-    float b = -INFINITY;
+  if (!out.z) return;
+  zm = group_all<TPT>(zm, MaxOp());
+  if (!tok) return;
+  if (q == 0) out.zmax[at] = zm;
+  float* row = out.z + t * V + v0 + q * E;
 #pragma unroll
-    for (int e = 0; e < E; ++e) b = fmaxf(b, z[e]);
+  for (int e = 0; e < E; e += 4) {
+    if (e + 4 <= n) {
+      const float f[4] = {z[e], z[e + 1], z[e + 2], z[e + 3]};
+      store_chunk(row, e, int64_t(e + 4), f);
+    } else {
 #pragma unroll
-    for (int o = TPT / 2; o > 0; o >>= 1) b = fmaxf(b, __shfl_xor(b, o));
-    const bool go = b > -INFINITY && tok;
-    if (__ballot(go) == 0) break;
-    int row = 255;
-#pragma unroll
-    for (int e = E - 1; e >= 0; --e) row = z[e] == b ? e * TPT + q : row;
-#pragma unroll
-    for (int o = TPT / 2; o > 0; o >>= 1) {
-      const int other = __shfl_xor(row, o);
-      row = other < row ? other : row;
-    }
-#pragma unroll
-    for (int e = 0; e < E; ++e) z[e] = row == e * TPT + q ? -INFINITY : z[e];
-    if (q == 0 && tok) {
-      out.cv[at + n * out.ck] = go ? b : -INFINITY;
-      out.ci[at + n * out.ck] = uint8_t(row);
+      for (int i = e; i < e + 4; ++i)
+        if (i < n) row[i] = z[i];
     }
   }
-  if (n < out.kc && q == 0 && tok) out.cv[at + n * out.ck] = -INFINITY;
 }
 
 // ---- few tokens -----------------------------------------------------------------------
@@ -394,15 +418,17 @@ __global__ __launch_bounds__(256) void k_lp_few(const uint16_t* __restrict__ h,
     for (int i = 0; i < 4; ++i)
       *reinterpret_cast<f32x4*>(&zb[w][j * 16 + r][i * 16 + (lane >> 4) * 4]) = acc[i][j];
   __syncthreads();
-  constexpr int TPT = 256 / (16 * NT), E = 64 / TPT;
+  constexpr int TPT = NT == 3 ? 4 : 256 / (16 * NT), E = 64 / TPT;
   const int t = tid / TPT, q = tid % TPT;
+  if (t >= 16 * NT) return;                        // NT = 3: whole waves
   float z[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    const int row = e * TPT + q;
+    const int row = q * E + e;
     z[e] = (zb[0][t][row] + zb[1][t][row]) + (zb[2][t][row] + zb[3][t][row]);
   }
-  tile_epilogue<TPT, SOFTCAP>(z, q, t, N, labels, v0, int(V - v0 < 64 ? V - v0 : 64), warp, out);
+  tile_epilogue<TPT, SOFTCAP>(z, q, t, N, labels, v0, int(V - v0 < 64 ? V - v0 : 64), V, warp,
+                              out);
 }
 
 // ---- float32 --------------------------------------------------------------------------
@@ -492,8 +518,8 @@ __global__ __launch_bounds__(256) void k_lp_f32(const float* __restrict__ h,
   const int tl = threadIdx.x >> 2, q = threadIdx.x & 3;
   float v[16];
 #pragma unroll
-  for (int e = 0; e < 16; ++e) v[e] = z[tl][e * 4 + q];
-  tile_epilogue<4, SOFTCAP>(v, q, t0 + tl, N, labels, v0, int(V - v0 < 64 ? V - v0 : 64), warp,
+  for (int e = 0; e < 16; ++e) v[e] = z[tl][q * 16 + e];
+  tile_epilogue<4, SOFTCAP>(v, q, t0 + tl, N, labels, v0, int(V - v0 < 64 ? V - v0 : 64), V, warp,
                             out);
 }
 
@@ -543,16 +569,20 @@ __device__ __forceinline__ void join_part(float& M, float& S, float& D, float m,
   M = Mn;
 }
 
-// Many tokens: 32 tokens a workgroup, 8 threads each taking every 8th part and list
-// of its token, then the eight in order. A thread's sorted candidates live in LDS.
+// Many tokens: 32 tokens a workgroup and G threads for each, thread g taking every
+// G-th part and list, then the threads pairwise. A thread's sorted candidates live
+// in LDS, so G goes by top_k: 32 up to 16 alternatives (128 KiB), 16 beyond. With
+// TAU_ONLY just the top_k-th largest logit of the lists so far.
 constexpr int kJoinTokens = 32;
+constexpr int kAhead = 4;                          // loads in flight
 
-template <bool SOFTCAP, bool TAU_ONLY, int KM>     // top_k <= KM
-__global__ __launch_bounds__(256) void k_lp_join(JoinArgs a, float* __restrict__ tau) {
-  __shared__ float lv[KM * 256];                   // [top_k][256]
-  __shared__ int32_t li[KM * 256];
-  __shared__ float4 grp[8][kJoinTokens];
-  __shared__ int cnt[256];
+template <bool SOFTCAP, bool TAU_ONLY, int G, int KM>     // top_k <= KM
+__global__ __launch_bounds__(32 * G) void k_lp_join(JoinArgs a, float* __restrict__ tau) {
+  constexpr int kT = 32 * G;
+  __shared__ float lv[KM * kT];                    // [top_k][thread]
+  __shared__ int32_t li[KM * kT];
+  __shared__ float4 grp[kT];
+  __shared__ int cnt[kT];
   const int tid = threadIdx.x, tk = tid % kJoinTokens, g = tid / kJoinTokens;
   const int64_t t = int64_t(blockIdx.x) * kJoinTokens + tk;
   int64_t n_live = a.N;
@@ -561,18 +591,27 @@ __global__ __launch_bounds__(256) void k_lp_join(JoinArgs a, float* __restrict__
   const int K = a.top_k;
   float M = -INFINITY, S = 0.f, D = 0.f;
   if (!TAU_ONLY && live) {
-    for (int64_t p = g; p < a.parts; p += 8) {
-      const int64_t at = p * a.in.sp + t * a.in.st;
-      const float2 ms = a.in.part[at];
-      join_part(M, S, D, ms.x, ms.y, a.in.pd[at]);
+    for (int64_t p = g; p < a.parts; p += kAhead * G) {
+      float2 ms[kAhead];
+      float d[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int64_t at = (p + u * G < a.parts ? p + u * G : p) * a.in.sp + t * a.in.st;
+        ms[u] = a.in.part[at];
+        d[u] = a.in.pd[at];
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+        if (p + u * G < a.parts) join_part(M, S, D, ms[u].x, ms[u].y, d[u]);
     }
   }
   int n = 0;
-  // v behind n sorted candidates of this thread, at its place; the last drops out
+  // (v, id) at its place among the n sorted candidates of this thread; the last one
+  // drops out of a full list. False if it ranks behind all of a full list.
   auto insert = [&](float v, int32_t id) {
     auto after = [&](int k) {                      // candidate k ranks behind (v, id)
-      const float o = lv[k * 256 + tid];
-      return o < v || (o == v && li[k * 256 + tid] > id);
+      const float o = lv[k * kT + tid];
+      return o < v || (o == v && li[k * kT + tid] > id);
     };
     if (n == K) {
       if (!after(K - 1)) return false;
@@ -580,62 +619,69 @@ __global__ __launch_bounds__(256) void k_lp_join(JoinArgs a, float* __restrict__
     }
     int k = n;
     while (k > 0 && after(k - 1)) {
-      lv[k * 256 + tid] = lv[(k - 1) * 256 + tid];
-      li[k * 256 + tid] = li[(k - 1) * 256 + tid];
+      lv[k * kT + tid] = lv[(k - 1) * kT + tid];
+      li[k * kT + tid] = li[(k - 1) * kT + tid];
       --k;
     }
-    lv[k * 256 + tid] = v;
-    li[k * 256 + tid] = id;
+    lv[k * kT + tid] = v;
+    li[k * kT + tid] = id;
     ++n;
     return true;
   };
-  if (K > 0) {
-    if (live) {
-      for (int64_t l = g; l < a.lists; l += 8) {
-        const int64_t at = l * a.in.cl + t * a.in.ct;
-        for (int k = 0; k < a.in.kc; ++k) {
-          const float v = a.in.cv[at + k * a.in.ck];
-          if (!(v > -INFINITY)) break;
-          if (!insert(v, int32_t(l * a.list_rows + a.in.ci[at + k * a.in.ck]))) break;
+  if (K > 0 && live) {
+    for (int64_t l = g; l < a.lists; l += kAhead * G) {
+      float head[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+        head[u] = l + u * G < a.lists ? a.in.cv[(l + u * G) * a.in.cl + t * a.in.ct] : -INFINITY;
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int64_t at = (l + u * G) * a.in.cl + t * a.in.ct;
+        float v = head[u];
+        for (int k = 0; v > -INFINITY;) {
+          insert(v, int32_t((l + u * G) * a.list_rows + a.in.ci[at + k * a.in.ck]));
+          v = ++k < a.in.kc ? a.in.cv[at + k * a.in.ck] : -INFINITY;
         }
       }
     }
-    for (int half = 4; half > 0; half >>= 1) {
-      cnt[tid] = n;
-      __syncthreads();
-      if (g < half) {
-        const int o = tid + half * kJoinTokens;
-        for (int k = 0; k < cnt[o]; ++k)
-          if (!insert(lv[k * 256 + o], li[k * 256 + o])) break;
-      }
-      __syncthreads();
-    }
-    if (TAU_ONLY) {
-      if (g == 0 && t < a.N) tau[t] = (live && n == K) ? lv[(K - 1) * 256 + tid] : -INFINITY;
-      return;
-    }
   }
-  grp[g][tk] = make_float4(M, S, D, 0.f);
-  __syncthreads();
-  if (g == 0 && t < a.N) {
-    M = -INFINITY; S = 0.f; D = 0.f;
-    for (int i = 0; i < 8; ++i) join_part(M, S, D, grp[i][tk].x, grp[i][tk].y, grp[i][tk].z);
-    const int64_t o = a.idx ? int64_t(a.idx[t]) : t;
-    const bool shown = live && (!a.labels || a.labels[t] != a.ignore_index);
-    write_token(a, t, o, shown, M, S, D);
-    const float ls = logf(S);
-    for (int k = 0; k < K; ++k) {
-      const bool has = shown && k < n;
-      write_alternative(a, o, k, has ? warp_logit<SOFTCAP>(a.warp, lv[k * 256 + tid]) : 0.f,
-                        has ? int64_t(li[k * 256 + tid]) : -1, M, ls);
+  grp[tid] = make_float4(M, S, D, 0.f);
+  for (int half = G / 2; half > 0; half >>= 1) {
+    cnt[tid] = n;
+    __syncthreads();
+    if (g < half) {
+      const int o = tid + half * kJoinTokens;
+      const float4 f = grp[o];
+      join_part(M, S, D, f.x, f.y, f.z);
+      grp[tid] = make_float4(M, S, D, 0.f);
+      for (int k = 0; k < cnt[o]; ++k)
+        if (!insert(lv[k * kT + o], li[k * kT + o])) break;
     }
+    __syncthreads();
+  }
+  if (g != 0 || t >= a.N) return;
+  if (TAU_ONLY) {
+    tau[t] = (live && n == K) ? lv[(K - 1) * kT + tid] : -INFINITY;
+    return;
+  }
+  const int64_t o = a.idx ? int64_t(a.idx[t]) : t;
+  const bool shown = live && (!a.labels || a.labels[t] != a.ignore_index);
+  write_token(a, t, o, shown, M, S, D);
+  const float ls = logf(S);
+  for (int k = 0; k < K; ++k) {
+    const bool has = shown && k < n;
+    write_alternative(a, o, k, has ? warp_logit<SOFTCAP>(a.warp, lv[k * kT + tid]) : 0.f,
+                      has ? int64_t(li[k * kT + tid]) : -1, M, ls);
   }
 }
 
-// Few tokens: a workgroup joins one token. Every thread holds the heads of up to
-// LPT sorted lists as 64-bit keys (the logit's order, then the lower id first);
-// each round takes the workgroup's largest and moves that list on.
+// A workgroup joins one token of 64-row tiles. The top_k of any grouped keys lie in
+// the top_k groups of the largest keys, so the alternatives are found in two or three
+// selections: of tiles (of threads, each with several tiles, and then of their tiles
+// beyond 2048 tiles), then of the logits of those tiles. A key is a logit's order and
+// then the lower id, so keys are distinct.
 constexpr int kFewThreads = 1024;
+constexpr int kSelMax = 2 * kFewThreads;           // keys of a selection
 
 __device__ __forceinline__ uint64_t rank_key(float v, int64_t id) {
   if (!(v > -INFINITY)) return 0;                  // none
@@ -647,69 +693,122 @@ __device__ __forceinline__ float key_value(uint64_t k) {
   const uint32_t o = uint32_t(k >> 32);
   return __uint_as_float((o >> 31) ? o & 0x7fffffffu : ~o);
 }
+__device__ __forceinline__ int64_t key_id(uint64_t k) { return int64_t(uint32_t(~uint32_t(k))); }
 __device__ __forceinline__ uint64_t max_u64(uint64_t a, uint64_t b) { return a > b ? a : b; }
 
-template <bool SOFTCAP, int LPT>
+struct Select {
+  uint64_t group[64];          // the largest key of each 16 threads
+  uint64_t bound;              // the K-th largest of those, or 1
+  int count;
+  uint64_t list[kSelMax];      // the keys from the bound up
+  uint64_t won[kLpTop];        // the K largest, in order; 0 behind the last
+};
+
+// The K <= 32 largest of the workgroup's keys (two a thread) in st.won: at least K
+// keys reach the K-th largest of the 64 groups' largest, and usually few more; those
+// are gathered and each counts the larger ones. Ends with a barrier.
+__device__ __forceinline__ void select_keys(uint64_t a, uint64_t b, int K, Select& st) {
+  const int tid = threadIdx.x;
+  const uint64_t m = max_u64(a, b);
+  const uint32_t hi = group_all<16>(uint32_t(m >> 32), MaxOp());
+  const uint32_t lo = group_all<16>(uint32_t(m >> 32) == hi ? uint32_t(m) : 0u, MaxOp());
+  if ((tid & 15) == 0) st.group[tid >> 4] = (uint64_t(hi) << 32) | lo;
+  if (tid < kLpTop) st.won[tid] = 0;
+  if (tid == 0) { st.count = 0; st.bound = 1; }
+  __syncthreads();
+  if (tid < 64) {
+    const uint64_t k = st.group[tid];
+    int above = 0;
+    for (int i = 0; i < 64; ++i) above += st.group[i] > k ? 1 : 0;
+    if (k != 0 && above == K - 1) st.bound = k;
+  }
+  __syncthreads();
+  const uint64_t bound = st.bound;
+  if (a >= bound) st.list[atomicAdd(&st.count, 1)] = a;     // any order: they are ranked
+  if (b >= bound) st.list[atomicAdd(&st.count, 1)] = b;
+  __syncthreads();
+  const int n = st.count;
+  for (int i = tid; i < n; i += kFewThreads) {
+    const uint64_t k = st.list[i];
+    int above = 0;
+    for (int o = 0; o < n && above < K; ++o) above += st.list[o] > k ? 1 : 0;
+    if (above < K) st.won[above] = k;
+  }
+  __syncthreads();
+}
+
+template <bool SOFTCAP>
 __global__ __launch_bounds__(kFewThreads) void k_lp_join_few(JoinArgs a) {
   constexpr int kWaves = kFewThreads / 64;
   __shared__ float red[3][kWaves];
-  __shared__ uint64_t best[2][kWaves];
-  __shared__ uint64_t won[kLpTop];
+  __shared__ Select st;
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
   const int64_t t = blockIdx.x;
   const bool live = !a.labels || a.labels[t] != a.ignore_index;
   const float2* part = a.in.part + t * a.in.st;
   const float* pd = a.in.pd + t * a.in.st;
+  const float* zmax = a.in.zmax + t * a.in.st;
+  const int K = a.top_k;
   float M = -INFINITY, S = 0.f, D = 0.f;
-  for (int64_t p = tid; p < a.parts; p += kFewThreads)
-    join_part(M, S, D, part[p].x, part[p].y, pd[p]);
+  uint64_t best[2] = {0, 0};                       // this thread's tiles, or the best of them
+  const bool direct = a.parts <= kSelMax;
+  auto tile_key = [&](int64_t p) -> uint64_t { return p < a.parts ? rank_key(zmax[p], p) : 0; };
+  for (int64_t p = tid; p < a.parts; p += 2 * kFewThreads) {
+    const int64_t p1 = p + kFewThreads < a.parts ? p + kFewThreads : p;
+    const float2 m0 = part[p], m1 = part[p1];
+    const float d0 = pd[p], d1 = pd[p1];
+    if (K > 0) {
+      const uint64_t k0 = tile_key(p), k1 = tile_key(p + kFewThreads);
+      best[0] = max_u64(best[0], direct ? k0 : max_u64(k0, k1));
+      if (direct) best[1] = k1;
+    }
+    join_part(M, S, D, m0.x, m0.y, d0);
+    if (p1 != p) join_part(M, S, D, m1.x, m1.y, d1);
+  }
+  const float Mw = wave_all(M, MaxOp());
+  const float f = M == -INFINITY ? 0.f : exp2f((M - Mw) * kLog2e);
+  D = wave_all(M == -INFINITY ? 0.f : f * fmaf(M - Mw, S, D), AddOp());
+  S = wave_all(S == 0.f ? 0.f : S * f, AddOp());
+  if (lane == 0) { red[0][w] = Mw; red[1][w] = S; red[2][w] = D; }
+  if (K > 0) {
+    select_keys(best[0], best[1], K, st);
+    if (!direct) {
+      // the tiles of the threads that won: key_id % kFewThreads names the thread
+      const int per = int((a.parts + kFewThreads - 1) / kFewThreads);
+      uint64_t c[2] = {0, 0};
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1)
-    join_part(M, S, D, __shfl_xor(M, o), __shfl_xor(S, o), __shfl_xor(D, o));
-  if (lane == 0) { red[0][w] = M; red[1][w] = S; red[2][w] = D; }
-  // heads of the lists
-  uint64_t head[LPT];
-  int pos[LPT];
-  const float* cv = a.in.cv + t * a.in.ct;
-  const uint8_t* ci = a.in.ci + t * a.in.ct;
-  auto key_of = [&](int j, int k) -> uint64_t {
-    const int64_t l = tid + int64_t(j) * kFewThreads;
-    if (k >= a.in.kc || l >= a.lists) return 0;
-    const int64_t at = l * a.in.cl + k * a.in.ck;
-    return rank_key(cv[at], l * a.list_rows + ci[at]);
-  };
-  if (a.top_k > 0) {
+      for (int j = 0; j < 2; ++j) {
+        const int i = tid + j * kFewThreads;
+        if (i < K * per && st.won[i / per] != 0)
+          c[j] = tile_key(key_id(st.won[i / per]) % kFewThreads + int64_t(i % per) * kFewThreads);
+      }
+      __syncthreads();                             // the winners are read
+      select_keys(c[0], c[1], K, st);
+    }
+    // the logits of the K tiles
+    uint64_t c[2] = {0, 0};
 #pragma unroll
-    for (int j = 0; j < LPT; ++j) { head[j] = key_of(j, 0); pos[j] = 0; }
-    for (int k = 0; k < a.top_k; ++k) {
-      uint64_t b = 0;
-#pragma unroll
-      for (int j = 0; j < LPT; ++j) b = max_u64(b, head[j]);
-      uint64_t m = b;
-#pragma unroll
-      for (int o = 32; o > 0; o >>= 1) m = max_u64(m, __shfl_xor(m, o));
-      if (lane == 0) best[k & 1][w] = m;
-      __syncthreads();
-      m = 0;
-#pragma unroll
-      for (int i = 0; i < kWaves; ++i) m = max_u64(m, best[k & 1][i]);
-      if (tid == 0) won[k] = m;
-      if (b == m && m != 0) {                      // keys are distinct: one thread
-#pragma unroll
-        for (int j = 0; j < LPT; ++j)
-          if (head[j] == m) head[j] = key_of(j, ++pos[j]);
+    for (int j = 0; j < 2; ++j) {
+      const int i = tid + j * kFewThreads;
+      if (i < K * 64 && st.won[i / 64] != 0) {
+        const int64_t v = key_id(st.won[i / 64]) * 64 + i % 64;
+        if (v < a.V) c[j] = rank_key(a.in.z[t * a.V + v], v);
       }
     }
+    __syncthreads();
+    select_keys(c[0], c[1], K, st);
+  } else {
+    __syncthreads();
   }
-  __syncthreads();
+  if (tid >= (K > 0 ? K : 1)) return;
   M = -INFINITY; S = 0.f; D = 0.f;
   for (int i = 0; i < kWaves; ++i) join_part(M, S, D, red[0][i], red[1][i], red[2][i]);
   if (tid == 0) write_token(a, t, t, live, M, S, D);
-  if (tid < a.top_k) {
-    const uint64_t m = won[tid];
+  if (K > 0) {
+    const uint64_t m = st.won[tid];
     const bool has = live && m != 0;
     write_alternative(a, t, tid, has ? warp_logit<SOFTCAP>(a.warp, key_value(m)) : 0.f,
-                      has ? int64_t(uint32_t(~uint32_t(m))) : -1, M, logf(S));
+                      has ? key_id(m) : -1, M, logf(S));
   }
 }
 
@@ -851,27 +950,141 @@ __global__ __launch_bounds__(256) void k_lp_f32_grad(
   }
 }
 
+// float32 products of a chunk's G^T [rows][ldg] on the float32 matrix instruction,
+// 64 x 64 tiles as above:
+//   DW:  C[m][n] = sum_t G^T[m][t] h[t][n]     (m vocabulary rows, K = tokens)
+//   !DW: C[t][n] = sum_m G^T[m][t] W[m][n]     (K = the chunk's vocabulary rows)
+// B (and for dH also A) is stored with its row contiguous across K: a chunk goes to
+// LDS as [k][64]. blockIdx.z takes a segment of K (dH has few tiles and a long K)
+// and leaves a partial product of its own.
+template <bool DW>
+__global__ __launch_bounds__(256) void k_f32_product(const float* __restrict__ gt, int64_t ldg,
+                                                     const float* __restrict__ B, int64_t M,
+                                                     int64_t H, int64_t K, int64_t kseg,
+                                                     int accumulate, float* __restrict__ C,
+                                                     int64_t seg_stride) {
+  __shared__ __attribute__((aligned(16))) float sa[DW ? 64 * kF32Ld : 32 * kZLd];
+  __shared__ __attribute__((aligned(16))) float sb[32 * kZLd];
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  const int64_t m0 = int64_t(blockIdx.x) * 64, n0 = int64_t(blockIdx.y) * 64;
+  const int64_t k0 = int64_t(blockIdx.z) * kseg, k1 = K - k0 < kseg ? K : k0 + kseg;
+  C += int64_t(blockIdx.z) * seg_stride;
+  // [k][64] chunks: rows tid / 16, + 16, columns 4 (tid % 16); [64][k] as f32_logits
+  const int kr = tid >> 4, kc = (tid & 15) * 4, lr = tid >> 3, lc = (tid & 7) * 4;
+  float ra[2][4], rb[2][4];
+  auto load = [&](int64_t k) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int64_t kk = k + kr + 16 * i;
+      if constexpr (DW) {
+        const int64_t m = m0 + lr + 32 * i;
+        load_chunk(gt + (m < M ? m : M - 1) * ldg, k + lc, k1, ra[i]);
+      } else {
+        load_chunk(gt + (kk < k1 ? kk : k1 - 1) * ldg, m0 + kc, kk < k1 ? M : 0, ra[i]);
+      }
+      load_chunk(B + (kk < k1 ? kk : k1 - 1) * H, n0 + kc, kk < k1 ? H : 0, rb[i]);
+    }
+  };
+  f32x4 acc[2][2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const int wm = (w & 1) * 32, wn = (w >> 1) * 32, r = lane & 15, kg = (lane >> 4) * 4;
+  load(k0);
+  for (int64_t k = k0; k < k1; k += 32) {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float* pa = DW ? sa + (lr + 32 * i) * kF32Ld + lc : sa + (kr + 16 * i) * kZLd + kc;
+      *reinterpret_cast<f32x4*>(pa) = f32x4{ra[i][0], ra[i][1], ra[i][2], ra[i][3]};
+      *reinterpret_cast<f32x4*>(sb + (kr + 16 * i) * kZLd + kc) =
+          f32x4{rb[i][0], rb[i][1], rb[i][2], rb[i][3]};
+    }
+    __syncthreads();
+    if (k + 32 < k1) load(k + 32);
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      float fa[2][4], fb[2][4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int kk = p * 16 + kg + e;
+          fa[i][e] = DW ? sa[(wm + 16 * i + r) * kF32Ld + kk] : sa[kk * kZLd + wm + 16 * i + r];
+          fb[i][e] = sb[kk * kZLd + wn + 16 * i + r];
+        }
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(fa[i][e], fb[j][e], acc[i][j], 0, 0, 0);
+    }
+  }
+  // acc[i][j][e]: row 16 i + 4 (lane / 16) + e, column 16 j + lane % 16
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int64_t m = m0 + wm + 16 * i + kg + e;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int64_t n = n0 + wn + 16 * j + r;
+        if (m < M && n < H) {
+          float* c = C + m * H + n;
+          *c = accumulate ? *c + acc[i][j][e] : acc[i][j][e];
+        }
+      }
+    }
+}
+
+// dH (+)= the segments' partial products, in order.
+__global__ __launch_bounds__(256) void k_f32_dh_sum(const float* __restrict__ part, int segs,
+                                                    int64_t n, int accumulate,
+                                                    float* __restrict__ dH) {
+  const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= n) return;
+  float v = accumulate ? dH[i] : 0.f;
+  for (int z = 0; z < segs; ++z) v += part[z * n + i];
+  dH[i] = v;
+}
+
 unsigned cdiv(int64_t a, int64_t b) { return unsigned((a + b - 1) / b); }
 
 template <bool SOFTCAP>
 hipError_t run_join(const LpPlan& q, const JoinArgs& j, const Launcher& L) {
   L.pre(kLpJoin);
-  if (q.sp == 1) {
-    const dim3 grid(unsigned(j.N)), block(kFewThreads);
-    const int64_t lpt = (q.lists + kFewThreads - 1) / kFewThreads;
-    if (lpt <= 1) hipLaunchKernelGGL((k_lp_join_few<SOFTCAP, 1>), grid, block, 0, L.stream, j);
-    else if (lpt <= 2) hipLaunchKernelGGL((k_lp_join_few<SOFTCAP, 2>), grid, block, 0, L.stream, j);
-    else if (lpt <= 4) hipLaunchKernelGGL((k_lp_join_few<SOFTCAP, 4>), grid, block, 0, L.stream, j);
-    else hipLaunchKernelGGL((k_lp_join_few<SOFTCAP, 8>), grid, block, 0, L.stream, j);
-  } else {
-    const dim3 grid(cdiv(j.N, kJoinTokens)), block(256);
+  if (q.tiles) {
+    const dim3 grid(cdiv(j.N, kJoinTokens));
     if (j.top_k <= 1)
-      hipLaunchKernelGGL((k_lp_join<SOFTCAP, false, 1>), grid, block, 0, L.stream, j, nullptr);
+      hipLaunchKernelGGL((k_lp_join<SOFTCAP, false, 32, 1>), grid, dim3(1024), 0, L.stream, j, nullptr);
     else if (j.top_k <= 8)
-      hipLaunchKernelGGL((k_lp_join<SOFTCAP, false, 8>), grid, block, 0, L.stream, j, nullptr);
+      hipLaunchKernelGGL((k_lp_join<SOFTCAP, false, 32, 8>), grid, dim3(1024), 0, L.stream, j, nullptr);
+    else if (j.top_k <= 16)
+      hipLaunchKernelGGL((k_lp_join<SOFTCAP, false, 32, 16>), grid, dim3(1024), 0, L.stream, j, nullptr);
     else
-      hipLaunchKernelGGL((k_lp_join<SOFTCAP, false, kLpTop>), grid, block, 0, L.stream, j, nullptr);
+      hipLaunchKernelGGL((k_lp_join<SOFTCAP, false, 16, kLpTop>), grid, dim3(512), 0, L.stream, j, nullptr);
+  } else {
+    hipLaunchKernelGGL(k_lp_join_few<SOFTCAP>, dim3(unsigned(j.N)), dim3(kFewThreads), 0,
+                       L.stream, j);
   }
+  L.post(kLpJoin);
+  return hipGetLastError();
+}
+
+// tau of the chunk's tokens from the first `lists` lists.
+hipError_t run_tau(JoinArgs j, int64_t lists, float* tau, const Launcher& L) {
+  j.lists = lists;
+  const dim3 grid(cdiv(j.N, kJoinTokens));
+  L.pre(kLpJoin);
+  if (j.top_k <= 8)
+    hipLaunchKernelGGL((k_lp_join<false, true, 32, 8>), grid, dim3(1024), 0, L.stream, j, tau);
+  else if (j.top_k <= 16)
+    hipLaunchKernelGGL((k_lp_join<false, true, 32, 16>), grid, dim3(1024), 0, L.stream, j, tau);
+  else
+    hipLaunchKernelGGL((k_lp_join<false, true, 16, kLpTop>), grid, dim3(512), 0, L.stream, j, tau);
   L.post(kLpJoin);
   return hipGetLastError();
 }
@@ -893,6 +1106,7 @@ hipError_t run_few(const LpArgs& a, const Warp& warp, const LpOut& out, const La
   L.pre(kLpTiles);
   if (a.N <= 16) go(std::integral_constant<int, 1>{});
   else if (a.N <= 32) go(std::integral_constant<int, 2>{});
+  else if (a.N <= 48) go(std::integral_constant<int, 3>{});
   else go(std::integral_constant<int, 4>{});
   L.post(kLpTiles);
   return hipGetLastError();
@@ -903,7 +1117,9 @@ hipError_t logprobs(const LpPlan& q, const LpArgs& a, char* ws, const Launcher& 
   const Warp warp = make_warp(a.softcap, a.temperature);
   LpOut out{reinterpret_cast<float2*>(ws + q.off_part), reinterpret_cast<float*>(ws + q.off_pd),
             reinterpret_cast<float*>(ws + q.off_zt), reinterpret_cast<float*>(ws + q.off_cv),
-            reinterpret_cast<uint8_t*>(ws + q.off_ci), q.sp, q.st, q.cl, q.ck, q.ct, int(q.kc)};
+            reinterpret_cast<uint8_t*>(ws + q.off_ci), reinterpret_cast<float*>(ws + q.off_zmax),
+            q.top_k && !q.tiles ? reinterpret_cast<float*>(ws + q.off_z) : nullptr,
+            q.sp, q.st, q.cl, q.ck, q.ct, int(q.kc)};
   JoinArgs j{out, q.parts, q.lists, q.list_rows, a.V, a.N, nullptr, nullptr, a.tokens,
              a.ignore_index, q.top_k, warp, a.logp, a.entropy, a.lse, a.top_logp, a.top_ids};
   hipError_t e = hipSuccess;
@@ -967,7 +1183,7 @@ hipError_t logprobs(const LpPlan& q, const LpArgs& a, char* ws, const Launcher& 
     }
   }
   if (e == hipSuccess && q.gather) e = launch_scan_gather(p, ag, false, L);
-  if (e == hipSuccess && q.gather) e = launch_chunk_counts(p, ag, false, L);
+  if (e == hipSuccess && q.gather && q.n_chunks > 1) e = launch_chunk_counts(p, ag, false, L);
   if (e == hipSuccess && !q.gather && a.status)
     e = launch_token_status(nullptr, 0, a.V, a.ignore_index, a.status, L);
   constexpr int NF = gemm::kFormN;
@@ -978,7 +1194,7 @@ hipError_t logprobs(const LpPlan& q, const LpArgs& a, char* ws, const Launcher& 
     if (q.gather) {
       jc.labels = ag.yc + t0;
       jc.idx = ag.idx + t0;
-      jc.count = ag.ccnt + c;
+      jc.count = q.n_chunks > 1 ? ag.ccnt + c : &ag.sc->n_valid;
     } else {
       at_token(jc, t0);
     }
@@ -997,7 +1213,18 @@ hipError_t logprobs(const LpPlan& q, const LpArgs& a, char* ws, const Launcher& 
         return run(EpiLp<SOFTCAP, true>{jc.labels, jc.N, a.V, v0, warp, out, tau});
       return run(EpiLp<SOFTCAP, false>{jc.labels, jc.N, a.V, v0, warp, out, nullptr});
     };
-    e = tiles(0, a.V, nullptr);
+    // Alternatives: the first tiles of the vocabulary alone, whole rounds of the
+    // chip, give every token a bound tau that few logits of the others exceed;
+    // their epilogues then have next to nothing to extract.
+    const int64_t pre = lp_first_tiles(q, jc.N);
+    if (pre > 0) {
+      float* tau = reinterpret_cast<float*>(ws + q.off_tau);
+      e = tiles(0, pre * kBM, nullptr);
+      if (e == hipSuccess) e = run_tau(jc, 2 * pre, tau, L);
+      if (e == hipSuccess) e = tiles(pre * kBM, a.V, tau);
+    } else {
+      e = tiles(0, a.V, nullptr);
+    }
     if (e == hipSuccess) e = run_join<SOFTCAP>(q, jc, L);
   }
   return e;
@@ -1007,6 +1234,34 @@ hipError_t logprobs(const LpPlan& q, const LpArgs& a, char* ws, const Launcher& 
 
 hipError_t launch_logprobs(const LpPlan& q, const LpArgs& a, char* ws, const Launcher& L) {
   return a.softcap > 0.f ? logprobs<true>(q, a, ws, L) : logprobs<false>(q, a, ws, L);
+}
+
+hipError_t launch_lp_f32_products(const Plan& p, const Args& a, int64_t chunk, const Launcher& L) {
+  const int64_t v0 = chunk * p.vchunk, vcur = gemm::chunk_rows(p, chunk);
+  const float* gt = static_cast<const float*>(a.g);
+  float* dW = static_cast<float*>(a.dW) + v0 * p.H;
+  float* dH = static_cast<float*>(a.dH);
+  L.pre(kGemmDW);
+  hipLaunchKernelGGL(k_f32_product<true>, dim3(cdiv(vcur, 64), cdiv(p.H, 64)), dim3(256), 0,
+                     L.stream, gt, p.ldg, static_cast<const float*>(a.h), vcur, p.H, p.N, p.N,
+                     a.accumulate_dW, dW, int64_t(0));
+  L.post(kGemmDW);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const float* W = static_cast<const float*>(a.W) + v0 * p.H;
+  const int64_t kseg = lp_f32_segment(p), segs = (vcur + kseg - 1) / kseg;
+  L.pre(kGemmDH);
+  hipLaunchKernelGGL(k_f32_product<false>, dim3(cdiv(p.N, 64), cdiv(p.H, 64), unsigned(segs)),
+                     dim3(256), 0, L.stream, gt, p.ldg, W, p.N, p.H, vcur, kseg,
+                     segs == 1 && chunk > 0 ? 1 : 0, segs == 1 ? dH : a.dh_part, p.N * p.H);
+  L.post(kGemmDH);
+  e = hipGetLastError();
+  if (e != hipSuccess || segs == 1) return e;
+  L.pre(kDhReduce);
+  hipLaunchKernelGGL(k_f32_dh_sum, dim3(cdiv(p.N * p.H, 256)), dim3(256), 0, L.stream, a.dh_part,
+                     int(segs), p.N * p.H, chunk > 0 ? 1 : 0, dH);
+  L.post(kDhReduce);
+  return hipGetLastError();
 }
 
 hipError_t launch_lp_coefficients(const Plan& p, const Args& a, const LpGradArgs& g,

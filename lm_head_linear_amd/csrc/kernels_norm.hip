@@ -25,6 +25,7 @@
 #include "flce_internal.h"
 #include "ops_plan.h"
 #include "row_io.h"
+#include "wave_ops.h"
 
 namespace flce {
 namespace {
@@ -33,8 +34,7 @@ namespace {
 // holds WAVES floats; a barrier separates two uses.
 template <int WAVES>
 __device__ __forceinline__ float block_sum(float x, float* red) {
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) x += __shfl_xor(x, off);
+  x = wave_all(x, AddOp());
   if constexpr (WAVES > 1) {
     __syncthreads();
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = x;

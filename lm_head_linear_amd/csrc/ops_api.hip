@@ -91,7 +91,7 @@ int flce_embedding_backward(const int64_t* tokens, const void* dout, int64_t ld_
   if (!flce::make_embed_plan(N, H, V, &p)) return FLCE_ERR_ARG;
   char* ws = static_cast<char*>(workspace);
   flce::EmbedGradArgs a{tokens, dout, ld_dout, N, H, V, padding_index, scale, dW,
-                        accumulate_dW ? 1 : 0, dtype, grad_dtype, status, p.window, {}, {},
+                        accumulate_dW ? 1 : 0, dtype, grad_dtype, status, {}, {},
                         nullptr, nullptr};
   for (int i = 0; i < 2; ++i) {
     a.key[i] = reinterpret_cast<uint32_t*>(ws + p.off_key[i]);
@@ -173,6 +173,7 @@ int flce_logprobs_backward(const void* h, const void* W, const int64_t* tokens, 
                            reinterpret_cast<float*>(own), reinterpret_cast<float*>(own + arr),
                            reinterpret_cast<float*>(own + 2 * arr),
                            reinterpret_cast<float*>(own + 3 * arr)};
+  if (dtype == FLCE_F32) a.dh_part = reinterpret_cast<float*>(own + 4 * arr);
   {
     Range s("flce.setup");
     e = flce::pad_inputs(p, a, ws, true, L);
@@ -186,7 +187,7 @@ int flce_logprobs_backward(const void* h, const void* W, const int64_t* tokens, 
     e = flce::launch_lp_gradient(p, a, g, c, L);
     if (e == hipSuccess)
       e = dtype == FLCE_BF16 ? flce::bf16_chunk_products(p, a, c, L)
-                             : flce::f32_chunk_products(p, a, c, L);
+                             : flce::launch_lp_f32_products(p, a, c, L);
   }
   if (e == hipSuccess) e = flce::crop_outputs(p, ws, dH, dW, L);
   return status_of(e);

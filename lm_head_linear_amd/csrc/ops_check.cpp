@@ -60,20 +60,15 @@ bool make_embed_plan(int64_t N, int64_t H, int64_t V, EmbedPlan* p) {
   if (N < 0 || H <= 0 || V <= 0) return false;
   if (N > kMaxRows || H > kMaxWidth || V > kMaxRows) return false;
   EmbedPlan q;
-  // 32 sorted tokens a wave; more for very many tokens, so that an id that
-  // fills many windows leaves at most about as many partial rows as a window
-  // has tokens
-  q.window = 32;
-  while (q.window < 4096 && q.window * q.window * 32 < N) q.window *= 2;
-  const int64_t windows = ceil_div(N, q.window), blocks = ceil_div(N, kSortBlock);
+  const int64_t windows = ceil_div(N, kEmbedWindow), blocks = ceil_div(N, kSortBlock);
   const size_t list = align256(size_t(N) * sizeof(uint32_t));
-  const int lists = N <= kSortLocal ? 1 : 2;
+  const int lists = N <= kSortChunk ? 1 : 2;
   size_t off = 0;
   for (int i = 0; i < lists; ++i) {
     q.off_key[i] = off; off += list;
     q.off_pos[i] = off; off += list;
   }
-  if (lists == 2) { q.off_hist = off; off = align256(off + size_t(256 * blocks) * 4); }
+  if (N > kSortMerge) { q.off_hist = off; off = align256(off + size_t(256 * blocks) * 4); }
   if (windows > 1) { q.off_part = off; off = align256(off + size_t(2 * windows) * H * 4); }
   q.total = off > 0 ? off : 256;
   *p = q;
@@ -86,30 +81,32 @@ bool make_lp_plan(int64_t N, int64_t H, int64_t V, int dtype, int top_k, bool to
   if (!make_plan(N, H, V, dtype, &q.p, false, -1, 0)) return false;
   const bool bf16 = dtype == FLCE_BF16;
   q.top_k = top_k;
-  q.few = bf16 && N <= kFewTokens && ceil_div(V, kLpRows) <= kFewMaxLists;
-  const bool tiles = bf16 && !q.few;
-  q.gather = tiles && tokens;
+  q.few = bf16 && N <= kFewTokens && V <= kLpMaxTopV;
+  q.tiles = bf16 && !q.few;
+  q.gather = q.tiles && tokens;
   q.p.compact = q.gather;
-  q.part_rows = tiles ? kTileBF16 : kLpRows;
-  q.list_rows = tiles ? kTileBF16 / 2 : kLpRows;
+  q.part_rows = q.tiles ? kTileBF16 : kLpRows;
   q.parts = ceil_div(V, q.part_rows);
-  q.lists = ceil_div(V, q.list_rows);
-  q.kc = top_k < q.list_rows ? top_k : q.list_rows;
-  const int64_t step = tiles ? kTileBF16 : kLpRows;      // tokens per tile
+  const int64_t step = q.tiles ? kTileBF16 : kLpRows;      // tokens per tile
   const int64_t nmax = ceil_div(N > 0 ? N : 1, step) * step;
   int64_t nc = nmax < kLpMaxChunk ? nmax : kLpMaxChunk;
-  if (q.kc > 0) {
-    const int64_t fit = kLpListBytes / (q.lists * q.kc * 5) / step * step;
+  if (q.tiles) {
+    q.list_rows = kTileBF16 / 2;
+    q.lists = ceil_div(V, q.list_rows);
+    q.kc = top_k;
+  }
+  if (top_k > 0) {
+    const int64_t per_token = q.tiles ? q.lists * q.kc * 5 : V * 4;
+    const int64_t fit = kLpListBytes / per_token / step * step;
     if (nc > fit) nc = fit > step ? fit : step;
   }
   q.nc = nc;
   q.n_chunks = ceil_div(N, nc);
-  if (q.few || (!bf16 && nc <= kFewTokens && q.lists <= kFewMaxLists)) {
-    q.sp = 1; q.st = q.parts;
-    q.ck = 1; q.cl = q.kc; q.ct = q.lists * q.kc;
-  } else {
+  if (q.tiles) {
     q.sp = nc; q.st = 1;
     q.ct = 1; q.ck = nc; q.cl = q.kc * nc;
+  } else {
+    q.sp = 1; q.st = q.parts;
   }
   size_t off = 0;
   auto take = [&](size_t bytes) { const size_t at = off; off = align256(off + bytes); return at; };
@@ -124,12 +121,17 @@ bool make_lp_plan(int64_t N, int64_t H, int64_t V, int dtype, int top_k, bool to
       q.off_bcnt = take(size_t(q.p.n_gather_blocks) * sizeof(int32_t));
       q.off_ccnt = take(size_t(2 * q.n_chunks) * sizeof(int64_t));
     }
-    if (q.gather || (tiles && q.p.pad_h)) q.off_h = take(size_t(N) * q.p.H * 2);
-    if (tiles && q.p.pad_h) q.off_wp = take(size_t(V) * q.p.H * 2);
-    q.off_part = take(size_t(q.parts) * nc * 2 * sizeof(float));
-    q.off_pd = take(size_t(q.parts) * nc * sizeof(float));
-    q.off_zt = take(size_t(nc) * sizeof(float));
-    if (top_k > 0) {
+    if (q.gather || (q.tiles && q.p.pad_h)) q.off_h = take(size_t(N) * q.p.H * 2);
+    if (q.tiles && q.p.pad_h) q.off_wp = take(size_t(V) * q.p.H * 2);
+    const int64_t rows = !q.tiles && N < nc ? N : nc;  // tokens of the largest chunk
+    q.off_part = take(size_t(q.parts) * rows * 2 * sizeof(float));
+    q.off_pd = take(size_t(q.parts) * rows * sizeof(float));
+    q.off_zt = take(size_t(rows) * sizeof(float));
+    if (top_k > 0 && !q.tiles) {
+      q.off_zmax = take(size_t(q.parts) * rows * sizeof(float));
+      q.off_z = take(size_t(V) * rows * sizeof(float));
+    }
+    if (top_k > 0 && q.tiles) {
       q.off_tau = take(size_t(nc) * sizeof(float));
       q.off_cv = take(size_t(q.lists) * q.kc * nc * sizeof(float));
       q.off_ci = take(size_t(q.lists) * q.kc * nc);
@@ -257,7 +259,7 @@ int flce_embedding_backward_check_args(const int64_t* tokens, const void* dout, 
             wk = vec(workspace, int64_t(workspace_bytes), 1);
   if (clash({bw, bst, wk}, {bt, bd})) return FLCE_ERR_ARG;
   if (dtype == FLCE_F32 && grad_dtype == FLCE_BF16) return FLCE_ERR_UNSUPPORTED;
-  if (ceil_div(ceil_div(N, p.window) * ceil_div(H, 512), 4) > kMaxGrid)
+  if (ceil_div(N, kEmbedWindow) * ceil_div(H, 512) > kMaxGrid)
     return FLCE_ERR_UNSUPPORTED;
   for (const Buf& b : {bt, bd, bw, bst})
     if (misaligned(b)) return FLCE_ERR_UNSUPPORTED;
@@ -298,6 +300,7 @@ int flce_logprobs_check_args(const void* h, const void* W, const int64_t* tokens
             bs = vec(status, 1, 4), wk = vec(workspace, int64_t(workspace_bytes), 1);
   if (clash({bl, be, bz, bv, bi, bs, wk}, {bh, bw, bt})) return FLCE_ERR_ARG;
   if (dtype == FLCE_BF16 && !bf16_shape_ok(N, p.p.H, V)) return FLCE_ERR_UNSUPPORTED;
+  if (top_k > 0 && !p.tiles && V > kLpMaxTopV) return FLCE_ERR_UNSUPPORTED;
   const uintptr_t mask = dtype == FLCE_BF16 ? 15u : 3u;
   if ((bw.begin() & mask) || (N > 0 && (bh.begin() & mask))) return FLCE_ERR_UNSUPPORTED;
   for (const Buf& b : {bt, bl, be, bz, bv, bi, bs})
@@ -312,8 +315,10 @@ size_t flce_logprobs_backward_workspace_size(int64_t N, int64_t H, int64_t V, in
                                              int grad_dtype) {
   Plan p;
   if (!make_plan(N, H, V, dtype, &p, true, grad_dtype)) return 0;
-  // the head's backward, its dummy count, and the token coefficients
-  return p.total + 256 + 4 * align256(size_t(p.ld_part) * sizeof(float));
+  // the head's backward, its dummy count, the token coefficients, and the partial
+  // products of a split float32 dH
+  return p.total + 256 + 4 * align256(size_t(p.ld_part) * sizeof(float)) +
+         (dtype == FLCE_F32 ? align256(lp_f32_part_bytes(p)) : 0);
 }
 
 int flce_logprobs_backward_check_args(const void* h, const void* W, const int64_t* tokens,

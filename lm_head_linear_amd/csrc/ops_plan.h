@@ -51,9 +51,13 @@ constexpr int64_t kNormShares = 1024;
 inline int64_t norm_shares(int64_t N) { return N < kNormShares ? N : kNormShares; }
 
 // ---- embedding ---------------------------------------------------------------------
-// Tokens that one workgroup sorts in LDS, and tokens per workgroup beyond that.
-constexpr int64_t kSortLocal = 16384;
+// Tokens that one workgroup sorts in LDS, tokens up to which such chunks are
+// merged at once, and tokens per workgroup of the digit passes beyond that.
+constexpr int64_t kSortChunk = 1024;
+constexpr int64_t kSortMerge = 32768;
 constexpr int64_t kSortBlock = 8192;
+// Sorted tokens whose rows one workgroup adds up.
+constexpr int64_t kEmbedWindow = 256;
 
 struct EmbedArgs {
   const int64_t* tokens;
@@ -76,15 +80,13 @@ struct EmbedGradArgs {
   int dtype, grad_dtype;
   int32_t* status;            // may be null
   // workspace
-  int64_t window;             // sorted tokens per wave of the sums
   uint32_t* key[2];           // sorted keys and the tokens' positions, twice
   uint32_t* pos[2];
-  uint32_t* hist;             // [256][blocks] digit counts (N > kSortLocal)
+  uint32_t* hist;             // [256][blocks] digit counts (N > kSortMerge)
   float* part;                // [windows][2][H] partial rows
 };
 
 struct EmbedPlan {
-  int64_t window = 0;
   size_t off_key[2] = {}, off_pos[2] = {}, off_hist = 0, off_part = 0, total = 0;
 };
 
@@ -97,31 +99,60 @@ bool make_embed_plan(int64_t N, int64_t H, int64_t V, EmbedPlan* p);
 constexpr int64_t kFewTokens = 64;
 // Vocabulary rows per workgroup of the few-token and float32 kernels.
 constexpr int64_t kLpRows = 64;
-// The join of few tokens keeps up to 8 lists a thread.
-constexpr int64_t kFewMaxLists = 8 * 1024;
-// Bytes of candidate lists per token chunk, and tokens per chunk.
+// Vocabulary up to which the 64-row tiles are joined with alternatives: 32 of the
+// join's 1024 threads hold at most 2048 tiles.
+constexpr int64_t kLpMaxTopV = int64_t(64) * 1024 * kLpRows;
+// Bytes of candidates (lists, or logits) per token chunk, and tokens per chunk.
 constexpr int64_t kLpListBytes = int64_t(1) << 30;
 constexpr int64_t kLpMaxChunk = 8192;
 
 struct LpPlan {
   Plan p;                     // sizes (H padded), the gather's blocks; its offsets are not used
   bool few = false;           // the few-token kernel
+  bool tiles = false;         // the 256 x 256 tiles (neither: float32)
   bool gather = false;        // live tokens first (bf16 tiles with tokens given)
   int top_k = 0;
   // Partials: per part_rows vocabulary rows and token the max, sum and weighted
-  // sum; candidates: per list_rows rows and token the kc largest logits, sorted.
+  // sum. Candidates, 256 x 256 tiles: per list_rows rows and token the kc largest
+  // logits, sorted; otherwise the largest logit per part and all logits.
   int64_t part_rows = 0, parts = 0, list_rows = 0, lists = 0, kc = 0;
   int64_t nc = 0, n_chunks = 0;   // tokens per chunk
   // Elements between parts / tokens, and between lists / candidates / tokens:
-  // token-major for few tokens (a workgroup joins one token), otherwise tokens
-  // adjacent (a workgroup joins 32).
+  // tokens adjacent for the tiles (a workgroup joins 32), otherwise parts adjacent
+  // (a workgroup joins one token).
   int64_t sp = 0, st = 0, cl = 0, ck = 0, ct = 0;
   size_t off_sc = 0, off_nt = 0, off_tokloss = 0, off_idx = 0, off_yc = 0, off_bcnt = 0,
          off_ccnt = 0, off_h = 0, off_wp = 0, off_part = 0, off_pd = 0, off_zt = 0, off_tau = 0,
-         off_cv = 0, off_ci = 0, total = 0;
+         off_cv = 0, off_ci = 0, off_zmax = 0, off_z = 0, total = 0;
 };
 
 bool make_lp_plan(int64_t N, int64_t H, int64_t V, int dtype, int top_k, bool tokens, LpPlan* p);
+
+// Vocabulary tiles of a chunk of nt tokens whose candidates are extracted first, to
+// give the others a bound; 0: all at once. A sixteenth of them, at least one round of
+// 256 workgroups, and only where that leaves most of the work for after.
+inline int64_t lp_first_tiles(const LpPlan& q, int64_t nt) {
+  if (q.kc == 0) return 0;
+  const int64_t tt = (nt + kTileBF16 - 1) / kTileBF16, tv = q.parts;
+  int64_t pre = (tv + 15) / 16;
+  if (pre * tt < 256) pre = (256 + tt - 1) / tt;
+  return 2 * pre <= tv ? pre : 0;
+}
+
+// Segment of the float32 dH product's K (vocabulary rows of a chunk): its
+// ceil(N / 64) x ceil(H / 64) tiles are split until about 1024 workgroups run, in
+// segments of at least 128 rows.
+inline int64_t lp_f32_segment(const Plan& p) {
+  const int64_t tiles = ((p.N + 63) / 64) * ((p.H + 63) / 64);
+  int64_t segs = tiles > 0 ? 1024 / tiles : 1;
+  if (segs > p.vchunk / 128) segs = p.vchunk / 128;
+  if (segs < 1) segs = 1;
+  return ((p.vchunk + segs - 1) / segs + 31) / 32 * 32;
+}
+inline size_t lp_f32_part_bytes(const Plan& p) {
+  const int64_t kseg = lp_f32_segment(p), segs = (p.vchunk + kseg - 1) / kseg;
+  return segs > 1 ? size_t(segs) * size_t(p.N) * size_t(p.H) * sizeof(float) : 0;
+}
 
 struct LpArgs {
   const void* h;
@@ -172,6 +203,7 @@ hipError_t launch_lp_coefficients(const Plan& p, const Args& a, const LpGradArgs
                                   const Launcher& L);
 hipError_t launch_lp_gradient(const Plan& p, const Args& a, const LpGradArgs& g, int64_t chunk,
                               const Launcher& L);
+hipError_t launch_lp_f32_products(const Plan& p, const Args& a, int64_t chunk, const Launcher& L);
 hipError_t launch_token_status(const int64_t* tokens, int64_t N, int64_t V, int64_t padding,
                                int32_t* status, const Launcher& L);
 

@@ -64,6 +64,8 @@ CASES = [(1, 8, 1, torch.bfloat16, "uniform"), (3, 1, 5, torch.float32, "uniform
          (1000, 1024, 600, torch.bfloat16, "zipf"), (4096, 131, 1000, torch.bfloat16, "runs"),
          (4097, 520, 70000, torch.float32, "zipf"), (16384, 264, 300, torch.bfloat16, "runs"),
          (16385, 136, 70001, torch.bfloat16, "zipf"), (50000, 72, 257, torch.float32, "zipf"),
+         (32768, 40, 9000, torch.bfloat16, "runs"), (1024, 65, 300, torch.float32, "runs"),
+         (32769, 40, 9000, torch.float32, "zipf"),
          (40000, 64, 3, torch.bfloat16, "same")]
 
 

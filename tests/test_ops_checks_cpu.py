@@ -125,7 +125,7 @@ def embed_bwd(**kw):
     (dict(dW=None), ARG), (dict(dout=None), ARG), (dict(dW=Buf(2 * M)), ARG),
     (dict(workspace=Buf(3 * M, 1 << 16)), ARG), (dict(status=Buf(3 * M)), ARG),
     (dict(dtype=torch.float32, grad_dtype=torch.bfloat16), UNSUP),
-    (dict(workspace=None), WS), (dict(workspace=Buf(5 * M, 1024)), WS),
+    (dict(workspace=None), WS), (dict(workspace=Buf(5 * M, 1023)), WS),
     (dict(workspace=Buf(5 * M + 128, 1 << 16)), WS),
 ])
 def test_embedding_backward(kw, want):
@@ -135,12 +135,13 @@ def test_embedding_backward(kw, want):
 def test_embedding_workspace():
     size = m.flce_embedding_backward_workspace_size
     assert size(0, 8, 8) == 256 and size(1, 8, 0) == 0
-    # one list of keys and positions, two partial rows for each 32 tokens
-    assert size(16384, 4096, 131072) == 2 * 16384 * 4 + 2 * 512 * 4096 * 4
-    # two lists beyond what one workgroup sorts, and 256 counts a block
-    assert size(1 << 15, 64, 100) == 4 * (1 << 15) * 4 + 256 * 4 * 4 + 2 * 1024 * 64 * 4
-    # windows grow with the tokens: the partial rows stay in proportion
-    assert size(1 << 20, 64, 100) < 4 * (1 << 20) * 4 + 256 * 128 * 4 + 2 * 8192 * 64 * 4 + 1
+    # keys and positions, twice beyond one chunk of 1024; two partial rows for each 256
+    # tokens
+    assert size(1024, 64, 100) == 2 * 1024 * 4 + 2 * 4 * 64 * 4
+    assert size(16384, 4096, 131072) == 4 * 16384 * 4 + 2 * 64 * 4096 * 4
+    # 256 digit counts a block beyond what is merged at once
+    assert size(1 << 15, 64, 100) == 4 * (1 << 15) * 4 + 2 * 128 * 64 * 4
+    assert size(1 << 16, 64, 100) == 4 * (1 << 16) * 4 + 256 * 8 * 4 + 2 * 256 * 64 * 4
 
 
 def lp(**kw):
@@ -216,9 +217,9 @@ def test_logprobs_workspace():
     size = m.flce_logprobs_workspace_size
     bf = torch.bfloat16
     assert size(4, 8, 8, bf, 33) == 0 and size(4, 0, 8, bf, 0) == 0 and size(0, 8, 8, bf, 4) == 512
-    # one token: three partials and 8 candidates of 5 bytes for each 64 vocabulary
-    # rows, held for 64 tokens
-    assert size(1, 4096, 131072, bf, 8) < 64 * 2048 * (12 + 8 * 5) + 4096
+    # one token: four partials for each 64 vocabulary rows, and its logits
+    assert size(1, 4096, 131072, bf, 8) < 2048 * 16 + 131072 * 4 + 4096
+    assert size(1, 4096, 131072, bf, 0) < 2048 * 12 + 4096
     # the candidates of a chunk of tokens stay below 1 GiB, whatever N is
     a, b = size(1 << 17, 64, 256000, bf, 32), size(1 << 18, 64, 256000, bf, 32)
     assert b - a < (1 << 17) * (64 * 2 + 32) and a < (1 << 30) + (1 << 17) * 256 + (1 << 25)
