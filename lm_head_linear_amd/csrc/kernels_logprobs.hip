@@ -108,30 +108,55 @@ struct EpiLp {
     if (TOPK && tau) stage_tokens<1>(tok + 2048, tau, n0, N, wave, lane);
   }
 
+  // The accumulators of column block j, as they are.
+  __device__ __forceinline__ static void column(const Acc& acc, int j, float (&z)[8][4]) {
+    auto take = [&](auto c) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) z[i][r] = acc[i][decltype(c)::value][r];
+    };
+    switch (j) {
+      case 0: take(std::integral_constant<int, 0>{}); break;
+      case 1: take(std::integral_constant<int, 1>{}); break;
+      case 2: take(std::integral_constant<int, 2>{}); break;
+      case 3: take(std::integral_constant<int, 3>{}); break;
+      case 4: take(std::integral_constant<int, 4>{}); break;
+      case 5: take(std::integral_constant<int, 5>{}); break;
+      case 6: take(std::integral_constant<int, 6>{}); break;
+      default: take(std::integral_constant<int, 7>{}); break;
+    }
+  }
+
+  // FULL: all 128 rows of the wave exist. `to`: this wave's [256] (m, s, d) in LDS.
   template <bool FULL>
-  __device__ __forceinline__ void columns(Acc& acc, int64_t m0, int64_t n0, int wm, int wn,
-                                          int lane, const char* tok, float (&mx)[8],
-                                          float (&sm)[8], float (&dm)[8]) const {
+  __device__ __forceinline__ void columns(const Acc& acc, int64_t m0, int64_t n0, int wm, int wn,
+                                          int lane, const char* tok, float4* to) const {
     const int64_t* lab = reinterpret_cast<const int64_t*>(tok);
     const float* tau_t = reinterpret_cast<const float*>(tok + 2048);
     const int g = lane >> 4;
     const int64_t vbase = v0 + m0 + wm * 128;        // vocabulary id of the wave's row 0
     const int live = FULL ? 128 : int(V - vbase < 128 ? (V - vbase > 0 ? V - vbase : 0) : 128);
-#pragma unroll
+    auto in = [&](int i, int r) { return FULL || i * 16 + 4 * g + r < live; };
+    // one column block at a time through the same code: unrolled over the blocks, the
+    // epilogue is several times the instruction cache and waits for its own fetches
+#pragma unroll 1
     for (int j = 0; j < 8; ++j) {
-      const int64_t t = n0 + acc_col(wn, j, lane);
-      auto in = [&](int i, int r) { return FULL || i * 16 + 4 * g + r < live; };
+      float z[8][4];
+      column(acc, j, z);
+      const int col = acc_col(wn, j, lane);
+      const int64_t t = n0 + col;
       float x[8][4];
       float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
       for (int i = 0; i < 8; ++i)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          x[i][r] = warp_logit<SOFTCAP>(warp, acc[i][j][r]);
+          x[i][r] = warp_logit<SOFTCAP>(warp, z[i][r]);
           mq[r] = fmaxf(mq[r], in(i, r) ? x[i][r] : -INFINITY);
         }
       if (labels) {
-        const int64_t y = t < N ? lab[acc_col(wn, j, lane)] : -1;
+        const int64_t y = t < N ? lab[col] : -1;
         if (y >= vbase && y < vbase + live) {
           const int d = int(y - vbase);
           if (((d >> 2) & 3) == g) {
@@ -146,132 +171,115 @@ struct EpiLp {
         }
       }
       const float m = col_max4(fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])));
-      float s = 0.f, d = 0.f;
-      if (m != -INFINITY) {
-        // in powers of two: u = (x - m) log2 e, d in units of ln 2
-        const float mb = m * kLog2e;
-        float sq[2] = {0.f, 0.f}, dq[2] = {0.f, 0.f};
+      // in powers of two: u = (x - m) log2 e, d in units of ln 2
+      const float mb = m == -INFINITY ? 0.f : m * kLog2e;
+      float sq[4] = {0.f, 0.f, 0.f, 0.f}, dq[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          // a row past the vocabulary: 2^-200 = 0; a logit of -inf keeps -inf out of d
+          float u = fmaf(x[i][r], kLog2e, -mb);
+          u = (in(i, r) && u != -INFINITY) ? u : -200.f;
+          const float e = __builtin_amdgcn_exp2f(u);
+          sq[r] += e;
+          dq[r] = fmaf(e, u, dq[r]);
+        }
+      const float s = col_sum4((sq[0] + sq[1]) + (sq[2] + sq[3]));
+      const float d = col_sum4((dq[0] + dq[1]) + (dq[2] + dq[3]));
+      if (g == 0) to[col] = make_float4(m, s, d * kLn2, 0.f);
+      if (!TOPK || live == 0) continue;              // rows past V have no list
+      const float th = tau ? tau_t[col] : -INFINITY;
+      const int64_t list = (vbase >> 7) * out.cl + t * out.ct;
+      int n = 0;
+      bool rounds = tau == nullptr;
+      // x rises with z: no x as large as that of tau, no logit above tau
+      if (tau && (SOFTCAP || __ballot(t < N && m >= th * warp.inv_t) != 0)) {
+        int own = 0;                                 // this lane's logits above tau
 #pragma unroll
         for (int i = 0; i < 8; ++i)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            // a row past the vocabulary: 2^-200 = 0; a logit of -inf keeps -inf out of d
-            float u = fmaf(x[i][r], kLog2e, -mb);
-            u = (in(i, r) && u != -INFINITY) ? u : -200.f;
-            const float e = __builtin_amdgcn_exp2f(u);
-            sq[r & 1] += e;
-            dq[r & 1] = fmaf(e, u, dq[r & 1]);
-          }
-        s = sq[0] + sq[1];
-        d = (dq[0] + dq[1]) * kLn2;
-      }
-      mx[j] = m;
-      sm[j] = col_sum4(s);
-      dm[j] = col_sum4(d);
-      if (TOPK && live > 0) {                      // rows past V have no list
-        const float th = tau ? tau_t[acc_col(wn, j, lane)] : -INFINITY;
-        const int64_t list = (vbase >> 7) * out.cl + t * out.ct;
-        int n = 0;
-        bool rounds = tau == nullptr;
-        // x rises with z: no x as large as that of tau, no logit above tau
-        if (tau && (SOFTCAP || __ballot(t < N && m >= th * warp.inv_t) != 0)) {
-          int own = 0;                               // this lane's logits above tau
+          for (int r = 0; r < 4; ++r) own += in(i, r) && z[i][r] > th ? 1 : 0;
+        own = t < N ? own : 0;
+        int at = before_rows(own, g);
+        n = rows_all(own, AddOp());
+        rounds = __ballot(n > out.kc) != 0;
+        if (!rounds && own > 0) {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) own += in(i, r) && acc[i][j][r] > th ? 1 : 0;
-          own = t < N ? own : 0;
-          int at = before_rows(own, g);
-          n = rows_all(own, AddOp());
-          rounds = __ballot(n > out.kc) != 0;
-          if (!rounds && own > 0) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-#pragma unroll
-              for (int r = 0; r < 4; ++r)
-                if (in(i, r) && acc[i][j][r] > th) {
-                  out.cv[list + at * out.ck] = acc[i][j][r];
-                  out.ci[list + at * out.ck] = uint8_t(i * 16 + 4 * g + r);
-                  ++at;
-                }
-          }
-        }
-        if (rounds) {
-          float z[8][4];
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) z[i][r] = in(i, r) ? acc[i][j][r] : -INFINITY;
-          for (n = 0; n < out.kc; ++n) {
-            float bq[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              bq[r] = z[0][r];
-#pragma unroll
-              for (int i = 1; i < 8; ++i) bq[r] = fmaxf(bq[r], z[i][r]);
-            }
-            const float b = col_max4(fmaxf(fmaxf(bq[0], bq[1]), fmaxf(bq[2], bq[3])));
-            const bool go = b > th && t < N;
-            if (__ballot(go) == 0) break;
-            uint32_t rq[4] = {255, 255, 255, 255};
 #pragma unroll
             for (int r = 0; r < 4; ++r)
+              if (in(i, r) && z[i][r] > th) {
+                out.cv[list + at * out.ck] = z[i][r];
+                out.ci[list + at * out.ck] = uint8_t(i * 16 + 4 * g + r);
+                ++at;
+              }
+        }
+      }
+      if (rounds) {
 #pragma unroll
-              for (int i = 7; i >= 0; --i)
-                rq[r] = z[i][r] == b ? uint32_t(i * 16 + 4 * g + r) : rq[r];
-            MinOp least;
-            const uint32_t row = rows_all(least(least(rq[0], rq[1]), least(rq[2], rq[3])), least);
-            const int mine = int(row) - 4 * g;       // the lane's register of that row
+        for (int i = 0; i < 8; ++i)
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+          for (int r = 0; r < 4; ++r) z[i][r] = in(i, r) ? z[i][r] : -INFINITY;
+#pragma unroll 1
+        for (n = 0; n < out.kc; ++n) {
+          float bq[4];
 #pragma unroll
-              for (int r = 0; r < 4; ++r) z[i][r] = mine == i * 16 + r ? -INFINITY : z[i][r];
-            if (g == 0 && t < N) {
-              out.cv[list + n * out.ck] = go ? b : -INFINITY;
-              out.ci[list + n * out.ck] = uint8_t(row);
-            }
+          for (int r = 0; r < 4; ++r) {
+            bq[r] = z[0][r];
+#pragma unroll
+            for (int i = 1; i < 8; ++i) bq[r] = fmaxf(bq[r], z[i][r]);
+          }
+          const float b = col_max4(fmaxf(fmaxf(bq[0], bq[1]), fmaxf(bq[2], bq[3])));
+          const bool go = b > th && t < N;
+          if (__ballot(go) == 0) break;
+          uint32_t rq[4] = {255, 255, 255, 255};
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int i = 7; i >= 0; --i)
+              rq[r] = z[i][r] == b ? uint32_t(i * 16 + 4 * g + r) : rq[r];
+          MinOp least;
+          const uint32_t row = rows_all(least(least(rq[0], rq[1]), least(rq[2], rq[3])), least);
+          const int mine = int(row) - 4 * g;         // the lane's register of that row
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) z[i][r] = mine == i * 16 + r ? -INFINITY : z[i][r];
+          if (g == 0 && t < N) {
+            out.cv[list + n * out.ck] = go ? b : -INFINITY;
+            out.ci[list + n * out.ck] = uint8_t(row);
           }
         }
-        if (n < out.kc && g == 0 && t < N) out.cv[list + n * out.ck] = -INFINITY;
       }
+      if (n < out.kc && g == 0 && t < N) out.cv[list + n * out.ck] = -INFINITY;
     }
   }
 
   __device__ __forceinline__ void operator()(Acc& acc, int64_t m0, int64_t n0, int wm, int wn,
                                              int lane, char* smem, const char* tok) const {
-    float mx[8], sm[8], dm[8];
-    if (v0 + m0 + kBM <= V) columns<true>(acc, m0, n0, wm, wn, lane, tok, mx, sm, dm);
-    else columns<false>(acc, m0, n0, wm, wn, lane, tok, mx, sm, dm);
-    float4* buf = reinterpret_cast<float4*>(smem);
-    const int g = lane >> 4;
-    if (wm == 1 && g == 0) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        buf[wn * 128 + j * 16 + lane] = make_float4(mx[j], sm[j], dm[j], 0.f);
-    }
+    float4* buf = reinterpret_cast<float4*>(smem);   // [2][256]
+    if (v0 + m0 + kBM <= V) columns<true>(acc, m0, n0, wm, wn, lane, tok, buf + wm * 256);
+    else columns<false>(acc, m0, n0, wm, wn, lane, tok, buf + wm * 256);
     __syncthreads();
-    if (wm == 0 && g == 0) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float4 o = buf[wn * 128 + j * 16 + lane];
-        const float M = fmaxf(mx[j], o.x);
-        float S = 0.f, D = 0.f;
-        auto add = [&](float m, float s, float d) {
-          if (m == -INFINITY) return;
-          const float dl = m - M, f = __builtin_amdgcn_exp2f(dl * kLog2e);
-          S += s * f;
-          D += f * fmaf(dl, s, d);
-        };
-        add(mx[j], sm[j], dm[j]);
-        add(o.x, o.y, o.z);
-        const int64_t t = n0 + acc_col(wn, j, lane);
-        if (t < N) {
-          const int64_t at = ((v0 + m0) / kBM) * out.sp + t * out.st;
-          out.part[at] = make_float2(M, S);
-          out.pd[at] = D;
-        }
-      }
-    }
+    // a token a thread: the two waves' rows joined
+    const int col = (wm + 2 * wn) * 64 + lane;
+    const int64_t t = n0 + col;
+    if (t >= N) return;
+    const float4 a = buf[col], b = buf[256 + col];
+    const float M = fmaxf(a.x, b.x);
+    float S = 0.f, D = 0.f;
+    auto add = [&](const float4& q) {
+      if (q.x == -INFINITY && q.y == 0.f) return;
+      const float dl = q.x - M, f = __builtin_amdgcn_exp2f(dl * kLog2e);
+      S += q.y * f;
+      D += f * fmaf(dl, q.y, q.z);
+    };
+    add(a);
+    add(b);
+    const int64_t at = ((v0 + m0) / kBM) * out.sp + t * out.st;
+    out.part[at] = make_float2(M, S);
+    out.pd[at] = D;
   }
 };
 
@@ -526,7 +534,7 @@ __global__ __launch_bounds__(256) void k_lp_f32(const float* __restrict__ h,
 // ---- the joins --------------------------------------------------------------------------
 struct JoinArgs {
   LpOut in;
-  int64_t parts, lists, list_rows, V;
+  int64_t parts, list0, lists, list_rows, V;       // lists list0 .. lists - 1
   int64_t N;                  // tokens of this chunk
   const int64_t* count;       // live ones among them (gathered order); null: N
   const int32_t* idx;         // their positions; null: t
@@ -539,6 +547,8 @@ struct JoinArgs {
   float* lse;
   float* top_logp;
   int64_t* top_ids;
+  uint64_t* first;            // top_k keys of the lists before list0, or null
+  float* tau;
 };
 
 // Token t's scalars at its position o, from M, S, D.
@@ -569,20 +579,63 @@ __device__ __forceinline__ void join_part(float& M, float& S, float& D, float m,
   M = Mn;
 }
 
+__device__ __forceinline__ uint64_t rank_key(float v, int64_t id) {
+  if (!(v > -INFINITY)) return 0;                  // none
+  const uint32_t b = __float_as_uint(v + 0.f);     // -0 ranks as 0
+  const uint32_t o = (b >> 31) ? ~b : b | 0x80000000u;
+  return (uint64_t(o) << 32) | uint32_t(~uint32_t(id));
+}
+__device__ __forceinline__ float key_value(uint64_t k) {
+  const uint32_t o = uint32_t(k >> 32);
+  return __uint_as_float((o >> 31) ? o & 0x7fffffffu : ~o);
+}
+__device__ __forceinline__ int64_t key_id(uint64_t k) { return int64_t(uint32_t(~uint32_t(k))); }
+__device__ __forceinline__ uint64_t max_u64(uint64_t a, uint64_t b) { return a > b ? a : b; }
+
 // Many tokens: 32 tokens a workgroup and G threads for each, thread g taking every
-// G-th part and list, then the threads pairwise. A thread's sorted candidates live
-// in LDS, so G goes by top_k: 32 up to 16 alternatives (128 KiB), 16 beyond. With
-// TAU_ONLY just the top_k-th largest logit of the lists so far.
+// G-th part and list, then the threads pairwise. A thread keeps its KM largest keys
+// sorted in registers; two threads' lists meet as a bitonic sequence, through LDS,
+// which bounds G (128 KiB at 16 keys of 32 threads, or 32 keys of 16). With TAU_ONLY
+// just the lists so far: the top_k keys, and the top_k-th largest logit.
 constexpr int kJoinTokens = 32;
 constexpr int kAhead = 4;                          // loads in flight
 
+template <int KM>
+struct TopKeys {
+  uint64_t k[KM];
+  __device__ __forceinline__ void insert(uint64_t x) {
+    if (x <= k[KM - 1]) return;
+#pragma unroll
+    for (int i = 0; i < KM; ++i) {
+      const bool up = x > k[i];
+      const uint64_t o = k[i];
+      k[i] = up ? x : o;
+      x = up ? o : x;
+    }
+  }
+  // with another sorted list, b(i) its i-th key
+  template <class Get>
+  __device__ __forceinline__ void merge(Get b) {
+#pragma unroll
+    for (int i = 0; i < KM; ++i) k[i] = max_u64(k[i], b(KM - 1 - i));
+#pragma unroll
+    for (int h = KM / 2; h > 0; h >>= 1)
+#pragma unroll
+      for (int i = 0; i < KM; ++i)
+        if (!(i & h)) {
+          const bool up = k[i + h] > k[i];
+          const uint64_t o = k[i];
+          k[i] = up ? k[i + h] : o;
+          k[i + h] = up ? o : k[i + h];
+        }
+  }
+};
+
 template <bool SOFTCAP, bool TAU_ONLY, int G, int KM>     // top_k <= KM
-__global__ __launch_bounds__(32 * G) void k_lp_join(JoinArgs a, float* __restrict__ tau) {
+__global__ __launch_bounds__(32 * G) void k_lp_join(JoinArgs a) {
   constexpr int kT = 32 * G;
-  __shared__ float lv[KM * kT];                    // [top_k][thread]
-  __shared__ int32_t li[KM * kT];
-  __shared__ float4 grp[kT];
-  __shared__ int cnt[kT];
+  __shared__ uint64_t keys[KM * kT / 2];           // [key][thread]
+  __shared__ float4 grp[kT / 2];
   const int tid = threadIdx.x, tk = tid % kJoinTokens, g = tid / kJoinTokens;
   const int64_t t = int64_t(blockIdx.x) * kJoinTokens + tk;
   int64_t n_live = a.N;
@@ -605,31 +658,16 @@ __global__ __launch_bounds__(32 * G) void k_lp_join(JoinArgs a, float* __restric
         if (p + u * G < a.parts) join_part(M, S, D, ms[u].x, ms[u].y, d[u]);
     }
   }
-  int n = 0;
-  // (v, id) at its place among the n sorted candidates of this thread; the last one
-  // drops out of a full list. False if it ranks behind all of a full list.
-  auto insert = [&](float v, int32_t id) {
-    auto after = [&](int k) {                      // candidate k ranks behind (v, id)
-      const float o = lv[k * kT + tid];
-      return o < v || (o == v && li[k * kT + tid] > id);
-    };
-    if (n == K) {
-      if (!after(K - 1)) return false;
-      --n;
-    }
-    int k = n;
-    while (k > 0 && after(k - 1)) {
-      lv[k * kT + tid] = lv[(k - 1) * kT + tid];
-      li[k * kT + tid] = li[(k - 1) * kT + tid];
-      --k;
-    }
-    lv[k * kT + tid] = v;
-    li[k * kT + tid] = id;
-    ++n;
-    return true;
-  };
+  TopKeys<KM> top;
+#pragma unroll
+  for (int k = 0; k < KM; ++k) top.k[k] = 0;
   if (K > 0 && live) {
-    for (int64_t l = g; l < a.lists; l += kAhead * G) {
+    if (!TAU_ONLY && a.first && g == 0) {          // the top_k of the lists before list0
+#pragma unroll
+      for (int k = 0; k < KM; ++k)
+        if (k < K) top.k[k] = a.first[k * a.in.ck + t];
+    }
+    for (int64_t l = a.list0 + g; l < a.lists; l += kAhead * G) {
       float head[kAhead];
 #pragma unroll
       for (int u = 0; u < kAhead; ++u)
@@ -639,40 +677,51 @@ __global__ __launch_bounds__(32 * G) void k_lp_join(JoinArgs a, float* __restric
         const int64_t at = (l + u * G) * a.in.cl + t * a.in.ct;
         float v = head[u];
         for (int k = 0; v > -INFINITY;) {
-          insert(v, int32_t((l + u * G) * a.list_rows + a.in.ci[at + k * a.in.ck]));
+          top.insert(rank_key(v, (l + u * G) * a.list_rows + a.in.ci[at + k * a.in.ck]));
           v = ++k < a.in.kc ? a.in.cv[at + k * a.in.ck] : -INFINITY;
         }
       }
     }
   }
-  grp[tid] = make_float4(M, S, D, 0.f);
   for (int half = G / 2; half > 0; half >>= 1) {
-    cnt[tid] = n;
+    // threads half .. 2 half - 1 of each token hand theirs to 0 .. half - 1
+    const int slot = tid % (half * kJoinTokens);
+    if (g >= half && g < 2 * half) {
+      grp[slot] = make_float4(M, S, D, 0.f);
+#pragma unroll
+      for (int k = 0; k < KM; ++k) keys[k * (kT / 2) + slot] = top.k[k];
+    }
     __syncthreads();
     if (g < half) {
-      const int o = tid + half * kJoinTokens;
-      const float4 f = grp[o];
+      const float4 f = grp[slot];
       join_part(M, S, D, f.x, f.y, f.z);
-      grp[tid] = make_float4(M, S, D, 0.f);
-      for (int k = 0; k < cnt[o]; ++k)
-        if (!insert(lv[k * kT + o], li[k * kT + o])) break;
+      if (K > 0) top.merge([&](int k) { return keys[k * (kT / 2) + slot]; });
     }
     __syncthreads();
   }
   if (g != 0 || t >= a.N) return;
   if (TAU_ONLY) {
-    tau[t] = (live && n == K) ? lv[(K - 1) * kT + tid] : -INFINITY;
+    float last = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < KM; ++k)
+      if (k < K) {
+        a.first[k * a.in.ck + t] = live ? top.k[k] : 0;
+        if (k == K - 1 && live && top.k[k] != 0) last = key_value(top.k[k]);
+      }
+    a.tau[t] = last;
     return;
   }
   const int64_t o = a.idx ? int64_t(a.idx[t]) : t;
   const bool shown = live && (!a.labels || a.labels[t] != a.ignore_index);
   write_token(a, t, o, shown, M, S, D);
   const float ls = logf(S);
-  for (int k = 0; k < K; ++k) {
-    const bool has = shown && k < n;
-    write_alternative(a, o, k, has ? warp_logit<SOFTCAP>(a.warp, lv[k * kT + tid]) : 0.f,
-                      has ? int64_t(li[k * kT + tid]) : -1, M, ls);
-  }
+#pragma unroll
+  for (int k = 0; k < KM; ++k)
+    if (k < K) {
+      const bool has = shown && top.k[k] != 0;
+      write_alternative(a, o, k, has ? warp_logit<SOFTCAP>(a.warp, key_value(top.k[k])) : 0.f,
+                        has ? key_id(top.k[k]) : -1, M, ls);
+    }
 }
 
 // A workgroup joins one token of 64-row tiles. The top_k of any grouped keys lie in
@@ -682,19 +731,6 @@ __global__ __launch_bounds__(32 * G) void k_lp_join(JoinArgs a, float* __restric
 // then the lower id, so keys are distinct.
 constexpr int kFewThreads = 1024;
 constexpr int kSelMax = 2 * kFewThreads;           // keys of a selection
-
-__device__ __forceinline__ uint64_t rank_key(float v, int64_t id) {
-  if (!(v > -INFINITY)) return 0;                  // none
-  const uint32_t b = __float_as_uint(v + 0.f);     // -0 ranks as 0
-  const uint32_t o = (b >> 31) ? ~b : b | 0x80000000u;
-  return (uint64_t(o) << 32) | uint32_t(~uint32_t(id));
-}
-__device__ __forceinline__ float key_value(uint64_t k) {
-  const uint32_t o = uint32_t(k >> 32);
-  return __uint_as_float((o >> 31) ? o & 0x7fffffffu : ~o);
-}
-__device__ __forceinline__ int64_t key_id(uint64_t k) { return int64_t(uint32_t(~uint32_t(k))); }
-__device__ __forceinline__ uint64_t max_u64(uint64_t a, uint64_t b) { return a > b ? a : b; }
 
 struct Select {
   uint64_t group[64];          // the largest key of each 16 threads
@@ -1053,38 +1089,24 @@ __global__ __launch_bounds__(256) void k_f32_dh_sum(const float* __restrict__ pa
 
 unsigned cdiv(int64_t a, int64_t b) { return unsigned((a + b - 1) / b); }
 
-template <bool SOFTCAP>
+template <bool SOFTCAP, bool TAU_ONLY>
 hipError_t run_join(const LpPlan& q, const JoinArgs& j, const Launcher& L) {
   L.pre(kLpJoin);
-  if (q.tiles) {
-    const dim3 grid(cdiv(j.N, kJoinTokens));
-    if (j.top_k <= 1)
-      hipLaunchKernelGGL((k_lp_join<SOFTCAP, false, 32, 1>), grid, dim3(1024), 0, L.stream, j, nullptr);
-    else if (j.top_k <= 8)
-      hipLaunchKernelGGL((k_lp_join<SOFTCAP, false, 32, 8>), grid, dim3(1024), 0, L.stream, j, nullptr);
-    else if (j.top_k <= 16)
-      hipLaunchKernelGGL((k_lp_join<SOFTCAP, false, 32, 16>), grid, dim3(1024), 0, L.stream, j, nullptr);
-    else
-      hipLaunchKernelGGL((k_lp_join<SOFTCAP, false, 16, kLpTop>), grid, dim3(512), 0, L.stream, j, nullptr);
-  } else {
+  if (!q.tiles) {
     hipLaunchKernelGGL(k_lp_join_few<SOFTCAP>, dim3(unsigned(j.N)), dim3(kFewThreads), 0,
                        L.stream, j);
+  } else {
+    const dim3 grid(cdiv(j.N, kJoinTokens));
+    if (j.top_k <= 1)
+      hipLaunchKernelGGL((k_lp_join<SOFTCAP, TAU_ONLY, 32, 1>), grid, dim3(1024), 0, L.stream, j);
+    else if (j.top_k <= 8)
+      hipLaunchKernelGGL((k_lp_join<SOFTCAP, TAU_ONLY, 32, 8>), grid, dim3(1024), 0, L.stream, j);
+    else if (j.top_k <= 16)
+      hipLaunchKernelGGL((k_lp_join<SOFTCAP, TAU_ONLY, 32, 16>), grid, dim3(1024), 0, L.stream, j);
+    else
+      hipLaunchKernelGGL((k_lp_join<SOFTCAP, TAU_ONLY, 16, kLpTop>), grid, dim3(512), 0, L.stream,
+                         j);
   }
-  L.post(kLpJoin);
-  return hipGetLastError();
-}
-
-// tau of the chunk's tokens from the first `lists` lists.
-hipError_t run_tau(JoinArgs j, int64_t lists, float* tau, const Launcher& L) {
-  j.lists = lists;
-  const dim3 grid(cdiv(j.N, kJoinTokens));
-  L.pre(kLpJoin);
-  if (j.top_k <= 8)
-    hipLaunchKernelGGL((k_lp_join<false, true, 32, 8>), grid, dim3(1024), 0, L.stream, j, tau);
-  else if (j.top_k <= 16)
-    hipLaunchKernelGGL((k_lp_join<false, true, 32, 16>), grid, dim3(1024), 0, L.stream, j, tau);
-  else
-    hipLaunchKernelGGL((k_lp_join<false, true, 16, kLpTop>), grid, dim3(512), 0, L.stream, j, tau);
   L.post(kLpJoin);
   return hipGetLastError();
 }
@@ -1120,8 +1142,9 @@ hipError_t logprobs(const LpPlan& q, const LpArgs& a, char* ws, const Launcher& 
             reinterpret_cast<uint8_t*>(ws + q.off_ci), reinterpret_cast<float*>(ws + q.off_zmax),
             q.top_k && !q.tiles ? reinterpret_cast<float*>(ws + q.off_z) : nullptr,
             q.sp, q.st, q.cl, q.ck, q.ct, int(q.kc)};
-  JoinArgs j{out, q.parts, q.lists, q.list_rows, a.V, a.N, nullptr, nullptr, a.tokens,
-             a.ignore_index, q.top_k, warp, a.logp, a.entropy, a.lse, a.top_logp, a.top_ids};
+  JoinArgs j{out, q.parts, 0, q.lists, q.list_rows, a.V, a.N, nullptr, nullptr, a.tokens,
+             a.ignore_index, q.top_k, warp, a.logp, a.entropy, a.lse, a.top_logp, a.top_ids,
+             nullptr, nullptr};
   hipError_t e = hipSuccess;
   if (a.dtype == FLCE_F32 || q.few) {
     if (a.status)
@@ -1131,7 +1154,7 @@ hipError_t logprobs(const LpPlan& q, const LpArgs& a, char* ws, const Launcher& 
   }
   if (q.few) {
     e = run_few<SOFTCAP>(a, warp, out, L);
-    return e == hipSuccess ? run_join<SOFTCAP>(q, j, L) : e;
+    return e == hipSuccess ? run_join<SOFTCAP, false>(q, j, L) : e;
   }
   // the outputs of a chunk of tokens in their own order start at its first token
   auto at_token = [&](JoinArgs& c, int64_t t0) {
@@ -1151,7 +1174,7 @@ hipError_t logprobs(const LpPlan& q, const LpArgs& a, char* ws, const Launcher& 
                          static_cast<const float*>(a.W), c.labels, c.N, a.H, a.V, warp, out);
       L.post(kLpTiles);
       e = hipGetLastError();
-      if (e == hipSuccess) e = run_join<SOFTCAP>(q, c, L);
+      if (e == hipSuccess) e = run_join<SOFTCAP, false>(q, c, L);
     }
     return e;
   }
@@ -1218,14 +1241,18 @@ hipError_t logprobs(const LpPlan& q, const LpArgs& a, char* ws, const Launcher& 
     // their epilogues then have next to nothing to extract.
     const int64_t pre = lp_first_tiles(q, jc.N);
     if (pre > 0) {
-      float* tau = reinterpret_cast<float*>(ws + q.off_tau);
+      jc.tau = reinterpret_cast<float*>(ws + q.off_tau);
+      jc.first = reinterpret_cast<uint64_t*>(ws + q.off_first);
       e = tiles(0, pre * kBM, nullptr);
-      if (e == hipSuccess) e = run_tau(jc, 2 * pre, tau, L);
-      if (e == hipSuccess) e = tiles(pre * kBM, a.V, tau);
+      jc.lists = 2 * pre;
+      if (e == hipSuccess) e = run_join<false, true>(q, jc, L);
+      if (e == hipSuccess) e = tiles(pre * kBM, a.V, jc.tau);
+      jc.list0 = 2 * pre;
+      jc.lists = q.lists;
     } else {
       e = tiles(0, a.V, nullptr);
     }
-    if (e == hipSuccess) e = run_join<SOFTCAP>(q, jc, L);
+    if (e == hipSuccess) e = run_join<SOFTCAP, false>(q, jc, L);
   }
   return e;
 }

@@ -133,6 +133,7 @@ bool make_lp_plan(int64_t N, int64_t H, int64_t V, int dtype, int top_k, bool to
     }
     if (top_k > 0 && q.tiles) {
       q.off_tau = take(size_t(nc) * sizeof(float));
+      q.off_first = take(size_t(top_k) * nc * sizeof(uint64_t));
       q.off_cv = take(size_t(q.lists) * q.kc * nc * sizeof(float));
       q.off_ci = take(size_t(q.lists) * q.kc * nc);
     }

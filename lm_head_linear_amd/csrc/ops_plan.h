@@ -123,7 +123,7 @@ struct LpPlan {
   int64_t sp = 0, st = 0, cl = 0, ck = 0, ct = 0;
   size_t off_sc = 0, off_nt = 0, off_tokloss = 0, off_idx = 0, off_yc = 0, off_bcnt = 0,
          off_ccnt = 0, off_h = 0, off_wp = 0, off_part = 0, off_pd = 0, off_zt = 0, off_tau = 0,
-         off_cv = 0, off_ci = 0, off_zmax = 0, off_z = 0, total = 0;
+         off_cv = 0, off_ci = 0, off_first = 0, off_zmax = 0, off_z = 0, total = 0;
 };
 
 bool make_lp_plan(int64_t N, int64_t H, int64_t V, int dtype, int top_k, bool tokens, LpPlan* p);
