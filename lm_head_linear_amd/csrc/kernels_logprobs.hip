@@ -348,93 +348,133 @@ __device__ __forceinline__ void tile_epilogue(const float (&z)[64 / TPT], int q,
 }
 
 // ---- few tokens -----------------------------------------------------------------------
-// A workgroup: 64 vocabulary rows, 16 NT tokens, the four waves taking every
-// fourth 32-k chunk each, so that they read 256 adjacent bytes of a row between
-// them. A wave's lane loads 16 bytes of row l % 16 at k = 8 (l / 16): the matrix
-// instruction's operand as it is, no LDS. h comes from the caches. The waves'
-// partial logits meet in LDS. Rows may start at any element (ANY: 2-byte aligned
-// 16-byte loads); the last chunk is read element by element where it would leave
-// the row.
-template <bool ANY>
-__device__ __forceinline__ bf16x8 load_k8(const uint16_t* row, int64_t k, int64_t H) {
-  if (k + 8 <= H) {
-    if constexpr (ANY) return __builtin_bit_cast(bf16x8, load_raw(row + k));
-    else return __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(row + k));
+// A workgroup: 64 vocabulary rows, 16 of them a wave, and 16 NT tokens. A lane loads
+// 16 bytes of W's row l % 16 at k = 8 (l / 16): the matrix instruction's operand as
+// it is, no LDS. The h of a 128-k chunk is shared by the waves through LDS, two
+// chunks in turn. Both come kAheadK chunks early, so that several KiB of W per wave
+// are under way all the time. The loads of whole chunks have no condition (past the
+// last one it is loaded again): a branch around a load makes the compiler wait for
+// it as if the other way had been taken. The part of a chunk at the end of a row that
+// is no multiple of 128 is read first, element by element where it leaves the row.
+constexpr int kChunkK = 128;                       // k per chunk: four matrix steps
+constexpr int kHld = kChunkK + 8;                  // elements of a token's chunk in LDS
+
+// Eight elements of a row at p. ALIGN: bytes that every row starts at a multiple of:
+// 16, 4 or 2. Odd rows of a 2-byte aligned matrix are read as aligned words and
+// shifted: the element behind p + 7 is read with them.
+template <int ALIGN>
+__device__ __forceinline__ bf16x8 load_k8(const uint16_t* p) {
+  typedef u32x4 __attribute__((aligned(4))) u32x4_word;
+  if constexpr (ALIGN == 16) {
+    return __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(p));
+  } else if constexpr (ALIGN == 4) {
+    return __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4_word*>(p));
+  } else {
+    const bool odd = (reinterpret_cast<uintptr_t>(p) & 2) != 0;
+    const uint16_t* q = odd ? p - 1 : p;
+    const u32x4 v = *reinterpret_cast<const u32x4_word*>(q);
+    const uint32_t e = *reinterpret_cast<const uint32_t*>(odd ? q + 8 : q + 6);
+    const uint32_t sh = odd ? 16 : 0;
+    return __builtin_bit_cast(bf16x8, u32x4{__builtin_amdgcn_alignbit(v[1], v[0], sh),
+                                            __builtin_amdgcn_alignbit(v[2], v[1], sh),
+                                            __builtin_amdgcn_alignbit(v[3], v[2], sh),
+                                            __builtin_amdgcn_alignbit(e, v[3], sh)});
   }
+}
+// The same at k of a row of H elements, zero past it.
+template <int ALIGN>
+__device__ __forceinline__ bf16x8 load_k8_end(const uint16_t* row, int64_t k, int64_t H) {
   typedef __attribute__((ext_vector_type(8))) uint16_t u16x8;
+  if (ALIGN != 2 && k + 8 <= H) return load_k8<ALIGN>(row + k);
   u16x8 v;
 #pragma unroll
   for (int e = 0; e < 8; ++e) v[e] = k + e < H ? row[k + e] : uint16_t(0);
   return __builtin_bit_cast(bf16x8, v);
 }
 
-template <int NT, bool SOFTCAP, bool ANY>
+template <int NT, bool SOFTCAP, int ALIGN>
 __global__ __launch_bounds__(256) void k_lp_few(const uint16_t* __restrict__ h,
                                                 const uint16_t* __restrict__ W,
                                                 const int64_t* __restrict__ labels, int64_t N,
                                                 int64_t H, int64_t V, Warp warp, LpOut out) {
-  constexpr int U = NT == 1 ? 4 : 2;               // chunks in flight per wave
-  constexpr int LD = 68;                           // floats per token of the partial logits
-  __shared__ __attribute__((aligned(16))) float zb[4][16 * NT][LD];
+  constexpr int kT = 16 * NT, kAheadK = NT == 8 ? 1 : 3, R = kAheadK + 1, LD = 68;
+  union Smem {
+    uint16_t h[2][kT][kHld];
+    float z[kT][LD];
+  };
+  __shared__ __attribute__((aligned(16))) Smem sm;
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
   const int64_t v0 = int64_t(blockIdx.x) * 64;
   const int r = lane & 15, kg = (lane >> 4) * 8;
-  const uint16_t* wrow[4];
+  const int64_t v = v0 + w * 16 + r < V ? v0 + w * 16 + r : V - 1;
+  const uint16_t* wrow = W + v * H;
+  // h: load p of a thread is 16 bytes of token 16 p + tid / 16 at k = 8 (tid % 16)
+  const int hr = tid >> 4, hk = (tid & 15) * 8;
   const uint16_t* hrow[NT];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t v = v0 + i * 16 + r;
-    wrow[i] = W + (v < V ? v : V - 1) * H;
-  }
+  for (int p = 0; p < NT; ++p) hrow[p] = h + (16 * p + hr < N ? 16 * p + hr : N - 1) * H;
+  bf16x8 a[R][4], b[R][NT];
+  auto load = [&](bf16x8 (&fa)[4], bf16x8 (&fb)[NT], int64_t k0) {
 #pragma unroll
-  for (int i = 0; i < NT; ++i) {
-    const int64_t t = i * 16 + r;
-    hrow[i] = h + (t < N ? t : N - 1) * H;
-  }
-  f32x4 acc[4][NT];
+    for (int p = 0; p < NT; ++p) fb[p] = load_k8<ALIGN>(hrow[p] + k0 + hk);
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  auto step = [&](int64_t k0, auto count) {
-    constexpr int C = decltype(count)::value;
-    bf16x8 a[C][4], b[C][NT];
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int64_t k = k0 + c * 128 + kg;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) a[c][i] = load_k8<ANY>(wrow[i], k, H);
-#pragma unroll
-      for (int j = 0; j < NT; ++j) b[c][j] = load_k8<ANY>(hrow[j], k, H);
-    }
-#pragma unroll
-    for (int c = 0; c < C; ++c)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-          acc[i][j] =
-              __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[c][i], b[c][j], acc[i][j], 0, 0, 0);
+    for (int s = 0; s < 4; ++s) fa[s] = load_k8<ALIGN>(wrow + k0 + s * 32 + kg);
   };
-  int64_t k = w * 32;
-  for (; k + (U - 1) * 128 + 32 <= H; k += U * 128) step(k, std::integral_constant<int, U>{});
-  for (; k < H; k += 128) step(k, std::integral_constant<int, 1>{});
-  // acc[i][j][e]: row 16 i + 4 (lane / 16) + e, token 16 j + lane % 16
+  auto keep = [&](const bf16x8 (&fb)[NT], int half) {
+#pragma unroll
+    for (int p = 0; p < NT; ++p) *reinterpret_cast<bf16x8*>(&sm.h[half][16 * p + hr][hk]) = fb[p];
+  };
+  f32x4 acc[NT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  auto multiply = [&](const bf16x8 (&fa)[4], int half) {
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const bf16x8 f = *reinterpret_cast<const bf16x8*>(&sm.h[half][16 * j + r][s * 32 + kg]);
+        acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[s], f, acc[j], 0, 0, 0);
+      }
+  };
+  const int64_t full = H / kChunkK, end = full * kChunkK;
+  auto chunk_k = [&](int64_t c) { return (c < full ? c : full - 1) * kChunkK; };
+  if (end < H) {                                   // the end of the rows
+    bf16x8 ea[4], eb[NT];
+#pragma unroll
+    for (int p = 0; p < NT; ++p) eb[p] = load_k8_end<ALIGN>(hrow[p], end + hk, H);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) ea[s] = load_k8_end<ALIGN>(wrow, end + s * 32 + kg, H);
+    keep(eb, 1);
+    __syncthreads();
+    multiply(ea, 1);
+  }
+  if (full > 0) {
+#pragma unroll
+    for (int u = 0; u < kAheadK; ++u) load(a[u], b[u], chunk_k(u));
+    keep(b[0], 0);
+    __syncthreads();
+    for (int64_t c0 = 0; c0 < full; c0 += R) {
+#pragma unroll
+      for (int u = 0; u < R; ++u) {
+        load(a[(u + kAheadK) % R], b[(u + kAheadK) % R], chunk_k(c0 + u + kAheadK));
+        if (c0 + u < full) multiply(a[u], u & 1);
+        keep(b[(u + 1) % R], (u + 1) & 1);
+        __syncthreads();
+      }
+    }
+  }
+  __syncthreads();
+  // acc[j][e]: row 16 w + 4 (lane / 16) + e, token 16 j + lane % 16
 #pragma unroll
   for (int j = 0; j < NT; ++j)
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      *reinterpret_cast<f32x4*>(&zb[w][j * 16 + r][i * 16 + (lane >> 4) * 4]) = acc[i][j];
+    *reinterpret_cast<f32x4*>(&sm.z[16 * j + r][16 * w + (lane >> 4) * 4]) = acc[j];
   __syncthreads();
-  constexpr int TPT = NT == 3 ? 4 : 256 / (16 * NT), E = 64 / TPT;
+  constexpr int TPT = NT == 3 ? 4 : 256 / kT, E = 64 / TPT;
   const int t = tid / TPT, q = tid % TPT;
-  if (t >= 16 * NT) return;                        // NT = 3: whole waves
+  if (t >= kT) return;                             // NT = 3: whole waves
   float z[E];
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const int row = q * E + e;
-    z[e] = (zb[0][t][row] + zb[1][t][row]) + (zb[2][t][row] + zb[3][t][row]);
-  }
+  for (int e = 0; e < E; ++e) z[e] = sm.z[t][q * E + e];
   tile_epilogue<TPT, SOFTCAP>(z, q, t, N, labels, v0, int(V - v0 < 64 ? V - v0 : 64), V, warp,
                               out);
 }
@@ -592,12 +632,13 @@ __device__ __forceinline__ float key_value(uint64_t k) {
 __device__ __forceinline__ int64_t key_id(uint64_t k) { return int64_t(uint32_t(~uint32_t(k))); }
 __device__ __forceinline__ uint64_t max_u64(uint64_t a, uint64_t b) { return a > b ? a : b; }
 
-// Many tokens: 32 tokens a workgroup and G threads for each, thread g taking every
+// Many tokens: JT tokens a workgroup and G threads for each, thread g taking every
 // G-th part and list, then the threads pairwise. A thread keeps its KM largest keys
 // sorted in registers; two threads' lists meet as a bitonic sequence, through LDS,
-// which bounds G (128 KiB at 16 keys of 32 threads, or 32 keys of 16). With TAU_ONLY
-// just the lists so far: the top_k keys, and the top_k-th largest logit.
-constexpr int kJoinTokens = 32;
+// which bounds the threads (64 KiB at 16 keys of 1024, or 32 keys of 512). 32 tokens
+// read whole lines of every list; below 4096 tokens that leaves most CUs idle, and 4
+// tokens a workgroup are faster. With TAU_ONLY just the lists so far: the top_k keys,
+// and the top_k-th largest logit.
 constexpr int kAhead = 4;                          // loads in flight
 
 template <int KM>
@@ -631,13 +672,13 @@ struct TopKeys {
   }
 };
 
-template <bool SOFTCAP, bool TAU_ONLY, int G, int KM>     // top_k <= KM
-__global__ __launch_bounds__(32 * G) void k_lp_join(JoinArgs a) {
-  constexpr int kT = 32 * G;
+template <bool SOFTCAP, bool TAU_ONLY, int JT, int G, int KM>     // top_k <= KM
+__global__ __launch_bounds__(JT * G) void k_lp_join(JoinArgs a) {
+  constexpr int kT = JT * G;
   __shared__ uint64_t keys[KM * kT / 2];           // [key][thread]
   __shared__ float4 grp[kT / 2];
-  const int tid = threadIdx.x, tk = tid % kJoinTokens, g = tid / kJoinTokens;
-  const int64_t t = int64_t(blockIdx.x) * kJoinTokens + tk;
+  const int tid = threadIdx.x, tk = tid % JT, g = tid / JT;
+  const int64_t t = int64_t(blockIdx.x) * JT + tk;
   int64_t n_live = a.N;
   if (a.count) { const int64_t c = *a.count; n_live = c < n_live ? c : n_live; }
   const bool live = t < n_live;
@@ -685,7 +726,7 @@ __global__ __launch_bounds__(32 * G) void k_lp_join(JoinArgs a) {
   }
   for (int half = G / 2; half > 0; half >>= 1) {
     // threads half .. 2 half - 1 of each token hand theirs to 0 .. half - 1
-    const int slot = tid % (half * kJoinTokens);
+    const int slot = tid % (half * JT);
     if (g >= half && g < 2 * half) {
       grp[slot] = make_float4(M, S, D, 0.f);
 #pragma unroll
@@ -1089,6 +1130,9 @@ __global__ __launch_bounds__(256) void k_f32_dh_sum(const float* __restrict__ pa
 
 unsigned cdiv(int64_t a, int64_t b) { return unsigned((a + b - 1) / b); }
 
+template <int I>
+using Int = std::integral_constant<int, I>;
+
 template <bool SOFTCAP, bool TAU_ONLY>
 hipError_t run_join(const LpPlan& q, const JoinArgs& j, const Launcher& L) {
   L.pre(kLpJoin);
@@ -1096,16 +1140,18 @@ hipError_t run_join(const LpPlan& q, const JoinArgs& j, const Launcher& L) {
     hipLaunchKernelGGL(k_lp_join_few<SOFTCAP>, dim3(unsigned(j.N)), dim3(kFewThreads), 0,
                        L.stream, j);
   } else {
-    const dim3 grid(cdiv(j.N, kJoinTokens));
-    if (j.top_k <= 1)
-      hipLaunchKernelGGL((k_lp_join<SOFTCAP, TAU_ONLY, 32, 1>), grid, dim3(1024), 0, L.stream, j);
-    else if (j.top_k <= 8)
-      hipLaunchKernelGGL((k_lp_join<SOFTCAP, TAU_ONLY, 32, 8>), grid, dim3(1024), 0, L.stream, j);
-    else if (j.top_k <= 16)
-      hipLaunchKernelGGL((k_lp_join<SOFTCAP, TAU_ONLY, 32, 16>), grid, dim3(1024), 0, L.stream, j);
-    else
-      hipLaunchKernelGGL((k_lp_join<SOFTCAP, TAU_ONLY, 16, kLpTop>), grid, dim3(512), 0, L.stream,
-                         j);
+    auto run = [&](auto jt, auto threads, auto km) {
+      constexpr int JT = decltype(jt)::value, T = decltype(threads)::value;
+      hipLaunchKernelGGL((k_lp_join<SOFTCAP, TAU_ONLY, JT, T / JT, decltype(km)::value>),
+                         dim3(cdiv(j.N, JT)), dim3(T), 0, L.stream, j);
+    };
+    auto by_k = [&](auto jt) {
+      if (j.top_k <= 1) run(jt, Int<1024>{}, Int<1>{});
+      else if (j.top_k <= 8) run(jt, Int<1024>{}, Int<8>{});
+      else if (j.top_k <= 16) run(jt, Int<1024>{}, Int<16>{});
+      else run(jt, Int<512>{}, Int<kLpTop>{});
+    };
+    j.N >= 4096 ? by_k(Int<32>{}) : by_k(Int<4>{});
   }
   L.post(kLpJoin);
   return hipGetLastError();
@@ -1118,18 +1164,20 @@ hipError_t run_few(const LpArgs& a, const Warp& warp, const LpOut& out, const La
   const dim3 grid(cdiv(a.V, kLpRows));
   auto go = [&](auto nt) {
     constexpr int NT = decltype(nt)::value;
-    if (a.H % 8 == 0)
-      hipLaunchKernelGGL((k_lp_few<NT, SOFTCAP, false>), grid, dim3(256), 0, L.stream, h, W,
-                         a.tokens, a.N, a.H, a.V, warp, out);
-    else
-      hipLaunchKernelGGL((k_lp_few<NT, SOFTCAP, true>), grid, dim3(256), 0, L.stream, h, W,
-                         a.tokens, a.N, a.H, a.V, warp, out);
+    auto run = [&](auto align) {
+      hipLaunchKernelGGL((k_lp_few<NT, SOFTCAP, decltype(align)::value>), grid, dim3(256), 0,
+                         L.stream, h, W, a.tokens, a.N, a.H, a.V, warp, out);
+    };
+    if (a.H % 8 == 0) run(Int<16>{});
+    else if (a.H % 2 == 0) run(Int<4>{});
+    else run(Int<2>{});
   };
   L.pre(kLpTiles);
-  if (a.N <= 16) go(std::integral_constant<int, 1>{});
-  else if (a.N <= 32) go(std::integral_constant<int, 2>{});
-  else if (a.N <= 48) go(std::integral_constant<int, 3>{});
-  else go(std::integral_constant<int, 4>{});
+  if (a.N <= 16) go(Int<1>{});
+  else if (a.N <= 32) go(Int<2>{});
+  else if (a.N <= 48) go(Int<3>{});
+  else if (a.N <= 64) go(Int<4>{});
+  else go(Int<8>{});
   L.post(kLpTiles);
   return hipGetLastError();
 }

@@ -96,7 +96,7 @@ bool make_embed_plan(int64_t N, int64_t H, int64_t V, EmbedPlan* p);
 // ---- token log probabilities -------------------------------------------------------
 // Tokens up to which a bf16 call streams W once through the few-token kernel
 // instead of the 256 x 256 tiles (see kernels_logprobs.hip for both sides).
-constexpr int64_t kFewTokens = 64;
+constexpr int64_t kFewTokens = 128;
 // Vocabulary rows per workgroup of the few-token and float32 kernels.
 constexpr int64_t kLpRows = 64;
 // Vocabulary up to which the 64-row tiles are joined with alternatives: 32 of the

@@ -109,7 +109,9 @@ BF, F = torch.bfloat16, torch.float32
 # matrix-core tiles (one and several of each edge, gathered, odd H), float32
 FORWARD = [(1, 64, 1, BF, 3), (1, 4096, 5000, BF, 8), (2, 33, 63, BF, 32), (15, 100, 64, BF, 4),
            (16, 1024, 4097, BF, 1), (17, 257, 1000, BF, 20), (33, 96, 70000, BF, 5),
-           (64, 512, 999, BF, 32), (65, 512, 999, BF, 10), (65, 41, 130, BF, 32),
+           (64, 512, 999, BF, 32), (65, 512, 999, BF, 10), (65, 41, 130, BF, 32), (40, 130, 515, BF, 4),
+           (128, 258, 1001, BF, 3), (100, 385, 333, BF, 17), (129, 512, 999, BF, 10),
+           (140, 41, 130, BF, 32),
            (300, 136, 2000, BF, 7), (513, 72, 255, BF, 3), (700, 520, 3001, BF, 0),
            (1, 64, 1, F, 2), (3, 77, 200, F, 6), (64, 33, 64, F, 20), (65, 515, 1001, F, 32),
            (257, 130, 333, F, 0)]
