@@ -397,7 +397,7 @@ __global__ __launch_bounds__(256) void k_lp_few(const uint16_t* __restrict__ h,
                                                 const uint16_t* __restrict__ W,
                                                 const int64_t* __restrict__ labels, int64_t N,
                                                 int64_t H, int64_t V, Warp warp, LpOut out) {
-  constexpr int kT = 16 * NT, kAheadK = NT == 8 ? 1 : 3, R = kAheadK + 1, LD = 68;
+  constexpr int kT = 16 * NT, kAheadK = NT == 8 ? 1 : NT >= 3 ? 2 : 3, R = kAheadK + 1, LD = 68;
   union Smem {
     uint16_t h[2][kT][kHld];
     float z[kT][LD];
@@ -457,8 +457,9 @@ __global__ __launch_bounds__(256) void k_lp_few(const uint16_t* __restrict__ h,
 #pragma unroll
       for (int u = 0; u < R; ++u) {
         load(a[(u + kAheadK) % R], b[(u + kAheadK) % R], chunk_k(c0 + u + kAheadK));
-        if (c0 + u < full) multiply(a[u], u & 1);
-        keep(b[(u + 1) % R], (u + 1) & 1);
+        const int half = int(c0 + u) & 1;
+        if (c0 + u < full) multiply(a[u], half);
+        keep(b[(u + 1) % R], half ^ 1);
         __syncthreads();
       }
     }
