@@ -381,11 +381,13 @@ constexpr int kSumWaves = 8, kSumWave = 32;
 static_assert(kSumWaves * kSumWave == kEmbedWindow, "tokens per workgroup");
 constexpr int kInFlight = 8;                       // rows loaded before they are added
 
-template <class T, class G>
+// WEIGHT: row i counts weight[i] times.
+template <class T, class G, bool WEIGHT>
 __global__ __launch_bounds__(64 * kSumWaves) void k_embed_sum(
     const uint32_t* __restrict__ skey, const uint32_t* __restrict__ spos,
     const T* __restrict__ dout, int64_t ldd, int64_t N, int64_t H, int64_t V, int64_t slices,
-    float scale, int accumulate, G* __restrict__ dW, float* __restrict__ part) {
+    float scale, int accumulate, G* __restrict__ dW, float* __restrict__ part,
+    const float* __restrict__ weight) {
   __shared__ float edge[2][kSumWaves][kSliceCols];           // first runs, last runs
   __shared__ uint32_t end_key[kSumWaves];          // the id that goes on behind a wave, or V
   __shared__ int whole[kSumWaves];                 // its 32 are one run of an id begun before
@@ -399,6 +401,7 @@ __global__ __launch_bounds__(64 * kSumWaves) void k_embed_sum(
   // the wave's keys and positions in its lanes; the keys beside them
   const int64_t il = n > 0 ? i0 + ((lane & 31) < n ? (lane & 31) : n - 1) : 0;
   const uint32_t keys = n > 0 ? skey[il] : none, poss = n > 0 ? spos[il] : 0;
+  const float wgts = WEIGHT && keys < none ? weight[poss] : 1.f;
   const uint32_t before = i0 > 0 && n > 0 ? skey[i0 - 1] : none;
   const uint32_t behind = n == kSumWave && i0 + n < N ? skey[i0 + n] : none;
   auto uni = [](uint32_t x) -> uint32_t { return __builtin_amdgcn_readfirstlane(x); };
@@ -425,8 +428,9 @@ __global__ __launch_bounds__(64 * kSumWaves) void k_embed_sum(
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[e] = 0.f;
       }
+      const float x = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(wgts), q + r));
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] += f[r][e];
+      for (int e = 0; e < 8; ++e) acc[e] = WEIGHT ? fmaf(x, f[r][e], acc[e]) : acc[e] + f[r][e];
     }
   };
 #pragma unroll
@@ -515,16 +519,16 @@ __global__ __launch_bounds__(256) void k_embed_join(const uint32_t* __restrict__
   write_row(dW, int64_t(key), H, c, scale, accumulate, acc);
 }
 
-template <class T, class G>
+template <class T, class G, bool WEIGHT = false>
 hipError_t sums(const EmbedGradArgs& a, const uint32_t* key, const uint32_t* pos,
                 const Launcher& L) {
   const int64_t slices = (a.H + kSliceCols - 1) / kSliceCols;
   const int64_t windows = (a.N + kEmbedWindow - 1) / kEmbedWindow;
   G* dW = static_cast<G*>(a.dW);
   L.pre(kEmbedGrad);
-  hipLaunchKernelGGL((k_embed_sum<T, G>), dim3(unsigned(windows * slices)), dim3(64 * kSumWaves), 0,
+  hipLaunchKernelGGL((k_embed_sum<T, G, WEIGHT>), dim3(unsigned(windows * slices)), dim3(64 * kSumWaves), 0,
                      L.stream, key, pos, static_cast<const T*>(a.dout), a.ld_dout, a.N, a.H, a.V,
-                     slices, a.scale, a.accumulate, dW, a.part);
+                     slices, a.scale, a.accumulate, dW, a.part, a.weight);
   L.post(kEmbedGrad);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || windows == 1) return e;
@@ -619,6 +623,10 @@ hipError_t launch_embedding_backward(const EmbedGradArgs& a, const Launcher& L) 
     }
   }
   if (e != hipSuccess) return e;
+  if (a.weight) {
+    if (a.dtype != FLCE_BF16 || a.grad_dtype != FLCE_BF16) return hipErrorInvalidValue;
+    return sums<Bf16Bits, Bf16Bits, true>(a, a.key[at], a.pos[at], L);
+  }
   if (a.dtype == FLCE_F32) return sums<float, float>(a, a.key[at], a.pos[at], L);
   if (a.grad_dtype == FLCE_F32) return sums<Bf16Bits, float>(a, a.key[at], a.pos[at], L);
   return sums<Bf16Bits, Bf16Bits>(a, a.key[at], a.pos[at], L);

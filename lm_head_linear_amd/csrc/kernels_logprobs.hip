@@ -896,6 +896,13 @@ __global__ __launch_bounds__(kFewThreads) void k_lp_join_few(JoinArgs a) {
 // so G = (ca [v = y] + p (c0 + c1 l)) dx/dz with ca = a, c0 = -(a + b entropy),
 // c1 = -b, formed once per live token in the gathered order. A token outside the
 // vocabulary gets NaN: its gradients fail closed, as the head's loss does.
+//
+// G goes to the products as bf16, off by up to 2^-9 of itself. That adds up where it
+// matters most: the G of the given tokens is by far the largest of its row, and the
+// dW row of a frequent token is the sum of many of them, often of either sign. So
+// what rounding those left is kept in float32 and added to dW afterwards, a weighted
+// lookup gradient over the same rows (a few 10 us next to milliseconds): a row whose
+// terms cancel is then off by half a step of its own value, not of its terms.
 __global__ __launch_bounds__(256) void k_lp_coef(
     const int32_t* __restrict__ idx, const int64_t* __restrict__ labels,
     const int64_t* __restrict__ count, int64_t N, int64_t V, int64_t ignore_index,
@@ -925,6 +932,7 @@ struct EpiLpGrad {
   Warp warp;
   uint16_t* g;
   int64_t lo_off;             // elements from the hi to the lo chunk (SPLIT)
+  float* rest;                // !SPLIT: what rounding the given token's G leaves
 
   static constexpr int kTokBytes = 6144;
   __device__ __forceinline__ void stage(char* tok, int64_t n0, int wave, int lane) const {
@@ -974,6 +982,7 @@ struct EpiLpGrad {
               if (i == ti && r == tr) { z = acc[i][j][r]; v = grad(i, j, r); }
           tp.pos[j] = target_slot(d, j * 16 + (lane & 15));
           tp.val[j] = fmaf(ca_t[tl], warp_slope<SOFTCAP>(warp, z), v);
+          if (!SPLIT) rest[n0 + tl] = tp.val[j] - bf16_to_f32(f32_to_bf16(tp.val[j]));
         }
       }
     }
@@ -1374,7 +1383,7 @@ hipError_t launch_lp_gradient(const Plan& p, const Args& a, const LpGradArgs& g,
   auto run = [&](auto cap, auto split) {
     const EpiLpGrad<decltype(cap)::value, decltype(split)::value> epi{
         a.yc, g.lse_g, g.c0, g.c1, g.ca, p.N, p.V, v0, vcur, gemm::g_block(p), warp,
-        static_cast<uint16_t*>(a.g), p.vchunk * p.ldg};
+        static_cast<uint16_t*>(a.g), p.vchunk * p.ldg, g.rest};
     return run_gemm<NF, NF, kDynN>(l, a, epi, kGradLogits, L, &a.sc->n_valid);
   };
   using Y = std::true_type;

@@ -92,13 +92,8 @@ int flce_embedding_backward(const int64_t* tokens, const void* dout, int64_t ld_
   char* ws = static_cast<char*>(workspace);
   flce::EmbedGradArgs a{tokens, dout, ld_dout, N, H, V, padding_index, scale, dW,
                         accumulate_dW ? 1 : 0, dtype, grad_dtype, status, {}, {},
-                        nullptr, nullptr};
-  for (int i = 0; i < 2; ++i) {
-    a.key[i] = reinterpret_cast<uint32_t*>(ws + p.off_key[i]);
-    a.pos[i] = reinterpret_cast<uint32_t*>(ws + p.off_pos[i]);
-  }
-  a.hist = reinterpret_cast<uint32_t*>(ws + p.off_hist);
-  a.part = reinterpret_cast<float*>(ws + p.off_part);
+                        nullptr, nullptr, nullptr};
+  flce::carve_embed(p, ws, &a);
   return status_of(flce::launch_embedding_backward(a, L));
 }
 
@@ -172,8 +167,10 @@ int flce_logprobs_backward(const void* h, const void* W, const int64_t* tokens, 
   const flce::LpGradArgs g{lse, entropy, grad_logp, grad_entropy, temperature,
                            reinterpret_cast<float*>(own), reinterpret_cast<float*>(own + arr),
                            reinterpret_cast<float*>(own + 2 * arr),
-                           reinterpret_cast<float*>(own + 3 * arr)};
-  if (dtype == FLCE_F32) a.dh_part = reinterpret_cast<float*>(own + 4 * arr);
+                           reinterpret_cast<float*>(own + 3 * arr),
+                           reinterpret_cast<float*>(own + 4 * arr)};
+  own += 5 * arr;
+  if (dtype == FLCE_F32) a.dh_part = reinterpret_cast<float*>(own);
   {
     Range s("flce.setup");
     e = flce::pad_inputs(p, a, ws, true, L);
@@ -188,6 +185,16 @@ int flce_logprobs_backward(const void* h, const void* W, const int64_t* tokens, 
     if (e == hipSuccess)
       e = dtype == FLCE_BF16 ? flce::bf16_chunk_products(p, a, c, L)
                              : flce::launch_lp_f32_products(p, a, c, L);
+  }
+  if (e == hipSuccess && dtype == FLCE_BF16 && grad_dtype == FLCE_BF16) {
+    // dW[token] += (what rounding the token's G left) h, over the gathered rows
+    Range s("flce.rounding_rest");
+    flce::EmbedPlan ep;
+    if (!flce::make_embed_plan(N, p.H, V, &ep)) return FLCE_ERR_ARG;
+    flce::EmbedGradArgs r{a.yc, a.hc, p.H, N, p.H, V, ignore_index, 1.f, a.dW, 1, dtype,
+                          grad_dtype, nullptr, {}, {}, nullptr, nullptr, g.rest};
+    flce::carve_embed(ep, own, &r);
+    e = flce::launch_embedding_backward(r, L);
   }
   if (e == hipSuccess) e = flce::crop_outputs(p, ws, dH, dW, L);
   return status_of(e);

@@ -317,9 +317,16 @@ size_t flce_logprobs_backward_workspace_size(int64_t N, int64_t H, int64_t V, in
   Plan p;
   if (!make_plan(N, H, V, dtype, &p, true, grad_dtype)) return 0;
   // the head's backward, its dummy count, the token coefficients, and the partial
-  // products of a split float32 dH
-  return p.total + 256 + 4 * align256(size_t(p.ld_part) * sizeof(float)) +
-         (dtype == FLCE_F32 ? align256(lp_f32_part_bytes(p)) : 0);
+  // products of a split float32 dH, or the lookup gradient that adds what rounding G
+  // to bf16 left of the given tokens
+  size_t more = 0;
+  if (dtype == FLCE_F32) more = align256(lp_f32_part_bytes(p));
+  else if (grad_dtype == FLCE_BF16) {
+    EmbedPlan e;
+    if (!make_embed_plan(N, p.H, V, &e)) return 0;
+    more = e.total;
+  }
+  return p.total + 256 + 5 * align256(size_t(p.ld_part) * sizeof(float)) + more;
 }
 
 int flce_logprobs_backward_check_args(const void* h, const void* W, const int64_t* tokens,

@@ -84,6 +84,7 @@ struct EmbedGradArgs {
   uint32_t* pos[2];
   uint32_t* hist;             // [256][blocks] digit counts (N > kSortMerge)
   float* part;                // [windows][2][H] partial rows
+  const float* weight;        // [N], or null: row i counts weight[i] times (bf16 only)
 };
 
 struct EmbedPlan {
@@ -92,6 +93,15 @@ struct EmbedPlan {
 
 // False for sizes that are not valid.
 bool make_embed_plan(int64_t N, int64_t H, int64_t V, EmbedPlan* p);
+// The plan's buffers in a workspace.
+inline void carve_embed(const EmbedPlan& p, char* ws, EmbedGradArgs* a) {
+  for (int i = 0; i < 2; ++i) {
+    a->key[i] = reinterpret_cast<uint32_t*>(ws + p.off_key[i]);
+    a->pos[i] = reinterpret_cast<uint32_t*>(ws + p.off_pos[i]);
+  }
+  a->hist = reinterpret_cast<uint32_t*>(ws + p.off_hist);
+  a->part = reinterpret_cast<float*>(ws + p.off_part);
+}
 
 // ---- token log probabilities -------------------------------------------------------
 // Tokens up to which a bf16 call streams W once through the few-token kernel
@@ -181,6 +191,7 @@ struct LpGradArgs {
   float* c0;
   float* c1;
   float* ca;
+  float* rest;                // what rounding the given token's G left (bf16 G)
 };
 
 }  // namespace flce

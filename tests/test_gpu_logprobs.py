@@ -250,6 +250,30 @@ def test_backward(N, H, V, dt, cap, T, parts, monkeypatch):
         gu.assert_grad("dW f32", eW, ref["dW"].cpu().numpy(), 1e-4)
 
 
+@pytest.mark.parametrize("H", [128, 133])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_a_row_whose_terms_cancel(H, accumulate, monkeypatch):
+    """300 pairs of rows with one token and upstream gradients a and -a (1 - 2^-8): the
+    token's dW row is 2^-8 of its terms, below what a bf16 G resolves of them. It has
+    to be right to a few steps of its own: G errs by exp's 2^-18 of the terms, 2^-10 of
+    the row, the other tokens' G by 2^-9 p of the terms with p < 2^-5 (2^-6 of the row)
+    with random signs over 600 rows, and the row is rounded twice (2^-8 each)."""
+    import lm_head_linear_amd as m
+    monkeypatch.setenv("FLCE_VCHUNK", "512")
+    h, W, y, a, _ = make(300, H, 1200, BF, ignored=0.0, peaked=False)
+    h = h.repeat(2, 1)
+    y = torch.full((600,), 700, device="cuda")
+    a = a.abs() + 0.5
+    a = torch.cat([a, -a * (1 - 2.0 ** -8)])
+    r = m.flce_logprobs(h, W, y)
+    base = torch.zeros_like(W)
+    _, dW = m.flce_logprobs_backward(h, W, y, r.lse, r.entropy, a, dW=base if accumulate else None,
+                                     accumulate_dW=accumulate)
+    ref = reference(h, W, y, 0, 0.0, 1.0, a, None)["dW"][700]
+    err = (dW[700].double() - ref).norm() / ref.norm()
+    assert float(err) < 2.0 ** -6, float(err)
+
+
 def test_gradients_against_differences():
     """Autograd of the float32 form against central differences of its forward in
     random directions: a step of 2^-7 (directions of norm 1) has a truncation
