@@ -4,8 +4,8 @@
 // The lookup reads and writes a row per token and is bound by that.
 //
 // The gradient sorts the tokens (stable, so equal ids keep their order), and the
-// rows of kEmbedWindow sorted tokens are then added up over a slice of columns by
-// a workgroup, one id after another: each row of dout is read once, a dW row whose
+// rows of 64 or 256 sorted tokens are then added up over a slice of columns by a
+// workgroup, one id after another: each row of dout is read once, a dW row whose
 // tokens lie in one window is written once, and the sums are float32 in a fixed
 // order. An id whose tokens reach past a window leaves a float32 partial row per
 // window; a second pass adds those up in window order. Atomic adds would need
@@ -326,103 +326,131 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_scatter(
 }
 
 // ---- the sums ---------------------------------------------------------------------
-// A lane's E values of a slice: 8 columns of either dout type.
-constexpr int kLaneCols = 8;
-constexpr int kSliceCols = 64 * kLaneCols;
+// A wave's slice of kSliceCols columns, 8 a lane: 8 adjacent ones (FULL, a slice within
+// the row), or every 64th (the slice at the row's end: loads past it read the row's
+// last value, stores there are left out).
+constexpr int kSliceCols = 512;
 
-template <class T>
-__device__ __forceinline__ void load_cols(const T* row, int64_t c, int64_t n, float (&f)[8]) {
-  if constexpr (sizeof(T) == 2) {
-    load_chunk(row, c, n, f);
-  } else {
-    float a[4], b[4];
-    load_chunk(row, c, n, a);
-    load_chunk(row, c + 4, n, b);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) { f[e] = a[e]; f[4 + e] = b[e]; }
+template <bool FULL>
+struct Slice {
+  int64_t c0, H;
+  int lane;
+  __device__ __forceinline__ int64_t col(int e) const {
+    const int64_t c = c0 + e * 64 + lane;
+    return c < H ? c : H - 1;
   }
-}
-template <class T>
-__device__ __forceinline__ void store_cols(T* row, int64_t c, int64_t n, const float (&f)[8]) {
-  if constexpr (sizeof(T) == 2) {
-    store_chunk(row, c, n, f);
-  } else {
-    float a[4], b[4];
+  template <class T>
+  __device__ __forceinline__ void load(const T* row, float (&f)[8]) const {
+    if constexpr (!FULL) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) { a[e] = f[e]; b[e] = f[4 + e]; }
-    store_chunk(row, c, n, a);
-    store_chunk(row, c + 4, n, b);
+      for (int e = 0; e < 8; ++e) f[e] = to_f32(row[col(e)]);
+    } else if constexpr (sizeof(T) == 2) {
+      unpack_chunk<T>(load_raw(row + c0 + lane * 8), f);
+    } else {
+      float a[4], b[4];
+      unpack_chunk<T>(load_raw(row + c0 + lane * 8), a);
+      unpack_chunk<T>(load_raw(row + c0 + lane * 8 + 4), b);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) { f[e] = a[e]; f[4 + e] = b[e]; }
+    }
   }
-}
+  template <class T>
+  __device__ __forceinline__ void store(T* row, const float (&f)[8]) const {
+    if constexpr (!FULL) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (c0 + e * 64 + lane < H) row[c0 + e * 64 + lane] = from_f32<T>(f[e]);
+    } else if constexpr (sizeof(T) == 2) {
+      *reinterpret_cast<row_u32x4_any*>(row + c0 + lane * 8) = pack_chunk<T>(f);
+    } else {
+      const float a[4] = {f[0], f[1], f[2], f[3]}, b[4] = {f[4], f[5], f[6], f[7]};
+      *reinterpret_cast<row_u32x4_any*>(row + c0 + lane * 8) = pack_chunk<T>(a);
+      *reinterpret_cast<row_u32x4_any*>(row + c0 + lane * 8 + 4) = pack_chunk<T>(b);
+    }
+  }
+  __device__ __forceinline__ int slot(int e) const { return FULL ? lane * 8 + e : e * 64 + lane; }
+};
 
-// dW[v] = scale acc, added to what is there when `accumulate`.
-template <class G>
-__device__ __forceinline__ void write_row(G* dW, int64_t v, int64_t H, int64_t c, float scale,
-                                          int accumulate, const float (&acc)[8]) {
-  float f[8];
-  if (accumulate) {
-    load_cols(dW + v * H, c, H, f);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = fmaf(acc[e], scale, f[e]);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = acc[e] * scale;
-  }
-  store_cols(dW + v * H, c, H, f);
-}
+struct SumArgs {
+  const uint32_t* skey;
+  const uint32_t* spos;
+  const void* dout;
+  const float* weight;        // WEIGHT: row i counts weight[i] times
+  int64_t ldd, N, H, V, slices;
+  float scale;
+  void* dW;
+  float* part;
+};
 
-// A workgroup: 256 sorted tokens over kSliceCols columns, 32 of them a wave, in
-// order. A wave writes the rows of the ids that begin and end in its 32; its first
-// run, if the id began before, and its last, if the id goes on, stay in LDS, where
-// the wave in which an id began adds up what the others left of it. What reaches past
-// the workgroup's tokens goes to memory: part[2 w] of an id that began before
-// workgroup w's tokens, part[2 w + 1] of one that begins there and goes on.
-constexpr int kSumWaves = 8, kSumWave = 32;
-static_assert(kSumWaves * kSumWave == kEmbedWindow, "tokens per workgroup");
+// A workgroup: 8 SW sorted tokens over a slice, SW of them a wave, in order. A wave
+// writes the rows of the ids that begin and end in its SW; its first run, if the id
+// began before, and its last, if the id goes on, stay in LDS, where the wave in which
+// an id began adds up what the others left of it. What reaches past the workgroup's
+// tokens goes to memory: part[2 w] of an id that began before workgroup w's tokens,
+// part[2 w + 1] of one that begins there and goes on. ADD: the dW row is added to; it
+// is loaded with the rows of dout, so that no id waits for its own.
+constexpr int kSumWaves = 8;
 constexpr int kInFlight = 8;                       // rows loaded before they are added
 
-// WEIGHT: row i counts weight[i] times.
-template <class T, class G, bool WEIGHT>
-__global__ __launch_bounds__(64 * kSumWaves) void k_embed_sum(
-    const uint32_t* __restrict__ skey, const uint32_t* __restrict__ spos,
-    const T* __restrict__ dout, int64_t ldd, int64_t N, int64_t H, int64_t V, int64_t slices,
-    float scale, int accumulate, G* __restrict__ dW, float* __restrict__ part,
-    const float* __restrict__ weight) {
-  __shared__ float edge[2][kSumWaves][kSliceCols];           // first runs, last runs
-  __shared__ uint32_t end_key[kSumWaves];          // the id that goes on behind a wave, or V
-  __shared__ int whole[kSumWaves];                 // its 32 are one run of an id begun before
-  const int lane = threadIdx.x & 63;
+struct SumEdges {
+  float run[2][kSumWaves][kSliceCols];             // first runs, last runs
+  int whole[kSumWaves];                            // a wave's tokens are one run of an id
+};                                                 //   that began before and goes on
+
+template <class T, class G, bool WEIGHT, bool ADD, int SW, bool FULL>
+__device__ __forceinline__ void sum_slice(const SumArgs& a, int64_t wd, const Slice<FULL>& sl,
+                                          SumEdges& edge) {
+  const int lane = sl.lane;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t wd = blockIdx.x / slices;
-  const int64_t cl = lane * kLaneCols, c = (blockIdx.x - wd * slices) * kSliceCols + cl;
-  const int64_t i0 = wd * kEmbedWindow + w * kSumWave;
-  const int n = i0 >= N ? 0 : int(N - i0 < kSumWave ? N - i0 : kSumWave);
-  const uint32_t none = uint32_t(V);
-  // the wave's keys and positions in its lanes; the keys beside them
-  const int64_t il = n > 0 ? i0 + ((lane & 31) < n ? (lane & 31) : n - 1) : 0;
-  const uint32_t keys = n > 0 ? skey[il] : none, poss = n > 0 ? spos[il] : 0;
-  const float wgts = WEIGHT && keys < none ? weight[poss] : 1.f;
-  const uint32_t before = i0 > 0 && n > 0 ? skey[i0 - 1] : none;
-  const uint32_t behind = n == kSumWave && i0 + n < N ? skey[i0 + n] : none;
+  const int64_t H = a.H, N = a.N;
+  G* dW = static_cast<G*>(a.dW);
+  const T* dout = static_cast<const T*>(a.dout);
+  const int64_t i0 = (wd * kSumWaves + w) * SW;
+  const int n = i0 >= N ? 0 : int(N - i0 < SW ? N - i0 : SW);
+  const uint32_t none = uint32_t(a.V);
+  // the wave's keys, positions and weights in its lanes; the keys beside them
+  const int li = lane & (SW - 1);
+  const int64_t il = n > 0 ? i0 + (li < n ? li : n - 1) : 0;
+  const uint32_t keys = n > 0 ? a.skey[il] : none, poss = n > 0 ? a.spos[il] : 0;
+  const float wgts = WEIGHT && keys < none ? a.weight[poss] : 1.f;
+  const uint32_t before = i0 > 0 && n > 0 ? a.skey[i0 - 1] : none;
+  const uint32_t behind = n == SW && i0 + n < N ? a.skey[i0 + n] : none;
   auto uni = [](uint32_t x) -> uint32_t { return __builtin_amdgcn_readfirstlane(x); };
   auto key_of = [&](int q) -> uint32_t { return __builtin_amdgcn_readlane(keys, q); };
   uint32_t cur = key_of(0);
   bool head = cur < none && uni(before) == cur;
-  const uint32_t last = n > 0 ? key_of(31) : none;
+  const uint32_t last = n > 0 ? key_of(SW - 1) : none;
   const bool tail = last < none && uni(behind) == last;
-  float acc[8] = {};
+  float acc[8] = {}, old[8] = {};
+  auto write = [&](uint32_t key) {
+    float f[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = ADD ? fmaf(acc[e], a.scale, old[e]) : acc[e] * a.scale;
+    sl.store(dW + int64_t(key) * H, f);
+  };
   auto leave = [&](int which) {                    // the run so far, to LDS
 #pragma unroll
-    for (int e = 0; e < 8; ++e) edge[which][w][cl + e] = acc[e];
+    for (int e = 0; e < 8; ++e) edge.run[which][w][sl.slot(e)] = acc[e];
   };
-  auto add_rows = [&](int q, const float (&f)[kInFlight][8]) {
+#pragma unroll 1
+  for (int q = 0; q < SW; q += kInFlight) {
+    if (q >= n || key_of(q) >= none) break;        // the rest has no rows
+    float f[kInFlight][8], g[ADD ? kInFlight : 1][8];
+#pragma unroll
+    for (int r = 0; r < kInFlight; ++r) {
+      sl.load(dout + int64_t(uint32_t(__builtin_amdgcn_readlane(poss, q + r))) * a.ldd, f[r]);
+      if constexpr (ADD) {
+        const uint32_t key = key_of(q + r);
+        sl.load(dW + int64_t(key < none ? key : 0) * H, g[r]);
+      }
+    }
 #pragma unroll
     for (int r = 0; r < kInFlight; ++r) {
       const uint32_t key = key_of(q + r);
       if (q + r >= n || key >= none) continue;
       if (key != cur) {
         if (head) leave(0);
-        else write_row(dW, int64_t(cur), H, c, scale, accumulate, acc);
+        else write(cur);
         cur = key;
         head = false;
 #pragma unroll
@@ -430,82 +458,81 @@ __global__ __launch_bounds__(64 * kSumWaves) void k_embed_sum(
       }
       const float x = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(wgts), q + r));
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] = WEIGHT ? fmaf(x, f[r][e], acc[e]) : acc[e] + f[r][e];
+      for (int e = 0; e < 8; ++e) {
+        acc[e] = WEIGHT ? fmaf(x, f[r][e], acc[e]) : acc[e] + f[r][e];
+        if constexpr (ADD) old[e] = g[r][e];
+      }
     }
-  };
-#pragma unroll
-  for (int q = 0; q < kSumWave; q += kInFlight) {
-    if (q >= n || key_of(q) >= none) break;        // the rest has no rows
-    float f[kInFlight][8];
-#pragma unroll
-    for (int r = 0; r < kInFlight; ++r)
-      load_cols(dout + int64_t(uint32_t(__builtin_amdgcn_readlane(poss, q + r))) * ldd, c, H, f[r]);
-    add_rows(q, f);
   }
   if (cur < none) {
     if (head) leave(0);
     else if (tail) leave(1);
-    else write_row(dW, int64_t(cur), H, c, scale, accumulate, acc);
+    else write(cur);
   }
-  if (lane == 0) {
-    end_key[w] = tail ? last : none;
-    whole[w] = tail && head;                       // head still set: no other id came
-  }
+  if (lane == 0) edge.whole[w] = tail && head;     // head still set: no other id came
   __syncthreads();
-  // wave w: the id that began in it and goes on; wave 0 also the one begun before
+  // wave w: the id that began in it and goes on; wave 0 also the one begun before.
+  // True if it goes on past the workgroup.
   auto join = [&](int from, bool began) {
     int x = began ? from + 1 : 0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] = began ? edge[1][from][cl + e] : 0.f;
+    for (int e = 0; e < 8; ++e) acc[e] = began ? edge.run[1][from][sl.slot(e)] : 0.f;
     for (; x < kSumWaves; ++x) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] += edge[0][x][cl + e];
-      if (!whole[x]) break;
+      for (int e = 0; e < 8; ++e) acc[e] += edge.run[0][x][sl.slot(e)];
+      if (!edge.whole[x]) break;
     }
-    return x == kSumWaves;                         // it goes on past the workgroup
+    return x == kSumWaves;
   };
-  if (w == 0 && uni(before) < none && uni(before) == key_of(0) && n > 0) {
+  const bool began_before = w == 0 && n > 0 && uni(before) < none && uni(before) == key_of(0);
+  if (began_before) {
     join(0, false);
-    store_cols(part + 2 * wd * H, c, H, acc);
+    sl.store(a.part + 2 * wd * H, acc);
   }
-  if (tail && !whole[w]) {
-    if (join(w, true)) store_cols(part + (2 * wd + 1) * H, c, H, acc);
-    else write_row(dW, int64_t(last), H, c, scale, accumulate, acc);
+  if (tail && !edge.whole[w]) {
+    if (join(w, true)) sl.store(a.part + (2 * wd + 1) * H, acc);
+    else write(last);                              // `old` is still the row of `last`
   }
 }
 
-// The ids that reach past the workgroup's tokens they begin in: their partial rows
-// added up in order. A wave per kEmbedWindow tokens and slice; most have none.
-template <class G>
-__global__ __launch_bounds__(256) void k_embed_join(const uint32_t* __restrict__ skey, int64_t N,
-                                                    int64_t H, int64_t V, int64_t slices,
-                                                    float scale, int accumulate,
-                                                    G* __restrict__ dW,
-                                                    const float* __restrict__ part) {
-  constexpr int64_t win = kEmbedWindow;
+template <class T, class G, bool WEIGHT, bool ADD, int SW>
+__global__ __launch_bounds__(64 * kSumWaves) void k_embed_sum(SumArgs a) {
+  __shared__ SumEdges edge;
   const int lane = threadIdx.x & 63;
-  const int64_t u = int64_t(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t wd = u / slices, c = (u - wd * slices) * kSliceCols + lane * kLaneCols;
-  const int64_t i0 = wd * win, i1 = i0 + win;
-  if (i1 >= N) return;                             // the last window: nothing behind it
-  const uint32_t key = skey[i1 - 1];
-  if (key >= uint32_t(V) || skey[i1] != key) return;
-  if (skey[i0] == key && i0 > 0 && skey[i0 - 1] == key) return;   // it began earlier
-  float acc[8];
-  load_cols(part + (2 * wd + 1) * H, c, H, acc);
-  // the windows behind that begin with this id, their rows loaded eight at a time
-  const int64_t windows = (N + win - 1) / win;
+  const int64_t wd = blockIdx.x / a.slices, c0 = (blockIdx.x - wd * a.slices) * kSliceCols;
+  if (c0 + kSliceCols <= a.H)
+    sum_slice<T, G, WEIGHT, ADD, SW, true>(a, wd, Slice<true>{c0, a.H, lane}, edge);
+  else
+    sum_slice<T, G, WEIGHT, ADD, SW, false>(a, wd, Slice<false>{c0, a.H, lane}, edge);
+}
+
+// The ids that reach past the workgroup's tokens they begin in: their partial rows
+// added up in order. A wave per workgroup's tokens and slice; most have none.
+template <class G, bool ADD, bool FULL>
+__device__ __forceinline__ void join_slice(const SumArgs& a, int64_t win, int64_t wd,
+                                           const Slice<FULL>& sl) {
+  const int64_t H = a.H, i0 = wd * win, i1 = i0 + win;
+  const uint32_t none = uint32_t(a.V);
+  if (i1 >= a.N) return;                           // the last one: nothing behind it
+  const uint32_t key = a.skey[i1 - 1];
+  if (key >= none || a.skey[i1] != key) return;
+  if (a.skey[i0] == key && i0 > 0 && a.skey[i0 - 1] == key) return;   // it began earlier
+  G* row = static_cast<G*>(a.dW) + int64_t(key) * H;
+  float acc[8], old[8] = {};
+  sl.load(a.part + (2 * wd + 1) * H, acc);
+  if constexpr (ADD) sl.load(row, old);
+  // those behind that begin with this id, their rows loaded eight at a time
+  const int64_t windows = (a.N + win - 1) / win;
   bool more = true;
+#pragma unroll 1
   for (int64_t x = wd + 1; more; x += kInFlight) {
     float f[kInFlight][8];
     uint32_t first[kInFlight];
 #pragma unroll
     for (int r = 0; r < kInFlight; ++r) {
-      first[r] = uint32_t(V);
-      if (x + r < windows) {
-        first[r] = skey[(x + r) * win];
-        load_cols(part + 2 * (x + r) * H, c, H, f[r]);
-      }
+      const int64_t y = x + r < windows ? x + r : wd;
+      first[r] = x + r < windows ? a.skey[y * win] : none;
+      sl.load(a.part + 2 * y * H, f[r]);           // not added unless it is this id's
     }
 #pragma unroll
     for (int r = 0; r < kInFlight; ++r) {
@@ -516,27 +543,47 @@ __global__ __launch_bounds__(256) void k_embed_join(const uint32_t* __restrict__
       }
     }
   }
-  write_row(dW, int64_t(key), H, c, scale, accumulate, acc);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) acc[e] = ADD ? fmaf(acc[e], a.scale, old[e]) : acc[e] * a.scale;
+  sl.store(row, acc);
+}
+
+template <class G, bool ADD>
+__global__ __launch_bounds__(256) void k_embed_join(SumArgs a, int64_t win) {
+  const int lane = threadIdx.x & 63;
+  const int64_t u = int64_t(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t wd = u / a.slices, c0 = (u - wd * a.slices) * kSliceCols;
+  if (c0 + kSliceCols <= a.H) join_slice<G, ADD>(a, win, wd, Slice<true>{c0, a.H, lane});
+  else join_slice<G, ADD>(a, win, wd, Slice<false>{c0, a.H, lane});
 }
 
 template <class T, class G, bool WEIGHT = false>
 hipError_t sums(const EmbedGradArgs& a, const uint32_t* key, const uint32_t* pos,
                 const Launcher& L) {
-  const int64_t slices = (a.H + kSliceCols - 1) / kSliceCols;
-  const int64_t windows = (a.N + kEmbedWindow - 1) / kEmbedWindow;
-  G* dW = static_cast<G*>(a.dW);
-  L.pre(kEmbedGrad);
-  hipLaunchKernelGGL((k_embed_sum<T, G, WEIGHT>), dim3(unsigned(windows * slices)), dim3(64 * kSumWaves), 0,
-                     L.stream, key, pos, static_cast<const T*>(a.dout), a.ld_dout, a.N, a.H, a.V,
-                     slices, a.scale, a.accumulate, dW, a.part, a.weight);
-  L.post(kEmbedGrad);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || windows == 1) return e;
-  L.pre(kEmbedGrad);
-  hipLaunchKernelGGL(k_embed_join<G>, dim3(unsigned((windows * slices + 3) / 4)), dim3(256), 0,
-                     L.stream, key, a.N, a.H, a.V, slices, a.scale, a.accumulate, dW, a.part);
-  L.post(kEmbedGrad);
-  return hipGetLastError();
+  const int64_t slices = (a.H + kSliceCols - 1) / kSliceCols, win = embed_window(a.N);
+  const int64_t windows = (a.N + win - 1) / win;
+  const SumArgs s{key, pos, a.dout, a.weight, a.ld_dout, a.N, a.H, a.V, slices, a.scale, a.dW,
+                  a.part};
+  auto run = [&](auto add) {
+    constexpr bool ADD = decltype(add)::value;
+    const dim3 grid(unsigned(windows * slices)), block(64 * kSumWaves);
+    L.pre(kEmbedGrad);
+    if (win == kSumWaves * 8)
+      hipLaunchKernelGGL((k_embed_sum<T, G, WEIGHT, ADD, 8>), grid, block, 0, L.stream, s);
+    else
+      hipLaunchKernelGGL((k_embed_sum<T, G, WEIGHT, ADD, 32>), grid, block, 0, L.stream, s);
+    L.post(kEmbedGrad);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || windows == 1) return e;
+    L.pre(kEmbedGrad);
+    hipLaunchKernelGGL((k_embed_join<G, ADD>), dim3(unsigned((windows * slices + 3) / 4)),
+                       dim3(256), 0, L.stream, s, win);
+    L.post(kEmbedGrad);
+    return hipGetLastError();
+  };
+  if constexpr (!WEIGHT)
+    if (!a.accumulate) return run(std::false_type{});
+  return run(std::true_type{});
 }
 
 }  // namespace
@@ -624,7 +671,8 @@ hipError_t launch_embedding_backward(const EmbedGradArgs& a, const Launcher& L) 
   }
   if (e != hipSuccess) return e;
   if (a.weight) {
-    if (a.dtype != FLCE_BF16 || a.grad_dtype != FLCE_BF16) return hipErrorInvalidValue;
+    if (a.dtype != FLCE_BF16 || a.grad_dtype != FLCE_BF16 || !a.accumulate)
+      return hipErrorInvalidValue;
     return sums<Bf16Bits, Bf16Bits, true>(a, a.key[at], a.pos[at], L);
   }
   if (a.dtype == FLCE_F32) return sums<float, float>(a, a.key[at], a.pos[at], L);

@@ -640,7 +640,7 @@ __device__ __forceinline__ uint64_t max_u64(uint64_t a, uint64_t b) { return a >
 // read whole lines of every list; below 4096 tokens that leaves most CUs idle, and 4
 // tokens a workgroup are faster. With TAU_ONLY just the lists so far: the top_k keys,
 // and the top_k-th largest logit.
-constexpr int kAhead = 4;                          // loads in flight
+constexpr int kAhead = 8;                          // loads in flight
 
 template <int KM>
 struct TopKeys {
@@ -709,18 +709,37 @@ __global__ __launch_bounds__(JT * G) void k_lp_join(JoinArgs a) {
       for (int k = 0; k < KM; ++k)
         if (k < K) top.k[k] = a.first[k * a.in.ck + t];
     }
-    for (int64_t l = a.list0 + g; l < a.lists; l += kAhead * G) {
-      float head[kAhead];
+    if (TAU_ONLY || !a.first) {
+      // lists taken in rounds are sorted: they merge as they are
+      for (int64_t l = a.list0 + g; l < a.lists; l += G) {
+        const int64_t at = l * a.in.cl + t * a.in.ct;
+        TopKeys<KM> list;
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u)
-        head[u] = l + u * G < a.lists ? a.in.cv[(l + u * G) * a.in.cl + t * a.in.ct] : -INFINITY;
+        for (int k = 0; k < KM; ++k) {
+          const bool in = k < a.in.kc;
+          const float v = in ? a.in.cv[at + k * a.in.ck] : -INFINITY;
+          list.k[k] = rank_key(v, l * a.list_rows + (in ? a.in.ci[at + k * a.in.ck] : 0));
+        }
+        // nothing behind the first place without a candidate is one
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        const int64_t at = (l + u * G) * a.in.cl + t * a.in.ct;
-        float v = head[u];
-        for (int k = 0; v > -INFINITY;) {
-          top.insert(rank_key(v, (l + u * G) * a.list_rows + a.in.ci[at + k * a.in.ck]));
-          v = ++k < a.in.kc ? a.in.cv[at + k * a.in.ck] : -INFINITY;
+        for (int k = 1; k < KM; ++k) list.k[k] = list.k[k - 1] != 0 ? list.k[k] : 0;
+        if (l == a.list0 + g) top = list;
+        else top.merge([&](int k) { return list.k[k]; });
+      }
+    } else {
+      for (int64_t l = a.list0 + g; l < a.lists; l += kAhead * G) {
+        float head[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+          head[u] = l + u * G < a.lists ? a.in.cv[(l + u * G) * a.in.cl + t * a.in.ct] : -INFINITY;
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+          const int64_t at = (l + u * G) * a.in.cl + t * a.in.ct;
+          float v = head[u];
+          for (int k = 0; v > -INFINITY;) {
+            top.insert(rank_key(v, (l + u * G) * a.list_rows + a.in.ci[at + k * a.in.ck]));
+            v = ++k < a.in.kc ? a.in.cv[at + k * a.in.ck] : -INFINITY;
+          }
         }
       }
     }

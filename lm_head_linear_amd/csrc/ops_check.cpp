@@ -60,7 +60,7 @@ bool make_embed_plan(int64_t N, int64_t H, int64_t V, EmbedPlan* p) {
   if (N < 0 || H <= 0 || V <= 0) return false;
   if (N > kMaxRows || H > kMaxWidth || V > kMaxRows) return false;
   EmbedPlan q;
-  const int64_t windows = ceil_div(N, kEmbedWindow), blocks = ceil_div(N, kSortBlock);
+  const int64_t windows = ceil_div(N, embed_window(N)), blocks = ceil_div(N, kSortBlock);
   const size_t list = align256(size_t(N) * sizeof(uint32_t));
   const int lists = N <= kSortChunk ? 1 : 2;
   size_t off = 0;
@@ -260,7 +260,7 @@ int flce_embedding_backward_check_args(const int64_t* tokens, const void* dout, 
             wk = vec(workspace, int64_t(workspace_bytes), 1);
   if (clash({bw, bst, wk}, {bt, bd})) return FLCE_ERR_ARG;
   if (dtype == FLCE_F32 && grad_dtype == FLCE_BF16) return FLCE_ERR_UNSUPPORTED;
-  if (ceil_div(N, kEmbedWindow) * ceil_div(H, 512) > kMaxGrid)
+  if (ceil_div(N, embed_window(N)) * ceil_div(H, 512) > kMaxGrid)
     return FLCE_ERR_UNSUPPORTED;
   for (const Buf& b : {bt, bd, bw, bst})
     if (misaligned(b)) return FLCE_ERR_UNSUPPORTED;

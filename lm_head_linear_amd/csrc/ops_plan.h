@@ -56,8 +56,9 @@ inline int64_t norm_shares(int64_t N) { return N < kNormShares ? N : kNormShares
 constexpr int64_t kSortChunk = 1024;
 constexpr int64_t kSortMerge = 32768;
 constexpr int64_t kSortBlock = 8192;
-// Sorted tokens whose rows one workgroup adds up.
-constexpr int64_t kEmbedWindow = 256;
+// Sorted tokens whose rows one workgroup adds up: 32 a wave, or 8 where that leaves
+// most CUs idle (2048 x 1024 rows: 36 us with 32, 12 us with 8).
+inline int64_t embed_window(int64_t N) { return N <= 8192 ? 64 : 256; }
 
 struct EmbedArgs {
   const int64_t* tokens;

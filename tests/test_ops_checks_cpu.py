@@ -136,8 +136,8 @@ def test_embedding_workspace():
     size = m.flce_embedding_backward_workspace_size
     assert size(0, 8, 8) == 256 and size(1, 8, 0) == 0
     # keys and positions, twice beyond one chunk of 1024; two partial rows for each 256
-    # tokens
-    assert size(1024, 64, 100) == 2 * 1024 * 4 + 2 * 4 * 64 * 4
+    # tokens, or 64 up to 8192
+    assert size(1024, 64, 100) == 2 * 1024 * 4 + 2 * 16 * 64 * 4
     assert size(16384, 4096, 131072) == 4 * 16384 * 4 + 2 * 64 * 4096 * 4
     # 256 digit counts a block beyond what is merged at once
     assert size(1 << 15, 64, 100) == 4 * (1 << 15) * 4 + 2 * 128 * 64 * 4
