@@ -91,9 +91,11 @@ __device__ __forceinline__ int before_rows(int x, int g) {
 // LDS; each wave leaves candidates of its own 128 rows. A candidate has to exceed
 // tau, the token's kc-th largest logit among lower ids: an equal one with a higher
 // id could not be listed either. Few do, so the wave counts them and stores them in
-// any order. Without a tau yet, or with more of them than the list holds, a column's
-// kc largest are taken in rounds: the largest logit left, lowest row first, in the
-// four lanes that hold the column; a wave stops when none of its 16 columns has one.
+// any order. Without a tau yet, or with more of them than the list holds, it looks for
+// a bound that exactly kc exceed. Where that fails (equal logits at the bound) the
+// column's kc largest are taken in rounds: the largest logit left, lowest row first,
+// in the four lanes that hold the column; a wave stops when none of its 16 columns
+// has one.
 template <bool SOFTCAP, bool TOPK>
 struct EpiLp {
   const int64_t* labels;      // null: no given tokens
@@ -189,27 +191,64 @@ struct EpiLp {
       const float d = col_sum4((dq[0] + dq[1]) + (dq[2] + dq[3]));
       if (g == 0) to[col] = make_float4(m, s, d * kLn2, 0.f);
       if (!TOPK || live == 0) continue;              // rows past V have no list
-      const float th = tau ? tau_t[col] : -INFINITY;
+      float th = tau ? tau_t[col] : -INFINITY;
       const int64_t list = (vbase >> 7) * out.cl + t * out.ct;
-      int n = 0;
-      bool rounds = tau == nullptr;
-      // x rises with z: no x as large as that of tau, no logit above tau
-      if (tau && (SOFTCAP || __ballot(t < N && m >= th * warp.inv_t) != 0)) {
-        int own = 0;                                 // this lane's logits above tau
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) z[i][r] = in(i, r) ? z[i][r] : -INFINITY;
+      auto above = [&](float x) {                    // this lane's logits above x
+        int c = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) own += in(i, r) && z[i][r] > th ? 1 : 0;
-        own = t < N ? own : 0;
-        int at = before_rows(own, g);
+          for (int r = 0; r < 4; ++r) c += z[i][r] > x ? 1 : 0;
+        return c;
+      };
+      int n = 0, own = 0;
+      bool rounds = false;
+      // x rises with z: no x as large as that of tau, no logit above tau
+      if (!tau || SOFTCAP || __ballot(t < N && m >= th * warp.inv_t) != 0) {
+        own = above(th);
         n = rows_all(own, AddOp());
-        rounds = __ballot(n > out.kc) != 0;
-        if (!rounds && own > 0) {
+        bool fits = n <= out.kc || t >= N;
+        rounds = __ballot(!fits) != 0;
+        if (rounds && out.kc > 8) {
+          // a bound that exactly kc logits exceed, by bisection between the column's
+          // smallest and largest: about a dozen counts, cheaper than more than 8
+          // rounds (20 of them 156 us a launch of 62 tiles, this 110 us; 5 of them 69,
+          // this 87)
+          float lo = INFINITY, hi = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              hi = fmaxf(hi, z[i][r]);
+              lo = fminf(lo, z[i][r] > th ? z[i][r] : INFINITY);
+            }
+          hi = col_max4(hi);
+          lo = -col_max4(-lo);
+          float part = 0.8f;                         // kc of 128 lie high in the range
+#pragma unroll 1
+          for (int it = 0; it < 16 && __ballot(!fits) != 0; ++it) {
+            const float mid = fmaf(part, hi - lo, lo);
+            part = 0.5f;
+            const int c = above(mid), total = rows_all(c, AddOp());
+            if (!fits) {
+              if (total == out.kc) { fits = true; th = mid; own = c; n = total; }
+              else if (total > out.kc) lo = mid;
+              else hi = mid;
+            }
+          }
+          rounds = __ballot(!fits) != 0;
+        }
+        int at = before_rows(own, g);
+        if (!rounds && t < N && own > 0) {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-              if (in(i, r) && z[i][r] > th) {
+              if (z[i][r] > th) {
                 out.cv[list + at * out.ck] = z[i][r];
                 out.ci[list + at * out.ck] = uint8_t(i * 16 + 4 * g + r);
                 ++at;
@@ -217,10 +256,7 @@ struct EpiLp {
         }
       }
       if (rounds) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) z[i][r] = in(i, r) ? z[i][r] : -INFINITY;
+        th = tau ? tau_t[col] : -INFINITY;
 #pragma unroll 1
         for (n = 0; n < out.kc; ++n) {
           float bq[4];
@@ -633,27 +669,32 @@ __device__ __forceinline__ float key_value(uint64_t k) {
 __device__ __forceinline__ int64_t key_id(uint64_t k) { return int64_t(uint32_t(~uint32_t(k))); }
 __device__ __forceinline__ uint64_t max_u64(uint64_t a, uint64_t b) { return a > b ? a : b; }
 
-// Many tokens: JT tokens a workgroup and G threads for each, thread g taking every
-// G-th part and list, then the threads pairwise. A thread keeps its KM largest keys
-// sorted in registers; two threads' lists meet as a bitonic sequence, through LDS,
-// which bounds the threads (64 KiB at 16 keys of 1024, or 32 keys of 512). 32 tokens
-// read whole lines of every list; below 4096 tokens that leaves most CUs idle, and 4
-// tokens a workgroup are faster. With TAU_ONLY just the lists so far: the top_k keys,
-// and the top_k-th largest logit.
-constexpr int kAhead = 8;                          // loads in flight
+// Many tokens, lists of tiles without a tau: JT tokens a workgroup and G threads for
+// each, thread g taking every G-th part and list, then the threads pairwise. A thread
+// keeps its KM largest keys sorted in registers; two threads' lists meet as a bitonic
+// sequence, through LDS, which bounds the threads (64 KiB at 16 keys of 1024, or 32
+// keys of 512). 32 tokens read whole lines of every list; below 4096 tokens that
+// leaves most CUs idle, and 16 (below 1024: 4) tokens a workgroup are faster. With
+// TAU_ONLY just the lists so far: the top_k keys, and the top_k-th largest logit.
+constexpr int kAhead = 4;                          // loads in flight
 
 template <int KM>
 struct TopKeys {
   uint64_t k[KM];
-  __device__ __forceinline__ void insert(uint64_t x) {
-    if (x <= k[KM - 1]) return;
+  __device__ __forceinline__ void exchange(int i, int o, bool down) {
+    const bool swap = down ? k[o] > k[i] : k[i] > k[o];
+    const uint64_t x = k[i];
+    k[i] = swap ? k[o] : x;
+    k[o] = swap ? x : k[o];
+  }
+  __device__ __forceinline__ void sort() {         // bitonic, largest first
 #pragma unroll
-    for (int i = 0; i < KM; ++i) {
-      const bool up = x > k[i];
-      const uint64_t o = k[i];
-      k[i] = up ? x : o;
-      x = up ? o : x;
-    }
+    for (int size = 2; size <= KM; size <<= 1)
+#pragma unroll
+      for (int h = size / 2; h > 0; h >>= 1)
+#pragma unroll
+        for (int i = 0; i < KM; ++i)
+          if (!(i & h)) exchange(i, i + h, (i & size) == 0);
   }
   // with another sorted list, b(i) its i-th key
   template <class Get>
@@ -664,12 +705,7 @@ struct TopKeys {
     for (int h = KM / 2; h > 0; h >>= 1)
 #pragma unroll
       for (int i = 0; i < KM; ++i)
-        if (!(i & h)) {
-          const bool up = k[i + h] > k[i];
-          const uint64_t o = k[i];
-          k[i] = up ? k[i + h] : o;
-          k[i + h] = up ? o : k[i + h];
-        }
+        if (!(i & h)) exchange(i, i + h, true);
   }
 };
 
@@ -704,44 +740,21 @@ __global__ __launch_bounds__(JT * G) void k_lp_join(JoinArgs a) {
 #pragma unroll
   for (int k = 0; k < KM; ++k) top.k[k] = 0;
   if (K > 0 && live) {
-    if (!TAU_ONLY && a.first && g == 0) {          // the top_k of the lists before list0
+    for (int64_t l = a.list0 + g; l < a.lists; l += G) {
+      const int64_t at = l * a.in.cl + t * a.in.ct;
+      TopKeys<KM> list;
 #pragma unroll
-      for (int k = 0; k < KM; ++k)
-        if (k < K) top.k[k] = a.first[k * a.in.ck + t];
-    }
-    if (TAU_ONLY || !a.first) {
-      // lists taken in rounds are sorted: they merge as they are
-      for (int64_t l = a.list0 + g; l < a.lists; l += G) {
-        const int64_t at = l * a.in.cl + t * a.in.ct;
-        TopKeys<KM> list;
-#pragma unroll
-        for (int k = 0; k < KM; ++k) {
-          const bool in = k < a.in.kc;
-          const float v = in ? a.in.cv[at + k * a.in.ck] : -INFINITY;
-          list.k[k] = rank_key(v, l * a.list_rows + (in ? a.in.ci[at + k * a.in.ck] : 0));
-        }
-        // nothing behind the first place without a candidate is one
-#pragma unroll
-        for (int k = 1; k < KM; ++k) list.k[k] = list.k[k - 1] != 0 ? list.k[k] : 0;
-        if (l == a.list0 + g) top = list;
-        else top.merge([&](int k) { return list.k[k]; });
+      for (int k = 0; k < KM; ++k) {
+        const bool in = k < a.in.kc;
+        const float v = in ? a.in.cv[at + k * a.in.ck] : -INFINITY;
+        list.k[k] = rank_key(v, l * a.list_rows + (in ? a.in.ci[at + k * a.in.ck] : 0));
       }
-    } else {
-      for (int64_t l = a.list0 + g; l < a.lists; l += kAhead * G) {
-        float head[kAhead];
+      // nothing behind the first place without a candidate is one
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u)
-          head[u] = l + u * G < a.lists ? a.in.cv[(l + u * G) * a.in.cl + t * a.in.ct] : -INFINITY;
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-          const int64_t at = (l + u * G) * a.in.cl + t * a.in.ct;
-          float v = head[u];
-          for (int k = 0; v > -INFINITY;) {
-            top.insert(rank_key(v, (l + u * G) * a.list_rows + a.in.ci[at + k * a.in.ck]));
-            v = ++k < a.in.kc ? a.in.cv[at + k * a.in.ck] : -INFINITY;
-          }
-        }
-      }
+      for (int k = 1; k < KM; ++k) list.k[k] = list.k[k - 1] != 0 ? list.k[k] : 0;
+      list.sort();
+      if (l == a.list0 + g) top = list;
+      else top.merge([&](int k) { return list.k[k]; });
     }
   }
   for (int half = G / 2; half > 0; half >>= 1) {
@@ -783,6 +796,142 @@ __global__ __launch_bounds__(JT * G) void k_lp_join(JoinArgs a) {
       write_alternative(a, o, k, has ? warp_logit<SOFTCAP>(a.warp, key_value(top.k[k])) : 0.f,
                         has ? key_id(top.k[k]) : -1, M, ls);
     }
+}
+
+// Many tokens, lists of tiles with a tau, few of which hold anything: 16 tokens a
+// workgroup, 32 threads for each. Every candidate goes to a list in LDS, with the
+// top_k of the tiles before. Of its keys those from a bound up are kept, the top_k-th
+// largest of the 32 threads' largest, and each counts the larger ones. A list that
+// overflows is filled again with just the keys from its own top_k-th on: that key
+// rises every time.
+constexpr int kSparseTokens = 16, kSparseG = 32, kSparseKeys = 512;
+
+template <bool SOFTCAP>
+__global__ __launch_bounds__(512) void k_lp_join_sparse(JoinArgs a) {
+  constexpr int JT = kSparseTokens, G = kSparseG, CAP = kSparseKeys;
+  __shared__ uint64_t list[JT][CAP];
+  __shared__ uint64_t best[JT][G + 1], won[JT][kLpTop + 1], bound[JT], floor_key[JT];
+  __shared__ float4 grp[G / 2 * JT];
+  __shared__ int count[JT], kept[JT];
+  const int tid = threadIdx.x, tk = tid % JT, g = tid / JT;
+  const int64_t t = int64_t(blockIdx.x) * JT + tk;
+  int64_t n_live = a.N;
+  if (a.count) { const int64_t c = *a.count; n_live = c < n_live ? c : n_live; }
+  const bool live = t < n_live;
+  const int K = a.top_k;
+  float M = -INFINITY, S = 0.f, D = 0.f;
+  if (live) {
+    for (int64_t p = g; p < a.parts; p += kAhead * G) {
+      float2 ms[kAhead];
+      float d[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int64_t at = (p + u * G < a.parts ? p + u * G : p) * a.in.sp + t * a.in.st;
+        ms[u] = a.in.part[at];
+        d[u] = a.in.pd[at];
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+        if (p + u * G < a.parts) join_part(M, S, D, ms[u].x, ms[u].y, d[u]);
+    }
+  }
+  if (g == 0) floor_key[tk] = 1;
+  bool again = true;
+  while (again) {
+    if (g == 0) { count[tk] = 0; kept[tk] = 0; bound[tk] = 1; }
+    won[tk][g] = 0;
+    __syncthreads();
+    const uint64_t least = floor_key[tk];
+    auto push = [&](uint64_t key) {
+      if (key < least) return;
+      const int at = atomicAdd(&count[tk], 1);     // any order: the keys are ranked
+      if (at < CAP) list[tk][at] = key;
+    };
+    if (live) {
+      if (g < K) push(a.first[g * a.in.ck + t]);
+      for (int64_t l = a.list0 + g; l < a.lists; l += 4 * G) {
+        float v[4][2];
+        uint8_t row[4][2];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {              // the first two of four lists at a time
+          const int64_t at = (l + u * G < a.lists ? l + u * G : l) * a.in.cl + t * a.in.ct;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int64_t i = at + (k < a.in.kc ? k : 0) * a.in.ck;
+            v[u][k] = a.in.cv[i];
+            row[u][k] = a.in.ci[i];
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          if (l + u * G >= a.lists || !(v[u][0] > -INFINITY)) continue;
+          const int64_t at = (l + u * G) * a.in.cl + t * a.in.ct, v0 = (l + u * G) * a.list_rows;
+          push(rank_key(v[u][0], v0 + row[u][0]));
+          if (a.in.kc < 2 || !(v[u][1] > -INFINITY)) continue;
+          push(rank_key(v[u][1], v0 + row[u][1]));
+          for (int k = 2; k < a.in.kc; ++k) {
+            const float x = a.in.cv[at + k * a.in.ck];
+            if (!(x > -INFINITY)) break;
+            push(rank_key(x, v0 + a.in.ci[at + k * a.in.ck]));
+          }
+        }
+      }
+    }
+    __syncthreads();
+    const int n = count[tk] < CAP ? count[tk] : CAP;
+    uint64_t mine = 0;
+    for (int i = g; i < n; i += G) mine = max_u64(mine, list[tk][i]);
+    best[tk][g] = mine;
+    __syncthreads();
+    int above = 0;
+    for (int i = 0; i < G; ++i) above += best[tk][i] > mine ? 1 : 0;
+    if (mine != 0 && above == K - 1) bound[tk] = mine;
+    __syncthreads();
+    const uint64_t from = bound[tk];
+    uint64_t hold[CAP / G];                        // this thread's keys from the bound up
+#pragma unroll
+    for (int u = 0; u < CAP / G; ++u) {
+      const int i = u * G + g;
+      hold[u] = i < n && list[tk][i] >= from ? list[tk][i] : 0;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < CAP / G; ++u)
+      if (hold[u] != 0) list[tk][atomicAdd(&kept[tk], 1)] = hold[u];
+    __syncthreads();
+    const int m = kept[tk];
+    for (int i = g; i < m; i += G) {
+      const uint64_t k = list[tk][i];
+      int larger = 0;
+      for (int o = 0; o < m && larger < K; ++o) larger += list[tk][o] > k ? 1 : 0;
+      if (larger < K) won[tk][larger] = k;
+    }
+    again = __syncthreads_or(count[tk] > CAP);
+    if (g == 0 && count[tk] > CAP) floor_key[tk] = won[tk][K - 1];
+  }
+  for (int half = G / 2; half > 0; half >>= 1) {
+    const int slot = tid % (half * JT);
+    if (g >= half && g < 2 * half) grp[slot] = make_float4(M, S, D, 0.f);
+    __syncthreads();
+    if (g < half) {
+      const float4 f = grp[slot];
+      join_part(M, S, D, f.x, f.y, f.z);
+    }
+    __syncthreads();
+  }
+  if (g == 0) grp[tk] = make_float4(M, S, D, 0.f);
+  __syncthreads();
+  if (t >= a.N) return;
+  const float4 f = grp[tk];
+  const int64_t o = a.idx ? int64_t(a.idx[t]) : t;
+  const bool shown = live && (!a.labels || a.labels[t] != a.ignore_index);
+  if (g == 0) write_token(a, t, o, shown, f.x, f.y, f.z);
+  if (g < K) {
+    const uint64_t k = won[tk][g];
+    const bool has = shown && k != 0;
+    write_alternative(a, o, g, has ? warp_logit<SOFTCAP>(a.warp, key_value(k)) : 0.f,
+                      has ? key_id(k) : -1, f.x, logf(f.y));
+  }
 }
 
 // A workgroup joins one token of 64-row tiles. The top_k of any grouped keys lie in
@@ -1168,6 +1317,9 @@ hipError_t run_join(const LpPlan& q, const JoinArgs& j, const Launcher& L) {
   if (!q.tiles) {
     hipLaunchKernelGGL(k_lp_join_few<SOFTCAP>, dim3(unsigned(j.N)), dim3(kFewThreads), 0,
                        L.stream, j);
+  } else if (!TAU_ONLY && j.first) {
+    hipLaunchKernelGGL(k_lp_join_sparse<SOFTCAP>, dim3(cdiv(j.N, kSparseTokens)), dim3(512), 0,
+                       L.stream, j);
   } else {
     auto run = [&](auto jt, auto threads, auto km) {
       constexpr int JT = decltype(jt)::value, T = decltype(threads)::value;
@@ -1180,7 +1332,9 @@ hipError_t run_join(const LpPlan& q, const JoinArgs& j, const Launcher& L) {
       else if (j.top_k <= 16) run(jt, Int<1024>{}, Int<16>{});
       else run(jt, Int<512>{}, Int<kLpTop>{});
     };
-    j.N >= 4096 ? by_k(Int<32>{}) : by_k(Int<4>{});
+    if (j.N >= 4096) by_k(Int<32>{});
+    else if (j.N >= 1024) by_k(Int<16>{});
+    else by_k(Int<4>{});
   }
   L.post(kLpJoin);
   return hipGetLastError();

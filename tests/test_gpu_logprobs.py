@@ -148,6 +148,27 @@ def test_ties_go_to_the_lowest_id(N, H, V, dt, K):
     assert r.top_ids[3].tolist() == list(range(K))
 
 
+@pytest.mark.parametrize("K", [1, 5, 9, 32])
+@pytest.mark.parametrize("order", ["rising", "falling", "flat"])
+def test_alternatives_wherever_they_are(K, order):
+    """A vocabulary large enough that its first tiles bound the rest: logits that rise
+    with the id (the bound holds nothing back and every list is full), that fall (the
+    rest is empty), and that do neither."""
+    import lm_head_linear_amd as m
+    N, H, V = 300, 64, 70000
+    h, W, y, _, _ = make(N, H, V, BF, seed=3)
+    step = (torch.arange(V, device="cuda") // 512).float() * 2.0 ** -3
+    W[:, 0] = (step if order == "rising" else -step if order == "falling" else 0 * step).to(BF)
+    h[:, 0] = 1
+    r = m.flce_logprobs(h, W, y, top_k=K)
+    ref = reference(h, W, y, K, 0.0, 1.0)
+    assert torch.equal(r.top_ids, ref["top_ids"])
+    live = ref["live"]
+    assert float((r.top_logp[live].double() - ref["top_logp"][live]).abs().max()) < 1e-4
+    again = m.flce_logprobs(h, W, y, top_k=K)
+    assert all(torch.equal(a, b) for a, b in zip(r, again))
+
+
 @pytest.mark.parametrize("N", [5, 130])
 @pytest.mark.parametrize("dt", [BF, F])
 def test_infinite_and_nan_rows(N, dt):
