@@ -7,6 +7,7 @@
 
 #include "../../include/flce.h"
 #include "flce_internal.h"
+#include "row_io.h"
 
 namespace flce {
 namespace {
@@ -395,15 +396,26 @@ __global__ __launch_bounds__(256) void k_gather_rows_pad(const uint16_t* __restr
 }
 
 // Row copy between widths: row r of dst (stride ld_dst) gets the first `cols`
-// elements of row r of src (stride ld_src) and zeros up to `width`.
+// elements of row r of src (stride ld_src) and zeros up to `width`. 16 bytes a
+// thread, at any element alignment: element by element the copies of an odd bf16
+// width ran at a third of the rate (8251 x 2988: 31 us).
 template <class T>
 __global__ __launch_bounds__(256) void k_copy_rows(const T* __restrict__ src, int64_t ld_src,
                                                    T* __restrict__ dst, int64_t ld_dst,
                                                    int64_t rows, int64_t cols, int64_t width) {
-  for (int64_t r = blockIdx.y; r < rows; r += gridDim.y)
-    for (int64_t c = int64_t(blockIdx.x) * 256 + threadIdx.x; c < width;
-         c += int64_t(gridDim.x) * 256)
-      dst[r * ld_dst + c] = c < cols ? src[r * ld_src + c] : T(0);
+  constexpr int E = 16 / int(sizeof(T));
+  for (int64_t r = int64_t(blockIdx.y) * blockDim.y + threadIdx.y; r < rows;
+       r += int64_t(gridDim.y) * blockDim.y)
+    for (int64_t c = (int64_t(blockIdx.x) * blockDim.x + threadIdx.x) * E; c < width;
+         c += int64_t(gridDim.x) * blockDim.x * E) {
+      const T* s = src + r * ld_src + c;
+      T* d = dst + r * ld_dst + c;
+      if (c + E <= cols) {
+        *reinterpret_cast<row_u32x4_any*>(d) = load_raw(s);
+      } else {
+        for (int e = 0; e < E && c + e < width; ++e) d[e] = c + e < cols ? s[e] : T(0);
+      }
+    }
 }
 
 // Live tokens of each chunk of nc gathered rows: cnt[c] for the forward (the
@@ -497,15 +509,20 @@ hipError_t launch_copy_rows(const void* src, int64_t ld_src, void* dst, int64_t 
                             const Launcher& L) {
   if (rows <= 0 || width <= 0) return hipSuccess;
   if (elem != 2 && elem != 4) return hipErrorInvalidValue;
-  const int64_t gx = (width + 255) / 256;
-  const dim3 grid(unsigned(gx < 64 ? gx : 64), unsigned(rows < 16384 ? rows : 16384));
+  // narrow rows: several of them in a workgroup
+  unsigned tx = 256;
+  while (tx > 16 && int64_t(tx / 2) * 16 >= width * int64_t(elem)) tx /= 2;
+  const dim3 block(tx, 256 / tx);
+  const int64_t gx = (width * int64_t(elem) + 16 * tx - 1) / (16 * tx);
+  const int64_t gy = (rows + block.y - 1) / block.y;
+  const dim3 grid(unsigned(gx < 64 ? gx : 64), unsigned(gy < 16384 ? gy : 16384));
   L.pre(kPadCopy);
   if (elem == 2)
-    hipLaunchKernelGGL(k_copy_rows<uint16_t>, grid, dim3(256), 0, L.stream,
+    hipLaunchKernelGGL(k_copy_rows<uint16_t>, grid, block, 0, L.stream,
                        static_cast<const uint16_t*>(src), ld_src, static_cast<uint16_t*>(dst),
                        ld_dst, rows, cols, width);
   else
-    hipLaunchKernelGGL(k_copy_rows<uint32_t>, grid, dim3(256), 0, L.stream,
+    hipLaunchKernelGGL(k_copy_rows<uint32_t>, grid, block, 0, L.stream,
                        static_cast<const uint32_t*>(src), ld_src, static_cast<uint32_t*>(dst),
                        ld_dst, rows, cols, width);
   L.post(kPadCopy);
