@@ -428,19 +428,22 @@ __device__ __forceinline__ bf16x8 load_k8_end(const uint16_t* row, int64_t k, in
   return __builtin_bit_cast(bf16x8, v);
 }
 
-template <int NT, bool SOFTCAP, int ALIGN>
-__global__ __launch_bounds__(256) void k_lp_few(const uint16_t* __restrict__ h,
-                                                const uint16_t* __restrict__ W,
-                                                const int64_t* __restrict__ labels, int64_t N,
-                                                int64_t H, int64_t V, Warp warp, LpOut out) {
-  constexpr int kT = 16 * NT, kAheadK = NT == 8 ? 1 : NT >= 3 ? 2 : 3, R = kAheadK + 1, LD = 68;
-  union Smem {
-    uint16_t h[2][kT][kHld];
-    float z[kT][LD];
-  };
-  __shared__ __attribute__((aligned(16))) Smem sm;
+template <int NT>
+union FewSmem {
+  uint16_t h[2][16 * NT][kHld];
+  float z[16 * NT][68];
+};
+// Lanes of a token in the epilogues of such a tile (48 tokens: whole waves idle).
+template <int NT>
+constexpr int kFewLanes = NT == 3 ? 4 : 256 / (16 * NT);
+
+// The tile's logits in sm.z: 64 rows from v0 of the V rows of W, tokens 0 .. N - 1 of h.
+template <int NT, int ALIGN>
+__device__ __forceinline__ void few_logits(const uint16_t* __restrict__ h,
+                                           const uint16_t* __restrict__ W, int64_t N, int64_t H,
+                                           int64_t V, int64_t v0, FewSmem<NT>& sm) {
+  constexpr int kAheadK = NT == 8 ? 1 : NT >= 3 ? 2 : 3, R = kAheadK + 1;
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-  const int64_t v0 = int64_t(blockIdx.x) * 64;
   const int r = lane & 15, kg = (lane >> 4) * 8;
   const int64_t v = v0 + w * 16 + r < V ? v0 + w * 16 + r : V - 1;
   const uint16_t* wrow = W + v * H;
@@ -506,9 +509,19 @@ __global__ __launch_bounds__(256) void k_lp_few(const uint16_t* __restrict__ h,
   for (int j = 0; j < NT; ++j)
     *reinterpret_cast<f32x4*>(&sm.z[16 * j + r][16 * w + (lane >> 4) * 4]) = acc[j];
   __syncthreads();
-  constexpr int TPT = NT == 3 ? 4 : 256 / kT, E = 64 / TPT;
-  const int t = tid / TPT, q = tid % TPT;
-  if (t >= kT) return;                             // NT = 3: whole waves
+}
+
+template <int NT, bool SOFTCAP, int ALIGN>
+__global__ __launch_bounds__(256) void k_lp_few(const uint16_t* __restrict__ h,
+                                                const uint16_t* __restrict__ W,
+                                                const int64_t* __restrict__ labels, int64_t N,
+                                                int64_t H, int64_t V, Warp warp, LpOut out) {
+  __shared__ __attribute__((aligned(16))) FewSmem<NT> sm;
+  const int64_t v0 = int64_t(blockIdx.x) * 64;
+  few_logits<NT, ALIGN>(h, W, N, H, V, v0, sm);
+  constexpr int TPT = kFewLanes<NT>, E = 64 / TPT;
+  const int t = threadIdx.x / TPT, q = threadIdx.x % TPT;
+  if (t >= 16 * NT) return;
   float z[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) z[e] = sm.z[t][q * E + e];
@@ -1174,6 +1187,59 @@ struct EpiLpGrad {
   }
 };
 
+// Few live tokens: the same G from the few-token kernel's logits. The coefficients
+// come straight from the call's arrays.
+struct FewGrad {
+  const int32_t* idx;
+  const int64_t* labels;      // gathered, as h is
+  const int64_t* count;
+  const float* lse;
+  const float* ent;
+  const float* ga;
+  const float* gb;
+  float* rest;
+  uint16_t* g;
+  int64_t V, v0, gblk;        // v0: the chunk's first vocabulary row
+};
+
+template <int NT, bool SOFTCAP>
+__global__ __launch_bounds__(256) void k_lp_few_grad(const uint16_t* __restrict__ h,
+                                                     const uint16_t* __restrict__ W, int64_t N,
+                                                     int64_t H, int64_t vcur, Warp warp,
+                                                     FewGrad a) {
+  __shared__ __attribute__((aligned(16))) FewSmem<NT> sm;
+  const int64_t c0 = int64_t(blockIdx.x) * 64;     // the chunk's column
+  few_logits<NT, 16>(h, W, N, H, vcur, c0, sm);
+  constexpr int TPT = kFewLanes<NT>, E = 64 / TPT;
+  const int t = threadIdx.x / TPT, q = threadIdx.x % TPT;
+  const int64_t live = *a.count;
+  if (t >= live || t >= N) return;
+  const int64_t o = a.idx[t], y = a.labels[t], at = c0 + q * E;
+  const float ca = (y < 0 || y >= a.V) ? NAN : a.ga ? a.ga[o] : 0.f;
+  const float cb = a.gb ? a.gb[o] : 0.f, l0 = a.lse[o];
+  const float k0 = -(ca + cb * (a.gb ? a.ent[o] : 0.f));
+  float g[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const float z = sm.z[t][q * E + e], l = warp_logit<SOFTCAP>(warp, z) - l0;
+    float x = __builtin_amdgcn_exp2f(l * kLog2e) * fmaf(-cb, l, k0);
+    const bool target = y == a.v0 + at + e && at + e < vcur;
+    x = (target ? x + ca : x) * warp_slope<SOFTCAP>(warp, z);
+    if (target) a.rest[t] = x - bf16_to_f32(f32_to_bf16(x));
+    g[e] = at + e < vcur ? x : 0.f;
+  }
+  // 4 (or 8) adjacent columns lie in one block of 32; dH reads whole runs of 8, so the
+  // zeros behind the last row are stored too
+  constexpr int RUN = E < 8 ? E : 8;
+#pragma unroll
+  for (int e = 0; e < E; e += RUN) {
+    if (at + e >= (vcur + 7) / 8 * 8) break;
+    uint32_t* to = reinterpret_cast<uint32_t*>(a.g + gemm::blocked_offset(t, at + e, a.gblk));
+#pragma unroll
+    for (int i = 0; i < RUN; i += 2) to[i / 2] = pack_bf16x2(g[e + i], g[e + i + 1]);
+  }
+}
+
 // float32: G^T[v - v0][t] of one vocabulary chunk, zero for ignored tokens and for
 // the columns N <= t < ldg.
 template <bool SOFTCAP>
@@ -1524,6 +1590,7 @@ hipError_t launch_lp_f32_products(const Plan& p, const Args& a, int64_t chunk, c
 
 hipError_t launch_lp_coefficients(const Plan& p, const Args& a, const LpGradArgs& g,
                                   const Launcher& L) {
+  if (lp_few_backward(p)) return hipSuccess;       // formed where they are used
   L.pre(kLpJoin);
   hipLaunchKernelGGL(k_lp_coef, dim3(cdiv(p.N, 256)), dim3(256), 0, L.stream,
                      p.compact ? a.idx : nullptr, p.compact ? a.yc : a.labels,
@@ -1551,6 +1618,28 @@ hipError_t launch_lp_gradient(const Plan& p, const Args& a, const LpGradArgs& g,
     return hipGetLastError();
   }
   if (!p.compact) return hipErrorInvalidValue;
+  if (lp_few_backward(p)) {
+    const FewGrad f{a.idx, a.yc, &a.sc->n_valid, g.lse, g.entropy, g.grad_logp, g.grad_entropy,
+                    g.rest, static_cast<uint16_t*>(a.g), p.V, v0, gemm::g_block(p)};
+    auto go = [&](auto nt) {
+      constexpr int NT = decltype(nt)::value;
+      const auto* h = static_cast<const uint16_t*>(a.hc);
+      const auto* W = static_cast<const uint16_t*>(a.W) + v0 * p.H;
+      if (a.softcap > 0.f)
+        hipLaunchKernelGGL((k_lp_few_grad<NT, true>), dim3(cdiv(vcur, 64)), dim3(256), 0, L.stream,
+                           h, W, p.N, p.H, vcur, warp, f);
+      else
+        hipLaunchKernelGGL((k_lp_few_grad<NT, false>), dim3(cdiv(vcur, 64)), dim3(256), 0,
+                           L.stream, h, W, p.N, p.H, vcur, warp, f);
+    };
+    L.pre(kGradLogits);
+    if (p.N <= 16) go(Int<1>{});
+    else if (p.N <= 32) go(Int<2>{});
+    else if (p.N <= 64) go(Int<4>{});
+    else go(Int<8>{});
+    L.post(kGradLogits);
+    return hipGetLastError();
+  }
   constexpr int NF = gemm::kFormN;
   const gemm::Launch l = gemm::backward_launch(p, chunk, 0);
   auto run = [&](auto cap, auto split) {

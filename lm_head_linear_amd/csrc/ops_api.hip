@@ -133,7 +133,7 @@ int flce_logprobs_backward(const void* h, const void* W, const int64_t* tokens, 
   Range r("flce_logprobs_backward");
   const Launcher L = flce::make_launcher(stream);
   flce::Plan p;
-  if (!flce::make_plan(N, H, V, dtype, &p, true, grad_dtype)) return FLCE_ERR_ARG;
+  if (!flce::make_lp_backward_plan(N, H, V, dtype, grad_dtype, &p)) return FLCE_ERR_ARG;
   hipError_t e = hipSuccess;
   if (N == 0) {
     if (!accumulate_dW) e = flce::launch_zero_bytes(dW, size_t(V) * H * p.grad_elem, L);

@@ -8,6 +8,9 @@
 #include "../../include/flce.h"
 
 namespace flce {
+
+static_assert(kBF16 == FLCE_BF16, "the header's type code");
+
 namespace {
 
 constexpr int64_t kMaxRows = int64_t(1) << 31, kMaxWidth = int64_t(1) << 24;
@@ -315,7 +318,7 @@ int flce_logprobs_check_args(const void* h, const void* W, const int64_t* tokens
 size_t flce_logprobs_backward_workspace_size(int64_t N, int64_t H, int64_t V, int dtype,
                                              int grad_dtype) {
   Plan p;
-  if (!make_plan(N, H, V, dtype, &p, true, grad_dtype)) return 0;
+  if (!make_lp_backward_plan(N, H, V, dtype, grad_dtype, &p)) return 0;
   // the head's backward, its dummy count, the token coefficients, and the partial
   // products of a split float32 dH, or the lookup gradient that adds what rounding G
   // to bf16 left of the given tokens

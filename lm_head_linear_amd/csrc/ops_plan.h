@@ -10,6 +10,8 @@
 
 namespace flce {
 
+constexpr int kBF16 = 1;      // FLCE_BF16
+
 // ---- root-mean-square norm ---------------------------------------------------------
 struct NormArgs {
   const void* x;
@@ -148,6 +150,29 @@ inline int64_t lp_first_tiles(const LpPlan& q, int64_t nt) {
   int64_t pre = (tv + 15) / 16;
   if (pre * tt < 256) pre = (256 + tt - 1) / tt;
   return 2 * pre <= tv ? pre : 0;
+}
+
+// The plan of the backward: the head's, with more K segments of dH for few tokens.
+// One 256-row tile of tokens makes ceil(H / 256) dH tiles with a K of the whole chunk:
+// the head's four segments leave each a long loop on an idle chip (3 rows, 43742 x 178:
+// 182 us against 20). False for invalid sizes.
+inline bool make_lp_backward_plan(int64_t N, int64_t H, int64_t V, int dtype, int grad_dtype,
+                                  Plan* p) {
+  if (!make_plan(N, H, V, dtype, p, true, grad_dtype)) return false;
+  if (p->dtype != kBF16 || p->g_parts != 1 || N <= 0 || N > kTileBF16) return true;
+  const int64_t tiles = (p->H + kTileBF16 - 1) / kTileBF16;
+  int64_t segs = 256 / tiles < 32 ? 256 / tiles : 32;
+  if (segs > p->vchunk / 512) segs = p->vchunk / 512;
+  if (segs <= p->dh_segs) return true;
+  p->dh_kseg = ((p->vchunk + segs - 1) / segs + 63) / 64 * 64;
+  p->dh_segs = (p->vchunk + p->dh_kseg - 1) / p->dh_kseg;
+  p->off_dhpart = p->total;                        // behind the head's own buffers
+  p->total = (p->total + size_t(p->dh_segs) * size_t(N) * p->H * sizeof(float) + 255) & ~size_t(255);
+  return true;
+}
+// Whether G comes from the few-token kernel (bf16 G; the gathered rows are aligned).
+inline bool lp_few_backward(const Plan& p) {
+  return p.dtype == kBF16 && p.g_parts == 1 && p.N <= kFewTokens;
 }
 
 // Segment of the float32 dH product's K (vocabulary rows of a chunk): its

@@ -238,7 +238,8 @@ def test_every_row_ignored_and_none(N):
     assert not bool(dW.any())
 
 
-BACKWARD = [(1, 64, 300, BF), (40, 128, 1000, BF), (300, 136, 2000, BF), (700, 133, 1500, BF),
+BACKWARD = [(1, 64, 300, BF), (17, 200, 3000, BF), (40, 128, 1000, BF), (128, 133, 700, BF),
+            (129, 264, 1100, BF), (300, 136, 2000, BF), (700, 133, 1500, BF),
             (1, 33, 300, F), (70, 130, 515, F), (300, 64, 1000, F)]
 
 
@@ -293,6 +294,24 @@ def test_a_row_whose_terms_cancel(H, accumulate, monkeypatch):
     ref = reference(h, W, y, 0, 0.0, 1.0, a, None)["dW"][700]
     err = (dW[700].double() - ref).norm() / ref.norm()
     assert float(err) < 2.0 ** -6, float(err)
+
+
+@pytest.mark.parametrize("N,H,V", [(1, 64, 300), (9, 72, 1100), (30, 65, 1001), (60, 64, 1003),
+                                   (100, 72, 997), (300, 72, 1001)])
+def test_what_the_workspace_held_does_not_matter(N, H, V, monkeypatch):
+    """Workspaces full of NaN bit patterns give the same bits as zeroed ones."""
+    import lm_head_linear_amd as m
+    monkeypatch.setenv("FLCE_VCHUNK", "512")
+    h, W, y, a, b = make(N, H, V, BF)
+    ws = torch.empty(m.flce_logprobs_workspace_size(N, H, V, BF, 6), dtype=torch.uint8, device="cuda")
+    wb = torch.empty(m.flce_logprobs_backward_workspace_size(N, H, V, BF), dtype=torch.uint8,
+                     device="cuda")
+    got = []
+    for byte in (0, 255):
+        ws.fill_(byte), wb.fill_(byte)
+        r = m.flce_logprobs(h, W, y, top_k=6, workspace=ws)
+        got.append([*r, *m.flce_logprobs_backward(h, W, y, r.lse, r.entropy, a, b, workspace=wb)])
+    assert all(torch.equal(p, q) for p, q in zip(*got))
 
 
 def test_gradients_against_differences():
