@@ -384,14 +384,20 @@ __device__ __forceinline__ void tile_epilogue(const float (&z)[64 / TPT], int q,
 }
 
 // ---- few tokens -----------------------------------------------------------------------
-// A workgroup: 64 vocabulary rows, 16 of them a wave, and 16 NT tokens. A lane loads
-// 16 bytes of W's row l % 16 at k = 8 (l / 16): the matrix instruction's operand as
-// it is, no LDS. The h of a 128-k chunk is shared by the waves through LDS, two
+// A workgroup: 64 RB vocabulary rows, 16 RB of them a wave, and 16 NT tokens. A lane
+// loads 16 bytes of W's row l % 16 at k = 8 (l / 16): the matrix instruction's operand
+// as it is, no LDS. The h of a 128-k chunk is shared by the waves through LDS, two
 // chunks in turn. Both come kAheadK chunks early, so that several KiB of W per wave
 // are under way all the time. The loads of whole chunks have no condition (past the
 // last one it is loaded again): a branch around a load makes the compiler wait for
 // it as if the other way had been taken. The part of a chunk at the end of a row that
 // is no multiple of 128 is read first, element by element where it leaves the row.
+//
+// Bound by reading W. Every workgroup reads all of h from L2 as well, so more than 32
+// tokens take two row blocks a wave (us with one and two, W of 131072 x 4096: 1 token
+// 211 and 226, 32 tokens 224 and 233, 64 tokens 254 and 241, 128 tokens 296 and 262;
+// 48 tokens, 256000 x 3584: 451 and 411). Non-temporal loads of W are slower (48
+// tokens: 533): the two halves of a 128-byte line come by two loads.
 constexpr int kChunkK = 128;                       // k per chunk: four matrix steps
 constexpr int kHld = kChunkK + 8;                  // elements of a token's chunk in LDS
 
@@ -428,61 +434,73 @@ __device__ __forceinline__ bf16x8 load_k8_end(const uint16_t* row, int64_t k, in
   return __builtin_bit_cast(bf16x8, v);
 }
 
-template <int NT>
+template <int NT, int RB>
 union FewSmem {
   uint16_t h[2][16 * NT][kHld];
-  float z[16 * NT][68];
+  float z[16 * NT][64 * RB + 4];
 };
 // Lanes of a token in the epilogues of such a tile (48 tokens: whole waves idle).
 template <int NT>
 constexpr int kFewLanes = NT == 3 ? 4 : 256 / (16 * NT);
 
 // The tile's logits in sm.z: 64 rows from v0 of the V rows of W, tokens 0 .. N - 1 of h.
-template <int NT, int ALIGN>
+template <int NT, int ALIGN, int RB>
 __device__ __forceinline__ void few_logits(const uint16_t* __restrict__ h,
                                            const uint16_t* __restrict__ W, int64_t N, int64_t H,
-                                           int64_t V, int64_t v0, FewSmem<NT>& sm) {
+                                           int64_t V, int64_t v0, FewSmem<NT, RB>& sm) {
   constexpr int kAheadK = NT == 8 ? 1 : NT >= 3 ? 2 : 3, R = kAheadK + 1;
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
   const int r = lane & 15, kg = (lane >> 4) * 8;
-  const int64_t v = v0 + w * 16 + r < V ? v0 + w * 16 + r : V - 1;
-  const uint16_t* wrow = W + v * H;
+  const uint16_t* wrow[RB];
+#pragma unroll
+  for (int i = 0; i < RB; ++i) {
+    const int64_t v = v0 + i * 64 + w * 16 + r;
+    wrow[i] = W + (v < V ? v : V - 1) * H;
+  }
   // h: load p of a thread is 16 bytes of token 16 p + tid / 16 at k = 8 (tid % 16)
   const int hr = tid >> 4, hk = (tid & 15) * 8;
   const uint16_t* hrow[NT];
 #pragma unroll
   for (int p = 0; p < NT; ++p) hrow[p] = h + (16 * p + hr < N ? 16 * p + hr : N - 1) * H;
-  bf16x8 a[R][4], b[R][NT];
-  auto load = [&](bf16x8 (&fa)[4], bf16x8 (&fb)[NT], int64_t k0) {
+  bf16x8 a[R][4][RB], b[R][NT];
+  auto load = [&](bf16x8 (&fa)[4][RB], bf16x8 (&fb)[NT], int64_t k0) {
 #pragma unroll
     for (int p = 0; p < NT; ++p) fb[p] = load_k8<ALIGN>(hrow[p] + k0 + hk);
 #pragma unroll
-    for (int s = 0; s < 4; ++s) fa[s] = load_k8<ALIGN>(wrow + k0 + s * 32 + kg);
+    for (int i = 0; i < RB; ++i)
+#pragma unroll
+      for (int s = 0; s < 4; ++s) fa[s][i] = load_k8<ALIGN>(wrow[i] + k0 + s * 32 + kg);
   };
   auto keep = [&](const bf16x8 (&fb)[NT], int half) {
 #pragma unroll
     for (int p = 0; p < NT; ++p) *reinterpret_cast<bf16x8*>(&sm.h[half][16 * p + hr][hk]) = fb[p];
   };
-  f32x4 acc[NT];
+  f32x4 acc[RB][NT];
 #pragma unroll
-  for (int j = 0; j < NT; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  auto multiply = [&](const bf16x8 (&fa)[4], int half) {
+  for (int i = 0; i < RB; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  auto multiply = [&](const bf16x8 (&fa)[4][RB], int half) {
 #pragma unroll
     for (int s = 0; s < 4; ++s)
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         const bf16x8 f = *reinterpret_cast<const bf16x8*>(&sm.h[half][16 * j + r][s * 32 + kg]);
-        acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[s], f, acc[j], 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < RB; ++i)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[s][i], f, acc[i][j], 0, 0, 0);
       }
   };
   const int64_t full = H / kChunkK, end = full * kChunkK;
   auto chunk_k = [&](int64_t c) { return (c < full ? c : full - 1) * kChunkK; };
   if (end < H) {                                   // the end of the rows
-    bf16x8 ea[4], eb[NT];
+    bf16x8 ea[4][RB], eb[NT];
 #pragma unroll
     for (int p = 0; p < NT; ++p) eb[p] = load_k8_end<ALIGN>(hrow[p], end + hk, H);
 #pragma unroll
-    for (int s = 0; s < 4; ++s) ea[s] = load_k8_end<ALIGN>(wrow, end + s * 32 + kg, H);
+    for (int i = 0; i < RB; ++i)
+#pragma unroll
+      for (int s = 0; s < 4; ++s) ea[s][i] = load_k8_end<ALIGN>(wrow[i], end + s * 32 + kg, H);
     keep(eb, 1);
     __syncthreads();
     multiply(ea, 1);
@@ -504,29 +522,36 @@ __device__ __forceinline__ void few_logits(const uint16_t* __restrict__ h,
     }
   }
   __syncthreads();
-  // acc[j][e]: row 16 w + 4 (lane / 16) + e, token 16 j + lane % 16
+  // acc[i][j][e]: row 64 i + 16 w + 4 (lane / 16) + e, token 16 j + lane % 16
 #pragma unroll
-  for (int j = 0; j < NT; ++j)
-    *reinterpret_cast<f32x4*>(&sm.z[16 * j + r][16 * w + (lane >> 4) * 4]) = acc[j];
+  for (int i = 0; i < RB; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+      *reinterpret_cast<f32x4*>(&sm.z[16 * j + r][64 * i + 16 * w + (lane >> 4) * 4]) = acc[i][j];
   __syncthreads();
 }
 
-template <int NT, bool SOFTCAP, int ALIGN>
+template <int NT, bool SOFTCAP, int ALIGN, int RB>
 __global__ __launch_bounds__(256) void k_lp_few(const uint16_t* __restrict__ h,
                                                 const uint16_t* __restrict__ W,
                                                 const int64_t* __restrict__ labels, int64_t N,
                                                 int64_t H, int64_t V, Warp warp, LpOut out) {
-  __shared__ __attribute__((aligned(16))) FewSmem<NT> sm;
-  const int64_t v0 = int64_t(blockIdx.x) * 64;
-  few_logits<NT, ALIGN>(h, W, N, H, V, v0, sm);
+  __shared__ __attribute__((aligned(16))) FewSmem<NT, RB> sm;
+  const int64_t v0 = int64_t(blockIdx.x) * (64 * RB);
+  few_logits<NT, ALIGN, RB>(h, W, N, H, V, v0, sm);
   constexpr int TPT = kFewLanes<NT>, E = 64 / TPT;
   const int t = threadIdx.x / TPT, q = threadIdx.x % TPT;
   if (t >= 16 * NT) return;
-  float z[E];
+#pragma unroll 1
+  for (int i = 0; i < RB; ++i) {
+    const int64_t at = v0 + 64 * i;
+    if (at >= V) break;
+    float z[E];
 #pragma unroll
-  for (int e = 0; e < E; ++e) z[e] = sm.z[t][q * E + e];
-  tile_epilogue<TPT, SOFTCAP>(z, q, t, N, labels, v0, int(V - v0 < 64 ? V - v0 : 64), V, warp,
-                              out);
+    for (int e = 0; e < E; ++e) z[e] = sm.z[t][64 * i + q * E + e];
+    tile_epilogue<TPT, SOFTCAP>(z, q, t, N, labels, at, int(V - at < 64 ? V - at : 64), V, warp,
+                                out);
+  }
 }
 
 // ---- float32 --------------------------------------------------------------------------
@@ -1207,9 +1232,9 @@ __global__ __launch_bounds__(256) void k_lp_few_grad(const uint16_t* __restrict_
                                                      const uint16_t* __restrict__ W, int64_t N,
                                                      int64_t H, int64_t vcur, Warp warp,
                                                      FewGrad a) {
-  __shared__ __attribute__((aligned(16))) FewSmem<NT> sm;
+  __shared__ __attribute__((aligned(16))) FewSmem<NT, 1> sm;
   const int64_t c0 = int64_t(blockIdx.x) * 64;     // the chunk's column
-  few_logits<NT, 16>(h, W, N, H, vcur, c0, sm);
+  few_logits<NT, 16, 1>(h, W, N, H, vcur, c0, sm);
   constexpr int TPT = kFewLanes<NT>, E = 64 / TPT;
   const int t = threadIdx.x / TPT, q = threadIdx.x % TPT;
   const int64_t live = *a.count;
@@ -1410,11 +1435,11 @@ template <bool SOFTCAP>
 hipError_t run_few(const LpArgs& a, const Warp& warp, const LpOut& out, const Launcher& L) {
   const auto* h = static_cast<const uint16_t*>(a.h);
   const auto* W = static_cast<const uint16_t*>(a.W);
-  const dim3 grid(cdiv(a.V, kLpRows));
   auto go = [&](auto nt) {
-    constexpr int NT = decltype(nt)::value;
+    constexpr int NT = decltype(nt)::value, RB = NT >= 3 ? 2 : 1;
+    const dim3 grid(cdiv(a.V, kLpRows * RB));
     auto run = [&](auto align) {
-      hipLaunchKernelGGL((k_lp_few<NT, SOFTCAP, decltype(align)::value>), grid, dim3(256), 0,
+      hipLaunchKernelGGL((k_lp_few<NT, SOFTCAP, decltype(align)::value, RB>), grid, dim3(256), 0,
                          L.stream, h, W, a.tokens, a.N, a.H, a.V, warp, out);
     };
     if (a.H % 8 == 0) run(Int<16>{});
