@@ -509,9 +509,9 @@ int flce_embedding_backward(const int64_t* tokens, const void* dout, int64_t ld_
  *   top_ids[i][k], top_logp[i][k]: the top_k tokens of highest logit, best
  *     first, equal logits by lowest id, and their log probabilities
  * Everything is float32 (ids int64) [N] or [N][top_k]; sums and logits are
- * float32 and no logit is stored in device memory. Alternatives are ranked by z
- * (the order of x without ties made by rounding); where fewer than top_k logits
- * exist above -inf the rest is id -1, value -inf. NaN logits are not ranked.
+ * float32. Alternatives are ranked by z (the order of x without ties made by
+ * rounding). Logits of -inf and NaN are not ranked: where fewer than top_k others
+ * exist the rest is id -1, value -inf.
  * tokens [N] int64 may be NULL (no given tokens: logp must be NULL too);
  * entropy, lse, status may be NULL; top_logp and top_ids are NULL exactly when
  * top_k is 0 (at most FLCE_MAX_TOP).
@@ -519,17 +519,22 @@ int flce_embedding_backward(const int64_t* tokens, const void* dout, int64_t ld_
  * and lse 0, ids -1, top_logp -inf. A row whose token is neither that nor in
  * [0, V) gets logp NaN and sets *status to FLCE_ERR_LABEL; its other outputs do
  * not depend on the token.
- * bf16 inputs with N <= 64 run a kernel that reads W once at the memory's rate;
- * more run the head's matrix-core tiles over the live rows.
- * The workspace (256-byte aligned) is flce_logprobs_workspace_size bytes: the
- * partials and candidates of up to 8192 tokens at a time, the gathered rows, and
- * padded copies for a bf16 H that is not a multiple of 8 and N > 64.
+ * bf16 inputs with N <= 128 run a kernel that reads W once, near the memory's rate;
+ * more run the head's matrix-core tiles over the live rows. A row's values can differ
+ * in the last bits between the two; within either they do not depend on N, and they
+ * are the same bits on every run.
+ * The workspace (256-byte aligned) is flce_logprobs_workspace_size bytes: partial
+ * sums of up to 8192 tokens at a time, the gathered rows, padded copies for a bf16 H
+ * that is not a multiple of 8 and N > 128, and with top_k > 0 the candidates: top_k
+ * for each token and 128 vocabulary rows, or the logits themselves (bf16 with
+ * N <= 128, float32), as many tokens at a time as fit 1 GiB.
  * flce_logprobs_check_args: FLCE_ERR_ARG for sizes as in flce_check_args, top_k
  * outside [0, FLCE_MAX_TOP], softcap negative or not finite, temperature not
  * positive, not finite or without a finite inverse, a missing or contradicting
  * pointer, an output that overlaps an input, another output or the workspace;
  * FLCE_ERR_UNSUPPORTED for a bf16 matrix that is not 16-byte aligned (any other
- * pointer: its element), FLCE_ERR_WORKSPACE.
+ * pointer: its element), for sizes beyond one grid and for float32 with top_k > 0 and
+ * V > 2^22, FLCE_ERR_WORKSPACE.
  */
 #define FLCE_MAX_TOP 32
 size_t flce_logprobs_workspace_size(int64_t N, int64_t H, int64_t V, int dtype, int top_k);
@@ -555,7 +560,8 @@ int flce_logprobs(const void* h, const void* W, const int64_t* tokens, int64_t N
  * for the same h, W, softcap and temperature. The logits are recomputed chunk by
  * chunk; G is rounded to bf16 once for bf16 inputs (kept as a bf16 pair with
  * grad_dtype FLCE_F32), the products are those of flce_forward_backward, and so
- * are accumulate_dW and grad_dtype. Ignored rows give dH rows of zeros; a token
+ * are accumulate_dW and grad_dtype. What that rounding takes from the given token's
+ * G, the largest of its row, is added to dW[token] afterwards. Ignored rows give dH rows of zeros; a token
  * outside [0, V) gives NaN in its dH row and in dW, and FLCE_ERR_LABEL in
  * *status. The same bits on every run. N = 0 zeroes dW unless it accumulates.
  * The workspace (256-byte aligned) is flce_logprobs_backward_workspace_size
@@ -603,8 +609,8 @@ int64_t flce_kept_chunks(int64_t N, int64_t H, int64_t V, int dtype, int accumul
 /*
  * Per-kernel timing (diagnostics for benchmarks; not thread-safe; this
  * library's own addition, no page defines it).
- * flce_profile_begin() clears the record and makes subsequent
- * flce_forward_backward calls bracket every kernel launch with a pair of
+ * flce_profile_begin() clears the record and makes subsequent calls of the
+ * compute entry points bracket every kernel launch with a pair of
  * HIP events on the call's stream. flce_profile_end() stops recording.
  * flce_profile_query(kind, &ms, &launches) waits for the recorded events and
  * returns the summed elapsed milliseconds and launch count of one kernel kind

@@ -10,6 +10,7 @@ from __future__ import annotations
 from typing import NamedTuple, Optional
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _lib
 from ._util import FlceError, _check_tensor, _dtype_code, _ptr
@@ -55,6 +56,8 @@ def _bytes(t):
 
 
 def _workspace(ws, need, dev):
+    if ws is not None and (ws.device != dev or not ws.is_contiguous()):
+        raise ValueError(f"the workspace must be contiguous memory of {dev}, got {ws.device}")
     return torch.empty(need, dtype=torch.uint8, device=dev) if _bytes(ws) < need else ws
 
 
@@ -174,12 +177,19 @@ def flce_rms_norm_backward(dy: torch.Tensor, s: torch.Tensor, weight: torch.Tens
     return dx, dweight
 
 
+def _flat_rows(t):
+    """t [..., H] as rows that the norm reads in place, or a copy of them."""
+    t = t.reshape(-1, t.shape[-1])
+    inplace = t.stride(1) == 1 and (t.stride(0) >= t.shape[1] or t.shape[0] <= 1)
+    return t if inplace else t.contiguous()
+
+
 class _RMSNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, residual, eps, weight_offset):
         shape = x.shape
-        flat = lambda t: None if t is None else t.reshape(-1, shape[-1])  # noqa: E731
-        y, s, rstd = flce_rms_norm(flat(x), weight, flat(residual), eps=eps,
+        y, s, rstd = flce_rms_norm(_flat_rows(x), weight,
+                                   None if residual is None else _flat_rows(residual), eps=eps,
                                    weight_offset=weight_offset)
         ctx.save_for_backward(s, weight, rstd)
         ctx.weight_offset = weight_offset
@@ -190,6 +200,7 @@ class _RMSNorm(torch.autograd.Function):
         return y.view(shape), s.view(shape)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, ds=None):
         s, weight, rstd = ctx.saved_tensors
         if dy is None:                       # only the sum was used
@@ -317,6 +328,7 @@ class _Embedding(torch.autograd.Function):
         return out.view(*tokens.shape, W.shape[1])
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         (tokens,) = ctx.saved_tensors
         V, scale, padding_index = ctx.args
@@ -496,6 +508,7 @@ class _TokenLogprobs(torch.autograd.Function):
         return tuple(out)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad_logp, grad_entropy, *_):
         h, W, tokens, lse, entropy = ctx.saved_tensors
         if grad_logp is None and grad_entropy is None:

@@ -204,3 +204,37 @@ def test_captured_and_replayed():
         g.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip((y, s, q, dx, dw), want))
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+def test_any_layout_through_autograd(dt):
+    """Transposed, sliced and broadcast rows give the bits of their copies, and a
+    broadcast input's gradient is the sum over its copies."""
+    import lm_head_linear_amd as m
+    x, r, w, dy, ds = (t.cuda() for t in make(12, 40, dt, 11))
+    want, s, _ = m.flce_rms_norm(x, w, r)
+    layouts = [x.t().contiguous().t(), torch.stack([x, x], 2)[:, :, 0], x.view(3, 4, 40)]
+    for a in layouts:
+        y, t = m.fused_rms_norm(a, w, r.view(a.shape))
+        assert torch.equal(y.reshape(12, 40), want) and torch.equal(t.reshape(12, 40), s)
+    one = x[:1].clone().requires_grad_()
+    y = m.fused_rms_norm(one.expand(12, 40), w)
+    assert torch.equal(y, m.flce_rms_norm(one.detach().expand(12, 40).contiguous(), w)[0])
+    y.backward(dy)
+    rows, _ = m.flce_rms_norm_backward(dy, one.detach().expand(12, 40).contiguous(), w,
+                                       m.flce_rms_norm(one.detach(), w)[2].expand(12).contiguous())
+    assert torch.equal(one.grad, rows.sum(0, keepdim=True))
+
+
+def test_a_second_derivative_and_a_foreign_workspace_are_refused():
+    import lm_head_linear_amd as m
+    x, r, w, dy, ds = (t.cuda() for t in make(4, 24, torch.float32, 12))
+    x.requires_grad_()
+    (g,) = torch.autograd.grad(m.fused_rms_norm(x, w).square().sum(), x,
+                               create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        g.sum().backward()
+    y, s, q = m.flce_rms_norm(x.detach(), w)
+    need = m.flce_rms_norm_backward_workspace_size(4, 24)
+    with pytest.raises(ValueError, match="workspace"):
+        m.flce_rms_norm_backward(dy, s, w, q, workspace=torch.empty(need, dtype=torch.uint8))
