@@ -562,88 +562,143 @@ __global__ __launch_bounds__(256) void k_lp_few(const uint16_t* __restrict__ h,
 constexpr int kF32Ld = 36;                         // floats per row of a chunk in LDS
 constexpr int kZLd = 68;
 
-struct F32Stage {
-  float a[64][kF32Ld], b[64][kF32Ld];
+constexpr int kF32K = 32;                          // k per chunk
+
+template <int TN>
+union F32Stage {
+  struct { float a[64][kF32Ld], b[TN][kF32Ld]; } half[2];
+  float z[TN][kZLd];
+};
+struct F32Regs {
+  float a[2][4], b[2][4];
 };
 
+// The chunks of k0 .. k1 - 1: whole(k, r) loads one without conditions, end(k, r) what
+// is left behind them, with zeros past k1 (it goes first); keep(r, half) puts it into
+// LDS, multiply(half) adds its products. Ends with a barrier.
+template <class Whole, class End, class Keep, class Multiply>
+__device__ __forceinline__ void f32_chunks(int64_t k0, int64_t k1, Whole whole, End end, Keep keep,
+                                           Multiply multiply) {
+  const int64_t full = (k1 - k0) / kF32K, rest = k0 + full * kF32K;
+  F32Regs r[2];
+  if (rest < k1) {
+    end(rest, r[0]);
+    keep(r[0], 1);
+    __syncthreads();
+    multiply(1);
+  }
+  if (full > 0) {
+    auto at = [&](int64_t c) { return k0 + (c < full ? c : full - 1) * kF32K; };
+    whole(at(0), r[0]);
+    whole(at(1), r[1]);
+    keep(r[0], 0);
+    __syncthreads();
+    for (int64_t c0 = 0; c0 < full; c0 += 2) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        whole(at(c0 + u + 2), r[u]);
+        if (c0 + u < full) multiply(u);
+        keep(r[u ^ 1], u ^ 1);
+        __syncthreads();
+      }
+    }
+  }
+  __syncthreads();
+}
+
+__device__ __forceinline__ f32x4 as_f32x4(const float (&f)[4]) {
+  return f32x4{f[0], f[1], f[2], f[3]};
+}
+
+// 64 rows from v0 of the V rows of W x TN rows from t0 of the N rows of h, in st.z.
+template <int TN>
 __device__ __forceinline__ void f32_logits(const float* __restrict__ W,
                                            const float* __restrict__ h, int64_t v0, int64_t V,
-                                           int64_t t0, int64_t N, int64_t H, F32Stage& st,
-                                           float (*z)[kZLd]) {
+                                           int64_t t0, int64_t N, int64_t H, F32Stage<TN>& st) {
+  constexpr int NB = TN / 32;                      // rows of h a thread loads, column blocks a wave
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
   const int lr = tid >> 3, lc = (tid & 7) * 4;     // rows lr, lr + 32, column lc of a chunk
   const float* ar[2];
-  const float* br[2];
+  const float* br[NB];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int64_t v = v0 + lr + 32 * i, t = t0 + lr + 32 * i;
     ar[i] = W + (v < V ? v : V - 1) * H;
-    br[i] = h + (t < N ? t : N - 1) * H;
+    if (i < NB) br[i] = h + (t < N ? t : N - 1) * H;
   }
-  float ra[2][4], rb[2][4];
-  auto load = [&](int64_t k0) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      load_chunk(ar[i], k0 + lc, H, ra[i]);
-      load_chunk(br[i], k0 + lc, H, rb[i]);
-    }
-  };
-  f32x4 acc[2][2];
+  f32x4 acc[2][NB];
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int j = 0; j < 2; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const int wm = (w & 1) * 32, wn = (w >> 1) * 32, r = lane & 15, kg = (lane >> 4) * 4;
-  load(0);
-  for (int64_t k0 = 0; k0 < H; k0 += 32) {
-    __syncthreads();
+    for (int j = 0; j < NB; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const int wm = (w & 1) * 32, wn = (w >> 1) * 16 * NB, r = lane & 15, kg = (lane >> 4) * 4;
+  f32_chunks(
+      0, H,
+      [&](int64_t k, F32Regs& f) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      *reinterpret_cast<f32x4*>(&st.a[lr + 32 * i][lc]) = f32x4{ra[i][0], ra[i][1], ra[i][2], ra[i][3]};
-      *reinterpret_cast<f32x4*>(&st.b[lr + 32 * i][lc]) = f32x4{rb[i][0], rb[i][1], rb[i][2], rb[i][3]};
-    }
-    __syncthreads();
-    if (k0 + 32 < H) load(k0 + 32);
+        for (int i = 0; i < 2; ++i) {
+          unpack_chunk<float>(load_raw(ar[i] + k + lc), f.a[i]);
+          if (i < NB) unpack_chunk<float>(load_raw(br[i] + k + lc), f.b[i]);
+        }
+      },
+      [&](int64_t k, F32Regs& f) {
 #pragma unroll
-    for (int p = 0; p < 2; ++p) {
-      f32x4 fa[2], fb[2];
+        for (int i = 0; i < 2; ++i) {
+          load_chunk(ar[i], k + lc, H, f.a[i]);
+          if (i < NB) load_chunk(br[i], k + lc, H, f.b[i]);
+        }
+      },
+      [&](const F32Regs& f, int half) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        fa[i] = *reinterpret_cast<const f32x4*>(&st.a[wm + 16 * i + r][p * 16 + kg]);
-        fb[i] = *reinterpret_cast<const f32x4*>(&st.b[wn + 16 * i + r][p * 16 + kg]);
-      }
+        for (int i = 0; i < 2; ++i) {
+          *reinterpret_cast<f32x4*>(&st.half[half].a[lr + 32 * i][lc]) = as_f32x4(f.a[i]);
+          if (i < NB)
+            *reinterpret_cast<f32x4*>(&st.half[half].b[lr + 32 * i][lc]) = as_f32x4(f.b[i]);
+        }
+      },
+      [&](int half) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
+        for (int p = 0; p < 2; ++p) {
+          f32x4 fa[2], fb[NB];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+          for (int i = 0; i < 2; ++i) {
+            fa[i] = *reinterpret_cast<const f32x4*>(&st.half[half].a[wm + 16 * i + r][p * 16 + kg]);
+            if (i < NB)
+              fb[i] = *reinterpret_cast<const f32x4*>(&st.half[half].b[wn + 16 * i + r][p * 16 + kg]);
+          }
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(fa[i][e], fb[j][e], acc[i][j], 0, 0, 0);
-    }
-  }
+          for (int e = 0; e < 4; ++e)
 #pragma unroll
-  for (int j = 0; j < 2; ++j)
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int j = 0; j < NB; ++j)
+                acc[i][j] =
+                    __builtin_amdgcn_mfma_f32_16x16x4f32(fa[i][e], fb[j][e], acc[i][j], 0, 0, 0);
+        }
+      });
+#pragma unroll
+  for (int j = 0; j < NB; ++j)
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      *reinterpret_cast<f32x4*>(&z[wn + 16 * j + r][wm + 16 * i + kg]) = acc[i][j];
+      *reinterpret_cast<f32x4*>(&st.z[wn + 16 * j + r][wm + 16 * i + kg]) = acc[i][j];
   __syncthreads();
 }
 
-template <bool SOFTCAP>
+template <int TN, bool SOFTCAP>
 __global__ __launch_bounds__(256) void k_lp_f32(const float* __restrict__ h,
                                                 const float* __restrict__ W,
                                                 const int64_t* __restrict__ labels, int64_t N,
                                                 int64_t H, int64_t V, Warp warp, LpOut out) {
-  __shared__ __attribute__((aligned(16))) F32Stage st;
-  __shared__ __attribute__((aligned(16))) float z[64][kZLd];
-  const int64_t v0 = int64_t(blockIdx.x) * 64, t0 = int64_t(blockIdx.y) * 64;
-  f32_logits(W, h, v0, V, t0, N, H, st, z);
-  const int tl = threadIdx.x >> 2, q = threadIdx.x & 3;
-  float v[16];
+  __shared__ __attribute__((aligned(16))) F32Stage<TN> st;
+  constexpr int TPT = 256 / TN, E = 64 / TPT;
+  const int64_t v0 = int64_t(blockIdx.x) * 64, t0 = int64_t(blockIdx.y) * TN;
+  f32_logits<TN>(W, h, v0, V, t0, N, H, st);
+  const int tl = threadIdx.x / TPT, q = threadIdx.x % TPT;
+  float v[E];
 #pragma unroll
-  for (int e = 0; e < 16; ++e) v[e] = z[tl][q * 16 + e];
-  tile_epilogue<4, SOFTCAP>(v, q, t0 + tl, N, labels, v0, int(V - v0 < 64 ? V - v0 : 64), V, warp,
-                            out);
+  for (int e = 0; e < E; ++e) v[e] = st.z[tl][q * E + e];
+  tile_epilogue<TPT, SOFTCAP>(v, q, t0 + tl, N, labels, v0, int(V - v0 < 64 ? V - v0 : 64), V,
+                              warp, out);
 }
 
 // ---- the joins --------------------------------------------------------------------------
@@ -1116,8 +1171,8 @@ __global__ __launch_bounds__(256) void k_lp_coef(
     const float* __restrict__ gb, float* __restrict__ lse_g, float* __restrict__ c0,
     float* __restrict__ c1, float* __restrict__ ca) {
   const int64_t r = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  if (r >= N || (count && r >= *count)) return;
-  const int64_t t = idx ? int64_t(idx[r]) : r, y = labels[r];
+  if (r >= N || r >= *count) return;
+  const int64_t t = idx[r], y = labels[r];
   float a = ga ? ga[t] : 0.f;
   const float b = gb ? gb[t] : 0.f, s = gb ? ent[t] : 0.f;
   if (y != ignore_index && (y < 0 || y >= V)) a = NAN;
@@ -1267,29 +1322,34 @@ __global__ __launch_bounds__(256) void k_lp_few_grad(const uint16_t* __restrict_
 
 // float32: G^T[v - v0][t] of one vocabulary chunk, zero for ignored tokens and for
 // the columns N <= t < ldg.
-template <bool SOFTCAP>
+template <int TN, bool SOFTCAP>
 __global__ __launch_bounds__(256) void k_lp_f32_grad(
     const float* __restrict__ h, const float* __restrict__ W, const int64_t* __restrict__ labels,
     int64_t N, int64_t H, int64_t V, int64_t ignore_index, Warp warp,
-    const float* __restrict__ lse, const float* __restrict__ c0, const float* __restrict__ c1,
-    const float* __restrict__ ca, int64_t v0, int64_t vcur, int64_t ldg, float* __restrict__ gt) {
-  __shared__ __attribute__((aligned(16))) F32Stage st;
-  __shared__ __attribute__((aligned(16))) float z[64][kZLd];
-  const int64_t m0 = int64_t(blockIdx.x) * 64, t0 = int64_t(blockIdx.y) * 64;
-  f32_logits(W + v0 * H, h, m0, vcur, t0, N, H, st, z);
-  const int tl = threadIdx.x & 63;
+    const float* __restrict__ lse, const float* __restrict__ ent, const float* __restrict__ ga,
+    const float* __restrict__ gb, int64_t v0, int64_t vcur, int64_t ldg, float* __restrict__ gt) {
+  __shared__ __attribute__((aligned(16))) F32Stage<TN> st;
+  const int64_t m0 = int64_t(blockIdx.x) * 64, t0 = int64_t(blockIdx.y) * TN;
+  f32_logits<TN>(W + v0 * H, h, m0, vcur, t0, N, H, st);
+  const int tl = threadIdx.x % TN;
   const int64_t t = t0 + tl;
   if (t >= ldg) return;
   const int64_t y = t < N ? labels[t] : ignore_index;
   const bool live = t < N && y != ignore_index;
-  const float l0 = live ? lse[t] : 0.f, k0 = live ? c0[t] : 0.f, k1 = live ? c1[t] : 0.f;
-  for (int r = threadIdx.x >> 6; r < 64; r += 4) {
+  float ca = 0.f, cb = 0.f, k0 = 0.f, l0 = 0.f;
+  if (live) {
+    ca = (y < 0 || y >= V) ? NAN : ga ? ga[t] : 0.f;
+    cb = gb ? gb[t] : 0.f;
+    k0 = -(ca + cb * (gb ? ent[t] : 0.f));
+    l0 = lse[t];
+  }
+  for (int r = threadIdx.x / TN; r < 64; r += 256 / TN) {
     if (m0 + r >= vcur) break;
     float v = 0.f;
     if (live) {
-      const float zz = z[tl][r], l = warp_logit<SOFTCAP>(warp, zz) - l0;
-      v = exp2f(l * kLog2e) * fmaf(k1, l, k0);
-      if (v0 + m0 + r == y) v += ca[t];
+      const float zz = st.z[tl][r], l = warp_logit<SOFTCAP>(warp, zz) - l0;
+      v = exp2f(l * kLog2e) * fmaf(-cb, l, k0);
+      if (v0 + m0 + r == y) v += ca;
       v *= warp_slope<SOFTCAP>(warp, zz);
     }
     gt[(m0 + r) * ldg + t] = v;
@@ -1301,34 +1361,53 @@ __global__ __launch_bounds__(256) void k_lp_f32_grad(
 //   DW:  C[m][n] = sum_t G^T[m][t] h[t][n]     (m vocabulary rows, K = tokens)
 //   !DW: C[t][n] = sum_m G^T[m][t] W[m][n]     (K = the chunk's vocabulary rows)
 // B (and for dH also A) is stored with its row contiguous across K: a chunk goes to
-// LDS as [k][64]. blockIdx.z takes a segment of K (dH has few tiles and a long K)
-// and leaves a partial product of its own.
+// LDS as [k][64]. A workgroup makes one tile of a segment of K (dH has few tiles and a
+// long K; each segment leaves a partial product of its own).
+struct F32Product {
+  const float* b;
+  int64_t M, K, kseg;
+  int accumulate;
+  float* c;
+  int64_t seg_stride;
+};
+struct F32ProductStage {
+  float a[2][64 * kF32Ld], b[2][kF32K * kZLd];     // 64 kF32Ld > kF32K kZLd
+};
+
 template <bool DW>
-__global__ __launch_bounds__(256) void k_f32_product(const float* __restrict__ gt, int64_t ldg,
-                                                     const float* __restrict__ B, int64_t M,
-                                                     int64_t H, int64_t K, int64_t kseg,
-                                                     int accumulate, float* __restrict__ C,
-                                                     int64_t seg_stride) {
-  __shared__ __attribute__((aligned(16))) float sa[DW ? 64 * kF32Ld : 32 * kZLd];
-  __shared__ __attribute__((aligned(16))) float sb[32 * kZLd];
+__device__ __forceinline__ void f32_product(const float* __restrict__ gt, int64_t ldg, int64_t H,
+                                            const F32Product& q, int64_t index,
+                                            F32ProductStage& st) {
+  const int64_t M = q.M, K = q.K, mt = (M + 63) / 64, nt = (H + 63) / 64;
+  const float* __restrict__ B = q.b;
+  float (&sa)[2][64 * kF32Ld] = st.a;
+  float (&sb)[2][kF32K * kZLd] = st.b;
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-  const int64_t m0 = int64_t(blockIdx.x) * 64, n0 = int64_t(blockIdx.y) * 64;
-  const int64_t k0 = int64_t(blockIdx.z) * kseg, k1 = K - k0 < kseg ? K : k0 + kseg;
-  C += int64_t(blockIdx.z) * seg_stride;
+  const int64_t m0 = index % mt * 64, n0 = index / mt % nt * 64, z = index / (mt * nt);
+  const int64_t k0 = z * q.kseg, k1 = K - k0 < q.kseg ? K : k0 + q.kseg;
+  float* __restrict__ C = q.c + z * q.seg_stride;
   // [k][64] chunks: rows tid / 16, + 16, columns 4 (tid % 16); [64][k] as f32_logits
   const int kr = tid >> 4, kc = (tid & 15) * 4, lr = tid >> 3, lc = (tid & 7) * 4;
-  float ra[2][4], rb[2][4];
-  auto load = [&](int64_t k) {
+  const float* ar[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int64_t m = m0 + lr + 32 * i, c = m0 + kc < ldg ? m0 + kc : 0;
+    ar[i] = DW ? gt + (m < M ? m : M - 1) * ldg + lc : gt + (kr + 16 * i) * ldg + c;
+  }
+  auto load_a = [&](int64_t k, F32Regs& f) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) unpack_chunk<float>(load_raw(ar[i] + (DW ? k : k * ldg)), f.a[i]);
+  };
+  auto end = [&](int64_t k, F32Regs& f) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int64_t kk = k + kr + 16 * i;
       if constexpr (DW) {
-        const int64_t m = m0 + lr + 32 * i;
-        load_chunk(gt + (m < M ? m : M - 1) * ldg, k + lc, k1, ra[i]);
+        load_chunk(ar[i] - lc, k + lc, k1, f.a[i]);
       } else {
-        load_chunk(gt + (kk < k1 ? kk : k1 - 1) * ldg, m0 + kc, kk < k1 ? M : 0, ra[i]);
+        load_chunk(gt + (kk < k1 ? kk : k1 - 1) * ldg, m0 + kc, kk < k1 ? M : 0, f.a[i]);
       }
-      load_chunk(B + (kk < k1 ? kk : k1 - 1) * H, n0 + kc, kk < k1 ? H : 0, rb[i]);
+      load_chunk(B + (kk < k1 ? kk : k1 - 1) * H, n0 + kc, kk < k1 ? H : 0, f.b[i]);
     }
   };
   f32x4 acc[2][2];
@@ -1337,18 +1416,15 @@ __global__ __launch_bounds__(256) void k_f32_product(const float* __restrict__ g
 #pragma unroll
     for (int j = 0; j < 2; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   const int wm = (w & 1) * 32, wn = (w >> 1) * 32, r = lane & 15, kg = (lane >> 4) * 4;
-  load(k0);
-  for (int64_t k = k0; k < k1; k += 32) {
-    __syncthreads();
+  auto keep = [&](const F32Regs& f, int half) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      float* pa = DW ? sa + (lr + 32 * i) * kF32Ld + lc : sa + (kr + 16 * i) * kZLd + kc;
-      *reinterpret_cast<f32x4*>(pa) = f32x4{ra[i][0], ra[i][1], ra[i][2], ra[i][3]};
-      *reinterpret_cast<f32x4*>(sb + (kr + 16 * i) * kZLd + kc) =
-          f32x4{rb[i][0], rb[i][1], rb[i][2], rb[i][3]};
+      float* pa = sa[half] + (DW ? (lr + 32 * i) * kF32Ld + lc : (kr + 16 * i) * kZLd + kc);
+      *reinterpret_cast<f32x4*>(pa) = as_f32x4(f.a[i]);
+      *reinterpret_cast<f32x4*>(sb[half] + (kr + 16 * i) * kZLd + kc) = as_f32x4(f.b[i]);
     }
-    __syncthreads();
-    if (k + 32 < k1) load(k + 32);
+  };
+  auto multiply = [&](int half) {
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
       float fa[2][4], fb[2][4];
@@ -1357,8 +1433,8 @@ __global__ __launch_bounds__(256) void k_f32_product(const float* __restrict__ g
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int kk = p * 16 + kg + e;
-          fa[i][e] = DW ? sa[(wm + 16 * i + r) * kF32Ld + kk] : sa[kk * kZLd + wm + 16 * i + r];
-          fb[i][e] = sb[kk * kZLd + wn + 16 * i + r];
+          fa[i][e] = sa[half][DW ? (wm + 16 * i + r) * kF32Ld + kk : kk * kZLd + wm + 16 * i + r];
+          fb[i][e] = sb[half][kk * kZLd + wn + 16 * i + r];
         }
 #pragma unroll
       for (int e = 0; e < 4; ++e)
@@ -1368,6 +1444,29 @@ __global__ __launch_bounds__(256) void k_f32_product(const float* __restrict__ g
           for (int j = 0; j < 2; ++j)
             acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(fa[i][e], fb[j][e], acc[i][j], 0, 0, 0);
     }
+  };
+  // B's columns: 16 bytes where the tile lies in the row, otherwise one by one, those
+  // past the row (their products are not stored) from its last
+  const bool inside = n0 + 64 <= H;
+  const float* b0 = B + (inside ? n0 + kc : 0);
+  int col[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) col[e] = int(n0 + kc + e < H ? n0 + kc + e : H - 1);
+  if (inside) {
+    f32_chunks(k0, k1, [&](int64_t k, F32Regs& f) {
+      load_a(k, f);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        unpack_chunk<float>(load_raw(b0 + (k + kr + 16 * i) * H), f.b[i]);
+    }, end, keep, multiply);
+  } else {
+    f32_chunks(k0, k1, [&](int64_t k, F32Regs& f) {
+      load_a(k, f);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f.b[i][e] = b0[(k + kr + 16 * i) * H + col[e]];
+    }, end, keep, multiply);
   }
   // acc[i][j][e]: row 16 i + 4 (lane / 16) + e, column 16 j + lane % 16
 #pragma unroll
@@ -1380,20 +1479,41 @@ __global__ __launch_bounds__(256) void k_f32_product(const float* __restrict__ g
         const int64_t n = n0 + wn + 16 * j + r;
         if (m < M && n < H) {
           float* c = C + m * H + n;
-          *c = accumulate ? *c + acc[i][j][e] : acc[i][j][e];
+          *c = q.accumulate ? *c + acc[i][j][e] : acc[i][j][e];
         }
       }
     }
 }
 
-// dH (+)= the segments' partial products, in order.
+// dH's tiles, then dW's.
+__global__ __launch_bounds__(256) void k_f32_products(const float* __restrict__ gt, int64_t ldg,
+                                                      int64_t H, F32Product dh, F32Product dw,
+                                                      int64_t dh_tiles) {
+  __shared__ __attribute__((aligned(16))) F32ProductStage st;
+  const int64_t i = blockIdx.x;
+  if (i < dh_tiles) f32_product<false>(gt, ldg, H, dh, i, st);
+  else f32_product<true>(gt, ldg, H, dw, i - dh_tiles, st);
+}
+
+// dH (+)= the segments' partial products, in an order of their count alone: 8 groups of
+// 32 threads add every 8th segment, then the groups' sums in order.
 __global__ __launch_bounds__(256) void k_f32_dh_sum(const float* __restrict__ part, int segs,
                                                     int64_t n, int accumulate,
                                                     float* __restrict__ dH) {
-  const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= n) return;
-  float v = accumulate ? dH[i] : 0.f;
-  for (int z = 0; z < segs; ++z) v += part[z * n + i];
+  __shared__ float red[8][32];
+  const int c = threadIdx.x & 31, g = threadIdx.x >> 5;
+  const int64_t i = int64_t(blockIdx.x) * 32 + c;
+  float v = 0.f;
+  if (i < n) {
+#pragma unroll 8
+    for (int z = g; z < segs; z += 8) v += part[z * n + i];
+  }
+  red[g][c] = v;
+  __syncthreads();
+  if (g > 0 || i >= n) return;
+  v = accumulate ? dH[i] : 0.f;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) v += red[k][c];
   dH[i] = v;
 }
 
@@ -1401,6 +1521,14 @@ unsigned cdiv(int64_t a, int64_t b) { return unsigned((a + b - 1) / b); }
 
 template <int I>
 using Int = std::integral_constant<int, I>;
+
+// Whether the float32 tiles take 32 tokens instead of 64: where the last 64 would be half
+// empty, or where there are too few tiles for the chip (us of a training step with 64 and
+// 32: 257 tokens of 515 over 5003 114 and 106, 20 of 1024 over 32000 167 and 140, 300 of
+// 515 over 1003 66 and 55; the other way 512 of 1024 over 32000 1148 and 1188).
+bool f32_narrow(int64_t N, int64_t V) {
+  return (N - 1) % 64 < 32 || ((N + 63) / 64) * ((V + 63) / 64) <= 256;
+}
 
 template <bool SOFTCAP, bool TAU_ONLY>
 hipError_t run_join(const LpPlan& q, const JoinArgs& j, const Launcher& L) {
@@ -1491,9 +1619,13 @@ hipError_t logprobs(const LpPlan& q, const LpArgs& a, char* ws, const Launcher& 
       at_token(c, t0);
       c.N = a.N - t0 < q.nc ? a.N - t0 : q.nc;
       L.pre(kLpTiles);
-      hipLaunchKernelGGL(k_lp_f32<SOFTCAP>, dim3(cdiv(a.V, 64), cdiv(c.N, 64)), dim3(256), 0,
-                         L.stream, static_cast<const float*>(a.h) + t0 * a.H,
-                         static_cast<const float*>(a.W), c.labels, c.N, a.H, a.V, warp, out);
+      auto run = [&](auto tn) {
+        constexpr int TN = decltype(tn)::value;
+        hipLaunchKernelGGL((k_lp_f32<TN, SOFTCAP>), dim3(cdiv(a.V, 64), cdiv(c.N, TN)), dim3(256),
+                           0, L.stream, static_cast<const float*>(a.h) + t0 * a.H,
+                           static_cast<const float*>(a.W), c.labels, c.N, a.H, a.V, warp, out);
+      };
+      f32_narrow(c.N, a.V) ? run(Int<32>{}) : run(Int<64>{});
       L.post(kLpTiles);
       e = hipGetLastError();
       if (e == hipSuccess) e = run_join<SOFTCAP, false>(q, c, L);
@@ -1587,27 +1719,21 @@ hipError_t launch_logprobs(const LpPlan& q, const LpArgs& a, char* ws, const Lau
 
 hipError_t launch_lp_f32_products(const Plan& p, const Args& a, int64_t chunk, const Launcher& L) {
   const int64_t v0 = chunk * p.vchunk, vcur = gemm::chunk_rows(p, chunk);
-  const float* gt = static_cast<const float*>(a.g);
-  float* dW = static_cast<float*>(a.dW) + v0 * p.H;
   float* dH = static_cast<float*>(a.dH);
-  L.pre(kGemmDW);
-  hipLaunchKernelGGL(k_f32_product<true>, dim3(cdiv(vcur, 64), cdiv(p.H, 64)), dim3(256), 0,
-                     L.stream, gt, p.ldg, static_cast<const float*>(a.h), vcur, p.H, p.N, p.N,
-                     a.accumulate_dW, dW, int64_t(0));
-  L.post(kGemmDW);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  const float* W = static_cast<const float*>(a.W) + v0 * p.H;
   const int64_t kseg = lp_f32_segment(p), segs = (vcur + kseg - 1) / kseg;
-  L.pre(kGemmDH);
-  hipLaunchKernelGGL(k_f32_product<false>, dim3(cdiv(p.N, 64), cdiv(p.H, 64), unsigned(segs)),
-                     dim3(256), 0, L.stream, gt, p.ldg, W, p.N, p.H, vcur, kseg,
-                     segs == 1 && chunk > 0 ? 1 : 0, segs == 1 ? dH : a.dh_part, p.N * p.H);
-  L.post(kGemmDH);
-  e = hipGetLastError();
+  const F32Product dh{static_cast<const float*>(a.W) + v0 * p.H, p.N, vcur, kseg,
+                      segs == 1 && chunk > 0 ? 1 : 0, segs == 1 ? dH : a.dh_part, p.N * p.H};
+  const F32Product dw{static_cast<const float*>(a.h), vcur, p.N, p.N, a.accumulate_dW,
+                      static_cast<float*>(a.dW) + v0 * p.H, 0};
+  const int64_t nt = cdiv(p.H, 64), dh_tiles = cdiv(p.N, 64) * nt * segs;
+  L.pre(kGemmDWDH);
+  hipLaunchKernelGGL(k_f32_products, dim3(unsigned(dh_tiles + cdiv(vcur, 64) * nt)), dim3(256), 0,
+                     L.stream, static_cast<const float*>(a.g), p.ldg, p.H, dh, dw, dh_tiles);
+  L.post(kGemmDWDH);
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess || segs == 1) return e;
   L.pre(kDhReduce);
-  hipLaunchKernelGGL(k_f32_dh_sum, dim3(cdiv(p.N * p.H, 256)), dim3(256), 0, L.stream, a.dh_part,
+  hipLaunchKernelGGL(k_f32_dh_sum, dim3(cdiv(p.N * p.H, 32)), dim3(256), 0, L.stream, a.dh_part,
                      int(segs), p.N * p.H, chunk > 0 ? 1 : 0, dH);
   L.post(kDhReduce);
   return hipGetLastError();
@@ -1615,12 +1741,12 @@ hipError_t launch_lp_f32_products(const Plan& p, const Args& a, int64_t chunk, c
 
 hipError_t launch_lp_coefficients(const Plan& p, const Args& a, const LpGradArgs& g,
                                   const Launcher& L) {
-  if (lp_few_backward(p)) return hipSuccess;       // formed where they are used
+  // few tokens and float32: formed where they are used
+  if (p.dtype != FLCE_BF16 || lp_few_backward(p)) return hipSuccess;
+  if (!p.compact) return hipErrorInvalidValue;
   L.pre(kLpJoin);
   hipLaunchKernelGGL(k_lp_coef, dim3(cdiv(p.N, 256)), dim3(256), 0, L.stream,
-                     p.compact ? a.idx : nullptr, p.compact ? a.yc : a.labels,
-                     p.compact ? &a.sc->n_valid : nullptr, p.N, p.V, a.ignore_index, g.lse,
-                     g.entropy, g.grad_logp, g.grad_entropy, g.lse_g, g.c0, g.c1, g.ca);
+                     a.idx, a.yc, &a.sc->n_valid, p.N, p.V, a.ignore_index, g.lse, g.entropy, g.grad_logp, g.grad_entropy, g.lse_g, g.c0, g.c1, g.ca);
   L.post(kLpJoin);
   return hipGetLastError();
 }
@@ -1630,15 +1756,19 @@ hipError_t launch_lp_gradient(const Plan& p, const Args& a, const LpGradArgs& g,
   const int64_t v0 = chunk * p.vchunk, vcur = gemm::chunk_rows(p, chunk);
   const Warp warp = make_warp(a.softcap, g.temperature);
   if (p.dtype == FLCE_F32) {
-    auto run = [&](auto cap) {
-      hipLaunchKernelGGL(k_lp_f32_grad<decltype(cap)::value>, dim3(cdiv(vcur, 64), cdiv(p.ldg, 64)),
-                         dim3(256), 0, L.stream, static_cast<const float*>(a.h),
-                         static_cast<const float*>(a.W), a.labels, p.N, p.H, p.V, a.ignore_index,
-                         warp, g.lse_g, g.c0, g.c1, g.ca, v0, vcur, p.ldg,
-                         static_cast<float*>(a.g));
+    auto run = [&](auto tn, auto cap) {
+      constexpr int TN = decltype(tn)::value;
+      hipLaunchKernelGGL((k_lp_f32_grad<TN, decltype(cap)::value>),
+                         dim3(cdiv(vcur, 64), cdiv(p.ldg, TN)), dim3(256), 0, L.stream,
+                         static_cast<const float*>(a.h), static_cast<const float*>(a.W), a.labels,
+                         p.N, p.H, p.V, a.ignore_index, warp, g.lse, g.entropy, g.grad_logp,
+                         g.grad_entropy, v0, vcur, p.ldg, static_cast<float*>(a.g));
+    };
+    auto by_cap = [&](auto tn) {
+      a.softcap > 0.f ? run(tn, std::true_type{}) : run(tn, std::false_type{});
     };
     L.pre(kGradLogits);
-    a.softcap > 0.f ? run(std::true_type{}) : run(std::false_type{});
+    f32_narrow(p.N, vcur) ? by_cap(Int<32>{}) : by_cap(Int<64>{});
     L.post(kGradLogits);
     return hipGetLastError();
   }
