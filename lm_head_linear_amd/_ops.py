@@ -51,6 +51,12 @@ def _run(where, dev, fn, *args):
         raise FlceError(rc, where)
 
 
+def _stream(dev):
+    """dev's current stream as a handle (torch.cuda.current_stream builds an object:
+    2 us of a call's 11)."""
+    return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
 def _bytes(t):
     return 0 if t is None else t.numel() * t.element_size()
 
@@ -112,7 +118,7 @@ def flce_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torc
     _run("flce_rms_norm", dev, _lib.load().flce_rms_norm, x.data_ptr(), ld_x, _ptr(residual), ld_r,
          weight.data_ptr(), N, H, float(eps), float(weight_offset), y.data_ptr(), ld_y, _ptr(s),
          ld_s, rstd.data_ptr(),
-         torch.cuda.current_stream(dev).cuda_stream, code, wcode)
+         _stream(dev), code, wcode)
     return y, x if residual is None else s, rstd
 
 
@@ -172,7 +178,7 @@ def flce_rms_norm_backward(dy: torch.Tensor, s: torch.Tensor, weight: torch.Tens
     _run("flce_rms_norm_backward", dev, _lib.load().flce_rms_norm_backward, dy.data_ptr(), ld_dy,
          _ptr(ds), ld_ds, s.data_ptr(), ld_s, weight.data_ptr(), rstd.data_ptr(), N, H,
          float(weight_offset), dx.data_ptr(), ld_dx, _ptr(dweight),
-         int(bool(accumulate_dweight)), torch.cuda.current_stream(dev).cuda_stream, code, wcode,
+         int(bool(accumulate_dweight)), _stream(dev), code, wcode,
          _ptr(workspace), _bytes(workspace))
     return dx, dweight
 
@@ -261,7 +267,7 @@ def flce_embedding(tokens: torch.Tensor, W: torch.Tensor, *, scale: float = 1.0,
         ld = _rows("out", out, N, H, W.dtype, dev)
     _run("flce_embedding", dev, _lib.load().flce_embedding, tokens.data_ptr(), W.data_ptr(), N, H,
          V, int(padding_index), float(scale), out.data_ptr(), ld,
-         torch.cuda.current_stream(dev).cuda_stream, code, _ptr(status))
+         _stream(dev), code, _ptr(status))
     return out
 
 
@@ -313,7 +319,7 @@ def flce_embedding_backward(tokens: torch.Tensor, dout: torch.Tensor, V: int, *,
     workspace = _workspace(workspace, flce_embedding_backward_workspace_size(N, H, V), dev)
     _run("flce_embedding_backward", dev, _lib.load().flce_embedding_backward, tokens.data_ptr(),
          dout.data_ptr(), ld, N, H, V, int(padding_index), float(scale), dW.data_ptr(),
-         int(bool(accumulate_dW)), torch.cuda.current_stream(dev).cuda_stream, code, gcode,
+         int(bool(accumulate_dW)), _stream(dev), code, gcode,
          workspace.data_ptr(), _bytes(workspace), _ptr(status))
     return dW
 
@@ -423,7 +429,7 @@ def flce_logprobs(h: torch.Tensor, W: torch.Tensor, tokens: Optional[torch.Tenso
     _run("flce_logprobs", dev, lib.flce_logprobs, h.data_ptr(), W.data_ptr(), _ptr(tokens), N, H,
          V, int(ignore_index), float(softcap), float(temperature), top_k, _ptr(logp),
          entropy.data_ptr(), lse.data_ptr(), top_logp.data_ptr() if top_k else None,
-         top_ids.data_ptr() if top_k else None, torch.cuda.current_stream(dev).cuda_stream, code,
+         top_ids.data_ptr() if top_k else None, _stream(dev), code,
          workspace.data_ptr(), _bytes(workspace), _ptr(status))
     return TokenLogprobs(logp, entropy, lse, top_logp, top_ids)
 
@@ -491,7 +497,7 @@ def flce_logprobs_backward(h: torch.Tensor, W: torch.Tensor, tokens: torch.Tenso
     _run("flce_logprobs_backward", dev, lib.flce_logprobs_backward, h.data_ptr(), W.data_ptr(),
          tokens.data_ptr(), lse.data_ptr(), _ptr(entropy), _ptr(grad_logp), _ptr(grad_entropy), N,
          H, V, int(ignore_index), float(softcap), float(temperature), dH.data_ptr(),
-         dW.data_ptr(), int(bool(accumulate_dW)), torch.cuda.current_stream(dev).cuda_stream, code,
+         dW.data_ptr(), int(bool(accumulate_dW)), _stream(dev), code,
          gcode, workspace.data_ptr(), _bytes(workspace), _ptr(status))
     return dH, dW
 
