@@ -246,8 +246,10 @@ __global__ __launch_bounds__(1024) void k_rms_norm_dw(const float* __restrict__ 
   const int col = threadIdx.x & 15, grp = threadIdx.x >> 4;
   const int64_t c = int64_t(blockIdx.x) * 16 + col;
   float a = 0.f;
-  if (c < H)
+  if (c < H) {
+#pragma unroll 8
     for (int64_t b = grp; b < nb; b += 64) a += part[b * H + c];
+  }
   red[grp][col] = a;
   __syncthreads();
   for (int k = 32; k > 0; k >>= 1) {
@@ -283,18 +285,25 @@ hipError_t norm_forward(const NormArgs& a, const Launcher& L) {
   const WT* w = static_cast<const WT*>(a.weight);
   T* y = static_cast<T*>(a.y);
   T* s = static_cast<T*>(a.s);
+  // a row a workgroup, and a grid holds less than 2^32 threads
+  constexpr int64_t kRows = int64_t(1) << 21;
   L.pre(kNorm);
-  with_variant(chunks, [&](auto waves, auto c) {
-    constexpr int WV = decltype(waves)::value, C = decltype(c)::value;
-    if (r)
-      hipLaunchKernelGGL((k_rms_norm<T, WT, WV, C, true>), dim3(unsigned(a.N)), dim3(WV * 64), 0,
-                         L.stream, x, a.ld_x, r, a.ld_res, w, a.H, a.eps, a.offset, y, a.ld_y, s,
-                         a.ld_s, a.rstd);
-    else
-      hipLaunchKernelGGL((k_rms_norm<T, WT, WV, C, false>), dim3(unsigned(a.N)), dim3(WV * 64), 0,
-                         L.stream, x, a.ld_x, r, a.ld_res, w, a.H, a.eps, a.offset, y, a.ld_y, s,
-                         a.ld_s, a.rstd);
-  });
+  for (int64_t t0 = 0; t0 < a.N; t0 += kRows) {
+    const dim3 grid(unsigned(a.N - t0 < kRows ? a.N - t0 : kRows));
+    const T* xt = x + t0 * a.ld_x;
+    T* yt = y + t0 * a.ld_y;
+    float* q = a.rstd ? a.rstd + t0 : nullptr;
+    with_variant(chunks, [&](auto waves, auto c) {
+      constexpr int WV = decltype(waves)::value, C = decltype(c)::value;
+      if (r)
+        hipLaunchKernelGGL((k_rms_norm<T, WT, WV, C, true>), grid, dim3(WV * 64), 0, L.stream, xt,
+                           a.ld_x, r + t0 * a.ld_res, a.ld_res, w, a.H, a.eps, a.offset, yt,
+                           a.ld_y, s + t0 * a.ld_s, a.ld_s, q);
+      else
+        hipLaunchKernelGGL((k_rms_norm<T, WT, WV, C, false>), grid, dim3(WV * 64), 0, L.stream, xt,
+                           a.ld_x, r, a.ld_res, w, a.H, a.eps, a.offset, yt, a.ld_y, s, a.ld_s, q);
+    });
+  }
   L.post(kNorm);
   return hipGetLastError();
 }

@@ -15,6 +15,8 @@ namespace {
 
 constexpr int64_t kMaxRows = int64_t(1) << 31, kMaxWidth = int64_t(1) << 24;
 constexpr int64_t kMaxGrid = (int64_t(1) << 31) - 1;
+// Workgroups of `threads` threads in one grid, which holds less than 2^32 threads.
+constexpr int64_t max_groups(int64_t threads) { return ((int64_t(1) << 32) - 1) / threads; }
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -55,6 +57,13 @@ bool clash(std::initializer_list<Buf> outs, std::initializer_list<Buf> ins) {
       if (overlap(*a, b)) return true;
   }
   return false;
+}
+
+// The float32 gradient's grids: tiles of 32 tokens along y, the products' tiles in one.
+bool lp_f32_grids_ok(const Plan& p) {
+  const int64_t ht = ceil_div(p.H, 64), segs = ceil_div(p.vchunk, lp_f32_segment(p));
+  return ceil_div(p.ldg, 32) <= 65535 &&
+         (ceil_div(p.N, 64) * segs + ceil_div(p.vchunk, 64)) * ht <= max_groups(256);
 }
 
 }  // namespace
@@ -235,7 +244,7 @@ int flce_embedding_check_args(const int64_t* tokens, const void* W, int64_t N, i
   const Buf bt = vec(tokens, N, 8), bw = matrix(W, V, H, H, es),
             bo = matrix(out, N, H, ld_out, es), bst = vec(status, 1, 4);
   if (clash({bo, bst}, {bt, bw})) return FLCE_ERR_ARG;
-  if (ceil_div(N * ceil_div(H * int64_t(es), 2048), 4) > kMaxGrid) return FLCE_ERR_UNSUPPORTED;
+  if (ceil_div(N * ceil_div(H * int64_t(es), 2048), 4) > max_groups(256)) return FLCE_ERR_UNSUPPORTED;
   for (const Buf& b : {bt, bw, bo, bst})
     if (misaligned(b)) return FLCE_ERR_UNSUPPORTED;
   return FLCE_OK;
@@ -263,7 +272,9 @@ int flce_embedding_backward_check_args(const int64_t* tokens, const void* dout, 
             wk = vec(workspace, int64_t(workspace_bytes), 1);
   if (clash({bw, bst, wk}, {bt, bd})) return FLCE_ERR_ARG;
   if (dtype == FLCE_F32 && grad_dtype == FLCE_BF16) return FLCE_ERR_UNSUPPORTED;
-  if (ceil_div(N, embed_window(N)) * ceil_div(H, 512) > kMaxGrid)
+  if (ceil_div(N, embed_window(N)) * ceil_div(H, 512) > max_groups(512) ||
+      ceil_div(V * H * int64_t(esize(grad_dtype)), 65536) + ceil_div(N, kSortChunk) >
+          max_groups(kSortChunk))
     return FLCE_ERR_UNSUPPORTED;
   for (const Buf& b : {bt, bd, bw, bst})
     if (misaligned(b)) return FLCE_ERR_UNSUPPORTED;
@@ -305,6 +316,7 @@ int flce_logprobs_check_args(const void* h, const void* W, const int64_t* tokens
   if (clash({bl, be, bz, bv, bi, bs, wk}, {bh, bw, bt})) return FLCE_ERR_ARG;
   if (dtype == FLCE_BF16 && !bf16_shape_ok(N, p.p.H, V)) return FLCE_ERR_UNSUPPORTED;
   if (top_k > 0 && !p.tiles && V > kLpMaxTopV) return FLCE_ERR_UNSUPPORTED;
+  if (dtype == FLCE_F32 && ceil_div(V, 64) > max_groups(256)) return FLCE_ERR_UNSUPPORTED;
   const uintptr_t mask = dtype == FLCE_BF16 ? 15u : 3u;
   if ((bw.begin() & mask) || (N > 0 && (bh.begin() & mask))) return FLCE_ERR_UNSUPPORTED;
   for (const Buf& b : {bt, bl, be, bz, bv, bi, bs})
@@ -359,6 +371,7 @@ int flce_logprobs_backward_check_args(const void* h, const void* W, const int64_
             wk = vec(workspace, int64_t(workspace_bytes), 1);
   if (clash({dh, dw, bs, wk}, {bh, bw, bt, bz, be, ga, gb})) return FLCE_ERR_ARG;
   if (dtype == FLCE_BF16 && !bf16_shape_ok(N, p.H, V)) return FLCE_ERR_UNSUPPORTED;
+  if (dtype == FLCE_F32 && !lp_f32_grids_ok(p)) return FLCE_ERR_UNSUPPORTED;
   const uintptr_t mask = dtype == FLCE_BF16 ? 15u : 3u;
   if (((bw.begin() | dw.begin()) & mask) || (N > 0 && ((bh.begin() | dh.begin()) & mask)))
     return FLCE_ERR_UNSUPPORTED;

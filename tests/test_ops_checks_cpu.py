@@ -225,6 +225,29 @@ def test_logprobs_workspace():
     assert b - a < (1 << 17) * (64 * 2 + 32) and a < (1 << 30) + (1 << 17) * 256 + (1 << 25)
 
 
+def test_sizes_beyond_one_grid():
+    """A grid holds less than 2^32 threads, and 65535 workgroups along its second axis."""
+    at = lambda i: Buf(i << 58)  # noqa: E731
+    big = dict(tokens=at(1), W=at(2), out=at(3), status=None, H=2048)
+    assert embed(**big, N=(1 << 24), V=100) == OK        # two 2 KiB pieces a row
+    assert embed(**big, N=(1 << 25) + 8, V=100) == UNSUP
+    back = dict(tokens=at(1), dout=at(2), dW=at(3), status=None, N=100, H=4096,
+                workspace=Buf(8 << 58, 1 << 30))
+    assert embed_bwd(**back, V=1 << 24) == OK            # 128 GiB of dW
+    assert embed_bwd(**back, V=1 << 25) == UNSUP
+    few = dict(h=at(1), W=at(2), tokens=at(3), logp=at(4), entropy=None, lse=None, status=None,
+               N=1, H=8, dtype=torch.float32, **NOTOP)
+    ws = lambda **k: Buf(5 << 58, m.flce_logprobs_workspace_size(  # noqa: E731
+        1, 8, k["V"], torch.float32, 0))
+    assert lp(**few, V=1 << 29, workspace=ws(V=1 << 29)) == OK
+    assert lp(**few, V=1 << 30, workspace=ws(V=1 << 30)) == UNSUP
+    grad = dict(h=at(1), W=at(2), tokens=at(3), lse=at(4), entropy=None, grad_logp=at(5),
+                grad_entropy=None, dH=at(6), dW=at(7), status=None, H=8, V=100,
+                dtype=torch.float32, workspace=Buf(8 << 58, 1 << 50))
+    assert lp_bwd(**grad, N=65535 * 32) == OK
+    assert lp_bwd(**grad, N=65535 * 32 + 1) == UNSUP
+
+
 def test_cpu_tensors_are_refused():
     t, W = torch.zeros(3, dtype=torch.int64), torch.zeros(5, 8)
     for call in (lambda: m.flce_embedding(t, W), lambda: m.flce_rms_norm(W, torch.ones(8)),
