@@ -49,6 +49,17 @@ __device__ __forceinline__ T rows_all(T x, Op op) {
   return x;
 }
 
+// op over the two lanes l, l ^ 16.
+template <class T, class Op>
+__device__ __forceinline__ T pair_rows(T x, Op op) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  const auto u = __builtin_bit_cast(uint32_t, x);
+  const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  x = op(__builtin_bit_cast(T, uint32_t(a[0])), __builtin_bit_cast(T, uint32_t(a[1])));
+#endif
+  return x;
+}
+
 // op over the wave.
 template <class T, class Op>
 __device__ __forceinline__ T wave_all(T x, Op op) {

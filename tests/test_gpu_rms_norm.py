@@ -6,7 +6,9 @@ the value); the float32 arithmetic before it adds relative errors of u = 2^-24 a
 rounding. A sum over a row goes through chains of at most H / 64 / waves + 10
 additions, below 100 at every width here, so a mean is off by 100 u of the sum of
 magnitudes and rstd (a square root) by half of that; a dozen roundings follow.
-dweight sums N rows in chains of at most N / 1024 + 25."""
+dweight sums N rows in chains of at most N / 1024 + 25, of rows up to 2 KiB (of which a
+workgroup takes up to 16 at a time) N / 2048 + 40; both stay below the bound's
+N / 1024 + 25 with the 70 for the roundings of each term."""
 import pytest
 import torch
 
@@ -60,7 +62,12 @@ def close(got, ref, dt, slack, what):
 CASES = [(1, 4096, torch.bfloat16), (16, 4096, torch.bfloat16), (37, 1, torch.float32),
          (5, 2, torch.bfloat16), (300, 513, torch.bfloat16), (2500, 1024, torch.bfloat16),
          (64, 2047, torch.float32), (1030, 515, torch.float32), (9, 8200, torch.bfloat16),
-         (7, 16384, torch.float32), (3, 40001, torch.bfloat16), (2, 33000, torch.float32)]
+         (7, 16384, torch.float32), (3, 40001, torch.bfloat16), (2, 33000, torch.float32),
+         # rows that share a workgroup: 16, 8, 4 and 2 of them, the last one part filled
+         (1, 64, torch.bfloat16), (1003, 128, torch.bfloat16), (20011, 100, torch.bfloat16),
+         (333, 200, torch.bfloat16), (70, 60, torch.float32), (9001, 121, torch.float32),
+         (1001, 250, torch.float32), (517, 511, torch.bfloat16), (45, 1000, torch.bfloat16),
+         (4099, 512, torch.float32)]
 
 
 @pytest.mark.parametrize("N,H,dt", CASES)
