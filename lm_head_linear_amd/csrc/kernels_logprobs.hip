@@ -70,7 +70,7 @@ struct LpOut {
   float* zmax;                // 64-row tiles: the largest raw logit
   float* z;                   //   and all of them, [token][vocabulary]; null: not wanted
   int64_t sp, st, cl, ck, ct;
-  int kc;
+  int kc, top_k;
 };
 
 // x summed over the lanes of this column with a smaller g (lane / 16).
@@ -89,13 +89,13 @@ __device__ __forceinline__ int before_rows(int x, int g) {
 // The accumulators are raw logits, tile rows vocabulary ids, columns tokens (see
 // EpiLse for the layout). The two waves of a column join their (m, s, d) through
 // LDS; each wave leaves candidates of its own 128 rows. A candidate has to exceed
-// tau, the token's kc-th largest logit among lower ids: an equal one with a higher
+// tau, the token's top_k-th largest logit among lower ids: an equal one with a higher
 // id could not be listed either. Few do, so the wave counts them and stores them in
 // any order. Without a tau yet, or with more of them than the list holds, it looks for
-// a bound that exactly kc exceed. Where that fails (equal logits at the bound) the
-// column's kc largest are taken in rounds: the largest logit left, lowest row first,
-// in the four lanes that hold the column; a wave stops when none of its 16 columns
-// has one.
+// a bound that top_k to kc exceed (top_k > 8). Where that fails (equal logits at the
+// bound) or does not pay, the column's top_k largest are taken in rounds: the largest
+// logit left, lowest row first, in the four lanes that hold the column; a wave stops
+// when none of its 16 columns has one.
 template <bool SOFTCAP, bool TOPK>
 struct EpiLp {
   const int64_t* labels;      // null: no given tokens
@@ -213,11 +213,11 @@ struct EpiLp {
         n = rows_all(own, AddOp());
         bool fits = n <= out.kc || t >= N;
         rounds = __ballot(!fits) != 0;
-        if (rounds && out.kc > 8) {
-          // a bound that exactly kc logits exceed, by bisection between the column's
-          // smallest and largest: about a dozen counts, cheaper than more than 8
-          // rounds (20 of them 156 us a launch of 62 tiles, this 110 us; 5 of them 69,
-          // this 87)
+        if (rounds && out.top_k > 8) {
+          // a bound that top_k to kc logits exceed, by bisection between the column's
+          // smallest and largest: a few counts, cheaper than more than 8 rounds (2000
+          // rows of 1024 over 32000, 20 alternatives: 332 us with a bound that exactly
+          // 20 exceed, 278 with 20 to 32; 4 alternatives: 86 us by rounds, 92 so)
           float lo = INFINITY, hi = -INFINITY;
 #pragma unroll
           for (int i = 0; i < 8; ++i)
@@ -228,14 +228,15 @@ struct EpiLp {
             }
           hi = col_max4(hi);
           lo = -col_max4(-lo);
-          float part = 0.8f;                         // kc of 128 lie high in the range
+          // where the bound lies in the range of 128 normal values
+          float part = 0.86f - 0.00375f * float(out.top_k + out.kc);
 #pragma unroll 1
           for (int it = 0; it < 16 && __ballot(!fits) != 0; ++it) {
             const float mid = fmaf(part, hi - lo, lo);
             part = 0.5f;
             const int c = above(mid), total = rows_all(c, AddOp());
             if (!fits) {
-              if (total == out.kc) { fits = true; th = mid; own = c; n = total; }
+              if (total >= out.top_k && total <= out.kc) { fits = true; th = mid; own = c; n = total; }
               else if (total > out.kc) lo = mid;
               else hi = mid;
             }
@@ -258,7 +259,7 @@ struct EpiLp {
       if (rounds) {
         th = tau ? tau_t[col] : -INFINITY;
 #pragma unroll 1
-        for (n = 0; n < out.kc; ++n) {
+        for (n = 0; n < out.top_k; ++n) {
           float bq[4];
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
@@ -1591,7 +1592,7 @@ hipError_t logprobs(const LpPlan& q, const LpArgs& a, char* ws, const Launcher& 
             reinterpret_cast<float*>(ws + q.off_zt), reinterpret_cast<float*>(ws + q.off_cv),
             reinterpret_cast<uint8_t*>(ws + q.off_ci), reinterpret_cast<float*>(ws + q.off_zmax),
             q.top_k && !q.tiles ? reinterpret_cast<float*>(ws + q.off_z) : nullptr,
-            q.sp, q.st, q.cl, q.ck, q.ct, int(q.kc)};
+            q.sp, q.st, q.cl, q.ck, q.ct, int(q.kc), q.top_k};
   JoinArgs j{out, q.parts, 0, q.lists, q.list_rows, a.V, a.N, nullptr, nullptr, a.tokens,
              a.ignore_index, q.top_k, warp, a.logp, a.entropy, a.lse, a.top_logp, a.top_ids,
              nullptr, nullptr};

@@ -105,7 +105,7 @@ bool make_lp_plan(int64_t N, int64_t H, int64_t V, int dtype, int top_k, bool to
   if (q.tiles) {
     q.list_rows = kTileBF16 / 2;
     q.lists = ceil_div(V, q.list_rows);
-    q.kc = top_k;
+    q.kc = lp_candidates(top_k);
   }
   if (top_k > 0) {
     const int64_t per_token = q.tiles ? q.lists * q.kc * 5 : V * 4;

@@ -119,6 +119,10 @@ constexpr int64_t kLpMaxTopV = int64_t(64) * 1024 * kLpRows;
 constexpr int64_t kLpListBytes = int64_t(1) << 30;
 constexpr int64_t kLpMaxChunk = 8192;
 
+// Candidates that a list of 128 vocabulary rows holds: for more than 8 as many as the
+// join's registers take, which saves the tiles a search for exactly top_k.
+inline int64_t lp_candidates(int top_k) { return top_k <= 8 ? top_k : top_k <= 16 ? 16 : 32; }
+
 struct LpPlan {
   Plan p;                     // sizes (H padded), the gather's blocks; its offsets are not used
   bool few = false;           // the few-token kernel
@@ -126,8 +130,8 @@ struct LpPlan {
   bool gather = false;        // live tokens first (bf16 tiles with tokens given)
   int top_k = 0;
   // Partials: per part_rows vocabulary rows and token the max, sum and weighted
-  // sum. Candidates, 256 x 256 tiles: per list_rows rows and token the kc largest
-  // logits, sorted; otherwise the largest logit per part and all logits.
+  // sum. Candidates, 256 x 256 tiles: per list_rows rows and token up to kc of the
+  // largest logits; otherwise the largest logit per part and all logits.
   int64_t part_rows = 0, parts = 0, list_rows = 0, lists = 0, kc = 0;
   int64_t nc = 0, n_chunks = 0;   // tokens per chunk
   // Elements between parts / tokens, and between lists / candidates / tokens:
@@ -152,16 +156,20 @@ inline int64_t lp_first_tiles(const LpPlan& q, int64_t nt) {
   return 2 * pre <= tv ? pre : 0;
 }
 
-// The plan of the backward: the head's, with more K segments of dH for few tokens.
-// One 256-row tile of tokens makes ceil(H / 256) dH tiles with a K of the whole chunk:
-// the head's four segments leave each a long loop on an idle chip (3 rows, 43742 x 178:
-// 182 us against 20). False for invalid sizes.
+// The plan of the backward: the head's, with more K segments of dH where dH has up to
+// 16 tiles, each of which would otherwise run a long loop over the chunk's vocabulary
+// beside the many short ones of dW. us of a training step with the head's segments (at
+// most four) and with 128 / tiles: 3 tokens of 178 over 43742 (1 tile) 260 and 108, 500
+// of 512 over 131072 (4) 815 and 407, 300 of 1024 over 32000 (8) 251 and 183, 1000 of
+// 1024 over 32000 (16) 317 and 293; with 256 / tiles the last two take 197 and 355, and
+// 32 tiles lose (300 of 4096 over 32000: 482 and 526). False for invalid sizes.
 inline bool make_lp_backward_plan(int64_t N, int64_t H, int64_t V, int dtype, int grad_dtype,
                                   Plan* p) {
   if (!make_plan(N, H, V, dtype, p, true, grad_dtype)) return false;
-  if (p->dtype != kBF16 || p->g_parts != 1 || N <= 0 || N > kTileBF16) return true;
-  const int64_t tiles = (p->H + kTileBF16 - 1) / kTileBF16;
-  int64_t segs = 256 / tiles < 32 ? 256 / tiles : 32;
+  if (p->dtype != kBF16 || p->g_parts != 1 || N <= 0) return true;
+  const int64_t tiles = p->n_tok_tiles * ((p->H + kTileBF16 - 1) / kTileBF16);
+  if (tiles > 16) return true;
+  int64_t segs = 128 / tiles < 32 ? 128 / tiles : 32;
   if (segs > p->vchunk / 512) segs = p->vchunk / 512;
   if (segs <= p->dh_segs) return true;
   p->dh_kseg = ((p->vchunk + segs - 1) / segs + 63) / 64 * 64;

@@ -112,6 +112,7 @@ FORWARD = [(1, 64, 1, BF, 3), (1, 4096, 5000, BF, 8), (2, 33, 63, BF, 32), (15, 
            (64, 512, 999, BF, 32), (65, 512, 999, BF, 10), (65, 41, 130, BF, 32), (40, 130, 515, BF, 4),
            (128, 258, 1001, BF, 3), (100, 385, 333, BF, 17), (129, 512, 999, BF, 10),
            (140, 41, 130, BF, 32),
+           (200, 64, 9000, BF, 9), (150, 64, 5000, BF, 17), (600, 72, 40000, BF, 20),
            (300, 136, 2000, BF, 7), (513, 72, 255, BF, 3), (700, 520, 3001, BF, 0),
            (1, 64, 1, F, 2), (3, 77, 200, F, 6), (64, 33, 64, F, 20), (65, 515, 1001, F, 32),
            (257, 130, 333, F, 0)]
@@ -270,6 +271,25 @@ def test_backward(N, H, V, dt, cap, T, parts, monkeypatch):
                                           grad_dtype=torch.float32, **kw)
         gu.assert_grad("dH f32", eH, ref["dH"].cpu().numpy(), 1e-4)
         gu.assert_grad("dW f32", eW, ref["dW"].cpu().numpy(), 1e-4)
+
+
+@pytest.mark.parametrize("N,H", [(5, 72), (129, 136), (300, 133), (800, 600), (1500, 64)])
+@pytest.mark.parametrize("chunk", ["0", "4096"])
+def test_backward_with_split_dH(N, H, chunk, monkeypatch):
+    """dH summed from many segments of a chunk's vocabulary, of one chunk and of three,
+    the last of which leaves segments empty."""
+    import lm_head_linear_amd as m
+    monkeypatch.setenv("FLCE_VCHUNK", chunk)
+    h, W, y, a, b = make(N, H, 9000, BF, seed=8)
+    r = m.flce_logprobs(h, W, y)
+    need = m.flce_logprobs_backward_workspace_size(N, H, 9000, BF)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    dH, dW = m.flce_logprobs_backward(h, W, y, r.lse, r.entropy, a, b, workspace=ws)
+    ref = reference(h, W, y, 0, 0.0, 1.0, a, b)
+    gu.assert_grad("dH", dH, ref["dH"].cpu().numpy(), gu.GRAD_TOL[BF])
+    gu.assert_grad("dW", dW, ref["dW"].cpu().numpy(), gu.GRAD_TOL[BF])
+    again = m.flce_logprobs_backward(h, W, y, r.lse, r.entropy, a, b)
+    assert torch.equal(dH, again[0]) and torch.equal(dW, again[1])
 
 
 @pytest.mark.parametrize("H", [128, 133])
