@@ -1,7 +1,8 @@
 // Embedding lookup with scaling, out_i = round(scale W[tok_i]), and its
 // gradient dW[v] (+)= round(scale sum of dout_i over tok_i = v).
 //
-// The lookup reads and writes a row per token and is bound by that.
+// The lookup reads and writes a row per token and is bound by that (bf16, 16384 rows of
+// 4096 of a table of 131072, frequent ids repeated: 40 us, 268 MB).
 //
 // The gradient sorts the tokens (stable, so equal ids keep their order), and the
 // rows of 64 or 256 sorted tokens are then added up over a slice of columns by a
@@ -19,6 +20,11 @@
 // the keys of each other chunk that go before it. More tokens go through one
 // histogram, scan and scatter pass per digit over many workgroups. (One
 // workgroup sorting 16384 tokens in LDS by itself took 163 us.)
+//
+// The gradient is bound by writing dW and reading dout. The same 16384 rows: 9 us for
+// the chunks, 168 us for the merge, which clears the 1.07 GB of dW beside it (6.4 TB/s),
+// 62 us for the sums and 5 us for the ids that cross windows. Added to a dW that is
+// there, the clearing falls away.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>

@@ -22,6 +22,11 @@
 // kernels of 64 vocabulary rows store the logits of their few tokens (N V 4 bytes
 // next to the V H 2 of W) and each tile's largest; the join then looks only into
 // the top_k tiles of the largest, which hold all top_k alternatives.
+//
+// Measured: 6144 live rows of 4096 over 131072 with 8 alternatives 4.88 ms in the tiles
+// (1352 TFLOP/s; 3690 rows without alternatives 2.90 ms, 1369 TFLOP/s); one row over
+// the same table 199 us (5.4 TB/s); float32 512 rows of 1024 over 32000 303 us (111
+// TFLOP/s, where the library's product of that type reaches 138).
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -557,9 +562,11 @@ __global__ __launch_bounds__(256) void k_lp_few(const uint16_t* __restrict__ h,
 
 // ---- float32 --------------------------------------------------------------------------
 // 64 vocabulary rows x 64 tokens a workgroup, a wave 32 x 32 of it in 2 x 2 blocks
-// of v_mfma_f32_16x16x4_f32. Both operands go through LDS in 32-k chunks, the next
-// chunk loaded while one is multiplied; a lane reads four k of a row at once and
-// feeds them to four instructions (both operands in the same order).
+// of v_mfma_f32_16x16x4_f32 (32 tokens: a wave 32 x 16). Both operands go through LDS
+// in 32-k chunks, two halves in turn, loaded two chunks early without conditions (see
+// the few tokens' loads); a lane reads four k of a row at once and feeds them to four
+// instructions (both operands in the same order). Bound by the matrix instruction where
+// the tiles fill the chip, otherwise by one tile's latency.
 constexpr int kF32Ld = 36;                         // floats per row of a chunk in LDS
 constexpr int kZLd = 68;
 
@@ -897,7 +904,8 @@ __global__ __launch_bounds__(JT * G) void k_lp_join(JoinArgs a) {
 // top_k of the tiles before. Of its keys those from a bound up are kept, the top_k-th
 // largest of the 32 threads' largest, and each counts the larger ones. A list that
 // overflows is filled again with just the keys from its own top_k-th on: that key
-// rises every time.
+// rises every time. 1946 rows over 186 lists with 5 alternatives 13 us, 6144 rows over
+// 1984 lists with 8 49 us.
 constexpr int kSparseTokens = 16, kSparseG = 32, kSparseKeys = 512;
 
 template <bool SOFTCAP>
@@ -1032,7 +1040,9 @@ __global__ __launch_bounds__(512) void k_lp_join_sparse(JoinArgs a) {
 // the top_k groups of the largest keys, so the alternatives are found in two or three
 // selections: of tiles (of threads, each with several tiles, and then of their tiles
 // beyond 2048 tiles), then of the logits of those tiles. A key is a logit's order and
-// then the lower id, so keys are distinct.
+// then the lower id, so keys are distinct. Each selection is a chain of a few barriers
+// and bound by that: 1 row over 2048 tiles with 8 alternatives 12 us, 48 over 4000 tiles
+// with 20 25 us, 257 over 79 tiles with 3 8 us.
 constexpr int kFewThreads = 1024;
 constexpr int kSelMax = 2 * kFewThreads;           // keys of a selection
 
@@ -1363,7 +1373,9 @@ __global__ __launch_bounds__(256) void k_lp_f32_grad(
 //   !DW: C[t][n] = sum_m G^T[m][t] W[m][n]     (K = the chunk's vocabulary rows)
 // B (and for dH also A) is stored with its row contiguous across K: a chunk goes to
 // LDS as [k][64]. A workgroup makes one tile of a segment of K (dH has few tiles and a
-// long K; each segment leaves a partial product of its own).
+// long K; each segment leaves a partial product of its own). Both products run in one
+// grid: 257 x 515 over 5003 46 us (50 in two), 512 x 1024 over 32000 585 us (115
+// TFLOP/s).
 struct F32Product {
   const float* b;
   int64_t M, K, kseg;
