@@ -899,6 +899,139 @@ __global__ __launch_bounds__(JT * G) void k_lp_join(JoinArgs a) {
     }
 }
 
+// Lists of tiles without a tau, more than 8 alternatives (up to 1024 lists): G threads a
+// token, a list each, held in registers (the candidates of a token lie together). The
+// top_k-th largest of the lists' largest keys bounds the alternatives, and at most top_k
+// lists reach it: their keys from the bound up go to LDS, where each counts the larger
+// ones. With 20 alternatives (us, and by sorted lists as above): 529 rows over 308 lists
+// 22 and 112, 272 over 194 13 and 87, 456 over 16 13 and 43.
+struct DenseList {
+  uint64_t group[64];          // the largest key of each G / 64 threads
+  uint64_t bound[2];           // the top_k-th largest of those, and of the threads' keys; or 1
+  int count[2];
+  uint64_t list[kLpTop * kLpTop];
+  uint64_t few[kLpTop * kLpTop / 2];
+  uint64_t won[kLpTop];
+};
+
+template <bool SOFTCAP, int G, int KC>             // kc = KC
+__global__ __launch_bounds__(G < 256 ? 256 : G) void k_lp_join_dense(JoinArgs a) {
+  constexpr int JT = G < 256 ? 256 / G : 1, PER = G / 64;
+  static_assert(KC <= kLpTop && kLpTop * PER <= kLpTop * kLpTop, "the list holds every key");
+  __shared__ DenseList sel[JT];
+  __shared__ float red[3][JT * PER];
+  const int tid = threadIdx.x, tk = tid / G, g = tid % G, w = tid >> 6;
+  const int64_t t = int64_t(blockIdx.x) * JT + tk;
+  int64_t n_live = a.N;
+  if (a.count) { const int64_t c = *a.count; n_live = c < n_live ? c : n_live; }
+  const bool live = t < n_live;
+  const int K = a.top_k;
+  DenseList& st = sel[tk];
+  row_u32x4 rv[KC / 4], ri[KC / 16];
+  bool on = live && g < a.lists;
+  if (on) {
+    const int64_t at = t * a.in.ct + g * a.in.cl;
+#pragma unroll
+    for (int i = 0; i < KC / 4; ++i) rv[i] = load_raw(a.in.cv + at + 4 * i);
+#pragma unroll
+    for (int i = 0; i < KC / 16; ++i) ri[i] = load_raw(a.in.ci + at + 16 * i);
+  }
+  float M = -INFINITY, S = 0.f, D = 0.f;
+  if (live)
+    for (int64_t p = g; p < a.parts; p += G) {
+      const int64_t at = p * a.in.sp + t * a.in.st;
+      const float2 ms = a.in.part[at];
+      join_part(M, S, D, ms.x, ms.y, a.in.pd[at]);
+    }
+  uint64_t key[KC], best = 0;
+#pragma unroll
+  for (int k = 0; k < KC; ++k) {
+    const float v = __uint_as_float(rv[k / 4][k % 4]);
+    on = on && v > -INFINITY;                      // nothing behind the first such place
+    key[k] = on ? rank_key(v, g * a.list_rows + ((ri[k / 16][k / 4 % 4] >> (8 * (k % 4))) & 255))
+                : 0;
+    best = max_u64(best, key[k]);
+  }
+  const float Mw = wave_all(M, MaxOp());
+  const float f = M == -INFINITY ? 0.f : exp2f((M - Mw) * kLog2e);
+  D = wave_all(M == -INFINITY ? 0.f : f * fmaf(M - Mw, S, D), AddOp());
+  S = wave_all(S == 0.f ? 0.f : S * f, AddOp());
+  if ((tid & 63) == 0) { red[0][w] = Mw; red[1][w] = S; red[2][w] = D; }
+  const uint32_t hi = group_all<PER>(uint32_t(best >> 32), MaxOp());
+  const uint32_t lo = group_all<PER>(uint32_t(best >> 32) == hi ? uint32_t(best) : 0u, MaxOp());
+  if (g % PER == 0) st.group[g / PER] = (uint64_t(hi) << 32) | lo;
+  if (g < kLpTop) st.won[g] = 0;
+  if (g < 2) { st.bound[g] = 1; st.count[g] = 0; }
+  __syncthreads();
+  if (g < 64) {
+    const uint64_t x = st.group[g];
+    int larger = 0;
+    for (int i = 0; i < 64; ++i) larger += st.group[i] > x ? 1 : 0;
+    if (x != 0 && larger == K - 1) st.bound[0] = x;
+  }
+  __syncthreads();
+  if (best >= st.bound[0]) st.list[atomicAdd(&st.count[0], 1)] = best;
+  __syncthreads();
+  int n = st.count[0];
+  for (int i = g; i < n; i += G) {
+    const uint64_t x = st.list[i];
+    int larger = 0;
+    for (int o = 0; o < n; ++o) larger += st.list[o] > x ? 1 : 0;
+    if (larger == K - 1) st.bound[1] = x;
+  }
+  __syncthreads();
+  const uint64_t bound = st.bound[1];
+  if (best >= bound) {
+#pragma unroll
+    for (int k = 0; k < KC; ++k)
+      if (key[k] >= bound) st.list[atomicAdd(&st.count[1], 1)] = key[k];
+  }
+  __syncthreads();
+  n = st.count[1];
+  const uint64_t* keys = st.list;
+  if (a.lists < 64) {
+    // few lists leave that bound low (fewer than top_k none at all): the same once more
+    // over the keys in 64 groups, of at most 16
+    if (g < 64) {
+      uint64_t x = 0;
+      for (int i = g; i < n; i += 64) x = max_u64(x, st.list[i]);
+      st.group[g] = x;
+    }
+    if (g == 0) { st.bound[0] = 1; st.count[0] = 0; }
+    __syncthreads();
+    if (g < 64) {
+      const uint64_t x = st.group[g];
+      int larger = 0;
+      for (int i = 0; i < 64; ++i) larger += st.group[i] > x ? 1 : 0;
+      if (x != 0 && larger == K - 1) st.bound[0] = x;
+    }
+    __syncthreads();
+    for (int i = g; i < n; i += G)
+      if (st.list[i] >= st.bound[0]) st.few[atomicAdd(&st.count[0], 1)] = st.list[i];
+    __syncthreads();
+    n = st.count[0];
+    keys = st.few;
+  }
+  for (int i = g; i < n; i += G) {
+    const uint64_t x = keys[i];
+    int larger = 0;
+    for (int o = 0; o < n; ++o) larger += keys[o] > x ? 1 : 0;
+    if (larger < K) st.won[larger] = x;
+  }
+  __syncthreads();
+  if (g >= K || t >= a.N) return;
+  M = -INFINITY; S = 0.f; D = 0.f;
+  for (int i = 0; i < PER; ++i)
+    join_part(M, S, D, red[0][tk * PER + i], red[1][tk * PER + i], red[2][tk * PER + i]);
+  const int64_t o = a.idx ? int64_t(a.idx[t]) : t;
+  const bool shown = live && (!a.labels || a.labels[t] != a.ignore_index);
+  if (g == 0) write_token(a, t, o, shown, M, S, D);
+  const uint64_t x = st.won[g];
+  const bool has = shown && x != 0;
+  write_alternative(a, o, g, has ? warp_logit<SOFTCAP>(a.warp, key_value(x)) : 0.f,
+                    has ? key_id(x) : -1, M, logf(S));
+}
+
 // Many tokens, lists of tiles with a tau, few of which hold anything: 16 tokens a
 // workgroup, 32 threads for each. Every candidate goes to a list in LDS, with the
 // top_k of the tiles before. Of its keys those from a bound up are kept, the top_k-th
@@ -1543,8 +1676,28 @@ bool f32_narrow(int64_t N, int64_t V) {
   return (N - 1) % 64 < 32 || ((N + 63) / 64) * ((V + 63) / 64) <= 256;
 }
 
+template <bool SOFTCAP>
+hipError_t run_join_dense(const LpPlan& q, const JoinArgs& j, const Launcher& L) {
+  auto run = [&](auto g, auto kc) {
+    constexpr int G = decltype(g)::value, T = G < 256 ? 256 : G;
+    hipLaunchKernelGGL((k_lp_join_dense<SOFTCAP, G, decltype(kc)::value>),
+                       dim3(cdiv(j.N, T / G)), dim3(T), 0, L.stream, j);
+  };
+  if (q.lists > 1024) return hipErrorInvalidValue;
+  auto by_kc = [&](auto g) { q.kc == 16 ? run(g, Int<16>{}) : run(g, Int<32>{}); };
+  L.pre(kLpJoin);
+  if (q.lists <= 128) by_kc(Int<128>{});
+  else if (q.lists <= 256) by_kc(Int<256>{});
+  else if (q.lists <= 512) by_kc(Int<512>{});
+  else by_kc(Int<1024>{});
+  L.post(kLpJoin);
+  return hipGetLastError();
+}
+
 template <bool SOFTCAP, bool TAU_ONLY>
 hipError_t run_join(const LpPlan& q, const JoinArgs& j, const Launcher& L) {
+  // lists without a tau and more than 8 alternatives go to run_join_dense
+  if (!TAU_ONLY && q.tiles && !j.first && j.top_k > 8) return hipErrorInvalidValue;
   L.pre(kLpJoin);
   if (!q.tiles) {
     hipLaunchKernelGGL(k_lp_join_few<SOFTCAP>, dim3(unsigned(j.N)), dim3(kFewThreads), 0,
@@ -1561,8 +1714,10 @@ hipError_t run_join(const LpPlan& q, const JoinArgs& j, const Launcher& L) {
     auto by_k = [&](auto jt) {
       if (j.top_k <= 1) run(jt, Int<1024>{}, Int<1>{});
       else if (j.top_k <= 8) run(jt, Int<1024>{}, Int<8>{});
-      else if (j.top_k <= 16) run(jt, Int<1024>{}, Int<16>{});
-      else run(jt, Int<512>{}, Int<kLpTop>{});
+      else if constexpr (TAU_ONLY) {
+        if (j.top_k <= 16) run(jt, Int<1024>{}, Int<16>{});
+        else run(jt, Int<512>{}, Int<kLpTop>{});
+      }
     };
     if (j.N >= 4096) by_k(Int<32>{});
     else if (j.N >= 1024) by_k(Int<16>{});
@@ -1688,6 +1843,13 @@ hipError_t logprobs(const LpPlan& q, const LpArgs& a, char* ws, const Launcher& 
     } else {
       at_token(jc, t0);
     }
+    const int64_t pre = lp_first_tiles(q, jc.N);
+    // More than 8 alternatives without such a group (then there are fewer than 512 tiles,
+    // 1024 lists): the candidates of a token lie together, for k_lp_join_dense.
+    const bool dense = pre == 0 && q.top_k > 8;
+    LpOut to = out;
+    if (dense) to.cl = q.kc, to.ck = 1, to.ct = q.lists * q.kc;
+    jc.in = to;
     // vocabulary rows [v0, v1) of the chunk's live tokens
     auto tiles = [&](int64_t v0, int64_t v1, const float* tau) {
       gemm::Launch l = gemm::forward_launch(p);
@@ -1700,13 +1862,12 @@ hipError_t logprobs(const LpPlan& q, const LpArgs& a, char* ws, const Launcher& 
                         : run_gemm<NF, NF>(l, ag, epi, kLpTiles, L);
       };
       if (q.top_k > 0)
-        return run(EpiLp<SOFTCAP, true>{jc.labels, jc.N, a.V, v0, warp, out, tau});
-      return run(EpiLp<SOFTCAP, false>{jc.labels, jc.N, a.V, v0, warp, out, nullptr});
+        return run(EpiLp<SOFTCAP, true>{jc.labels, jc.N, a.V, v0, warp, to, tau});
+      return run(EpiLp<SOFTCAP, false>{jc.labels, jc.N, a.V, v0, warp, to, nullptr});
     };
     // Alternatives: the first tiles of the vocabulary alone, whole rounds of the
     // chip, give every token a bound tau that few logits of the others exceed;
     // their epilogues then have next to nothing to extract.
-    const int64_t pre = lp_first_tiles(q, jc.N);
     if (pre > 0) {
       jc.tau = reinterpret_cast<float*>(ws + q.off_tau);
       jc.first = reinterpret_cast<uint64_t*>(ws + q.off_first);
@@ -1719,7 +1880,8 @@ hipError_t logprobs(const LpPlan& q, const LpArgs& a, char* ws, const Launcher& 
     } else {
       e = tiles(0, a.V, nullptr);
     }
-    if (e == hipSuccess) e = run_join<SOFTCAP, false>(q, jc, L);
+    if (e == hipSuccess)
+      e = dense ? run_join_dense<SOFTCAP>(q, jc, L) : run_join<SOFTCAP, false>(q, jc, L);
   }
   return e;
 }
