@@ -533,6 +533,8 @@ def token_logprobs(hidden_states: torch.Tensor, tokens: Optional[torch.Tensor],
     there are no gradients."""
     lead, H = hidden_states.shape[:-1], hidden_states.shape[-1]
     h, W = hidden_states.reshape(-1, H).contiguous(), lm_weight.contiguous()
+    if h.data_ptr() % 16:                # a slice that starts inside odd rows
+        h = h.clone()
     y = None if tokens is None else tokens.reshape(-1).contiguous()
     if y is None or not torch.is_grad_enabled() or not (h.requires_grad or W.requires_grad):
         out = flce_logprobs(h.detach(), W.detach(), y, ignore_index=ignore_index, softcap=softcap,

@@ -171,7 +171,7 @@ inline bool make_lp_backward_plan(int64_t N, int64_t H, int64_t V, int dtype, in
   if (tiles > 16) return true;
   int64_t segs = 128 / tiles < 32 ? 128 / tiles : 32;
   if (segs > p->vchunk / 512) segs = p->vchunk / 512;
-  if (segs <= p->dh_segs) return true;
+  if (segs <= 1 || segs <= p->dh_segs) return true;
   p->dh_kseg = ((p->vchunk + segs - 1) / segs + 63) / 64 * 64;
   p->dh_segs = (p->vchunk + p->dh_kseg - 1) / p->dh_kseg;
   p->off_dhpart = p->total;                        // behind the head's own buffers

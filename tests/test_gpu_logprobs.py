@@ -115,6 +115,7 @@ FORWARD = [(1, 64, 1, BF, 3), (1, 4096, 5000, BF, 8), (2, 33, 63, BF, 32), (15, 
            (200, 64, 9000, BF, 9), (150, 64, 5000, BF, 17), (600, 72, 40000, BF, 20),
            (200, 64, 20000, BF, 12), (140, 64, 70000, BF, 32),
            (300, 136, 2000, BF, 7), (513, 72, 255, BF, 3), (700, 520, 3001, BF, 0),
+           (3, 1, 70, BF, 2), (130, 3, 300, BF, 5), (5, 1, 70, F, 2),
            (1, 64, 1, F, 2), (3, 77, 200, F, 6), (64, 33, 64, F, 20), (65, 515, 1001, F, 32),
            (257, 130, 333, F, 0)]
 

@@ -135,6 +135,22 @@ def test_decoding_one_token_at_a_time():
         assert last.logp is None and last.top_ids.shape == (2, 2)
 
 
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+def test_a_slice_of_odd_rows(dt):
+    """Rows from the middle of a batch of odd width start at any element."""
+    import lm_head_linear_amd as m
+    torch.manual_seed(2)
+    W = (0.1 * torch.randn(700, 37, device="cuda")).to(dt)
+    x = torch.randn(9, 37, device="cuda").to(dt).requires_grad_()
+    y = torch.randint(0, 700, (9,), device="cuda")
+    a = m.token_logprobs(x[2:7], y[2:7], W, top_k=2)
+    b = m.token_logprobs(x[2:7].clone(), y[2:7].clone(), W, top_k=2)
+    assert torch.equal(a.logp, b.logp) and torch.equal(a.top_ids, b.top_ids)
+    (g,) = torch.autograd.grad(a.logp.sum(), x)
+    (h,) = torch.autograd.grad(b.logp.sum(), x)
+    assert torch.equal(g, h) and not bool(g[:2].any()) and bool(g[2:7].any())
+
+
 def test_two_streams_at_once():
     """The same calls on two streams, each with workspaces of its own, and one of them
     made current only for the call."""
