@@ -109,7 +109,7 @@ struct EpiLp {
   LpOut out;
   const float* tau;           // TOPK; null: -inf
 
-  static constexpr int kTokBytes = 3072;
+  static constexpr int kTokBytes = 3 * 1024;
   __device__ __forceinline__ void stage(char* tok, int64_t n0, int wave, int lane) const {
     if (labels) stage_tokens<2>(tok, labels, n0, N, wave, lane);
     if (TOPK && tau) stage_tokens<1>(tok + 2048, tau, n0, N, wave, lane);
@@ -770,13 +770,13 @@ __device__ __forceinline__ float key_value(uint64_t k) {
 __device__ __forceinline__ int64_t key_id(uint64_t k) { return int64_t(uint32_t(~uint32_t(k))); }
 __device__ __forceinline__ uint64_t max_u64(uint64_t a, uint64_t b) { return a > b ? a : b; }
 
-// Many tokens, lists of tiles without a tau: JT tokens a workgroup and G threads for
-// each, thread g taking every G-th part and list, then the threads pairwise. A thread
-// keeps its KM largest keys sorted in registers; two threads' lists meet as a bitonic
-// sequence, through LDS, which bounds the threads (64 KiB at 16 keys of 1024, or 32
-// keys of 512). 32 tokens read whole lines of every list; below 4096 tokens that
-// leaves most CUs idle, and 16 (below 1024: 4) tokens a workgroup are faster. With
-// TAU_ONLY just the lists so far: the top_k keys, and the top_k-th largest logit.
+// Many tokens, all parts with at most one candidate a list, or (TAU_ONLY) the lists of
+// the first tiles, for a token's top_k keys and its top_k-th largest logit. JT tokens a
+// workgroup and G threads for each, thread g taking every G-th part and list, then the
+// threads pairwise. A thread keeps its KM largest keys sorted in registers; two threads'
+// lists meet as a bitonic sequence, through LDS, which bounds the threads (64 KiB at 16
+// keys of 1024, or 32 keys of 512). 32 tokens read whole lines of every list; below 4096
+// tokens that leaves most CUs idle, and 16 (below 1024: 4) tokens a workgroup are faster.
 constexpr int kAhead = 4;                          // loads in flight
 
 template <int KM>
@@ -899,12 +899,13 @@ __global__ __launch_bounds__(JT * G) void k_lp_join(JoinArgs a) {
     }
 }
 
-// Lists of tiles without a tau, more than 8 alternatives (up to 1024 lists): G threads a
+// Lists of tiles without a tau, more than one alternative (up to 1024 lists): G threads a
 // token, a list each, held in registers (the candidates of a token lie together). The
 // top_k-th largest of the lists' largest keys bounds the alternatives, and at most top_k
 // lists reach it: their keys from the bound up go to LDS, where each counts the larger
 // ones. With 20 alternatives (us, and by sorted lists as above): 529 rows over 308 lists
-// 22 and 112, 272 over 194 13 and 87, 456 over 16 13 and 43.
+// 22 and 112, 272 over 194 13 and 87, 456 over 16 13 and 43; with 4 the whole call of
+// 300 rows over 250 lists 80 and 85.
 struct DenseList {
   uint64_t group[64];          // the largest key of each G / 64 threads
   uint64_t bound[2];           // the top_k-th largest of those, and of the threads' keys; or 1
@@ -927,14 +928,15 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void k_lp_join_dense(JoinArgs a)
   const bool live = t < n_live;
   const int K = a.top_k;
   DenseList& st = sel[tk];
-  row_u32x4 rv[KC / 4], ri[KC / 16];
+  row_u32x4 rv[KC / 4];
+  uint32_t ri[KC / 4];
   bool on = live && g < a.lists;
   if (on) {
     const int64_t at = t * a.in.ct + g * a.in.cl;
 #pragma unroll
     for (int i = 0; i < KC / 4; ++i) rv[i] = load_raw(a.in.cv + at + 4 * i);
 #pragma unroll
-    for (int i = 0; i < KC / 16; ++i) ri[i] = load_raw(a.in.ci + at + 16 * i);
+    for (int i = 0; i < KC / 4; ++i) ri[i] = reinterpret_cast<const uint32_t*>(a.in.ci + at)[i];
   }
   float M = -INFINITY, S = 0.f, D = 0.f;
   if (live)
@@ -948,7 +950,7 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void k_lp_join_dense(JoinArgs a)
   for (int k = 0; k < KC; ++k) {
     const float v = __uint_as_float(rv[k / 4][k % 4]);
     on = on && v > -INFINITY;                      // nothing behind the first such place
-    key[k] = on ? rank_key(v, g * a.list_rows + ((ri[k / 16][k / 4 % 4] >> (8 * (k % 4))) & 255))
+    key[k] = on ? rank_key(v, g * a.list_rows + ((ri[k / 4] >> (8 * (k % 4))) & 255))
                 : 0;
     best = max_u64(best, key[k]);
   }
@@ -1343,7 +1345,7 @@ struct EpiLpGrad {
   __device__ __forceinline__ void stage(char* tok, int64_t n0, int wave, int lane) const {
     stage_tokens<2>(tok, labels, n0, N, wave, lane);
     stage_tokens<1>(tok + 2048, lse, n0, N, wave, lane);
-    stage_tokens<1>(tok + 3072, c0, n0, N, wave, lane);
+    stage_tokens<1>(tok + 3 * 1024, c0, n0, N, wave, lane);
     stage_tokens<1>(tok + 4096, c1, n0, N, wave, lane);
     stage_tokens<1>(tok + 5120, ca, n0, N, wave, lane);
   }
@@ -1352,7 +1354,7 @@ struct EpiLpGrad {
                                              int lane, char* smem, const char* tok) const {
     const int64_t* lab = reinterpret_cast<const int64_t*>(tok);
     const float* lse_t = reinterpret_cast<const float*>(tok + 2048);
-    const float* c0_t = reinterpret_cast<const float*>(tok + 3072);
+    const float* c0_t = reinterpret_cast<const float*>(tok + 3 * 1024);
     const float* c1_t = reinterpret_cast<const float*>(tok + 4096);
     const float* ca_t = reinterpret_cast<const float*>(tok + 5120);
     const int lg = lane >> 4;
@@ -1684,7 +1686,11 @@ hipError_t run_join_dense(const LpPlan& q, const JoinArgs& j, const Launcher& L)
                        dim3(cdiv(j.N, T / G)), dim3(T), 0, L.stream, j);
   };
   if (q.lists > 1024) return hipErrorInvalidValue;
-  auto by_kc = [&](auto g) { q.kc == 16 ? run(g, Int<16>{}) : run(g, Int<32>{}); };
+  auto by_kc = [&](auto g) {
+    if (q.kc == 8) run(g, Int<8>{});
+    else if (q.kc == 16) run(g, Int<16>{});
+    else run(g, Int<32>{});
+  };
   L.pre(kLpJoin);
   if (q.lists <= 128) by_kc(Int<128>{});
   else if (q.lists <= 256) by_kc(Int<256>{});
@@ -1696,8 +1702,8 @@ hipError_t run_join_dense(const LpPlan& q, const JoinArgs& j, const Launcher& L)
 
 template <bool SOFTCAP, bool TAU_ONLY>
 hipError_t run_join(const LpPlan& q, const JoinArgs& j, const Launcher& L) {
-  // lists without a tau and more than 8 alternatives go to run_join_dense
-  if (!TAU_ONLY && q.tiles && !j.first && j.top_k > 8) return hipErrorInvalidValue;
+  // lists without a tau and more than one alternative go to run_join_dense
+  if (!TAU_ONLY && q.tiles && !j.first && j.top_k > 1) return hipErrorInvalidValue;
   L.pre(kLpJoin);
   if (!q.tiles) {
     hipLaunchKernelGGL(k_lp_join_few<SOFTCAP>, dim3(unsigned(j.N)), dim3(kFewThreads), 0,
@@ -1713,9 +1719,9 @@ hipError_t run_join(const LpPlan& q, const JoinArgs& j, const Launcher& L) {
     };
     auto by_k = [&](auto jt) {
       if (j.top_k <= 1) run(jt, Int<1024>{}, Int<1>{});
-      else if (j.top_k <= 8) run(jt, Int<1024>{}, Int<8>{});
       else if constexpr (TAU_ONLY) {
-        if (j.top_k <= 16) run(jt, Int<1024>{}, Int<16>{});
+        if (j.top_k <= 8) run(jt, Int<1024>{}, Int<8>{});
+        else if (j.top_k <= 16) run(jt, Int<1024>{}, Int<16>{});
         else run(jt, Int<512>{}, Int<kLpTop>{});
       }
     };
@@ -1844,10 +1850,12 @@ hipError_t logprobs(const LpPlan& q, const LpArgs& a, char* ws, const Launcher& 
       at_token(jc, t0);
     }
     const int64_t pre = lp_first_tiles(q, jc.N);
-    // More than 8 alternatives without such a group (then there are fewer than 512 tiles,
-    // 1024 lists): the candidates of a token lie together, for k_lp_join_dense.
-    const bool dense = pre == 0 && q.top_k > 8;
+    // More than one alternative without such a group (then there are fewer than 512
+    // tiles, 1024 lists): the candidates of a token lie together, for k_lp_join_dense.
+    // Otherwise up to 8 are all that the join reads of a list.
+    const bool dense = pre == 0 && q.top_k > 1;
     LpOut to = out;
+    if (!dense && q.top_k <= 8) to.kc = q.top_k;
     if (dense) to.cl = q.kc, to.ck = 1, to.ct = q.lists * q.kc;
     jc.in = to;
     // vocabulary rows [v0, v1) of the chunk's live tokens

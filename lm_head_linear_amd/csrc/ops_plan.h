@@ -119,9 +119,12 @@ constexpr int64_t kLpMaxTopV = int64_t(64) * 1024 * kLpRows;
 constexpr int64_t kLpListBytes = int64_t(1) << 30;
 constexpr int64_t kLpMaxChunk = 8192;
 
-// Candidates that a list of 128 vocabulary rows holds: for more than 8 as many as the
-// join's registers take, which saves the tiles a search for exactly top_k.
-inline int64_t lp_candidates(int top_k) { return top_k <= 8 ? top_k : top_k <= 16 ? 16 : 32; }
+// Candidates that a list of 128 vocabulary rows has room for, as many as the joins'
+// registers take: for more than 8 alternatives it saves the tiles a search for exactly
+// top_k.
+inline int64_t lp_candidates(int top_k) {
+  return top_k <= 1 ? top_k : top_k <= 8 ? 8 : top_k <= 16 ? 16 : 32;
+}
 
 struct LpPlan {
   Plan p;                     // sizes (H padded), the gather's blocks; its offsets are not used
