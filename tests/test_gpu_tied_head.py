@@ -182,3 +182,75 @@ def test_two_streams_at_once():
     for i in range(2):
         for g in got[i]:
             assert all(torch.equal(p, q) for p, q in zip(g, want[i]))
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+def test_a_captured_training_step(dt):
+    """Embedding, norm, loss, log probabilities and all their gradients in one graph,
+    recorded with no eager autograd graph of the parameters alive."""
+    t = head(dt)
+    x, y = batch()
+    c = torch.randn(2, 70, device="cuda")
+
+    def step():
+        e = t.embed(x)
+        loss = t.loss(torch.tanh(e), y, residual=e)
+        r = t.logprobs(torch.tanh(e), y, residual=e, top_k=3)
+        out = loss + (r.logp * c).sum()
+        out.backward()
+        return out.detach(), r.top_ids, r.lse
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            t.zero_grad(set_to_none=True)
+            want = [v.clone() for v in step()] + [p.grad.clone() for p in t.parameters()]
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    t.zero_grad(set_to_none=True)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        outs = step()
+    got = [*outs, *(p.grad for p in t.parameters())]
+    for _ in range(3):
+        for v in got:
+            v.fill_(7)
+        torch.randn(300, 300, device="cuda").sum()
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_two_graphs_with_one_workspace():
+    """Graphs of different calls that share their workspace, replayed in turn."""
+    import lm_head_linear_amd as m
+    torch.manual_seed(6)
+    W = (0.1 * torch.randn(3000, 64, device="cuda")).bfloat16()
+    need = max(m.flce_logprobs_workspace_size(n, 64, 3000, torch.bfloat16, 9) for n in (12, 300))
+    need = max(need, m.flce_embedding_backward_workspace_size(300, 64, 3000))
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    jobs = []
+    for n in (12, 300):
+        h = torch.randn(n, 64, device="cuda").bfloat16()
+        y = torch.randint(0, 3000, (n,), device="cuda")
+        r = m.flce_logprobs(h, W, y, top_k=9, workspace=ws)
+        dW = m.flce_embedding_backward(y, h, 3000, workspace=ws)
+        kw = dict(logp=r.logp, entropy=r.entropy, lse=r.lse, top_logp=r.top_logp,
+                  top_ids=r.top_ids)
+        torch.cuda.synchronize()
+        want = [v.clone() for v in (*r, dW)]
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            m.flce_logprobs(h, W, y, top_k=9, workspace=ws, **kw)
+            m.flce_embedding_backward(y, h, 3000, dW=dW, workspace=ws)
+        jobs.append((g, [*r, dW], want, (h, y)))
+    for _ in range(3):
+        for g, got, want, _ in jobs:
+            for v in got:
+                v.fill_(5)
+            g.replay()
+        torch.cuda.synchronize()
+        for g, got, want, _ in jobs:
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
