@@ -221,8 +221,8 @@ struct EpiLp {
         if (rounds && out.top_k > 8) {
           // a bound that top_k to kc logits exceed, by bisection between the column's
           // smallest and largest: a few counts, cheaper than more than 8 rounds (2000
-          // rows of 1024 over 32000, 20 alternatives: 332 us with a bound that exactly
-          // 20 exceed, 278 with 20 to 32; 4 alternatives: 86 us by rounds, 92 so)
+          // rows of 1024 over 32000, 20 alternatives: 54 us less than with a bound
+          // that exactly 20 exceed; 300 rows, 4 alternatives: 86 us by rounds, 92 so)
           float lo = INFINITY, hi = -INFINITY;
 #pragma unroll
           for (int i = 0; i < 8; ++i)
@@ -725,7 +725,8 @@ struct JoinArgs {
   float* lse;
   float* top_logp;
   int64_t* top_ids;
-  uint64_t* first;            // top_k keys of the lists before list0, or null
+  uint64_t* first;            // [top_k][first_ld] keys of the lists before list0, or null
+  int64_t first_ld;
   float* tau;
 };
 
@@ -770,50 +771,17 @@ __device__ __forceinline__ float key_value(uint64_t k) {
 __device__ __forceinline__ int64_t key_id(uint64_t k) { return int64_t(uint32_t(~uint32_t(k))); }
 __device__ __forceinline__ uint64_t max_u64(uint64_t a, uint64_t b) { return a > b ? a : b; }
 
-// Many tokens, all parts with at most one candidate a list, or (TAU_ONLY) the lists of
-// the first tiles, for a token's top_k keys and its top_k-th largest logit. JT tokens a
-// workgroup and G threads for each, thread g taking every G-th part and list, then the
-// threads pairwise. A thread keeps its KM largest keys sorted in registers; two threads'
-// lists meet as a bitonic sequence, through LDS, which bounds the threads (64 KiB at 16
-// keys of 1024, or 32 keys of 512). 32 tokens read whole lines of every list; below 4096
-// tokens that leaves most CUs idle, and 16 (below 1024: 4) tokens a workgroup are faster.
+// Many tokens and at most one alternative: all parts and lists, or (TAU_ONLY) the lists
+// of the first tiles, for a token's largest key. JT tokens a workgroup and G threads for
+// each, thread g taking every G-th part and list, then the threads pairwise. 32 tokens
+// read whole lines of every part; below 4096 tokens that leaves most CUs idle, and 16
+// (below 1024: 4) tokens a workgroup are faster.
 constexpr int kAhead = 4;                          // loads in flight
 
-template <int KM>
-struct TopKeys {
-  uint64_t k[KM];
-  __device__ __forceinline__ void exchange(int i, int o, bool down) {
-    const bool swap = down ? k[o] > k[i] : k[i] > k[o];
-    const uint64_t x = k[i];
-    k[i] = swap ? k[o] : x;
-    k[o] = swap ? x : k[o];
-  }
-  __device__ __forceinline__ void sort() {         // bitonic, largest first
-#pragma unroll
-    for (int size = 2; size <= KM; size <<= 1)
-#pragma unroll
-      for (int h = size / 2; h > 0; h >>= 1)
-#pragma unroll
-        for (int i = 0; i < KM; ++i)
-          if (!(i & h)) exchange(i, i + h, (i & size) == 0);
-  }
-  // with another sorted list, b(i) its i-th key
-  template <class Get>
-  __device__ __forceinline__ void merge(Get b) {
-#pragma unroll
-    for (int i = 0; i < KM; ++i) k[i] = max_u64(k[i], b(KM - 1 - i));
-#pragma unroll
-    for (int h = KM / 2; h > 0; h >>= 1)
-#pragma unroll
-      for (int i = 0; i < KM; ++i)
-        if (!(i & h)) exchange(i, i + h, true);
-  }
-};
-
-template <bool SOFTCAP, bool TAU_ONLY, int JT, int G, int KM>     // top_k <= KM
+template <bool SOFTCAP, bool TAU_ONLY, int JT, int G>
 __global__ __launch_bounds__(JT * G) void k_lp_join(JoinArgs a) {
   constexpr int kT = JT * G;
-  __shared__ uint64_t keys[KM * kT / 2];           // [key][thread]
+  __shared__ uint64_t keys[kT / 2];
   __shared__ float4 grp[kT / 2];
   const int tid = threadIdx.x, tk = tid % JT, g = tid / JT;
   const int64_t t = int64_t(blockIdx.x) * JT + tk;
@@ -837,25 +805,12 @@ __global__ __launch_bounds__(JT * G) void k_lp_join(JoinArgs a) {
         if (p + u * G < a.parts) join_part(M, S, D, ms[u].x, ms[u].y, d[u]);
     }
   }
-  TopKeys<KM> top;
-#pragma unroll
-  for (int k = 0; k < KM; ++k) top.k[k] = 0;
+  uint64_t top = 0;
   if (K > 0 && live) {
+#pragma unroll 4
     for (int64_t l = a.list0 + g; l < a.lists; l += G) {
       const int64_t at = l * a.in.cl + t * a.in.ct;
-      TopKeys<KM> list;
-#pragma unroll
-      for (int k = 0; k < KM; ++k) {
-        const bool in = k < a.in.kc;
-        const float v = in ? a.in.cv[at + k * a.in.ck] : -INFINITY;
-        list.k[k] = rank_key(v, l * a.list_rows + (in ? a.in.ci[at + k * a.in.ck] : 0));
-      }
-      // nothing behind the first place without a candidate is one
-#pragma unroll
-      for (int k = 1; k < KM; ++k) list.k[k] = list.k[k - 1] != 0 ? list.k[k] : 0;
-      list.sort();
-      if (l == a.list0 + g) top = list;
-      else top.merge([&](int k) { return list.k[k]; });
+      top = max_u64(top, rank_key(a.in.cv[at], l * a.list_rows + a.in.ci[at]));
     }
   }
   for (int half = G / 2; half > 0; half >>= 1) {
@@ -863,63 +818,56 @@ __global__ __launch_bounds__(JT * G) void k_lp_join(JoinArgs a) {
     const int slot = tid % (half * JT);
     if (g >= half && g < 2 * half) {
       grp[slot] = make_float4(M, S, D, 0.f);
-#pragma unroll
-      for (int k = 0; k < KM; ++k) keys[k * (kT / 2) + slot] = top.k[k];
+      keys[slot] = top;
     }
     __syncthreads();
     if (g < half) {
       const float4 f = grp[slot];
       join_part(M, S, D, f.x, f.y, f.z);
-      if (K > 0) top.merge([&](int k) { return keys[k * (kT / 2) + slot]; });
+      top = max_u64(top, keys[slot]);
     }
     __syncthreads();
   }
   if (g != 0 || t >= a.N) return;
   if (TAU_ONLY) {
-    float last = -INFINITY;
-#pragma unroll
-    for (int k = 0; k < KM; ++k)
-      if (k < K) {
-        a.first[k * a.in.ck + t] = live ? top.k[k] : 0;
-        if (k == K - 1 && live && top.k[k] != 0) last = key_value(top.k[k]);
-      }
-    a.tau[t] = last;
+    a.first[t] = top;                              // 0 of no list
+    a.tau[t] = top != 0 ? key_value(top) : -INFINITY;
     return;
   }
   const int64_t o = a.idx ? int64_t(a.idx[t]) : t;
   const bool shown = live && (!a.labels || a.labels[t] != a.ignore_index);
   write_token(a, t, o, shown, M, S, D);
-  const float ls = logf(S);
-#pragma unroll
-  for (int k = 0; k < KM; ++k)
-    if (k < K) {
-      const bool has = shown && top.k[k] != 0;
-      write_alternative(a, o, k, has ? warp_logit<SOFTCAP>(a.warp, key_value(top.k[k])) : 0.f,
-                        has ? key_id(top.k[k]) : -1, M, ls);
-    }
+  if (K > 0) {
+    const bool has = shown && top != 0;
+    write_alternative(a, o, 0, has ? warp_logit<SOFTCAP>(a.warp, key_value(top)) : 0.f,
+                      has ? key_id(top) : -1, M, logf(S));
+  }
 }
 
-// Lists of tiles without a tau, more than one alternative (up to 1024 lists): G threads a
-// token, a list each, held in registers (the candidates of a token lie together). The
+// Lists of tiles without a tau, more than one alternative (up to 1024 lists; TAU_ONLY:
+// those of the first tiles, for the top_k keys and the top_k-th logit): G threads a token,
+// a list each, held in registers (the candidates of a token lie together). The
 // top_k-th largest of the lists' largest keys bounds the alternatives, and at most top_k
 // lists reach it: their keys from the bound up go to LDS, where each counts the larger
-// ones. With 20 alternatives (us, and by sorted lists as above): 529 rows over 308 lists
-// 22 and 112, 272 over 194 13 and 87, 456 over 16 13 and 43; with 4 the whole call of
-// 300 rows over 250 lists 80 and 85.
+// ones. With 20 alternatives (us, and by sorted lists): 529 rows over 308 lists
+// 22 and 112, 272 over 194 13 and 87, 456 over 16 13 and 43. "Sorted lists": a thread's
+// lists sorted and merged in registers, then the threads' pairwise through LDS; for the
+// first tiles of 2000 rows over 32000 with 20 alternatives that made the call 284 us, this
+// 236.
+template <int PER, int KC>    // K <= KC
 struct DenseList {
-  uint64_t group[64];          // the largest key of each G / 64 threads
+  uint64_t group[64];          // the largest key of each PER threads
   uint64_t bound[2];           // the top_k-th largest of those, and of the threads' keys; or 1
   int count[2];
-  uint64_t list[kLpTop * kLpTop];
-  uint64_t few[kLpTop * kLpTop / 2];
-  uint64_t won[kLpTop];
+  uint64_t list[KC * (KC > PER ? KC : PER)];       // K threads' keys, K groups' threads
+  uint64_t few[KC * (KC * KC / 64 + 1)];           // K groups' keys of the list
+  uint64_t won[KC];
 };
 
-template <bool SOFTCAP, int G, int KC>             // kc = KC
+template <bool SOFTCAP, bool TAU_ONLY, int G, int KC>             // kc = KC
 __global__ __launch_bounds__(G < 256 ? 256 : G) void k_lp_join_dense(JoinArgs a) {
   constexpr int JT = G < 256 ? 256 / G : 1, PER = G / 64;
-  static_assert(KC <= kLpTop && kLpTop * PER <= kLpTop * kLpTop, "the list holds every key");
-  __shared__ DenseList sel[JT];
+  __shared__ DenseList<PER, KC> sel[JT];
   __shared__ float red[3][JT * PER];
   const int tid = threadIdx.x, tk = tid / G, g = tid % G, w = tid >> 6;
   const int64_t t = int64_t(blockIdx.x) * JT + tk;
@@ -927,7 +875,7 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void k_lp_join_dense(JoinArgs a)
   if (a.count) { const int64_t c = *a.count; n_live = c < n_live ? c : n_live; }
   const bool live = t < n_live;
   const int K = a.top_k;
-  DenseList& st = sel[tk];
+  DenseList<PER, KC>& st = sel[tk];
   row_u32x4 rv[KC / 4];
   uint32_t ri[KC / 4];
   bool on = live && g < a.lists;
@@ -939,7 +887,7 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void k_lp_join_dense(JoinArgs a)
     for (int i = 0; i < KC / 4; ++i) ri[i] = reinterpret_cast<const uint32_t*>(a.in.ci + at)[i];
   }
   float M = -INFINITY, S = 0.f, D = 0.f;
-  if (live)
+  if (!TAU_ONLY && live)
     for (int64_t p = g; p < a.parts; p += G) {
       const int64_t at = p * a.in.sp + t * a.in.st;
       const float2 ms = a.in.part[at];
@@ -954,15 +902,17 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void k_lp_join_dense(JoinArgs a)
                 : 0;
     best = max_u64(best, key[k]);
   }
-  const float Mw = wave_all(M, MaxOp());
-  const float f = M == -INFINITY ? 0.f : exp2f((M - Mw) * kLog2e);
-  D = wave_all(M == -INFINITY ? 0.f : f * fmaf(M - Mw, S, D), AddOp());
-  S = wave_all(S == 0.f ? 0.f : S * f, AddOp());
-  if ((tid & 63) == 0) { red[0][w] = Mw; red[1][w] = S; red[2][w] = D; }
+  if constexpr (!TAU_ONLY) {
+    const float Mw = wave_all(M, MaxOp());
+    const float f = M == -INFINITY ? 0.f : exp2f((M - Mw) * kLog2e);
+    D = wave_all(M == -INFINITY ? 0.f : f * fmaf(M - Mw, S, D), AddOp());
+    S = wave_all(S == 0.f ? 0.f : S * f, AddOp());
+    if ((tid & 63) == 0) { red[0][w] = Mw; red[1][w] = S; red[2][w] = D; }
+  }
   const uint32_t hi = group_all<PER>(uint32_t(best >> 32), MaxOp());
   const uint32_t lo = group_all<PER>(uint32_t(best >> 32) == hi ? uint32_t(best) : 0u, MaxOp());
   if (g % PER == 0) st.group[g / PER] = (uint64_t(hi) << 32) | lo;
-  if (g < kLpTop) st.won[g] = 0;
+  if (g < KC) st.won[g] = 0;
   if (g < 2) { st.bound[g] = 1; st.count[g] = 0; }
   __syncthreads();
   if (g < 64) {
@@ -1022,6 +972,11 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void k_lp_join_dense(JoinArgs a)
   }
   __syncthreads();
   if (g >= K || t >= a.N) return;
+  if constexpr (TAU_ONLY) {
+    a.first[g * a.first_ld + t] = st.won[g];       // of no list: 0
+    if (g == K - 1) a.tau[t] = st.won[g] != 0 ? key_value(st.won[g]) : -INFINITY;
+    return;
+  }
   M = -INFINITY; S = 0.f; D = 0.f;
   for (int i = 0; i < PER; ++i)
     join_part(M, S, D, red[0][tk * PER + i], red[1][tk * PER + i], red[2][tk * PER + i]);
@@ -1085,7 +1040,7 @@ __global__ __launch_bounds__(512) void k_lp_join_sparse(JoinArgs a) {
       if (at < CAP) list[tk][at] = key;
     };
     if (live) {
-      if (g < K) push(a.first[g * a.in.ck + t]);
+      if (g < K) push(a.first[g * a.first_ld + t]);
       for (int64_t l = a.list0 + g; l < a.lists; l += 4 * G) {
         float v[4][2];
         uint8_t row[4][2];
@@ -1678,23 +1633,24 @@ bool f32_narrow(int64_t N, int64_t V) {
   return (N - 1) % 64 < 32 || ((N + 63) / 64) * ((V + 63) / 64) <= 256;
 }
 
-template <bool SOFTCAP>
+template <bool SOFTCAP, bool TAU_ONLY>
 hipError_t run_join_dense(const LpPlan& q, const JoinArgs& j, const Launcher& L) {
   auto run = [&](auto g, auto kc) {
     constexpr int G = decltype(g)::value, T = G < 256 ? 256 : G;
-    hipLaunchKernelGGL((k_lp_join_dense<SOFTCAP, G, decltype(kc)::value>),
+    hipLaunchKernelGGL((k_lp_join_dense<SOFTCAP, TAU_ONLY, G, decltype(kc)::value>),
                        dim3(cdiv(j.N, T / G)), dim3(T), 0, L.stream, j);
   };
-  if (q.lists > 1024) return hipErrorInvalidValue;
   auto by_kc = [&](auto g) {
     if (q.kc == 8) run(g, Int<8>{});
     else if (q.kc == 16) run(g, Int<16>{});
     else run(g, Int<32>{});
   };
+  if (j.lists > 1024) return hipErrorInvalidValue;
   L.pre(kLpJoin);
-  if (q.lists <= 128) by_kc(Int<128>{});
-  else if (q.lists <= 256) by_kc(Int<256>{});
-  else if (q.lists <= 512) by_kc(Int<512>{});
+  if (j.lists <= 64) by_kc(Int<64>{});
+  else if (j.lists <= 128) by_kc(Int<128>{});
+  else if (j.lists <= 256) by_kc(Int<256>{});
+  else if (j.lists <= 512) by_kc(Int<512>{});
   else by_kc(Int<1024>{});
   L.post(kLpJoin);
   return hipGetLastError();
@@ -1703,7 +1659,7 @@ hipError_t run_join_dense(const LpPlan& q, const JoinArgs& j, const Launcher& L)
 template <bool SOFTCAP, bool TAU_ONLY>
 hipError_t run_join(const LpPlan& q, const JoinArgs& j, const Launcher& L) {
   // lists without a tau and more than one alternative go to run_join_dense
-  if (!TAU_ONLY && q.tiles && !j.first && j.top_k > 1) return hipErrorInvalidValue;
+  if (q.tiles && (TAU_ONLY || !j.first) && j.top_k > 1) return hipErrorInvalidValue;
   L.pre(kLpJoin);
   if (!q.tiles) {
     hipLaunchKernelGGL(k_lp_join_few<SOFTCAP>, dim3(unsigned(j.N)), dim3(kFewThreads), 0,
@@ -1712,22 +1668,14 @@ hipError_t run_join(const LpPlan& q, const JoinArgs& j, const Launcher& L) {
     hipLaunchKernelGGL(k_lp_join_sparse<SOFTCAP>, dim3(cdiv(j.N, kSparseTokens)), dim3(512), 0,
                        L.stream, j);
   } else {
-    auto run = [&](auto jt, auto threads, auto km) {
-      constexpr int JT = decltype(jt)::value, T = decltype(threads)::value;
-      hipLaunchKernelGGL((k_lp_join<SOFTCAP, TAU_ONLY, JT, T / JT, decltype(km)::value>),
-                         dim3(cdiv(j.N, JT)), dim3(T), 0, L.stream, j);
+    auto run = [&](auto jt) {
+      constexpr int JT = decltype(jt)::value;
+      hipLaunchKernelGGL((k_lp_join<SOFTCAP, TAU_ONLY, JT, 1024 / JT>), dim3(cdiv(j.N, JT)),
+                         dim3(1024), 0, L.stream, j);
     };
-    auto by_k = [&](auto jt) {
-      if (j.top_k <= 1) run(jt, Int<1024>{}, Int<1>{});
-      else if constexpr (TAU_ONLY) {
-        if (j.top_k <= 8) run(jt, Int<1024>{}, Int<8>{});
-        else if (j.top_k <= 16) run(jt, Int<1024>{}, Int<16>{});
-        else run(jt, Int<512>{}, Int<kLpTop>{});
-      }
-    };
-    if (j.N >= 4096) by_k(Int<32>{});
-    else if (j.N >= 1024) by_k(Int<16>{});
-    else by_k(Int<4>{});
+    if (j.N >= 4096) run(Int<32>{});
+    else if (j.N >= 1024) run(Int<16>{});
+    else run(Int<4>{});
   }
   L.post(kLpJoin);
   return hipGetLastError();
@@ -1768,7 +1716,7 @@ hipError_t logprobs(const LpPlan& q, const LpArgs& a, char* ws, const Launcher& 
             q.sp, q.st, q.cl, q.ck, q.ct, int(q.kc), q.top_k};
   JoinArgs j{out, q.parts, 0, q.lists, q.list_rows, a.V, a.N, nullptr, nullptr, a.tokens,
              a.ignore_index, q.top_k, warp, a.logp, a.entropy, a.lse, a.top_logp, a.top_ids,
-             nullptr, nullptr};
+             nullptr, q.nc, nullptr};
   hipError_t e = hipSuccess;
   if (a.dtype == FLCE_F32 || q.few) {
     if (a.status)
@@ -1850,16 +1798,15 @@ hipError_t logprobs(const LpPlan& q, const LpArgs& a, char* ws, const Launcher& 
       at_token(jc, t0);
     }
     const int64_t pre = lp_first_tiles(q, jc.N);
-    // More than one alternative without such a group (then there are fewer than 512
-    // tiles, 1024 lists): the candidates of a token lie together, for k_lp_join_dense.
-    // Otherwise up to 8 are all that the join reads of a list.
-    const bool dense = pre == 0 && q.top_k > 1;
-    LpOut to = out;
-    if (!dense && q.top_k <= 8) to.kc = q.top_k;
-    if (dense) to.cl = q.kc, to.ck = 1, to.ct = q.lists * q.kc;
-    jc.in = to;
+    // More than one alternative: in tiles without a bound (the first group, at most 512,
+    // or all where there is none: fewer than 512) the candidates of a token lie together,
+    // for k_lp_join_dense. In the others up to 8 are all that the join reads of a list.
+    const bool dense = q.top_k > 1;
+    LpOut lone = out, to = out;
+    if (dense) lone.cl = q.kc, lone.ck = 1, lone.ct = (pre > 0 ? 2 * pre : q.lists) * q.kc;
+    if (q.top_k <= 8) to.kc = q.top_k;
     // vocabulary rows [v0, v1) of the chunk's live tokens
-    auto tiles = [&](int64_t v0, int64_t v1, const float* tau) {
+    auto tiles = [&](int64_t v0, int64_t v1, const LpOut& to, const float* tau) {
       gemm::Launch l = gemm::forward_launch(p);
       l.M = l.a.rows = v1 - v0;
       l.off_a = v0 * p.H;
@@ -1879,17 +1826,22 @@ hipError_t logprobs(const LpPlan& q, const LpArgs& a, char* ws, const Launcher& 
     if (pre > 0) {
       jc.tau = reinterpret_cast<float*>(ws + q.off_tau);
       jc.first = reinterpret_cast<uint64_t*>(ws + q.off_first);
-      e = tiles(0, pre * kBM, nullptr);
+      e = tiles(0, pre * kBM, lone, nullptr);
+      jc.in = lone;
       jc.lists = 2 * pre;
-      if (e == hipSuccess) e = run_join<false, true>(q, jc, L);
-      if (e == hipSuccess) e = tiles(pre * kBM, a.V, jc.tau);
+      if (e == hipSuccess)
+        e = dense ? run_join_dense<false, true>(q, jc, L) : run_join<false, true>(q, jc, L);
+      if (e == hipSuccess) e = tiles(pre * kBM, a.V, to, jc.tau);
+      jc.in = to;
       jc.list0 = 2 * pre;
       jc.lists = q.lists;
     } else {
-      e = tiles(0, a.V, nullptr);
+      e = tiles(0, a.V, lone, nullptr);
+      jc.in = lone;
     }
     if (e == hipSuccess)
-      e = dense ? run_join_dense<SOFTCAP>(q, jc, L) : run_join<SOFTCAP, false>(q, jc, L);
+      e = dense && pre == 0 ? run_join_dense<SOFTCAP, false>(q, jc, L)
+                            : run_join<SOFTCAP, false>(q, jc, L);
   }
   return e;
 }

@@ -154,7 +154,7 @@ bool make_lp_plan(int64_t N, int64_t H, int64_t V, int dtype, int top_k, bool to
 inline int64_t lp_first_tiles(const LpPlan& q, int64_t nt) {
   if (q.kc == 0) return 0;
   const int64_t tt = (nt + kTileBF16 - 1) / kTileBF16, tv = q.parts;
-  int64_t pre = (tv + 15) / 16;
+  int64_t pre = (tv + 15) / 16 < 512 ? (tv + 15) / 16 : 512;
   if (pre * tt < 256) pre = (256 + tt - 1) / tt;
   return 2 * pre <= tv ? pre : 0;
 }
