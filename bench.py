@@ -42,7 +42,8 @@ KERNEL_SOURCES = [os.path.join(ROOT, "lm_head_linear_amd", "csrc", f)
                             "flce_api.hip", "flce_check.cpp", "flce_plan.h", "flce_internal.h",
                             "gemm_index.h", "gemm_bf16.h", "api_util.h", "ops_api.hip",
                             "ops_check.cpp", "ops_plan.h", "row_io.h", "kernels_norm.hip",
-                            "kernels_embed.hip", "kernels_logprobs.hip", "wave_ops.h")]
+                            "kernels_embed.hip", "kernels_logprobs.hip", "wave_ops.h",
+                            "join_sparse.h")]
 
 
 def log(*a):

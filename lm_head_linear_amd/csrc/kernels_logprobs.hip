@@ -35,6 +35,7 @@
 #include "../../include/flce.h"
 #include "flce_internal.h"
 #include "gemm_bf16.h"
+#include "join_sparse.h"
 #include "ops_plan.h"
 #include "row_io.h"
 #include "wave_ops.h"
@@ -991,20 +992,22 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void k_lp_join_dense(JoinArgs a)
 
 // Many tokens, lists of tiles with a tau, few of which hold anything: 16 tokens a
 // workgroup, 32 threads for each. Every candidate goes to a list in LDS, with the
-// top_k of the tiles before. Of its keys those from a bound up are kept, the top_k-th
-// largest of the 32 threads' largest, and each counts the larger ones. A list that
-// overflows is filled again with just the keys from its own top_k-th on: that key
-// rises every time. 1946 rows over 186 lists with 5 alternatives 13 us, 6144 rows over
-// 1984 lists with 8 49 us.
-constexpr int kSparseTokens = 16, kSparseG = 32, kSparseKeys = 512;
+// top_k of the tiles before, and the top_k of those are selected (join_sparse.h); a list
+// that overflows is filled again from its own top_k-th key on. 1946 rows over 186 lists
+// with 5 alternatives 13 us, 6144 rows over 1984 lists with 8 49 us.
+constexpr int kSparseTokens = 16;
+
+struct WorkgroupEnv {
+  __device__ __forceinline__ void sync() const { __syncthreads(); }
+  __device__ __forceinline__ bool any(bool x) const { return __syncthreads_or(x) != 0; }
+  __device__ __forceinline__ int add(int* p) const { return atomicAdd(p, 1); }
+};
 
 template <bool SOFTCAP>
 __global__ __launch_bounds__(512) void k_lp_join_sparse(JoinArgs a) {
-  constexpr int JT = kSparseTokens, G = kSparseG, CAP = kSparseKeys;
-  __shared__ uint64_t list[JT][CAP];
-  __shared__ uint64_t best[JT][G + 1], won[JT][kLpTop + 1], bound[JT], floor_key[JT];
+  constexpr int JT = kSparseTokens, G = kSparseG;
+  __shared__ SparseKeys<JT> st;
   __shared__ float4 grp[G / 2 * JT];
-  __shared__ int count[JT], kept[JT];
   const int tid = threadIdx.x, tk = tid % JT, g = tid / JT;
   const int64_t t = int64_t(blockIdx.x) * JT + tk;
   int64_t n_live = a.N;
@@ -1027,80 +1030,41 @@ __global__ __launch_bounds__(512) void k_lp_join_sparse(JoinArgs a) {
         if (p + u * G < a.parts) join_part(M, S, D, ms[u].x, ms[u].y, d[u]);
     }
   }
-  if (g == 0) floor_key[tk] = 1;
-  bool again = true;
-  while (again) {
-    if (g == 0) { count[tk] = 0; kept[tk] = 0; bound[tk] = 1; }
-    won[tk][g] = 0;
-    __syncthreads();
-    const uint64_t least = floor_key[tk];
-    auto push = [&](uint64_t key) {
-      if (key < least) return;
-      const int at = atomicAdd(&count[tk], 1);     // any order: the keys are ranked
-      if (at < CAP) list[tk][at] = key;
-    };
-    if (live) {
-      if (g < K) push(a.first[g * a.first_ld + t]);
-      for (int64_t l = a.list0 + g; l < a.lists; l += 4 * G) {
-        float v[4][2];
-        uint8_t row[4][2];
+  const int64_t keys = K + (a.lists - a.list0) * a.in.kc;
+  sparse_top(st, tk, g, K, keys, WorkgroupEnv(), [&](auto push) {
+    if (!live) return;
+    if (g < K) {
+      const uint64_t key = a.first[g * a.first_ld + t];
+      if (key != 0) push(key);
+    }
+    for (int64_t l = a.list0 + g; l < a.lists; l += 4 * G) {
+      float v[4][2];
+      uint8_t row[4][2];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {              // the first two of four lists at a time
-          const int64_t at = (l + u * G < a.lists ? l + u * G : l) * a.in.cl + t * a.in.ct;
+      for (int u = 0; u < 4; ++u) {              // the first two of four lists at a time
+        const int64_t at = (l + u * G < a.lists ? l + u * G : l) * a.in.cl + t * a.in.ct;
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int64_t i = at + (k < a.in.kc ? k : 0) * a.in.ck;
-            v[u][k] = a.in.cv[i];
-            row[u][k] = a.in.ci[i];
-          }
+        for (int k = 0; k < 2; ++k) {
+          const int64_t i = at + (k < a.in.kc ? k : 0) * a.in.ck;
+          v[u][k] = a.in.cv[i];
+          row[u][k] = a.in.ci[i];
         }
+      }
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          if (l + u * G >= a.lists || !(v[u][0] > -INFINITY)) continue;
-          const int64_t at = (l + u * G) * a.in.cl + t * a.in.ct, v0 = (l + u * G) * a.list_rows;
-          push(rank_key(v[u][0], v0 + row[u][0]));
-          if (a.in.kc < 2 || !(v[u][1] > -INFINITY)) continue;
-          push(rank_key(v[u][1], v0 + row[u][1]));
-          for (int k = 2; k < a.in.kc; ++k) {
-            const float x = a.in.cv[at + k * a.in.ck];
-            if (!(x > -INFINITY)) break;
-            push(rank_key(x, v0 + a.in.ci[at + k * a.in.ck]));
-          }
+      for (int u = 0; u < 4; ++u) {
+        if (l + u * G >= a.lists || !(v[u][0] > -INFINITY)) continue;
+        const int64_t at = (l + u * G) * a.in.cl + t * a.in.ct, v0 = (l + u * G) * a.list_rows;
+        push(rank_key(v[u][0], v0 + row[u][0]));
+        if (a.in.kc < 2 || !(v[u][1] > -INFINITY)) continue;
+        push(rank_key(v[u][1], v0 + row[u][1]));
+        for (int k = 2; k < a.in.kc; ++k) {
+          const float x = a.in.cv[at + k * a.in.ck];
+          if (!(x > -INFINITY)) break;
+          push(rank_key(x, v0 + a.in.ci[at + k * a.in.ck]));
         }
       }
     }
-    __syncthreads();
-    const int n = count[tk] < CAP ? count[tk] : CAP;
-    uint64_t mine = 0;
-    for (int i = g; i < n; i += G) mine = max_u64(mine, list[tk][i]);
-    best[tk][g] = mine;
-    __syncthreads();
-    int above = 0;
-    for (int i = 0; i < G; ++i) above += best[tk][i] > mine ? 1 : 0;
-    if (mine != 0 && above == K - 1) bound[tk] = mine;
-    __syncthreads();
-    const uint64_t from = bound[tk];
-    uint64_t hold[CAP / G];                        // this thread's keys from the bound up
-#pragma unroll
-    for (int u = 0; u < CAP / G; ++u) {
-      const int i = u * G + g;
-      hold[u] = i < n && list[tk][i] >= from ? list[tk][i] : 0;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int u = 0; u < CAP / G; ++u)
-      if (hold[u] != 0) list[tk][atomicAdd(&kept[tk], 1)] = hold[u];
-    __syncthreads();
-    const int m = kept[tk];
-    for (int i = g; i < m; i += G) {
-      const uint64_t k = list[tk][i];
-      int larger = 0;
-      for (int o = 0; o < m && larger < K; ++o) larger += list[tk][o] > k ? 1 : 0;
-      if (larger < K) won[tk][larger] = k;
-    }
-    again = __syncthreads_or(count[tk] > CAP);
-    if (g == 0 && count[tk] > CAP) floor_key[tk] = won[tk][K - 1];
-  }
+  });
   for (int half = G / 2; half > 0; half >>= 1) {
     const int slot = tid % (half * JT);
     if (g >= half && g < 2 * half) grp[slot] = make_float4(M, S, D, 0.f);
@@ -1119,7 +1083,7 @@ __global__ __launch_bounds__(512) void k_lp_join_sparse(JoinArgs a) {
   const bool shown = live && (!a.labels || a.labels[t] != a.ignore_index);
   if (g == 0) write_token(a, t, o, shown, f.x, f.y, f.z);
   if (g < K) {
-    const uint64_t k = won[tk][g];
+    const uint64_t k = st.won[tk][g];
     const bool has = shown && k != 0;
     write_alternative(a, o, g, has ? warp_logit<SOFTCAP>(a.warp, key_value(k)) : 0.f,
                       has ? key_id(k) : -1, f.x, logf(f.y));
