@@ -511,7 +511,8 @@ int flce_embedding_backward(const int64_t* tokens, const void* dout, int64_t ld_
  * Everything is float32 (ids int64) [N] or [N][top_k]; sums and logits are
  * float32. Alternatives are ranked by z (the order of x without ties made by
  * rounding). Logits of -inf and NaN are not ranked: where fewer than top_k others
- * exist the rest is id -1, value -inf.
+ * exist the rest is id -1, value -inf. A NaN logit makes its row's lse, logp and
+ * entropy NaN.
  * tokens [N] int64 may be NULL (no given tokens: logp must be NULL too);
  * entropy, lse, status may be NULL; top_logp and top_ids are NULL exactly when
  * top_k is 0 (at most FLCE_MAX_TOP).

@@ -347,11 +347,12 @@ __device__ __forceinline__ void tile_epilogue(const float (&z)[64 / TPT], int q,
   }
   m = group_all<TPT>(m, MaxOp());
   float s = 0.f, d = 0.f;
-  const float mb = m * kLog2e;
+  // no largest logit: all are -inf (their u too) or NaN, which the sums keep
+  const float mb = m == -INFINITY ? 0.f : m * kLog2e;
 #pragma unroll
   for (int e = 0; e < E; ++e) {
     float u = fmaf(x[e], kLog2e, -mb);
-    u = (e < n && m != -INFINITY && u != -INFINITY) ? u : -200.f;
+    u = (e < n && u != -INFINITY) ? u : -200.f;
     const float p = __builtin_amdgcn_exp2f(u);
     s += p;
     d = fmaf(p, u, d);
@@ -748,14 +749,15 @@ __device__ __forceinline__ void write_alternative(const JoinArgs& a, int64_t o, 
   a.top_ids[o * a.top_k + k] = id;
 }
 
-// (m, s, d) joined into (M, S, D).
+// (m, s, d) joined into (M, S, D). A part of NaN logits alone has the max -inf and a sum
+// of NaN, which stays.
 __device__ __forceinline__ void join_part(float& M, float& S, float& D, float m, float s, float d) {
   if (m == -INFINITY && s == 0.f) return;
   const float Mn = fmaxf(M, m);
   const float a = M == -INFINITY ? 0.f : exp2f((M - Mn) * kLog2e);
   const float b = exp2f((m - Mn) * kLog2e);
   D = (M == -INFINITY ? 0.f : a * fmaf(M - Mn, S, D)) + b * fmaf(m - Mn, s, d);
-  S = (M == -INFINITY ? 0.f : S * a) + s * b;
+  S = S * a + s * b;
   M = Mn;
 }
 
