@@ -7,8 +7,10 @@
 // which join over tiles by rescaling to the larger max:
 //   s' = s exp(m - M),  d' = exp(m - M) (d + (m - M) s)
 // so that  lse = M + log S,  log p_y = (x_y - M) - log S,  entropy = log S - D / S.
-// log S is taken apart from M: a token that holds nearly all of the probability
-// keeps its small log probability. Alternatives are ranked by the raw logit z (the
+// The exponents are formed from the difference x - m, so the largest term is exactly 1,
+// S >= 1 and no log probability is above 0; log S is taken apart from M, so a token that
+// holds nearly all of the probability keeps its small one to some 2^-24, wherever its
+// logit lies. Alternatives are ranked by the raw logit z (the
 // order of x, without the ties that rounding x makes), equal ones by lowest id.
 //
 // Three kernels compute logits:
@@ -53,6 +55,12 @@ struct Warp {
 template <bool SOFTCAP>
 __device__ __forceinline__ float warp_logit(const Warp& w, float z) {
   return SOFTCAP ? w.cap_t * tanh_fast(z * w.inv_cap) : z * w.inv_t;
+}
+// a - b of the two rounded values. Contracted with the product that made a, it would be
+// what rounding a left and not 0 where they are equal.
+__device__ __forceinline__ float minus(float a, float b) {
+#pragma clang fp contract(off)
+  return a - b;
 }
 // dx / dz
 template <bool SOFTCAP>
@@ -179,15 +187,16 @@ struct EpiLp {
         }
       }
       const float m = col_max4(fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])));
-      // in powers of two: u = (x - m) log2 e, d in units of ln 2
-      const float mb = m == -INFINITY ? 0.f : m * kLog2e;
+      // in powers of two: u = (x - m) log2 e, d in units of ln 2. The form
+      // x log2 e - (m log2 e) saves an instruction, but its largest term is not 1
+      const float mb = m == -INFINITY ? 0.f : m;
       float sq[4] = {0.f, 0.f, 0.f, 0.f}, dq[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int i = 0; i < 8; ++i)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           // a row past the vocabulary: 2^-200 = 0; a logit of -inf keeps -inf out of d
-          float u = fmaf(x[i][r], kLog2e, -mb);
+          float u = minus(x[i][r], mb) * kLog2e;
           u = (in(i, r) && u != -INFINITY) ? u : -200.f;
           const float e = __builtin_amdgcn_exp2f(u);
           sq[r] += e;
@@ -348,10 +357,10 @@ __device__ __forceinline__ void tile_epilogue(const float (&z)[64 / TPT], int q,
   m = group_all<TPT>(m, MaxOp());
   float s = 0.f, d = 0.f;
   // no largest logit: all are -inf (their u too) or NaN, which the sums keep
-  const float mb = m == -INFINITY ? 0.f : m * kLog2e;
+  const float mb = m == -INFINITY ? 0.f : m;
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    float u = fmaf(x[e], kLog2e, -mb);
+    float u = minus(x[e], mb) * kLog2e;
     u = (e < n && u != -INFINITY) ? u : -200.f;
     const float p = __builtin_amdgcn_exp2f(u);
     s += p;
@@ -740,12 +749,12 @@ __device__ __forceinline__ void write_token(const JoinArgs& a, int64_t t, int64_
   if (a.entropy) a.entropy[o] = live ? ls - D / S : 0.f;
   if (a.labels) {
     const int64_t y = a.labels[t];
-    a.logp[o] = !live ? 0.f : (y < 0 || y >= a.V) ? NAN : (a.in.zt[t] - M) - ls;
+    a.logp[o] = !live ? 0.f : (y < 0 || y >= a.V) ? NAN : minus(a.in.zt[t], M) - ls;
   }
 }
 __device__ __forceinline__ void write_alternative(const JoinArgs& a, int64_t o, int k, float x,
                                                   int64_t id, float M, float ls) {
-  a.top_logp[o * a.top_k + k] = id >= 0 ? (x - M) - ls : -INFINITY;
+  a.top_logp[o * a.top_k + k] = id >= 0 ? minus(x, M) - ls : -INFINITY;
   a.top_ids[o * a.top_k + k] = id;
 }
 
