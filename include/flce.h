@@ -522,8 +522,9 @@ int flce_embedding_backward(const int64_t* tokens, const void* dout, int64_t ld_
  * not depend on the token.
  * bf16 inputs with N <= 128 run a kernel that reads W once, near the memory's rate;
  * more run the head's matrix-core tiles over the live rows. A row's values can differ
- * in the last bits between the two; within either they do not depend on N, and they
- * are the same bits on every run.
+ * in the last bits between the two; within either, and for float32, they do not depend on
+ * N or on the other rows: their sums are added up in one order. They are the same bits on
+ * every run.
  * The workspace (256-byte aligned) is flce_logprobs_workspace_size bytes: partial
  * sums of up to 8192 tokens at a time, the gathered rows, padded copies for a bf16 H
  * that is not a multiple of 8 and N > 128, and with top_k > 0 the candidates: up to 32

@@ -355,7 +355,11 @@ __device__ __forceinline__ void tile_epilogue(const float (&z)[64 / TPT], int q,
     zm = fmaxf(zm, e < n ? z[e] : -INFINITY);
   }
   m = group_all<TPT>(m, MaxOp());
-  float s = 0.f, d = 0.f;
+  // 16 groups of four rows, each in order, then a tree over the groups: whichever lanes
+  // hold them, the same order of additions, so that a token's sums do not depend on how
+  // many others the call has
+  constexpr int Q = E / 4;
+  float sq[Q] = {}, dq[Q] = {};
   // no largest logit: all are -inf (their u too) or NaN, which the sums keep
   const float mb = m == -INFINITY ? 0.f : m;
 #pragma unroll
@@ -363,11 +367,18 @@ __device__ __forceinline__ void tile_epilogue(const float (&z)[64 / TPT], int q,
     float u = minus(x[e], mb) * kLog2e;
     u = (e < n && u != -INFINITY) ? u : -200.f;
     const float p = __builtin_amdgcn_exp2f(u);
-    s += p;
-    d = fmaf(p, u, d);
+    sq[e / 4] += p;
+    dq[e / 4] = fmaf(p, u, dq[e / 4]);
   }
-  s = group_all<TPT>(s, AddOp());
-  d = group_all<TPT>(d * kLn2, AddOp());
+#pragma unroll
+  for (int w = 1; w < Q; w *= 2)
+#pragma unroll
+    for (int i = 0; i < Q; i += 2 * w) {
+      sq[i] += sq[i + w];
+      dq[i] += dq[i + w];
+    }
+  const float s = group_all<TPT>(sq[0], AddOp());
+  const float d = group_all<TPT>(dq[0], AddOp()) * kLn2;
   const int64_t at = (v0 / 64) * out.sp + t * out.st;
   if (tok && q == 0) {
     out.part[at] = make_float2(m, s);
@@ -765,9 +776,72 @@ __device__ __forceinline__ void join_part(float& M, float& S, float& D, float m,
   const float Mn = fmaxf(M, m);
   const float a = M == -INFINITY ? 0.f : exp2f((M - Mn) * kLog2e);
   const float b = exp2f((m - Mn) * kLog2e);
-  D = (M == -INFINITY ? 0.f : a * fmaf(M - Mn, S, D)) + b * fmaf(m - Mn, s, d);
-  S = S * a + s * b;
+  // spelled out: which product is contracted decides the last bit
+  D = fmaf(b, fmaf(m - Mn, s, d), M == -INFINITY ? 0.f : a * fmaf(M - Mn, S, D));
+  S = fmaf(s, b, S * a);
   M = Mn;
+}
+
+// The joins over tiles of many tokens add a token's parts up in one order, whatever the
+// threads they have for it: chain c takes parts c, c + kChains, ... in order, then chain c
+// joins chain c + half for half = kChains / 2 ... 1. A token's values are then the same
+// bits in calls of any count of tokens (another join, other threads). With chains of as
+// many as the threads, one row in forty of 131072 logits got another last bit.
+constexpr int kChains = 256;
+
+// Thread g of G: its chains c = g (mod G), joined as far as they lie in this thread.
+template <int G>
+__device__ __forceinline__ void join_chains(const LpOut& in, int64_t parts, int64_t t, int g,
+                                            float& M, float& S, float& D) {
+  constexpr int C = kChains / G, A = C >= 4 ? 1 : 4 / C;   // four loads in flight at least
+  float cm[C], cs[C], cd[C];
+#pragma unroll
+  for (int u = 0; u < C; ++u) { cm[u] = -INFINITY; cs[u] = 0.f; cd[u] = 0.f; }
+  for (int64_t p0 = g; p0 < parts; p0 += A * kChains) {
+    float2 ms[A][C];
+    float d[A][C];
+#pragma unroll
+    for (int x = 0; x < A; ++x)
+#pragma unroll
+      for (int u = 0; u < C; ++u) {
+        const int64_t p = p0 + x * kChains + u * G, at = (p < parts ? p : p0) * in.sp + t * in.st;
+        ms[x][u] = in.part[at];
+        d[x][u] = in.pd[at];
+      }
+#pragma unroll
+    for (int x = 0; x < A; ++x)
+#pragma unroll
+      for (int u = 0; u < C; ++u)
+        if (p0 + x * kChains + u * G < parts)
+          join_part(cm[u], cs[u], cd[u], ms[x][u].x, ms[x][u].y, d[x][u]);
+  }
+#pragma unroll
+  for (int h = C / 2; h > 0; h /= 2)
+#pragma unroll
+    for (int u = 0; u < h; ++u) join_part(cm[u], cs[u], cd[u], cm[u + h], cs[u + h], cd[u + h]);
+  M = cm[0]; S = cs[0]; D = cd[0];
+}
+
+// The chains of a wave's lanes: lane l joins lane l + half for half = 32 ... 1. Every lane
+// gets lane 0's.
+__device__ __forceinline__ void join_lanes(float& M, float& S, float& D) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  auto lower_upper = [&](auto swap) {              // both lanes of a pair join alike
+    const auto m = swap(__float_as_uint(M)), s = swap(__float_as_uint(S)),
+               d = swap(__float_as_uint(D));
+    M = __uint_as_float(m[0]); S = __uint_as_float(s[0]); D = __uint_as_float(d[0]);
+    join_part(M, S, D, __uint_as_float(m[1]), __uint_as_float(s[1]), __uint_as_float(d[1]));
+  };
+  lower_upper([](uint32_t x) { return __builtin_amdgcn_permlane32_swap(x, x, false, false); });
+  lower_upper([](uint32_t x) { return __builtin_amdgcn_permlane16_swap(x, x, false, false); });
+  // within 16 lanes: from the lane `half` further on, for the lower ones
+  join_part(M, S, D, dpp_move<kDppDown + 8>(M), dpp_move<kDppDown + 8>(S), dpp_move<kDppDown + 8>(D));
+  join_part(M, S, D, dpp_move<kDppDown + 4>(M), dpp_move<kDppDown + 4>(S), dpp_move<kDppDown + 4>(D));
+  join_part(M, S, D, dpp_move<kDppDown + 2>(M), dpp_move<kDppDown + 2>(S), dpp_move<kDppDown + 2>(D));
+  join_part(M, S, D, dpp_move<kDppDown + 1>(M), dpp_move<kDppDown + 1>(S), dpp_move<kDppDown + 1>(D));
+  auto first = [](float x) { return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), 0)); };
+  M = first(M); S = first(S); D = first(D);
+#endif
 }
 
 __device__ __forceinline__ uint64_t rank_key(float v, int64_t id) {
@@ -788,8 +862,6 @@ __device__ __forceinline__ uint64_t max_u64(uint64_t a, uint64_t b) { return a >
 // each, thread g taking every G-th part and list, then the threads pairwise. 32 tokens
 // read whole lines of every part; below 4096 tokens that leaves most CUs idle, and 16
 // (below 1024: 4) tokens a workgroup are faster.
-constexpr int kAhead = 4;                          // loads in flight
-
 template <bool SOFTCAP, bool TAU_ONLY, int JT, int G>
 __global__ __launch_bounds__(JT * G) void k_lp_join(JoinArgs a) {
   constexpr int kT = JT * G;
@@ -802,21 +874,7 @@ __global__ __launch_bounds__(JT * G) void k_lp_join(JoinArgs a) {
   const bool live = t < n_live;
   const int K = a.top_k;
   float M = -INFINITY, S = 0.f, D = 0.f;
-  if (!TAU_ONLY && live) {
-    for (int64_t p = g; p < a.parts; p += kAhead * G) {
-      float2 ms[kAhead];
-      float d[kAhead];
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        const int64_t at = (p + u * G < a.parts ? p + u * G : p) * a.in.sp + t * a.in.st;
-        ms[u] = a.in.part[at];
-        d[u] = a.in.pd[at];
-      }
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u)
-        if (p + u * G < a.parts) join_part(M, S, D, ms[u].x, ms[u].y, d[u]);
-    }
-  }
+  if (!TAU_ONLY && live) join_chains<G>(a.in, a.parts, t, g, M, S, D);
   uint64_t top = 0;
   if (K > 0 && live) {
 #pragma unroll 4
@@ -879,9 +937,10 @@ struct DenseList {
 template <bool SOFTCAP, bool TAU_ONLY, int G, int KC>             // kc = KC
 __global__ __launch_bounds__(G < 256 ? 256 : G) void k_lp_join_dense(JoinArgs a) {
   constexpr int JT = G < 256 ? 256 / G : 1, PER = G / 64;
+  constexpr int GC = G < kChains ? G : kChains;    // threads with a chain
   __shared__ DenseList<PER, KC> sel[JT];
-  __shared__ float red[3][JT * PER];
-  const int tid = threadIdx.x, tk = tid / G, g = tid % G, w = tid >> 6;
+  __shared__ float red[3][JT][GC];
+  const int tid = threadIdx.x, tk = tid / G, g = tid % G;
   const int64_t t = int64_t(blockIdx.x) * JT + tk;
   int64_t n_live = a.N;
   if (a.count) { const int64_t c = *a.count; n_live = c < n_live ? c : n_live; }
@@ -899,8 +958,8 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void k_lp_join_dense(JoinArgs a)
     for (int i = 0; i < KC / 4; ++i) ri[i] = reinterpret_cast<const uint32_t*>(a.in.ci + at)[i];
   }
   float M = -INFINITY, S = 0.f, D = 0.f;
-  if (!TAU_ONLY && live)
-    for (int64_t p = g; p < a.parts; p += G) {
+  if (!TAU_ONLY && live && g < GC)                 // parts <= G: see run_join_dense
+    for (int64_t p = g; p < a.parts; p += kChains) {
       const int64_t at = p * a.in.sp + t * a.in.st;
       const float2 ms = a.in.part[at];
       join_part(M, S, D, ms.x, ms.y, a.in.pd[at]);
@@ -915,11 +974,7 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void k_lp_join_dense(JoinArgs a)
     best = max_u64(best, key[k]);
   }
   if constexpr (!TAU_ONLY) {
-    const float Mw = wave_all(M, MaxOp());
-    const float f = M == -INFINITY ? 0.f : exp2f((M - Mw) * kLog2e);
-    D = wave_all(M == -INFINITY ? 0.f : f * fmaf(M - Mw, S, D), AddOp());
-    S = wave_all(S == 0.f ? 0.f : S * f, AddOp());
-    if ((tid & 63) == 0) { red[0][w] = Mw; red[1][w] = S; red[2][w] = D; }
+    if (g < GC) { red[0][tk][g] = M; red[1][tk][g] = S; red[2][tk][g] = D; }
   }
   const uint32_t hi = group_all<PER>(uint32_t(best >> 32), MaxOp());
   const uint32_t lo = group_all<PER>(uint32_t(best >> 32) == hi ? uint32_t(best) : 0u, MaxOp());
@@ -983,15 +1038,27 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void k_lp_join_dense(JoinArgs a)
     if (larger < K) st.won[larger] = x;
   }
   __syncthreads();
+  if (g >= 64) return;
+  if constexpr (!TAU_ONLY) {
+    auto join = [&](float& m, float& s, float& d, int c) {
+      join_part(m, s, d, red[0][tk][c], red[1][tk][c], red[2][tk][c]);
+    };
+    if constexpr (GC == 256) {
+      float m = red[0][tk][g + 64], s = red[1][tk][g + 64], d = red[2][tk][g + 64];
+      join(M, S, D, g + 128);
+      join(m, s, d, g + 192);
+      join_part(M, S, D, m, s, d);
+    } else if constexpr (GC == 128) {
+      join(M, S, D, g + 64);
+    }
+    join_lanes(M, S, D);
+  }
   if (g >= K || t >= a.N) return;
   if constexpr (TAU_ONLY) {
     a.first[g * a.first_ld + t] = st.won[g];       // of no list: 0
     if (g == K - 1) a.tau[t] = st.won[g] != 0 ? key_value(st.won[g]) : -INFINITY;
     return;
   }
-  M = -INFINITY; S = 0.f; D = 0.f;
-  for (int i = 0; i < PER; ++i)
-    join_part(M, S, D, red[0][tk * PER + i], red[1][tk * PER + i], red[2][tk * PER + i]);
   const int64_t o = a.idx ? int64_t(a.idx[t]) : t;
   const bool shown = live && (!a.labels || a.labels[t] != a.ignore_index);
   if (g == 0) write_token(a, t, o, shown, M, S, D);
@@ -1026,21 +1093,7 @@ __global__ __launch_bounds__(512) void k_lp_join_sparse(JoinArgs a) {
   const bool live = t < n_live;
   const int K = a.top_k;
   float M = -INFINITY, S = 0.f, D = 0.f;
-  if (live) {
-    for (int64_t p = g; p < a.parts; p += kAhead * G) {
-      float2 ms[kAhead];
-      float d[kAhead];
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        const int64_t at = (p + u * G < a.parts ? p + u * G : p) * a.in.sp + t * a.in.st;
-        ms[u] = a.in.part[at];
-        d[u] = a.in.pd[at];
-      }
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u)
-        if (p + u * G < a.parts) join_part(M, S, D, ms[u].x, ms[u].y, d[u]);
-    }
-  }
+  if (live) join_chains<G>(a.in, a.parts, t, g, M, S, D);
   const int64_t keys = K + (a.lists - a.list0) * a.in.kc;
   sparse_top(st, tk, g, K, keys, WorkgroupEnv(), [&](auto push) {
     if (!live) return;
@@ -1620,7 +1673,8 @@ hipError_t run_join_dense(const LpPlan& q, const JoinArgs& j, const Launcher& L)
     else if (q.kc == 16) run(g, Int<16>{});
     else run(g, Int<32>{});
   };
-  if (j.lists > 1024) return hipErrorInvalidValue;
+  // a thread a list, and two lists a part: no more parts than threads
+  if (j.lists > 1024 || (!TAU_ONLY && 2 * j.parts > j.lists + 1)) return hipErrorInvalidValue;
   L.pre(kLpJoin);
   if (j.lists <= 64) by_kc(Int<64>{});
   else if (j.lists <= 128) by_kc(Int<128>{});

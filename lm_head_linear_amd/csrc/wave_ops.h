@@ -22,6 +22,7 @@ __device__ __forceinline__ T dpp_move(T x) {
 }
 
 constexpr int kDppXor1 = 0xB1, kDppXor2 = 0x4E;              // within 4 lanes
+constexpr int kDppDown = 0x100;      // + n: from the lane n further on, 0 past the 16
 constexpr int kDppHalfMirror = 0x141, kDppMirror = 0x140;    // reversed within 8, 16 lanes
 
 // op over the TPT (a power of two up to 16) adjacent lanes of a group.
