@@ -190,19 +190,20 @@ def _flat_rows(t):
     return t if inplace else t.contiguous()
 
 
-# The functions take and return rows: a view made inside one could not be changed in place
-# by its caller.
-
-
 class _RMSNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, residual, eps, weight_offset):
-        y, s, rstd = flce_rms_norm(x, weight, residual, eps=eps, weight_offset=weight_offset)
+        shape = x.shape
+        y, s, rstd = flce_rms_norm(_flat_rows(x), weight,
+                                   None if residual is None else _flat_rows(residual), eps=eps,
+                                   weight_offset=weight_offset)
         ctx.save_for_backward(s, weight, rstd)
         ctx.weight_offset = weight_offset
         ctx.has_residual = residual is not None
         ctx.set_materialize_grads(False)
-        return y if residual is None else (y, s)
+        if residual is None:
+            return y.view(shape)
+        return y.view(shape), s.view(shape)
 
     @staticmethod
     @once_differentiable
@@ -210,9 +211,12 @@ class _RMSNorm(torch.autograd.Function):
         s, weight, rstd = ctx.saved_tensors
         if dy is None:                       # only the sum was used
             return ds, None, ds if ctx.has_residual else None, None, None
+        shape = dy.shape
+        rows = lambda t: t.contiguous().view(-1, shape[-1])  # noqa: E731
         dx, dw = flce_rms_norm_backward(
-            dy.contiguous(), s, weight, rstd, None if ds is None else ds.contiguous(),
+            rows(dy), s, weight, rstd, None if ds is None else rows(ds),
             weight_offset=ctx.weight_offset, want_dweight=ctx.needs_input_grad[1])
+        dx = dx.view(shape)
         return dx, dw, dx if ctx.has_residual else None, None, None
 
 
@@ -224,12 +228,7 @@ def fused_rms_norm(x: torch.Tensor, weight: torch.Tensor,
     The gradients of x and of the residual are the same tensor of values: both
     inputs enter through their sum.
     """
-    rows = None if residual is None else _flat_rows(residual)
-    out = _RMSNorm.apply(_flat_rows(x), weight.contiguous(), rows, float(eps),
-                         float(weight_offset))
-    if residual is None:
-        return out.view(x.shape)
-    return out[0].view(x.shape), out[1].view(x.shape)
+    return _RMSNorm.apply(x, weight.contiguous(), residual, float(eps), float(weight_offset))
 
 
 # ---- embedding -----------------------------------------------------------------------
@@ -328,26 +327,26 @@ def flce_embedding_backward(tokens: torch.Tensor, dout: torch.Tensor, V: int, *,
 class _Embedding(torch.autograd.Function):
     @staticmethod
     def forward(ctx, tokens, W, scale, padding_index):
-        ctx.save_for_backward(tokens)
+        flat = tokens.reshape(-1).contiguous()
+        out = flce_embedding(flat, W, scale=scale, padding_index=padding_index)
+        ctx.save_for_backward(flat)
         ctx.args = (W.shape[0], scale, padding_index)
-        return flce_embedding(tokens, W, scale=scale, padding_index=padding_index)
+        return out.view(*tokens.shape, W.shape[1])
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dout):
         (tokens,) = ctx.saved_tensors
         V, scale, padding_index = ctx.args
-        dW = flce_embedding_backward(tokens, dout.contiguous(), V, scale=scale,
-                                     padding_index=padding_index)
+        dW = flce_embedding_backward(tokens, dout.contiguous().view(-1, dout.shape[-1]), V,
+                                     scale=scale, padding_index=padding_index)
         return None, dW, None, None
 
 
 def fused_embedding(tokens: torch.Tensor, W: torch.Tensor, *, scale: float = 1.0,
                     padding_index: int = -100) -> torch.Tensor:
     """scale * W[tokens] for tokens of any shape, with the table's gradient."""
-    flat = tokens.reshape(-1).contiguous()
-    out = _Embedding.apply(flat, W.contiguous(), float(scale), int(padding_index))
-    return out.view(*tokens.shape, W.shape[1])
+    return _Embedding.apply(tokens, W.contiguous(), float(scale), int(padding_index))
 
 
 # ---- token log probabilities ---------------------------------------------------------
