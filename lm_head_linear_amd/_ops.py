@@ -190,10 +190,14 @@ def _flat_rows(t):
     return t if inplace else t.contiguous()
 
 
+# The functions return rows, which their wrappers shape: a view made inside a function could
+# not be changed in place by its caller.
+
+
 class _RMSNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, residual, eps, weight_offset):
-        shape = x.shape
+        ctx.shape = x.shape
         y, s, rstd = flce_rms_norm(_flat_rows(x), weight,
                                    None if residual is None else _flat_rows(residual), eps=eps,
                                    weight_offset=weight_offset)
@@ -201,22 +205,20 @@ class _RMSNorm(torch.autograd.Function):
         ctx.weight_offset = weight_offset
         ctx.has_residual = residual is not None
         ctx.set_materialize_grads(False)
-        if residual is None:
-            return y.view(shape)
-        return y.view(shape), s.view(shape)
+        return y if residual is None else (y, s)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dy, ds=None):
         s, weight, rstd = ctx.saved_tensors
         if dy is None:                       # only the sum was used
-            return ds, None, ds if ctx.has_residual else None, None, None
-        shape = dy.shape
-        rows = lambda t: t.contiguous().view(-1, shape[-1])  # noqa: E731
-        dx, dw = flce_rms_norm_backward(
-            rows(dy), s, weight, rstd, None if ds is None else rows(ds),
-            weight_offset=ctx.weight_offset, want_dweight=ctx.needs_input_grad[1])
-        dx = dx.view(shape)
+            dx, dw = ds, None
+        else:
+            dx, dw = flce_rms_norm_backward(
+                dy.contiguous(), s, weight, rstd, None if ds is None else ds.contiguous(),
+                weight_offset=ctx.weight_offset, want_dweight=ctx.needs_input_grad[1])
+        # one tensor for both: autograd then copies it where a leaf would keep it
+        dx = dx.reshape(ctx.shape)
         return dx, dw, dx if ctx.has_residual else None, None, None
 
 
@@ -228,7 +230,10 @@ def fused_rms_norm(x: torch.Tensor, weight: torch.Tensor,
     The gradients of x and of the residual are the same tensor of values: both
     inputs enter through their sum.
     """
-    return _RMSNorm.apply(x, weight.contiguous(), residual, float(eps), float(weight_offset))
+    out = _RMSNorm.apply(x, weight.contiguous(), residual, float(eps), float(weight_offset))
+    if residual is None:
+        return out.view(x.shape)
+    return out[0].view(x.shape), out[1].view(x.shape)
 
 
 # ---- embedding -----------------------------------------------------------------------
@@ -327,26 +332,26 @@ def flce_embedding_backward(tokens: torch.Tensor, dout: torch.Tensor, V: int, *,
 class _Embedding(torch.autograd.Function):
     @staticmethod
     def forward(ctx, tokens, W, scale, padding_index):
-        flat = tokens.reshape(-1).contiguous()
-        out = flce_embedding(flat, W, scale=scale, padding_index=padding_index)
-        ctx.save_for_backward(flat)
+        ctx.save_for_backward(tokens)
         ctx.args = (W.shape[0], scale, padding_index)
-        return out.view(*tokens.shape, W.shape[1])
+        return flce_embedding(tokens, W, scale=scale, padding_index=padding_index)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dout):
         (tokens,) = ctx.saved_tensors
         V, scale, padding_index = ctx.args
-        dW = flce_embedding_backward(tokens, dout.contiguous().view(-1, dout.shape[-1]), V,
-                                     scale=scale, padding_index=padding_index)
+        dW = flce_embedding_backward(tokens, dout.contiguous(), V, scale=scale,
+                                     padding_index=padding_index)
         return None, dW, None, None
 
 
 def fused_embedding(tokens: torch.Tensor, W: torch.Tensor, *, scale: float = 1.0,
                     padding_index: int = -100) -> torch.Tensor:
     """scale * W[tokens] for tokens of any shape, with the table's gradient."""
-    return _Embedding.apply(tokens, W.contiguous(), float(scale), int(padding_index))
+    flat = tokens.reshape(-1).contiguous()
+    out = _Embedding.apply(flat, W.contiguous(), float(scale), int(padding_index))
+    return out.view(*tokens.shape, W.shape[1])
 
 
 # ---- token log probabilities ---------------------------------------------------------
