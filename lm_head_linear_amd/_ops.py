@@ -61,7 +61,9 @@ def _bytes(t):
     return 0 if t is None else t.numel() * t.element_size()
 
 
-def _workspace(ws, need, dev):
+def _workspace(where, ws, need, dev):
+    if need == 0:                        # sizes the library does not take
+        raise FlceError(_lib.ERR_ARG, where)
     if ws is not None and (ws.device != dev or not ws.is_contiguous()):
         raise ValueError(f"the workspace must be contiguous memory of {dev}, got {ws.device}")
     return torch.empty(need, dtype=torch.uint8, device=dev) if _bytes(ws) < need else ws
@@ -174,7 +176,8 @@ def flce_rms_norm_backward(dy: torch.Tensor, s: torch.Tensor, weight: torch.Tens
     elif want_dweight:
         dweight = torch.empty(H, dtype=weight.dtype, device=dev)
     if dweight is not None:
-        workspace = _workspace(workspace, flce_rms_norm_backward_workspace_size(N, H), dev)
+        workspace = _workspace("flce_rms_norm_backward", workspace,
+                               flce_rms_norm_backward_workspace_size(N, H), dev)
     _run("flce_rms_norm_backward", dev, _lib.load().flce_rms_norm_backward, dy.data_ptr(), ld_dy,
          _ptr(ds), ld_ds, s.data_ptr(), ld_s, weight.data_ptr(), rstd.data_ptr(), N, H,
          float(weight_offset), dx.data_ptr(), ld_dx, _ptr(dweight),
@@ -321,7 +324,8 @@ def flce_embedding_backward(tokens: torch.Tensor, dout: torch.Tensor, V: int, *,
         _check_tensor("dW", dW, (V, H), gdt, dev)
     if status is not None:
         _check_tensor("status", status, (), torch.int32, dev)
-    workspace = _workspace(workspace, flce_embedding_backward_workspace_size(N, H, V), dev)
+    workspace = _workspace("flce_embedding_backward", workspace,
+                           flce_embedding_backward_workspace_size(N, H, V), dev)
     _run("flce_embedding_backward", dev, _lib.load().flce_embedding_backward, tokens.data_ptr(),
          dout.data_ptr(), ld, N, H, V, int(padding_index), float(scale), dW.data_ptr(),
          int(bool(accumulate_dW)), _stream(dev), code, gcode,
@@ -430,7 +434,7 @@ def flce_logprobs(h: torch.Tensor, W: torch.Tensor, tokens: Optional[torch.Tenso
         _check_tensor("status", status, (), torch.int32, dev)
     lib = _lib.load()
     need = lib.flce_logprobs_workspace_size(N, H, V, code, top_k)
-    workspace = _workspace(workspace, need, dev)
+    workspace = _workspace("flce_logprobs", workspace, need, dev)
     _run("flce_logprobs", dev, lib.flce_logprobs, h.data_ptr(), W.data_ptr(), _ptr(tokens), N, H,
          V, int(ignore_index), float(softcap), float(temperature), top_k, _ptr(logp),
          entropy.data_ptr(), lse.data_ptr(), top_logp.data_ptr() if top_k else None,
@@ -495,10 +499,9 @@ def flce_logprobs_backward(h: torch.Tensor, W: torch.Tensor, tokens: torch.Tenso
         _check_tensor("status", status, (), torch.int32, dev)
     lib = _lib.load()
     need = lib.flce_logprobs_backward_workspace_size(N, H, V, code, gcode)
-    if need == 0:
-        raise FlceError(_lib.ERR_UNSUPPORTED if W.dtype == torch.float32 else _lib.ERR_ARG,
-                        "flce_logprobs_backward_workspace_size")
-    workspace = _workspace(workspace, need, dev)
+    if need == 0 and W.dtype == torch.float32 and gdt == torch.bfloat16:
+        raise FlceError(_lib.ERR_UNSUPPORTED, "flce_logprobs_backward_workspace_size")
+    workspace = _workspace("flce_logprobs_backward", workspace, need, dev)
     _run("flce_logprobs_backward", dev, lib.flce_logprobs_backward, h.data_ptr(), W.data_ptr(),
          tokens.data_ptr(), lse.data_ptr(), _ptr(entropy), _ptr(grad_logp), _ptr(grad_entropy), N,
          H, V, int(ignore_index), float(softcap), float(temperature), dH.data_ptr(),
