@@ -528,8 +528,8 @@ int flce_embedding_backward(const int64_t* tokens, const void* dout, int64_t ld_
  * The workspace (256-byte aligned) is flce_logprobs_workspace_size bytes: partial
  * sums of up to 8192 tokens at a time, the gathered rows, padded copies for a bf16 H
  * that is not a multiple of 8 and N > 128, and with top_k > 0 the candidates: up to 32
- * for each token and 128 vocabulary rows, or the logits themselves (bf16 with
- * N <= 128, float32), as many tokens at a time as fit 1 GiB.
+ * for each token and 128 vocabulary rows, or the logits themselves (float32), as many
+ * tokens at a time as fit 1 GiB; for bf16 with N <= 128 the logits of all N rows.
  * flce_logprobs_check_args: FLCE_ERR_ARG for sizes as in flce_check_args, top_k
  * outside [0, FLCE_MAX_TOP], softcap negative or not finite, temperature not
  * positive, not finite or without a finite inverse, a missing or contradicting

@@ -107,7 +107,7 @@ bool make_lp_plan(int64_t N, int64_t H, int64_t V, int dtype, int top_k, bool to
     q.lists = ceil_div(V, q.list_rows);
     q.kc = lp_candidates(top_k);
   }
-  if (top_k > 0) {
+  if (top_k > 0 && !q.few) {            // the few-token kernel takes all rows at once
     const int64_t per_token = q.tiles ? q.lists * q.kc * 5 : V * 4;
     const int64_t fit = kLpListBytes / per_token / step * step;
     if (nc > fit) nc = fit > step ? fit : step;

@@ -115,7 +115,8 @@ constexpr int64_t kLpRows = 64;
 // Vocabulary up to which the 64-row tiles are joined with alternatives: 32 of the
 // join's 1024 threads hold at most 2048 tiles.
 constexpr int64_t kLpMaxTopV = int64_t(64) * 1024 * kLpRows;
-// Bytes of candidates (lists, or logits) per token chunk, and tokens per chunk.
+// Bytes of candidates (lists, or logits) per token chunk, and tokens per chunk. The
+// few-token kernel has one chunk.
 constexpr int64_t kLpListBytes = int64_t(1) << 30;
 constexpr int64_t kLpMaxChunk = 8192;
 
@@ -147,6 +148,8 @@ struct LpPlan {
 };
 
 bool make_lp_plan(int64_t N, int64_t H, int64_t V, int dtype, int top_k, bool tokens, LpPlan* p);
+// Tokens of the largest launch: the few-token kernel takes all of a call at once.
+inline int64_t lp_launch_rows(const LpPlan& q, int64_t N) { return q.few || N < q.nc ? N : q.nc; }
 
 // Vocabulary tiles of a chunk of nt tokens whose candidates are extracted first, to
 // give the others a bound; 0: all at once. A sixteenth of them, at least one round of

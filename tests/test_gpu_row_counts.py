@@ -58,3 +58,21 @@ def test_the_last_rows_of_a_long_call():
     first = m.flce_logprobs(h[:300], W, y[:300], top_k=5)
     assert all(torch.equal(a[8192:], b) for a, b in zip(whole, last))
     assert all(torch.equal(a[:300], b) for a, b in zip(whole, first))
+
+
+def test_many_rows_over_millions_of_ids():
+    """The logits of 100 rows over a vocabulary of more than 2^21 ids (844 MB) and of 128
+    over 2^22 (2 GiB) with alternatives, next to the first rows alone."""
+    import lm_head_linear_amd as m
+    g = torch.Generator().manual_seed(1)
+    for N, V in ((100, 2200001), (128, 4194304)):
+        W = torch.randn(V, 8, generator=g).bfloat16().cuda()
+        h = torch.randn(N, 8, generator=g).bfloat16().cuda()
+        y = torch.randint(0, V, (N,), generator=g).cuda()
+        whole = m.flce_logprobs(h, W, y, top_k=3)
+        for n in (1, 40):
+            part = m.flce_logprobs(h[N - n:], W, y[N - n:], top_k=3)
+            assert all(torch.equal(a[N - n:], b) for a, b in zip(whole, part))
+        x = h[-1].double() @ W.double().t()
+        assert abs(float(whole.lse[-1]) - float(torch.logsumexp(x, 0))) < 1e-4
+        assert bool((x[whole.top_ids[-1]] >= x.topk(3).values.min() - 1e-4).all())
