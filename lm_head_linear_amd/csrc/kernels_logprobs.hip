@@ -62,6 +62,10 @@ __device__ __forceinline__ float minus(float a, float b) {
 #pragma clang fp contract(off)
   return a - b;
 }
+// How far the max of a part lies below another one, m - M. Held above -1e30, where the
+// part's factor exp(m - M) is 0 and the factor of its weighted sum still finite: the
+// difference of two logits may leave float32's range.
+__device__ __forceinline__ float below(float m, float M) { return fmaxf(minus(m, M), -1e30f); }
 // dx / dz
 template <bool SOFTCAP>
 __device__ __forceinline__ float warp_slope(const Warp& w, float z) {
@@ -322,8 +326,10 @@ struct EpiLp {
     const float M = fmaxf(a.x, b.x);
     float S = 0.f, D = 0.f;
     auto add = [&](const float4& q) {
-      if (q.x == -INFINITY && q.y == 0.f) return;
-      const float dl = q.x - M, f = __builtin_amdgcn_exp2f(dl * kLog2e);
+      // nothing from so far below, also where the difference leaves float32's range; NaN stays
+      const float dl = q.x == M ? 0.f : q.x - M;
+      if (dl < -1e30f && q.y == q.y) return;
+      const float f = __builtin_amdgcn_exp2f(dl * kLog2e);
       S += q.y * f;
       D += f * fmaf(dl, q.y, q.z);
     };
@@ -774,10 +780,10 @@ __device__ __forceinline__ void write_alternative(const JoinArgs& a, int64_t o, 
 __device__ __forceinline__ void join_part(float& M, float& S, float& D, float m, float s, float d) {
   if (m == -INFINITY && s == 0.f) return;
   const float Mn = fmaxf(M, m);
-  const float a = M == -INFINITY ? 0.f : exp2f((M - Mn) * kLog2e);
-  const float b = exp2f((m - Mn) * kLog2e);
-  // spelled out: which product is contracted decides the last bit
-  D = fmaf(b, fmaf(m - Mn, s, d), M == -INFINITY ? 0.f : a * fmaf(M - Mn, S, D));
+  const float da = below(M, Mn), db = below(m, Mn);
+  const float a = exp2f(da * kLog2e), b = exp2f(db * kLog2e);
+  // spelled out: what is contracted decides the last bit
+  D = fmaf(b, fmaf(db, s, d), a * fmaf(da, S, D));
   S = fmaf(s, b, S * a);
   M = Mn;
 }
@@ -1234,8 +1240,8 @@ __global__ __launch_bounds__(kFewThreads) void k_lp_join_few(JoinArgs a) {
     if (p1 != p) join_part(M, S, D, m1.x, m1.y, d1);
   }
   const float Mw = wave_all(M, MaxOp());
-  const float f = M == -INFINITY ? 0.f : exp2f((M - Mw) * kLog2e);
-  D = wave_all(M == -INFINITY ? 0.f : f * fmaf(M - Mw, S, D), AddOp());
+  const float dl = below(M, Mw), f = exp2f(dl * kLog2e);
+  D = wave_all(f * fmaf(dl, S, D), AddOp());
   S = wave_all(S == 0.f ? 0.f : S * f, AddOp());
   if (lane == 0) { red[0][w] = Mw; red[1][w] = S; red[2][w] = D; }
   if (K > 0) {
