@@ -16,18 +16,18 @@
 // Three kernels compute logits:
 //  - the 256 x 256 bf16 tiles of the head's own forward (gemm_bf16.h), live tokens
 //    gathered first: bound by the matrix cores;
-//  - few bf16 tokens: 64 vocabulary rows a workgroup, W streamed from memory
+//  - few bf16 tokens: 64 or 128 vocabulary rows a workgroup, W streamed from memory
 //    straight into the matrix cores' operand registers: bound by reading W once;
 //  - float32: 64 x 64 tiles on the float32 matrix instruction.
 // The 256 x 256 tiles never store a logit; each leaves its top_k largest logits
-// that could still be listed, sorted, and the join merges those lists. The two
-// kernels of 64 vocabulary rows store the logits of their few tokens (N V 4 bytes
-// next to the V H 2 of W) and each tile's largest; the join then looks only into
-// the top_k tiles of the largest, which hold all top_k alternatives.
+// that could still be listed, and the join selects from those lists. The other two
+// store the logits of their tokens (N V 4 bytes, for few tokens next to the V H 2 of W)
+// and the largest of each 64 vocabulary rows; the join then looks only into the top_k
+// of those parts with the largest, which hold all top_k alternatives.
 //
-// Measured: 6144 live rows of 4096 over 131072 with 8 alternatives 4.88 ms in the tiles
-// (1352 TFLOP/s; 3690 rows without alternatives 2.90 ms, 1369 TFLOP/s); one row over
-// the same table 199 us (5.4 TB/s); float32 512 rows of 1024 over 32000 303 us (111
+// Measured: 6144 live rows of 4096 over 131072 with 8 alternatives 5.02 ms in the tiles
+// (1315 TFLOP/s; 3687 rows without alternatives 2.87 ms, 1380 TFLOP/s); one row over
+// the same table 200 us (5.4 TB/s); float32 512 rows of 1024 over 32000 303 us (111
 // TFLOP/s, where the library's product of that type reaches 138).
 #include <hip/hip_runtime.h>
 
@@ -85,7 +85,7 @@ struct LpOut {
   float* zt;                  // x of the given token, one writer per token
   float* cv;                  // 256 x 256 tiles: candidates, -inf behind the last,
   uint8_t* ci;                //   and their rows within the list
-  float* zmax;                // 64-row tiles: the largest raw logit
+  float* zmax;                // parts of 64 rows: the largest raw logit
   float* z;                   //   and all of them, [token][vocabulary]; null: not wanted
   int64_t sp, st, cl, ck, ct;
   int kc, top_k;
@@ -341,7 +341,7 @@ struct EpiLp {
   }
 };
 
-// ---- epilogue of the 64-row tiles ---------------------------------------------------
+// ---- epilogue of parts of 64 rows ---------------------------------------------------
 // z[e] is the raw logit of row q E + e (q = this lane's place among the TPT adjacent
 // lanes of token t, E = 64 / TPT) of the 64 vocabulary rows from v0; `live` exist.
 template <int TPT, bool SOFTCAP>
@@ -925,8 +925,8 @@ __global__ __launch_bounds__(JT * G) void k_lp_join(JoinArgs a) {
 // a list each, held in registers (the candidates of a token lie together). The
 // top_k-th largest of the lists' largest keys bounds the alternatives, and at most top_k
 // lists reach it: their keys from the bound up go to LDS, where each counts the larger
-// ones. With 20 alternatives (us, and by sorted lists): 529 rows over 308 lists
-// 22 and 112, 272 over 194 13 and 87, 456 over 16 13 and 43. "Sorted lists": a thread's
+// ones. With 20 alternatives (us, and by sorted lists): 529 rows over 307 lists
+// 21 and 112, 272 over 194 12 and 87, 456 over 16 13 and 43. "Sorted lists": a thread's
 // lists sorted and merged in registers, then the threads' pairwise through LDS; for the
 // first tiles of 2000 rows over 32000 with 20 alternatives that made the call 284 us, this
 // 236.
@@ -1078,7 +1078,7 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void k_lp_join_dense(JoinArgs a)
 // workgroup, 32 threads for each. Every candidate goes to a list in LDS, with the
 // top_k of the tiles before, and the top_k of those are selected (join_sparse.h); a list
 // that overflows is filled again from its own top_k-th key on. 1946 rows over 186 lists
-// with 5 alternatives 13 us, 6144 rows over 1984 lists with 8 49 us.
+// with 5 alternatives 13 us, 6144 rows over 1984 lists with 8 51 us.
 constexpr int kSparseTokens = 16;
 
 struct WorkgroupEnv {
@@ -1293,7 +1293,10 @@ __global__ __launch_bounds__(kFewThreads) void k_lp_join_few(JoinArgs a) {
 // c1 = -b, formed once per live token in the gathered order. A token outside the
 // vocabulary gets NaN: its gradients fail closed, as the head's loss does.
 //
-// G goes to the products as bf16, off by up to 2^-9 of itself. That adds up where it
+// G goes to the products as bf16, off by up to 2^-8 of itself: a pair of bf16, which
+// float32 gradients use, takes a step of 3687 rows of 4096 over 131072 from 8.9 to 15.4 ms.
+// dH and dW are then off by 0.0021 to 0.0024 of their norm, where rounding the exact ones
+// to bf16 leaves 0.0017. That adds up where it
 // matters most: the G of the given tokens is by far the largest of its row, and the
 // dW row of a frequent token is the sum of many of them, often of either sign. So
 // what rounding those left is kept in float32 and added to dW afterwards, a weighted

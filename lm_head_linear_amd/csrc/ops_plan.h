@@ -110,7 +110,8 @@ inline void carve_embed(const EmbedPlan& p, char* ws, EmbedGradArgs* a) {
 // Tokens up to which a bf16 call streams W once through the few-token kernel
 // instead of the 256 x 256 tiles (see kernels_logprobs.hip for both sides).
 constexpr int64_t kFewTokens = 128;
-// Vocabulary rows per workgroup of the few-token and float32 kernels.
+// Vocabulary rows per part of the few-token kernel (one or two parts a workgroup) and of
+// the float32 one (one).
 constexpr int64_t kLpRows = 64;
 // Vocabulary up to which the 64-row tiles are joined with alternatives: 32 of the
 // join's 1024 threads hold at most 2048 tiles.
