@@ -563,11 +563,13 @@ int flce_logprobs(const void* h, const void* W, const int64_t* tokens, int64_t N
  * chunk; G is rounded to bf16 once for bf16 inputs (kept as a bf16 pair with
  * grad_dtype FLCE_F32), the products are those of flce_forward_backward, and so
  * are accumulate_dW and grad_dtype. What that rounding takes from the given token's
- * G, the largest of its row, is added to dW[token] afterwards. Ignored rows give dH rows of zeros; a token
- * outside [0, V) gives NaN in its dH row and in dW, and FLCE_ERR_LABEL in
- * *status. The same bits on every run. N = 0 zeroes dW unless it accumulates.
+ * G, the largest of its row, is added to its dH row and to dW[token] before those are
+ * rounded. Ignored rows give dH rows of zeros; a token outside [0, V) gives NaN in its dH
+ * row and in dW, and FLCE_ERR_LABEL in *status. The same bits on every run. N = 0 zeroes
+ * dW unless it accumulates.
  * The workspace (256-byte aligned) is flce_logprobs_backward_workspace_size
- * bytes (0 for invalid sizes). Errors as flce_logprobs_check_args.
+ * bytes (0 for invalid sizes): for bf16 gradients the head's, two float32 rows of H for each
+ * token and 4 V bytes. Errors as flce_logprobs_check_args.
  */
 size_t flce_logprobs_backward_workspace_size(int64_t N, int64_t H, int64_t V, int dtype,
                                              int grad_dtype);

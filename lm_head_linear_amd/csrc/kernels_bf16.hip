@@ -583,16 +583,29 @@ __device__ __forceinline__ void staged_rows(Acc& acc, int wm, int wn, int lane, 
 }
 
 // ---- dW epilogue: rows v0 + m of dW, bf16, optionally added to ------------
-template <bool ACCUM>
+// KEEP: the rows that have a slot go to `keep` in float32 instead, where what is
+// still missing from them is added before they are rounded (Args::dw_slot).
+template <bool ACCUM, bool KEEP = false>
 struct EpiDW {
   uint16_t* dW;
   int64_t H, v0, vcur;
+  const uint32_t* slot = nullptr;
+  float* keep = nullptr;
 
   struct Pass {
     const EpiDW& e;
     int64_t r0, c0;   // global (chunk-relative row, column) of the wave block
+    // KEEP: the slots of rows lane and 64 + lane of the wave's 128, and which rows
+    // have one
+    uint32_t at[2] = {0, 0};
+    uint64_t any[2] = {0, 0};
     __device__ __forceinline__ void prefetch(int, int) {}
-    __device__ __forceinline__ void store(int i, int, int row, int col, float4 v) {
+    __device__ __forceinline__ void store(int i, int q, int row, int col, float4 v) {
+      uint32_t s = 0;
+      if constexpr (KEEP) {                        // rows 2 q and 2 q + 1 of block i
+        const int rr = i * 32 + 2 * q;
+        if ((any[rr >> 6] >> (rr & 63)) & 3) s = __shfl(at[rr >> 6], (i * 32 + row) & 63);
+      }
       const int64_t m = r0 + i * 32 + row, n = c0 + col;
       if (m >= e.vcur || n >= e.H) return;
       uint16_t* p = e.dW + (e.v0 + m) * e.H + n;
@@ -600,6 +613,10 @@ struct EpiDW {
         const uint2 o = *reinterpret_cast<const uint2*>(p);
         v.x += bf16_to_f32(uint16_t(o.x)); v.y += bf16_to_f32(uint16_t(o.x >> 16));
         v.z += bf16_to_f32(uint16_t(o.y)); v.w += bf16_to_f32(uint16_t(o.y >> 16));
+      }
+      if (KEEP && s != 0) {
+        *reinterpret_cast<float4*>(e.keep + int64_t(s - 1) * e.H + n) = v;
+        return;
       }
       *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
     }
@@ -611,6 +628,14 @@ struct EpiDW {
   __device__ __forceinline__ void operator()(Acc& acc, int64_t m0, int64_t n0, int wm, int wn,
                                              int lane, char* smem, const char*) const {
     Pass pass{*this, m0 + wm * 128, n0 + wn * 128};
+    if constexpr (KEEP) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const int64_t m = pass.r0 + b * 64 + lane;
+        pass.at[b] = m < vcur ? slot[v0 + m] : 0;
+        pass.any[b] = __ballot(pass.at[b] != 0);
+      }
+    }
     staged_rows(acc, wm, wn, lane, smem, pass);
   }
 };
@@ -783,14 +808,23 @@ struct EpiDHPart {
 // first), after the float32 running sum of the earlier vocabulary chunks
 // when there is one (PRIOR), stored as the new running sum or, for the last
 // chunk, as bf16 dH rounded to nearest even (BF16OUT). Four consecutive
-// elements per thread; n4 = elements / 4, stride = elements per segment.
-template <bool PRIOR, bool BF16OUT>
+// elements per thread; n4 = elements / 4, stride = elements per segment. REST: before
+// that rounding row m gets rest[m] W[y[m]], what rounding G of its label left.
+struct DhRest {
+  const float* rest;
+  const int64_t* y;
+  const uint16_t* W;
+  int64_t V;
+};
+
+template <bool PRIOR, bool BF16OUT, bool REST>
 __global__ __launch_bounds__(256) void k_dh_reduce(const float* __restrict__ part, int segs,
                                                    int64_t n4, int64_t stride,
                                                    const float* prior, float* out32,
                                                    uint16_t* out16, int64_t H,
                                                    const int64_t* __restrict__ rows_dyn,
-                                                   const int32_t* __restrict__ row_map) {
+                                                   const int32_t* __restrict__ row_map,
+                                                   DhRest rest) {
   // a compact plan: only the first *rows_dyn rows, the bf16 row m at row_map[m]
   if (rows_dyn) {
     const int64_t n4d = *rows_dyn * (H / 4);
@@ -805,9 +839,20 @@ __global__ __launch_bounds__(256) void k_dh_reduce(const float* __restrict__ par
     }
     if (BF16OUT) {
       int64_t o = i;
-      if (row_map) {
-        const int64_t m = i / (H / 4);
-        o = int64_t(row_map[m]) * (H / 4) + (i - m * (H / 4));
+      if (REST || row_map) {
+        const int64_t m = i / (H / 4), c4 = i - m * (H / 4);
+        if (row_map) o = int64_t(row_map[m]) * (H / 4) + c4;
+        if constexpr (REST) {
+          const int64_t y = rest.y[m];
+          if (y >= 0 && y < rest.V) {              // otherwise the row is NaN
+            const float r = rest.rest[m];
+            const uint2 w = reinterpret_cast<const uint2*>(rest.W + y * H)[c4];
+            v.x = fmaf(r, bf16_to_f32(uint16_t(w.x)), v.x);
+            v.y = fmaf(r, bf16_to_f32(uint16_t(w.x >> 16)), v.y);
+            v.z = fmaf(r, bf16_to_f32(uint16_t(w.y)), v.z);
+            v.w = fmaf(r, bf16_to_f32(uint16_t(w.y >> 16)), v.w);
+          }
+        }
       }
       reinterpret_cast<uint2*>(out16)[o] = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
     } else {
@@ -818,23 +863,23 @@ __global__ __launch_bounds__(256) void k_dh_reduce(const float* __restrict__ par
 
 hipError_t launch_dh_reduce(const float* part, int64_t segs, int64_t n, const float* prior,
                             float* out32, uint16_t* out16, const Launcher& L, int64_t H,
-                            const int64_t* rows_dyn = nullptr, const int32_t* row_map = nullptr) {
+                            const int64_t* rows_dyn = nullptr, const int32_t* row_map = nullptr,
+                            const DhRest& rest = {}) {
   const int64_t n4 = n / 4;
   const int64_t want = (n4 + 255) / 256;
   const dim3 grid(unsigned(want < 4096 ? want : 4096));
+  auto run = [&](auto has_prior, auto out, auto has_rest) {
+    hipLaunchKernelGGL((k_dh_reduce<decltype(has_prior)::value, decltype(out)::value,
+                                    decltype(has_rest)::value>),
+                       grid, dim3(256), 0, L.stream, part, int(segs), n4, n, prior, out32, out16,
+                       H, rows_dyn, row_map, rest);
+  };
+  using Y = std::true_type;
+  using No = std::false_type;
   L.pre(kDhReduce);
-  if (prior && out16)
-    hipLaunchKernelGGL((k_dh_reduce<true, true>), grid, dim3(256), 0, L.stream, part, int(segs),
-                       n4, n, prior, out32, out16, H, rows_dyn, row_map);
-  else if (prior)
-    hipLaunchKernelGGL((k_dh_reduce<true, false>), grid, dim3(256), 0, L.stream, part, int(segs),
-                       n4, n, prior, out32, out16, H, rows_dyn, row_map);
-  else if (out16)
-    hipLaunchKernelGGL((k_dh_reduce<false, true>), grid, dim3(256), 0, L.stream, part, int(segs),
-                       n4, n, prior, out32, out16, H, rows_dyn, row_map);
-  else
-    hipLaunchKernelGGL((k_dh_reduce<false, false>), grid, dim3(256), 0, L.stream, part,
-                       int(segs), n4, n, prior, out32, out16, H, rows_dyn, row_map);
+  if (!out16) prior ? run(Y{}, No{}, No{}) : run(No{}, No{}, No{});
+  else if (!rest.rest) prior ? run(Y{}, Y{}, No{}) : run(No{}, Y{}, No{});
+  else prior ? run(Y{}, Y{}, Y{}) : run(No{}, Y{}, Y{});
   L.post(kDhReduce);
   return hipGetLastError();
 }
@@ -1057,20 +1102,43 @@ hipError_t bf16_chunk_products(const Plan& p, const Args& a, int64_t chunk, cons
   const gemm::Launch lw = gemm::backward_launch(p, chunk, 1);
   const gemm::Launch lh = gemm::backward_launch(p, chunk, 2);
   const bool first = chunk == 0, last = chunk == p.n_chunks - 1;
+  const DhRest rest{a.rest, a.yc, static_cast<const uint16_t*>(a.W), p.V};
   if (p.dh_kseg) {
     // few dH output tiles: dH split along K, then dW, in one grid, and the
     // segments' partial products added up in a fixed order afterwards
     const int64_t segs = (lh.K + p.dh_kseg - 1) / p.dh_kseg;
     const EpiDHPart ep{a.dh_part, p.N, p.H, p.N * p.H};
-    if (a.accumulate_dW)
-      err = run_gemm_pair<NF, TF, kDynM, TF, TF, kDynK, true>(
-          lh, ep, lw, EpiDW<true>{dW, p.H, v0, vcur}, a, kGemmDWDH, L, nv, p.dh_kseg, segs);
+    auto pair = [&](auto edw) {
+      return run_gemm_pair<NF, TF, kDynM, TF, TF, kDynK, true>(lh, ep, lw, edw, a, kGemmDWDH, L,
+                                                               nv, p.dh_kseg, segs);
+    };
+    if (a.rest)
+      err = a.accumulate_dW ? pair(EpiDW<true, true>{dW, p.H, v0, vcur, a.dw_slot, a.dw_keep})
+                            : pair(EpiDW<false, true>{dW, p.H, v0, vcur, a.dw_slot, a.dw_keep});
     else
-      err = run_gemm_pair<NF, TF, kDynM, TF, TF, kDynK, true>(
-          lh, ep, lw, EpiDW<false>{dW, p.H, v0, vcur}, a, kGemmDWDH, L, nv, p.dh_kseg, segs);
+      err = a.accumulate_dW ? pair(EpiDW<true>{dW, p.H, v0, vcur})
+                            : pair(EpiDW<false>{dW, p.H, v0, vcur});
     if (err != hipSuccess) return err;
     return launch_dh_reduce(a.dh_part, segs, p.N * p.H, first ? nullptr : a.dh_acc,
-                            last ? nullptr : a.dh_acc, last ? dH : nullptr, L, p.H, nv, a.idx);
+                            last ? nullptr : a.dh_acc, last ? dH : nullptr, L, p.H, nv, a.idx,
+                            rest);
+  }
+  if (a.rest) {
+    // dH stays a float32 running sum to the end, where what rounding G left is added
+    if (!a.dh_acc) return hipErrorInvalidValue;
+    auto pair = [&](auto edh) {
+      if (a.accumulate_dW)
+        return run_gemm_pair<NF, TF, kDynM, TF, TF, kDynK>(
+            lh, edh, lw, EpiDW<true, true>{dW, p.H, v0, vcur, a.dw_slot, a.dw_keep}, a, kGemmDWDH,
+            L, nv);
+      return run_gemm_pair<NF, TF, kDynM, TF, TF, kDynK>(
+          lh, edh, lw, EpiDW<false, true>{dW, p.H, v0, vcur, a.dw_slot, a.dw_keep}, a, kGemmDWDH,
+          L, nv);
+    };
+    err = first ? pair(EpiDH<true, false>{dH, a.dh_acc, p.N, p.H, a.idx})
+                : pair(EpiDH<false, false>{dH, a.dh_acc, p.N, p.H, a.idx});
+    if (err != hipSuccess || !last) return err;
+    return launch_dh_reduce(nullptr, 0, p.N * p.H, a.dh_acc, nullptr, dH, L, p.H, nv, a.idx, rest);
   }
   // dH's tiles and then dW's in one grid
   auto pair = [&](auto edh) {

@@ -381,7 +381,9 @@ struct SumArgs {
   const uint32_t* skey;
   const uint32_t* spos;
   const void* dout;
-  const float* weight;        // WEIGHT: row i counts weight[i] times
+  const float* weight;        // WEIGHT: row i counts weight[i] times, and what is added
+  const uint32_t* slot;       //   to are the float32 rows slot[id] - 1 of keep, not dW
+  const float* keep;
   int64_t ldd, N, H, V, slices;
   float scale;
   void* dW;
@@ -419,6 +421,7 @@ __device__ __forceinline__ void sum_slice(const SumArgs& a, int64_t wd, const Sl
   const int64_t il = n > 0 ? i0 + (li < n ? li : n - 1) : 0;
   const uint32_t keys = n > 0 ? a.skey[il] : none, poss = n > 0 ? a.spos[il] : 0;
   const float wgts = WEIGHT && keys < none ? a.weight[poss] : 1.f;
+  const uint32_t slots = WEIGHT && keys < none ? a.slot[keys] - 1 : 0;
   const uint32_t before = i0 > 0 && n > 0 ? a.skey[i0 - 1] : none;
   const uint32_t behind = n == SW && i0 + n < N ? a.skey[i0 + n] : none;
   auto uni = [](uint32_t x) -> uint32_t { return __builtin_amdgcn_readfirstlane(x); };
@@ -447,7 +450,10 @@ __device__ __forceinline__ void sum_slice(const SumArgs& a, int64_t wd, const Sl
       sl.load(dout + int64_t(uint32_t(__builtin_amdgcn_readlane(poss, q + r))) * a.ldd, f[r]);
       if constexpr (ADD) {
         const uint32_t key = key_of(q + r);
-        sl.load(dW + int64_t(key < none ? key : 0) * H, g[r]);
+        if constexpr (WEIGHT)
+          sl.load(a.keep + int64_t(uint32_t(__builtin_amdgcn_readlane(slots, q + r))) * H, g[r]);
+        else
+          sl.load(dW + int64_t(key < none ? key : 0) * H, g[r]);
       }
     }
 #pragma unroll
@@ -514,7 +520,7 @@ __global__ __launch_bounds__(64 * kSumWaves) void k_embed_sum(SumArgs a) {
 
 // The ids that reach past the workgroup's tokens they begin in: their partial rows
 // added up in order. A wave per workgroup's tokens and slice; most have none.
-template <class G, bool ADD, bool FULL>
+template <class G, bool WEIGHT, bool ADD, bool FULL>
 __device__ __forceinline__ void join_slice(const SumArgs& a, int64_t win, int64_t wd,
                                            const Slice<FULL>& sl) {
   const int64_t H = a.H, i0 = wd * win, i1 = i0 + win;
@@ -526,7 +532,8 @@ __device__ __forceinline__ void join_slice(const SumArgs& a, int64_t win, int64_
   G* row = static_cast<G*>(a.dW) + int64_t(key) * H;
   float acc[8], old[8] = {};
   sl.load(a.part + (2 * wd + 1) * H, acc);
-  if constexpr (ADD) sl.load(row, old);
+  if constexpr (WEIGHT) sl.load(a.keep + int64_t(a.slot[key] - 1) * H, old);
+  else if constexpr (ADD) sl.load(row, old);
   // those behind that begin with this id, their rows loaded eight at a time
   const int64_t windows = (a.N + win - 1) / win;
   bool more = true;
@@ -554,13 +561,13 @@ __device__ __forceinline__ void join_slice(const SumArgs& a, int64_t win, int64_
   sl.store(row, acc);
 }
 
-template <class G, bool ADD>
+template <class G, bool WEIGHT, bool ADD>
 __global__ __launch_bounds__(256) void k_embed_join(SumArgs a, int64_t win) {
   const int lane = threadIdx.x & 63;
   const int64_t u = int64_t(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t wd = u / a.slices, c0 = (u - wd * a.slices) * kSliceCols;
-  if (c0 + kSliceCols <= a.H) join_slice<G, ADD>(a, win, wd, Slice<true>{c0, a.H, lane});
-  else join_slice<G, ADD>(a, win, wd, Slice<false>{c0, a.H, lane});
+  if (c0 + kSliceCols <= a.H) join_slice<G, WEIGHT, ADD>(a, win, wd, Slice<true>{c0, a.H, lane});
+  else join_slice<G, WEIGHT, ADD>(a, win, wd, Slice<false>{c0, a.H, lane});
 }
 
 template <class T, class G, bool WEIGHT = false>
@@ -568,8 +575,8 @@ hipError_t sums(const EmbedGradArgs& a, const uint32_t* key, const uint32_t* pos
                 const Launcher& L) {
   const int64_t slices = (a.H + kSliceCols - 1) / kSliceCols, win = embed_window(a.N);
   const int64_t windows = (a.N + win - 1) / win;
-  const SumArgs s{key, pos, a.dout, a.weight, a.ld_dout, a.N, a.H, a.V, slices, a.scale, a.dW,
-                  a.part};
+  const SumArgs s{key, pos, a.dout, a.weight, a.slot, a.keep, a.ld_dout, a.N, a.H, a.V, slices,
+                  a.scale, a.dW, a.part};
   auto run = [&](auto add) {
     constexpr bool ADD = decltype(add)::value;
     const dim3 grid(unsigned(windows * slices)), block(64 * kSumWaves);
@@ -582,7 +589,7 @@ hipError_t sums(const EmbedGradArgs& a, const uint32_t* key, const uint32_t* pos
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || windows == 1) return e;
     L.pre(kEmbedGrad);
-    hipLaunchKernelGGL((k_embed_join<G, ADD>), dim3(unsigned((windows * slices + 3) / 4)),
+    hipLaunchKernelGGL((k_embed_join<G, WEIGHT, ADD>), dim3(unsigned((windows * slices + 3) / 4)),
                        dim3(256), 0, L.stream, s, win);
     L.post(kEmbedGrad);
     return hipGetLastError();
@@ -592,52 +599,31 @@ hipError_t sums(const EmbedGradArgs& a, const uint32_t* key, const uint32_t* pos
   return run(std::true_type{});
 }
 
-}  // namespace
-
-hipError_t launch_embedding(const EmbedArgs& a, const Launcher& L) {
-  const int64_t e = a.dtype == FLCE_BF16 ? 8 : 4;
-  const int64_t units = (a.H + kUnitChunks * e - 1) / (kUnitChunks * e);
-  const dim3 grid(unsigned((a.N * units + 3) / 4));
-  L.pre(kEmbed);
-  if (a.dtype == FLCE_BF16)
-    hipLaunchKernelGGL(k_embed<Bf16Bits>, grid, dim3(256), 0, L.stream, a.tokens,
-                       static_cast<const Bf16Bits*>(a.W), a.N, a.H, a.V, a.padding, a.scale,
-                       static_cast<Bf16Bits*>(a.out), a.ld_out, units);
-  else
-    hipLaunchKernelGGL(k_embed<float>, grid, dim3(256), 0, L.stream, a.tokens,
-                       static_cast<const float*>(a.W), a.N, a.H, a.V, a.padding, a.scale,
-                       static_cast<float*>(a.out), a.ld_out, units);
-  L.post(kEmbed);
-  hipError_t r = hipGetLastError();
-  if (r != hipSuccess || !a.status) return r;
-  return launch_token_status(a.tokens, a.N, a.V, a.padding, a.status, L);
+// slot[v] = 1 + the sorted position of id v's first token; of ids without one it stays.
+__global__ __launch_bounds__(256) void k_token_slots(const uint32_t* __restrict__ skey, int64_t N,
+                                                     uint32_t none, uint32_t* __restrict__ slot) {
+  const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= N) return;
+  const uint32_t k = skey[i];
+  if (k < none && (i == 0 || skey[i - 1] != k)) slot[k] = uint32_t(i) + 1;
 }
 
-hipError_t launch_token_status(const int64_t* tokens, int64_t N, int64_t V, int64_t padding,
-                               int32_t* status, const Launcher& L) {
-  L.pre(kEmbedSort);
-  hipLaunchKernelGGL(k_token_status, dim3(1), dim3(1024), 0, L.stream, tokens, N, V, padding,
-                     status);
-  L.post(kEmbedSort);
-  return hipGetLastError();
-}
-
-hipError_t launch_embedding_backward(const EmbedGradArgs& a, const Launcher& L) {
+// The tokens sorted into list *list of the workspace's two; `bytes` at `clear` are set to
+// zero on the way.
+hipError_t sort_tokens(const EmbedGradArgs& a, void* clear, size_t bytes, const Launcher& L,
+                       int* list) {
   hipError_t e = hipSuccess;
-  if (a.status) e = launch_token_status(a.tokens, a.N, a.V, a.padding, a.status, L);
-  // dW cleared beside the sort as far as it is whole 16-byte pieces, else before it
-  const size_t bytes = a.accumulate ? 0 : size_t(a.V) * a.H * (a.grad_dtype == FLCE_BF16 ? 2 : 4);
-  const bool beside = a.N <= kSortMerge && (reinterpret_cast<uintptr_t>(a.dW) & 15u) == 0;
+  // cleared beside the sort as far as it is whole 16-byte pieces, else before it
+  const bool beside = a.N <= kSortMerge && (reinterpret_cast<uintptr_t>(clear) & 15u) == 0;
   const size_t with = beside ? bytes / 16 * 16 : 0;
-  if (e == hipSuccess)
-    e = launch_zero_bytes(static_cast<char*>(a.dW) + with, bytes - with, L);
+  e = launch_zero_bytes(static_cast<char*>(clear) + with, bytes - with, L);
   if (e != hipSuccess) return e;
   int bits = 1;
   while (bits < 32 && (int64_t(1) << bits) <= a.V) ++bits;   // keys 0 .. V
   int at = 0;
   if (a.N <= kSortMerge) {
     const int64_t chunks = (a.N + kSortChunk - 1) / kSortChunk;
-    Clear fill{static_cast<uint4*>(a.dW), int64_t(with / 16), 0};
+    Clear fill{static_cast<uint4*>(clear), int64_t(with / 16), 0};
     const int64_t pieces = (fill.n16 + 4095) / 4096;
     const int64_t first = chunks > 1 && pieces > 512 ? 512 : pieces;
     L.pre(kEmbedSort);
@@ -675,15 +661,66 @@ hipError_t launch_embedding_backward(const EmbedGradArgs& a, const Launcher& L) 
       at = 1 - at;
     }
   }
+  *list = at;
+  return e;
+}
+
+}  // namespace
+
+hipError_t launch_embedding(const EmbedArgs& a, const Launcher& L) {
+  const int64_t e = a.dtype == FLCE_BF16 ? 8 : 4;
+  const int64_t units = (a.H + kUnitChunks * e - 1) / (kUnitChunks * e);
+  const dim3 grid(unsigned((a.N * units + 3) / 4));
+  L.pre(kEmbed);
+  if (a.dtype == FLCE_BF16)
+    hipLaunchKernelGGL(k_embed<Bf16Bits>, grid, dim3(256), 0, L.stream, a.tokens,
+                       static_cast<const Bf16Bits*>(a.W), a.N, a.H, a.V, a.padding, a.scale,
+                       static_cast<Bf16Bits*>(a.out), a.ld_out, units);
+  else
+    hipLaunchKernelGGL(k_embed<float>, grid, dim3(256), 0, L.stream, a.tokens,
+                       static_cast<const float*>(a.W), a.N, a.H, a.V, a.padding, a.scale,
+                       static_cast<float*>(a.out), a.ld_out, units);
+  L.post(kEmbed);
+  hipError_t r = hipGetLastError();
+  if (r != hipSuccess || !a.status) return r;
+  return launch_token_status(a.tokens, a.N, a.V, a.padding, a.status, L);
+}
+
+hipError_t launch_token_status(const int64_t* tokens, int64_t N, int64_t V, int64_t padding,
+                               int32_t* status, const Launcher& L) {
+  L.pre(kEmbedSort);
+  hipLaunchKernelGGL(k_token_status, dim3(1), dim3(1024), 0, L.stream, tokens, N, V, padding,
+                     status);
+  L.post(kEmbedSort);
+  return hipGetLastError();
+}
+
+hipError_t launch_embedding_backward(const EmbedGradArgs& a, const Launcher& L) {
+  hipError_t e = hipSuccess;
+  if (a.status) e = launch_token_status(a.tokens, a.N, a.V, a.padding, a.status, L);
+  int at = 0;
+  const size_t bytes = a.accumulate ? 0 : size_t(a.V) * a.H * (a.grad_dtype == FLCE_BF16 ? 2 : 4);
+  if (e == hipSuccess) e = sort_tokens(a, a.dW, bytes, L, &at);
   if (e != hipSuccess) return e;
-  if (a.weight) {
-    if (a.dtype != FLCE_BF16 || a.grad_dtype != FLCE_BF16 || !a.accumulate)
-      return hipErrorInvalidValue;
-    return sums<Bf16Bits, Bf16Bits, true>(a, a.key[at], a.pos[at], L);
-  }
   if (a.dtype == FLCE_F32) return sums<float, float>(a, a.key[at], a.pos[at], L);
   if (a.grad_dtype == FLCE_F32) return sums<Bf16Bits, float>(a, a.key[at], a.pos[at], L);
   return sums<Bf16Bits, Bf16Bits>(a, a.key[at], a.pos[at], L);
+}
+
+hipError_t launch_weighted_sort(const EmbedGradArgs& a, const Launcher& L, int* list) {
+  const hipError_t e = sort_tokens(a, a.slot, lp_slot_bytes(a.V), L, list);
+  if (e != hipSuccess) return e;
+  L.pre(kEmbedSort);
+  hipLaunchKernelGGL(k_token_slots, dim3(unsigned((a.N + 255) / 256)), dim3(256), 0, L.stream,
+                     a.key[*list], a.N, uint32_t(a.V), a.slot);
+  L.post(kEmbedSort);
+  return hipGetLastError();
+}
+
+hipError_t launch_weighted_sums(const EmbedGradArgs& a, int list, const Launcher& L) {
+  if (!a.weight || !a.slot || !a.keep || a.dtype != FLCE_BF16 || a.grad_dtype != FLCE_BF16)
+    return hipErrorInvalidValue;
+  return sums<Bf16Bits, Bf16Bits, true>(a, a.key[list], a.pos[list], L);
 }
 
 }  // namespace flce

@@ -1294,14 +1294,16 @@ __global__ __launch_bounds__(kFewThreads) void k_lp_join_few(JoinArgs a) {
 // vocabulary gets NaN: its gradients fail closed, as the head's loss does.
 //
 // G goes to the products as bf16, off by up to 2^-8 of itself: a pair of bf16, which
-// float32 gradients use, takes a step of 3687 rows of 4096 over 131072 from 8.9 to 15.4 ms.
-// dH and dW are then off by 0.0021 to 0.0024 of their norm, where rounding the exact ones
-// to bf16 leaves 0.0017. That adds up where it
-// matters most: the G of the given tokens is by far the largest of its row, and the
-// dW row of a frequent token is the sum of many of them, often of either sign. So
-// what rounding those left is kept in float32 and added to dW afterwards, a weighted
-// lookup gradient over the same rows (a few 10 us next to milliseconds): a row whose
-// terms cancel is then off by half a step of its own value, not of its terms.
+// float32 gradients use, takes the gradients of 3687 rows of 4096 over 131072 from 8.9 to
+// 15.4 ms. That adds up where it matters most: the G of the given tokens is by far the
+// largest of its row, the dW row of a frequent token is the sum of many of them, often of
+// either sign, and what all rows of W share cancels in dH only against it. So what rounding
+// those left is kept in float32. It is added to dH's float32 sums (times W's row of the
+// token) and, a weighted lookup gradient over the same rows, to the float32 dW rows of the
+// tokens, which the products leave beside dW for it; both are then rounded once. That
+// takes 12 us of 563 (2048 rows of 1024 over 32000) and 80 of 12120 (4096 of 4096 over 131072),
+// and leaves dH and dW off by 0.00166 of their norm, as much as rounding the exact ones
+// does (0.0024 and 0.0022 with bf16 G alone and a repair of the rounded dW).
 __global__ __launch_bounds__(256) void k_lp_coef(
     const int32_t* __restrict__ idx, const int64_t* __restrict__ labels,
     const int64_t* __restrict__ count, int64_t N, int64_t V, int64_t ignore_index,
@@ -1318,6 +1320,12 @@ __global__ __launch_bounds__(256) void k_lp_coef(
   c0[r] = -(a + b * s);
   c1[r] = -b;
   ca[r] = a;
+}
+
+// What rounding x to bf16 leaves of it; nothing of infinities and NaN.
+__device__ __forceinline__ float bf16_rest(float x) {
+  const float r = x - bf16_to_f32(f32_to_bf16(x));
+  return fabsf(r) < INFINITY ? r : 0.f;
 }
 
 template <bool SOFTCAP, bool SPLIT>
@@ -1381,7 +1389,7 @@ struct EpiLpGrad {
               if (i == ti && r == tr) { z = acc[i][j][r]; v = grad(i, j, r); }
           tp.pos[j] = target_slot(d, j * 16 + (lane & 15));
           tp.val[j] = fmaf(ca_t[tl], warp_slope<SOFTCAP>(warp, z), v);
-          if (!SPLIT) rest[n0 + tl] = tp.val[j] - bf16_to_f32(f32_to_bf16(tp.val[j]));
+          if (!SPLIT) rest[n0 + tl] = bf16_rest(tp.val[j]);
         }
       }
     }
@@ -1443,7 +1451,7 @@ __global__ __launch_bounds__(256) void k_lp_few_grad(const uint16_t* __restrict_
     float x = __builtin_amdgcn_exp2f(l * kLog2e) * fmaf(-cb, l, k0);
     const bool target = y == a.v0 + at + e && at + e < vcur;
     x = (target ? x + ca : x) * warp_slope<SOFTCAP>(warp, z);
-    if (target) a.rest[t] = x - bf16_to_f32(f32_to_bf16(x));
+    if (target) a.rest[t] = bf16_rest(x);
     g[e] = at + e < vcur ? x : 0.f;
   }
   // 4 (or 8) adjacent columns lie in one block of 32; dH reads whole runs of 8, so the

@@ -171,6 +171,20 @@ int flce_logprobs_backward(const void* h, const void* W, const int64_t* tokens, 
                            reinterpret_cast<float*>(own + 4 * arr)};
   own += 5 * arr;
   if (dtype == FLCE_F32) a.dh_part = reinterpret_cast<float*>(own);
+  // bf16 gradients: what rounding the given tokens' G leaves is added to their dH rows and,
+  // (what was left) h over the gathered rows, to the float32 dW rows of those tokens
+  const bool rest = dtype == FLCE_BF16 && grad_dtype == FLCE_BF16;
+  flce::EmbedGradArgs left{};
+  int list = 0;
+  if (rest) {
+    flce::EmbedPlan ep;
+    if (!flce::make_embed_plan(N, p.H, V, &ep)) return FLCE_ERR_ARG;
+    flce::carve_embed(ep, own, &left);
+    left.slot = reinterpret_cast<uint32_t*>(own + ep.total);
+    a.dw_keep = reinterpret_cast<float*>(own + ep.total + flce::lp_slot_bytes(V));
+    a.dw_slot = left.slot;
+    a.rest = g.rest;
+  }
   {
     Range s("flce.setup");
     e = flce::pad_inputs(p, a, ws, true, L);
@@ -178,6 +192,14 @@ int flce_logprobs_backward(const void* h, const void* W, const int64_t* tokens, 
     if (e == hipSuccess && !p.compact && status)
       e = flce::launch_token_status(tokens, N, V, ignore_index, status, L);
     if (e == hipSuccess) e = flce::launch_lp_coefficients(p, a, g, L);
+    if (rest) {
+      left.tokens = a.yc; left.dout = a.hc; left.ld_dout = p.H;
+      left.N = N; left.H = p.H; left.V = V; left.padding = ignore_index;
+      left.scale = 1.f; left.dW = a.dW; left.accumulate = 1;
+      left.dtype = dtype; left.grad_dtype = grad_dtype;
+      left.weight = g.rest; left.keep = a.dw_keep;
+      if (e == hipSuccess) e = flce::launch_weighted_sort(left, L, &list);
+    }
   }
   for (int64_t c = 0; e == hipSuccess && c < p.n_chunks; ++c) {
     Range s("flce.backward_chunk");
@@ -186,15 +208,9 @@ int flce_logprobs_backward(const void* h, const void* W, const int64_t* tokens, 
       e = dtype == FLCE_BF16 ? flce::bf16_chunk_products(p, a, c, L)
                              : flce::launch_lp_f32_products(p, a, c, L);
   }
-  if (e == hipSuccess && dtype == FLCE_BF16 && grad_dtype == FLCE_BF16) {
-    // dW[token] += (what rounding the token's G left) h, over the gathered rows
+  if (e == hipSuccess && rest) {
     Range s("flce.rounding_rest");
-    flce::EmbedPlan ep;
-    if (!flce::make_embed_plan(N, p.H, V, &ep)) return FLCE_ERR_ARG;
-    flce::EmbedGradArgs r{a.yc, a.hc, p.H, N, p.H, V, ignore_index, 1.f, a.dW, 1, dtype,
-                          grad_dtype, nullptr, {}, {}, nullptr, nullptr, g.rest};
-    flce::carve_embed(ep, own, &r);
-    e = flce::launch_embedding_backward(r, L);
+    e = flce::launch_weighted_sums(left, list, L);
   }
   if (e == hipSuccess) e = flce::crop_outputs(p, ws, dH, dW, L);
   return status_of(e);

@@ -332,14 +332,14 @@ size_t flce_logprobs_backward_workspace_size(int64_t N, int64_t H, int64_t V, in
   Plan p;
   if (!make_lp_backward_plan(N, H, V, dtype, grad_dtype, &p)) return 0;
   // the head's backward, its dummy count, the token coefficients, and the partial
-  // products of a split float32 dH, or the lookup gradient that adds what rounding G
-  // to bf16 left of the given tokens
+  // products of a split float32 dH, or what adds the part of the given tokens' G that
+  // rounding to bf16 left: a sort, the slots and the float32 dW rows of those tokens
   size_t more = 0;
   if (dtype == FLCE_F32) more = align256(lp_f32_part_bytes(p));
   else if (grad_dtype == FLCE_BF16) {
     EmbedPlan e;
     if (!make_embed_plan(N, p.H, V, &e)) return 0;
-    more = e.total;
+    more = e.total + lp_slot_bytes(V) + lp_keep_bytes(N, p.H);
   }
   return p.total + 256 + 5 * align256(size_t(p.ld_part) * sizeof(float)) + more;
 }

@@ -87,7 +87,11 @@ struct EmbedGradArgs {
   uint32_t* pos[2];
   uint32_t* hist;             // [256][blocks] digit counts (N > kSortMerge)
   float* part;                // [windows][2][H] partial rows
-  const float* weight;        // [N], or null: row i counts weight[i] times (bf16 only)
+  // weighted form, or null (bf16 only): row i counts weight[i] times, and what the sums
+  // are added to are the float32 rows of `keep`: id v's row is slot[v] - 1
+  const float* weight;        // [N]
+  uint32_t* slot;             // [V]
+  const float* keep;          // [N][H]
 };
 
 struct EmbedPlan {
@@ -169,21 +173,36 @@ inline int64_t lp_first_tiles(const LpPlan& q, int64_t nt) {
 // most four) and with 128 / tiles: 3 tokens of 178 over 43742 (1 tile) 260 and 108, 500
 // of 512 over 131072 (4) 815 and 407, 300 of 1024 over 32000 (8) 251 and 183, 1000 of
 // 1024 over 32000 (16) 317 and 293; with 256 / tiles the last two take 197 and 355, and
-// 32 tiles lose (300 of 4096 over 32000: 482 and 526). False for invalid sizes.
+// 32 tiles lose (300 of 4096 over 32000: 482 and 526). bf16 gradients always have the
+// float32 sum of dH, to which what rounding G left is added last. False for invalid sizes.
 inline bool make_lp_backward_plan(int64_t N, int64_t H, int64_t V, int dtype, int grad_dtype,
                                   Plan* p) {
   if (!make_plan(N, H, V, dtype, p, true, grad_dtype)) return false;
   if (p->dtype != kBF16 || p->g_parts != 1 || N <= 0) return true;
+  auto more = [&](int64_t times) {                 // behind the head's own buffers
+    const size_t at = p->total;
+    p->total = (at + size_t(times) * size_t(N) * p->H * sizeof(float) + 255) & ~size_t(255);
+    return at;
+  };
   const int64_t tiles = p->n_tok_tiles * ((p->H + kTileBF16 - 1) / kTileBF16);
-  if (tiles > 16) return true;
-  int64_t segs = 128 / tiles < 32 ? 128 / tiles : 32;
+  int64_t segs = tiles > 16 ? 1 : 128 / tiles < 32 ? 128 / tiles : 32;
   if (segs > p->vchunk / 512) segs = p->vchunk / 512;
-  if (segs <= 1 || segs <= p->dh_segs) return true;
-  p->dh_kseg = ((p->vchunk + segs - 1) / segs + 63) / 64 * 64;
-  p->dh_segs = (p->vchunk + p->dh_kseg - 1) / p->dh_kseg;
-  p->off_dhpart = p->total;                        // behind the head's own buffers
-  p->total = (p->total + size_t(p->dh_segs) * size_t(N) * p->H * sizeof(float) + 255) & ~size_t(255);
+  if (segs > 1 && segs > p->dh_segs) {
+    p->dh_kseg = ((p->vchunk + segs - 1) / segs + 63) / 64 * 64;
+    p->dh_segs = (p->vchunk + p->dh_kseg - 1) / p->dh_kseg;
+    p->off_dhpart = more(p->dh_segs);
+  }
+  if (!p->dh_kseg && !p->need_dh_acc) {
+    p->need_dh_acc = true;
+    p->off_dhacc = more(1);
+  }
   return true;
+}
+// Bytes of the slots of the ids that are labels, whole 16-byte pieces, and of their
+// float32 dW rows (bf16 gradients).
+inline size_t lp_slot_bytes(int64_t V) { return (size_t(V) * sizeof(uint32_t) + 255) & ~size_t(255); }
+inline size_t lp_keep_bytes(int64_t N, int64_t H) {
+  return (size_t(N) * size_t(H) * sizeof(float) + 255) & ~size_t(255);
 }
 // Whether G comes from the few-token kernel (bf16 G; the gathered rows are aligned).
 inline bool lp_few_backward(const Plan& p) {
@@ -249,6 +268,10 @@ hipError_t launch_rms_norm(const NormArgs& a, const Launcher& L);
 hipError_t launch_rms_norm_backward(const NormBwdArgs& a, const Launcher& L);
 hipError_t launch_embedding(const EmbedArgs& a, const Launcher& L);
 hipError_t launch_embedding_backward(const EmbedGradArgs& a, const Launcher& L);
+// The weighted form in two parts: the sort, which fills a.slot (and says which of the two
+// lists it leaves), and the sums.
+hipError_t launch_weighted_sort(const EmbedGradArgs& a, const Launcher& L, int* list);
+hipError_t launch_weighted_sums(const EmbedGradArgs& a, int list, const Launcher& L);
 hipError_t launch_logprobs(const LpPlan& q, const LpArgs& a, char* ws, const Launcher& L);
 // The logit gradient of vocabulary chunk `chunk` (a.g) from the coefficients,
 // and the kernel that forms those.
