@@ -568,8 +568,8 @@ int flce_logprobs(const void* h, const void* W, const int64_t* tokens, int64_t N
  * row and in dW, and FLCE_ERR_LABEL in *status. The same bits on every run. N = 0 zeroes
  * dW unless it accumulates.
  * The workspace (256-byte aligned) is flce_logprobs_backward_workspace_size
- * bytes (0 for invalid sizes): for bf16 gradients the head's, two float32 rows of H for each
- * token and 4 V bytes. Errors as flce_logprobs_check_args.
+ * bytes (0 for invalid sizes): for bf16 gradients the head's, one or two float32 rows of H
+ * for each token and 4 V bytes. Errors as flce_logprobs_check_args.
  */
 size_t flce_logprobs_backward_workspace_size(int64_t N, int64_t H, int64_t V, int dtype,
                                              int grad_dtype);

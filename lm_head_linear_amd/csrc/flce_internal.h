@@ -75,7 +75,7 @@ struct Args {
                   // the forward ([n_tok_chunks]) and then for the backward
   // log probabilities' bf16 gradients (null otherwise): what rounding G of each gathered
   // token's label left, and the float32 dW rows of the ids that are labels, by slot: id v's
-  // is slot dw_slot[v] - 1 of dw_keep (0: no label), not stored in dW
+  // is slot dw_slot[v] - 1 of dw_keep (0: no label); what dW holds of it is replaced
   const float* rest;
   const uint32_t* dw_slot;
   float* dw_keep;  // [N][H]

@@ -1301,9 +1301,9 @@ __global__ __launch_bounds__(kFewThreads) void k_lp_join_few(JoinArgs a) {
 // those left is kept in float32. It is added to dH's float32 sums (times W's row of the
 // token) and, a weighted lookup gradient over the same rows, to the float32 dW rows of the
 // tokens, which the products leave beside dW for it; both are then rounded once. That
-// takes 12 us of 563 (2048 rows of 1024 over 32000) and 80 of 12120 (4096 of 4096 over 131072),
-// and leaves dH and dW off by 0.00166 of their norm, as much as rounding the exact ones
-// does (0.0024 and 0.0022 with bf16 G alone and a repair of the rounded dW).
+// takes 7 us of 562 (a training step of 2048 rows of 1024 over 32000) and 30 of 12190 (4096
+// of 4096 over 131072) more than a repair of the rounded dW alone, and leaves dH and dW off
+// by 0.00166 of their norm, as much as rounding the exact ones does (0.0024 and 0.0022 so).
 __global__ __launch_bounds__(256) void k_lp_coef(
     const int32_t* __restrict__ idx, const int64_t* __restrict__ labels,
     const int64_t* __restrict__ count, int64_t N, int64_t V, int64_t ignore_index,
