@@ -30,7 +30,7 @@ def loss(x, exact):
 
 
 CASES = [(40, 64, 300), (128, 133, 700), (300, 72, 1001), (600, 256, 300), (1000, 512, 2000),
-         (3000, 128, 9000), (700, 64, 70000), (2500, 1024, 1500)]
+         (3000, 128, 9000), (700, 64, 70000), (2500, 1024, 1500), (40000, 16, 300), (70000, 8, 200)]
 
 
 @pytest.mark.parametrize("N,H,V", CASES)
