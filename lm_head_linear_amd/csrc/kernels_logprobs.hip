@@ -25,9 +25,9 @@
 // and the largest of each 64 vocabulary rows; the join then looks only into the top_k
 // of those parts with the largest, which hold all top_k alternatives.
 //
-// Measured: 6144 live rows of 4096 over 131072 with 8 alternatives 5.02 ms in the tiles
-// (1315 TFLOP/s; 3687 rows without alternatives 2.87 ms, 1380 TFLOP/s); one row over
-// the same table 200 us (5.4 TB/s); float32 512 rows of 1024 over 32000 303 us (111
+// Measured: 6144 live rows of 4096 over 131072 with 8 alternatives 4.97 ms in the tiles
+// (1326 TFLOP/s; 3687 rows without alternatives 2.85 ms, 1390 TFLOP/s); one row over
+// the same table 196 us (5.5 TB/s); float32 512 rows of 1024 over 32000 303 us (111
 // TFLOP/s, where the library's product of that type reaches 138).
 #include <hip/hip_runtime.h>
 
@@ -1078,7 +1078,7 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void k_lp_join_dense(JoinArgs a)
 // workgroup, 32 threads for each. Every candidate goes to a list in LDS, with the
 // top_k of the tiles before, and the top_k of those are selected (join_sparse.h); a list
 // that overflows is filled again from its own top_k-th key on. 1946 rows over 186 lists
-// with 5 alternatives 13 us, 6144 rows over 1984 lists with 8 51 us.
+// with 5 alternatives 13 us, 6144 rows over 1984 lists with 8 50 us.
 constexpr int kSparseTokens = 16;
 
 struct WorkgroupEnv {
