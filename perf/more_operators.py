@@ -323,12 +323,12 @@ def _own_sample(s):
 def _own_linear(s):
     import lm_head_linear_amd as flce
     c = s["case"]
-    y, z = flce.flce_linear(s["x"], s["weight"], s["bias"], s["residual"],
-                            activation=c["activation"], save_z=c["train"])
+    y, slope = flce.flce_linear(s["x"], s["weight"], s["bias"], s["residual"],
+                            activation=c["activation"], save_slope=c["train"])
     out = dict(y=y)
     if c["train"]:
         out["dx"], out["dweight"], db = flce.flce_linear_backward(
-            s["dy"], s["x"], s["weight"], z, activation=c["activation"], bias=c["bias"])
+            s["dy"], s["x"], s["weight"], slope, bias=c["bias"])
         if c["bias"]:
             out["dbias"] = db
     return out
