@@ -43,7 +43,8 @@ KERNEL_SOURCES = [os.path.join(ROOT, "lm_head_linear_amd", "csrc", f)
                             "gemm_index.h", "gemm_bf16.h", "api_util.h", "ops_api.hip",
                             "ops_check.cpp", "ops_plan.h", "row_io.h", "kernels_norm.hip",
                             "kernels_embed.hip", "kernels_logprobs.hip", "wave_ops.h",
-                            "join_sparse.h")]
+                            "join_sparse.h", "check_util.h", "dropout.h", "dropout_check.cpp",
+                            "kernels_dropout.hip")]
 
 
 def log(*a):

@@ -588,6 +588,69 @@ int flce_logprobs_backward(const void* h, const void* W, const int64_t* tokens, 
                            void* dW, int accumulate_dW, void* stream, int dtype, int grad_dtype,
                            void* workspace, size_t workspace_bytes, int32_t* status);
 
+/*
+ * ---- Dropout -----------------------------------------------------------------
+ * The mask of [N,H] values is a function of a seed and an offset, formed where it is
+ * needed and never stored: ten rounds of Philox 4x32 (Salmon et al., SC 2011) under the
+ * key (seed) of the counter, four words of 32 bits: (column / 8, row, offset low, offset
+ * high) give four words, and columns 8 j .. 8 j + 7 take their 16-bit halves in order, low
+ * half first. A value is kept where its 16 bits are at least t = floor(65536 p + 0.5) (at
+ * most 65535) and then multiplied by 65536 / (65536 - t): the mean is kept exactly.
+ * step: a device int64 added to the offset (mod 2^64) when the kernel runs, or NULL: a
+ * captured graph gets another mask on each replay by advancing it. The backward has to
+ * see the same step. Different offsets of one seed give independent masks.
+ *
+ * flce_dropout -- out = round(residual + keep * x * scale); residual may be NULL (zero).
+ * A dropped value counts as zero whatever x holds there. Its backward is the same call of
+ * dout without a residual: dx = keep * dout * scale (the residual's gradient is dout).
+ * In place: out may be x or the residual (same pointer and stride). N = 0 does nothing.
+ * flce_dropout_check_args: FLCE_ERR_ARG for N < 0 or N >= 2^31, H <= 0 or H > 2^24, an
+ * unknown type, p outside [0, 1), a NULL x or out, a row stride below H or above 2^31,
+ * any other overlap of out; FLCE_ERR_UNSUPPORTED for a pointer not aligned to its
+ * elements or sizes beyond one grid.
+ */
+int flce_dropout_check_args(const void* x, int64_t ld_x, const void* residual, int64_t ld_res,
+                            int64_t N, int64_t H, double p, uint64_t seed, uint64_t offset,
+                            const int64_t* step, const void* out, int64_t ld_out,
+                            const void* stream, int dtype);
+int flce_dropout(const void* x, int64_t ld_x, const void* residual, int64_t ld_res, int64_t N,
+                 int64_t H, double p, uint64_t seed, uint64_t offset, const int64_t* step,
+                 void* out, int64_t ld_out, void* stream, int dtype);
+
+/*
+ * flce_dropout_norm -- flce_rms_norm of s = round(residual + keep * x * scale), which is
+ * written (s is not NULL; the residual may be). In place as flce_rms_norm.
+ * flce_dropout_norm_backward -- with d = ds + rstd * (g - n * mean_h(g * n)) as in
+ * flce_rms_norm_backward (whose workspace it takes): dresidual = round(d) (NULL: not
+ * wanted), dx = round(keep * d * scale), and dweight. In place: dx and dresidual may each
+ * be dy or ds. Errors as those of the norm, and FLCE_ERR_ARG for p outside [0, 1).
+ */
+int flce_dropout_norm_check_args(const void* x, int64_t ld_x, const void* residual,
+                                 int64_t ld_res, const void* weight, int64_t N, int64_t H,
+                                 float eps, float weight_offset, double p, uint64_t seed,
+                                 uint64_t offset, const int64_t* step, const void* y,
+                                 int64_t ld_y, const void* s, int64_t ld_s, const float* rstd,
+                                 const void* stream, int dtype, int weight_dtype);
+int flce_dropout_norm(const void* x, int64_t ld_x, const void* residual, int64_t ld_res,
+                      const void* weight, int64_t N, int64_t H, float eps, float weight_offset,
+                      double p, uint64_t seed, uint64_t offset, const int64_t* step, void* y,
+                      int64_t ld_y, void* s, int64_t ld_s, float* rstd, void* stream, int dtype,
+                      int weight_dtype);
+int flce_dropout_norm_backward_check_args(
+    const void* dy, int64_t ld_dy, const void* ds, int64_t ld_ds, const void* s, int64_t ld_s,
+    const void* weight, const float* rstd, int64_t N, int64_t H, float weight_offset, double p,
+    uint64_t seed, uint64_t offset, const int64_t* step, const void* dx, int64_t ld_dx,
+    const void* dresidual, int64_t ld_dres, const void* dweight, int accumulate_dweight,
+    const void* stream, int dtype, int weight_dtype, const void* workspace,
+    size_t workspace_bytes);
+int flce_dropout_norm_backward(const void* dy, int64_t ld_dy, const void* ds, int64_t ld_ds,
+                               const void* s, int64_t ld_s, const void* weight, const float* rstd,
+                               int64_t N, int64_t H, float weight_offset, double p, uint64_t seed,
+                               uint64_t offset, const int64_t* step, void* dx, int64_t ld_dx,
+                               void* dresidual, int64_t ld_dres, void* dweight,
+                               int accumulate_dweight, void* stream, int dtype, int weight_dtype,
+                               void* workspace, size_t workspace_bytes);
+
 /* flce_status_string -- a static, human-readable name for a status code
  * (this library's own addition; no page defines status codes). */
 const char* flce_status_string(int status);

@@ -33,6 +33,10 @@ from typing import Optional
 import torch
 
 from . import _lib
+from ._dropout import (  # noqa: F401
+    DropoutMask, flce_dropout, flce_dropout_backward, flce_dropout_check_args,
+    flce_dropout_norm, flce_dropout_norm_backward, flce_dropout_norm_backward_check_args,
+    flce_dropout_norm_check_args, fused_dropout, fused_dropout_norm)
 from ._ops import (  # noqa: F401
     TokenLogprobs,
     flce_embedding, flce_embedding_backward, flce_embedding_backward_check_args,
@@ -84,6 +88,16 @@ __all__ = [
     "flce_embedding_backward_workspace_size",
     "fused_rms_norm",
     "fused_embedding",
+    "DropoutMask",
+    "flce_dropout",
+    "flce_dropout_check_args",
+    "flce_dropout_backward",
+    "flce_dropout_norm",
+    "flce_dropout_norm_check_args",
+    "flce_dropout_norm_backward",
+    "flce_dropout_norm_backward_check_args",
+    "fused_dropout",
+    "fused_dropout_norm",
     "flce_status_string",
     "flce_vocab_chunk",
     "flce_kept_chunks",
@@ -600,20 +614,28 @@ class TiedLMHead(torch.nn.Module):
         self.norm_eps = float(norm_eps)
         self.weight_offset = float(weight_offset)
 
-    def embed(self, tokens: torch.Tensor) -> torch.Tensor:
-        """embed_scale * W[tokens]; a token equal to ignore_index gives zeros."""
-        return fused_embedding(tokens, self.weight, scale=self.embed_scale,
-                               padding_index=self.criterion.ignore_index)
+    def embed(self, tokens: torch.Tensor, dropout: Optional[DropoutMask] = None) -> torch.Tensor:
+        """embed_scale * W[tokens], dropped out by the mask where one is given; a token equal
+        to ignore_index gives zeros."""
+        e = fused_embedding(tokens, self.weight, scale=self.embed_scale,
+                            padding_index=self.criterion.ignore_index)
+        return e if dropout is None else fused_dropout(e, dropout)
 
-    def norm(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None) -> torch.Tensor:
+    def norm(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None,
+             dropout: Optional[DropoutMask] = None) -> torch.Tensor:
+        """The final norm of residual + x, x dropped out by the mask where one is given."""
+        if dropout is not None:
+            return fused_dropout_norm(x, self.norm_weight, dropout, residual, eps=self.norm_eps,
+                                      weight_offset=self.weight_offset)[0]
         out = fused_rms_norm(x, self.norm_weight, residual, eps=self.norm_eps,
                              weight_offset=self.weight_offset)
         return out if residual is None else out[0]
 
     def loss(self, x: torch.Tensor, labels: torch.Tensor,
-             residual: Optional[torch.Tensor] = None, **kw) -> torch.Tensor:
+             residual: Optional[torch.Tensor] = None, *,
+             dropout: Optional[DropoutMask] = None, **kw) -> torch.Tensor:
         """The head's loss (:class:`FusedLinearCrossEntropy`) of the normalised rows."""
-        return self.criterion(self.norm(x, residual), labels, self.weight, **kw)
+        return self.criterion(self.norm(x, residual, dropout), labels, self.weight, **kw)
 
     def logprobs(self, x: torch.Tensor, tokens: Optional[torch.Tensor] = None,
                  residual: Optional[torch.Tensor] = None, *, temperature: float = 1.0,

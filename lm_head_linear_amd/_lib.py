@@ -33,6 +33,13 @@ _LP = [_vp, _vp, _vp, _i64, _i64, _i64, _i64, _f32, _f32, _i32, _vp, _vp, _vp, _
        _vp, _sz, _vp]
 _LP_BWD = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _f32, _f32, _vp, _vp, _i32,
            _vp, _i32, _i32, _vp, _sz, _vp]
+_u64, _f64 = _c.c_uint64, _c.c_double
+_DROP = [_f64, _u64, _u64, _vp]
+_DROPOUT = [_vp, _i64, _vp, _i64, _i64, _i64] + _DROP + [_vp, _i64, _vp, _i32]
+_DROP_NORM = [_vp, _i64, _vp, _i64, _vp, _i64, _i64, _f32, _f32] + _DROP + [
+    _vp, _i64, _vp, _i64, _vp, _vp, _i32, _i32]
+_DROP_NORM_BWD = [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _f32] + _DROP + [
+    _vp, _i64, _vp, _i64, _vp, _i32, _vp, _i32, _i32, _vp, _sz]
 SIGNATURES = {
     "flce_workspace_size": (_sz, [_i64, _i64, _i64, _i32]),
     "flce_check_args": (_i32, _FB_ARGS),
@@ -57,6 +64,12 @@ SIGNATURES = {
     "flce_rms_norm_backward_workspace_size": (_sz, [_i64, _i64]),
     "flce_rms_norm_backward_check_args": (_i32, _NORM_BWD),
     "flce_rms_norm_backward": (_i32, _NORM_BWD),
+    "flce_dropout_check_args": (_i32, _DROPOUT),
+    "flce_dropout": (_i32, _DROPOUT),
+    "flce_dropout_norm_check_args": (_i32, _DROP_NORM),
+    "flce_dropout_norm": (_i32, _DROP_NORM),
+    "flce_dropout_norm_backward_check_args": (_i32, _DROP_NORM_BWD),
+    "flce_dropout_norm_backward": (_i32, _DROP_NORM_BWD),
     "flce_embedding_check_args": (_i32, _EMBED),
     "flce_embedding": (_i32, _EMBED),
     "flce_embedding_backward_workspace_size": (_sz, [_i64, _i64, _i64]),

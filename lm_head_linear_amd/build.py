@@ -13,8 +13,9 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libflce.so")
 
 HIP_SOURCES = ["flce_api.hip", "kernels_common.hip", "kernels_bf16.hip", "kernels_f32.hip",
-               "ops_api.hip", "kernels_norm.hip", "kernels_embed.hip", "kernels_logprobs.hip"]
-CXX_SOURCES = ["flce_check.cpp", "ops_check.cpp"]
+               "ops_api.hip", "kernels_norm.hip", "kernels_embed.hip", "kernels_logprobs.hip",
+               "kernels_dropout.hip"]
+CXX_SOURCES = ["flce_check.cpp", "ops_check.cpp", "dropout_check.cpp"]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [

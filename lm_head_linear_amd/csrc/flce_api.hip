@@ -101,7 +101,8 @@ const char* kKindNames[flce::kNumKinds] = {"label_scan", "lse_fwd_gemm", "lse_me
                                            "dH_gemm", "fill", "probs_to_grad", "dH_reduce",
                                            "gather", "dH_dW_gemm", "pad_copy", "rms_norm",
                                            "rms_norm_bwd", "embed", "embed_sort",
-                                           "embed_grad", "logprobs_tiles", "logprobs_join"};
+                                           "embed_grad", "logprobs_tiles", "logprobs_join",
+                                           "dropout", "sample", "linear", "linear_bwd"};
 
 // ---- scratch of flce_forward_noalloc ---------------------------------------
 // One copy on every GPU the library runs on, held until the process ends. In

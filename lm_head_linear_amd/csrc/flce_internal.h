@@ -31,7 +31,11 @@ enum Kind : int {
   kEmbedGrad = 17,
   kLpTiles = 18,
   kLpJoin = 19,
-  kNumKinds = 20,
+  kDropout = 20,
+  kSample = 21,
+  kLinear = 22,
+  kLinearGrad = 23,
+  kNumKinds = 24,
 };
 
 // Everything one call needs on the device side.

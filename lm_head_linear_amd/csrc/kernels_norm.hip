@@ -18,6 +18,10 @@
 // per CU, walk rows with a fixed stride and keep their share of dw in registers; a
 // second kernel adds the shares up in a fixed order.
 //
+// With dropout (DROP) the same passes take x's mask (dropout.h) in stride: s is then
+// round(r + keep x scale), and the backward writes two rows, the sum's gradient for the
+// residual and the masked one for x.
+//
 // bf16 with the residual, 8192 rows of 4096: forward 50 us (268 MB, 5.4 TB/s), backward
 // 56 us (4.8 TB/s) and 7 us for dw. Both directions together, with this many threads
 // and with others: 8192 x 4096, 256 threads 112 us (64: 211, 1024: 151); 16384 x 1024,
@@ -28,6 +32,7 @@
 #include <cstdint>
 
 #include "../../include/flce.h"
+#include "dropout.h"
 #include "flce_internal.h"
 #include "ops_plan.h"
 #include "row_io.h"
@@ -62,11 +67,14 @@ __device__ __forceinline__ float row_sum(float x, float* red) {
 
 // LANES threads a row. C > 0: the row stays in registers, C chunks a thread; C = 0:
 // rows of any length, read again for the second pass.
-template <class T, class WT, int LANES, int C, bool RES>
+// DROP: x is dropped out before the residual (null: none) is added, s is always written;
+// row 0 is row `row0` of the mask.
+template <class T, class WT, int LANES, int C, bool RES, bool DROP>
 __global__ __launch_bounds__(kBlock<LANES>) void k_rms_norm(
     const T* x, int64_t ldx, const T* res, int64_t ldr, const WT* __restrict__ w, int64_t N,
     int64_t H, float eps, float offset, T* y, int64_t ldy, T* s, int64_t lds,
-    float* __restrict__ rstd) {
+    float* __restrict__ rstd, DropSpec drop, int64_t row0) {
+  constexpr bool SUM = RES || DROP;                // s is another value than x
   constexpr int E = kPerChunk<T>, R = kBlock<LANES> / LANES;
   __shared__ float red[kBlock<LANES> / 64];
   const int tid = threadIdx.x % LANES;
@@ -75,13 +83,25 @@ __global__ __launch_bounds__(kBlock<LANES>) void k_rms_norm(
   const int64_t Hs = at < N ? H : 0;               // columns that are stored
   x += row * ldx;
   y += row * ldy;
-  if (RES) { res += row * ldr; s += row * lds; }
+  if (RES) res += row * ldr;
+  if (SUM) s += row * lds;
+  DropKey key{};
+  if constexpr (DROP) key = drop_key(drop);
   float sum = 0.f;
   auto load_sum = [&](int64_t c, float (&v)[E]) {
     load_chunk(x, c, H, v);
-    if (RES) {
-      float r[E];
-      load_chunk(res, c, H, r);
+    float r[E];
+    if (RES) load_chunk(res, c, H, r);
+    if constexpr (DROP) {
+      const Mask8 m = drop_chunk<E>(key, row0 + row, c);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float add = RES ? r[e] : 0.f;
+        v[e] = drop_keeps(m, e, drop.threshold) ? fmaf(v[e], drop.scale, add) : add;
+      }
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] = to_f32(from_f32<T>(v[e]));
+    } else if (RES) {
 #pragma unroll
       for (int e = 0; e < E; ++e) v[e] = to_f32(from_f32<T>(v[e] + r[e]));
     }
@@ -114,7 +134,7 @@ __global__ __launch_bounds__(kBlock<LANES>) void k_rms_norm(
     for (int k = 0; k < C; ++k) {
 #pragma unroll
       for (int e = 0; e < E; ++e) sum = fmaf(v[k][e], v[k][e], sum);
-      if (RES) store_chunk(s, (int64_t(k) * LANES + tid) * E, Hs, v[k]);
+      if (SUM) store_chunk(s, (int64_t(k) * LANES + tid) * E, Hs, v[k]);
     }
     const float q = finish(row_sum<LANES>(sum, red));
 #pragma unroll
@@ -129,14 +149,14 @@ __global__ __launch_bounds__(kBlock<LANES>) void k_rms_norm(
       load_sum(c, v);
 #pragma unroll
       for (int e = 0; e < E; ++e) sum = fmaf(v[e], v[e], sum);
-      if (RES) store_chunk(s, c, H, v);
+      if (SUM) store_chunk(s, c, H, v);
     }
     const float q = finish(row_sum<LANES>(sum, red));
     // a thread reads back only what it wrote itself (s), or x, whose element it
     // replaces last when y is x
     for (int64_t c = int64_t(tid) * E; c < H; c += LANES * E) {
       float v[E], f[E];
-      load_chunk(RES ? const_cast<const T*>(s) : x, c, H, v);
+      load_chunk(SUM ? const_cast<const T*>(s) : x, c, H, v);
       load_w(c, f);
 #pragma unroll
       for (int e = 0; e < E; ++e) v[e] = (v[e] * q) * (f[e] + offset);
@@ -148,12 +168,13 @@ __global__ __launch_bounds__(kBlock<LANES>) void k_rms_norm(
 // dx of every gridDim.x R-th row (R rows a workgroup, LANES threads each), and the
 // workgroup's share of dw (DW) in dw_part[blockIdx.x][H], its R rows' shares joined in
 // LDS. C = 0: rows of any length; dw's share is then added up in memory (each thread its
-// own columns).
-template <class T, class WT, int LANES, int C, bool DS, bool DW>
+// own columns). DROP: d, the gradient of the sum, goes to dres (null: not wanted), and dx
+// gets keep d scale.
+template <class T, class WT, int LANES, int C, bool DS, bool DW, bool DROP>
 __global__ __launch_bounds__(kBlock<LANES>) void k_rms_norm_bwd(
     const T* dy, int64_t lddy, const T* ds, int64_t ldds, const T* __restrict__ s, int64_t lds,
     const WT* __restrict__ w, const float* __restrict__ rstd, int64_t N, int64_t H, float offset,
-    T* dx, int64_t lddx, float* __restrict__ dw_part) {
+    T* dx, int64_t lddx, float* __restrict__ dw_part, T* dres, int64_t lddres, DropSpec drop) {
   constexpr int E = kPerChunk<T>, R = kBlock<LANES> / LANES;
   __shared__ float red[kBlock<LANES> / 64];
   const int tid = threadIdx.x % LANES, group = threadIdx.x / LANES;
@@ -171,6 +192,18 @@ __global__ __launch_bounds__(kBlock<LANES>) void k_rms_norm_bwd(
     for (int e = 0; e < E; ++e) f[e] += offset;
   };
   const float inv_h = 1.f / float(H);
+  DropKey key{};
+  if constexpr (DROP) key = drop_key(drop);
+  // the gradients of columns c .. of a row, d that of the sum
+  auto store_grads = [&](int64_t row, int64_t c, int64_t Hs, float (&d)[E]) {
+    if constexpr (DROP) {
+      if (dres) store_chunk(dres + row * lddres, c, Hs, d);
+      const Mask8 m = drop_chunk<E>(key, row, c);
+#pragma unroll
+      for (int e = 0; e < E; ++e) d[e] = drop_keeps(m, e, drop.threshold) ? d[e] * drop.scale : 0.f;
+    }
+    store_chunk(dx + row * lddx, c, Hs, d);
+  };
   if constexpr (C > 0) {
     float f[C][E], acc[C][E];
 #pragma unroll
@@ -210,7 +243,7 @@ __global__ __launch_bounds__(kBlock<LANES>) void k_rms_norm_bwd(
           const float v = q * (g[k][e] - n[k][e] * mean);
           g[k][e] = DS ? d[k][e] + v : v;
         }
-        store_chunk(dx + row * lddx, (int64_t(k) * LANES + tid) * E, live ? H : 0, g[k]);
+        store_grads(row, (int64_t(k) * LANES + tid) * E, live ? H : 0, g[k]);
       }
     }
     if (DW) {
@@ -266,7 +299,7 @@ __global__ __launch_bounds__(kBlock<LANES>) void k_rms_norm_bwd(
           const float v = q * (g[e] * f[e] - n[e] * mean);
           g[e] = DS ? d[e] + v : v;
         }
-        store_chunk(dx + row * lddx, c, H, g);
+        store_grads(row, c, H, g);
       }
       first = false;
     }
@@ -336,13 +369,17 @@ hipError_t norm_forward(const NormArgs& a, const Launcher& L) {
     with_variant(chunks, [&](auto lanes, auto c) {
       constexpr int LN = decltype(lanes)::value, C = decltype(c)::value, R = kBlock<LN> / LN;
       const dim3 grid(unsigned((n + R - 1) / R)), block(kBlock<LN>);
-      if (r)
-        hipLaunchKernelGGL((k_rms_norm<T, WT, LN, C, true>), grid, block, 0, L.stream, xt, a.ld_x,
-                           r + t0 * a.ld_res, a.ld_res, w, n, a.H, a.eps, a.offset, yt, a.ld_y,
-                           s + t0 * a.ld_s, a.ld_s, q);
-      else
-        hipLaunchKernelGGL((k_rms_norm<T, WT, LN, C, false>), grid, block, 0, L.stream, xt, a.ld_x,
-                           r, a.ld_res, w, n, a.H, a.eps, a.offset, yt, a.ld_y, s, a.ld_s, q);
+      auto go = [&](auto has_res, auto has_drop) {
+        constexpr bool RES = decltype(has_res)::value, DROP = decltype(has_drop)::value;
+        hipLaunchKernelGGL((k_rms_norm<T, WT, LN, C, RES, DROP>), grid, block, 0, L.stream, xt,
+                           a.ld_x, RES ? r + t0 * a.ld_res : r, a.ld_res, w, n, a.H, a.eps, a.offset,
+                           yt, a.ld_y, RES || DROP ? s + t0 * a.ld_s : s, a.ld_s, q,
+                           DROP ? *a.drop : DropSpec{}, t0);
+      };
+      using Y = std::true_type;
+      using No = std::false_type;
+      if (a.drop) r ? go(Y{}, Y{}) : go(No{}, Y{});
+      else r ? go(Y{}, No{}) : go(No{}, No{});
     });
   }
   L.post(kNorm);
@@ -362,16 +399,21 @@ hipError_t norm_backward(const NormBwdArgs& a, const Launcher& L) {
   with_variant(chunks, [&](auto lanes, auto c) {
     constexpr int LN = decltype(lanes)::value, C = decltype(c)::value, R = kBlock<LN> / LN;
     nb = norm_shares((a.N + R - 1) / R);
-    auto go = [&](auto has_ds, auto has_dw) {
+    auto go = [&](auto has_ds, auto has_dw, auto has_drop) {
       constexpr bool DS = decltype(has_ds)::value, DW = decltype(has_dw)::value;
-      hipLaunchKernelGGL((k_rms_norm_bwd<T, WT, LN, C, DS, DW>), dim3(unsigned(nb)),
+      constexpr bool DROP = decltype(has_drop)::value;
+      hipLaunchKernelGGL((k_rms_norm_bwd<T, WT, LN, C, DS, DW, DROP>), dim3(unsigned(nb)),
                          dim3(kBlock<LN>), 0, L.stream, dy, a.ld_dy, ds, a.ld_ds, s, a.ld_s, w, a.rstd, a.N, a.H,
-                         a.offset, dx, a.ld_dx, a.dw_part);
+                         a.offset, dx, a.ld_dx, a.dw_part, static_cast<T*>(a.dres), a.ld_dres,
+                         DROP ? *a.drop : DropSpec{});
     };
     using Y = std::true_type;
     using No = std::false_type;
-    if (ds) a.dweight ? go(Y{}, Y{}) : go(Y{}, No{});
-    else a.dweight ? go(No{}, Y{}) : go(No{}, No{});
+    auto pick = [&](auto has_drop) {
+      if (ds) a.dweight ? go(Y{}, Y{}, has_drop) : go(Y{}, No{}, has_drop);
+      else a.dweight ? go(No{}, Y{}, has_drop) : go(No{}, No{}, has_drop);
+    };
+    a.drop ? pick(Y{}) : pick(No{});
   });
   L.post(kNormBwd);
   hipError_t e = hipGetLastError();

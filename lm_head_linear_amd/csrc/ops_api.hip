@@ -54,6 +54,61 @@ int flce_rms_norm_backward(const void* dy, int64_t ld_dy, const void* ds, int64_
   return status_of(flce::launch_rms_norm_backward(a, L));
 }
 
+int flce_dropout(const void* x, int64_t ld_x, const void* residual, int64_t ld_res, int64_t N,
+                 int64_t H, double p, uint64_t seed, uint64_t offset, const int64_t* step,
+                 void* out, int64_t ld_out, void* stream, int dtype) {
+  const int st = flce_dropout_check_args(x, ld_x, residual, ld_res, N, H, p, seed, offset, step,
+                                         out, ld_out, stream, dtype);
+  if (st != FLCE_OK || N == 0) return st;
+  Range r("flce_dropout");
+  const flce::DropoutArgs a{x, ld_x, residual, ld_res, N, H,
+                            flce::make_drop(p, seed, offset, step), out, ld_out, dtype};
+  return status_of(flce::launch_dropout(a, flce::make_launcher(stream)));
+}
+
+int flce_dropout_norm(const void* x, int64_t ld_x, const void* residual, int64_t ld_res,
+                      const void* weight, int64_t N, int64_t H, float eps, float weight_offset,
+                      double p, uint64_t seed, uint64_t offset, const int64_t* step, void* y,
+                      int64_t ld_y, void* s, int64_t ld_s, float* rstd, void* stream, int dtype,
+                      int weight_dtype) {
+  const int st = flce_dropout_norm_check_args(x, ld_x, residual, ld_res, weight, N, H, eps,
+                                              weight_offset, p, seed, offset, step, y, ld_y, s,
+                                              ld_s, rstd, stream, dtype, weight_dtype);
+  if (st != FLCE_OK || N == 0) return st;
+  Range r("flce_dropout_norm");
+  const flce::DropSpec drop = flce::make_drop(p, seed, offset, step);
+  const flce::NormArgs a{x, ld_x, residual, ld_res, weight, N, H, eps, weight_offset,
+                         y, ld_y, s, ld_s, rstd, dtype, weight_dtype, &drop};
+  return status_of(flce::launch_rms_norm(a, flce::make_launcher(stream)));
+}
+
+int flce_dropout_norm_backward(const void* dy, int64_t ld_dy, const void* ds, int64_t ld_ds,
+                               const void* s, int64_t ld_s, const void* weight, const float* rstd,
+                               int64_t N, int64_t H, float weight_offset, double p, uint64_t seed,
+                               uint64_t offset, const int64_t* step, void* dx, int64_t ld_dx,
+                               void* dresidual, int64_t ld_dres, void* dweight,
+                               int accumulate_dweight, void* stream, int dtype, int weight_dtype,
+                               void* workspace, size_t workspace_bytes) {
+  const int st = flce_dropout_norm_backward_check_args(
+      dy, ld_dy, ds, ld_ds, s, ld_s, weight, rstd, N, H, weight_offset, p, seed, offset, step, dx,
+      ld_dx, dresidual, ld_dres, dweight, accumulate_dweight, stream, dtype, weight_dtype,
+      workspace, workspace_bytes);
+  if (st != FLCE_OK) return st;
+  Range r("flce_dropout_norm_backward");
+  const Launcher L = flce::make_launcher(stream);
+  if (N == 0) {
+    if (!dweight || accumulate_dweight) return FLCE_OK;
+    return status_of(
+        flce::launch_zero_bytes(dweight, size_t(H) * (weight_dtype == FLCE_BF16 ? 2 : 4), L));
+  }
+  const flce::DropSpec drop = flce::make_drop(p, seed, offset, step);
+  const flce::NormBwdArgs a{dy, ld_dy, ds, ld_ds, s, ld_s, weight, rstd, N, H, weight_offset,
+                            dx, ld_dx, dweight, accumulate_dweight ? 1 : 0, dtype, weight_dtype,
+                            dweight ? static_cast<float*>(workspace) : nullptr, &drop, dresidual,
+                            ld_dres};
+  return status_of(flce::launch_rms_norm_backward(a, L));
+}
+
 int flce_embedding(const int64_t* tokens, const void* W, int64_t N, int64_t H, int64_t V,
                    int64_t padding_index, float scale, void* out, int64_t ld_out, void* stream,
                    int dtype, int32_t* status) {

@@ -12,6 +12,39 @@ namespace flce {
 
 constexpr int kBF16 = 1;      // FLCE_BF16
 
+// ---- dropout -------------------------------------------------------------------------
+// The mask (dropout.h): a value stays where its 16 bits are at least the threshold, and
+// is multiplied by the scale.
+struct DropSpec {
+  uint64_t seed, offset;
+  const int64_t* step;        // device, added to the offset; may be null
+  uint32_t threshold;
+  float scale;
+};
+
+inline DropSpec make_drop(double p, uint64_t seed, uint64_t offset, const int64_t* step) {
+  const double t = p * 65536.0 + 0.5;
+  const uint32_t threshold = t < 65535.0 ? uint32_t(t) : 65535u;
+  return DropSpec{seed, offset, step, threshold, float(65536.0 / (65536.0 - threshold))};
+}
+
+struct DropoutArgs {
+  const void* x;
+  int64_t ld_x;
+  const void* residual;       // may be null
+  int64_t ld_res;
+  int64_t N, H;
+  DropSpec drop;
+  void* out;
+  int64_t ld_out;
+  int dtype;
+};
+
+// Blocks of eight columns a thread takes, from kDropMany of them: below, the chip has more
+// lanes than blocks.
+constexpr int kDropBlocks = 4;
+constexpr int64_t kDropMany = int64_t(1) << 20;
+
 // ---- root-mean-square norm ---------------------------------------------------------
 struct NormArgs {
   const void* x;
@@ -27,6 +60,7 @@ struct NormArgs {
   int64_t ld_s;
   float* rstd;                // may be null
   int dtype, weight_dtype;
+  const DropSpec* drop = nullptr;  // x's dropout; s is written then also without a residual
 };
 
 struct NormBwdArgs {
@@ -46,6 +80,10 @@ struct NormBwdArgs {
   int accumulate;
   int dtype, weight_dtype;
   float* dw_part;             // [norm_shares(N)][H], null without dweight
+  // x's dropout: dx is then masked, and the sum's gradient goes to dres (may be null)
+  const DropSpec* drop = nullptr;
+  void* dres = nullptr;
+  int64_t ld_dres = 0;
 };
 
 // Workgroups of the norm's backward, each with a share of dw: four per CU.
@@ -266,6 +304,7 @@ namespace flce {
 
 hipError_t launch_rms_norm(const NormArgs& a, const Launcher& L);
 hipError_t launch_rms_norm_backward(const NormBwdArgs& a, const Launcher& L);
+hipError_t launch_dropout(const DropoutArgs& a, const Launcher& L);
 hipError_t launch_embedding(const EmbedArgs& a, const Launcher& L);
 hipError_t launch_embedding_backward(const EmbedGradArgs& a, const Launcher& L);
 // The weighted form in two parts: the sort, which fills a.slot (and says which of the two
