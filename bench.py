@@ -44,7 +44,9 @@ KERNEL_SOURCES = [os.path.join(ROOT, "lm_head_linear_amd", "csrc", f)
                             "ops_check.cpp", "ops_plan.h", "row_io.h", "kernels_norm.hip",
                             "kernels_embed.hip", "kernels_logprobs.hip", "wave_ops.h",
                             "join_sparse.h", "check_util.h", "dropout.h", "dropout_check.cpp",
-                            "kernels_dropout.hip")]
+                            "kernels_dropout.hip", "kernels_linear.hip",
+                            "kernels_sample.hip", "gemm_small.h", "activation.h",
+                            "linear_check.cpp", "sample_check.cpp")]
 
 
 def log(*a):

@@ -651,6 +651,119 @@ int flce_dropout_norm_backward(const void* dy, int64_t ld_dy, const void* ds, in
                                int accumulate_dweight, void* stream, int dtype, int weight_dtype,
                                void* workspace, size_t workspace_bytes);
 
+/*
+ * flce_linear -- the transform in front of a head (an extra prediction head's block, a
+ * masked model's transform), or any linear layer:
+ *   z = x . weight^T + bias,  y = round(act(z) + residual)
+ * for N rows of I values, weight [O,I], bias [O] and residual [N,O] (either may be NULL).
+ * x, weight, bias, residual and slope are of `dtype`; y is of `y_dtype`: `dtype`, or
+ * float32 with bf16 rows. With z in float32, act is one of
+ *   NONE z;  RELU max(z, 0);  GELU z Phi(z);  GELU_TANH z (1 + tanh(sqrt(2/pi) (z +
+ *   0.044715 z^3))) / 2;  SILU z / (1 + exp(-z))
+ * slope [N,O] (dense; NULL: not wanted) gets round(act'(z)), which the backward reads
+ * (relu's slope at 0 is 0). weight and bias are dense; x, residual, y have row strides. In
+ * place: y may be the residual (same pointer, stride and type). N = 0 does nothing.
+ * flce_linear_check_args: FLCE_ERR_ARG for N < 0 or N >= 2^31, I or O outside [1, 2^24], an
+ * unknown type or activation, a missing pointer, a row stride below its row or above 2^31,
+ * an output that overlaps anything else; FLCE_ERR_UNSUPPORTED for float32 rows with a bf16
+ * y, a pointer not aligned to its elements or sizes beyond one grid.
+ */
+typedef enum {
+  FLCE_ACT_NONE = 0, FLCE_ACT_RELU = 1, FLCE_ACT_GELU = 2, FLCE_ACT_GELU_TANH = 3,
+  FLCE_ACT_SILU = 4
+} flce_activation_t;
+int flce_linear_check_args(const void* x, int64_t ld_x, const void* weight, const void* bias,
+                           const void* residual, int64_t ld_res, int64_t N, int64_t I, int64_t O,
+                           int activation, const void* y, int64_t ld_y, const void* slope,
+                           const void* stream, int dtype, int y_dtype);
+int flce_linear(const void* x, int64_t ld_x, const void* weight, const void* bias,
+                const void* residual, int64_t ld_res, int64_t N, int64_t I, int64_t O,
+                int activation, void* y, int64_t ld_y, void* slope, void* stream, int dtype,
+                int y_dtype);
+
+/*
+ * flce_linear_backward -- with dz = round(dy * slope) (slope NULL: dz is dy):
+ *   dx = round(dz . weight),  dweight = round(dz^T . x),  dbias = round(sum over rows of
+ *   dy * slope);  the residual's gradient is dy.
+ * Any of dx [N,I], dweight [O,I], dbias [O] may be NULL (not wanted; then weight, x are
+ * needed only by dx, dweight). With `accumulate` dweight and dbias are added to what is
+ * there. Sums are float32 in a fixed order: the same bits on every run. N = 0 zeroes
+ * dweight and dbias unless it accumulates. All are of `dtype`; dy, x, dx have row strides.
+ * The workspace (256-byte aligned) is flce_linear_backward_workspace_size bytes (0 for
+ * invalid sizes): dz and partial sums. No output may overlap anything else. Errors as
+ * flce_linear_check_args, and FLCE_ERR_WORKSPACE.
+ */
+size_t flce_linear_backward_workspace_size(int64_t N, int64_t I, int64_t O, int dtype);
+int flce_linear_backward_check_args(const void* dy, int64_t ld_dy, const void* x, int64_t ld_x,
+                                    const void* weight, const void* slope, int64_t N, int64_t I,
+                                    int64_t O, const void* dx, int64_t ld_dx,
+                                    const void* dweight, const void* dbias, int accumulate,
+                                    const void* stream, int dtype, const void* workspace,
+                                    size_t workspace_bytes);
+int flce_linear_backward(const void* dy, int64_t ld_dy, const void* x, int64_t ld_x,
+                         const void* weight, const void* slope, int64_t N, int64_t I, int64_t O,
+                         void* dx, int64_t ld_dx, void* dweight, void* dbias, int accumulate,
+                         void* stream, int dtype, void* workspace, size_t workspace_bytes);
+
+/*
+ * flce_sample_logits -- the next token of each of N rows of logits z [N,V] (float32 or
+ * bf16, row stride ld_logits) from one uniform number in [0, 1) a row:
+ *   x = softcap(z) / temperature;  w = exp(x - max x)
+ *   ranks: largest z first, equal ones by lowest index
+ *   top-k:  the first top_k ranks are kept (top_k <= 0 or >= V: all)
+ *   top-p:  of those, a rank is kept while the mass of the ranks above it is below top_p
+ *           times the mass of all of them (top_p >= 1: all; the first always)
+ *   min-p:  of those, w >= min_p (the first always)
+ *   tokens[i] = the lowest index with (mass of the kept ones up to it) > u * (their mass)
+ *   logp[i]   = log of its share of the kept mass (float32; NULL: not wanted)
+ * temperature 0 takes the largest logit (lowest index). A uniform number outside [0, 1) is
+ * moved to the nearer end (the last kept token at 1; NaN counts as 0). Each setting is one
+ * value, or with its array not NULL a device value for each row (float32, top_k int32; the
+ * value is then not read): of those, temperatures that are not above 0 take the largest
+ * logit, top_p below 0 or NaN count as 0, min_p is moved into [0, 1] (NaN: 0).
+ * Logits of -inf have no mass (a softcap leaves them so). A row with a NaN gives token -1 and logp NaN, a row of -inf
+ * alone token -1 and logp -inf; next to a +inf only the +inf have mass.
+ * Weights are formed in 64-bit floating point and summed as whole multiples of 2^-S of the
+ * largest, S = min(51, 62 - ceil(log2 V)): the result does not depend on an order of sums.
+ * flce_sample_logits_check_args: FLCE_ERR_ARG for N < 0 or N >= 2^31, V outside [1, 2^24], an
+ * unknown type, a missing pointer (logits, uniforms, tokens), ld_logits < V, softcap
+ * negative or not finite, a setting without array that is NaN, a temperature or top_k below
+ * 0, a temperature that is not finite, top_p outside (0, 1], min_p outside [0, 1], an
+ * output that overlaps anything; FLCE_ERR_UNSUPPORTED for a misaligned pointer or more
+ * rows than one grid takes (2^22 - 1).
+ */
+int flce_sample_logits_check_args(const void* logits, int64_t ld_logits, int64_t N, int64_t V,
+                                  const float* uniforms, float temperature,
+                                  const float* temperatures, int32_t top_k,
+                                  const int32_t* top_ks, float top_p, const float* top_ps,
+                                  float min_p, const float* min_ps, float softcap,
+                                  const int64_t* tokens, const float* logp, const void* stream,
+                                  int dtype);
+int flce_sample_logits(const void* logits, int64_t ld_logits, int64_t N, int64_t V,
+                       const float* uniforms, float temperature, const float* temperatures,
+                       int32_t top_k, const int32_t* top_ks, float top_p, const float* top_ps,
+                       float min_p, const float* min_ps, float softcap, int64_t* tokens,
+                       float* logp, void* stream, int dtype);
+
+/*
+ * flce_sample -- flce_sample_logits of the logits z = h . W^T (float32) of the head W [V,H]
+ * at N rows h [N,H] (dense, `dtype`). The logits live in the workspace, as many rows at a
+ * time as fit 512 MiB: flce_sample_workspace_size bytes (0 for invalid sizes), 256-byte
+ * aligned. Errors as flce_sample_logits and flce_linear, and FLCE_ERR_WORKSPACE.
+ */
+size_t flce_sample_workspace_size(int64_t N, int64_t H, int64_t V, int dtype);
+int flce_sample_check_args(const void* h, const void* W, int64_t N, int64_t H, int64_t V,
+                           const float* uniforms, float temperature, const float* temperatures,
+                           int32_t top_k, const int32_t* top_ks, float top_p,
+                           const float* top_ps, float min_p, const float* min_ps, float softcap,
+                           const int64_t* tokens, const float* logp, const void* stream,
+                           int dtype, const void* workspace, size_t workspace_bytes);
+int flce_sample(const void* h, const void* W, int64_t N, int64_t H, int64_t V,
+                const float* uniforms, float temperature, const float* temperatures,
+                int32_t top_k, const int32_t* top_ks, float top_p, const float* top_ps,
+                float min_p, const float* min_ps, float softcap, int64_t* tokens, float* logp,
+                void* stream, int dtype, void* workspace, size_t workspace_bytes);
+
 /* flce_status_string -- a static, human-readable name for a status code
  * (this library's own addition; no page defines status codes). */
 const char* flce_status_string(int status);

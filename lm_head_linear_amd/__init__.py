@@ -47,6 +47,12 @@ from ._ops import (  # noqa: F401
     flce_rms_norm_backward, flce_rms_norm_backward_check_args,
     flce_rms_norm_backward_workspace_size, flce_rms_norm_check_args, fused_embedding,
     fused_rms_norm, token_logprobs)
+from ._linear import (  # noqa: F401
+    HeadTransform, flce_linear, flce_linear_backward, flce_linear_backward_check_args,
+    flce_linear_backward_workspace_size, flce_linear_check_args, fused_linear)
+from ._sample import (  # noqa: F401
+    Sampled, flce_sample, flce_sample_check_args, flce_sample_logits,
+    flce_sample_logits_check_args, flce_sample_workspace_size)
 from ._util import FlceError, _check_tensor, _dtype_code, _ptr, flce_status_string
 
 __all__ = [
@@ -88,6 +94,19 @@ __all__ = [
     "flce_embedding_backward_workspace_size",
     "fused_rms_norm",
     "fused_embedding",
+    "flce_linear",
+    "flce_linear_check_args",
+    "flce_linear_backward",
+    "flce_linear_backward_check_args",
+    "flce_linear_backward_workspace_size",
+    "fused_linear",
+    "HeadTransform",
+    "flce_sample",
+    "flce_sample_check_args",
+    "flce_sample_workspace_size",
+    "flce_sample_logits",
+    "flce_sample_logits_check_args",
+    "Sampled",
     "DropoutMask",
     "flce_dropout",
     "flce_dropout_check_args",
@@ -598,12 +617,15 @@ class TiedLMHead(torch.nn.Module):
     ``embed(tokens)`` looks tokens up (times ``embed_scale``); the model's layers
     run between; ``loss(x, labels, residual)`` and ``logprobs(x, tokens,
     residual)`` add the residual, normalise (norm_eps, norm_weight + weight_offset)
-    and run the head. W's gradient is the sum of the embedding's and the head's.
+    and run the head; ``sample(x, uniforms, residual)`` draws each position's next token.
+    W's gradient is the sum of the embedding's and the head's. With ``transform`` (an
+    activation) a :class:`HeadTransform` stands between the norm and the head.
     """
 
     def __init__(self, vocab_size: int, hidden_size: int, *, ignore_index: int = -100,
                  logit_softcapping: float = 0.0, reduction: str = "sum", embed_scale: float = 1.0,
-                 norm_eps: float = 1e-6, weight_offset: float = 0.0, device=None, dtype=None):
+                 norm_eps: float = 1e-6, weight_offset: float = 0.0,
+                 transform: Optional[str] = None, device=None, dtype=None):
         super().__init__()
         kw = dict(device=device, dtype=dtype)
         self.weight = torch.nn.Parameter(torch.randn(vocab_size, hidden_size, **kw) * 0.02)
@@ -613,6 +635,9 @@ class TiedLMHead(torch.nn.Module):
         self.embed_scale = float(embed_scale)
         self.norm_eps = float(norm_eps)
         self.weight_offset = float(weight_offset)
+        self.transform = None
+        if transform is not None:
+            self.transform = HeadTransform(hidden_size, activation=transform, **kw)
 
     def embed(self, tokens: torch.Tensor, dropout: Optional[DropoutMask] = None) -> torch.Tensor:
         """embed_scale * W[tokens], dropped out by the mask where one is given; a token equal
@@ -631,17 +656,36 @@ class TiedLMHead(torch.nn.Module):
                              weight_offset=self.weight_offset)
         return out if residual is None else out[0]
 
+    def rows(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None,
+             dropout: Optional[DropoutMask] = None) -> torch.Tensor:
+        """What the head multiplies by: the normalised rows, transformed."""
+        n = self.norm(x, residual, dropout)
+        return n if self.transform is None else self.transform(n)
+
     def loss(self, x: torch.Tensor, labels: torch.Tensor,
              residual: Optional[torch.Tensor] = None, *,
              dropout: Optional[DropoutMask] = None, **kw) -> torch.Tensor:
-        """The head's loss (:class:`FusedLinearCrossEntropy`) of the normalised rows."""
-        return self.criterion(self.norm(x, residual, dropout), labels, self.weight, **kw)
+        """The head's loss (:class:`FusedLinearCrossEntropy`) of the normalised (and
+        transformed) rows."""
+        return self.criterion(self.rows(x, residual, dropout), labels, self.weight, **kw)
 
     def logprobs(self, x: torch.Tensor, tokens: Optional[torch.Tensor] = None,
                  residual: Optional[torch.Tensor] = None, *, temperature: float = 1.0,
                  top_k: int = 0) -> TokenLogprobs:
         """:func:`token_logprobs` of the normalised rows."""
-        return token_logprobs(self.norm(x, residual), tokens, self.weight,
+        return token_logprobs(self.rows(x, residual), tokens, self.weight,
                               ignore_index=self.criterion.ignore_index,
                               softcap=self.criterion.logit_softcapping, temperature=temperature,
                               top_k=top_k)
+
+    @torch.no_grad()
+    def sample(self, x: torch.Tensor, uniforms: torch.Tensor,
+               residual: Optional[torch.Tensor] = None, **kw) -> Sampled:
+        """:func:`flce_sample` of the normalised rows of x [..., H] from uniforms [...];
+        settings given as tensors have the uniforms' shape."""
+        n = self.rows(x, residual)
+        flat = lambda v: v.reshape(-1).contiguous() if isinstance(v, torch.Tensor) else v  # noqa: E731
+        r = flce_sample(n.reshape(-1, n.shape[-1]).contiguous(), self.weight.contiguous(),
+                        flat(uniforms), softcap=self.criterion.logit_softcapping,
+                        **{k: flat(v) for k, v in kw.items()})
+        return Sampled(*(t.view(uniforms.shape) for t in r))

@@ -12,6 +12,8 @@ SUM, MEAN = 0, 1
 OK, ERR_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_HIP, ERR_LABEL, ERR_SCRATCH = range(7)
 # bytes of the fixed scratch array behind flce_forward_noalloc (FLCE_NOALLOC_SCRATCH_BYTES)
 NOALLOC_SCRATCH_BYTES = 96 << 20
+# activations of flce_linear (flce_activation_t)
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 # most alternatives of flce_logprobs (FLCE_MAX_TOP)
 MAX_TOP = 32
 
@@ -40,6 +42,12 @@ _DROP_NORM = [_vp, _i64, _vp, _i64, _vp, _i64, _i64, _f32, _f32] + _DROP + [
     _vp, _i64, _vp, _i64, _vp, _vp, _i32, _i32]
 _DROP_NORM_BWD = [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _f32] + _DROP + [
     _vp, _i64, _vp, _i64, _vp, _i32, _vp, _i32, _i32, _vp, _sz]
+_LINEAR = [_vp, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i32, _vp, _i64, _vp, _vp, _i32, _i32]
+_LINEAR_BWD = [_vp, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _i32, _vp,
+               _i32, _vp, _sz]
+_SETTINGS = [_vp, _f32, _vp, _i32, _vp, _f32, _vp, _f32, _vp, _f32, _vp, _vp, _vp, _i32]
+_SAMPLE_LOGITS = [_vp, _i64, _i64, _i64] + _SETTINGS
+_SAMPLE = [_vp, _vp, _i64, _i64, _i64] + _SETTINGS + [_vp, _sz]
 SIGNATURES = {
     "flce_workspace_size": (_sz, [_i64, _i64, _i64, _i32]),
     "flce_check_args": (_i32, _FB_ARGS),
@@ -64,6 +72,16 @@ SIGNATURES = {
     "flce_rms_norm_backward_workspace_size": (_sz, [_i64, _i64]),
     "flce_rms_norm_backward_check_args": (_i32, _NORM_BWD),
     "flce_rms_norm_backward": (_i32, _NORM_BWD),
+    "flce_linear_check_args": (_i32, _LINEAR),
+    "flce_linear": (_i32, _LINEAR),
+    "flce_linear_backward_workspace_size": (_sz, [_i64, _i64, _i64, _i32]),
+    "flce_linear_backward_check_args": (_i32, _LINEAR_BWD),
+    "flce_linear_backward": (_i32, _LINEAR_BWD),
+    "flce_sample_logits_check_args": (_i32, _SAMPLE_LOGITS),
+    "flce_sample_logits": (_i32, _SAMPLE_LOGITS),
+    "flce_sample_workspace_size": (_sz, [_i64, _i64, _i64, _i32]),
+    "flce_sample_check_args": (_i32, _SAMPLE),
+    "flce_sample": (_i32, _SAMPLE),
     "flce_dropout_check_args": (_i32, _DROPOUT),
     "flce_dropout": (_i32, _DROPOUT),
     "flce_dropout_norm_check_args": (_i32, _DROP_NORM),

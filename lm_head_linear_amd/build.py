@@ -14,8 +14,9 @@ LIB = os.path.join(PKG, "libflce.so")
 
 HIP_SOURCES = ["flce_api.hip", "kernels_common.hip", "kernels_bf16.hip", "kernels_f32.hip",
                "ops_api.hip", "kernels_norm.hip", "kernels_embed.hip", "kernels_logprobs.hip",
-               "kernels_dropout.hip"]
-CXX_SOURCES = ["flce_check.cpp", "ops_check.cpp", "dropout_check.cpp"]
+               "kernels_dropout.hip", "kernels_linear.hip", "kernels_sample.hip"]
+CXX_SOURCES = ["flce_check.cpp", "ops_check.cpp", "dropout_check.cpp", "linear_check.cpp",
+               "sample_check.cpp"]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [

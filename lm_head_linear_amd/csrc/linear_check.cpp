@@ -1,0 +1,95 @@
+// Synchronous argument checks and workspace plan of the linear transform (no HIP calls).
+#include "../../include/flce.h"
+#include "check_util.h"
+#include "ops_plan.h"
+
+namespace flce {
+
+namespace {
+bool sizes_ok(int64_t N, int64_t I, int64_t O) {
+  return N >= 0 && N <= kMaxGrid && I > 0 && I <= kMaxWidth && O > 0 && O <= kMaxWidth;
+}
+}  // namespace
+
+bool make_linear_plan(int64_t N, int64_t I, int64_t O, int dtype, LinearPlan* out) {
+  if (!sizes_ok(N, I, O) || !is_dtype(dtype)) return false;
+  LinearPlan p;
+  p.dz_parts = ceil_div(N, kLinearDzRows);
+  size_t off = 0;
+  p.off_dz = off; off = align256(off + size_t(N) * O * esize(dtype));
+  p.off_part = off; off = align256(off + size_t(p.dz_parts) * O * 4);
+  p.total = off ? off : 256;
+  *out = p;
+  return true;
+}
+
+}  // namespace flce
+
+using namespace flce;
+
+namespace {
+
+bool is_act(int a) { return a >= FLCE_ACT_NONE && a <= FLCE_ACT_SILU; }
+
+// Tiles of 128 x 128 of a product in one grid of 256 threads each.
+int64_t tiles(int64_t a, int64_t b) { return ceil_div(a, 128) * ceil_div(b, 128); }
+
+}  // namespace
+
+extern "C" {
+
+int flce_linear_check_args(const void* x, int64_t ld_x, const void* weight, const void* bias,
+                           const void* residual, int64_t ld_res, int64_t N, int64_t I, int64_t O,
+                           int activation, const void* y, int64_t ld_y, const void* slope,
+                           const void* stream, int dtype, int y_dtype) {
+  (void)stream;
+  if (!sizes_ok(N, I, O) || !is_dtype(dtype) || !is_dtype(y_dtype) || !is_act(activation))
+    return FLCE_ERR_ARG;
+  if (!weight || (N > 0 && (!x || !y))) return FLCE_ERR_ARG;
+  if (bad_ld(ld_x, I) || bad_ld(ld_y, O) || (residual && bad_ld(ld_res, O))) return FLCE_ERR_ARG;
+  const size_t es = esize(dtype), ys = esize(y_dtype);
+  const Buf bx = matrix(x, N, I, ld_x, es), bw = matrix(weight, O, I, I, es), bb = vec(bias, O, es),
+            br = matrix(residual, N, O, ld_res, es), by = matrix(y, N, O, ld_y, ys),
+            bs = matrix(slope, N, O, O, es);
+  // in place: y may be the residual
+  if (overlap(by, br) && !same(by, br)) return FLCE_ERR_ARG;
+  if (clash({by, bs}, {bx, bw, bb}) || overlap(bs, br)) return FLCE_ERR_ARG;
+  if (dtype == FLCE_F32 && y_dtype != FLCE_F32) return FLCE_ERR_UNSUPPORTED;
+  if (tiles(O, N) > max_groups(256)) return FLCE_ERR_UNSUPPORTED;
+  for (const Buf& b : {bx, bw, bb, br, by, bs})
+    if (misaligned(b)) return FLCE_ERR_UNSUPPORTED;
+  return FLCE_OK;
+}
+
+size_t flce_linear_backward_workspace_size(int64_t N, int64_t I, int64_t O, int dtype) {
+  LinearPlan p;
+  return make_linear_plan(N, I, O, dtype, &p) ? p.total : 0;
+}
+
+int flce_linear_backward_check_args(const void* dy, int64_t ld_dy, const void* x, int64_t ld_x,
+                                    const void* weight, const void* slope, int64_t N, int64_t I,
+                                    int64_t O, const void* dx, int64_t ld_dx,
+                                    const void* dweight, const void* dbias, int accumulate,
+                                    const void* stream, int dtype, const void* workspace,
+                                    size_t workspace_bytes) {
+  (void)stream; (void)accumulate;
+  LinearPlan p;
+  if (!make_linear_plan(N, I, O, dtype, &p)) return FLCE_ERR_ARG;
+  if (N > 0 && (!dy || (dx && !weight) || (dweight && !x))) return FLCE_ERR_ARG;
+  if (bad_ld(ld_dy, O) || (x && bad_ld(ld_x, I)) || (dx && bad_ld(ld_dx, I))) return FLCE_ERR_ARG;
+  const size_t es = esize(dtype);
+  const Buf bg = matrix(dy, N, O, ld_dy, es), bx = matrix(x, N, I, ld_x, es),
+            bw = matrix(weight, O, I, I, es), bs = matrix(slope, N, O, O, es),
+            bdx = matrix(dx, N, I, ld_dx, es), bdw = matrix(dweight, O, I, I, es),
+            bdb = vec(dbias, O, es), wk = vec(workspace, int64_t(workspace_bytes), 1);
+  if (clash({bdx, bdw, bdb, wk}, {bg, bx, bw, bs})) return FLCE_ERR_ARG;
+  if (tiles(I, N) + 8 + tiles(I, O) > max_groups(256) ||
+      ceil_div(O, 128) * p.dz_parts > max_groups(256))
+    return FLCE_ERR_UNSUPPORTED;
+  for (const Buf& b : {bg, bx, bw, bs, bdx, bdw, bdb})
+    if (misaligned(b)) return FLCE_ERR_UNSUPPORTED;
+  if (!workspace || wk.begin() % 256 != 0 || workspace_bytes < p.total) return FLCE_ERR_WORKSPACE;
+  return FLCE_OK;
+}
+
+}  // extern "C"

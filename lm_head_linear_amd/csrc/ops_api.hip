@@ -54,6 +54,91 @@ int flce_rms_norm_backward(const void* dy, int64_t ld_dy, const void* ds, int64_
   return status_of(flce::launch_rms_norm_backward(a, L));
 }
 
+int flce_linear(const void* x, int64_t ld_x, const void* weight, const void* bias,
+                const void* residual, int64_t ld_res, int64_t N, int64_t I, int64_t O,
+                int activation, void* y, int64_t ld_y, void* slope, void* stream, int dtype,
+                int y_dtype) {
+  const int st = flce_linear_check_args(x, ld_x, weight, bias, residual, ld_res, N, I, O,
+                                        activation, y, ld_y, slope, stream, dtype, y_dtype);
+  if (st != FLCE_OK || N == 0) return st;
+  Range r("flce_linear");
+  const flce::LinearArgs a{x, ld_x, weight, bias, residual, ld_res, N, I, O, activation,
+                           y, ld_y, slope, dtype, y_dtype};
+  return status_of(flce::launch_linear(a, flce::make_launcher(stream)));
+}
+
+int flce_linear_backward(const void* dy, int64_t ld_dy, const void* x, int64_t ld_x,
+                         const void* weight, const void* slope, int64_t N, int64_t I, int64_t O,
+                         void* dx, int64_t ld_dx, void* dweight, void* dbias, int accumulate,
+                         void* stream, int dtype, void* workspace, size_t workspace_bytes) {
+  const int st = flce_linear_backward_check_args(dy, ld_dy, x, ld_x, weight, slope, N, I, O, dx,
+                                                 ld_dx, dweight, dbias, accumulate, stream, dtype,
+                                                 workspace, workspace_bytes);
+  if (st != FLCE_OK) return st;
+  Range r("flce_linear_backward");
+  const Launcher L = flce::make_launcher(stream);
+  if (N == 0) {
+    const size_t es = dtype == FLCE_BF16 ? 2 : 4;
+    hipError_t e = hipSuccess;
+    if (dweight && !accumulate) e = flce::launch_zero_bytes(dweight, size_t(O) * I * es, L);
+    if (e == hipSuccess && dbias && !accumulate) e = flce::launch_zero_bytes(dbias, size_t(O) * es, L);
+    return status_of(e);
+  }
+  flce::LinearPlan p;
+  if (!flce::make_linear_plan(N, I, O, dtype, &p)) return FLCE_ERR_ARG;
+  const flce::LinearBwdArgs a{dy, ld_dy, x, ld_x, weight, slope, N, I, O, dx, ld_dx, dweight,
+                              dbias, accumulate ? 1 : 0, dtype};
+  return status_of(flce::launch_linear_backward(p, a, static_cast<char*>(workspace), L));
+}
+
+int flce_sample_logits(const void* logits, int64_t ld_logits, int64_t N, int64_t V,
+                       const float* uniforms, float temperature, const float* temperatures,
+                       int32_t top_k, const int32_t* top_ks, float top_p, const float* top_ps,
+                       float min_p, const float* min_ps, float softcap, int64_t* tokens,
+                       float* logp, void* stream, int dtype) {
+  const int st = flce_sample_logits_check_args(logits, ld_logits, N, V, uniforms, temperature,
+                                               temperatures, top_k, top_ks, top_p, top_ps, min_p,
+                                               min_ps, softcap, tokens, logp, stream, dtype);
+  if (st != FLCE_OK || N == 0) return st;
+  Range r("flce_sample_logits");
+  const flce::SampleArgs a{logits, ld_logits, N, V, uniforms, {temperatures, temperature},
+                           {top_ps, top_p}, {min_ps, min_p}, {top_ks, top_k}, softcap, tokens,
+                           logp, dtype, flce::sample_weight_bits(V)};
+  return status_of(flce::launch_sample(a, flce::make_launcher(stream)));
+}
+
+int flce_sample(const void* h, const void* W, int64_t N, int64_t H, int64_t V,
+                const float* uniforms, float temperature, const float* temperatures,
+                int32_t top_k, const int32_t* top_ks, float top_p, const float* top_ps,
+                float min_p, const float* min_ps, float softcap, int64_t* tokens, float* logp,
+                void* stream, int dtype, void* workspace, size_t workspace_bytes) {
+  const int st = flce_sample_check_args(h, W, N, H, V, uniforms, temperature, temperatures, top_k,
+                                        top_ks, top_p, top_ps, min_p, min_ps, softcap, tokens,
+                                        logp, stream, dtype, workspace, workspace_bytes);
+  if (st != FLCE_OK || N == 0) return st;
+  Range range("flce_sample");
+  const Launcher L = flce::make_launcher(stream);
+  flce::SamplePlan p;
+  if (!flce::make_sample_plan(N, H, V, dtype, &p)) return FLCE_ERR_ARG;
+  const size_t es = dtype == FLCE_BF16 ? 2 : 4;
+  auto from = [](auto* v, int64_t r) { return v ? v + r : v; };
+  for (int64_t r = 0; r < N; r += p.rows) {
+    const int64_t n = N - r < p.rows ? N - r : p.rows;
+    const flce::LinearArgs z{static_cast<const char*>(h) + size_t(r) * H * es, H, W, nullptr,
+                             nullptr, V, n, H, V, FLCE_ACT_NONE, workspace, V, nullptr, dtype,
+                             FLCE_F32};
+    hipError_t e = flce::launch_linear(z, L);
+    if (e != hipSuccess) return status_of(e);
+    const flce::SampleArgs a{workspace, V, n, V, uniforms + r, {from(temperatures, r), temperature},
+                             {from(top_ps, r), top_p}, {from(min_ps, r), min_p},
+                             {from(top_ks, r), top_k}, softcap, tokens + r, from(logp, r), FLCE_F32,
+                             flce::sample_weight_bits(V)};
+    e = flce::launch_sample(a, L);
+    if (e != hipSuccess) return status_of(e);
+  }
+  return FLCE_OK;
+}
+
 int flce_dropout(const void* x, int64_t ld_x, const void* residual, int64_t ld_res, int64_t N,
                  int64_t H, double p, uint64_t seed, uint64_t offset, const int64_t* step,
                  void* out, int64_t ld_out, void* stream, int dtype) {

@@ -90,6 +90,90 @@ struct NormBwdArgs {
 constexpr int64_t kNormShares = 1024;
 inline int64_t norm_shares(int64_t N) { return N < kNormShares ? N : kNormShares; }
 
+// ---- the linear transform in front of the head ---------------------------------------
+struct LinearArgs {
+  const void* x;
+  int64_t ld_x;
+  const void* weight;         // [O][I]
+  const void* bias;           // may be null
+  const void* residual;       // may be null
+  int64_t ld_res;
+  int64_t N, I, O;
+  int activation;
+  void* y;
+  int64_t ld_y;
+  void* slope;                // may be null
+  int dtype, y_dtype;
+};
+
+struct LinearBwdArgs {
+  const void* dy;
+  int64_t ld_dy;
+  const void* x;
+  int64_t ld_x;
+  const void* weight;
+  const void* slope;          // null: 1
+  int64_t N, I, O;
+  void* dx;                   // may be null
+  int64_t ld_dx;
+  void* dweight;              // may be null
+  void* dbias;                // may be null
+  int accumulate;             // dweight and dbias are added to
+  int dtype;
+};
+
+// Rows of dz a workgroup forms (and adds up for db).
+constexpr int64_t kLinearDzRows = 64;
+
+struct LinearPlan {
+  int64_t dz_parts = 0;
+  size_t off_dz = 0, off_part = 0, total = 0;
+};
+
+bool make_linear_plan(int64_t N, int64_t I, int64_t O, int dtype, LinearPlan* p);
+
+// ---- sampling ------------------------------------------------------------------------
+// A setting of a call: one value, or a value a row (device).
+template <class T>
+struct Setting {
+  const T* rows;              // null: value
+  T value;
+#if defined(__HIPCC__)
+  __device__ __forceinline__ T at(int64_t r) const { return rows ? rows[r] : value; }
+#endif
+};
+
+struct SampleArgs {
+  const void* logits;         // [N][ld]
+  int64_t ld, N, V;
+  const float* uniforms;
+  Setting<float> temperature, top_p, min_p;
+  Setting<int32_t> top_k;
+  float softcap;
+  int64_t* tokens;
+  float* logp;                // may be null
+  int dtype;
+  int weight_bits;            // S: weights are multiples of 2^-S of the largest
+};
+
+// Bits of a weight so that V of them sum up below 2^63, and at most what one rounding of a
+// 64-bit floating-point value to a whole number holds.
+inline int sample_weight_bits(int64_t V) {
+  int log_v = 0;
+  while ((int64_t(1) << log_v) < V) ++log_v;
+  return 62 - log_v < 51 ? 62 - log_v : 51;
+}
+
+// Logits of the head form: as many rows at a time as fit these bytes.
+constexpr int64_t kSampleLogitBytes = int64_t(512) << 20;
+
+struct SamplePlan {
+  int64_t rows = 0;
+  size_t total = 0;
+};
+
+bool make_sample_plan(int64_t N, int64_t H, int64_t V, int dtype, SamplePlan* p);
+
 // ---- embedding ---------------------------------------------------------------------
 // Tokens that one workgroup sorts in LDS, tokens up to which such chunks are
 // merged at once, and tokens per workgroup of the digit passes beyond that.
@@ -304,6 +388,10 @@ namespace flce {
 
 hipError_t launch_rms_norm(const NormArgs& a, const Launcher& L);
 hipError_t launch_rms_norm_backward(const NormBwdArgs& a, const Launcher& L);
+hipError_t launch_linear(const LinearArgs& a, const Launcher& L);
+hipError_t launch_linear_backward(const LinearPlan& p, const LinearBwdArgs& a, char* ws,
+                                  const Launcher& L);
+hipError_t launch_sample(const SampleArgs& a, const Launcher& L);
 hipError_t launch_dropout(const DropoutArgs& a, const Launcher& L);
 hipError_t launch_embedding(const EmbedArgs& a, const Launcher& L);
 hipError_t launch_embedding_backward(const EmbedGradArgs& a, const Launcher& L);
