@@ -656,8 +656,8 @@ int flce_dropout_norm_backward(const void* dy, int64_t ld_dy, const void* ds, in
  * masked model's transform), or any linear layer:
  *   z = x . weight^T + bias,  y = round(act(z) + residual)
  * for N rows of I values, weight [O,I], bias [O] and residual [N,O] (either may be NULL).
- * x, weight, bias, residual and slope are of `dtype`; y is of `y_dtype`: `dtype`, or
- * float32 with bf16 rows. With z in float32, act is one of
+ * x, weight, bias and residual are of `dtype`; y is of `y_dtype`: `dtype`, or float32
+ * with bf16 rows; slope is float32 with float32 rows and IEEE half (float16) with bf16. With z in float32, act is one of
  *   NONE z;  RELU max(z, 0);  GELU z Phi(z);  GELU_TANH z (1 + tanh(sqrt(2/pi) (z +
  *   0.044715 z^3))) / 2;  SILU z / (1 + exp(-z))
  * slope [N,O] (dense; NULL: not wanted) gets round(act'(z)), which the backward reads

@@ -18,6 +18,10 @@ def _act_code(activation: str) -> int:
     return _lib.ACTIVATIONS[activation]
 
 
+def _slope_dtype(dt):
+    return torch.float16 if dt == torch.bfloat16 else torch.float32
+
+
 def flce_linear_check_args(x, weight, bias=None, residual=None, *, N, I, O, activation="none",
                            ld_x=None, ld_res=None, y=None, ld_y=None, slope=None,
                            dtype=torch.bfloat16, y_dtype=None) -> int:
@@ -35,8 +39,8 @@ def flce_linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tens
                 y: Optional[torch.Tensor] = None, slope: Optional[torch.Tensor] = None):
     """act(x weight^T + bias) + residual for x [N, I], weight [O, I]: (y, slope).
 
-    ``slope`` is the activation's derivative, which :func:`flce_linear_backward` takes:
-    formed with ``save_slope`` (or where a tensor for it is passed in), otherwise None, and
+    ``slope`` is the activation's derivative (float32, or float16 with bf16 rows), which
+    :func:`flce_linear_backward` takes: formed with ``save_slope`` (or where a tensor for it is passed in), otherwise None, and
     None without an activation. y has x's type, or float32 with ``y_dtype``; ``y`` may be
     the residual (in place).
     """
@@ -61,7 +65,7 @@ def flce_linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tens
         if slope is not None:
             raise ValueError("slope is written only with an activation")
     elif slope is not None or save_slope:
-        slope = _out("slope", slope, (N, O), dt, dev)
+        slope = _out("slope", slope, (N, O), _slope_dtype(dt), dev)
     _run("flce_linear", dev, _lib.load().flce_linear, x.data_ptr(), ld_x, weight.data_ptr(),
          _ptr(bias), _ptr(residual), ld_r, N, I, O, act, y.data_ptr(), ld_y, _ptr(slope),
          _stream(dev), code, ycode)
@@ -103,7 +107,7 @@ def flce_linear_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor
     _check_tensor("weight", weight, (O, I), dt, dev)
     ld_dy, ld_x = _rows("dy", dy, N, O, dt, dev), _rows("x", x, N, I, dt, dev)
     if slope is not None:
-        _check_tensor("slope", slope, (N, O), dt, dev)
+        _check_tensor("slope", slope, (N, O), _slope_dtype(dt), dev)
     if accumulate and ((want_dweight and dweight is None) or (bias and dbias is None)):
         raise ValueError("accumulate needs the dweight and dbias tensors to add to")
     ld_dx = I

@@ -18,9 +18,15 @@ struct Activated {
   float y, slope;
 };
 
-__device__ __forceinline__ float sigma(float a) { return 1.f / (1.f + expf(-a)); }
+// FAST (results rounded to bf16): by the hardware's exponential and reciprocal, a few 2^-22
+// of the value for arguments to 80 in size, instead of their correctly rounded forms.
+template <bool FAST>
+__device__ __forceinline__ float sigma(float a) {
+  if constexpr (FAST) return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(a * -1.44269504f));
+  return 1.f / (1.f + expf(-a));
+}
 
-template <int ACT>
+template <int ACT, bool FAST>
 __device__ __forceinline__ Activated activate(float z) {
   if constexpr (ACT == FLCE_ACT_RELU) {
     return z > 0.f ? Activated{z, 1.f} : Activated{z != z ? z : 0.f, 0.f};
@@ -29,10 +35,10 @@ __device__ __forceinline__ Activated activate(float z) {
     return {z * P, fmaf(z * 0.39894228f, expf(-0.5f * z * z), P)};
   } else if constexpr (ACT == FLCE_ACT_GELU_TANH) {
     constexpr float k = 1.5957691216f, c = 0.044715f;         // 2 sqrt(2 / pi)
-    const float zz = z * z, s = sigma(k * z * fmaf(c, zz, 1.f));
+    const float zz = z * z, s = sigma<FAST>(k * z * fmaf(c, zz, 1.f));
     return {z * s, fmaf(z * s * (1.f - s), k * fmaf(3.f * c, zz, 1.f), s)};
   } else if constexpr (ACT == FLCE_ACT_SILU) {
-    const float s = sigma(z);
+    const float s = sigma<FAST>(z);
     return {z * s, s * fmaf(z, 1.f - s, 1.f)};
   } else {
     return {z, 1.f};

@@ -738,7 +738,55 @@ __device__ __forceinline__ void store_token_major(const Get& get, char* smem, in
   }
 }
 
-const uint16_t* buf_ptr(const Args& a, int buf) {
+// ---- row-major epilogues staged through LDS ---------------------------------
+// A wave's 128 x 128 float32 block goes out in 4 passes of 32 rows (row blocks
+// 2P and 2P + 1 of 16): the lane values are written to the wave's LDS scratch
+// as [32][128] float32 (the four 64-byte column quarters of a 256-byte bank
+// window permuted by row / 4, which puts the four 16-lane groups of a write on
+// different banks), then read back as float4 runs of 4 consecutive columns of
+// one row, which the caller's functor stores. Before the staging of each pass
+// the functor may issue its own global loads for that pass (prefetch), so
+// their latency overlaps the LDS traffic.
+__device__ __forceinline__ int staged_col(int row, int col) {
+  return col ^ (((row >> 2) & 3) << 4);
+}
+
+// Whether a pass also looks at each staged block as a whole.
+template <class P, class = void>
+struct HasStaged : std::false_type {};
+template <class P>
+struct HasStaged<P, std::void_t<decltype(&P::staged)>> : std::true_type {};
+
+template <class Pass>
+__device__ __forceinline__ void staged_rows(Acc& acc, int wm, int wn, int lane, char* smem,
+                                            Pass& pass) {
+  float* reg = reinterpret_cast<float*>(smem + (wm + 2 * wn) * kWaveScratch);
+  pass.prefetch(0, lane);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (i + 1 < 4) pass.prefetch(i + 1, lane);     // in flight while block i is staged
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int row = 16 * h + 4 * (lane >> 4) + r;
+          reg[row * 128 + staged_col(row, j * 16 + (lane & 15))] = acc[2 * i + h][j][r];
+        }
+    __builtin_amdgcn_wave_barrier();
+    if constexpr (HasStaged<Pass>::value) pass.staged(i, reg);
+#pragma unroll
+    for (int q = 0; q < 16; ++q) {
+      const int idx = q * 64 + lane, row = idx >> 5, c4 = idx & 31;
+      const float4 v = *reinterpret_cast<const float4*>(reg + row * 128 + staged_col(row, 4 * c4));
+      pass.store(i, q, row, 4 * c4, v);
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+[[maybe_unused]] const uint16_t* buf_ptr(const Args& a, int buf) {
   return buf == gemm::kBufW  ? static_cast<const uint16_t*>(a.W)
        : buf == gemm::kBufH  ? static_cast<const uint16_t*>(a.h)
        : buf == gemm::kBufHc ? static_cast<const uint16_t*>(a.hc)

@@ -1,19 +1,27 @@
 // The linear transform y = act(x W^T + b) + r, with W [O][I], and its backward:
 //   dz = dy act'(z);  dx = dz W;  dW = dz^T x;  db = sum over rows of dz   (dr is dy)
-// The forward stores the slope act'(z) where a backward will want it, rounded to the rows'
-// type: dz then needs no z and no exponential, and its error is the slope's half step,
-// where a rounded z would be carried through the slope's own steepness.
+// The forward stores the slope act'(z) where a backward will want it: dz then needs no z
+// and no exponential. With bf16 rows it is an IEEE half: slopes are at most 1.13, so its
+// range does, and its half step of 2^-12 leaves dz's own rounding (2^-9) the only one
+// that counts; a bf16 slope made the gradients' error 0.0029 of their size instead of
+// 0.0024, where rounding the exact ones once leaves 0.0017.
 //
 // Everything is float32 between a load and a store; what is rounded besides the outputs
 // is the slope and dz (bf16 rows: the products' operand). db sums dz before its rounding.
+//
+// Products of bf16 rows whose lengths and addresses are multiples of 16 bytes, with enough
+// tiles of 256 x 256 to fill the chip, run on the head's product (gemm_bf16.h); all others
+// on the one of 128 x 128 tiles (gemm_small.h).
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <initializer_list>
 #include <type_traits>
 
 #include "../../include/flce.h"
 #include "activation.h"
 #include "flce_internal.h"
+#include "gemm_bf16.h"
 #include "gemm_small.h"
 #include "ops_plan.h"
 #include "row_io.h"
@@ -62,6 +70,37 @@ __device__ __forceinline__ void store4(Bf16Bits* row, int64_t c, int64_t n, cons
   }
 }
 
+__device__ __forceinline__ void store4(_Float16* row, int64_t c, int64_t n, const float (&f)[4]) {
+  typedef __attribute__((ext_vector_type(4))) _Float16 f16x4;
+  typedef f16x4 __attribute__((aligned(2))) f16x4_any;
+  if (c + 4 <= n) {
+    *reinterpret_cast<f16x4_any*>(row + c) =
+        f16x4{_Float16(f[0]), _Float16(f[1]), _Float16(f[2]), _Float16(f[3])};
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (c + e < n) row[c + e] = _Float16(f[e]);
+  }
+}
+// A chunk of slopes.
+__device__ __forceinline__ void load_slope(const float* row, int64_t c, int64_t n, float (&f)[4]) {
+  load_chunk(row, c, n, f);
+}
+__device__ __forceinline__ void load_slope(const _Float16* row, int64_t c, int64_t n,
+                                           float (&f)[8]) {
+  typedef __attribute__((ext_vector_type(8))) _Float16 f16x8;
+  if (c + 8 <= n) {
+    const f16x8 v = __builtin_bit_cast(f16x8, load_raw(row + c));
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = float(v[e]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = c + e < n ? float(row[c + e]) : 0.f;
+  }
+}
+template <class T>
+using Slope = std::conditional_t<sizeof(T) == 2, _Float16, float>;
+
 // What follows z in the forward, four columns of a row at a time.
 template <class T, class OT>
 struct Finish {
@@ -70,7 +109,7 @@ struct Finish {
   int64_t ld_res;
   OT* y;
   int64_t ld_y;
-  T* slope;                   // may be null; [N][O]
+  Slope<T>* slope;            // may be null; [N][O]
   int64_t N, O;
   template <int ACT>
   __device__ __forceinline__ void store(int64_t c, int64_t r, float (&z)[4]) const {
@@ -83,7 +122,7 @@ struct Finish {
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const Activated a = activate<ACT>(z[e]);
+      const Activated a = activate<ACT, sizeof(OT) == 2>(z[e]);
       z[e] = a.y;
       d[e] = a.slope;
     }
@@ -128,6 +167,97 @@ __global__ __launch_bounds__(small::kThreads) void k_linear(small::Operand<T> W,
     fin.template store<ACT>(c, r, z);
   });
 }
+
+// The same behind the head's tiles: rows are tokens, columns W's rows. A lane has the same
+// four columns in every row of its wave's 128 x 128 block; the residual's are loaded a
+// pass of 32 rows ahead.
+template <class OT, int ACT>
+struct EpiLinear {
+  Finish<Bf16Bits, OT> fin;
+  bool res;
+
+  struct Pass {
+    const EpiLinear& e;
+    int64_t r0, c0;
+    int lane;
+    float bias[4];
+    uint2 res[2][16];
+    __device__ __forceinline__ void prefetch(int i, int) {
+      if (!e.res) return;
+      const int64_t c = c0 + 4 * (lane & 31);
+#pragma unroll
+      for (int q = 0; q < 16; ++q) {
+        const int64_t r = r0 + i * 32 + 2 * q + (lane >> 5);
+        if (r < e.fin.N && c < e.fin.O)
+          res[i & 1][q] = *reinterpret_cast<const uint2*>(e.fin.res + r * e.fin.ld_res + c);
+      }
+    }
+    __device__ __forceinline__ void store(int i, int q, int row, int col, float4 v) {
+      const int64_t r = r0 + i * 32 + row, c = c0 + col;
+      if (r >= e.fin.N || c >= e.fin.O) return;
+      const float z[4] = {v.x, v.y, v.z, v.w};
+      float y[4], d[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const Activated a = activate<ACT, sizeof(OT) == 2>(z[k] + bias[k]);
+        y[k] = a.y;
+        d[k] = a.slope;
+      }
+      if (ACT != FLCE_ACT_NONE && e.fin.slope) store4(e.fin.slope + r * e.fin.O, c, e.fin.O, d);
+      if (e.res) {
+        const uint2 o = res[i & 1][q];
+        y[0] += bf16_to_f32(uint16_t(o.x));
+        y[1] += bf16_to_f32(uint16_t(o.x >> 16));
+        y[2] += bf16_to_f32(uint16_t(o.y));
+        y[3] += bf16_to_f32(uint16_t(o.y >> 16));
+      }
+      store4(e.fin.y + r * e.fin.ld_y, c, e.fin.O, y);
+    }
+  };
+
+  static constexpr int kTokBytes = 0;
+  __device__ __forceinline__ void stage(char*, int64_t, int, int) const {}
+  __device__ __forceinline__ void operator()(Acc& acc, int64_t m0, int64_t n0, int wm, int wn,
+                                             int lane, char* smem, const char*) const {
+    Pass pass{*this, m0 + wm * 128, n0 + wn * 128, lane, {0.f, 0.f, 0.f, 0.f}, {}};
+    const int64_t c = n0 + wn * 128 + 4 * (lane & 31);
+    if (fin.bias && c < fin.O) load4(fin.bias, c, fin.O, pass.bias);
+    staged_rows(acc, wm, wn, lane, smem, pass);
+  }
+};
+
+// A gradient's rows behind the head's tiles.
+template <bool ACCUM>
+struct EpiGrad {
+  Bf16Bits* p;
+  int64_t ld, rows, cols;
+
+  struct Pass {
+    const EpiGrad& e;
+    int64_t r0, c0;
+    __device__ __forceinline__ void prefetch(int, int) {}
+    __device__ __forceinline__ void store(int i, int, int row, int col, float4 v) {
+      const int64_t r = r0 + i * 32 + row, c = c0 + col;
+      if (r >= e.rows || c >= e.cols) return;
+      float f[4] = {v.x, v.y, v.z, v.w};
+      if (ACCUM) {
+        float o[4];
+        load4(e.p + r * e.ld, c, e.cols, o);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) f[k] += o[k];
+      }
+      store4(e.p + r * e.ld, c, e.cols, f);
+    }
+  };
+
+  static constexpr int kTokBytes = 0;
+  __device__ __forceinline__ void stage(char*, int64_t, int, int) const {}
+  __device__ __forceinline__ void operator()(Acc& acc, int64_t m0, int64_t n0, int wm, int wn,
+                                             int lane, char* smem, const char*) const {
+    Pass pass{*this, m0 + wm * 128, n0 + wn * 128};
+    staged_rows(acc, wm, wn, lane, smem, pass);
+  }
+};
 
 // A gradient's tiles: C[rows][cols], row stride ld.
 template <class T>
@@ -176,8 +306,8 @@ __global__ __launch_bounds__(small::kThreads) void k_linear_grads(
 // rows of 32 chunks of columns, 8 rows at a time; cols workgroups stand side by side.
 template <class T, bool SLOPE>
 __global__ __launch_bounds__(256) void k_linear_dz(const T* __restrict__ dy, int64_t ld_dy,
-                                                   const T* __restrict__ slope, int64_t N,
-                                                   int64_t O, T* __restrict__ dz,
+                                                   const Slope<T>* __restrict__ slope,
+                                                   int64_t N, int64_t O, T* __restrict__ dz,
                                                    float* __restrict__ part, uint32_t cols) {
   constexpr int E = kPerChunk<T>;
   __shared__ float red[8][32 * E + 1];
@@ -197,7 +327,7 @@ __global__ __launch_bounds__(256) void k_linear_dz(const T* __restrict__ dy, int
       load_chunk(dy + r * ld_dy, c, O, g);
       if (SLOPE) {
         float d[E];
-        load_chunk(slope + r * O, c, O, d);
+        load_slope(slope + r * O, c, O, d);
 #pragma unroll
         for (int e = 0; e < E; ++e) g[e] *= d[e];
         store_chunk(dz + r * O, c, O, g);
@@ -245,14 +375,59 @@ __global__ __launch_bounds__(256) void k_linear_db(const float* __restrict__ par
   }
 }
 
+bool aligned16(std::initializer_list<const void*> ptrs, std::initializer_list<int64_t> lds) {
+  for (const void* p : ptrs)
+    if (reinterpret_cast<uintptr_t>(p) % 16) return false;
+  for (int64_t l : lds)
+    if (l % 8) return false;
+  return true;
+}
+
+// Whether a product of a x b outputs runs on the head's tiles: enough of them for most of
+// the 256 CUs (a workgroup each).
+bool on_large_tiles(int64_t a, int64_t b) { return gemm::num_tiles(a, b) >= kLinearLargeTiles; }
+
+// An operand of the head's product.
+struct Large {
+  int form;
+  const void* p;
+  gemm::Geom g;
+  bool fits() const {
+    return operand_offsets_fit(form, g) && (form == gemm::kFormN || g.rows >= 8);
+  }
+  Operand op() const { return Operand{static_cast<const uint16_t*>(p), g}; }
+};
+
+template <class OT>
+bool forward_large(const LinearArgs& a, const Finish<Bf16Bits, OT>& fin, const Launcher& L) {
+  const Large x{gemm::kFormN, a.x, {a.ld_x, a.N, a.I}}, W{gemm::kFormN, a.weight, {a.I, a.O, a.I}};
+  if (!on_large_tiles(a.N, a.O) || !x.fits() || !W.fits()) return false;
+  if (!aligned16({a.x, a.weight, a.bias, a.residual, a.y, a.slope},
+                 {a.I, a.O, a.ld_x, a.ld_y, a.residual ? a.ld_res : 0}))
+    return false;
+  with_activation(a.activation, [&](auto act) {
+    using Epi = EpiLinear<OT, decltype(act)::value>;
+    hipLaunchKernelGGL((k_gemm<0, 0, Epi, kDynNone>), dim3(unsigned(gemm::num_tiles(a.N, a.O))),
+                       dim3(kThreads), 0, L.stream, x.op(), W.op(), a.N, a.O, a.I, gemm::kGroupM,
+                       Epi{fin, a.residual != nullptr}, nullptr);
+  });
+  return true;
+}
+
 template <class T, class OT>
 hipError_t forward(const LinearArgs& a, const Launcher& L) {
   const T* W = static_cast<const T*>(a.weight);
   const T* x = static_cast<const T*>(a.x);
   const Finish<T, OT> fin{static_cast<const T*>(a.bias), static_cast<const T*>(a.residual),
-                          a.ld_res, static_cast<OT*>(a.y), a.ld_y, static_cast<T*>(a.slope),
+                          a.ld_res, static_cast<OT*>(a.y), a.ld_y, static_cast<Slope<T>*>(a.slope),
                           a.N, a.O};
   L.pre(kLinear);
+  if constexpr (sizeof(T) == 2) {
+    if (forward_large<OT>(a, fin, L)) {
+      L.post(kLinear);
+      return hipGetLastError();
+    }
+  }
   with_activation(a.activation, [&](auto act) {
     const dim3 grid(unsigned(tiles_of(a.O) * tiles_of(a.N)));
     hipLaunchKernelGGL((k_linear<T, OT, decltype(act)::value>), grid, dim3(small::kThreads), 0,
@@ -263,10 +438,32 @@ hipError_t forward(const LinearArgs& a, const Launcher& L) {
   return hipGetLastError();
 }
 
+// dx and dW in one grid, dx's tiles first.
+bool backward_large(const LinearBwdArgs& a, const Bf16Bits* g, int64_t ld_g, const Launcher& L) {
+  if (!a.dx || !a.dweight || !on_large_tiles(a.N + a.O, a.I)) return false;
+  const Large g1{gemm::kFormN, g, {ld_g, a.N, a.O}}, W{gemm::kFormT, a.weight, {a.I, a.I, a.O}};
+  const Large g2{gemm::kFormT, g, {ld_g, a.O, a.N}}, x{gemm::kFormT, a.x, {a.ld_x, a.I, a.N}};
+  if (!g1.fits() || !W.fits() || !g2.fits() || !x.fits()) return false;
+  if (!aligned16({g, a.weight, a.x, a.dx, a.dweight}, {a.I, a.O, ld_g, a.ld_x, a.ld_dx}))
+    return false;
+  const int64_t n1 = gemm::num_tiles(a.N, a.I), n1p = (n1 + 7) / 8 * 8;
+  const int64_t n2 = gemm::num_tiles(a.O, a.I);
+  const EpiGrad<false> e1{static_cast<Bf16Bits*>(a.dx), a.ld_dx, a.N, a.I};
+  auto go = [&](auto accum) {
+    using Epi2 = EpiGrad<decltype(accum)::value>;
+    hipLaunchKernelGGL((k_gemm_pair<0, 1, EpiGrad<false>, kDynNone, false, 1, 1, Epi2, kDynNone, 1>),
+                       dim3(unsigned(n1p + n2)), dim3(kThreads), 0, L.stream, n1p, n1, n1, int64_t(0),
+                       g1.op(), W.op(), a.N, a.I, a.O, e1, g2.op(), x.op(), a.O, a.I, a.N,
+                       Epi2{static_cast<Bf16Bits*>(a.dweight), a.I, a.O, a.I}, int64_t(0), nullptr);
+  };
+  a.accumulate ? go(std::true_type{}) : go(std::false_type{});
+  return true;
+}
+
 template <class T>
 hipError_t backward(const LinearPlan& p, const LinearBwdArgs& a, char* ws, const Launcher& L) {
   const T* dy = static_cast<const T*>(a.dy);
-  const T* slope = static_cast<const T*>(a.slope);
+  const auto* slope = static_cast<const Slope<T>*>(a.slope);
   const T* x = static_cast<const T*>(a.x);
   T* dz = reinterpret_cast<T*>(ws + p.off_dz);
   float* part = a.dbias ? reinterpret_cast<float*>(ws + p.off_part) : nullptr;
@@ -295,6 +492,12 @@ hipError_t backward(const LinearPlan& p, const LinearBwdArgs& a, char* ws, const
   if (e != hipSuccess || (!a.dx && !a.dweight)) return e;
   const T* g = slope ? dz : dy;
   const int64_t ld_g = slope ? a.O : a.ld_dy;
+  if constexpr (sizeof(T) == 2) {
+    L.pre(kLinearGrad);
+    const bool done = backward_large(a, g, ld_g, L);
+    L.post(kLinearGrad);
+    if (done) return hipGetLastError();
+  }
   const int64_t n1 = a.dx ? tiles_of(a.I) * tiles_of(a.N) : 0, n1p = (n1 + 7) / 8 * 8;
   const int64_t n2 = a.dweight ? tiles_of(a.I) * tiles_of(a.O) : 0;
   L.pre(kLinearGrad);

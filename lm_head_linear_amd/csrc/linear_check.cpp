@@ -50,7 +50,7 @@ int flce_linear_check_args(const void* x, int64_t ld_x, const void* weight, cons
   const size_t es = esize(dtype), ys = esize(y_dtype);
   const Buf bx = matrix(x, N, I, ld_x, es), bw = matrix(weight, O, I, I, es), bb = vec(bias, O, es),
             br = matrix(residual, N, O, ld_res, es), by = matrix(y, N, O, ld_y, ys),
-            bs = matrix(slope, N, O, O, es);
+            bs = matrix(slope, N, O, O, es);            // half or float: as wide as the rows
   // in place: y may be the residual
   if (overlap(by, br) && !same(by, br)) return FLCE_ERR_ARG;
   if (clash({by, bs}, {bx, bw, bb}) || overlap(bs, br)) return FLCE_ERR_ARG;

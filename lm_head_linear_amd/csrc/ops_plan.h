@@ -122,6 +122,9 @@ struct LinearBwdArgs {
   int dtype;
 };
 
+// Tiles of 256 x 256 from which a bf16 product runs on the head's tiles.
+constexpr int64_t kLinearLargeTiles = 192;
+
 // Rows of dz a workgroup forms (and adds up for db).
 constexpr int64_t kLinearDzRows = 64;
 

@@ -74,7 +74,10 @@ def check(N, I, O, dt, act, bias, residual, ydt=None, seed=0):
     elif act == "relu":                     # which side of zero only a z near it leaves open
         assert bool(((slope.double() == d) | (z.abs() <= ez)).all())
     else:
-        inside(slope, d, half(dt) * d.abs() * 1.02 + ez + 16 * U * z.abs().clamp_min(1), "slope")
+        sdt = torch.float16 if dt == torch.bfloat16 else dt
+        assert slope.dtype == sdt
+        # a half below 2^-14 is a multiple of 2^-24
+        inside(slope, d, 2.0 ** -25 + half(sdt) * d.abs() * 1.02 + ez + 16 * U * z.abs().clamp_min(1), "slope")
     dx, dw, db = m.flce_linear_backward(dy, x, w, slope, bias=bias)
     full = dy.float() if slope is None else dy.float() * slope.float()
     dz, fd = full.to(dt).double(), full.double()
@@ -173,7 +176,7 @@ def test_strides_alignment_in_place(dt, N):
 def test_accumulate_and_parts(dt, N, I, O):
     import lm_head_linear_amd as m
     x, w, _, _, dy = make(N, I, O, dt, 3)
-    slope = torch.rand(N, O, device="cuda").to(dt)
+    slope = torch.rand(N, O, device="cuda").to(torch.float16 if dt == torch.bfloat16 else dt)
     dx, dw, db = m.flce_linear_backward(dy, x, w, slope)
     one = m.flce_linear_backward(dy, x, w, slope, want_dweight=False, bias=False)
     assert torch.equal(one[0], dx) and one[1] is None and one[2] is None
@@ -298,6 +301,6 @@ def test_streams_and_refusals():
         with pytest.raises(ValueError):
             bad()
     with pytest.raises(m.FlceError):
-        m.flce_linear(x, w, residual=r, activation="silu", slope=r)
+        m.flce_linear(x, w, residual=r, activation="silu", slope=r.view(torch.float16))
     with pytest.raises(m.FlceError):
         m.flce_linear(x.float(), w.float(), y_dtype=torch.bfloat16)
