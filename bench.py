@@ -45,7 +45,7 @@ KERNEL_SOURCES = [os.path.join(ROOT, "lm_head_linear_amd", "csrc", f)
                             "kernels_embed.hip", "kernels_logprobs.hip", "wave_ops.h",
                             "join_sparse.h", "check_util.h", "dropout.h", "dropout_check.cpp",
                             "kernels_dropout.hip", "kernels_linear.hip",
-                            "kernels_sample.hip", "gemm_small.h", "activation.h",
+                            "kernels_sample.hip", "gemm_small.h", "activation.h", "few_rows.h",
                             "linear_check.cpp", "sample_check.cpp")]
 
 

@@ -10,8 +10,9 @@
 // is the slope and dz (bf16 rows: the products' operand). db sums dz before its rounding.
 //
 // Products of bf16 rows whose lengths and addresses are multiples of 16 bytes, with enough
-// tiles of 256 x 256 to fill the chip, run on the head's product (gemm_bf16.h); all others
-// on the one of 128 x 128 tiles (gemm_small.h).
+// tiles of 256 x 256 to fill the chip, run on the head's product (gemm_bf16.h); others
+// on the one of 128 x 128 or 64 x 64 tiles (gemm_small.h). Up to 64 rows forward, where
+// reading W is all there is to it, take k_linear_few, or (a wide W: a head) k_linear_wide.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -20,6 +21,7 @@
 
 #include "../../include/flce.h"
 #include "activation.h"
+#include "few_rows.h"
 #include "flce_internal.h"
 #include "gemm_bf16.h"
 #include "gemm_small.h"
@@ -101,7 +103,31 @@ __device__ __forceinline__ void load_slope(const _Float16* row, int64_t c, int64
 template <class T>
 using Slope = std::conditional_t<sizeof(T) == 2, _Float16, float>;
 
-// What follows z in the forward, four columns of a row at a time.
+// Columns [c, c + 4) of row r of a matrix of rows x n: as they are where the tile lies inside
+// it (WHOLE), otherwise element by element from clamped places. No load has a condition:
+// one would be waited for before the next is issued.
+template <bool WHOLE, class T>
+__device__ __forceinline__ void load4_at(const T* p, int64_t ld, int64_t r, int64_t c, int64_t rows,
+                                         int64_t n, float (&f)[4]) {
+  if constexpr (WHOLE) {
+    load4(p + r * ld, c, c + 4, f);
+  } else {
+    const T* row = p + (r < rows ? r : rows - 1) * ld;
+    T x[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = row[c + e < n ? c + e : n - 1];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[e] = to_f32(x[e]);
+  }
+}
+template <bool WHOLE, class T>
+__device__ __forceinline__ void store4_at(T* p, int64_t ld, int64_t r, int64_t c, int64_t rows,
+                                          int64_t n, const float (&f)[4]) {
+  if (WHOLE) store4(p + r * ld, c, c + 4, f);
+  else if (r < rows && c < n) store4(p + r * ld, c, n, f);
+}
+
+// What follows z in the forward.
 template <class T, class OT>
 struct Finish {
   const T* bias;              // may be null
@@ -111,33 +137,67 @@ struct Finish {
   int64_t ld_y;
   Slope<T>* slope;            // may be null; [N][O]
   int64_t N, O;
-  template <int ACT>
-  __device__ __forceinline__ void store(int64_t c, int64_t r, float (&z)[4]) const {
-    if (r >= N || c >= O) return;
-    float t[4], d[4];
+  // Columns c .. c + 3 of row r; bias and residual as load() left them.
+  struct Ends {
+    float b[4], t[4];
+  };
+  __device__ __forceinline__ Ends load(int64_t c, int64_t r) const {
+    Ends s{};
+    if (bias) load4_at<false>(bias, 0, 0, c, 1, O, s.b);
+    if (res) load4_at<false>(res, ld_res, r, c, N, O, s.t);
+    return s;
+  }
+  __device__ __forceinline__ void store(int act, int64_t c, int64_t r, const float (&z)[4],
+                                        const Ends& s) const {
+    float v[4], d[4];
+    with_activation(act, [&](auto k) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const Activated a = activate<decltype(k)::value, sizeof(OT) == 2>(z[e] + s.b[e]);
+        v[e] = a.y + s.t[e];
+        d[e] = a.slope;
+      }
+    });
+    if (slope) store4_at<false>(slope, O, r, c, N, O, d);
+    store4_at<false>(y, ld_y, r, c, N, O, v);
+  }
+  // A lane's part of a tile of the small product.
+  template <int ACT, bool WHOLE, int TS>
+  __device__ __forceinline__ void store(const small::Acc<TS>& acc, int64_t c0, int64_t r0) const {
+    constexpr int B = small::Acc<TS>::B;
+    float b[B][4] = {}, t[B][B][4] = {};
     if (bias) {
-      load4(bias, c, O, t);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) z[e] += t[e];
+      for (int i = 0; i < B; ++i) load4_at<WHOLE>(bias, 0, 0, c0 + 16 * i, 1, O, b[i]);
     }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const Activated a = activate<ACT, sizeof(OT) == 2>(z[e]);
-      z[e] = a.y;
-      d[e] = a.slope;
-    }
-    if (slope) store4(slope + r * O, c, O, d);
     if (res) {
-      load4(res + r * ld_res, c, O, t);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) z[e] += t[e];
+      for (int j = 0; j < B; ++j)
+#pragma unroll
+        for (int i = 0; i < B; ++i)
+          load4_at<WHOLE>(res, ld_res, r0 + 16 * j, c0 + 16 * i, N, O, t[j][i]);
     }
-    store4(y + r * ld_y, c, O, z);
+#pragma unroll
+    for (int j = 0; j < B; ++j)
+#pragma unroll
+      for (int i = 0; i < B; ++i) {
+        const int64_t r = r0 + 16 * j, c = c0 + 16 * i;
+        float v[4], d[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const Activated a = activate<ACT, sizeof(OT) == 2>(acc.v[i][j][e] + b[i][e]);
+          v[e] = a.y + t[j][i][e];
+          d[e] = a.slope;
+        }
+        if (ACT != FLCE_ACT_NONE && slope) store4_at<WHOLE>(slope, O, r, c, N, O, d);
+        store4_at<WHOLE>(y, ld_y, r, c, N, O, v);
+      }
   }
 };
 
 // Tile `b` of na x nb: the XCDs (workgroups go to them in turn) take contiguous runs of
 // tiles, in groups of four rows of tiles, so that one's tiles share operands in its L2.
+template <int TS>
 __device__ __forceinline__ void tile_at(int64_t b, int64_t na, int64_t nb, int64_t& a0,
                                         int64_t& b0) {
   constexpr int kGroup = 4;
@@ -146,26 +206,156 @@ __device__ __forceinline__ void tile_at(int64_t b, int64_t na, int64_t nb, int64
   const int64_t g = t / (kGroup * na), first = g * kGroup;
   const int64_t rows = nb - first < kGroup ? nb - first : kGroup;
   const int64_t in = t - g * kGroup * na;
-  b0 = (first + in % rows) * small::kTile;
-  a0 = (in / rows) * small::kTile;
+  b0 = (first + in % rows) * TS;
+  a0 = (in / rows) * TS;
 }
+template <int TS>
 __host__ __device__ __forceinline__ int64_t tiles_of(int64_t n) {
-  return (n + small::kTile - 1) / small::kTile;
+  return (n + TS - 1) / TS;
 }
 
-template <class T, class OT, int ACT>
+template <class T, class OT, int TS, bool DIRECT>
 __global__ __launch_bounds__(small::kThreads) void k_linear(small::Operand<T> W,
                                                             small::Operand<T> x, int64_t I,
-                                                            Finish<T, OT> fin) {
-  __shared__ __attribute__((aligned(16))) char smem[4 * small::kStageBytes];
+                                                            Finish<T, OT> fin, int act) {
+  __shared__ __attribute__((aligned(1024))) char smem[small::kSmemBytes<TS, DIRECT>];
   int64_t a0, b0;
-  tile_at(blockIdx.x, tiles_of(W.rows), tiles_of(x.rows), a0, b0);
-  small::Acc acc;
-  small::tile<T, 0, 0>(acc, W, x, a0, b0, I, smem);
-  small::for_acc(acc, a0, b0, [&](int64_t c, int64_t r, const small::f32x4& v) {
-    float z[4] = {v[0], v[1], v[2], v[3]};
-    fin.template store<ACT>(c, r, z);
+  tile_at<TS>(blockIdx.x, tiles_of<TS>(W.rows), tiles_of<TS>(x.rows), a0, b0);
+  small::Acc<TS> acc;
+  small::tile<T, 0, 0, TS, DIRECT>(acc, W, x, a0, b0, I, smem);
+  const int64_t c0 = small::lane_col<TS>(a0), r0 = small::lane_row<TS>(b0);
+  const bool whole = a0 + TS <= W.rows && b0 + TS <= x.rows;
+  with_activation(act, [&](auto k) {
+    constexpr int ACT = decltype(k)::value;
+    if (whole) fin.template store<ACT, true>(acc, c0, r0);
+    else fin.template store<ACT, false>(acc, c0, r0);
   });
+}
+
+// ---- few rows -----------------------------------------------------------------------------
+// A workgroup: 16 of W's rows and 16 NT rows of x; its eight waves take 256 bytes of k in
+// turn, so that each loads both operands of its matrix instructions straight into registers
+// and all of a short row is under way at once; their sums are joined in LDS in wave order.
+// Bound by reading W, if it is large. What 64 rows of W a workgroup, each wave over all of k
+// (as a head's), leave of a W of 4096 rows is 64 workgroups for 256 CUs.
+// 16 rows of 4096, W 4096 x 4096: 9.6 us; tiles of 64 x 64 17, of 128 x 128 39.
+constexpr int kFewWaves = 8;
+
+template <class T, class OT, int NT>
+__global__ __launch_bounds__(64 * kFewWaves) void k_linear_few(small::Operand<T> W,
+                                                               small::Operand<T> x, int64_t I,
+                                                               Finish<T, OT> fin, int act) {
+  constexpr int E = kPerChunk<T>, KC = 16 * E;     // k of a chunk: four steps of 4 lanes' 16 bytes
+  constexpr int D = NT == 1 ? 4 : 2;               // chunks under way
+  __shared__ __attribute__((aligned(16))) f32x4 red[kFewWaves][NT][64];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
+  const int r = lane & 15, kg = (lane >> 4) * E;
+  const int64_t v0 = int64_t(blockIdx.x) * 16;
+  const int64_t c = v0 + 4 * (lane >> 4);          // the finishing waves' column, row 16 w + r
+  typename Finish<T, OT>::Ends ends{};
+  if (w < NT) ends = fin.load(c, 16 * w + r);
+  const T* wrow = W.p + (v0 + r < W.rows ? v0 + r : W.rows - 1) * I;
+  const T* xrow[NT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) xrow[j] = x.p + (16 * j + r < x.rows ? 16 * j + r : x.rows - 1) * x.ld;
+  f32x4 acc[NT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  auto multiply = [&](const row_u32x4 (&a)[4], const row_u32x4 (&b)[NT][4]) {
+#if defined(__HIP_DEVICE_COMPILE__)
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        if constexpr (sizeof(T) == 2) {
+          acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a[s]),
+                                                           __builtin_bit_cast(bf16x8, b[j][s]),
+                                                           acc[j], 0, 0, 0);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            acc[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(
+                __uint_as_float(a[s][e]), __uint_as_float(b[j][s][e]), acc[j], 0, 0, 0);
+        }
+      }
+#endif
+  };
+  const int64_t full = I / KC, end = full * KC;
+  if (end < I && full % kFewWaves == w) {          // the rest of the rows, element by element
+    T ea[4][E], eb[NT][4][E];
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const int64_t k = end + s * 4 * E + kg + e, at = k < I ? k : I - 1;
+        ea[s][e] = wrow[at];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) eb[j][s][e] = xrow[j][at];
+      }
+    row_u32x4 a[4], b[NT][4];
+    auto pack = [&](const T (&v)[E], int s) {
+      float f[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) f[e] = end + s * 4 * E + kg + e < I ? to_f32(v[e]) : 0.f;
+      return pack_chunk<T>(f);
+    };
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      a[s] = pack(ea[s], s);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) b[j][s] = pack(eb[j][s], s);
+    }
+    multiply(a, b);
+  }
+  if (full > w) {
+    row_u32x4 a[D][4], b[D][NT][4];
+    // the wave's chunk i; past the last one the row's last (loaded, not multiplied)
+    auto load = [&](int u, int64_t i) {
+      const int64_t at = w + i * kFewWaves < full ? w + i * kFewWaves : full - 1;
+      const int64_t k = at * KC + kg;
+#pragma unroll
+      for (int s = 0; s < 4; ++s) a[u][s] = load_raw(wrow + k + s * 4 * E);
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int s = 0; s < 4; ++s) b[u][j][s] = load_raw(xrow[j] + k + s * 4 * E);
+    };
+#pragma unroll
+    for (int u = 0; u < D - 1; ++u) load(u, u);
+    for (int64_t i = 0; w + i * kFewWaves < full; i += D) {
+#pragma unroll
+      for (int u = 0; u < D; ++u) {
+        load((u + D - 1) % D, i + u + D - 1);
+        if (w + (i + u) * kFewWaves < full) multiply(a[u], b[u]);
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < NT; ++j) red[w][j][lane] = acc[j];
+  __syncthreads();
+  if (w >= NT) return;
+  f32x4 v = red[0][w][lane];
+#pragma unroll
+  for (int i = 1; i < kFewWaves; ++i) v += red[i][w][lane];
+  const float z[4] = {v[0], v[1], v[2], v[3]};
+  fin.store(act, c, 16 * w + r, z, ends);
+}
+
+// A wide W, as a head: 64 RB of its rows a workgroup (few_rows.h).
+template <int NT, int ALIGN, int RB, class OT>
+__global__ __launch_bounds__(256) void k_linear_wide(const uint16_t* __restrict__ W,
+                                                     const uint16_t* __restrict__ x, int64_t ld_x,
+                                                     int64_t I, Finish<Bf16Bits, OT> fin, int act) {
+  __shared__ __attribute__((aligned(16))) FewSmem<NT, RB> sm;
+  const int64_t v0 = int64_t(blockIdx.x) * (64 * RB);
+  few_logits<NT, ALIGN, RB>(x, ld_x, W, fin.N, I, fin.O, v0, sm);
+  for (int i = threadIdx.x; i < 16 * NT * 16 * RB; i += 256) {
+    const int64_t r = i / (16 * RB), c = v0 + 4 * (i % (16 * RB));
+    if (r >= fin.N) break;
+    const float* s = &sm.z[r][4 * (i % (16 * RB))];
+    const float z[4] = {s[0], s[1], s[2], s[3]};
+    fin.store(act, c, r, z, fin.load(c, r));
+  }
 }
 
 // The same behind the head's tiles: rows are tokens, columns W's rows. A lane has the same
@@ -265,62 +455,117 @@ struct GradOut {
   T* p;
   int64_t ld, rows, cols;
   int accumulate;
-  __device__ __forceinline__ void store(int64_t c, int64_t r, const small::f32x4& v) const {
-    if (r >= rows || c >= cols) return;
-    float f[4] = {v[0], v[1], v[2], v[3]};
+  template <bool WHOLE, int TS>
+  __device__ __forceinline__ void store(const small::Acc<TS>& acc, int64_t c0, int64_t r0) const {
+    constexpr int B = small::Acc<TS>::B;
+    float t[B][B][4] = {};
     if (accumulate) {
-      float o[4];
-      load4(p + r * ld, c, cols, o);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) f[e] += o[e];
+      for (int j = 0; j < B; ++j)
+#pragma unroll
+        for (int i = 0; i < B; ++i)
+          load4_at<WHOLE>(p, ld, r0 + 16 * j, c0 + 16 * i, rows, cols, t[j][i]);
     }
-    store4(p + r * ld, c, cols, f);
+#pragma unroll
+    for (int j = 0; j < B; ++j)
+#pragma unroll
+      for (int i = 0; i < B; ++i) {
+        float f[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[e] = acc.v[i][j][e] + t[j][i][e];
+        store4_at<WHOLE>(p, ld, r0 + 16 * j, c0 + 16 * i, rows, cols, f);
+      }
+  }
+  template <int TS>
+  __device__ __forceinline__ void store_tile(const small::Acc<TS>& acc, int64_t a0,
+                                             int64_t b0) const {
+    const int64_t c0 = small::lane_col<TS>(a0), r0 = small::lane_row<TS>(b0);
+    if (a0 + TS <= cols && b0 + TS <= rows) store<true>(acc, c0, r0);
+    else store<false>(acc, c0, r0);
   }
 };
 
-// dx's tiles (n1 of them, padded to a multiple of 8) and then dW's, in one grid.
+// db from the workgroups' sums, in a fixed order: 16 columns a workgroup, 16 chains of
+// every 16th sum, joined pairwise.
 template <class T>
+struct BiasGrad {
+  const float* part;          // [np][O]; null: none
+  int64_t np, O;
+  T* db;
+  int accumulate;
+  __host__ __device__ int64_t groups() const { return part ? (O + 15) / 16 : 0; }
+  __device__ __forceinline__ void run(int64_t group, float (*red)[17]) const {
+    const int col = threadIdx.x & 15, grp = threadIdx.x >> 4;
+    const int64_t c = group * 16 + col;
+    float a = 0.f;
+    if (c < O) {
+#pragma unroll 8
+      for (int64_t i = grp; i < np; i += 16) a += part[i * O + c];
+    }
+    red[grp][col] = a;
+    __syncthreads();
+    for (int k = 8; k > 0; k >>= 1) {
+      if (grp < k) red[grp][col] += red[grp + k][col];
+      __syncthreads();
+    }
+    if (grp == 0 && c < O) {
+      const float v = red[0][col];
+      db[c] = from_f32<T>(accumulate ? to_f32(db[c]) + v : v);
+    }
+  }
+};
+
+template <class T>
+__global__ __launch_bounds__(256) void k_linear_db(BiasGrad<T> b) {
+  __shared__ float red[16][17];
+  b.run(blockIdx.x, red);
+}
+
+// dx's tiles (n1 of them, padded to a multiple of 8), then dW's (n2), then db, in one grid.
+template <class T, int TS, bool DIRECT>
 __global__ __launch_bounds__(small::kThreads) void k_linear_grads(
-    int64_t n1, int64_t n1p, small::Operand<T> Wt, small::Operand<T> dz, int64_t O,
-    GradOut<T> dx, small::Operand<T> xt, small::Operand<T> dzt, int64_t N, GradOut<T> dw) {
-  __shared__ __attribute__((aligned(16))) char smem[4 * small::kStageBytes];
+    int64_t n1, int64_t n1p, int64_t n2, small::Operand<T> Wt, small::Operand<T> dz, int64_t O,
+    GradOut<T> dx, small::Operand<T> xt, small::Operand<T> dzt, int64_t N, GradOut<T> dw,
+    BiasGrad<T> db) {
+  __shared__ __attribute__((aligned(1024))) char smem[small::kSmemBytes<TS, DIRECT>];
   const int64_t b = blockIdx.x;
   int64_t a0, b0;
-  small::Acc acc;
+  small::Acc<TS> acc;
   if (b < n1p) {
     if (b >= n1) return;
-    tile_at(b, tiles_of(dx.cols), tiles_of(dx.rows), a0, b0);
-    small::tile<T, 1, 0>(acc, Wt, dz, a0, b0, O, smem);
-    small::for_acc(acc, a0, b0,
-                   [&](int64_t c, int64_t r, const small::f32x4& v) { dx.store(c, r, v); });
+    tile_at<TS>(b, tiles_of<TS>(dx.cols), tiles_of<TS>(dx.rows), a0, b0);
+    small::tile<T, 1, 0, TS, DIRECT>(acc, Wt, dz, a0, b0, O, smem);
+    dx.store_tile(acc, a0, b0);
+  } else if (b >= n1p + n2) {
+    db.run(b - n1p - n2, reinterpret_cast<float (*)[17]>(smem));
   } else {
-    tile_at(b - n1p, tiles_of(dw.cols), tiles_of(dw.rows), a0, b0);
-    small::tile<T, 1, 1>(acc, xt, dzt, a0, b0, N, smem);
-    small::for_acc(acc, a0, b0,
-                   [&](int64_t c, int64_t r, const small::f32x4& v) { dw.store(c, r, v); });
+    tile_at<TS>(b - n1p, tiles_of<TS>(dw.cols), tiles_of<TS>(dw.rows), a0, b0);
+    small::tile<T, 1, 1, TS, DIRECT>(acc, xt, dzt, a0, b0, N, smem);
+    dw.store_tile(acc, a0, b0);
   }
 }
 
 // dz = dy slope (rounded; SLOPE false: dz is dy, not written), and the workgroup's rows'
-// sums of dz in its row of part[][O] (null: not wanted). A workgroup takes kLinearDzRows
-// rows of 32 chunks of columns, 8 rows at a time; cols workgroups stand side by side.
+// sums of dz in its row of part[][O] (null: not wanted). A workgroup takes `rows` rows
+// of 32 chunks of columns, 8 rows at a time; cols workgroups stand side by side.
 template <class T, bool SLOPE>
 __global__ __launch_bounds__(256) void k_linear_dz(const T* __restrict__ dy, int64_t ld_dy,
                                                    const Slope<T>* __restrict__ slope,
                                                    int64_t N, int64_t O, T* __restrict__ dz,
-                                                   float* __restrict__ part, uint32_t cols) {
+                                                   float* __restrict__ part, uint32_t cols,
+                                                   int rows) {
   constexpr int E = kPerChunk<T>;
   __shared__ float red[8][32 * E + 1];
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
   const uint32_t by = blockIdx.x / cols, bx = blockIdx.x - by * cols;
   const int64_t c = (int64_t(bx) * 32 + tx) * E;
-  const int64_t r0 = int64_t(by) * kLinearDzRows;
+  const int64_t r0 = int64_t(by) * rows;
   float sum[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) sum[e] = 0.f;
   if (c < O) {
 #pragma unroll 4
-    for (int i = ty; i < kLinearDzRows; i += 8) {
+    for (int i = ty; i < rows; i += 8) {
       const int64_t r = r0 + i;
       if (r >= N) break;
       float g[E];
@@ -350,37 +595,25 @@ __global__ __launch_bounds__(256) void k_linear_dz(const T* __restrict__ dy, int
   }
 }
 
-// db from the workgroups' sums, in a fixed order: 16 columns a workgroup, 16 chains of
-// every 16th sum, joined pairwise.
+// Whether every row starts at a multiple of 16 bytes.
 template <class T>
-__global__ __launch_bounds__(256) void k_linear_db(const float* __restrict__ part, int64_t np,
-                                                   int64_t O, T* __restrict__ db, int accumulate) {
-  __shared__ float red[16][17];
-  const int col = threadIdx.x & 15, grp = threadIdx.x >> 4;
-  const int64_t c = int64_t(blockIdx.x) * 16 + col;
-  float a = 0.f;
-  if (c < O) {
-#pragma unroll 8
-    for (int64_t i = grp; i < np; i += 16) a += part[i * O + c];
-  }
-  red[grp][col] = a;
-  __syncthreads();
-  for (int k = 8; k > 0; k >>= 1) {
-    if (grp < k) red[grp][col] += red[grp + k][col];
-    __syncthreads();
-  }
-  if (grp == 0 && c < O) {
-    const float v = red[0][col];
-    db[c] = from_f32<T>(accumulate ? to_f32(db[c]) + v : v);
-  }
-}
-
 bool aligned16(std::initializer_list<const void*> ptrs, std::initializer_list<int64_t> lds) {
   for (const void* p : ptrs)
     if (reinterpret_cast<uintptr_t>(p) % 16) return false;
   for (int64_t l : lds)
-    if (l % 8) return false;
+    if (l % kPerChunk<T>) return false;
   return true;
+}
+
+// run(the tile's edge, whether its loads are direct) for a product of n tiles of 128 x 128.
+template <class F>
+void with_tile(int64_t n, bool direct, F&& run) {
+  using Whole = std::integral_constant<int, 128>;
+  using Half = std::integral_constant<int, 64>;
+  if (n >= kLinearWholeTiles)
+    direct ? run(Whole{}, std::true_type{}) : run(Whole{}, std::false_type{});
+  else
+    direct ? run(Half{}, std::true_type{}) : run(Half{}, std::false_type{});
 }
 
 // Whether a product of a x b outputs runs on the head's tiles: enough of them for most of
@@ -402,7 +635,7 @@ template <class OT>
 bool forward_large(const LinearArgs& a, const Finish<Bf16Bits, OT>& fin, const Launcher& L) {
   const Large x{gemm::kFormN, a.x, {a.ld_x, a.N, a.I}}, W{gemm::kFormN, a.weight, {a.I, a.O, a.I}};
   if (!on_large_tiles(a.N, a.O) || !x.fits() || !W.fits()) return false;
-  if (!aligned16({a.x, a.weight, a.bias, a.residual, a.y, a.slope},
+  if (!aligned16<Bf16Bits>({a.x, a.weight, a.bias, a.residual, a.y, a.slope},
                  {a.I, a.O, a.ld_x, a.ld_y, a.residual ? a.ld_res : 0}))
     return false;
   with_activation(a.activation, [&](auto act) {
@@ -415,6 +648,41 @@ bool forward_large(const LinearArgs& a, const Finish<Bf16Bits, OT>& fin, const L
 }
 
 template <class T, class OT>
+bool forward_few(const LinearArgs& a, const Finish<T, OT>& fin, const Launcher& L) {
+  const T* W = static_cast<const T*>(a.weight);
+  const T* x = static_cast<const T*>(a.x);
+  if constexpr (sizeof(T) == 2) {
+    // few_rows.h reads odd rows as the words they lie in: dense rows, from aligned addresses
+    const bool whole = aligned16<T>({W, x}, {a.I, a.ld_x});
+    const bool dense = aligned16<T>({W, x}, {}) && a.ld_x == a.I;
+    if (a.N <= kFewTokens && a.O >= kLinearWide && (whole || dense)) {
+      with_few(a.N, [&](auto nt, auto rb) {
+        constexpr int NT = decltype(nt)::value, RB = decltype(rb)::value;
+        auto go = [&](auto align) {
+          hipLaunchKernelGGL((k_linear_wide<NT, decltype(align)::value, RB, OT>),
+                             dim3(unsigned((a.O + 64 * RB - 1) / (64 * RB))), dim3(256), 0, L.stream,
+                             W, x, a.ld_x, a.I, fin, a.activation);
+        };
+        if (whole) go(std::integral_constant<int, 16>{});
+        else if (a.I % 2 == 0) go(std::integral_constant<int, 4>{});
+        else go(std::integral_constant<int, 2>{});
+      });
+      return true;
+    }
+  }
+  if (a.N > kLinearFew) return false;
+  auto go = [&](auto nt) {
+    hipLaunchKernelGGL((k_linear_few<T, OT, decltype(nt)::value>), dim3(unsigned((a.O + 15) / 16)),
+                       dim3(64 * kFewWaves), 0, L.stream, small::Operand<T>{W, a.I, a.O},
+                       small::Operand<T>{x, a.ld_x, a.N}, a.I, fin, a.activation);
+  };
+  if (a.N <= 16) go(std::integral_constant<int, 1>{});
+  else if (a.N <= 32) go(std::integral_constant<int, 2>{});
+  else go(std::integral_constant<int, 4>{});
+  return true;
+}
+
+template <class T, class OT>
 hipError_t forward(const LinearArgs& a, const Launcher& L) {
   const T* W = static_cast<const T*>(a.weight);
   const T* x = static_cast<const T*>(a.x);
@@ -422,17 +690,23 @@ hipError_t forward(const LinearArgs& a, const Launcher& L) {
                           a.ld_res, static_cast<OT*>(a.y), a.ld_y, static_cast<Slope<T>*>(a.slope),
                           a.N, a.O};
   L.pre(kLinear);
+  if (forward_few<T, OT>(a, fin, L)) {
+    L.post(kLinear);
+    return hipGetLastError();
+  }
   if constexpr (sizeof(T) == 2) {
     if (forward_large<OT>(a, fin, L)) {
       L.post(kLinear);
       return hipGetLastError();
     }
   }
-  with_activation(a.activation, [&](auto act) {
-    const dim3 grid(unsigned(tiles_of(a.O) * tiles_of(a.N)));
-    hipLaunchKernelGGL((k_linear<T, OT, decltype(act)::value>), grid, dim3(small::kThreads), 0,
-                       L.stream, small::Operand<T>{W, a.I, a.O}, small::Operand<T>{x, a.ld_x, a.N},
-                       a.I, fin);
+  const bool direct = aligned16<T>({a.x, a.weight}, {a.I, a.ld_x});
+  with_tile(tiles_of<128>(a.O) * tiles_of<128>(a.N), direct, [&](auto ts, auto di) {
+    constexpr int TS = decltype(ts)::value;
+    const dim3 grid(unsigned(tiles_of<TS>(a.O) * tiles_of<TS>(a.N)));
+    hipLaunchKernelGGL((k_linear<T, OT, TS, decltype(di)::value>), grid, dim3(small::kThreads), 0,
+                       L.stream, small::Operand<T>{W, a.I, a.O},
+                       small::Operand<T>{x, a.ld_x, a.N}, a.I, fin, a.activation);
   });
   L.post(kLinear);
   return hipGetLastError();
@@ -444,7 +718,7 @@ bool backward_large(const LinearBwdArgs& a, const Bf16Bits* g, int64_t ld_g, con
   const Large g1{gemm::kFormN, g, {ld_g, a.N, a.O}}, W{gemm::kFormT, a.weight, {a.I, a.I, a.O}};
   const Large g2{gemm::kFormT, g, {ld_g, a.O, a.N}}, x{gemm::kFormT, a.x, {a.ld_x, a.I, a.N}};
   if (!g1.fits() || !W.fits() || !g2.fits() || !x.fits()) return false;
-  if (!aligned16({g, a.weight, a.x, a.dx, a.dweight}, {a.I, a.O, ld_g, a.ld_x, a.ld_dx}))
+  if (!aligned16<Bf16Bits>({g, a.weight, a.x, a.dx, a.dweight}, {a.I, a.O, ld_g, a.ld_x, a.ld_dx}))
     return false;
   const int64_t n1 = gemm::num_tiles(a.N, a.I), n1p = (n1 + 7) / 8 * 8;
   const int64_t n2 = gemm::num_tiles(a.O, a.I);
@@ -456,7 +730,9 @@ bool backward_large(const LinearBwdArgs& a, const Bf16Bits* g, int64_t ld_g, con
                        g1.op(), W.op(), a.N, a.I, a.O, e1, g2.op(), x.op(), a.O, a.I, a.N,
                        Epi2{static_cast<Bf16Bits*>(a.dweight), a.I, a.O, a.I}, int64_t(0), nullptr);
   };
+  L.pre(kLinearGrad);
   a.accumulate ? go(std::true_type{}) : go(std::false_type{});
+  L.post(kLinearGrad);
   return true;
 }
 
@@ -475,38 +751,49 @@ hipError_t backward(const LinearPlan& p, const LinearBwdArgs& a, char* ws, const
     L.pre(kLinearGrad);
     if (slope)
       hipLaunchKernelGGL((k_linear_dz<T, true>), grid, dim3(256), 0, L.stream, dy, a.ld_dy, slope,
-                         a.N, a.O, dz, part, cols);
+                         a.N, a.O, dz, part, cols, int(p.dz_rows));
     else
       hipLaunchKernelGGL((k_linear_dz<T, false>), grid, dim3(256), 0, L.stream, dy, a.ld_dy, slope,
-                         a.N, a.O, dz, part, cols);
+                         a.N, a.O, dz, part, cols, int(p.dz_rows));
     L.post(kLinearGrad);
     e = hipGetLastError();
   }
-  if (e == hipSuccess && part) {
+  if (e != hipSuccess) return e;
+  BiasGrad<T> db{part, p.dz_parts, a.O, static_cast<T*>(a.dbias), a.accumulate};
+  auto bias_alone = [&] {
+    if (!part) return hipSuccess;
     L.pre(kLinearGrad);
-    hipLaunchKernelGGL(k_linear_db<T>, dim3(unsigned((a.O + 15) / 16)), dim3(256), 0, L.stream, part,
-                       p.dz_parts, a.O, static_cast<T*>(a.dbias), a.accumulate);
+    hipLaunchKernelGGL(k_linear_db<T>, dim3(unsigned(db.groups())), dim3(256), 0, L.stream, db);
     L.post(kLinearGrad);
-    e = hipGetLastError();
-  }
-  if (e != hipSuccess || (!a.dx && !a.dweight)) return e;
+    return hipGetLastError();
+  };
+  if (!a.dx && !a.dweight) return bias_alone();
   const T* g = slope ? dz : dy;
   const int64_t ld_g = slope ? a.O : a.ld_dy;
   if constexpr (sizeof(T) == 2) {
-    L.pre(kLinearGrad);
-    const bool done = backward_large(a, g, ld_g, L);
-    L.post(kLinearGrad);
-    if (done) return hipGetLastError();
+    if (backward_large(a, g, ld_g, L)) {
+      e = hipGetLastError();
+      return e == hipSuccess ? bias_alone() : e;
+    }
   }
-  const int64_t n1 = a.dx ? tiles_of(a.I) * tiles_of(a.N) : 0, n1p = (n1 + 7) / 8 * 8;
-  const int64_t n2 = a.dweight ? tiles_of(a.I) * tiles_of(a.O) : 0;
   L.pre(kLinearGrad);
-  hipLaunchKernelGGL(k_linear_grads<T>, dim3(unsigned(n1p + n2)), dim3(small::kThreads), 0, L.stream,
-                     n1, n1p, small::Operand<T>{static_cast<const T*>(a.weight), a.I, a.I},
-                     small::Operand<T>{g, ld_g, a.N}, a.O,
-                     GradOut<T>{static_cast<T*>(a.dx), a.ld_dx, a.N, a.I, 0},
-                     small::Operand<T>{x, a.ld_x, a.I}, small::Operand<T>{g, ld_g, a.O}, a.N,
-                     GradOut<T>{static_cast<T*>(a.dweight), a.I, a.O, a.I, a.accumulate});
+  const int64_t n = tiles_of<128>(a.I) * ((a.dx ? tiles_of<128>(a.N) : 0) +
+                                          (a.dweight ? tiles_of<128>(a.O) : 0));
+  bool direct = aligned16<T>({g}, {ld_g, a.I});
+  if (a.dx) direct = direct && aligned16<T>({a.weight}, {});
+  if (a.dweight) direct = direct && aligned16<T>({x}, {a.ld_x, a.O});
+  with_tile(n, direct, [&](auto ts, auto di) {
+    constexpr int TS = decltype(ts)::value;
+    const int64_t n1 = a.dx ? tiles_of<TS>(a.I) * tiles_of<TS>(a.N) : 0, n1p = (n1 + 7) / 8 * 8;
+    const int64_t n2 = a.dweight ? tiles_of<TS>(a.I) * tiles_of<TS>(a.O) : 0;
+    hipLaunchKernelGGL((k_linear_grads<T, TS, decltype(di)::value>), dim3(unsigned(n1p + n2 + db.groups())),
+                       dim3(small::kThreads), 0, L.stream, n1, n1p, n2,
+                       small::Operand<T>{static_cast<const T*>(a.weight), a.I, a.I},
+                       small::Operand<T>{g, ld_g, a.N}, a.O,
+                       GradOut<T>{static_cast<T*>(a.dx), a.ld_dx, a.N, a.I, 0},
+                       small::Operand<T>{x, a.ld_x, a.I}, small::Operand<T>{g, ld_g, a.O}, a.N,
+                       GradOut<T>{static_cast<T*>(a.dweight), a.I, a.O, a.I, a.accumulate}, db);
+  });
   L.post(kLinearGrad);
   return hipGetLastError();
 }

@@ -14,7 +14,10 @@ bool sizes_ok(int64_t N, int64_t I, int64_t O) {
 bool make_linear_plan(int64_t N, int64_t I, int64_t O, int dtype, LinearPlan* out) {
   if (!sizes_ok(N, I, O) || !is_dtype(dtype)) return false;
   LinearPlan p;
-  p.dz_parts = ceil_div(N, kLinearDzRows);
+  // 64 rows a workgroup where that leaves four of them for each CU, otherwise fewer
+  const int64_t cols = ceil_div(O * int64_t(esize(dtype)), 512);
+  for (p.dz_rows = 64; p.dz_rows > 8 && cols * ceil_div(N, p.dz_rows) < 1024;) p.dz_rows /= 2;
+  p.dz_parts = ceil_div(N, p.dz_rows);
   size_t off = 0;
   p.off_dz = off; off = align256(off + size_t(N) * O * esize(dtype));
   p.off_part = off; off = align256(off + size_t(p.dz_parts) * O * 4);
@@ -55,7 +58,7 @@ int flce_linear_check_args(const void* x, int64_t ld_x, const void* weight, cons
   if (overlap(by, br) && !same(by, br)) return FLCE_ERR_ARG;
   if (clash({by, bs}, {bx, bw, bb}) || overlap(bs, br)) return FLCE_ERR_ARG;
   if (dtype == FLCE_F32 && y_dtype != FLCE_F32) return FLCE_ERR_UNSUPPORTED;
-  if (tiles(O, N) > max_groups(256)) return FLCE_ERR_UNSUPPORTED;
+  if (tiles(O, N) > max_groups(256) || ceil_div(O, 16) > max_groups(512)) return FLCE_ERR_UNSUPPORTED;
   for (const Buf& b : {bx, bw, bb, br, by, bs})
     if (misaligned(b)) return FLCE_ERR_UNSUPPORTED;
   return FLCE_OK;
@@ -83,7 +86,7 @@ int flce_linear_backward_check_args(const void* dy, int64_t ld_dy, const void* x
             bdx = matrix(dx, N, I, ld_dx, es), bdw = matrix(dweight, O, I, I, es),
             bdb = vec(dbias, O, es), wk = vec(workspace, int64_t(workspace_bytes), 1);
   if (clash({bdx, bdw, bdb, wk}, {bg, bx, bw, bs})) return FLCE_ERR_ARG;
-  if (tiles(I, N) + 8 + tiles(I, O) > max_groups(256) ||
+  if (tiles(I, N) + 8 + tiles(I, O) + ceil_div(O, 16) > max_groups(256) ||
       ceil_div(O, 128) * p.dz_parts > max_groups(256))
     return FLCE_ERR_UNSUPPORTED;
   for (const Buf& b : {bg, bx, bw, bs, bdx, bdw, bdb})

@@ -125,11 +125,16 @@ struct LinearBwdArgs {
 // Tiles of 256 x 256 from which a bf16 product runs on the head's tiles.
 constexpr int64_t kLinearLargeTiles = 192;
 
-// Rows of dz a workgroup forms (and adds up for db).
-constexpr int64_t kLinearDzRows = 64;
+// Rows up to which a forward takes the kernels that read W once, and W's rows from which
+// those are the head's (two workgroups of 64 rows for each CU).
+constexpr int64_t kLinearFew = 64, kLinearWide = 32768;
+
+// Tiles of 128 x 128 from which a product takes those (others: of 64 x 64).
+constexpr int64_t kLinearWholeTiles = 384;
 
 struct LinearPlan {
-  int64_t dz_parts = 0;
+  int64_t dz_rows = 8;        // rows of dz a workgroup forms (and adds up for db)
+  int64_t dz_parts = 0;       // workgroups along the rows
   size_t off_dz = 0, off_part = 0, total = 0;
 };
 
