@@ -137,14 +137,20 @@ struct Finish {
   int64_t ld_y;
   Slope<T>* slope;            // may be null; [N][O]
   int64_t N, O;
-  // Columns c .. c + 3 of row r; bias and residual as load() left them.
+  // Columns c .. c + 3 of row r; bias and residual as load() left them, in memory's type (a
+  // conversion would wait for them there).
   struct Ends {
-    float b[4], t[4];
+    T b[4], t[4];
   };
   __device__ __forceinline__ Ends load(int64_t c, int64_t r) const {
     Ends s{};
-    if (bias) load4_at<false>(bias, 0, 0, c, 1, O, s.b);
-    if (res) load4_at<false>(res, ld_res, r, c, N, O, s.t);
+    const int64_t rr = r < N ? r : N - 1;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int64_t at = c + e < O ? c + e : O - 1;
+      if (bias) s.b[e] = bias[at];
+      if (res) s.t[e] = res[rr * ld_res + at];
+    }
     return s;
   }
   __device__ __forceinline__ void store(int act, int64_t c, int64_t r, const float (&z)[4],
@@ -153,8 +159,8 @@ struct Finish {
     with_activation(act, [&](auto k) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const Activated a = activate<decltype(k)::value, sizeof(OT) == 2>(z[e] + s.b[e]);
-        v[e] = a.y + s.t[e];
+        const Activated a = activate<decltype(k)::value, sizeof(OT) == 2>(z[e] + to_f32(s.b[e]));
+        v[e] = a.y + to_f32(s.t[e]);
         d[e] = a.slope;
       }
     });
@@ -238,7 +244,7 @@ __global__ __launch_bounds__(small::kThreads) void k_linear(small::Operand<T> W,
 // and all of a short row is under way at once; their sums are joined in LDS in wave order.
 // Bound by reading W, if it is large. What 64 rows of W a workgroup, each wave over all of k
 // (as a head's), leave of a W of 4096 rows is 64 workgroups for 256 CUs.
-// 16 rows of 4096, W 4096 x 4096: 9.6 us; tiles of 64 x 64 17, of 128 x 128 39.
+// 16 rows of 4096, W 4096 x 4096: 10.7 us; tiles of 64 x 64 17, of 128 x 128 39.
 constexpr int kFewWaves = 8;
 
 template <class T, class OT, int NT>
@@ -246,7 +252,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_linear_few(small::Operand<T>
                                                                small::Operand<T> x, int64_t I,
                                                                Finish<T, OT> fin, int act) {
   constexpr int E = kPerChunk<T>, KC = 16 * E;     // k of a chunk: four steps of 4 lanes' 16 bytes
-  constexpr int D = NT == 1 ? 4 : 2;               // chunks under way
+  constexpr int D = NT == 1 ? 4 : 2;               // chunks loaded at once
   __shared__ __attribute__((aligned(16))) f32x4 red[kFewWaves][NT][64];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
   const int r = lane & 15, kg = (lane >> 4) * E;
@@ -307,29 +313,28 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_linear_few(small::Operand<T>
     }
     multiply(a, b);
   }
-  if (full > w) {
-    row_u32x4 a[D][4], b[D][NT][4];
-    // the wave's chunk i; past the last one the row's last (loaded, not multiplied)
-    auto load = [&](int u, int64_t i) {
-      const int64_t at = w + i * kFewWaves < full ? w + i * kFewWaves : full - 1;
-      const int64_t k = at * KC + kg;
+  // G chunks of the wave from its i-th on
+  auto group = [&](auto count, int64_t i) {
+    constexpr int G = decltype(count)::value;
+    row_u32x4 a[G][4], b[G][NT][4];
+#pragma unroll
+    for (int u = 0; u < G; ++u) {
+      const int64_t k = (w + (i + u) * kFewWaves) * KC + kg;
 #pragma unroll
       for (int s = 0; s < 4; ++s) a[u][s] = load_raw(wrow + k + s * 4 * E);
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int s = 0; s < 4; ++s) b[u][j][s] = load_raw(xrow[j] + k + s * 4 * E);
-    };
-#pragma unroll
-    for (int u = 0; u < D - 1; ++u) load(u, u);
-    for (int64_t i = 0; w + i * kFewWaves < full; i += D) {
-#pragma unroll
-      for (int u = 0; u < D; ++u) {
-        load((u + D - 1) % D, i + u + D - 1);
-        if (w + (i + u) * kFewWaves < full) multiply(a[u], b[u]);
-      }
     }
-  }
+#pragma unroll
+    for (int u = 0; u < G; ++u) multiply(a[u], b[u]);
+  };
+  int64_t i = 0, n = full > w ? (full - w + kFewWaves - 1) / kFewWaves : 0;
+  for (; n - i >= D; i += D) group(std::integral_constant<int, D>{}, i);
+  if (D > 3 && n - i == 3) group(std::integral_constant<int, 3>{}, i);
+  else if (D > 2 && n - i == 2) group(std::integral_constant<int, 2>{}, i);
+  else if (n - i == 1) group(std::integral_constant<int, 1>{}, i);
 #pragma unroll
   for (int j = 0; j < NT; ++j) red[w][j][lane] = acc[j];
   __syncthreads();

@@ -15,6 +15,19 @@
 // on their order, so the LDS atomics and the split over threads leave the same bits on
 // every run, and which token a uniform number falls on is decided to 2^-S of the largest
 // weight, not to a float's 2^-24 of the sum.
+//
+// A workgroup takes a row. Its waves take contiguous sixteenths of it (segments), so that
+// sums by wave are sums by place. The first pass finds the largest logit; what follows
+// depends on what can be ruled out before the selection:
+// - top-k: the k-th largest of the threads' own maxima is a bound that few logits but the
+//   first k pass. Those are collected in LDS, in index order, and everything else is done
+//   on the list. min-p alone bounds the list in the same way.
+// - top-p without top-k: one pass forms all weights and adds them up by bins of an eighth
+//   of a power of two, for each wave; the bin in which the mass passes p is then collected,
+//   and the selection runs on that.
+// - no filter: one pass sums the weights of each segment.
+// The token is then found in the segment that holds it. A list that does not fit (thousands
+// of equal logits) leaves the row to the selection over the whole row.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -29,7 +42,10 @@ namespace flce {
 namespace {
 
 constexpr int kThreads = 1024, kWaves = kThreads / 64;
-constexpr int kBins = 2048;
+constexpr int kBins = 2048;                        // of a radix selection's digit
+constexpr int kMassBins = 384;                     // of weights: eighths of 2^-48 .. 1
+constexpr int kWaveList = 256;                     // candidates a wave collects
+constexpr int kSmallList = 256;                    // of a list ranked by counting
 constexpr double kLog2eD = 1.4426950408889634074;
 
 __device__ __forceinline__ uint32_t order_key(float z) {
@@ -62,18 +78,26 @@ __device__ __forceinline__ double exp2_neg(double t) {
 
 // A row's weights.
 struct Weights {
-  double cap, inv_cap, xmax, scale;                // scale: log2(e) / T
+  double cap, two_inv_cap, xmax, scale;            // scale: log2(e) / T
   float zmax;
   int S;
-  double min_p;
+  double min_p, log_min_p;                         // log_min_p: for a first look
+  // cap tanh(z / cap) = sign cap (1 - e) / (1 + e), e = exp(-2 |z| / cap): off by a few 2^-53
+  // of cap, which is all that a difference to xmax needs.
   __device__ __forceinline__ double warp(float z) const {
-    return cap > 0.0 ? cap * tanh(double(z) * inv_cap) : double(z);
+    if (!(cap > 0.0)) return double(z);
+    const double t = fmax(fabs(double(z)) * two_inv_cap * -kLog2eD, -1000.0), e = exp2_neg(t);
+    return copysign(cap * ((1.0 - e) / (1.0 + e)), double(z));
   }
-  // w of a logit, at most 1; zero below 2^-(S + 1), for -inf, and next to a logit of +inf.
-  __device__ __forceinline__ double weight(float z) const {
-    if (z == zmax) return 1.0;
-    if (z == -INFINITY) return 0.0;                // also where a softcap makes it finite
+  // log2 of w of a logit, or below -(S + 1) where w is zero: there, for -inf (also where a
+  // softcap makes it finite), and next to a logit of +inf.
+  __device__ __forceinline__ double log_weight(float z) const {
+    if (z == zmax) return 0.0;
     const double t = (warp(z) - xmax) * scale;
+    return z > -INFINITY && t > -64.0 ? t : -64.0;
+  }
+  __device__ __forceinline__ double weight(float z) const {
+    const double t = log_weight(z);
     return t > -(S + 1.0) ? exp2_neg(t) : 0.0;
   }
   __device__ __forceinline__ uint64_t fixed(double w) const {
@@ -82,6 +106,10 @@ struct Weights {
            0xfffffffffffffull;
   }
   __device__ __forceinline__ uint64_t mass(float z) const { return fixed(weight(z)); }
+  __device__ __forceinline__ bool reaches_min_p(float z) const {
+    const double t = log_weight(z);
+    return t > log_min_p - 1e-6 && exp2_neg(t) >= min_p;
+  }
   // ... after min-p
   __device__ __forceinline__ uint64_t kept(float z) const {
     const double w = weight(z);
@@ -90,11 +118,15 @@ struct Weights {
 };
 
 struct Shared {
-  uint64_t hist[kBins];
+  union {
+    uint64_t hist[kBins];
+    uint64_t mass[kWaves][kMassBins];
+  };
+  uint32_t key[kWaves * kWaveList], idx[kWaves * kWaveList];   // a list, in index order
   uint64_t wave_sum[kWaves];
   uint32_t wave_cnt[kWaves];
   uint64_t above;
-  uint32_t bin;
+  uint32_t bin, found;
 };
 
 __device__ __forceinline__ uint64_t shfl_up64(uint64_t v, int d) {
@@ -119,19 +151,58 @@ __device__ __forceinline__ uint64_t wave_sum(uint64_t v) {
   return v;
 }
 
-// The row's elements [lo, hi) dealt to `count` threads in 16-byte chunks, f(z) for each.
-template <class T, class F>
-__device__ __forceinline__ void for_each(const T* row, int64_t lo, int64_t hi, int t, int count,
-                                         F f) {
-  constexpr int E = kPerChunk<T>;
-  for (int64_t c = lo + int64_t(t) * E; c < hi; c += int64_t(count) * E) {
-    float v[E];
-    load_chunk(row, c, hi, v);
+// A row in memory.
+template <class T>
+struct Row {
+  static constexpr int E = kPerChunk<T>;
+  const T* p;
+  int64_t n;
+  __device__ __forceinline__ float at(int64_t i) const { return to_f32(p[i]); }
+  // f(the chunk's values, its first index, how many) for the chunks of [lo, hi) that lane t of
+  // `count` takes, four loads under way at once; lo is a multiple of E.
+  template <class F>
+  __device__ __forceinline__ void chunks(int64_t lo, int64_t hi, int t, int count, F f) const {
+    constexpr int U = 4;
+    const int64_t step = int64_t(count) * E;
+    int64_t c = lo + int64_t(t) * E, base = lo;
+    for (; base + U * step <= hi; base += U * step, c += U * step) {
+      row_u32x4 raw[U];
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-      if (c + e < hi) f(v[e], c + e);
+      for (int u = 0; u < U; ++u) raw[u] = load_raw(p + c + u * step);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float v[E];
+        unpack_chunk<T>(raw[u], v);
+        f(v, c + u * step, E);
+      }
+    }
+    for (; base < hi; base += step, c += step) {
+      float v[E];
+      if (c < hi) load_chunk(p, c, hi, v);
+      f(v, c, c >= hi ? 0 : hi - c < E ? int(hi - c) : E);
+    }
   }
-}
+  template <class F>
+  __device__ __forceinline__ void each(int64_t lo, int64_t hi, int t, int count, F f) const {
+    chunks(lo, hi, t, count, [&](const float (&v)[E], int64_t c, int n) {
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (e < n) f(v[e], c + e);
+    });
+  }
+};
+
+// The list in LDS.
+struct List {
+  static constexpr int E = 1;
+  const uint32_t* key;
+  int64_t n;
+  __device__ __forceinline__ float at(int64_t i) const { return key_value(key[i]); }
+  template <class F>
+  __device__ __forceinline__ void each(int64_t lo, int64_t hi, int t, int count, F f) const {
+    for (int64_t i = lo + t; i < hi; i += count) f(key_value(key[i]), i);
+  }
+};
 
 // With the histogram's bins, highest first, summed up: the bin in which the sum passes
 // `target` (above < target <= above + bin; target 1 .. total), in sm.bin, sm.above. If
@@ -171,8 +242,8 @@ __device__ __forceinline__ uint64_t find_bin(Shared& sm, uint64_t target, double
 
 // The key tau at which the sum of add(z) over the row's keys, highest first, passes
 // `target`, and the sum above it. extra: added once for key extra_key.
-template <class T, class Add>
-__device__ __forceinline__ uint32_t select_key(const T* row, int64_t V, Shared& sm,
+template <class Src, class Add>
+__device__ __forceinline__ uint32_t select_key(const Src& src, Shared& sm,
                                                uint64_t& target, double p, bool share,
                                                uint64_t& above, uint32_t extra_key,
                                                uint64_t extra, Add add) {
@@ -189,7 +260,7 @@ __device__ __forceinline__ uint32_t select_key(const T* row, int64_t V, Shared& 
                       &sm.hist[(key >> shift) & ((1u << bits) - 1)]),
                   static_cast<unsigned long long>(v));
     };
-    for_each(row, 0, V, threadIdx.x, kThreads, [&](float z, int64_t) {
+    src.each(0, src.n, threadIdx.x, kThreads, [&](float z, int64_t) {
       const uint32_t key = order_key(z);
       if ((key & mask) == prefix) count(key, add(z, key));
     });
@@ -203,29 +274,290 @@ __device__ __forceinline__ uint32_t select_key(const T* row, int64_t V, Shared& 
   return prefix;
 }
 
+// What is kept of a row's keys: those above tau and the first m equal to it, of both those
+// whose weight is at least min-p.
+struct Kept {
+  uint32_t tau = 0;
+  uint64_t m = ~0ull >> 1;
+};
+
+// top-k and then top-p over a source that holds at least the first k ranks.
+template <class Src>
+__device__ __forceinline__ Kept select(const Src& src, Shared& sm, const Weights& wt, int64_t k,
+                                       double p) {
+  Kept s;
+  if (k < src.n) {
+    uint64_t above, target = uint64_t(k);
+    s.tau = select_key(src, sm, target, 0.0, false, above, 0u, 0ull,
+                       [](float, uint32_t) { return uint64_t(1); });
+    s.m = uint64_t(k) - above;
+  }
+  if (p < 1.0) {
+    uint64_t above, target = 0;
+    const uint64_t w_tau = s.tau ? wt.mass(key_value(s.tau)) : 0;
+    const uint32_t tau_k = s.tau;
+    s.tau = select_key(src, sm, target, p, true, above, tau_k, tau_k ? s.m * w_tau : 0,
+                       [&](float z, uint32_t key) { return key > tau_k ? wt.mass(z) : 0; });
+    const uint64_t w = wt.mass(key_value(s.tau));
+    const uint64_t need = (target - above + w - 1) / w;
+    s.m = s.tau == tau_k && s.m < need ? s.m : need;
+  }
+  return s;
+}
+
+// Where the target lies: the mass and the count of keys equal to tau before [lo, lo + len).
+struct Place {
+  int64_t lo, len;
+  uint64_t sum, ties;
+};
+
+__device__ __forceinline__ uint64_t target_of(float uniform, uint64_t total) {
+  const double u = fmin(fmax(double(uniform), 0.0), 1.0) * double(total);
+  const uint64_t t = u >= double(total) ? total - 1 : uint64_t(u);
+  return t < total ? t : total - 1;
+}
+
+// With every wave's kept mass and ties of part i of `at` in sm.wave_sum[i], sm.wave_cnt[i]:
+// the part that holds the target. total = 0: first call, which forms total and target.
+__device__ __forceinline__ void enter(Place& at, int64_t part, Shared& sm, const Kept& s,
+                                      uint64_t w_tau, float uniform, uint64_t& total,
+                                      uint64_t& target) {
+  auto mass_at = [&](uint64_t sum, uint64_t ties) { return sum + (ties < s.m ? ties : s.m) * w_tau; };
+  __syncthreads();
+  if (total == 0) {
+    uint64_t a = 0, t = 0;
+    for (int i = 0; i < kWaves; ++i) {
+      a += sm.wave_sum[i];
+      t += sm.wave_cnt[i];
+    }
+    total = mass_at(a, t);
+    target = target_of(uniform, total);
+  }
+  Place next = at;
+  for (int i = 0; i < kWaves; ++i) {
+    const uint64_t a = at.sum + sm.wave_sum[i], t = at.ties + sm.wave_cnt[i];
+    next.lo = at.lo + i * part;
+    const int64_t left = at.lo + at.len - next.lo;
+    next.len = left < part ? left : part;
+    next.sum = at.sum;
+    next.ties = at.ties;
+    if (target < mass_at(a, t)) break;
+    at.sum = a;
+    at.ties = t;
+  }
+  at = next;
+  __syncthreads();
+}
+
+// The source's index that the target falls on: in the place's sixteenth that holds it, that
+// one's sixteenth, and so on.
+template <class Src>
+__device__ __forceinline__ int64_t descend(const Src& src, Place at, Shared& sm, const Weights& wt,
+                                           const Kept& s, float uniform, uint64_t& total,
+                                           uint64_t target) {
+  constexpr int E = Src::E;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const uint64_t w_tau = s.tau ? wt.kept(key_value(s.tau)) : 0;
+  while (at.len > 64 || total == 0) {
+    const int64_t part = (((at.len + kWaves - 1) / kWaves) + E - 1) / E * E;
+    const int64_t from = at.lo + wave * part, end = at.lo + at.len;
+    uint64_t sum = 0;
+    uint32_t ties = 0;
+    if (from < end)
+      src.each(from, from + part < end ? from + part : end, lane, 64, [&](float z, int64_t) {
+        const uint32_t key = order_key(z);
+        if (key > s.tau) sum += wt.kept(z);
+        else if (key == s.tau) ++ties;
+      });
+    sum = wave_sum(sum);
+    ties = uint32_t(wave_sum(ties));
+    if (lane == 0) {
+      sm.wave_sum[wave] = sum;
+      sm.wave_cnt[wave] = ties;
+    }
+    enter(at, part, sm, s, w_tau, uniform, total, target);
+  }
+  if (wave == 0) {
+    const bool in = lane < at.len;
+    const float z = in ? src.at(at.lo + lane) : 0.f;
+    const uint32_t key = order_key(z);
+    const uint64_t a = at.sum + wave_scan(in && key > s.tau ? wt.kept(z) : 0, lane);
+    const uint64_t t = at.ties + wave_scan(in && key == s.tau ? 1 : 0, lane);
+    const uint64_t hit = __ballot(in && target < a + (t < s.m ? t : s.m) * w_tau);
+    if (lane == 0) sm.found = hit ? __builtin_ctzll(hit) : 0;
+  }
+  __syncthreads();
+  return at.lo + sm.found;
+}
+
+// The list's index for a list of up to kSmallList that holds the first k ranks: each thread
+// counts the ranks above its own, and their mass.
+__device__ __forceinline__ int64_t small_list(Shared& sm, int n, const Weights& wt, int64_t k,
+                                              double p, float uniform, uint64_t& total) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  uint64_t* mass = sm.hist;
+  const float z = tid < n ? key_value(sm.key[tid]) : 0.f;
+  const double w = tid < n ? wt.weight(z) : 0.0;
+  const uint64_t own = tid < n ? wt.fixed(w) : 0;
+  if (tid < kSmallList) mass[tid] = own;
+  __syncthreads();
+  bool keep = tid < n;
+  uint64_t above = 0;
+  if (wave * 64 < n) {
+    const uint32_t key = tid < n ? sm.key[tid] : 0;
+    int rank = 0;
+    for (int j = 0; j < n; ++j) {
+      const uint32_t o = sm.key[j];
+      const bool better = o > key || (o == key && j < tid);
+      rank += better;
+      above += better ? mass[j] : 0;
+    }
+    keep = keep && rank < k;
+  }
+  auto block_sum = [&](uint64_t v, uint64_t& before) {      // of waves 0 .. 3, which hold n
+    if (lane == 63 && wave < kSmallList / 64) sm.wave_sum[wave] = v;
+    __syncthreads();
+    uint64_t all = 0;
+    before = 0;
+    for (int i = 0; i < kSmallList / 64; ++i) {
+      if (i < wave) before += sm.wave_sum[i];
+      all += sm.wave_sum[i];
+    }
+    __syncthreads();
+    return all;
+  };
+  uint64_t before;
+  if (p < 1.0) {
+    const uint64_t all = block_sum(wave_scan(keep ? own : 0, lane), before);
+    const double r = __builtin_ceil(p * double(all));
+    const uint64_t limit = r >= double(all) ? all : r >= 1.0 ? uint64_t(r) : 1;
+    keep = keep && above < limit;
+  }
+  keep = keep && w >= wt.min_p;
+  const uint64_t incl = wave_scan(keep ? own : 0, lane);
+  total = block_sum(incl, before);
+  const uint64_t target = target_of(uniform, total);
+  const uint64_t upto = before + incl;
+  if (keep && own && upto > target && upto - own <= target) sm.found = tid;
+  __syncthreads();
+  return sm.found;
+}
+
+// The row's logits for which take(z, i) holds, in index order, into sm.key and sm.idx. Each
+// wave first fills a place of its own from its segment. Returns how many, or -1 if a wave
+// found more than its place holds.
+template <class T, class Take>
+__device__ __forceinline__ int collect(const Row<T>& row, int64_t seg, Shared& sm, Take take) {
+  constexpr int E = Row<T>::E;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t from = wave * seg, to = from + seg < row.n ? from + seg : row.n;
+  const uint64_t below = (1ull << lane) - 1;
+  uint32_t* key = sm.key + wave * kWaveList;
+  uint32_t* idx = sm.idx + wave * kWaveList;
+  int have = 0;
+  if (from < to)
+    row.chunks(from, to, lane, 64, [&](const float (&v)[E], int64_t c, int n) {
+      uint32_t mine = 0;
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (e < n && take(v[e])) mine |= 1u << e;
+      if (__ballot(mine != 0) == 0) return;
+      int before = 0, all = 0;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const uint64_t b = __ballot((mine >> e) & 1);
+        before += __popcll(b & below);
+        all += __popcll(b);
+      }
+      int at = have + before;
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if ((mine >> e) & 1) {
+          if (at < kWaveList) {
+            key[at] = order_key(v[e]);
+            idx[at] = uint32_t(c + e);
+          }
+          ++at;
+        }
+      have += all;
+    });
+  if (lane == 0) sm.wave_cnt[wave] = have;
+  __syncthreads();
+  int n = 0, start = 0;
+  bool fits = true;
+  for (int i = 0; i < kWaves; ++i) {
+    const int c = sm.wave_cnt[i];
+    if (i < wave) start += c;
+    fits = fits && c <= kWaveList;
+    n += c;
+  }
+  // close the gaps: every wave reads its place before any writes
+  uint32_t k[kWaveList / 64], x[kWaveList / 64];
+#pragma unroll
+  for (int i = 0; i < kWaveList / 64; ++i) {
+    k[i] = key[i * 64 + lane];
+    x[i] = idx[i * 64 + lane];
+  }
+  __syncthreads();
+  if (!fits) return -1;
+#pragma unroll
+  for (int i = 0; i < kWaveList / 64; ++i)
+    if (i * 64 + lane < have) {
+      sm.key[start + i * 64 + lane] = k[i];
+      sm.idx[start + i * 64 + lane] = x[i];
+    }
+  __syncthreads();
+  return n;
+}
+
+// A key that at least k of the threads' maxima reach (0 if fewer have one): the k-th
+// largest's upper 22 bits.
+__device__ __forceinline__ uint32_t bound_of_maxima(uint32_t own, int64_t k, Shared& sm) {
+  uint32_t prefix = 0, mask = 0;
+  uint64_t above = 0;
+#pragma unroll 1
+  for (int digit = 0; digit < 2; ++digit) {
+    const int shift = digit == 0 ? 21 : 10;
+    for (int i = threadIdx.x; i < kBins; i += kThreads) sm.hist[i] = 0;
+    __syncthreads();
+    if (own && (own & mask) == prefix)
+      atomicAdd(reinterpret_cast<unsigned long long*>(&sm.hist[(own >> shift) & (kBins - 1)]), 1ull);
+    if (threadIdx.x == 0) sm.bin = kBins;
+    find_bin(sm, uint64_t(k) - above, 0.0, false);
+    if (sm.bin == kBins) return 0;                 // fewer than k (at the first digit)
+    prefix |= sm.bin << shift;
+    mask |= uint32_t(kBins - 1) << shift;
+    above += sm.above;
+    __syncthreads();
+  }
+  return prefix;
+}
+
 // A workgroup a row.
 template <class T>
 __global__ __launch_bounds__(kThreads) void k_sample(SampleArgs a) {
   __shared__ Shared sm;
   constexpr int E = kPerChunk<T>;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int64_t r = blockIdx.x, V = a.V;
-  const T* row = static_cast<const T*>(a.logits) + r * a.ld;
+  const int64_t r = blockIdx.x;
+  const Row<T> row{static_cast<const T*>(a.logits) + r * a.ld, a.V};
+  const int64_t V = a.V, part = (V + kWaves - 1) / kWaves, seg = (part + E - 1) / E * E;
+  const int64_t from = wave * seg, to = from + seg < V ? from + seg : V;
 
   // the largest logit; a row of -inf alone or with a NaN has no token
-  uint32_t best = 0;
+  uint32_t own = 0;
   bool nan = false;
-  for_each(row, 0, V, tid, kThreads, [&](float z, int64_t) {
-    if (z != z) nan = true;
-    else best = MaxOp()(best, order_key(z));
-  });
-  best = wave_all(best, MaxOp());
+  if (from < to)
+    row.each(from, to, lane, 64, [&](float z, int64_t) {
+      nan |= z != z;
+      own = MaxOp()(own, order_key(z));
+    });
+  uint32_t best = wave_all(own, MaxOp());
+  const uint64_t any_nan = __ballot(nan);
   if (lane == 0) {
     sm.wave_cnt[wave] = best;
-    sm.wave_sum[wave] = 0;
+    sm.wave_sum[wave] = any_nan;
   }
-  __syncthreads();
-  if (nan) sm.wave_sum[wave] = 1;
   __syncthreads();
   best = 0;
   nan = false;
@@ -243,105 +575,164 @@ __global__ __launch_bounds__(kThreads) void k_sample(SampleArgs a) {
     return;
   }
 
-  const float T_ = a.temperature.at(r);
+  const float T_ = a.temperature.at(r), uniform = a.uniforms[r];
   int64_t k = a.top_k.at(r);
   if (k <= 0 || k > V) k = V;
   if (!(T_ > 0.f)) k = 1;
   Weights wt;
   wt.cap = a.softcap;
-  wt.inv_cap = a.softcap > 0.f ? 1.0 / a.softcap : 0.0;
+  wt.two_inv_cap = a.softcap > 0.f ? 2.0 / a.softcap : 0.0;
   wt.zmax = key_value(best);
   wt.xmax = wt.warp(wt.zmax);
   wt.scale = T_ > 0.f ? kLog2eD / double(T_) : 0.0;
   wt.S = a.weight_bits;
   wt.min_p = fmin(fmax(double(a.min_p.at(r)), 0.0), 1.0);
+  wt.log_min_p = wt.min_p > 0.0 ? fmax(log2(wt.min_p), -63.0) : -63.0;
   const double p = fmax(double(a.top_p.at(r)), 0.0);
 
-  uint32_t tau = 0;
-  uint64_t m = ~0ull >> 1;                         // keys equal to tau that are kept
-  if (k == 1) {
-    tau = best;
-    m = 1;
-  } else if (k < V) {
-    uint64_t above, target = uint64_t(k);
-    tau = select_key(row, V, sm, target, 0.0, false, above, 0u, 0ull,
-                     [](float, uint32_t) { return uint64_t(1); });
-    m = uint64_t(k) - above;
-  }
-  if (k > 1 && p < 1.0) {
-    uint64_t above, target = 0;
-    const uint64_t w_tau = tau ? wt.mass(key_value(tau)) : 0;
-    const uint32_t tau_k = tau;
-    tau = select_key(row, V, sm, target, p, true, above, tau_k, tau_k ? m * w_tau : 0,
-                     [&](float z, uint32_t key) { return key > tau_k ? wt.mass(z) : 0; });
-    const uint64_t w = wt.mass(key_value(tau));
-    const uint64_t need = (target - above + w - 1) / w;
-    m = tau == tau_k && m < need ? m : need;
-  }
-  // masses and counts of equal keys before a place: the mass kept there
-  const uint64_t w_tau = tau ? wt.kept(key_value(tau)) : 0;
-  auto mass_at = [&](uint64_t sum, uint64_t ties) { return sum + (ties < m ? ties : m) * w_tau; };
-
-  // the token: the row's sixteenth that holds the target, its sixteenth, and so on
-  int64_t lo = 0, len = V;
-  uint64_t sum0 = 0, tie0 = 0, target = 0, total = 0;
-  bool first = true;
-  do {
-    const int64_t part = (((len + kWaves - 1) / kWaves) + E - 1) / E * E;
-    const int64_t from = lo + wave * part;
-    const int64_t to = from + part < lo + len ? from + part : lo + len;
-    uint64_t sum = 0;
-    uint32_t ties = 0;
-    for_each(row, from, to, lane, 64, [&](float z, int64_t) {
-      const uint32_t key = order_key(z);
-      if (key > tau) sum += wt.kept(z);
-      else if (key == tau) ++ties;
-    });
-    sum = wave_sum(sum);
-    ties = uint32_t(wave_sum(ties));
-    if (lane == 0) {
-      sm.wave_sum[wave] = sum;
-      sm.wave_cnt[wave] = ties;
+  uint64_t total = 0, target = 0;
+  int64_t token = -1;
+  if (k == 1) {                                    // the first of the largest
+    if (own == best) {
+      uint32_t first = ~0u;
+      row.each(from, to, lane, 64, [&](float z, int64_t i) {
+        if (order_key(z) == best && uint32_t(i) < first) first = uint32_t(i);
+      });
+      sm.idx[tid] = first;
+    } else {
+      sm.idx[tid] = ~0u;
     }
     __syncthreads();
-    if (first) {
-      uint64_t s = 0, t = 0;
-      for (int i = 0; i < kWaves; ++i) {
-        s += sm.wave_sum[i];
-        t += sm.wave_cnt[i];
+    uint32_t first = sm.idx[lane];
+#pragma unroll
+    for (int i = 1; i < kWaves; ++i) first = MinOp()(first, sm.idx[i * 64 + lane]);
+    token = wave_all(first, MinOp());
+    total = 1ull << wt.S;
+  } else if (k < V || (p >= 1.0 && wt.min_p > 0.0)) {
+    // a list of all that may be kept
+    int n;
+    if (k < V) {
+      const uint32_t bound = k <= kThreads ? bound_of_maxima(own, k, sm) : 0u;
+      n = bound ? collect(row, seg, sm, [&](float z) { return order_key(z) >= bound; }) : -1;
+    } else {
+      n = collect(row, seg, sm, [&](float z) { return wt.reaches_min_p(z); });
+    }
+    if (n >= 0) {
+      int64_t at;
+      if (n <= kSmallList) {
+        at = small_list(sm, n, wt, k, p, uniform, total);
+      } else {
+        const List list{sm.key, n};
+        const Kept s = select(list, sm, wt, k, p);
+        at = descend(list, Place{0, n, 0, 0}, sm, wt, s, uniform, total, target);
       }
-      total = mass_at(s, t);
-      const double u = fmin(fmax(double(a.uniforms[r]), 0.0), 1.0) * double(total);
-      target = u >= double(total) ? total - 1 : uint64_t(u);
-      if (target >= total) target = total - 1;
-      first = false;
+      token = sm.idx[at];
     }
-    int64_t next = lo, rest = len;
-    for (int i = 0; i < kWaves; ++i) {
-      const uint64_t s = sum0 + sm.wave_sum[i], t = tie0 + sm.wave_cnt[i];
-      next = lo + i * part;
-      rest = lo + len - next < part ? lo + len - next : part;
-      if (target < mass_at(s, t)) break;
-      sum0 = s;
-      tie0 = t;
-    }
-    lo = next;
-    len = rest;
+  } else if (p < 1.0) {
+    // weights by bins of an eighth of a power of two, each wave its own
+    for (int i = tid; i < kWaves * kMassBins; i += kThreads) (&sm.mass[0][0])[i] = 0;
     __syncthreads();
-  } while (len > 64);
-  if (wave == 0) {
-    const float z = lane < len ? to_f32(row[lo + lane]) : -INFINITY;
-    const uint32_t key = lane < len ? order_key(z) : 0;
-    const uint64_t s = sum0 + wave_scan(lane < len && key > tau ? wt.kept(z) : 0, lane);
-    const uint64_t t = tie0 + wave_scan(lane < len && key == tau ? 1 : 0, lane);
-    const uint64_t hit = __ballot(target < mass_at(s, t));
-    const int at = hit ? __builtin_ctzll(hit) : 0;
-    if (lane == at) {
-      a.tokens[r] = lo + at;
-      if (a.logp) {
-        const double x = z == wt.zmax ? 0.0 : (wt.warp(z) - wt.xmax) * wt.scale;
-        a.logp[r] = float(x / kLog2eD - log(__builtin_ldexp(double(total), -wt.S)));
+    // 0: the largest weights; the last holds all below 2^-47.9
+    auto bin_of = [](double t) {
+      const int b = int(t * -8.0);
+      return b < kMassBins - 1 ? b : kMassBins - 1;
+    };
+    if (from < to)
+      row.each(from, to, lane, 64, [&](float z, int64_t) {
+        const double t = wt.log_weight(z);
+        if (t > -(wt.S + 1.0)) {
+          const uint64_t w = wt.fixed(exp2_neg(t));
+          if (w)
+            atomicAdd(reinterpret_cast<unsigned long long*>(&sm.mass[wave][bin_of(t)]),
+                      static_cast<unsigned long long>(w));
+        }
+      });
+    __syncthreads();
+    // the bin in which the sum passes p of all
+    uint64_t mine = 0;
+    if (tid < kMassBins)
+      for (int i = 0; i < kWaves; ++i) mine += sm.mass[i][tid];
+    const uint64_t incl = wave_scan(mine, lane);
+    if (lane == 63) sm.wave_sum[wave] = incl;
+    __syncthreads();
+    uint64_t before = 0, all = 0;
+    for (int i = 0; i < kMassBins / 64; ++i) {
+      if (i < wave) before += sm.wave_sum[i];
+      all += sm.wave_sum[i];
+    }
+    const double share = __builtin_ceil(p * double(all));
+    const uint64_t limit = share >= double(all) ? all : share >= 1.0 ? uint64_t(share) : 1;
+    const uint64_t upto = before + incl;
+    if (tid < kMassBins && upto >= limit && upto - mine < limit) {
+      sm.bin = tid;
+      sm.above = upto - mine;
+    }
+    __syncthreads();
+    const int p_bin = sm.bin;
+    const uint64_t above_bin = sm.above;
+    int bin = p_bin;
+    if (wt.min_p > 0.0) {
+      // what min-p leaves lies in higher bins alone: it is all kept
+      if (bin_of(wt.log_min_p) + 1 < bin) bin = -1;
+    }
+    int n;
+    if (bin < 0) {
+      n = collect(row, seg, sm, [&](float z) { return wt.reaches_min_p(z); });
+      if (n >= 0) {
+        const List list{sm.key, n};
+        const int64_t at = descend(list, Place{0, n, 0, 0}, sm, wt, Kept{}, uniform, total, target);
+        token = sm.idx[at];
       }
+    } else {
+      // each segment's mass in the bins above is kept, unless min-p's border is near
+      const bool clean = !(wt.min_p > 0.0) || bin_of(wt.log_min_p) - 1 > bin;
+      uint64_t sum = 0;
+      if (clean) {
+        for (int i = lane; i < bin; i += 64) sum += sm.mass[wave][i];
+        sum = wave_sum(sum);
+      }
+      n = clean ? collect(row, seg, sm, [&](float z) {
+        const double t = wt.log_weight(z);
+        return t > -(wt.S + 1.0) && bin_of(t) == bin;
+      }) : -1;
+      if (n >= 0) {
+        const List list{sm.key, n};
+        Kept s;
+        uint64_t above, goal = limit - above_bin;
+        s.tau = select_key(list, sm, goal, 0.0, false, above, 0u, 0ull,
+                           [&](float z, uint32_t) { return wt.mass(z); });
+        const uint64_t w = wt.mass(key_value(s.tau));
+        s.m = (goal - above + w - 1) / w;
+        // the kept mass and ties of each segment
+        uint64_t in = 0;
+        uint32_t ties = 0;
+        for (int i = lane; i < n; i += 64) {
+          if (int64_t(sm.idx[i]) < from || int64_t(sm.idx[i]) >= to) continue;
+          if (sm.key[i] > s.tau) in += wt.mass(key_value(sm.key[i]));
+          else if (sm.key[i] == s.tau) ++ties;
+        }
+        in = wave_sum(in) + sum;
+        ties = uint32_t(wave_sum(ties));
+        if (lane == 0) {
+          sm.wave_sum[wave] = in;
+          sm.wave_cnt[wave] = ties;
+        }
+        Place at{0, V, 0, 0};
+        enter(at, seg, sm, s, w, uniform, total, target);
+        token = descend(row, at, sm, wt, s, uniform, total, target);
+      }
+    }
+  }
+  if (token < 0) {                                 // no filter, or a list that does not fit
+    const Kept s = k < V || p < 1.0 ? select(row, sm, wt, k, p) : Kept{};
+    token = descend(row, Place{0, V, 0, 0}, sm, wt, s, uniform, total, target);
+  }
+  if (tid == 0) {
+    a.tokens[r] = token;
+    if (a.logp) {
+      const float z = row.at(token);
+      const double x = z == wt.zmax ? 0.0 : (wt.warp(z) - wt.xmax) * wt.scale;
+      a.logp[r] = float(x / kLog2eD - log(__builtin_ldexp(double(total), -wt.S)));
     }
   }
 }
