@@ -57,63 +57,59 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 }
 constexpr uint32_t kKeyNegInf = 0x007fffffu;       // order_key(-inf)
 
-// 2^t for t in (-1022, 0]: 2^n 2^f with |f| <= 1/2, the exponential's series to f^11 (what
-// it leaves out is below 2^-47).
-__device__ __forceinline__ double exp2_neg(double t) {
-  const double n = __builtin_rint(t), y = (t - n) * 0.69314718055994530942;
-  double s = 1.0 / 39916800;
-  s = fma(s, y, 1.0 / 3628800);
-  s = fma(s, y, 1.0 / 362880);
-  s = fma(s, y, 1.0 / 40320);
-  s = fma(s, y, 1.0 / 5040);
-  s = fma(s, y, 1.0 / 720);
-  s = fma(s, y, 1.0 / 120);
-  s = fma(s, y, 1.0 / 24);
-  s = fma(s, y, 1.0 / 6);
-  s = fma(s, y, 0.5);
-  s = fma(s, y, 1.0);
-  s = fma(s, y, 1.0);
-  return __builtin_ldexp(s, int(n));
+// 2^(t + up) for t in [-1000, 0]: 2^n 2^f with |f| <= 1/2, and 2^f by the polynomial of
+// degree 10 through its values at the Chebyshev points (off by 2^-51).
+__device__ __forceinline__ double exp2_neg(double t, int up = 0) {
+  const double n = __builtin_rint(t), f = t - n;
+  double s = 7.072585949269224e-09;
+  s = fma(s, f, 1.0208690299958306e-07);
+  s = fma(s, f, 1.321544258792169e-06);
+  s = fma(s, f, 1.5252657260200837e-05);
+  s = fma(s, f, 0.0001540353044173605);
+  s = fma(s, f, 0.0013333558230164974);
+  s = fma(s, f, 0.009618129107606888);
+  s = fma(s, f, 0.05550410866444772);
+  s = fma(s, f, 0.24022650695910097);
+  s = fma(s, f, 0.69314718055995);
+  s = fma(s, f, 1.0);
+  return __builtin_ldexp(s, int(n) + up);
 }
 
-// A row's weights.
+// A row's weights. CAP: logits are capped first.
+template <bool CAP>
 struct Weights {
   double cap, two_inv_cap, xmax, scale;            // scale: log2(e) / T
-  float zmax;
   int S;
   double min_p, log_min_p;                         // log_min_p: for a first look
   // cap tanh(z / cap) = sign cap (1 - e) / (1 + e), e = exp(-2 |z| / cap): off by a few 2^-53
-  // of cap, which is all that a difference to xmax needs.
+  // of cap, which is all that a difference to xmax needs. A logit of -inf stays.
   __device__ __forceinline__ double warp(float z) const {
-    if (!(cap > 0.0)) return double(z);
+    if constexpr (!CAP) return double(z);
     const double t = fmax(fabs(double(z)) * two_inv_cap * -kLog2eD, -1000.0), e = exp2_neg(t);
-    return copysign(cap * ((1.0 - e) / (1.0 + e)), double(z));
+    return z == -INFINITY ? -INFINITY : copysign(cap * ((1.0 - e) / (1.0 + e)), double(z));
   }
-  // log2 of w of a logit, or below -(S + 1) where w is zero: there, for -inf (also where a
-  // softcap makes it finite), and next to a logit of +inf.
+  // log2 of w of a logit, or -64 where that is lower (w is then zero): so for -inf, and for
+  // all others next to one of +inf, whose difference to itself, a NaN, counts as 0.
   __device__ __forceinline__ double log_weight(float z) const {
-    if (z == zmax) return 0.0;
-    const double t = (warp(z) - xmax) * scale;
-    return z > -INFINITY && t > -64.0 ? t : -64.0;
+    return fmax(fmin((warp(z) - xmax) * scale, 0.0), -64.0);
   }
-  __device__ __forceinline__ double weight(float z) const {
-    const double t = log_weight(z);
-    return t > -(S + 1.0) ? exp2_neg(t) : 0.0;
+  __device__ __forceinline__ double weight(float z) const { return exp2_neg(log_weight(z)); }
+  // w 2^S + 2^52 has its whole part, rounded to nearest, in its low 52 bits
+  __device__ __forceinline__ uint64_t whole(double w_s) const {
+    return __builtin_bit_cast(uint64_t, w_s + 4503599627370496.0) & 0xfffffffffffffull;
   }
-  __device__ __forceinline__ uint64_t fixed(double w) const {
-    // w 2^S + 2^52 has its whole part, rounded to nearest, in its low 52 bits
-    return __builtin_bit_cast(uint64_t, __builtin_ldexp(w, S) + 4503599627370496.0) &
-           0xfffffffffffffull;
+  __device__ __forceinline__ uint64_t fixed_of(double log_w) const {
+    return whole(exp2_neg(log_w, S));
   }
-  __device__ __forceinline__ uint64_t mass(float z) const { return fixed(weight(z)); }
+  __device__ __forceinline__ uint64_t mass(float z) const { return fixed_of(log_weight(z)); }
   __device__ __forceinline__ bool reaches_min_p(float z) const {
     const double t = log_weight(z);
     return t > log_min_p - 1e-6 && exp2_neg(t) >= min_p;
   }
   // ... after min-p
   __device__ __forceinline__ uint64_t kept(float z) const {
-    const double w = weight(z);
-    return w >= min_p ? fixed(w) : 0;
+    const double t = log_weight(z);
+    return exp2_neg(t) >= min_p ? fixed_of(t) : 0;
   }
 };
 
@@ -282,8 +278,8 @@ struct Kept {
 };
 
 // top-k and then top-p over a source that holds at least the first k ranks.
-template <class Src>
-__device__ __forceinline__ Kept select(const Src& src, Shared& sm, const Weights& wt, int64_t k,
+template <class Src, bool CAP>
+__device__ __forceinline__ Kept select(const Src& src, Shared& sm, const Weights<CAP>& wt, int64_t k,
                                        double p) {
   Kept s;
   if (k < src.n) {
@@ -351,8 +347,8 @@ __device__ __forceinline__ void enter(Place& at, int64_t part, Shared& sm, const
 
 // The source's index that the target falls on: in the place's sixteenth that holds it, that
 // one's sixteenth, and so on.
-template <class Src>
-__device__ __forceinline__ int64_t descend(const Src& src, Place at, Shared& sm, const Weights& wt,
+template <class Src, bool CAP>
+__device__ __forceinline__ int64_t descend(const Src& src, Place at, Shared& sm, const Weights<CAP>& wt,
                                            const Kept& s, float uniform, uint64_t& total,
                                            uint64_t target) {
   constexpr int E = Src::E;
@@ -392,13 +388,14 @@ __device__ __forceinline__ int64_t descend(const Src& src, Place at, Shared& sm,
 
 // The list's index for a list of up to kSmallList that holds the first k ranks: each thread
 // counts the ranks above its own, and their mass.
-__device__ __forceinline__ int64_t small_list(Shared& sm, int n, const Weights& wt, int64_t k,
+template <bool CAP>
+__device__ __forceinline__ int64_t small_list(Shared& sm, int n, const Weights<CAP>& wt, int64_t k,
                                               double p, float uniform, uint64_t& total) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   uint64_t* mass = sm.hist;
   const float z = tid < n ? key_value(sm.key[tid]) : 0.f;
-  const double w = tid < n ? wt.weight(z) : 0.0;
-  const uint64_t own = tid < n ? wt.fixed(w) : 0;
+  const double lw = tid < n ? wt.log_weight(z) : -64.0;
+  const uint64_t own = tid < n ? wt.fixed_of(lw) : 0;
   if (tid < kSmallList) mass[tid] = own;
   __syncthreads();
   bool keep = tid < n;
@@ -433,7 +430,7 @@ __device__ __forceinline__ int64_t small_list(Shared& sm, int n, const Weights& 
     const uint64_t limit = r >= double(all) ? all : r >= 1.0 ? uint64_t(r) : 1;
     keep = keep && above < limit;
   }
-  keep = keep && w >= wt.min_p;
+  keep = keep && exp2_neg(lw) >= wt.min_p;
   const uint64_t incl = wave_scan(keep ? own : 0, lane);
   total = block_sum(incl, before);
   const uint64_t target = target_of(uniform, total);
@@ -520,7 +517,7 @@ __device__ __forceinline__ uint32_t bound_of_maxima(uint32_t own, int64_t k, Sha
     const int shift = digit == 0 ? 21 : 10;
     for (int i = threadIdx.x; i < kBins; i += kThreads) sm.hist[i] = 0;
     __syncthreads();
-    if (own && (own & mask) == prefix)
+    if (own > kKeyNegInf && (own & mask) == prefix)
       atomicAdd(reinterpret_cast<unsigned long long*>(&sm.hist[(own >> shift) & (kBins - 1)]), 1ull);
     if (threadIdx.x == 0) sm.bin = kBins;
     find_bin(sm, uint64_t(k) - above, 0.0, false);
@@ -534,7 +531,7 @@ __device__ __forceinline__ uint32_t bound_of_maxima(uint32_t own, int64_t k, Sha
 }
 
 // A workgroup a row.
-template <class T>
+template <class T, bool CAP>
 __global__ __launch_bounds__(kThreads) void k_sample(SampleArgs a) {
   __shared__ Shared sm;
   constexpr int E = kPerChunk<T>;
@@ -545,13 +542,14 @@ __global__ __launch_bounds__(kThreads) void k_sample(SampleArgs a) {
   const int64_t from = wave * seg, to = from + seg < V ? from + seg : V;
 
   // the largest logit; a row of -inf alone or with a NaN has no token
-  uint32_t own = 0;
+  float most = -INFINITY;
   bool nan = false;
   if (from < to)
     row.each(from, to, lane, 64, [&](float z, int64_t) {
       nan |= z != z;
-      own = MaxOp()(own, order_key(z));
+      most = fmaxf(most, z);
     });
+  const uint32_t own = order_key(most);            // key of -inf: nothing
   uint32_t best = wave_all(own, MaxOp());
   const uint64_t any_nan = __ballot(nan);
   if (lane == 0) {
@@ -579,12 +577,12 @@ __global__ __launch_bounds__(kThreads) void k_sample(SampleArgs a) {
   int64_t k = a.top_k.at(r);
   if (k <= 0 || k > V) k = V;
   if (!(T_ > 0.f)) k = 1;
-  Weights wt;
+  Weights<CAP> wt;
   wt.cap = a.softcap;
   wt.two_inv_cap = a.softcap > 0.f ? 2.0 / a.softcap : 0.0;
-  wt.zmax = key_value(best);
-  wt.xmax = wt.warp(wt.zmax);
-  wt.scale = T_ > 0.f ? kLog2eD / double(T_) : 0.0;
+  wt.xmax = wt.warp(key_value(best));
+  // not 0 for an infinite temperature: -inf times it is to stay -inf
+  wt.scale = T_ > 0.f ? fmax(kLog2eD / double(T_), 1e-300) : 0.0;
   wt.S = a.weight_bits;
   wt.min_p = fmin(fmax(double(a.min_p.at(r)), 0.0), 1.0);
   wt.log_min_p = wt.min_p > 0.0 ? fmax(log2(wt.min_p), -63.0) : -63.0;
@@ -640,12 +638,10 @@ __global__ __launch_bounds__(kThreads) void k_sample(SampleArgs a) {
     if (from < to)
       row.each(from, to, lane, 64, [&](float z, int64_t) {
         const double t = wt.log_weight(z);
-        if (t > -(wt.S + 1.0)) {
-          const uint64_t w = wt.fixed(exp2_neg(t));
-          if (w)
-            atomicAdd(reinterpret_cast<unsigned long long*>(&sm.mass[wave][bin_of(t)]),
-                      static_cast<unsigned long long>(w));
-        }
+        const uint64_t w = wt.fixed_of(t);
+        if (w)
+          atomicAdd(reinterpret_cast<unsigned long long*>(&sm.mass[wave][bin_of(t)]),
+                    static_cast<unsigned long long>(w));
       });
     __syncthreads();
     // the bin in which the sum passes p of all
@@ -692,8 +688,7 @@ __global__ __launch_bounds__(kThreads) void k_sample(SampleArgs a) {
         sum = wave_sum(sum);
       }
       n = clean ? collect(row, seg, sm, [&](float z) {
-        const double t = wt.log_weight(z);
-        return t > -(wt.S + 1.0) && bin_of(t) == bin;
+        return bin_of(wt.log_weight(z)) == bin;
       }) : -1;
       if (n >= 0) {
         const List list{sm.key, n};
@@ -730,8 +725,7 @@ __global__ __launch_bounds__(kThreads) void k_sample(SampleArgs a) {
   if (tid == 0) {
     a.tokens[r] = token;
     if (a.logp) {
-      const float z = row.at(token);
-      const double x = z == wt.zmax ? 0.0 : (wt.warp(z) - wt.xmax) * wt.scale;
+      const double x = k == 1 ? 0.0 : fmin((wt.warp(row.at(token)) - wt.xmax) * wt.scale, 0.0);
       a.logp[r] = float(x / kLog2eD - log(__builtin_ldexp(double(total), -wt.S)));
     }
   }
@@ -740,7 +734,7 @@ __global__ __launch_bounds__(kThreads) void k_sample(SampleArgs a) {
 template <class T>
 hipError_t sample(const SampleArgs& a, const Launcher& L) {
   L.pre(kSample);
-  hipLaunchKernelGGL(k_sample<T>, dim3(unsigned(a.N)), dim3(kThreads), 0, L.stream, a);
+  hipLaunchKernelGGL((a.softcap > 0.f ? k_sample<T, true> : k_sample<T, false>), dim3(unsigned(a.N)), dim3(kThreads), 0, L.stream, a);
   L.post(kSample);
   return hipGetLastError();
 }
