@@ -125,40 +125,26 @@ struct Shared {
   uint32_t bin, found;
 };
 
-__device__ __forceinline__ uint64_t shfl_up64(uint64_t v, int d) {
-  const uint32_t lo = __shfl_up(uint32_t(v), d), hi = __shfl_up(uint32_t(v >> 32), d);
-  return uint64_t(hi) << 32 | lo;
-}
-// Sum over the lanes up to this one.
-__device__ __forceinline__ uint64_t wave_scan(uint64_t v, int lane) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const uint64_t o = shfl_up64(v, d);
-    if (lane >= d) v += o;
-  }
-  return v;
-}
-__device__ __forceinline__ uint64_t wave_sum(uint64_t v) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) {
-    const uint32_t lo = __shfl_xor(uint32_t(v), d), hi = __shfl_xor(uint32_t(v >> 32), d);
-    v += uint64_t(hi) << 32 | lo;
-  }
-  return v;
-}
-
 // A row in memory.
+constexpr int kLaneMost = 8;                       // values a lane reads at once (lane_values)
 template <class T>
 struct Row {
   static constexpr int E = kPerChunk<T>;
   const T* p;
   int64_t n;
   __device__ __forceinline__ float at(int64_t i) const { return to_f32(p[i]); }
-  // f(the chunk's values, its first index, how many) for the chunks of [lo, hi) that lane t of
-  // `count` takes, four loads under way at once; lo is a multiple of E.
-  template <class F>
+  // The chunk at c (a multiple of E) of [.., hi), without a condition on the load: at the
+  // end of the range, or behind it, the range's last E values are read instead. Value e is
+  // that of index i + e, and belongs to the chunk for e >= the result.
+  __device__ __forceinline__ int chunk(int64_t c, int64_t hi, float (&v)[E], int64_t& i) const {
+    i = c + E <= hi ? c : hi - E;
+    unpack_chunk<T>(load_raw(p + i), v);
+    return c - i < E ? int(c - i) : E;
+  }
+  // f(a chunk's values, index of the first, the first that counts) for the chunks of [lo, hi)
+  // that lane t of `count` takes, U loads under way at once; lo is a multiple of E.
+  template <int U, class F>
   __device__ __forceinline__ void chunks(int64_t lo, int64_t hi, int t, int count, F f) const {
-    constexpr int U = 4;
     const int64_t step = int64_t(count) * E;
     int64_t c = lo + int64_t(t) * E, base = lo;
     for (; base + U * step <= hi; base += U * step, c += U * step) {
@@ -169,22 +155,55 @@ struct Row {
       for (int u = 0; u < U; ++u) {
         float v[E];
         unpack_chunk<T>(raw[u], v);
-        f(v, c + u * step, E);
+        f(v, c + u * step, 0);
       }
     }
-    for (; base < hi; base += step, c += step) {
+    if (hi < E) {                                  // fewer values than a chunk
+      if (base >= hi) return;
       float v[E];
-      if (c < hi) load_chunk(p, c, hi, v);
-      f(v, c, c >= hi ? 0 : hi - c < E ? int(hi - c) : E);
+      load_chunk(p, c, hi, v);
+#pragma unroll
+      for (int e = 0; e < E; ++e)                  // the last one to the end: [0, hi) at e0 = 0
+        if (e >= hi) v[e] = -INFINITY;
+      f(v, c, c < hi ? 0 : E);
+      return;
+    }
+    constexpr int H = U / 2;
+    for (; base < hi; base += H * step, c += H * step) {
+      float v[H][E];
+      int64_t i[H];
+      int e0[H];
+#pragma unroll
+      for (int u = 0; u < H; ++u) e0[u] = chunk(c + u * step, hi, v[u], i[u]);
+#pragma unroll
+      for (int u = 0; u < H; ++u) f(v[u], i[u], e0[u]);
     }
   }
-  template <class F>
+  template <int U = 4, class F>
   __device__ __forceinline__ void each(int64_t lo, int64_t hi, int t, int count, F f) const {
-    chunks(lo, hi, t, count, [&](const float (&v)[E], int64_t c, int n) {
+    chunks<U>(lo, hi, t, count, [&](const float (&v)[E], int64_t i, int e0) {
 #pragma unroll
       for (int e = 0; e < E; ++e)
-        if (e < n) f(v[e], c + e);
+        if (e >= e0) f(v[e], i + e);
     });
+  }
+  // f(j, z, i) for the values j of [lo, hi), at most kLaneMost of them; lo is a multiple of E.
+  template <class F>
+  __device__ __forceinline__ void lane_values(int64_t lo, int64_t hi, F f) const {
+    constexpr int C = kLaneMost / E;
+    if (n < E) {
+      for (int j = 0; j < hi - lo; ++j) f(j, at(lo + j), lo + j);
+      return;
+    }
+    float v[C][E];
+    int64_t i[C];
+#pragma unroll
+    for (int u = 0; u < C; ++u) chunk(lo + u * E, n, v[u], i[u]);
+#pragma unroll
+    for (int u = 0; u < C; ++u)
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (i[u] + e >= lo + u * E && i[u] + e < hi) f(u * E + e, v[u][e], i[u] + e);
   }
 };
 
@@ -198,6 +217,12 @@ struct List {
   __device__ __forceinline__ void each(int64_t lo, int64_t hi, int t, int count, F f) const {
     for (int64_t i = lo + t; i < hi; i += count) f(key_value(key[i]), i);
   }
+  template <class F>
+  __device__ __forceinline__ void lane_values(int64_t lo, int64_t hi, F f) const {
+#pragma unroll
+    for (int j = 0; j < kLaneMost; ++j)
+      if (lo + j < hi) f(j, key_value(key[lo + j]), lo + j);
+  }
 };
 
 // With the histogram's bins, highest first, summed up: the bin in which the sum passes
@@ -210,7 +235,7 @@ __device__ __forceinline__ uint64_t find_bin(Shared& sm, uint64_t target, double
   uint64_t v[kEach], sum = 0;
 #pragma unroll
   for (int i = 0; i < kEach; ++i) sum += v[i] = sm.hist[kBins - 1 - (tid * kEach + i)];
-  const uint64_t incl = wave_scan(sum, lane);
+  const uint64_t incl = wave_scan64(sum);
   if (lane == 63) sm.wave_sum[w] = incl;
   __syncthreads();
   uint64_t before = 0, total = 0;
@@ -236,18 +261,22 @@ __device__ __forceinline__ uint64_t find_bin(Shared& sm, uint64_t target, double
   return target;
 }
 
-// The key tau at which the sum of add(z) over the row's keys, highest first, passes
-// `target`, and the sum above it. extra: added once for key extra_key.
+// The key tau at which the sum of add(z) over the source's keys, highest first, passes
+// `target`, and the sum above it. extra: added once for key extra_key. The keys share
+// their bits above the lowest `bits`, which are those of `prefix`.
 template <class Src, class Add>
 __device__ __forceinline__ uint32_t select_key(const Src& src, Shared& sm,
                                                uint64_t& target, double p, bool share,
                                                uint64_t& above, uint32_t extra_key,
-                                               uint64_t extra, Add add) {
-  uint32_t prefix = 0, mask = 0;
+                                               uint64_t extra, Add add, int left = 32,
+                                               uint32_t prefix = 0) {
+  uint32_t mask = left < 32 ? ~0u << left : 0;
   above = 0;
+  bool first = true;
 #pragma unroll 1
-  for (int digit = 0; digit < 3; ++digit) {
-    const int shift = digit == 0 ? 21 : digit == 1 ? 10 : 0, bits = digit < 2 ? 11 : 10;
+  while (left > 0) {
+    const int bits = left < 11 ? left : 11, shift = left - bits;
+    left = shift;
     for (int i = threadIdx.x; i < kBins; i += kThreads) sm.hist[i] = 0;
     __syncthreads();
     auto count = [&](uint32_t key, uint64_t v) {
@@ -261,7 +290,8 @@ __device__ __forceinline__ uint32_t select_key(const Src& src, Shared& sm,
       if ((key & mask) == prefix) count(key, add(z, key));
     });
     if (threadIdx.x == 0) count(extra_key, extra);
-    target = find_bin(sm, target - above, p, share && digit == 0) + above;
+    target = find_bin(sm, target - above, p, share && first) + above;
+    first = false;
     prefix |= sm.bin << shift;
     mask |= ((1u << bits) - 1) << shift;
     above += sm.above;
@@ -315,46 +345,55 @@ __device__ __forceinline__ uint64_t target_of(float uniform, uint64_t total) {
 
 // With every wave's kept mass and ties of part i of `at` in sm.wave_sum[i], sm.wave_cnt[i]:
 // the part that holds the target. total = 0: first call, which forms total and target.
-__device__ __forceinline__ void enter(Place& at, int64_t part, Shared& sm, const Kept& s,
-                                      uint64_t w_tau, float uniform, uint64_t& total,
-                                      uint64_t& target) {
+__device__ __forceinline__ int enter(Place& at, int64_t part, Shared& sm, const Kept& s,
+                                     uint64_t w_tau, float uniform, uint64_t& total,
+                                     uint64_t& target) {
   auto mass_at = [&](uint64_t sum, uint64_t ties) { return sum + (ties < s.m ? ties : s.m) * w_tau; };
   __syncthreads();
+  uint64_t a[kWaves + 1], c[kWaves + 1];           // before part i
+  a[0] = at.sum;
+  c[0] = at.ties;
+#pragma unroll
+  for (int i = 0; i < kWaves; ++i) {
+    a[i + 1] = a[i] + sm.wave_sum[i];
+    c[i + 1] = c[i] + sm.wave_cnt[i];
+  }
+  __syncthreads();
   if (total == 0) {
-    uint64_t a = 0, t = 0;
-    for (int i = 0; i < kWaves; ++i) {
-      a += sm.wave_sum[i];
-      t += sm.wave_cnt[i];
-    }
-    total = mass_at(a, t);
+    total = mass_at(a[kWaves], c[kWaves]);
     target = target_of(uniform, total);
   }
-  Place next = at;
-  for (int i = 0; i < kWaves; ++i) {
-    const uint64_t a = at.sum + sm.wave_sum[i], t = at.ties + sm.wave_cnt[i];
-    next.lo = at.lo + i * part;
-    const int64_t left = at.lo + at.len - next.lo;
-    next.len = left < part ? left : part;
-    next.sum = at.sum;
-    next.ties = at.ties;
-    if (target < mass_at(a, t)) break;
-    at.sum = a;
-    at.ties = t;
-  }
-  at = next;
-  __syncthreads();
+  int part_of = 0;                                 // parts that end at or before the target
+#pragma unroll
+  for (int i = 1; i < kWaves; ++i)
+    if (mass_at(a[i], c[i]) <= target) {
+      part_of = i;
+      at.sum = a[i];
+      at.ties = c[i];
+    }
+  at.lo += part_of * part;
+  at.len -= part_of * part;
+  if (at.len > part) at.len = part;
+  return part_of;
 }
 
-// The source's index that the target falls on: in the place's sixteenth that holds it, that
-// one's sixteenth, and so on.
+// The source's index that the target falls on. A long place is first cut to its sixteenth
+// that holds the target; then every lane takes up to kLaneMost consecutive values, and the
+// wave whose values hold it finds the lane and the value.
 template <class Src, bool CAP>
-__device__ __forceinline__ int64_t descend(const Src& src, Place at, Shared& sm, const Weights<CAP>& wt,
-                                           const Kept& s, float uniform, uint64_t& total,
-                                           uint64_t target) {
+__device__ __forceinline__ int64_t descend(const Src& src, Place at, Shared& sm,
+                                           const Weights<CAP>& wt, const Kept& s, float uniform,
+                                           uint64_t& total, uint64_t target) {
   constexpr int E = Src::E;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const uint64_t w_tau = s.tau ? wt.kept(key_value(s.tau)) : 0;
-  while (at.len > 64 || total == 0) {
+  auto put = [&](uint64_t sum, uint64_t ties) {
+    if (lane == 0) {
+      sm.wave_sum[wave] = sum;
+      sm.wave_cnt[wave] = uint32_t(ties);
+    }
+  };
+  while (at.len > kThreads * kLaneMost) {
     const int64_t part = (((at.len + kWaves - 1) / kWaves) + E - 1) / E * E;
     const int64_t from = at.lo + wave * part, end = at.lo + at.len;
     uint64_t sum = 0;
@@ -365,25 +404,54 @@ __device__ __forceinline__ int64_t descend(const Src& src, Place at, Shared& sm,
         if (key > s.tau) sum += wt.kept(z);
         else if (key == s.tau) ++ties;
       });
-    sum = wave_sum(sum);
-    ties = uint32_t(wave_sum(ties));
-    if (lane == 0) {
-      sm.wave_sum[wave] = sum;
-      sm.wave_cnt[wave] = ties;
-    }
+    put(wave_sum64(sum), wave_sum64(ties));
     enter(at, part, sm, s, w_tau, uniform, total, target);
   }
-  if (wave == 0) {
-    const bool in = lane < at.len;
-    const float z = in ? src.at(at.lo + lane) : 0.f;
-    const uint32_t key = order_key(z);
-    const uint64_t a = at.sum + wave_scan(in && key > s.tau ? wt.kept(z) : 0, lane);
-    const uint64_t t = at.ties + wave_scan(in && key == s.tau ? 1 : 0, lane);
-    const uint64_t hit = __ballot(in && target < a + (t < s.m ? t : s.m) * w_tau);
-    if (lane == 0) sm.found = hit ? __builtin_ctzll(hit) : 0;
+  const int64_t per = ((at.len + kThreads - 1) / kThreads + E - 1) / E * E;
+  const int64_t end = at.lo + at.len, lo = at.lo + threadIdx.x * per;
+  const int64_t hi = lo + per < end ? lo + per : end;
+  uint64_t mass[kLaneMost], sum = 0;
+  uint32_t equal = 0;
+#pragma unroll
+  for (int j = 0; j < kLaneMost; ++j) mass[j] = 0;
+  if (lo < hi)
+    src.lane_values(lo, hi, [&](int j, float z, int64_t i) {
+      const uint32_t key = order_key(z);
+      const int at_j = int(i - lo);
+      if (key == s.tau) equal |= 1u << at_j;
+      const uint64_t w = key > s.tau ? wt.kept(z) : 0;
+      sum += w;
+#pragma unroll
+      for (int q = 0; q < kLaneMost; ++q)
+        if (q == at_j) mass[q] = w;
+    });
+  const uint64_t own_ties = __popc(equal);
+  uint64_t sums = wave_scan64(sum), ties = wave_scan64(own_ties);
+  put(from_lane64(sums, 63), from_lane64(ties, 63));
+  const int part_of = enter(at, 64 * per, sm, s, w_tau, uniform, total, target);
+  if (wave == part_of) {
+    auto mass_at = [&](uint64_t a, uint64_t c) { return a + (c < s.m ? c : s.m) * w_tau; };
+    sums += at.sum;
+    ties += at.ties;
+    const uint64_t hit = __ballot(target < mass_at(sums, ties));
+    if (lane == (hit ? __builtin_ctzll(hit) : 63)) {
+      uint64_t a = sums - sum, c = ties - own_ties;
+      uint32_t found = 0;
+      bool done = false;
+#pragma unroll
+      for (int j = 0; j < kLaneMost; ++j) {
+        a += mass[j];
+        c += (equal >> j) & 1;
+        if (!done && target < mass_at(a, c)) {
+          found = j;
+          done = true;
+        }
+      }
+      sm.found = uint32_t(lo + found);
+    }
   }
   __syncthreads();
-  return at.lo + sm.found;
+  return sm.found;
 }
 
 // The list's index for a list of up to kSmallList that holds the first k ranks: each thread
@@ -403,6 +471,7 @@ __device__ __forceinline__ int64_t small_list(Shared& sm, int n, const Weights<C
   if (wave * 64 < n) {
     const uint32_t key = tid < n ? sm.key[tid] : 0;
     int rank = 0;
+#pragma unroll 8
     for (int j = 0; j < n; ++j) {
       const uint32_t o = sm.key[j];
       const bool better = o > key || (o == key && j < tid);
@@ -425,13 +494,13 @@ __device__ __forceinline__ int64_t small_list(Shared& sm, int n, const Weights<C
   };
   uint64_t before;
   if (p < 1.0) {
-    const uint64_t all = block_sum(wave_scan(keep ? own : 0, lane), before);
+    const uint64_t all = block_sum(wave_scan64(keep ? own : 0), before);
     const double r = __builtin_ceil(p * double(all));
     const uint64_t limit = r >= double(all) ? all : r >= 1.0 ? uint64_t(r) : 1;
     keep = keep && above < limit;
   }
   keep = keep && exp2_neg(lw) >= wt.min_p;
-  const uint64_t incl = wave_scan(keep ? own : 0, lane);
+  const uint64_t incl = wave_scan64(keep ? own : 0);
   total = block_sum(incl, before);
   const uint64_t target = target_of(uniform, total);
   const uint64_t upto = before + incl;
@@ -453,11 +522,11 @@ __device__ __forceinline__ int collect(const Row<T>& row, int64_t seg, Shared& s
   uint32_t* idx = sm.idx + wave * kWaveList;
   int have = 0;
   if (from < to)
-    row.chunks(from, to, lane, 64, [&](const float (&v)[E], int64_t c, int n) {
+    row.template chunks<4>(from, to, lane, 64, [&](const float (&v)[E], int64_t c, int e0) {
       uint32_t mine = 0;
 #pragma unroll
       for (int e = 0; e < E; ++e)
-        if (e < n && take(v[e])) mine |= 1u << e;
+        if (e >= e0 && take(v[e])) mine |= 1u << e;
       if (__ballot(mine != 0) == 0) return;
       int before = 0, all = 0;
 #pragma unroll
@@ -507,6 +576,39 @@ __device__ __forceinline__ int collect(const Row<T>& row, int64_t seg, Shared& s
   return n;
 }
 
+// The same in any order within a wave's place, which keep their gaps: wave w's are
+// sm.wave_cnt[w] from w kWaveList on. False if a wave found more than its place holds.
+template <class T, class Take>
+__device__ __forceinline__ bool gather(const Row<T>& row, int64_t seg, Shared& sm, Take take) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t from = wave * seg, to = from + seg < row.n ? from + seg : row.n;
+  if (lane == 0) sm.wave_cnt[wave] = 0;
+  if (from < to)
+    row.template each<8>(from, to, lane, 64, [&](float z, int64_t) {
+      if (take(z)) {
+        const uint32_t at = atomicAdd(&sm.wave_cnt[wave], 1u);
+        if (at < kWaveList) sm.key[wave * kWaveList + at] = order_key(z);
+      }
+    });
+  __syncthreads();
+  bool fits = true;
+#pragma unroll
+  for (int i = 0; i < kWaves; ++i) fits = fits && sm.wave_cnt[i] <= uint32_t(kWaveList);
+  return fits;
+}
+
+// What gather() left, as a source without an order.
+struct Gathered {
+  const Shared& sm;
+  int64_t n;
+  template <class F>
+  __device__ __forceinline__ void each(int64_t, int64_t, int t, int, F f) const {
+    const int lane = t & 63, wave = t >> 6;
+    for (uint32_t i = lane; i < sm.wave_cnt[wave]; i += 64)
+      f(key_value(sm.key[wave * kWaveList + i]), int64_t(0));
+  }
+};
+
 // A key that at least k of the threads' maxima reach (0 if fewer have one): the k-th
 // largest's upper 22 bits.
 __device__ __forceinline__ uint32_t bound_of_maxima(uint32_t own, int64_t k, Shared& sm) {
@@ -545,7 +647,7 @@ __global__ __launch_bounds__(kThreads) void k_sample(SampleArgs a) {
   float most = -INFINITY;
   bool nan = false;
   if (from < to)
-    row.each(from, to, lane, 64, [&](float z, int64_t) {
+    row.template each<8>(from, to, lane, 64, [&](float z, int64_t) {
       nan |= z != z;
       most = fmaxf(most, z);
     });
@@ -648,7 +750,7 @@ __global__ __launch_bounds__(kThreads) void k_sample(SampleArgs a) {
     uint64_t mine = 0;
     if (tid < kMassBins)
       for (int i = 0; i < kWaves; ++i) mine += sm.mass[i][tid];
-    const uint64_t incl = wave_scan(mine, lane);
+    const uint64_t incl = wave_scan64(mine);
     if (lane == 63) sm.wave_sum[wave] = incl;
     __syncthreads();
     uint64_t before = 0, all = 0;
@@ -685,29 +787,43 @@ __global__ __launch_bounds__(kThreads) void k_sample(SampleArgs a) {
       uint64_t sum = 0;
       if (clean) {
         for (int i = lane; i < bin; i += 64) sum += sm.mass[wave][i];
-        sum = wave_sum(sum);
+        sum = wave_sum64(sum);
       }
-      n = clean ? collect(row, seg, sm, [&](float z) {
-        return bin_of(wt.log_weight(z)) == bin;
-      }) : -1;
-      if (n >= 0) {
-        const List list{sm.key, n};
+      if (clean && gather(row, seg, sm, [&](float z) { return bin_of(wt.log_weight(z)) == bin; })) {
+        const Gathered in_bin{sm, 0};
+        uint32_t least = ~0u, most = 0;
+        in_bin.each(0, 0, tid, kThreads, [&](float z, int64_t) {
+          least = MinOp()(least, order_key(z));
+          most = MaxOp()(most, order_key(z));
+        });
+        least = wave_all(least, MinOp());
+        most = wave_all(most, MaxOp());
+        if (lane == 0) sm.wave_sum[wave] = uint64_t(most) << 32 | least;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kWaves; ++i) {
+          least = MinOp()(least, uint32_t(sm.wave_sum[i]));
+          most = MaxOp()(most, uint32_t(sm.wave_sum[i] >> 32));
+        }
+        const int differ = 32 - __builtin_clz((least ^ most) | 1u);
         Kept s;
         uint64_t above, goal = limit - above_bin;
-        s.tau = select_key(list, sm, goal, 0.0, false, above, 0u, 0ull,
-                           [&](float z, uint32_t) { return wt.mass(z); });
+        s.tau = select_key(in_bin, sm, goal, 0.0, false, above, 0u, 0ull,
+                           [&](float z, uint32_t) { return wt.mass(z); }, differ,
+                           differ < 32 ? most >> differ << differ : 0u);
         const uint64_t w = wt.mass(key_value(s.tau));
         s.m = (goal - above + w - 1) / w;
         // the kept mass and ties of each segment
         uint64_t in = 0;
         uint32_t ties = 0;
-        for (int i = lane; i < n; i += 64) {
-          if (int64_t(sm.idx[i]) < from || int64_t(sm.idx[i]) >= to) continue;
-          if (sm.key[i] > s.tau) in += wt.mass(key_value(sm.key[i]));
-          else if (sm.key[i] == s.tau) ++ties;
-        }
-        in = wave_sum(in) + sum;
-        ties = uint32_t(wave_sum(ties));
+        in_bin.each(0, 0, tid, kThreads, [&](float z, int64_t) {
+          const uint32_t key = order_key(z);
+          if (key > s.tau) in += wt.mass(z);
+          else if (key == s.tau) ++ties;
+        });
+        in = wave_sum64(in) + sum;
+        ties = uint32_t(wave_sum64(ties));
+        __syncthreads();                           // the counts are read
         if (lane == 0) {
           sm.wave_sum[wave] = in;
           sm.wave_cnt[wave] = ties;

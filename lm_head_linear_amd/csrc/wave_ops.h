@@ -67,6 +67,39 @@ __device__ __forceinline__ T wave_all(T x, Op op) {
   return rows_all(group_all<16>(x, op), op);
 }
 
+constexpr int kDppUp = 0x110;        // + n: from the lane n before, 0 before the 16
+constexpr int kDppLast16 = 0x142, kDppLast32 = 0x143;   // a row's (half's) last lane, to the next
+
+// dpp_move of both halves; rows of 16 lanes that are not in ROWS get 0.
+template <int CTRL, int ROWS = 0xf>
+__device__ __forceinline__ uint64_t dpp_move64(uint64_t x) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, int(uint32_t(x)), CTRL, ROWS, 0xf, false);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, int(uint32_t(x >> 32)), CTRL, ROWS, 0xf, false);
+  return uint64_t(hi) << 32 | lo;
+#else
+  return x;
+#endif
+}
+
+// Sum over the lanes of the wave up to this one.
+__device__ __forceinline__ uint64_t wave_scan64(uint64_t x) {
+  x += dpp_move64<kDppUp + 1>(x);
+  x += dpp_move64<kDppUp + 2>(x);
+  x += dpp_move64<kDppUp + 4>(x);
+  x += dpp_move64<kDppUp + 8>(x);
+  x += dpp_move64<kDppLast16, 0xa>(x);
+  x += dpp_move64<kDppLast32, 0xc>(x);
+  return x;
+}
+// Lane l's value, in every lane.
+__device__ __forceinline__ uint64_t from_lane64(uint64_t x, int l) {
+  const uint32_t lo = __builtin_amdgcn_readlane(uint32_t(x), l);
+  const uint32_t hi = __builtin_amdgcn_readlane(uint32_t(x >> 32), l);
+  return uint64_t(hi) << 32 | lo;
+}
+__device__ __forceinline__ uint64_t wave_sum64(uint64_t x) { return from_lane64(wave_scan64(x), 63); }
+
 struct AddOp {
   template <class T>
   __device__ __forceinline__ T operator()(T a, T b) const { return a + b; }
