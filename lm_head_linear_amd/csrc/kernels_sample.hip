@@ -108,8 +108,8 @@ struct Weights {
   }
   // ... after min-p
   __device__ __forceinline__ uint64_t kept(float z) const {
-    const double t = log_weight(z);
-    return exp2_neg(t) >= min_p ? fixed_of(t) : 0;
+    const double w = weight(z);
+    return w >= min_p ? whole(__builtin_ldexp(w, S)) : 0;
   }
 };
 
@@ -126,7 +126,7 @@ struct Shared {
 };
 
 // A row in memory.
-constexpr int kLaneMost = 8;                       // values a lane reads at once (lane_values)
+constexpr int kLaneMost = 8;                       // values of a lane in descend()
 template <class T>
 struct Row {
   static constexpr int E = kPerChunk<T>;
@@ -141,69 +141,52 @@ struct Row {
     unpack_chunk<T>(load_raw(p + i), v);
     return c - i < E ? int(c - i) : E;
   }
-  // f(a chunk's values, index of the first, the first that counts) for the chunks of [lo, hi)
-  // that lane t of `count` takes, U loads under way at once; lo is a multiple of E.
-  template <int U, class F>
-  __device__ __forceinline__ void chunks(int64_t lo, int64_t hi, int t, int count, F f) const {
+  // f(u, values, index of the first, the first that counts) for the chunks u = 0 .. U - 1 of
+  // each turn that lane t of `count` takes of [lo, hi), all under way at once, and end() behind
+  // every turn; lo is a multiple of E. What whole turns leave goes chunk by chunk.
+  template <int U, class F, class End>
+  __device__ __forceinline__ void turns(int64_t lo, int64_t hi, int t, int count, F f,
+                                        End end) const {
     const int64_t step = int64_t(count) * E;
-    int64_t c = lo + int64_t(t) * E, base = lo;
-    for (; base + U * step <= hi; base += U * step, c += U * step) {
+    if (hi < E) {                                  // fewer values than a chunk: -inf behind them
+      float v[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] = e < hi ? at(e) : -INFINITY;
+      f(0, v, int64_t(0), lo == 0 && t == 0 ? 0 : E);
+      end();
+      return;
+    }
+    int64_t base = lo;
+    const T* q = p + lo + int64_t(t) * E;
+#pragma unroll 1
+    for (; base + U * step <= hi; base += U * step, q += U * step) {
       row_u32x4 raw[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) raw[u] = load_raw(p + c + u * step);
+      for (int u = 0; u < U; ++u) raw[u] = load_raw(q + u * step);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         float v[E];
         unpack_chunk<T>(raw[u], v);
-        f(v, c + u * step, 0);
+        f(u, v, base + (u * count + t) * int64_t(E), 0);
       }
+      end();
     }
-    if (hi < E) {                                  // fewer values than a chunk
-      if (base >= hi) return;
+#pragma unroll 1
+    for (; base < hi; base += step) {
       float v[E];
-      load_chunk(p, c, hi, v);
-#pragma unroll
-      for (int e = 0; e < E; ++e)                  // the last one to the end: [0, hi) at e0 = 0
-        if (e >= hi) v[e] = -INFINITY;
-      f(v, c, c < hi ? 0 : E);
-      return;
-    }
-    constexpr int H = U / 2;
-    for (; base < hi; base += H * step, c += H * step) {
-      float v[H][E];
-      int64_t i[H];
-      int e0[H];
-#pragma unroll
-      for (int u = 0; u < H; ++u) e0[u] = chunk(c + u * step, hi, v[u], i[u]);
-#pragma unroll
-      for (int u = 0; u < H; ++u) f(v[u], i[u], e0[u]);
+      int64_t i;
+      const int e0 = chunk(base + t * int64_t(E), hi, v, i);
+      f(0, v, i, e0);
+      end();
     }
   }
   template <int U = 4, class F>
   __device__ __forceinline__ void each(int64_t lo, int64_t hi, int t, int count, F f) const {
-    chunks<U>(lo, hi, t, count, [&](const float (&v)[E], int64_t i, int e0) {
+    turns<U>(lo, hi, t, count, [&](int, const float (&v)[E], int64_t i, int e0) {
 #pragma unroll
       for (int e = 0; e < E; ++e)
         if (e >= e0) f(v[e], i + e);
-    });
-  }
-  // f(j, z, i) for the values j of [lo, hi), at most kLaneMost of them; lo is a multiple of E.
-  template <class F>
-  __device__ __forceinline__ void lane_values(int64_t lo, int64_t hi, F f) const {
-    constexpr int C = kLaneMost / E;
-    if (n < E) {
-      for (int j = 0; j < hi - lo; ++j) f(j, at(lo + j), lo + j);
-      return;
-    }
-    float v[C][E];
-    int64_t i[C];
-#pragma unroll
-    for (int u = 0; u < C; ++u) chunk(lo + u * E, n, v[u], i[u]);
-#pragma unroll
-    for (int u = 0; u < C; ++u)
-#pragma unroll
-      for (int e = 0; e < E; ++e)
-        if (i[u] + e >= lo + u * E && i[u] + e < hi) f(u * E + e, v[u][e], i[u] + e);
+    }, [] {});
   }
 };
 
@@ -217,13 +200,15 @@ struct List {
   __device__ __forceinline__ void each(int64_t lo, int64_t hi, int t, int count, F f) const {
     for (int64_t i = lo + t; i < hi; i += count) f(key_value(key[i]), i);
   }
-  template <class F>
-  __device__ __forceinline__ void lane_values(int64_t lo, int64_t hi, F f) const {
-#pragma unroll
-    for (int j = 0; j < kLaneMost; ++j)
-      if (lo + j < hi) f(j, key_value(key[lo + j]), lo + j);
-  }
 };
+
+// The sum of the waves' sm.wave_sum before wave w, and of all.
+__device__ __forceinline__ uint64_t before_wave(const Shared& sm, int w, uint64_t& total) {
+  const int lane = threadIdx.x & 63;
+  const uint64_t v = lane < kWaves ? sm.wave_sum[lane] : 0, s = wave_scan64(v);
+  total = from_lane64(s, kWaves - 1);
+  return from_lane64(s - v, __builtin_amdgcn_readfirstlane(w));
+}
 
 // With the histogram's bins, highest first, summed up: the bin in which the sum passes
 // `target` (above < target <= above + bin; target 1 .. total), in sm.bin, sm.above. If
@@ -238,12 +223,8 @@ __device__ __forceinline__ uint64_t find_bin(Shared& sm, uint64_t target, double
   const uint64_t incl = wave_scan64(sum);
   if (lane == 63) sm.wave_sum[w] = incl;
   __syncthreads();
-  uint64_t before = 0, total = 0;
-#pragma unroll
-  for (int i = 0; i < kWaves; ++i) {
-    if (i < w) before += sm.wave_sum[i];
-    total += sm.wave_sum[i];
-  }
+  uint64_t total;
+  const uint64_t before = before_wave(sm, w, total);
   if (share) {
     const double r = __builtin_ceil(p * double(total));
     target = r >= double(total) ? total : r >= 1.0 ? uint64_t(r) : 1;
@@ -350,27 +331,19 @@ __device__ __forceinline__ int enter(Place& at, int64_t part, Shared& sm, const 
                                      uint64_t& target) {
   auto mass_at = [&](uint64_t sum, uint64_t ties) { return sum + (ties < s.m ? ties : s.m) * w_tau; };
   __syncthreads();
-  uint64_t a[kWaves + 1], c[kWaves + 1];           // before part i
-  a[0] = at.sum;
-  c[0] = at.ties;
-#pragma unroll
-  for (int i = 0; i < kWaves; ++i) {
-    a[i + 1] = a[i] + sm.wave_sum[i];
-    c[i + 1] = c[i] + sm.wave_cnt[i];
-  }
+  // lane i: up to and with part i
+  const int lane = threadIdx.x & 63;
+  const uint64_t a0 = lane < kWaves ? sm.wave_sum[lane] : 0, c0 = lane < kWaves ? sm.wave_cnt[lane] : 0;
+  const uint64_t a = at.sum + wave_scan64(a0), c = at.ties + wave_scan64(c0);
   __syncthreads();
   if (total == 0) {
-    total = mass_at(a[kWaves], c[kWaves]);
+    total = from_lane64(mass_at(a, c), 63);
     target = target_of(uniform, total);
   }
-  int part_of = 0;                                 // parts that end at or before the target
-#pragma unroll
-  for (int i = 1; i < kWaves; ++i)
-    if (mass_at(a[i], c[i]) <= target) {
-      part_of = i;
-      at.sum = a[i];
-      at.ties = c[i];
-    }
+  const uint64_t past = __ballot(lane < kWaves && mass_at(a, c) <= target);
+  const int part_of = __popcll(past) < kWaves ? __popcll(past) : kWaves - 1;
+  at.sum = from_lane64(a - a0, part_of);
+  at.ties = from_lane64(c - c0, part_of);
   at.lo += part_of * part;
   at.len -= part_of * part;
   if (at.len > part) at.len = part;
@@ -410,22 +383,14 @@ __device__ __forceinline__ int64_t descend(const Src& src, Place at, Shared& sm,
   const int64_t per = ((at.len + kThreads - 1) / kThreads + E - 1) / E * E;
   const int64_t end = at.lo + at.len, lo = at.lo + threadIdx.x * per;
   const int64_t hi = lo + per < end ? lo + per : end;
-  uint64_t mass[kLaneMost], sum = 0;
-  uint32_t equal = 0;
-#pragma unroll
-  for (int j = 0; j < kLaneMost; ++j) mass[j] = 0;
-  if (lo < hi)
-    src.lane_values(lo, hi, [&](int j, float z, int64_t i) {
-      const uint32_t key = order_key(z);
-      const int at_j = int(i - lo);
-      if (key == s.tau) equal |= 1u << at_j;
-      const uint64_t w = key > s.tau ? wt.kept(z) : 0;
-      sum += w;
-#pragma unroll
-      for (int q = 0; q < kLaneMost; ++q)
-        if (q == at_j) mass[q] = w;
-    });
-  const uint64_t own_ties = __popc(equal);
+  uint64_t sum = 0, own_ties = 0;
+#pragma unroll 1
+  for (int64_t i = lo; i < hi; ++i) {
+    const float z = src.at(i);
+    const uint32_t key = order_key(z);
+    if (key > s.tau) sum += wt.kept(z);
+    else if (key == s.tau) ++own_ties;
+  }
   uint64_t sums = wave_scan64(sum), ties = wave_scan64(own_ties);
   put(from_lane64(sums, 63), from_lane64(ties, 63));
   const int part_of = enter(at, 64 * per, sm, s, w_tau, uniform, total, target);
@@ -436,18 +401,16 @@ __device__ __forceinline__ int64_t descend(const Src& src, Place at, Shared& sm,
     const uint64_t hit = __ballot(target < mass_at(sums, ties));
     if (lane == (hit ? __builtin_ctzll(hit) : 63)) {
       uint64_t a = sums - sum, c = ties - own_ties;
-      uint32_t found = 0;
-      bool done = false;
-#pragma unroll
-      for (int j = 0; j < kLaneMost; ++j) {
-        a += mass[j];
-        c += (equal >> j) & 1;
-        if (!done && target < mass_at(a, c)) {
-          found = j;
-          done = true;
-        }
+      int64_t i = lo;
+#pragma unroll 1
+      for (; i < hi - 1; ++i) {
+        const float z = src.at(i);
+        const uint32_t key = order_key(z);
+        if (key > s.tau) a += wt.kept(z);
+        else if (key == s.tau) ++c;
+        if (target < mass_at(a, c)) break;
       }
-      sm.found = uint32_t(lo + found);
+      sm.found = uint32_t(i);
     }
   }
   __syncthreads();
@@ -480,15 +443,11 @@ __device__ __forceinline__ int64_t small_list(Shared& sm, int n, const Weights<C
     }
     keep = keep && rank < k;
   }
-  auto block_sum = [&](uint64_t v, uint64_t& before) {      // of waves 0 .. 3, which hold n
-    if (lane == 63 && wave < kSmallList / 64) sm.wave_sum[wave] = v;
+  auto block_sum = [&](uint64_t v, uint64_t& before) {      // v: sums along each wave
+    if (lane == 63) sm.wave_sum[wave] = v;
     __syncthreads();
-    uint64_t all = 0;
-    before = 0;
-    for (int i = 0; i < kSmallList / 64; ++i) {
-      if (i < wave) before += sm.wave_sum[i];
-      all += sm.wave_sum[i];
-    }
+    uint64_t all;
+    before = before_wave(sm, wave, all);
     __syncthreads();
     return all;
   };
@@ -518,62 +477,56 @@ __device__ __forceinline__ int collect(const Row<T>& row, int64_t seg, Shared& s
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t from = wave * seg, to = from + seg < row.n ? from + seg : row.n;
   const uint64_t below = (1ull << lane) - 1;
-  uint32_t* key = sm.key + wave * kWaveList;
   uint32_t* idx = sm.idx + wave * kWaveList;
+  constexpr int U = 32 / E;                        // a bit a value
   int have = 0;
+  uint32_t mine = 0;
+  int64_t at[U];
   if (from < to)
-    row.template chunks<4>(from, to, lane, 64, [&](const float (&v)[E], int64_t c, int e0) {
-      uint32_t mine = 0;
+    row.template turns<U>(from, to, lane, 64, [&](int u, const float (&v)[E], int64_t i, int e0) {
+      at[u] = i;
 #pragma unroll
       for (int e = 0; e < E; ++e)
-        if (e >= e0 && take(v[e])) mine |= 1u << e;
-      if (__ballot(mine != 0) == 0) return;
-      int before = 0, all = 0;
+        if (e >= e0 && take(v[e])) mine |= 1u << (u * E + e);
+    }, [&] {
+      if (__ballot(mine != 0) != 0) {
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const uint64_t b = __ballot((mine >> e) & 1);
-        before += __popcll(b & below);
-        all += __popcll(b);
-      }
-      int at = have + before;
-#pragma unroll
-      for (int e = 0; e < E; ++e)
-        if ((mine >> e) & 1) {
-          if (at < kWaveList) {
-            key[at] = order_key(v[e]);
-            idx[at] = uint32_t(c + e);
+        for (int u = 0; u < U; ++u) {
+          uint32_t m = (mine >> (u * E)) & ((1u << E) - 1);
+          if (__ballot(m != 0) == 0) continue;
+          int before = 0, all = 0;
+#pragma unroll 1
+          for (int e = 0; e < E; ++e) {
+            const uint64_t b = __ballot((m >> e) & 1);
+            before += __popcll(b & below);
+            all += __popcll(b);
           }
-          ++at;
+          for (int to_ = have + before; m != 0; m &= m - 1, ++to_)
+            if (to_ < kWaveList) idx[to_] = uint32_t(at[u] + __builtin_ctz(m));
+          have += all;
         }
-      have += all;
+        mine = 0;
+      }
     });
-  if (lane == 0) sm.wave_cnt[wave] = have;
+  if (lane == 0) sm.wave_sum[wave] = uint64_t(have);
   __syncthreads();
-  int n = 0, start = 0;
-  bool fits = true;
-  for (int i = 0; i < kWaves; ++i) {
-    const int c = sm.wave_cnt[i];
-    if (i < wave) start += c;
-    fits = fits && c <= kWaveList;
-    n += c;
-  }
+  uint64_t n;
+  const int start = int(before_wave(sm, wave, n));
+  const bool fits = __ballot(lane < kWaves && sm.wave_sum[lane & (kWaves - 1)] > kWaveList) == 0;
   // close the gaps: every wave reads its place before any writes
-  uint32_t k[kWaveList / 64], x[kWaveList / 64];
+  uint32_t x[kWaveList / 64];
 #pragma unroll
-  for (int i = 0; i < kWaveList / 64; ++i) {
-    k[i] = key[i * 64 + lane];
-    x[i] = idx[i * 64 + lane];
-  }
+  for (int i = 0; i < kWaveList / 64; ++i) x[i] = idx[i * 64 + lane];
   __syncthreads();
   if (!fits) return -1;
 #pragma unroll
   for (int i = 0; i < kWaveList / 64; ++i)
     if (i * 64 + lane < have) {
-      sm.key[start + i * 64 + lane] = k[i];
       sm.idx[start + i * 64 + lane] = x[i];
+      sm.key[start + i * 64 + lane] = order_key(row.at(x[i]));
     }
   __syncthreads();
-  return n;
+  return int(n);
 }
 
 // The same in any order within a wave's place, which keep their gaps: wave w's are
@@ -591,10 +544,7 @@ __device__ __forceinline__ bool gather(const Row<T>& row, int64_t seg, Shared& s
       }
     });
   __syncthreads();
-  bool fits = true;
-#pragma unroll
-  for (int i = 0; i < kWaves; ++i) fits = fits && sm.wave_cnt[i] <= uint32_t(kWaveList);
-  return fits;
+  return __ballot(sm.wave_cnt[lane & (kWaves - 1)] > uint32_t(kWaveList)) == 0;
 }
 
 // What gather() left, as a source without an order.
@@ -647,10 +597,14 @@ __global__ __launch_bounds__(kThreads) void k_sample(SampleArgs a) {
   float most = -INFINITY;
   bool nan = false;
   if (from < to)
-    row.template each<8>(from, to, lane, 64, [&](float z, int64_t) {
-      nan |= z != z;
-      most = fmaxf(most, z);
-    });
+    row.template turns<8>(from, to, lane, 64, [&](int, const float (&v)[E], int64_t, int e0) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        nan |= v[e] != v[e];
+        // each value in one thread's maximum: bound_of_maxima counts them
+        most = fmaxf(most, e >= e0 ? v[e] : -INFINITY);
+      }
+    }, [] {});
   const uint32_t own = order_key(most);            // key of -inf: nothing
   uint32_t best = wave_all(own, MaxOp());
   const uint64_t any_nan = __ballot(nan);
@@ -659,13 +613,8 @@ __global__ __launch_bounds__(kThreads) void k_sample(SampleArgs a) {
     sm.wave_sum[wave] = any_nan;
   }
   __syncthreads();
-  best = 0;
-  nan = false;
-#pragma unroll
-  for (int i = 0; i < kWaves; ++i) {
-    best = MaxOp()(best, sm.wave_cnt[i]);
-    nan |= sm.wave_sum[i] != 0;
-  }
+  best = wave_all(sm.wave_cnt[lane & (kWaves - 1)], MaxOp());
+  nan = __ballot(sm.wave_sum[lane & (kWaves - 1)] != 0) != 0;
   __syncthreads();                                 // read before they are written again
   if (nan || best <= kKeyNegInf) {
     if (tid == 0) {
@@ -704,7 +653,7 @@ __global__ __launch_bounds__(kThreads) void k_sample(SampleArgs a) {
     }
     __syncthreads();
     uint32_t first = sm.idx[lane];
-#pragma unroll
+#pragma unroll 1
     for (int i = 1; i < kWaves; ++i) first = MinOp()(first, sm.idx[i * 64 + lane]);
     token = wave_all(first, MinOp());
     total = 1ull << wt.S;
@@ -753,11 +702,8 @@ __global__ __launch_bounds__(kThreads) void k_sample(SampleArgs a) {
     const uint64_t incl = wave_scan64(mine);
     if (lane == 63) sm.wave_sum[wave] = incl;
     __syncthreads();
-    uint64_t before = 0, all = 0;
-    for (int i = 0; i < kMassBins / 64; ++i) {
-      if (i < wave) before += sm.wave_sum[i];
-      all += sm.wave_sum[i];
-    }
+    uint64_t all;
+    const uint64_t before = before_wave(sm, wave, all);
     const double share = __builtin_ceil(p * double(all));
     const uint64_t limit = share >= double(all) ? all : share >= 1.0 ? uint64_t(share) : 1;
     const uint64_t upto = before + incl;
@@ -800,11 +746,9 @@ __global__ __launch_bounds__(kThreads) void k_sample(SampleArgs a) {
         most = wave_all(most, MaxOp());
         if (lane == 0) sm.wave_sum[wave] = uint64_t(most) << 32 | least;
         __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kWaves; ++i) {
-          least = MinOp()(least, uint32_t(sm.wave_sum[i]));
-          most = MaxOp()(most, uint32_t(sm.wave_sum[i] >> 32));
-        }
+        const uint64_t ends = sm.wave_sum[lane & (kWaves - 1)];
+        least = wave_all(uint32_t(ends), MinOp());
+        most = wave_all(uint32_t(ends >> 32), MaxOp());
         const int differ = 32 - __builtin_clz((least ^ most) | 1u);
         Kept s;
         uint64_t above, goal = limit - above_bin;
