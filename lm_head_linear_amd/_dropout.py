@@ -27,17 +27,19 @@ class DropoutMask(NamedTuple):
     step: Optional[torch.Tensor] = None
 
 
+_U64 = (1 << 64) - 1
+
+
 def _mask_args(where, dev, p, seed, offset, step):
-    p = float(p)
     if not 0.0 <= p < 1.0:
         raise ValueError(f"{where}: p must be in [0, 1), got {p}")
-    for name, v in (("seed", seed), ("offset", offset)):
-        if not 0 <= int(v) < 1 << 64:
-            raise ValueError(f"{where}: {name} must be in [0, 2^64), got {v}")
-    if step is not None:
-        if step.dtype != torch.int64 or step.numel() != 1 or step.device != dev:
-            raise ValueError(f"{where}: step must be one int64 on {dev}")
-    return p, int(seed), int(offset), _ptr(step)
+    if not (0 <= seed <= _U64 and 0 <= offset <= _U64):
+        raise ValueError(f"{where}: seed and offset must be in [0, 2^64), got {seed}, {offset}")
+    if step is None:
+        return p, seed, offset, None
+    if step.dtype != torch.int64 or step.numel() != 1 or step.device != dev:
+        raise ValueError(f"{where}: step must be one int64 on {dev}")
+    return p, seed, offset, step.data_ptr()
 
 
 def _mat(name, t, N, H, dt, dev):
@@ -73,7 +75,10 @@ def flce_dropout(x: torch.Tensor, residual: Optional[torch.Tensor] = None, *, p:
     mask = _mask_args("flce_dropout", dev, p, seed, offset, step)
     ld_x = _rows("x", x, N, H, dt, dev)
     ld_r = H if residual is None else _rows("residual", residual, N, H, dt, dev)
-    out, ld_o = _mat("out", out, N, H, dt, dev)
+    if out is None:
+        out, ld_o = torch.empty(N, H, dtype=dt, device=dev), H
+    else:
+        ld_o = _rows("out", out, N, H, dt, dev)
     _run("flce_dropout", dev, _lib.load().flce_dropout, x.data_ptr(), ld_x, _ptr(residual), ld_r,
          N, H, *mask, out.data_ptr(), ld_o, _stream(dev), code)
     return out

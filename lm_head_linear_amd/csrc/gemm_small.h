@@ -1,6 +1,7 @@
 // A matrix product on CDNA4 matrix cores (gfx950) for rows of any length, stride and
 // alignment, bf16 or float32: C[m][n] = sum_k B(m, k) A(n, k) in float32, tiles of TS x TS
-// (128, or 64 where those leave CUs without work). The head's product (gemm_bf16.h) takes 256 x 256 tiles of aligned bf16 rows; this
+// (128, or 64 where those leave CUs without work, and 32 of float32, whose matrix
+// instruction is sixteen times slower than its loads are short). The head's product (gemm_bf16.h) takes 256 x 256 tiles of aligned bf16 rows; this
 // one serves what that does not: float32, odd rows, and outputs of too few such tiles.
 //
 // A's rows are C's columns, so that a lane of the matrix instruction's result holds four
@@ -48,6 +49,13 @@ struct Operand {
 // fragment read lie in different banks.
 __device__ __forceinline__ int lds_n(int r, int c) { return (r * 8 + (c ^ ((r >> 1) & 7))) * 16; }
 // LDS byte of columns [col, col + 16 / sizeof(T)) of k-row k, form T.
+// (row_t: the place of k-row k, its own inverse.)
+template <class T, int TS>
+__device__ __forceinline__ int row_t(int k) {
+  // rows of 128 bytes of float32 lie two to the banks' window: the upper eight trade places
+  // with their neighbours
+  return sizeof(T) == 4 && TS == 32 ? k ^ ((k >> 3) & 1) : k;
+}
 template <class T, int TS>
 __device__ __forceinline__ int lds_t(int k, int col) {
   if constexpr (sizeof(T) == 2) {
@@ -58,7 +66,7 @@ __device__ __forceinline__ int lds_t(int k, int col) {
     return (k * (TS / 8) + ((col >> 3) ^ swz)) * 16 + ((col >> 2) & 1) * 8;
   } else {
     // a fragment read takes 16 columns of four k-rows 4 apart: 16 banks each
-    return k * (TS * 4) + (col ^ (((k >> 2) & 3) << 4)) * 4;
+    return row_t<T, TS>(k) * (TS * 4) + (col ^ (((k >> 2) & (TS == 32 ? 1 : 3)) << 4)) * 4;
   }
 }
 
@@ -84,7 +92,7 @@ struct Loads {
         at[i] = o.p + r * o.ld + k[i];
       } else {
         constexpr int kPerRow = TS / E;
-        k[i] = id / kPerRow;
+        k[i] = row_t<T, TS>(id / kPerRow);
         row[i] = ((lds_t<T, TS>(k[i], (id % kPerRow) * E) >> 4) % kPerRow) * E;
         const int64_t c = r0 + row[i] < o.rows ? r0 + row[i] : 0;
         at[i] = o.p + int64_t(k[i]) * o.ld + c;

@@ -611,14 +611,14 @@ bool aligned16(std::initializer_list<const void*> ptrs, std::initializer_list<in
 }
 
 // run(the tile's edge, whether its loads are direct) for a product of n tiles of 128 x 128.
-template <class F>
+template <class T, class F>
 void with_tile(int64_t n, bool direct, F&& run) {
-  using Whole = std::integral_constant<int, 128>;
-  using Half = std::integral_constant<int, 64>;
-  if (n >= kLinearWholeTiles)
-    direct ? run(Whole{}, std::true_type{}) : run(Whole{}, std::false_type{});
-  else
-    direct ? run(Half{}, std::true_type{}) : run(Half{}, std::false_type{});
+  auto go = [&](auto edge) {
+    direct ? run(edge, std::true_type{}) : run(edge, std::false_type{});
+  };
+  if (n >= kLinearWholeTiles) go(std::integral_constant<int, 128>{});
+  else if (sizeof(T) == 2 || n >= kLinearQuarterTiles) go(std::integral_constant<int, 64>{});
+  else if constexpr (sizeof(T) == 4) go(std::integral_constant<int, 32>{});
 }
 
 // Whether a product of a x b outputs runs on the head's tiles: enough of them for most of
@@ -706,7 +706,7 @@ hipError_t forward(const LinearArgs& a, const Launcher& L) {
     }
   }
   const bool direct = aligned16<T>({a.x, a.weight}, {a.I, a.ld_x});
-  with_tile(tiles_of<128>(a.O) * tiles_of<128>(a.N), direct, [&](auto ts, auto di) {
+  with_tile<T>(tiles_of<128>(a.O) * tiles_of<128>(a.N), direct, [&](auto ts, auto di) {
     constexpr int TS = decltype(ts)::value;
     const dim3 grid(unsigned(tiles_of<TS>(a.O) * tiles_of<TS>(a.N)));
     hipLaunchKernelGGL((k_linear<T, OT, TS, decltype(di)::value>), grid, dim3(small::kThreads), 0,
@@ -787,7 +787,7 @@ hipError_t backward(const LinearPlan& p, const LinearBwdArgs& a, char* ws, const
   bool direct = aligned16<T>({g}, {ld_g, a.I});
   if (a.dx) direct = direct && aligned16<T>({a.weight}, {});
   if (a.dweight) direct = direct && aligned16<T>({x}, {a.ld_x, a.O});
-  with_tile(n, direct, [&](auto ts, auto di) {
+  with_tile<T>(n, direct, [&](auto ts, auto di) {
     constexpr int TS = decltype(ts)::value;
     const int64_t n1 = a.dx ? tiles_of<TS>(a.I) * tiles_of<TS>(a.N) : 0, n1p = (n1 + 7) / 8 * 8;
     const int64_t n2 = a.dweight ? tiles_of<TS>(a.I) * tiles_of<TS>(a.O) : 0;

@@ -194,13 +194,22 @@ __global__ __launch_bounds__(kBlock<LANES>) void k_rms_norm_bwd(
   const float inv_h = 1.f / float(H);
   DropKey key{};
   if constexpr (DROP) key = drop_key(drop);
-  // the gradients of columns c .. of a row, d that of the sum
-  auto store_grads = [&](int64_t row, int64_t c, int64_t Hs, float (&d)[E]) {
+  // a bit for each value of a chunk that stays
+  auto keep_bits = [&](int64_t row, int64_t c) {
+    uint32_t bits = 0;
     if constexpr (DROP) {
-      if (dres) store_chunk(dres + row * lddres, c, Hs, d);
       const Mask8 m = drop_chunk<E>(key, row, c);
 #pragma unroll
-      for (int e = 0; e < E; ++e) d[e] = drop_keeps(m, e, drop.threshold) ? d[e] * drop.scale : 0.f;
+      for (int e = 0; e < E; ++e) bits |= drop_keeps(m, e, drop.threshold) ? 1u << e : 0u;
+    }
+    return bits;
+  };
+  // the gradients of columns c .. of a row, d that of the sum
+  auto store_grads = [&](int64_t row, int64_t c, int64_t Hs, float (&d)[E], uint32_t bits) {
+    if constexpr (DROP) {
+      if (dres) store_chunk(dres + row * lddres, c, Hs, d);
+#pragma unroll
+      for (int e = 0; e < E; ++e) d[e] = (bits >> e) & 1 ? d[e] * drop.scale : 0.f;
     }
     store_chunk(dx + row * lddx, c, Hs, d);
   };
@@ -226,6 +235,11 @@ __global__ __launch_bounds__(kBlock<LANES>) void k_rms_norm_bwd(
         load_chunk(s + row * lds, c, H, n[k]);
         if (DS) load_chunk(ds + row * ldds, c, H, d[k]);
       }
+      // the mask while the loads are under way
+      uint32_t bits[C];
+#pragma unroll
+      for (int k = 0; k < C; ++k) bits[k] = keep_bits(row, (int64_t(k) * LANES + tid) * E);
+      if constexpr (DROP) __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int k = 0; k < C; ++k)
 #pragma unroll
@@ -243,7 +257,7 @@ __global__ __launch_bounds__(kBlock<LANES>) void k_rms_norm_bwd(
           const float v = q * (g[k][e] - n[k][e] * mean);
           g[k][e] = DS ? d[k][e] + v : v;
         }
-        store_grads(row, (int64_t(k) * LANES + tid) * E, live ? H : 0, g[k]);
+        store_grads(row, (int64_t(k) * LANES + tid) * E, live ? H : 0, g[k], bits[k]);
       }
     }
     if (DW) {
@@ -299,7 +313,7 @@ __global__ __launch_bounds__(kBlock<LANES>) void k_rms_norm_bwd(
           const float v = q * (g[e] * f[e] - n[e] * mean);
           g[e] = DS ? d[e] + v : v;
         }
-        store_grads(row, c, H, g);
+        store_grads(row, c, H, g, keep_bits(row, c));
       }
       first = false;
     }

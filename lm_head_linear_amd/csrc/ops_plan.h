@@ -131,6 +131,8 @@ constexpr int64_t kLinearFew = 64, kLinearWide = 32768;
 
 // Tiles of 128 x 128 from which a product takes those (others: of 64 x 64).
 constexpr int64_t kLinearWholeTiles = 384;
+// ... and of float32, below which it takes tiles of 32 x 32.
+constexpr int64_t kLinearQuarterTiles = 64;
 
 struct LinearPlan {
   int64_t dz_rows = 8;        // rows of dz a workgroup forms (and adds up for db)
