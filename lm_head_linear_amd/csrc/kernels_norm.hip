@@ -88,16 +88,14 @@ __global__ __launch_bounds__(kBlock<LANES>) void k_rms_norm(
   DropKey key{};
   if constexpr (DROP) key = drop_key(drop);
   float sum = 0.f;
-  auto load_sum = [&](int64_t c, float (&v)[E]) {
-    load_chunk(x, c, H, v);
-    float r[E];
-    if (RES) load_chunk(res, c, H, r);
+  // s of a chunk: v is x's and becomes s
+  auto add = [&](int64_t c, float (&v)[E], const float (&r)[E]) {
     if constexpr (DROP) {
       const Mask8 m = drop_chunk<E>(key, row0 + row, c);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const float add = RES ? r[e] : 0.f;
-        v[e] = drop_keeps(m, e, drop.threshold) ? fmaf(v[e], drop.scale, add) : add;
+        const float with = RES ? r[e] : 0.f;
+        v[e] = drop_keeps(m, e, drop.threshold) ? fmaf(v[e], drop.scale, with) : with;
       }
 #pragma unroll
       for (int e = 0; e < E; ++e) v[e] = to_f32(from_f32<T>(v[e]));
@@ -105,6 +103,12 @@ __global__ __launch_bounds__(kBlock<LANES>) void k_rms_norm(
 #pragma unroll
       for (int e = 0; e < E; ++e) v[e] = to_f32(from_f32<T>(v[e] + r[e]));
     }
+  };
+  auto load_sum = [&](int64_t c, float (&v)[E]) {
+    float r[E];
+    load_chunk(x, c, H, v);
+    if (RES) load_chunk(res, c, H, r);
+    add(c, v, r);
   };
   auto load_w = [&](int64_t c, float (&f)[E]) {
     if constexpr (sizeof(WT) == sizeof(T)) {
@@ -124,11 +128,30 @@ __global__ __launch_bounds__(kBlock<LANES>) void k_rms_norm(
   };
   if constexpr (C > 0) {
     float v[C][E], f[C][E];
+    if (H % E == 0) {                              // every load before the first is used
+      row_u32x4 rx[C], rr[C];
 #pragma unroll
-    for (int k = 0; k < C; ++k) {
-      const int64_t c = (int64_t(k) * LANES + tid) * E;
-      load_sum(c, v[k]);
-      load_w(c, f[k]);
+      for (int k = 0; k < C; ++k) {
+        const int64_t c = (int64_t(k) * LANES + tid) * E;
+        rx[k] = load_whole(x, c, H);
+        if (RES) rr[k] = load_whole(res, c, H);
+      }
+#pragma unroll
+      for (int k = 0; k < C; ++k) {
+        const int64_t c = (int64_t(k) * LANES + tid) * E;
+        float r[E];
+        unpack_whole<T>(rx[k], c, H, v[k]);
+        if (RES) unpack_whole<T>(rr[k], c, H, r);
+        add(c, v[k], r);
+        load_w(c, f[k]);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < C; ++k) {
+        const int64_t c = (int64_t(k) * LANES + tid) * E;
+        load_sum(c, v[k]);
+        load_w(c, f[k]);
+      }
     }
 #pragma unroll
     for (int k = 0; k < C; ++k) {
@@ -192,6 +215,7 @@ __global__ __launch_bounds__(kBlock<LANES>) void k_rms_norm_bwd(
     for (int e = 0; e < E; ++e) f[e] += offset;
   };
   const float inv_h = 1.f / float(H);
+  const bool whole = H % E == 0;
   DropKey key{};
   if constexpr (DROP) key = drop_key(drop);
   // a bit for each value of a chunk that stays
@@ -228,18 +252,38 @@ __global__ __launch_bounds__(kBlock<LANES>) void k_rms_norm_bwd(
       const float q = live ? rstd[row] : 0.f;
       float g[C][E], n[C][E], d[C][E];
       float sum = 0.f;
-#pragma unroll
-      for (int k = 0; k < C; ++k) {
-        const int64_t c = (int64_t(k) * LANES + tid) * E;
-        load_chunk(dy + row * lddy, c, H, g[k]);
-        load_chunk(s + row * lds, c, H, n[k]);
-        if (DS) load_chunk(ds + row * ldds, c, H, d[k]);
-      }
-      // the mask while the loads are under way
       uint32_t bits[C];
+      auto masks = [&] {
 #pragma unroll
-      for (int k = 0; k < C; ++k) bits[k] = keep_bits(row, (int64_t(k) * LANES + tid) * E);
-      if constexpr (DROP) __builtin_amdgcn_sched_barrier(0);
+        for (int k = 0; k < C; ++k) bits[k] = keep_bits(row, (int64_t(k) * LANES + tid) * E);
+      };
+      if (whole) {
+        row_u32x4 rg[C], rn[C], rd[C];
+#pragma unroll
+        for (int k = 0; k < C; ++k) {
+          const int64_t c = (int64_t(k) * LANES + tid) * E;
+          rg[k] = load_whole(dy + row * lddy, c, H);
+          rn[k] = load_whole(s + row * lds, c, H);
+          if (DS) rd[k] = load_whole(ds + row * ldds, c, H);
+        }
+        masks();                                   // while the loads are under way
+#pragma unroll
+        for (int k = 0; k < C; ++k) {
+          const int64_t c = (int64_t(k) * LANES + tid) * E;
+          unpack_whole<T>(rg[k], c, H, g[k]);
+          unpack_whole<T>(rn[k], c, H, n[k]);
+          if (DS) unpack_whole<T>(rd[k], c, H, d[k]);
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < C; ++k) {
+          const int64_t c = (int64_t(k) * LANES + tid) * E;
+          load_chunk(dy + row * lddy, c, H, g[k]);
+          load_chunk(s + row * lds, c, H, n[k]);
+          if (DS) load_chunk(ds + row * ldds, c, H, d[k]);
+        }
+        masks();
+      }
 #pragma unroll
       for (int k = 0; k < C; ++k)
 #pragma unroll

@@ -79,6 +79,18 @@ __device__ __forceinline__ void load_chunk(const T* row, int64_t c, int64_t n,
   }
 }
 
+// The same in two steps for rows of whole chunks (n a multiple of a chunk): the load, without
+// a condition that would have it waited for before the next one is issued, and the values.
+template <class T>
+__device__ __forceinline__ row_u32x4 load_whole(const T* row, int64_t c, int64_t n) {
+  return load_raw(row + (c < n ? c : 0));
+}
+template <class T>
+__device__ __forceinline__ void unpack_whole(const row_u32x4& v, int64_t c, int64_t n,
+                                             float (&f)[kPerChunk<T>]) {
+  unpack_chunk<T>(c < n ? v : row_u32x4{0u, 0u, 0u, 0u}, f);
+}
+
 template <class T>
 __device__ __forceinline__ void store_chunk(T* row, int64_t c, int64_t n,
                                             const float (&f)[kPerChunk<T>]) {
