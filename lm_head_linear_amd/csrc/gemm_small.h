@@ -11,8 +11,10 @@
 // Each operand is stored with k contiguous ([rows][k], form N) or with its rows contiguous
 // ([k][rows], form T). A stage holds 128 bytes of k a row (64 bf16, 32 float32). A tile has
 // few waves to hide a load behind, so several stages are under way at once: where every row
-// starts at a multiple of 16 bytes (DIRECT) four stages take turns, loaded straight into
-// LDS, three ahead; otherwise two stages, loaded two ahead through registers. A lane reads 16
+// starts at a multiple of 16 bytes (DIRECT) stages are loaded straight into LDS, four in turn,
+// or three of the smaller tiles, of which another workgroup then fits beside (gradients of
+// 2048 x 1024 x 1024: 20 us, with four 23, with two 24); otherwise two stages, loaded two
+// ahead through registers. A lane reads 16
 // bytes of k of a row at a time: eight bf16 feed one v_mfma_f32_16x16x32_bf16, four float32
 // four v_mfma_f32_16x16x4_f32, both operands in the same order of k.
 #pragma once
@@ -219,10 +221,10 @@ __device__ __forceinline__ void multiply(Acc<TS>& acc, const char* sa, const cha
 }
 
 // LDS of a tile: its stages of two operands.
-template <bool DIRECT>
-constexpr int kStages = DIRECT ? 4 : 2;
 template <int TS, bool DIRECT>
-constexpr int kSmemBytes = 2 * kStages<DIRECT> * kStageBytes<TS>;
+constexpr int kStages = !DIRECT ? 2 : TS == 128 ? 4 : 3;
+template <int TS, bool DIRECT>
+constexpr int kSmemBytes = 2 * kStages<TS, DIRECT> * kStageBytes<TS>;
 
 // Waits until at most N of the wave's loads are under way.
 template <int N>
@@ -249,7 +251,7 @@ __device__ __forceinline__ void direct_step(Acc<TS>& acc, const Loads<T, FA, TS>
 template <class T, int FA, int FB, int TS, bool DIRECT>
 __device__ __forceinline__ void tile(Acc<TS>& acc, const Operand<T>& A, const Operand<T>& B,
                                      int64_t a0, int64_t b0, int64_t K, char* smem) {
-  constexpr int SB = kStageBytes<TS>, C = kChunks<TS>, NS = kStages<DIRECT>;
+  constexpr int SB = kStageBytes<TS>, C = kChunks<TS>, NS = kStages<TS, DIRECT>;
   const int tid = threadIdx.x, lane = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wa = (w & 1) * (TS / 2), wb = (w >> 1) * (TS / 2);

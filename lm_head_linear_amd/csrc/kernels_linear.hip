@@ -526,25 +526,31 @@ __global__ __launch_bounds__(256) void k_linear_db(BiasGrad<T> b) {
   b.run(blockIdx.x, red);
 }
 
-// dx's tiles (n1 of them, padded to a multiple of 8), then dW's (n2), then db, in one grid.
+// dx's tiles (n1 of them) and dW's (n2), those of the longer k first, the first kind's count
+// padded to a multiple of 8, then db, in one grid.
 template <class T, int TS, bool DIRECT>
 __global__ __launch_bounds__(small::kThreads) void k_linear_grads(
-    int64_t n1, int64_t n1p, int64_t n2, small::Operand<T> Wt, small::Operand<T> dz, int64_t O,
+    int64_t n1, int64_t n2, bool dw_first, small::Operand<T> Wt, small::Operand<T> dz, int64_t O,
     GradOut<T> dx, small::Operand<T> xt, small::Operand<T> dzt, int64_t N, GradOut<T> dw,
     BiasGrad<T> db) {
   __shared__ __attribute__((aligned(1024))) char smem[small::kSmemBytes<TS, DIRECT>];
   const int64_t b = blockIdx.x;
   int64_t a0, b0;
   small::Acc<TS> acc;
-  if (b < n1p) {
-    if (b >= n1) return;
-    tile_at<TS>(b, tiles_of<TS>(dx.cols), tiles_of<TS>(dx.rows), a0, b0);
+  const int64_t first = ((dw_first ? n2 : n1) + 7) / 8 * 8, second = dw_first ? n1 : n2;
+  if (b >= first + second) {
+    db.run(b - first - second, reinterpret_cast<float (*)[17]>(smem));
+    return;
+  }
+  const bool is_dw = (b < first) == dw_first;
+  const int64_t t = b < first ? b : b - first;
+  if (t >= (is_dw ? n2 : n1)) return;
+  if (!is_dw) {
+    tile_at<TS>(t, tiles_of<TS>(dx.cols), tiles_of<TS>(dx.rows), a0, b0);
     small::tile<T, 1, 0, TS, DIRECT>(acc, Wt, dz, a0, b0, O, smem);
     dx.store_tile(acc, a0, b0);
-  } else if (b >= n1p + n2) {
-    db.run(b - n1p - n2, reinterpret_cast<float (*)[17]>(smem));
   } else {
-    tile_at<TS>(b - n1p, tiles_of<TS>(dw.cols), tiles_of<TS>(dw.rows), a0, b0);
+    tile_at<TS>(t, tiles_of<TS>(dw.cols), tiles_of<TS>(dw.rows), a0, b0);
     small::tile<T, 1, 1, TS, DIRECT>(acc, xt, dzt, a0, b0, N, smem);
     dw.store_tile(acc, a0, b0);
   }
@@ -789,10 +795,12 @@ hipError_t backward(const LinearPlan& p, const LinearBwdArgs& a, char* ws, const
   if (a.dweight) direct = direct && aligned16<T>({x}, {a.ld_x, a.O});
   with_tile<T>(n, direct, [&](auto ts, auto di) {
     constexpr int TS = decltype(ts)::value;
-    const int64_t n1 = a.dx ? tiles_of<TS>(a.I) * tiles_of<TS>(a.N) : 0, n1p = (n1 + 7) / 8 * 8;
+    const int64_t n1 = a.dx ? tiles_of<TS>(a.I) * tiles_of<TS>(a.N) : 0;
     const int64_t n2 = a.dweight ? tiles_of<TS>(a.I) * tiles_of<TS>(a.O) : 0;
-    hipLaunchKernelGGL((k_linear_grads<T, TS, decltype(di)::value>), dim3(unsigned(n1p + n2 + db.groups())),
-                       dim3(small::kThreads), 0, L.stream, n1, n1p, n2,
+    const bool dw_first = a.N > a.O;
+    const int64_t tiles = ((dw_first ? n2 : n1) + 7) / 8 * 8 + (dw_first ? n1 : n2);
+    hipLaunchKernelGGL((k_linear_grads<T, TS, decltype(di)::value>), dim3(unsigned(tiles + db.groups())),
+                       dim3(small::kThreads), 0, L.stream, n1, n2, dw_first,
                        small::Operand<T>{static_cast<const T*>(a.weight), a.I, a.I},
                        small::Operand<T>{g, ld_g, a.N}, a.O,
                        GradOut<T>{static_cast<T*>(a.dx), a.ld_dx, a.N, a.I, 0},
