@@ -27,6 +27,7 @@
 #include "gemm_small.h"
 #include "ops_plan.h"
 #include "row_io.h"
+#include "wave_ops.h"
 
 namespace flce {
 namespace {
@@ -346,11 +347,21 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_linear_few(small::Operand<T>
   fin.store(act, c, 16 * w + r, z, ends);
 }
 
-// A wide W, as a head: 64 RB of its rows a workgroup (few_rows.h).
+// The larger one; NaN if either is.
+struct MaxNanOp {
+  __device__ __forceinline__ float operator()(float a, float b) const {
+    return a != a ? a : b != b ? b : fmaxf(a, b);
+  }
+};
+
+// A wide W, as a head: 64 RB of its rows a workgroup (few_rows.h). maxima, where given
+// (float32 y): [N][gridDim.x], the largest of each workgroup's part of a row, so that what
+// samples from it need not read it all again.
 template <int NT, int ALIGN, int RB, class OT>
 __global__ __launch_bounds__(256) void k_linear_wide(const uint16_t* __restrict__ W,
                                                      const uint16_t* __restrict__ x, int64_t ld_x,
-                                                     int64_t I, Finish<Bf16Bits, OT> fin, int act) {
+                                                     int64_t I, Finish<Bf16Bits, OT> fin, int act,
+                                                     float* __restrict__ maxima) {
   __shared__ __attribute__((aligned(16))) FewSmem<NT, RB> sm;
   const int64_t v0 = int64_t(blockIdx.x) * (64 * RB);
   few_logits<NT, ALIGN, RB>(x, ld_x, W, fin.N, I, fin.O, v0, sm);
@@ -360,6 +371,15 @@ __global__ __launch_bounds__(256) void k_linear_wide(const uint16_t* __restrict_
     const float* s = &sm.z[r][4 * (i % (16 * RB))];
     const float z[4] = {s[0], s[1], s[2], s[3]};
     fin.store(act, c, r, z, fin.load(c, r));
+    if (maxima) {
+      float m = -INFINITY;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (c + e < fin.O) m = MaxNanOp()(m, z[e]);
+      m = group_all<16>(m, MaxNanOp());
+      if (RB == 2) m = pair_rows(m, MaxNanOp());
+      if (i % (16 * RB) == 0) maxima[r * gridDim.x + blockIdx.x] = m;
+    }
   }
 }
 
@@ -658,21 +678,27 @@ bool forward_large(const LinearArgs& a, const Finish<Bf16Bits, OT>& fin, const L
   return true;
 }
 
+// Whether a forward takes k_linear_wide. few_rows.h reads odd rows as the words they lie in:
+// dense rows, from aligned addresses.
+bool takes_wide(const LinearArgs& a) {
+  if (a.dtype != FLCE_BF16 || a.N > kFewTokens || a.O < kLinearWide) return false;
+  return aligned16<Bf16Bits>({a.weight, a.x}, {}) &&
+         (a.ld_x == a.I || aligned16<Bf16Bits>({}, {a.I, a.ld_x}));
+}
+
 template <class T, class OT>
 bool forward_few(const LinearArgs& a, const Finish<T, OT>& fin, const Launcher& L) {
   const T* W = static_cast<const T*>(a.weight);
   const T* x = static_cast<const T*>(a.x);
   if constexpr (sizeof(T) == 2) {
-    // few_rows.h reads odd rows as the words they lie in: dense rows, from aligned addresses
-    const bool whole = aligned16<T>({W, x}, {a.I, a.ld_x});
-    const bool dense = aligned16<T>({W, x}, {}) && a.ld_x == a.I;
-    if (a.N <= kFewTokens && a.O >= kLinearWide && (whole || dense)) {
+    if (takes_wide(a)) {
+      const bool whole = aligned16<T>({}, {a.I, a.ld_x});
       with_few(a.N, [&](auto nt, auto rb) {
         constexpr int NT = decltype(nt)::value, RB = decltype(rb)::value;
         auto go = [&](auto align) {
           hipLaunchKernelGGL((k_linear_wide<NT, decltype(align)::value, RB, OT>),
                              dim3(unsigned((a.O + 64 * RB - 1) / (64 * RB))), dim3(256), 0, L.stream,
-                             W, x, a.ld_x, a.I, fin, a.activation);
+                             W, x, a.ld_x, a.I, fin, a.activation, a.maxima);
         };
         if (whole) go(std::integral_constant<int, 16>{});
         else if (a.I % 2 == 0) go(std::integral_constant<int, 4>{});
@@ -812,6 +838,16 @@ hipError_t backward(const LinearPlan& p, const LinearBwdArgs& a, char* ws, const
 }
 
 }  // namespace
+
+int64_t linear_max_blocks(const LinearArgs& a) {
+  if (!takes_wide(a)) return 0;
+  int64_t n = 0;
+  with_few(a.N, [&](auto, auto rb) {
+    constexpr int kCols = 64 * decltype(rb)::value;
+    n = (a.O + kCols - 1) / kCols;
+  });
+  return n;
+}
 
 hipError_t launch_linear(const LinearArgs& a, const Launcher& L) {
   if (a.dtype == FLCE_F32) return forward<float, float>(a, L);

@@ -20,7 +20,8 @@
 // sums by wave are sums by place. The first pass finds the largest logit; what follows
 // depends on what can be ruled out before the selection:
 // - top-k: the k-th largest of the threads' own maxima is a bound that few logits but the
-//   first k pass. Those are collected in LDS, in index order, and everything else is done
+//   first k pass (where the head's product left the maxima of each 64 or 128 logits, those
+//   are read in the logits' place, and the parts that reach the bound). Those are collected in LDS, in index order, and everything else is done
 //   on the list. min-p alone bounds the list in the same way.
 // - top-p without top-k: one pass forms all weights and adds them up by bins of an eighth
 //   of a power of two, for each wave; the bin in which the mass passes p is then collected,
@@ -468,6 +469,34 @@ __device__ __forceinline__ int64_t small_list(Shared& sm, int n, const Weights<C
   return sm.found;
 }
 
+// With `have` indices of each wave, in order, in its place of sm.idx (at most kWaveList are
+// there): all of them and their keys from the front on. Returns how many, or -1 if a wave
+// found more than its place holds.
+template <class T>
+__device__ __forceinline__ int close_gaps(const Row<T>& row, Shared& sm, int have) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const uint32_t* idx = sm.idx + wave * kWaveList;
+  if (lane == 0) sm.wave_sum[wave] = uint64_t(have);
+  __syncthreads();
+  uint64_t n;
+  const int start = int(before_wave(sm, wave, n));
+  const bool fits = __ballot(lane < kWaves && sm.wave_sum[lane & (kWaves - 1)] > kWaveList) == 0;
+  // every wave reads its place before any writes
+  uint32_t x[kWaveList / 64];
+#pragma unroll
+  for (int i = 0; i < kWaveList / 64; ++i) x[i] = idx[i * 64 + lane];
+  __syncthreads();
+  if (!fits) return -1;
+#pragma unroll
+  for (int i = 0; i < kWaveList / 64; ++i)
+    if (i * 64 + lane < have) {
+      sm.idx[start + i * 64 + lane] = x[i];
+      sm.key[start + i * 64 + lane] = order_key(row.at(x[i]));
+    }
+  __syncthreads();
+  return int(n);
+}
+
 // The row's logits for which take(z, i) holds, in index order, into sm.key and sm.idx. Each
 // wave first fills a place of its own from its segment. Returns how many, or -1 if a wave
 // found more than its place holds.
@@ -508,25 +537,35 @@ __device__ __forceinline__ int collect(const Row<T>& row, int64_t seg, Shared& s
         mine = 0;
       }
     });
-  if (lane == 0) sm.wave_sum[wave] = uint64_t(have);
-  __syncthreads();
-  uint64_t n;
-  const int start = int(before_wave(sm, wave, n));
-  const bool fits = __ballot(lane < kWaves && sm.wave_sum[lane & (kWaves - 1)] > kWaveList) == 0;
-  // close the gaps: every wave reads its place before any writes
-  uint32_t x[kWaveList / 64];
-#pragma unroll
-  for (int i = 0; i < kWaveList / 64; ++i) x[i] = idx[i * 64 + lane];
-  __syncthreads();
-  if (!fits) return -1;
-#pragma unroll
-  for (int i = 0; i < kWaveList / 64; ++i)
-    if (i * 64 + lane < have) {
-      sm.idx[start + i * 64 + lane] = x[i];
-      sm.key[start + i * 64 + lane] = order_key(row.at(x[i]));
+  return close_gaps(row, sm, have);
+}
+
+// The row's keys of at least `bound` in the parts whose maxima reach it, as collect(): wave w
+// looks at the parts from w bseg on.
+template <class T>
+__device__ __forceinline__ int collect_parts(const Row<T>& row, const SampleArgs& a,
+                                             const float* maxima, int64_t bseg, uint32_t bound,
+                                             Shared& sm) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const uint64_t below = (1ull << lane) - 1;
+  uint32_t* idx = sm.idx + wave * kWaveList;
+  const int64_t first = wave * bseg, last = first + bseg < a.blocks ? first + bseg : a.blocks;
+  int have = 0;
+  for (int64_t b0 = first; b0 < last; b0 += 64) {
+    const bool in = b0 + lane < last;
+    uint64_t parts = __ballot(in && order_key(in ? maxima[b0 + lane] : 0.f) >= bound);
+    for (; parts != 0; parts &= parts - 1) {
+      const int64_t at = (b0 + __builtin_ctzll(parts)) * a.block;
+      for (int64_t i = at + lane; i - lane < at + a.block; i += 64) {
+        const bool take = i < row.n && order_key(row.at(i < row.n ? i : 0)) >= bound;
+        const uint64_t hits = __ballot(take);
+        const int to = have + __popcll(hits & below);
+        if (take && to < kWaveList) idx[to] = uint32_t(i);
+        have += __popcll(hits);
+      }
     }
-  __syncthreads();
-  return int(n);
+  }
+  return close_gaps(row, sm, have);
 }
 
 // The same in any order within a wave's place, which keep their gaps: wave w's are
@@ -596,7 +635,14 @@ __global__ __launch_bounds__(kThreads) void k_sample(SampleArgs a) {
   // the largest logit; a row of -inf alone or with a NaN has no token
   float most = -INFINITY;
   bool nan = false;
-  if (from < to)
+  const float* maxima = a.maxima ? a.maxima + r * a.blocks : nullptr;
+  const int64_t bseg = (a.blocks + kWaves - 1) / kWaves;
+  if (maxima) {
+    for (int64_t b = wave * bseg + lane; b < (wave + 1) * bseg && b < a.blocks; b += 64) {
+      nan |= maxima[b] != maxima[b];
+      most = fmaxf(most, maxima[b]);
+    }
+  } else if (from < to) {
     row.template turns<8>(from, to, lane, 64, [&](int, const float (&v)[E], int64_t, int e0) {
 #pragma unroll
       for (int e = 0; e < E; ++e) {
@@ -605,6 +651,7 @@ __global__ __launch_bounds__(kThreads) void k_sample(SampleArgs a) {
         most = fmaxf(most, e >= e0 ? v[e] : -INFINITY);
       }
     }, [] {});
+  }
   const uint32_t own = order_key(most);            // key of -inf: nothing
   uint32_t best = wave_all(own, MaxOp());
   const uint64_t any_nan = __ballot(nan);
@@ -641,8 +688,13 @@ __global__ __launch_bounds__(kThreads) void k_sample(SampleArgs a) {
 
   uint64_t total = 0, target = 0;
   int64_t token = -1;
-  if (k == 1) {                                    // the first of the largest
-    if (own == best) {
+  if (k == 1 && maxima) {                          // the first of the largest
+    const int n = collect_parts(row, a, maxima, bseg, best, sm);
+    if (n > 0) token = sm.idx[0];
+    total = 1ull << wt.S;
+  }
+  if (k == 1 && token < 0) {
+    if (maxima || own == best) {
       uint32_t first = ~0u;
       row.each(from, to, lane, 64, [&](float z, int64_t i) {
         if (order_key(z) == best && uint32_t(i) < first) first = uint32_t(i);
@@ -657,12 +709,14 @@ __global__ __launch_bounds__(kThreads) void k_sample(SampleArgs a) {
     for (int i = 1; i < kWaves; ++i) first = MinOp()(first, sm.idx[i * 64 + lane]);
     token = wave_all(first, MinOp());
     total = 1ull << wt.S;
-  } else if (k < V || (p >= 1.0 && wt.min_p > 0.0)) {
+  } else if (k > 1 && (k < V || (p >= 1.0 && wt.min_p > 0.0))) {
     // a list of all that may be kept
     int n;
     if (k < V) {
       const uint32_t bound = k <= kThreads ? bound_of_maxima(own, k, sm) : 0u;
-      n = bound ? collect(row, seg, sm, [&](float z) { return order_key(z) >= bound; }) : -1;
+      n = !bound ? -1
+          : maxima ? collect_parts(row, a, maxima, bseg, bound, sm)
+                   : collect(row, seg, sm, [&](float z) { return order_key(z) >= bound; });
     } else {
       n = collect(row, seg, sm, [&](float z) { return wt.reaches_min_p(z); });
     }
@@ -677,7 +731,7 @@ __global__ __launch_bounds__(kThreads) void k_sample(SampleArgs a) {
       }
       token = sm.idx[at];
     }
-  } else if (p < 1.0) {
+  } else if (k > 1 && p < 1.0) {
     // weights by bins of an eighth of a power of two, each wave its own
     for (int i = tid; i < kWaves * kMassBins; i += kThreads) (&sm.mass[0][0])[i] = 0;
     __syncthreads();

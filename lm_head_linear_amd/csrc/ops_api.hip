@@ -124,15 +124,18 @@ int flce_sample(const void* h, const void* W, int64_t N, int64_t H, int64_t V,
   auto from = [](auto* v, int64_t r) { return v ? v + r : v; };
   for (int64_t r = 0; r < N; r += p.rows) {
     const int64_t n = N - r < p.rows ? N - r : p.rows;
-    const flce::LinearArgs z{static_cast<const char*>(h) + size_t(r) * H * es, H, W, nullptr,
+    flce::LinearArgs z{static_cast<const char*>(h) + size_t(r) * H * es, H, W, nullptr,
                              nullptr, V, n, H, V, FLCE_ACT_NONE, workspace, V, nullptr, dtype,
                              FLCE_F32};
+    const int64_t blocks = flce::linear_max_blocks(z);
+    if (blocks) z.maxima = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.off_max);
     hipError_t e = flce::launch_linear(z, L);
     if (e != hipSuccess) return status_of(e);
     const flce::SampleArgs a{workspace, V, n, V, uniforms + r, {from(temperatures, r), temperature},
                              {from(top_ps, r), top_p}, {from(min_ps, r), min_p},
                              {from(top_ks, r), top_k}, softcap, tokens + r, from(logp, r), FLCE_F32,
-                             flce::sample_weight_bits(V)};
+                             flce::sample_weight_bits(V), z.maxima, blocks,
+                             blocks == (V + 63) / 64 ? 64 : 128};
     e = flce::launch_sample(a, L);
     if (e != hipSuccess) return status_of(e);
   }

@@ -104,6 +104,7 @@ struct LinearArgs {
   int64_t ld_y;
   void* slope;                // may be null
   int dtype, y_dtype;
+  float* maxima = nullptr;    // [N][linear_max_blocks()], of y without bias and activation
 };
 
 struct LinearBwdArgs {
@@ -164,6 +165,8 @@ struct SampleArgs {
   float* logp;                // may be null
   int dtype;
   int weight_bits;            // S: weights are multiples of 2^-S of the largest
+  const float* maxima = nullptr;   // [N][blocks], of equal parts of each row, if at hand
+  int64_t blocks = 0, block = 0;   // how many, and a part's length
 };
 
 // Bits of a weight so that V of them sum up below 2^63, and at most what one rounding of a
@@ -174,12 +177,13 @@ inline int sample_weight_bits(int64_t V) {
   return 62 - log_v < 51 ? 62 - log_v : 51;
 }
 
-// Logits of the head form: as many rows at a time as fit these bytes.
-constexpr int64_t kSampleLogitBytes = int64_t(512) << 20;
+// Logits of the head form: as many rows at a time as fit these bytes. Their maxima add at most
+// a 64th: 512 MiB in all.
+constexpr int64_t kSampleLogitBytes = int64_t(504) << 20;
 
 struct SamplePlan {
   int64_t rows = 0;
-  size_t total = 0;
+  size_t off_max = 0, total = 0;   // the maxima of 64 logits or more each
 };
 
 bool make_sample_plan(int64_t N, int64_t H, int64_t V, int dtype, SamplePlan* p);
@@ -399,6 +403,9 @@ namespace flce {
 hipError_t launch_rms_norm(const NormArgs& a, const Launcher& L);
 hipError_t launch_rms_norm_backward(const NormBwdArgs& a, const Launcher& L);
 hipError_t launch_linear(const LinearArgs& a, const Launcher& L);
+// Parts of a row whose maxima a forward of these arguments can leave (0: none); all but the
+// last are equally long: 64 columns up to 32 rows, 128 from there.
+int64_t linear_max_blocks(const LinearArgs& a);
 hipError_t launch_linear_backward(const LinearPlan& p, const LinearBwdArgs& a, char* ws,
                                   const Launcher& L);
 hipError_t launch_sample(const SampleArgs& a, const Launcher& L);

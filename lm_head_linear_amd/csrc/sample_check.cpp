@@ -15,7 +15,9 @@ bool make_sample_plan(int64_t N, int64_t H, int64_t V, int dtype, SamplePlan* ou
   const int64_t fit = kSampleLogitBytes / (V * 4);
   p.rows = N < fit ? N : fit;
   if (p.rows < 1) p.rows = 1;
-  p.total = align256(size_t(p.rows) * V * 4);
+  p.off_max = align256(size_t(p.rows) * V * 4);
+  p.total = p.off_max + align256(size_t(p.rows < kFewTokens ? p.rows : kFewTokens) *
+                                 ceil_div(V, 64) * 4);
   *out = p;
   return true;
 }

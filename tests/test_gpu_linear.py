@@ -104,6 +104,22 @@ def test_sizes(N, I, O, dt):
         check(N, I, O, dt, act, bias=i % 2 == 0, residual=i in (0, 1, 4), seed=i)
 
 
+@pytest.mark.parametrize("N,I,O", [(1, 64, 32768), (5, 129, 33001), (16, 130, 32770), (33, 256, 40000),
+                                   (48, 65, 32769), (100, 40, 33333), (128, 128, 32800)])
+@pytest.mark.parametrize("act", ["none", "gelu_tanh"])
+def test_wide_weights(N, I, O, act):
+    check(N, I, O, torch.bfloat16, act, act != "none", act == "none")
+    # rows of x apart: another kernel where they are odd, the same sums to their error
+    import lm_head_linear_amd as m
+    x, w, b, r, _ = make(N, I, O, torch.bfloat16, 4)
+    wide = torch.zeros(N, I + 13, device="cuda").bfloat16()
+    wide[:, 8:8 + I] = x
+    y, _ = m.flce_linear(wide[:, 8:8 + I], w, b, r, activation=act)
+    want, _ = m.flce_linear(x, w, b, r, activation=act)
+    tol = 6 * I ** 0.5 * U * 2 * 1.13 * (x.double().abs() @ w.double().abs().T + 1)
+    inside(y, want.double(), tol + 2 * half(torch.bfloat16) * want.double().abs() * 1.02, "y")
+
+
 @pytest.mark.parametrize("N,I,O", [(1, 512, 1000), (130, 257, 129), (600, 256, 512), (40, 64, 64)])
 def test_float32_out_of_bf16_rows(N, I, O):
     import lm_head_linear_amd as m

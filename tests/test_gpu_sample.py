@@ -224,10 +224,36 @@ def test_from_the_head(N, H, V, dt):
         compare(r, z, u, **s)
 
 
+@pytest.mark.parametrize("N,H,V", [(1, 64, 33000), (17, 130, 40001), (33, 64, 32768), (48, 72, 50000),
+                                   (64, 65, 32769), (128, 64, 34567), (129, 64, 34567)])
+def test_from_a_wide_head(N, H, V):
+    """The head's product leaves maxima of each 64 or 128 logits: the tokens are those of the
+    logits alone, ties and NaN among them."""
+    import lm_head_linear_amd as m
+    g = torch.Generator().manual_seed(N + V)
+    W = ((torch.randn(V, H, generator=g) * 16).round().clamp(-255, 255) / 64).bfloat16().cuda()
+    h = ((torch.randn(N, H, generator=g) * 8).round().clamp(-255, 255) / 32).bfloat16().cuda()
+    W[V - 1], W[V // 2] = W[5], W[5]                      # equal logits far apart
+    z = (h.double() @ W.double().T).float()
+    u = torch.rand(N, generator=g).cuda()
+    k = torch.randint(0, 60, (N,), generator=g, dtype=torch.int32).cuda()
+    for kw in (dict(top_k=50), dict(temperature=0.0), dict(top_k=k, top_p=0.8, temperature=2.0),
+               dict(top_k=1000, softcap=20.0), dict(top_p=0.9), dict(min_p=0.1), dict(top_k=1200)):
+        a, b = m.flce_sample(h, W, u, **kw), m.flce_sample_logits(z, u, **kw)
+        assert torch.equal(a.tokens, b.tokens) and torch.equal(a.logp, b.logp), kw
+    W[7, 3] = float("nan")
+    r = m.flce_sample(h, W, u, top_k=5)
+    assert bool((r.tokens == -1).all()) and bool(r.logp.isnan().all())
+    r = m.flce_sample(torch.zeros_like(h), torch.zeros_like(W), u, top_k=40)   # all equal
+    assert bool((r.tokens < 40).all())
+    r = m.flce_sample(torch.zeros_like(h), torch.zeros_like(W), u, temperature=0.0)
+    assert bool((r.tokens == 0).all())
+
+
 def test_rows_in_parts_of_the_workspace():
     """More rows than the logits' 512 MiB hold at once: each row is what it is alone."""
     import lm_head_linear_amd as m
-    N, H, V = 700, 8, 200000                # 671 rows at a time
+    N, H, V = 700, 8, 200000                # 660 rows at a time
     g = torch.Generator(device="cuda").manual_seed(0)
     h = torch.randn(N, H, generator=g, device="cuda").bfloat16()
     W = torch.randn(V, H, generator=g, device="cuda").bfloat16()
