@@ -730,20 +730,24 @@ int flce_linear_backward(const void* dy, int64_t ld_dy, const void* x, int64_t l
  * negative or not finite, a setting without array that is NaN, a temperature or top_k below
  * 0, a temperature that is not finite, top_p outside (0, 1], min_p outside [0, 1], an
  * output that overlaps anything; FLCE_ERR_UNSUPPORTED for a misaligned pointer or more
- * rows than one grid takes (2^22 - 1).
+ * rows than one grid takes (2^22 - 1); FLCE_ERR_WORKSPACE. The workspace (256-byte aligned)
+ * is flce_sample_logits_workspace_size bytes (0 for invalid sizes): maxima of parts of up to
+ * 64 long rows.
  */
+size_t flce_sample_logits_workspace_size(int64_t N, int64_t V, int dtype);
 int flce_sample_logits_check_args(const void* logits, int64_t ld_logits, int64_t N, int64_t V,
                                   const float* uniforms, float temperature,
                                   const float* temperatures, int32_t top_k,
                                   const int32_t* top_ks, float top_p, const float* top_ps,
                                   float min_p, const float* min_ps, float softcap,
                                   const int64_t* tokens, const float* logp, const void* stream,
-                                  int dtype);
+                                  int dtype, const void* workspace, size_t workspace_bytes);
 int flce_sample_logits(const void* logits, int64_t ld_logits, int64_t N, int64_t V,
                        const float* uniforms, float temperature, const float* temperatures,
                        int32_t top_k, const int32_t* top_ks, float top_p, const float* top_ps,
                        float min_p, const float* min_ps, float softcap, int64_t* tokens,
-                       float* logp, void* stream, int dtype);
+                       float* logp, void* stream, int dtype, void* workspace,
+                       size_t workspace_bytes);
 
 /*
  * flce_sample -- flce_sample_logits of the logits z = h . W^T (float32) of the head W [V,H]

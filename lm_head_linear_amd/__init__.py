@@ -52,7 +52,7 @@ from ._linear import (  # noqa: F401
     flce_linear_backward_workspace_size, flce_linear_check_args, fused_linear)
 from ._sample import (  # noqa: F401
     Sampled, flce_sample, flce_sample_check_args, flce_sample_logits,
-    flce_sample_logits_check_args, flce_sample_workspace_size)
+    flce_sample_logits_check_args, flce_sample_logits_workspace_size, flce_sample_workspace_size)
 from ._util import FlceError, _check_tensor, _dtype_code, _ptr, flce_status_string
 
 __all__ = [
@@ -106,6 +106,7 @@ __all__ = [
     "flce_sample_workspace_size",
     "flce_sample_logits",
     "flce_sample_logits_check_args",
+    "flce_sample_logits_workspace_size",
     "Sampled",
     "DropoutMask",
     "flce_dropout",

@@ -46,7 +46,7 @@ _LINEAR = [_vp, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i32, _vp, _i64, _v
 _LINEAR_BWD = [_vp, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _i32, _vp,
                _i32, _vp, _sz]
 _SETTINGS = [_vp, _f32, _vp, _i32, _vp, _f32, _vp, _f32, _vp, _f32, _vp, _vp, _vp, _i32]
-_SAMPLE_LOGITS = [_vp, _i64, _i64, _i64] + _SETTINGS
+_SAMPLE_LOGITS = [_vp, _i64, _i64, _i64] + _SETTINGS + [_vp, _sz]
 _SAMPLE = [_vp, _vp, _i64, _i64, _i64] + _SETTINGS + [_vp, _sz]
 SIGNATURES = {
     "flce_workspace_size": (_sz, [_i64, _i64, _i64, _i32]),
@@ -77,6 +77,7 @@ SIGNATURES = {
     "flce_linear_backward_workspace_size": (_sz, [_i64, _i64, _i64, _i32]),
     "flce_linear_backward_check_args": (_i32, _LINEAR_BWD),
     "flce_linear_backward": (_i32, _LINEAR_BWD),
+    "flce_sample_logits_workspace_size": (_sz, [_i64, _i64, _i32]),
     "flce_sample_logits_check_args": (_i32, _SAMPLE_LOGITS),
     "flce_sample_logits": (_i32, _SAMPLE_LOGITS),
     "flce_sample_workspace_size": (_sz, [_i64, _i64, _i64, _i32]),

@@ -41,21 +41,26 @@ def _settings(N, dev, temperature, top_k, top_p, min_p, softcap):
     return _check_settings(temperature, top_k, top_p, min_p, softcap)
 
 
+def flce_sample_logits_workspace_size(N: int, V: int, dtype: torch.dtype) -> int:
+    return int(_lib.load().flce_sample_logits_workspace_size(N, V, _dtype_code(dtype)))
+
+
 def flce_sample_logits_check_args(logits, uniforms, *, N, V, ld_logits=None, temperature=1.0,
                                   top_k=0, top_p=1.0, min_p=0.0, softcap=0.0, tokens=None,
-                                  logp=None, dtype=torch.float32) -> int:
+                                  logp=None, dtype=torch.float32, workspace=None) -> int:
     """The synchronous checks of sampling from logits (no GPU work); a status code."""
     return int(_lib.load().flce_sample_logits_check_args(
         _ptr(logits), V if ld_logits is None else int(ld_logits), N, V, _ptr(uniforms),
         *_check_settings(temperature, top_k, top_p, min_p, softcap), _ptr(tokens), _ptr(logp),
-        None, _dtype_code(dtype)))
+        None, _dtype_code(dtype), _ptr(workspace), _bytes(workspace)))
 
 
 def flce_sample_logits(logits: torch.Tensor, uniforms: torch.Tensor, *,
                        temperature: _Number = 1.0, top_k: _Number = 0, top_p: _Number = 1.0,
                        min_p: _Number = 0.0, softcap: float = 0.0,
                        tokens: Optional[torch.Tensor] = None,
-                       logp: Optional[torch.Tensor] = None) -> Sampled:
+                       logp: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None) -> Sampled:
     """A token of each row of logits [N, V] from uniform numbers [N] (float32, in [0, 1)).
 
     Each setting is a number, or a tensor [N] with each row's own (float32, top_k int32).
@@ -72,8 +77,12 @@ def flce_sample_logits(logits: torch.Tensor, uniforms: torch.Tensor, *,
     settings = _settings(N, dev, temperature, top_k, top_p, min_p, softcap)
     tokens = _out("tokens", tokens, (N,), torch.int64, dev)
     logp = _out("logp", logp, (N,), torch.float32, dev)
-    _run("flce_sample_logits", dev, _lib.load().flce_sample_logits, logits.data_ptr(), ld, N, V,
-         uniforms.data_ptr(), *settings, tokens.data_ptr(), logp.data_ptr(), _stream(dev), code)
+    lib = _lib.load()
+    workspace = _workspace("flce_sample_logits", workspace,
+                           lib.flce_sample_logits_workspace_size(N, V, code), dev)
+    _run("flce_sample_logits", dev, lib.flce_sample_logits, logits.data_ptr(), ld, N, V,
+         uniforms.data_ptr(), *settings, tokens.data_ptr(), logp.data_ptr(), _stream(dev), code,
+         workspace.data_ptr(), _bytes(workspace))
     return Sampled(tokens, logp)
 
 

@@ -347,13 +347,6 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_linear_few(small::Operand<T>
   fin.store(act, c, 16 * w + r, z, ends);
 }
 
-// The larger one; NaN if either is.
-struct MaxNanOp {
-  __device__ __forceinline__ float operator()(float a, float b) const {
-    return a != a ? a : b != b ? b : fmaxf(a, b);
-  }
-};
-
 // A wide W, as a head: 64 RB of its rows a workgroup (few_rows.h). maxima, where given
 // (float32 y): [N][gridDim.x], the largest of each workgroup's part of a row, so that what
 // samples from it need not read it all again.

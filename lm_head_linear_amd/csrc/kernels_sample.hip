@@ -20,8 +20,9 @@
 // sums by wave are sums by place. The first pass finds the largest logit; what follows
 // depends on what can be ruled out before the selection:
 // - top-k: the k-th largest of the threads' own maxima is a bound that few logits but the
-//   first k pass (where the head's product left the maxima of each 64 or 128 logits, those
-//   are read in the logits' place, and the parts that reach the bound). Those are collected in LDS, in index order, and everything else is done
+//   first k pass (where the maxima of each 64 or 128 logits are at hand, from the head's
+//   product or, for few long rows, a kernel before this one, those are read in the logits'
+//   place, and the parts that reach the bound). Those are collected in LDS, in index order, and everything else is done
 //   on the list. min-p alone bounds the list in the same way.
 // - top-p without top-k: one pass forms all weights and adds them up by bins of an eighth
 //   of a power of two, for each wave; the bin in which the mass passes p is then collected,
@@ -47,6 +48,7 @@ constexpr int kBins = 2048;                        // of a radix selection's dig
 constexpr int kMassBins = 384;                     // of weights: eighths of 2^-48 .. 1
 constexpr int kWaveList = 256;                     // candidates a wave collects
 constexpr int kSmallList = 256;                    // of a list ranked by counting
+constexpr int kMaximaChunks = 4;                   // a thread of k_sample_maxima loads
 constexpr double kLog2eD = 1.4426950408889634074;
 
 __device__ __forceinline__ uint32_t order_key(float z) {
@@ -845,8 +847,42 @@ __global__ __launch_bounds__(kThreads) void k_sample(SampleArgs a) {
   }
 }
 
+// The maxima of each 16 chunks of the rows: 64 float32 or 128 bf16 logits, NaN where one is.
+// Where a few rows are long a workgroup a row leaves most CUs idle, and reads the row twice.
 template <class T>
-hipError_t sample(const SampleArgs& a, const Launcher& L) {
+__global__ __launch_bounds__(256) void k_sample_maxima(SampleArgs a, float* __restrict__ maxima) {
+  constexpr int E = kPerChunk<T>, U = kMaximaChunks;
+  const int64_t r = blockIdx.y;
+  const Row<T> row{static_cast<const T*>(a.logits) + r * a.ld, a.V};
+  const int64_t c0 = (int64_t(blockIdx.x) * (256 * U) + threadIdx.x) * E;
+  float v[U][E];
+  int64_t i[U];
+  int e0[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) e0[u] = row.chunk(c0 + u * 256 * E, a.V, v[u], i[u]);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int e = 0; e < E; ++e) m = MaxNanOp()(m, e >= e0[u] ? v[u][e] : -INFINITY);
+    m = group_all<16>(m, MaxNanOp());
+    const int64_t part = (c0 + u * 256 * E) / (16 * E);
+    if (threadIdx.x % 16 == 0 && part < a.blocks) maxima[r * a.blocks + part] = m;
+  }
+}
+
+template <class T>
+hipError_t sample(SampleArgs a, float* maxima, const Launcher& L) {
+  if (maxima && a.blocks && !a.maxima) {
+    constexpr int64_t kCols = 256 * kMaximaChunks * kPerChunk<T>;
+    L.pre(kSample);
+    hipLaunchKernelGGL(k_sample_maxima<T>, dim3(unsigned((a.V + kCols - 1) / kCols), unsigned(a.N)),
+                       dim3(256), 0, L.stream, a, maxima);
+    L.post(kSample);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    a.maxima = maxima;
+  }
   L.pre(kSample);
   hipLaunchKernelGGL((a.softcap > 0.f ? k_sample<T, true> : k_sample<T, false>), dim3(unsigned(a.N)), dim3(kThreads), 0, L.stream, a);
   L.post(kSample);
@@ -855,8 +891,8 @@ hipError_t sample(const SampleArgs& a, const Launcher& L) {
 
 }  // namespace
 
-hipError_t launch_sample(const SampleArgs& a, const Launcher& L) {
-  return a.dtype == FLCE_F32 ? sample<float>(a, L) : sample<Bf16Bits>(a, L);
+hipError_t launch_sample(const SampleArgs& a, float* maxima, const Launcher& L) {
+  return a.dtype == FLCE_F32 ? sample<float>(a, maxima, L) : sample<Bf16Bits>(a, maxima, L);
 }
 
 }  // namespace flce

@@ -95,16 +95,24 @@ int flce_sample_logits(const void* logits, int64_t ld_logits, int64_t N, int64_t
                        const float* uniforms, float temperature, const float* temperatures,
                        int32_t top_k, const int32_t* top_ks, float top_p, const float* top_ps,
                        float min_p, const float* min_ps, float softcap, int64_t* tokens,
-                       float* logp, void* stream, int dtype) {
+                       float* logp, void* stream, int dtype, void* workspace,
+                       size_t workspace_bytes) {
   const int st = flce_sample_logits_check_args(logits, ld_logits, N, V, uniforms, temperature,
                                                temperatures, top_k, top_ks, top_p, top_ps, min_p,
-                                               min_ps, softcap, tokens, logp, stream, dtype);
+                                               min_ps, softcap, tokens, logp, stream, dtype,
+                                               workspace, workspace_bytes);
   if (st != FLCE_OK || N == 0) return st;
   Range r("flce_sample_logits");
-  const flce::SampleArgs a{logits, ld_logits, N, V, uniforms, {temperatures, temperature},
+  flce::SampleArgs a{logits, ld_logits, N, V, uniforms, {temperatures, temperature},
                            {top_ps, top_p}, {min_ps, min_p}, {top_ks, top_k}, softcap, tokens,
                            logp, dtype, flce::sample_weight_bits(V)};
-  return status_of(flce::launch_sample(a, flce::make_launcher(stream)));
+  float* maxima = nullptr;
+  if (top_ks || top_k > 0 || temperatures || temperature == 0.f) {
+    a.blocks = flce::sample_parts(N, V, dtype);
+    a.block = dtype == FLCE_BF16 ? 128 : 64;
+    if (a.blocks) maxima = static_cast<float*>(workspace);
+  }
+  return status_of(flce::launch_sample(a, maxima, flce::make_launcher(stream)));
 }
 
 int flce_sample(const void* h, const void* W, int64_t N, int64_t H, int64_t V,
@@ -136,7 +144,7 @@ int flce_sample(const void* h, const void* W, int64_t N, int64_t H, int64_t V,
                              {from(top_ks, r), top_k}, softcap, tokens + r, from(logp, r), FLCE_F32,
                              flce::sample_weight_bits(V), z.maxima, blocks,
                              blocks == (V + 63) / 64 ? 64 : 128};
-    e = flce::launch_sample(a, L);
+    e = flce::launch_sample(a, nullptr, L);
     if (e != hipSuccess) return status_of(e);
   }
   return FLCE_OK;

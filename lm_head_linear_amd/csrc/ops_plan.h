@@ -177,6 +177,14 @@ inline int sample_weight_bits(int64_t V) {
   return 62 - log_v < 51 ? 62 - log_v : 51;
 }
 
+// Rows of given logits whose maxima a kernel of its own forms first (parts of 16 chunks of 16
+// bytes): a few long ones, of which top-k or temperature 0 may need no more than those. 0:
+// none. top-p alone reads every logit in any case.
+inline int64_t sample_parts(int64_t N, int64_t V, int dtype) {
+  const int64_t part = dtype == kBF16 ? 128 : 64;
+  return N <= 64 && V >= 16384 ? (V + part - 1) / part : 0;
+}
+
 // Logits of the head form: as many rows at a time as fit these bytes. Their maxima add at most
 // a 64th: 512 MiB in all.
 constexpr int64_t kSampleLogitBytes = int64_t(504) << 20;
@@ -408,7 +416,8 @@ hipError_t launch_linear(const LinearArgs& a, const Launcher& L);
 int64_t linear_max_blocks(const LinearArgs& a);
 hipError_t launch_linear_backward(const LinearPlan& p, const LinearBwdArgs& a, char* ws,
                                   const Launcher& L);
-hipError_t launch_sample(const SampleArgs& a, const Launcher& L);
+// maxima: room for a.blocks of them a row, formed where a.maxima has none; may be null.
+hipError_t launch_sample(const SampleArgs& a, float* maxima, const Launcher& L);
 hipError_t launch_dropout(const DropoutArgs& a, const Launcher& L);
 hipError_t launch_embedding(const EmbedArgs& a, const Launcher& L);
 hipError_t launch_embedding_backward(const EmbedGradArgs& a, const Launcher& L);

@@ -53,13 +53,19 @@ bool settings_ok(const Common& c) {
 
 extern "C" {
 
+size_t flce_sample_logits_workspace_size(int64_t N, int64_t V, int dtype) {
+  if (N < 0 || N > kMaxGrid || V <= 0 || V > kMaxWidth || !is_dtype(dtype)) return 0;
+  const size_t n = align256(size_t(N) * sample_parts(N, V, dtype) * 4);
+  return n ? n : 256;
+}
+
 int flce_sample_logits_check_args(const void* logits, int64_t ld_logits, int64_t N, int64_t V,
                                   const float* uniforms, float temperature,
                                   const float* temperatures, int32_t top_k,
                                   const int32_t* top_ks, float top_p, const float* top_ps,
                                   float min_p, const float* min_ps, float softcap,
                                   const int64_t* tokens, const float* logp, const void* stream,
-                                  int dtype) {
+                                  int dtype, const void* workspace, size_t workspace_bytes) {
   (void)stream;
   if (N < 0 || N > kMaxGrid || V <= 0 || V > kMaxWidth || !is_dtype(dtype)) return FLCE_ERR_ARG;
   if (N > 0 && (!logits || !uniforms || !tokens)) return FLCE_ERR_ARG;
@@ -68,11 +74,15 @@ int flce_sample_logits_check_args(const void* logits, int64_t ld_logits, int64_t
     return FLCE_ERR_ARG;
   const Buf bz = matrix(logits, N, V, ld_logits, esize(dtype)), bu = vec(uniforms, N, 4),
             bt = vec(temperatures, N, 4), bk = vec(top_ks, N, 4), bp = vec(top_ps, N, 4),
-            bm = vec(min_ps, N, 4), bo = vec(tokens, N, 8), bl = vec(logp, N, 4);
-  if (clash({bo, bl}, {bz, bu, bt, bk, bp, bm})) return FLCE_ERR_ARG;
+            bm = vec(min_ps, N, 4), bo = vec(tokens, N, 8), bl = vec(logp, N, 4),
+            wk = vec(workspace, int64_t(workspace_bytes), 1);
+  if (clash({bo, bl, wk}, {bz, bu, bt, bk, bp, bm})) return FLCE_ERR_ARG;
   if (N > max_groups(1024)) return FLCE_ERR_UNSUPPORTED;
   for (const Buf& b : {bz, bu, bt, bk, bp, bm, bo, bl})
     if (misaligned(b)) return FLCE_ERR_UNSUPPORTED;
+  if (!workspace || wk.begin() % 256 != 0 ||
+      workspace_bytes < flce_sample_logits_workspace_size(N, V, dtype))
+    return FLCE_ERR_WORKSPACE;
   return FLCE_OK;
 }
 

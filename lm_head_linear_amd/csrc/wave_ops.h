@@ -108,6 +108,12 @@ struct MaxOp {
   __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
   __device__ __forceinline__ uint32_t operator()(uint32_t a, uint32_t b) const { return a > b ? a : b; }
 };
+// The larger one; NaN if either is.
+struct MaxNanOp {
+  __device__ __forceinline__ float operator()(float a, float b) const {
+    return a != a ? a : b != b ? b : fmaxf(a, b);
+  }
+};
 struct MinOp {
   __device__ __forceinline__ uint32_t operator()(uint32_t a, uint32_t b) const { return a < b ? a : b; }
 };
