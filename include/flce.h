@@ -662,7 +662,9 @@ int flce_dropout_norm_backward(const void* dy, int64_t ld_dy, const void* ds, in
  *   0.044715 z^3))) / 2;  SILU z / (1 + exp(-z))
  * slope [N,O] (dense; NULL: not wanted) gets round(act'(z)), which the backward reads
  * (relu's slope at 0 is 0). weight and bias are dense; x, residual, y have row strides. In
- * place: y may be the residual (same pointer, stride and type). N = 0 does nothing.
+ * place: y may be the residual (same pointer, stride and type). N = 0 does nothing. The same
+ * bits on every run; a row's last bits can differ between calls of other N, whose sums are
+ * split in other places.
  * flce_linear_check_args: FLCE_ERR_ARG for N < 0 or N >= 2^31, I or O outside [1, 2^24], an
  * unknown type or activation, a missing pointer, a row stride below its row or above 2^31,
  * an output that overlaps anything else; FLCE_ERR_UNSUPPORTED for float32 rows with a bf16
@@ -721,8 +723,9 @@ int flce_linear_backward(const void* dy, int64_t ld_dy, const void* x, int64_t l
  * value, or with its array not NULL a device value for each row (float32, top_k int32; the
  * value is then not read): of those, temperatures that are not above 0 take the largest
  * logit, top_p below 0 or NaN count as 0, min_p is moved into [0, 1] (NaN: 0).
- * Logits of -inf have no mass (a softcap leaves them so). A row with a NaN gives token -1 and logp NaN, a row of -inf
- * alone token -1 and logp -inf; next to a +inf only the +inf have mass.
+ * Logits of -inf have no mass (a softcap leaves them so). A row with a NaN gives token -1
+ * and logp NaN, a row of -inf alone token -1 and logp -inf; without a softcap, next to a
+ * +inf only the +inf have mass.
  * Weights are formed in 64-bit floating point and summed as whole multiples of 2^-S of the
  * largest, S = min(51, 62 - ceil(log2 V)): the result does not depend on an order of sums.
  * flce_sample_logits_check_args: FLCE_ERR_ARG for N < 0 or N >= 2^31, V outside [1, 2^24], an

@@ -30,6 +30,14 @@
 // - no filter: one pass sums the weights of each segment.
 // The token is then found in the segment that holds it. A list that does not fit (thousands
 // of equal logits) leaves the row to the selection over the whole row.
+//
+// Top-p without top-k is bound by the vector units: 256 rows of 131072 float32 take 102 us
+// (134 MB; at the memory's rate 26), of which the maximum takes 19, the weights in 64 bits
+// 37, collecting and selecting 27, the token 9. A selection over whole rows, three digits of
+// counts and three of masses, took 239. Keeping each logit's bin as a byte in LDS, so that
+// collecting reads no memory, gave 97, and 2 us more for rows of 32000: not kept. Top-k is
+// bound by latency: one row of 131072 18 us (4 of them the maxima), 128 bf16 rows of 32000
+// with settings of their own 22.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
