@@ -539,17 +539,46 @@ __global__ __launch_bounds__(256) void k_linear_db(BiasGrad<T> b) {
   b.run(blockIdx.x, red);
 }
 
+// One of the backward's products: C[rows][cols] = sum_k B(row, k) A(col, k) in tiles of TS,
+// `segs` segments of k of each (1: whole).
+template <class T>
+struct Product {
+  small::Operand<T> A, B;
+  int64_t K, seg;
+  int64_t tiles, segs;
+  GradOut<T> out;             // segs = 1
+  float* part;                // [segs][rows][cols] otherwise
+  __host__ __device__ int64_t groups() const { return tiles * segs; }
+  template <int FB, int TS, bool DIRECT>
+  __device__ __forceinline__ void run(int64_t i, char* smem) const {
+    const int64_t s = segs > 1 ? i / tiles : 0;
+    small::Operand<T> a = A, b = B;
+    int64_t k = K, a0, b0;
+    if (segs > 1) {
+      const int64_t k0 = s * seg;
+      k = K - k0 < seg ? K - k0 : seg;
+      a.p += k0 * a.ld;                            // form T
+      b.p += FB == 0 ? k0 : k0 * b.ld;
+    }
+    tile_at<TS>(i - s * tiles, tiles_of<TS>(out.cols), tiles_of<TS>(out.rows), a0, b0);
+    small::Acc<TS> acc;
+    small::tile<T, 1, FB, TS, DIRECT>(acc, a, b, a0, b0, k, smem);
+    if (segs > 1)
+      GradOut<float>{part + s * out.rows * out.cols, out.cols, out.rows, out.cols, 0}.store_tile(
+          acc, a0, b0);
+    else
+      out.store_tile(acc, a0, b0);
+  }
+};
+
 // dx's tiles (n1 of them) and dW's (n2), those of the longer k first, the first kind's count
-// padded to a multiple of 8, then db, in one grid.
+// padded to a multiple of 8, then db, in one grid. The mapping of tiles to XCDs goes by a
+// tile's index, so segments of tiles that are no multiple of 8 are dealt a little unevenly.
 template <class T, int TS, bool DIRECT>
-__global__ __launch_bounds__(small::kThreads) void k_linear_grads(
-    int64_t n1, int64_t n2, bool dw_first, small::Operand<T> Wt, small::Operand<T> dz, int64_t O,
-    GradOut<T> dx, small::Operand<T> xt, small::Operand<T> dzt, int64_t N, GradOut<T> dw,
-    BiasGrad<T> db) {
+__global__ __launch_bounds__(small::kThreads) void k_linear_grads(Product<T> dx, Product<T> dw,
+                                                                  bool dw_first, BiasGrad<T> db) {
   __shared__ __attribute__((aligned(1024))) char smem[small::kSmemBytes<TS, DIRECT>];
-  const int64_t b = blockIdx.x;
-  int64_t a0, b0;
-  small::Acc<TS> acc;
+  const int64_t b = blockIdx.x, n1 = dx.groups(), n2 = dw.groups();
   const int64_t first = ((dw_first ? n2 : n1) + 7) / 8 * 8, second = dw_first ? n1 : n2;
   if (b >= first + second) {
     db.run(b - first - second, reinterpret_cast<float (*)[17]>(smem));
@@ -558,14 +587,43 @@ __global__ __launch_bounds__(small::kThreads) void k_linear_grads(
   const bool is_dw = (b < first) == dw_first;
   const int64_t t = b < first ? b : b - first;
   if (t >= (is_dw ? n2 : n1)) return;
-  if (!is_dw) {
-    tile_at<TS>(t, tiles_of<TS>(dx.cols), tiles_of<TS>(dx.rows), a0, b0);
-    small::tile<T, 1, 0, TS, DIRECT>(acc, Wt, dz, a0, b0, O, smem);
-    dx.store_tile(acc, a0, b0);
+  if (is_dw) dw.template run<1, TS, DIRECT>(t, smem);
+  else dx.template run<0, TS, DIRECT>(t, smem);
+}
+
+// The partial products of split products added up, in order: dx's n1 groups of 256 chunks of
+// four values, then dW's.
+template <class T>
+__global__ __launch_bounds__(256) void k_linear_join(Product<T> dx, Product<T> dw, int64_t n1) {
+  const bool is_dw = int64_t(blockIdx.x) >= n1;
+  const Product<T>& p = is_dw ? dw : dx;
+  const int64_t cols = p.out.cols, n = p.out.rows * cols;
+  const int64_t i = ((int64_t(blockIdx.x) - (is_dw ? n1 : 0)) * 256 + threadIdx.x) * 4;
+  if (i >= n) return;
+  float v[4];
+  load_chunk(p.part, i, n, v);
+#pragma unroll 4
+  for (int64_t s = 1; s < p.segs; ++s) {
+    float o[4];
+    load_chunk(p.part + s * n, i, n, o);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] += o[e];
+  }
+  const int64_t r = i / cols, c = i - r * cols;
+  if (c + 4 <= cols) {
+    T* row = p.out.p + r * p.out.ld;
+    if (p.out.accumulate) {
+      float o[4];
+      load4(row, c, cols, o);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] += o[e];
+    }
+    store4(row, c, cols, v);
   } else {
-    tile_at<TS>(t, tiles_of<TS>(dw.cols), tiles_of<TS>(dw.rows), a0, b0);
-    small::tile<T, 1, 1, TS, DIRECT>(acc, xt, dzt, a0, b0, N, smem);
-    dw.store_tile(acc, a0, b0);
+    for (int e = 0; e < 4 && i + e < n; ++e) {
+      T* at = p.out.p + (i + e) / cols * p.out.ld + (i + e) % cols;
+      *at = from_f32<T>(p.out.accumulate ? to_f32(*at) + v[e] : v[e]);
+    }
   }
 }
 
@@ -629,14 +687,12 @@ bool aligned16(std::initializer_list<const void*> ptrs, std::initializer_list<in
   return true;
 }
 
-// run(the tile's edge, whether its loads are direct) for a product of n tiles of 128 x 128.
+// run(the tile's edge, whether its loads are direct).
 template <class T, class F>
-void with_tile(int64_t n, bool direct, F&& run) {
-  auto go = [&](auto edge) {
-    direct ? run(edge, std::true_type{}) : run(edge, std::false_type{});
-  };
-  if (n >= kLinearWholeTiles) go(std::integral_constant<int, 128>{});
-  else if (sizeof(T) == 2 || n >= kLinearQuarterTiles) go(std::integral_constant<int, 64>{});
+void with_tile(int64_t edge, bool direct, F&& run) {
+  auto go = [&](auto e) { direct ? run(e, std::true_type{}) : run(e, std::false_type{}); };
+  if (edge == 128) go(std::integral_constant<int, 128>{});
+  else if (edge == 64) go(std::integral_constant<int, 64>{});
   else if constexpr (sizeof(T) == 4) go(std::integral_constant<int, 32>{});
 }
 
@@ -731,7 +787,7 @@ hipError_t forward(const LinearArgs& a, const Launcher& L) {
     }
   }
   const bool direct = aligned16<T>({a.x, a.weight}, {a.I, a.ld_x});
-  with_tile<T>(tiles_of<128>(a.O) * tiles_of<128>(a.N), direct, [&](auto ts, auto di) {
+  with_tile<T>(linear_tile(tiles_of<128>(a.O) * tiles_of<128>(a.N), a.dtype), direct, [&](auto ts, auto di) {
     constexpr int TS = decltype(ts)::value;
     const dim3 grid(unsigned(tiles_of<TS>(a.O) * tiles_of<TS>(a.N)));
     hipLaunchKernelGGL((k_linear<T, OT, TS, decltype(di)::value>), grid, dim3(small::kThreads), 0,
@@ -807,25 +863,35 @@ hipError_t backward(const LinearPlan& p, const LinearBwdArgs& a, char* ws, const
     }
   }
   L.pre(kLinearGrad);
-  const int64_t n = tiles_of<128>(a.I) * ((a.dx ? tiles_of<128>(a.N) : 0) +
-                                          (a.dweight ? tiles_of<128>(a.O) : 0));
   bool direct = aligned16<T>({g}, {ld_g, a.I});
   if (a.dx) direct = direct && aligned16<T>({a.weight}, {});
   if (a.dweight) direct = direct && aligned16<T>({x}, {a.ld_x, a.O});
-  with_tile<T>(n, direct, [&](auto ts, auto di) {
+  Product<T> dx{{static_cast<const T*>(a.weight), a.I, a.I}, {g, ld_g, a.N}, a.O, p.dx.seg, 0,
+                p.dx.segs, {static_cast<T*>(a.dx), a.ld_dx, a.N, a.I, 0},
+                reinterpret_cast<float*>(ws + p.off_dx)};
+  Product<T> dw{{x, a.ld_x, a.I}, {g, ld_g, a.O}, a.N, p.dw.seg, 0, p.dw.segs,
+                {static_cast<T*>(a.dweight), a.I, a.O, a.I, a.accumulate},
+                reinterpret_cast<float*>(ws + p.off_dw)};
+  const bool dw_first = a.N > a.O;
+  with_tile<T>(p.tile, direct, [&](auto ts, auto di) {
     constexpr int TS = decltype(ts)::value;
-    const int64_t n1 = a.dx ? tiles_of<TS>(a.I) * tiles_of<TS>(a.N) : 0;
-    const int64_t n2 = a.dweight ? tiles_of<TS>(a.I) * tiles_of<TS>(a.O) : 0;
-    const bool dw_first = a.N > a.O;
+    if (a.dx) dx.tiles = tiles_of<TS>(a.I) * tiles_of<TS>(a.N);
+    if (a.dweight) dw.tiles = tiles_of<TS>(a.I) * tiles_of<TS>(a.O);
+    const int64_t n1 = dx.groups(), n2 = dw.groups();
     const int64_t tiles = ((dw_first ? n2 : n1) + 7) / 8 * 8 + (dw_first ? n1 : n2);
-    hipLaunchKernelGGL((k_linear_grads<T, TS, decltype(di)::value>), dim3(unsigned(tiles + db.groups())),
-                       dim3(small::kThreads), 0, L.stream, n1, n2, dw_first,
-                       small::Operand<T>{static_cast<const T*>(a.weight), a.I, a.I},
-                       small::Operand<T>{g, ld_g, a.N}, a.O,
-                       GradOut<T>{static_cast<T*>(a.dx), a.ld_dx, a.N, a.I, 0},
-                       small::Operand<T>{x, a.ld_x, a.I}, small::Operand<T>{g, ld_g, a.O}, a.N,
-                       GradOut<T>{static_cast<T*>(a.dweight), a.I, a.O, a.I, a.accumulate}, db);
+    hipLaunchKernelGGL((k_linear_grads<T, TS, decltype(di)::value>),
+                       dim3(unsigned(tiles + db.groups())), dim3(small::kThreads), 0, L.stream, dx,
+                       dw, dw_first, db);
   });
+  L.post(kLinearGrad);
+  e = hipGetLastError();
+  auto join_groups = [](const Product<T>& q) {
+    return q.tiles && q.segs > 1 ? (q.out.rows * q.out.cols + 1023) / 1024 : 0;
+  };
+  const int64_t j1 = join_groups(dx), j2 = join_groups(dw);
+  if (e != hipSuccess || j1 + j2 == 0) return e;
+  L.pre(kLinearGrad);
+  hipLaunchKernelGGL(k_linear_join<T>, dim3(unsigned(j1 + j2)), dim3(256), 0, L.stream, dx, dw, j1);
   L.post(kLinearGrad);
   return hipGetLastError();
 }

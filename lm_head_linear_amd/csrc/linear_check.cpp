@@ -6,6 +6,20 @@
 namespace flce {
 
 namespace {
+// Half of the CUs' worth of tiles or more are left whole; others are cut until two workgroups
+// stand on each CU, with eight stages at least to a segment.
+LinearSplit split(int64_t tiles, int64_t K, int64_t stage) {
+  LinearSplit s;
+  const int64_t stages = ceil_div(K, stage);
+  if (tiles <= 0 || tiles >= 128) return s;
+  int64_t n = 512 / tiles;
+  if (n > stages / 8) n = stages / 8;
+  if (n < 2) return s;
+  s.seg = ceil_div(stages, n) * stage;
+  s.segs = ceil_div(K, s.seg);
+  return s;
+}
+
 bool sizes_ok(int64_t N, int64_t I, int64_t O) {
   return N >= 0 && N <= kMaxGrid && I > 0 && I <= kMaxWidth && O > 0 && O <= kMaxWidth;
 }
@@ -15,12 +29,19 @@ bool make_linear_plan(int64_t N, int64_t I, int64_t O, int dtype, LinearPlan* ou
   if (!sizes_ok(N, I, O) || !is_dtype(dtype)) return false;
   LinearPlan p;
   // 64 rows a workgroup where that leaves four of them for each CU, otherwise fewer
-  const int64_t cols = ceil_div(O * int64_t(esize(dtype)), 512);
-  for (p.dz_rows = 64; p.dz_rows > 8 && cols * ceil_div(N, p.dz_rows) < 1024;) p.dz_rows /= 2;
+  const int64_t groups = ceil_div(O * int64_t(esize(dtype)), 512);
+  for (p.dz_rows = 64; p.dz_rows > 8 && groups * ceil_div(N, p.dz_rows) < 1024;) p.dz_rows /= 2;
   p.dz_parts = ceil_div(N, p.dz_rows);
   size_t off = 0;
   p.off_dz = off; off = align256(off + size_t(N) * O * esize(dtype));
   p.off_part = off; off = align256(off + size_t(p.dz_parts) * O * 4);
+  const int64_t n128 = ceil_div(I, 128) * (ceil_div(N, 128) + ceil_div(O, 128));
+  p.tile = linear_tile(n128, dtype);
+  const int64_t stage = 128 / int64_t(esize(dtype)), cols = ceil_div(I, p.tile);
+  p.dx = split(cols * ceil_div(N, p.tile), O, stage);
+  p.dw = split(cols * ceil_div(O, p.tile), N, stage);
+  p.off_dx = off; if (p.dx.segs > 1) off = align256(off + size_t(p.dx.segs) * N * I * 4);
+  p.off_dw = off; if (p.dw.segs > 1) off = align256(off + size_t(p.dw.segs) * O * I * 4);
   p.total = off ? off : 256;
   *out = p;
   return true;
@@ -86,7 +107,7 @@ int flce_linear_backward_check_args(const void* dy, int64_t ld_dy, const void* x
             bdx = matrix(dx, N, I, ld_dx, es), bdw = matrix(dweight, O, I, I, es),
             bdb = vec(dbias, O, es), wk = vec(workspace, int64_t(workspace_bytes), 1);
   if (clash({bdx, bdw, bdb, wk}, {bg, bx, bw, bs})) return FLCE_ERR_ARG;
-  if (tiles(I, N) + 8 + tiles(I, O) + ceil_div(O, 16) > max_groups(256) ||
+  if (tiles(I, N) + 1024 + tiles(I, O) + ceil_div(O, 16) > max_groups(256) ||
       ceil_div(O, 128) * p.dz_parts > max_groups(256))
     return FLCE_ERR_UNSUPPORTED;
   for (const Buf& b : {bg, bx, bw, bs, bdx, bdw, bdb})

@@ -135,11 +135,25 @@ constexpr int64_t kLinearWholeTiles = 384;
 // ... and of float32, below which it takes tiles of 32 x 32.
 constexpr int64_t kLinearQuarterTiles = 64;
 
+// A gradient's product of rows x cols over k: split along k into segments of `seg` (a multiple
+// of a stage) where its tiles leave CUs without work, each a partial product of its own.
+struct LinearSplit {
+  int64_t segs = 1, seg = 0;
+};
+
 struct LinearPlan {
   int64_t dz_rows = 8;        // rows of dz a workgroup forms (and adds up for db)
   int64_t dz_parts = 0;       // workgroups along the rows
-  size_t off_dz = 0, off_part = 0, total = 0;
+  int64_t tile = 0;           // edge of the products' tiles, unless they run on the head's
+  LinearSplit dx, dw;
+  size_t off_dz = 0, off_part = 0, off_dx = 0, off_dw = 0, total = 0;
 };
+
+// The edge of the tiles of a product of n tiles of 128 x 128.
+inline int64_t linear_tile(int64_t n, int dtype) {
+  if (n >= kLinearWholeTiles) return 128;
+  return dtype == kBF16 || n >= kLinearQuarterTiles ? 64 : 32;
+}
 
 bool make_linear_plan(int64_t N, int64_t I, int64_t O, int dtype, LinearPlan* p);
 

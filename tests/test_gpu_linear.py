@@ -320,3 +320,21 @@ def test_streams_and_refusals():
         m.flce_linear(x, w, residual=r, activation="silu", slope=r.view(torch.float16))
     with pytest.raises(m.FlceError):
         m.flce_linear(x.float(), w.float(), y_dtype=torch.bfloat16)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("N,I,O", [(7110, 495, 211), (79, 130, 3428), (3000, 64, 64), (5000, 33, 7), (130, 72, 2048)])
+def test_split_gradients(dt, N, I, O):
+    """Products of few tiles and a long k, cut into segments: both, one of them, added to."""
+    import lm_head_linear_amd as m
+    check(N, I, O, dt, "silu", True, False)
+    x, w, _, _, dy = make(N, I, O, dt, 3)
+    a = m.flce_linear_backward(dy, x, w)
+    b = m.flce_linear_backward(dy, x, w, want_dx=False, bias=False)
+    c = m.flce_linear_backward(dy, x, w, want_dweight=False, bias=False)
+    assert torch.equal(a[1], b[1]) and torch.equal(a[0], c[0])
+    big = torch.full((N, I + 5), 7.0, device="cuda").to(dt)
+    d = m.flce_linear_backward(dy, x, w, dx=big[:, 2:2 + I], dweight=torch.zeros_like(w),
+                               dbias=torch.zeros(O, device="cuda", dtype=dt), accumulate=True)
+    assert all(torch.equal(p, q) for p, q in zip(a, d))
+    assert bool((big[:, :2] == 7).all()) and bool((big[:, 2 + I:] == 7).all())
