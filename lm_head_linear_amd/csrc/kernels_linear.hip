@@ -11,8 +11,12 @@
 //
 // Products of bf16 rows whose lengths and addresses are multiples of 16 bytes, with enough
 // tiles of 256 x 256 to fill the chip, run on the head's product (gemm_bf16.h); others
-// on the one of 128 x 128 or 64 x 64 tiles (gemm_small.h). Up to 64 rows forward, where
-// reading W is all there is to it, take k_linear_few, or (a wide W: a head) k_linear_wide.
+// on the one of smaller tiles (gemm_small.h; 2048 x 1024 x 1024: forward 20 us on 128 x 128
+// tiles, 13 on 64 x 64). 8192 x 4096 x 4096, both directions: 730 us, of which the forward
+// takes 267 to 284, the gradients' products 441 to 478, dz 46; all on 128 x 128 tiles, before
+// those had direct loads, 1058. Few rows forward,
+// where reading W is all there is to it, take k_linear_few (up to 64), or, for a wide W (a
+// head), k_linear_wide (up to 128).
 #include <hip/hip_runtime.h>
 
 #include <cstdint>

@@ -22,11 +22,16 @@
 // round(r + keep x scale), and the backward writes two rows, the sum's gradient for the
 // residual and the masked one for x.
 //
-// bf16 with the residual, 8192 rows of 4096: forward 50 us (268 MB, 5.4 TB/s), backward
-// 56 us (4.8 TB/s) and 7 us for dw. Both directions together, with this many threads
-// and with others: 8192 x 4096, 256 threads 112 us (64: 211, 1024: 151); 16384 x 1024,
-// 128 threads 49 (64: 54); 32768 x 512, 64 threads 48 (32: 53); 65536 x 128, 16 threads
-// 29 (32: 40, one row a 64-thread workgroup: 126).
+// Rows of whole chunks are loaded without conditions, all before the first value is used: a
+// branch around a load has it waited for before the next.
+//
+// bf16 with the residual, 8192 rows of 4096, in a training step: forward 43 us, backward 56
+// (268 MB each) and 7 for dw; with dropout 48 and 63 (335 MB; loads with conditions 54 and
+// 98). Both directions together, on rows that the last pass left in the caches, by threads a
+// row: 8192 x 4096, 256 threads 102 us; 16384 x 1024, 128 threads 48; 32768 x 512, 64
+// threads 47; 65536 x 128, 16 threads 28. With conditional loads those took 112, 49, 48 and
+// 29, and other counts: 64 threads 211 and 1024 151; 64 threads 54; 32 threads 53; 32 threads
+// 40, and one row a 64-thread workgroup 126.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>

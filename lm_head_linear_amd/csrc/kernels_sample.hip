@@ -22,8 +22,8 @@
 // - top-k: the k-th largest of the threads' own maxima is a bound that few logits but the
 //   first k pass (where the maxima of each 64 or 128 logits are at hand, from the head's
 //   product or, for few long rows, a kernel before this one, those are read in the logits'
-//   place, and the parts that reach the bound). Those are collected in LDS, in index order, and everything else is done
-//   on the list. min-p alone bounds the list in the same way.
+//   place, and the parts that reach the bound). Those are collected in LDS, in index
+//   order, and everything else is done on the list. min-p alone bounds the list in the same way.
 // - top-p without top-k: one pass forms all weights and adds them up by bins of an eighth
 //   of a power of two, for each wave; the bin in which the mass passes p is then collected,
 //   and the selection runs on that.
@@ -37,7 +37,7 @@
 // counts and three of masses, took 239. Keeping each logit's bin as a byte in LDS, so that
 // collecting reads no memory, gave 97, and 2 us more for rows of 32000: not kept. Top-k is
 // bound by latency: one row of 131072 18 us (4 of them the maxima), 128 bf16 rows of 32000
-// with settings of their own 22.
+// with settings of their own 22 to 28, by the settings drawn.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
