@@ -29,7 +29,8 @@
 //   and the selection runs on that.
 // - no filter: one pass sums the weights of each segment.
 // The token is then found in the segment that holds it. A list that does not fit (thousands
-// of equal logits) leaves the row to the selection over the whole row.
+// of equal logits, or a k near the 1024 threads, whose bound then keeps a good part of a long
+// row) or a k above them leaves the row to the selection over the whole row.
 //
 // Top-p without top-k is bound by the vector units: 256 rows of 131072 float32 take 102 us
 // (134 MB; at the memory's rate 26), of which the maximum takes 19, the weights in 64 bits
@@ -642,10 +643,19 @@ __global__ __launch_bounds__(kThreads) void k_sample(SampleArgs a) {
   const int64_t V = a.V, part = (V + kWaves - 1) / kWaves, seg = (part + E - 1) / E * E;
   const int64_t from = wave * seg, to = from + seg < V ? from + seg : V;
 
+  const float T_ = a.temperature.at(r), uniform = a.uniforms[r];
+  int64_t k = a.top_k.at(r);
+  if (k <= 0 || k > V) k = V;
+  if (!(T_ > 0.f)) k = 1;
+
   // the largest logit; a row of -inf alone or with a NaN has no token
   float most = -INFINITY;
   bool nan = false;
-  const float* maxima = a.maxima ? a.maxima + r * a.blocks : nullptr;
+  // fewer parts than k bound nothing: then the threads' own maxima, of which there are more
+  // (one capped bf16 row of 56291, 440 parts: top-500 85 -> 38 us, top-900 91 -> 43; where the
+  // list then overflows, top-1000, 90 -> 104)
+  const bool few_parts = k > a.blocks && k <= kThreads && k < V;
+  const float* maxima = a.maxima && !few_parts ? a.maxima + r * a.blocks : nullptr;
   const int64_t bseg = (a.blocks + kWaves - 1) / kWaves;
   if (maxima) {
     for (int64_t b = wave * bseg + lane; b < (wave + 1) * bseg && b < a.blocks; b += 64) {
@@ -681,10 +691,6 @@ __global__ __launch_bounds__(kThreads) void k_sample(SampleArgs a) {
     return;
   }
 
-  const float T_ = a.temperature.at(r), uniform = a.uniforms[r];
-  int64_t k = a.top_k.at(r);
-  if (k <= 0 || k > V) k = V;
-  if (!(T_ > 0.f)) k = 1;
   Weights<CAP> wt;
   wt.cap = a.softcap;
   wt.two_inv_cap = a.softcap > 0.f ? 2.0 / a.softcap : 0.0;

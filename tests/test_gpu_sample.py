@@ -250,6 +250,16 @@ def test_from_a_wide_head(N, H, V):
     assert bool((r.tokens == 0).all())
 
 
+@pytest.mark.parametrize("N,V,dt", [(1, 56291, torch.bfloat16), (3, 20000, torch.float32),
+                                    (64, 16384, torch.bfloat16)])
+@pytest.mark.parametrize("k", [100, 130, 500, 1000, 1024, 1025, 2000])
+def test_more_ranks_than_parts(N, V, dt, k):
+    """Few long rows have the maxima of their parts at hand; a k beyond their number."""
+    z, u = make(N, V, dt, V + k)
+    for cap in (0.0, 30.0):
+        compare(run(z, u, T=1.3, k=k, p=0.7, cap=cap), z, u, T=1.3, k=k, p=0.7, cap=cap)
+
+
 def test_rows_in_parts_of_the_workspace():
     """More rows than the logits' 512 MiB hold at once: each row is what it is alone."""
     import lm_head_linear_amd as m
