@@ -661,10 +661,10 @@ int flce_dropout_norm_backward(const void* dy, int64_t ld_dy, const void* ds, in
  *   NONE z;  RELU max(z, 0);  GELU z Phi(z);  GELU_TANH z (1 + tanh(sqrt(2/pi) (z +
  *   0.044715 z^3))) / 2;  SILU z / (1 + exp(-z))
  * slope [N,O] (dense; NULL: not wanted) gets round(act'(z)), which the backward reads
- * (relu's slope at 0 is 0). weight and bias are dense; x, residual, y have row strides. In
- * place: y may be the residual (same pointer, stride and type). N = 0 does nothing. The same
- * bits on every run; a row's last bits can differ between calls of other N, whose sums are
- * split in other places.
+ * (relu's slope at 0 is 0, NONE's is 1). weight and bias are dense; x, residual, y have row
+ * strides. In place: y may be the residual (same pointer, stride and type). N = 0 does
+ * nothing. The same bits on every run; a row's last bits can differ between calls of other
+ * N, whose sums are split in other places.
  * flce_linear_check_args: FLCE_ERR_ARG for N < 0 or N >= 2^31, I or O outside [1, 2^24], an
  * unknown type or activation, a missing pointer, a row stride below its row or above 2^31,
  * an output that overlaps anything else; FLCE_ERR_UNSUPPORTED for float32 rows with a bf16

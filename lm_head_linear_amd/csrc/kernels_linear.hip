@@ -200,7 +200,7 @@ struct Finish {
           v[e] = a.y + t[j][i][e];
           d[e] = a.slope;
         }
-        if (ACT != FLCE_ACT_NONE && slope) store4_at<WHOLE>(slope, O, r, c, N, O, d);
+        if (slope) store4_at<WHOLE>(slope, O, r, c, N, O, d);
         store4_at<WHOLE>(y, ld_y, r, c, N, O, v);
       }
   }
@@ -415,7 +415,7 @@ struct EpiLinear {
         y[k] = a.y;
         d[k] = a.slope;
       }
-      if (ACT != FLCE_ACT_NONE && e.fin.slope) store4(e.fin.slope + r * e.fin.O, c, e.fin.O, d);
+      if (e.fin.slope) store4(e.fin.slope + r * e.fin.O, c, e.fin.O, d);
       if (e.res) {
         const uint2 o = res[i & 1][q];
         y[0] += bf16_to_f32(uint16_t(o.x));
