@@ -60,7 +60,8 @@ __device__ __forceinline__ Activated activate(float z) {
     return {z * P, fmaf(z * 0.39894228f, E, P)};
   } else if constexpr (ACT == FLCE_ACT_GELU_TANH) {
     constexpr float k = 1.5957691216f, c = 0.044715f;         // 2 sqrt(2 / pi)
-    const float zz = z * z, s = sigma<FAST>(k * z * fmaf(c, zz, 1.f));
+    // an infinite square would make the slope 0 times infinity; sigma is 0 or 1 long before
+    const float zz = fminf(z * z, 1e20f), s = sigma<FAST>(k * z * fmaf(c, zz, 1.f));
     return {z * s, fmaf(z * s * (1.f - s), k * fmaf(3.f * c, zz, 1.f), s)};
   } else if constexpr (ACT == FLCE_ACT_SILU) {
     const float s = sigma<FAST>(z);

@@ -1,5 +1,6 @@
 """Calls of the linear transform beside its usual ones: a slope asked for without an
-activation, on each kernel that a size selects."""
+activation, on each kernel that a size selects, and arguments whose square leaves
+float32."""
 import pytest
 import torch
 
@@ -48,3 +49,18 @@ def test_slope_without_an_activation_is_one(N, I, O, dt):
     # the gradients are those of no slope: dz is dy
     for a, b in zip(m.flce_linear_backward(dy, x, w, slope), m.flce_linear_backward(dy, x, w)):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("N", [12, 300])
+@pytest.mark.parametrize("act", ["relu", "gelu", "gelu_tanh", "silu"])
+def test_arguments_of_any_finite_size(act, N, dt):
+    """From 1e4 on every activation is z or zero and its slope one or zero in float32 (each
+    factor's exponent is beyond 2^-149), up to the largest z, whose square is infinite."""
+    import lm_head_linear_amd as m
+    z = torch.tensor([1e4, 1e10, 1e18, 1.9e19, 1e25, 3e38], device="cuda")
+    z = torch.cat([z, -z]).repeat((N + 11) // 12)[:N, None].to(dt)
+    one = torch.ones(1, 1, device="cuda", dtype=dt)
+    y, slope = m.flce_linear(z, one, activation=act, save_slope=True)
+    assert torch.equal(y, torch.where(z > 0, z, torch.zeros_like(z)))
+    assert torch.equal(slope, (z > 0).to(slope.dtype))
