@@ -683,10 +683,15 @@ class TiedLMHead(torch.nn.Module):
     def sample(self, x: torch.Tensor, uniforms: torch.Tensor,
                residual: Optional[torch.Tensor] = None, **kw) -> Sampled:
         """:func:`flce_sample` of the normalised rows of x [..., H] from uniforms [...];
-        settings given as tensors have the uniforms' shape."""
+        settings given as tensors have the uniforms' shape, and so have ``tokens`` and
+        ``logp`` where passed in (contiguous: they are written in place)."""
         n = self.rows(x, residual)
         flat = lambda v: v.reshape(-1).contiguous() if isinstance(v, torch.Tensor) else v  # noqa: E731
+        for name in ("tokens", "logp"):
+            if kw.get(name) is not None and not kw[name].is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+        workspace = kw.pop("workspace", None)
         r = flce_sample(n.reshape(-1, n.shape[-1]).contiguous(), self.weight.contiguous(),
                         flat(uniforms), softcap=self.criterion.logit_softcapping,
-                        **{k: flat(v) for k, v in kw.items()})
+                        workspace=workspace, **{k: flat(v) for k, v in kw.items()})
         return Sampled(*(t.view(uniforms.shape) for t in r))
