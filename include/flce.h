@@ -755,8 +755,8 @@ int flce_sample_logits(const void* logits, int64_t ld_logits, int64_t N, int64_t
 /*
  * flce_sample -- flce_sample_logits of the logits z = h . W^T (float32) of the head W [V,H]
  * at N rows h [N,H] (dense, `dtype`). The logits live in the workspace, as many rows at a
- * time as fit 512 MiB with their maxima: flce_sample_workspace_size bytes (0 for invalid
- * sizes), 256-byte aligned. Errors as flce_sample_logits and flce_linear, and FLCE_ERR_WORKSPACE.
+ * time as fit 512 MiB with their maxima and one grid (2^22 - 1; N itself may be larger):
+ * flce_sample_workspace_size bytes (0 for invalid sizes), 256-byte aligned. Errors as flce_sample_logits and flce_linear, and FLCE_ERR_WORKSPACE.
  */
 size_t flce_sample_workspace_size(int64_t N, int64_t H, int64_t V, int dtype);
 int flce_sample_check_args(const void* h, const void* W, int64_t N, int64_t H, int64_t V,

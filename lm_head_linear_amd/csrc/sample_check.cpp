@@ -12,7 +12,9 @@ bool make_sample_plan(int64_t N, int64_t H, int64_t V, int dtype, SamplePlan* ou
       !is_dtype(dtype))
     return false;
   SamplePlan p;
-  const int64_t fit = kSampleLogitBytes / (V * 4);
+  // rows of a pass: a workgroup of 1024 threads each
+  int64_t fit = kSampleLogitBytes / (V * 4);
+  if (fit > max_groups(1024)) fit = max_groups(1024);
   p.rows = N < fit ? N : fit;
   if (p.rows < 1) p.rows = 1;
   p.off_max = align256(size_t(p.rows) * V * 4);
