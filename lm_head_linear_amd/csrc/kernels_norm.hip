@@ -22,16 +22,16 @@
 // round(r + keep x scale), and the backward writes two rows, the sum's gradient for the
 // residual and the masked one for x.
 //
-// Rows of whole chunks are loaded without conditions, all before the first value is used: a
-// branch around a load has it waited for before the next.
+// Rows of whole chunks are loaded without conditions, all before the first value is used, in
+// the forward, with dropout, and elsewhere where it pays (kLoadsAhead): a branch around a
+// load has it waited for before the next.
 //
-// bf16 with the residual, 8192 rows of 4096, in a training step: forward 43 us, backward 56
-// (268 MB each) and 7 for dw; with dropout 48 and 63 (335 MB; loads with conditions 54 and
-// 98). Both directions together, on rows that the last pass left in the caches, by threads a
-// row: 8192 x 4096, 256 threads 102 us; 16384 x 1024, 128 threads 48; 32768 x 512, 64
-// threads 47; 65536 x 128, 16 threads 28. With conditional loads those took 112, 49, 48 and
-// 29, and other counts: 64 threads 211 and 1024 151; 64 threads 54; 32 threads 53; 32 threads
-// 40, and one row a 64-thread workgroup 126.
+// bf16 with the residual, 8192 rows of 4096: forward 40 us, backward 57 with dw's 7 (268 MB
+// each); with dropout 42 and 79 (335 MB; loads with conditions 44 and 107). Both directions
+// together, by threads a row: 8192 x 4096, 256 threads 97 us; 16384 x 1024, 128 threads 48;
+// 32768 x 512, 64 threads 47; 65536 x 128, 16 threads 28. With conditional loads those took
+// 103, 50, 48 and 30, and other counts: 64 threads 211 and 1024 151; 64 threads 54; 32 threads
+// 53; 32 threads 40, and one row a 64-thread workgroup 126.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -197,8 +197,9 @@ __global__ __launch_bounds__(kBlock<LANES>) void k_rms_norm(
 // workgroup's share of dw (DW) in dw_part[blockIdx.x][H], its R rows' shares joined in
 // LDS. C = 0: rows of any length; dw's share is then added up in memory (each thread its
 // own columns). DROP: d, the gradient of the sum, goes to dres (null: not wanted), and dx
-// gets keep d scale.
-template <class T, class WT, int LANES, int C, bool DS, bool DW, bool DROP>
+// gets keep d scale. WHOLE: rows of whole chunks, loaded without conditions (with DROP that
+// is found at run time).
+template <class T, class WT, int LANES, int C, bool DS, bool DW, bool DROP, bool WHOLE>
 __global__ __launch_bounds__(kBlock<LANES>) void k_rms_norm_bwd(
     const T* dy, int64_t lddy, const T* ds, int64_t ldds, const T* __restrict__ s, int64_t lds,
     const WT* __restrict__ w, const float* __restrict__ rstd, int64_t N, int64_t H, float offset,
@@ -220,7 +221,7 @@ __global__ __launch_bounds__(kBlock<LANES>) void k_rms_norm_bwd(
     for (int e = 0; e < E; ++e) f[e] += offset;
   };
   const float inv_h = 1.f / float(H);
-  const bool whole = H % E == 0;
+  const bool whole = DROP ? H % E == 0 : WHOLE;
   DropKey key{};
   if constexpr (DROP) key = drop_key(drop);
   // a bit for each value of a chunk that stays
@@ -306,7 +307,9 @@ __global__ __launch_bounds__(kBlock<LANES>) void k_rms_norm_bwd(
           const float v = q * (g[k][e] - n[k][e] * mean);
           g[k][e] = DS ? d[k][e] + v : v;
         }
-        store_grads(row, (int64_t(k) * LANES + tid) * E, live ? H : 0, g[k], bits[k]);
+        const int64_t c = (int64_t(k) * LANES + tid) * E;
+        if constexpr (DROP) store_grads(row, c, live ? H : 0, g[k], bits[k]);
+        else store_chunk(dx + row * lddx, c, live ? H : 0, g[k]);
       }
     }
     if (DW) {
@@ -396,6 +399,18 @@ __global__ __launch_bounds__(1024) void k_rms_norm_dw(const float* __restrict__ 
   }
 }
 
+// Whether the backward without dropout of rows of whole chunks loads all of them before the
+// first is used. Where registers are short, or a row's loads are few, that costs more than
+// the wait it saves. us with conditional loads and without, bf16: 2048 x 8192 (four chunks
+// for each of 256 threads) 60 and 55 with ds and dw, 28 and 24 with ds, 22 and 18 with
+// neither; 8192 x 4096 (two) 61 and 57 with both, 39 and 41, 30 and 31; 4096 x 16384 (four
+// for each of 1024 threads) 691 and 522 with both, 382 and 480 with dw, 222 and 230 with ds,
+// 99 and 106. float32: 8192 x 4096 107 and 114 with both, 32768 x 512 29 and 31 with neither,
+// the same elsewhere.
+template <class T, int LANES, int C, bool DS, bool DW, bool DROP>
+constexpr bool kLoadsAhead =
+    !DROP && C > 0 && sizeof(T) == 2 && (LANES == 1024 ? DS && DW : C != 2 || DW);
+
 // Calls run(lanes, chunks) with the integral constants of the variant for rows
 // of n chunks.
 template <int I>
@@ -465,10 +480,16 @@ hipError_t norm_backward(const NormBwdArgs& a, const Launcher& L) {
     auto go = [&](auto has_ds, auto has_dw, auto has_drop) {
       constexpr bool DS = decltype(has_ds)::value, DW = decltype(has_dw)::value;
       constexpr bool DROP = decltype(has_drop)::value;
-      hipLaunchKernelGGL((k_rms_norm_bwd<T, WT, LN, C, DS, DW, DROP>), dim3(unsigned(nb)),
-                         dim3(kBlock<LN>), 0, L.stream, dy, a.ld_dy, ds, a.ld_ds, s, a.ld_s, w, a.rstd, a.N, a.H,
-                         a.offset, dx, a.ld_dx, a.dw_part, static_cast<T*>(a.dres), a.ld_dres,
-                         DROP ? *a.drop : DropSpec{});
+      auto launch = [&](auto whole) {
+        hipLaunchKernelGGL((k_rms_norm_bwd<T, WT, LN, C, DS, DW, DROP, decltype(whole)::value>),
+                           dim3(unsigned(nb)), dim3(kBlock<LN>), 0, L.stream, dy, a.ld_dy, ds, a.ld_ds, s,
+                           a.ld_s, w, a.rstd, a.N, a.H, a.offset, dx, a.ld_dx, a.dw_part,
+                           static_cast<T*>(a.dres), a.ld_dres, DROP ? *a.drop : DropSpec{});
+      };
+      if constexpr (kLoadsAhead<T, LN, C, DS, DW, DROP>) {
+        if (a.H % kPerChunk<T> == 0) return launch(std::true_type{});
+      }
+      launch(std::false_type{});
     };
     using Y = std::true_type;
     using No = std::false_type;
