@@ -36,28 +36,34 @@ def code_objects(path):
         at = data.find(magic, at + 24)
 
 
-@pytest.fixture(scope="module")
-def kernels(tmp_path_factory):
-    """{name: (vector registers, spilled ones)} of the norm's backward without dropout."""
+def notes(needle, folder):
+    """{name: {noted: value}} of the kernels in the code objects that hold `needle`."""
     if not os.path.exists(_lib.LIB_PATH):
         import __graft_entry__ as g
         g.build()
-    path, out = str(tmp_path_factory.mktemp("co") / "k.co"), {}
+    path, out = str(folder / "k.co"), {}
     for code in code_objects(_lib.LIB_PATH):
-        if b"k_rms_norm_bwd" not in code:
+        if needle.encode() not in code:
             continue
         with open(path, "wb") as f:
             f.write(code)
-        notes = subprocess.run([READELF, "--notes", path], capture_output=True, text=True).stdout
+        text = subprocess.run([READELF, "--notes", path], capture_output=True, text=True).stdout
         cur = {}
-        for line in notes.split("\n"):
-            m = re.match(r"\s+(?:- )?\.(name|vgpr_count|vgpr_spill_count):\s+(\S+)", line)
+        for line in text.split("\n"):
+            m = re.match(r"\s+(?:- )?\.(name|private_segment_fixed_size|vgpr_count|vgpr_spill_count):\s+(\S+)",
+                         line)
             if m:
                 cur[m.group(1)] = m.group(2)
-                if m.group(1) == "vgpr_spill_count":       # the keys are in order: the last
-                    out[cur["name"]] = (int(cur["vgpr_count"]), int(cur["vgpr_spill_count"]))
+                if m.group(1) == "vgpr_spill_count":       # a kernel's keys are in order: the last
+                    name = cur.pop("name")
+                    out[name] = {k: int(v) for k, v in cur.items()}
     plain = subprocess.run(["c++filt"], input="\n".join(out), capture_output=True, text=True).stdout
     return dict(zip((n.replace("flce::(anonymous namespace)::", "") for n in plain.split("\n")), out.values()))
+
+
+@pytest.fixture(scope="module")
+def kernels(tmp_path_factory):
+    return notes("k_rms_norm_bwd", tmp_path_factory.mktemp("co"))
 
 
 # (rows' type, threads, chunks a thread): registers and spilled ones with neither, dw, ds, both
@@ -80,4 +86,5 @@ def test_registers(kernels, which):
         found = {n: v for n, v in kernels.items() if n.startswith(pre)}
         assert found
         for name, got in found.items():
+            got = got["vgpr_count"], got["vgpr_spill_count"]
             assert got[0] <= most[0] and got[1] <= most[1], (name.split("(")[0], got, most)
