@@ -193,10 +193,17 @@ inline int sample_weight_bits(int64_t V) {
 
 // Rows of given logits whose maxima a kernel of its own forms first (parts of 16 chunks of 16
 // bytes): a few long ones, of which top-k or temperature 0 may need no more than those. 0:
-// none. top-p alone reads every logit in any case.
+// none. top-p alone reads every logit in any case. us without and with it, top-50 and greedy:
+//   float32   1 x  32768  15.7 17.4   5.2  7.4      64 x  32768  16.8 19.1   5.7  8.5
+//             1 x  49152  19.1 17.2   7.1  7.4      64 x  49152  20.6 18.7   7.6  8.7
+//             1 x 131072  23.6 18.1  10.1  7.9      64 x 131072  24.8 23.7  11.3 11.9
+//            96 x 131072  28.3 28.1  14.9 16.5      96 x  49152  22.3 19.8   8.8  9.5
+//   bf16      1 x  32768  17.2 19.8   6.6  8.6      64 x  32768  18.2 21.5   6.8  9.3
+//             1 x  49152  20.2 20.0   8.4  8.4      64 x  49152  21.4 21.0   9.0  9.3
+//             1 x 131072  24.1 19.8  10.0  8.5      64 x 131072  25.5 22.5  11.2 10.5
 inline int64_t sample_parts(int64_t N, int64_t V, int dtype) {
   const int64_t part = dtype == kBF16 ? 128 : 64;
-  return N <= 64 && V >= 16384 ? (V + part - 1) / part : 0;
+  return N <= 64 && V >= 49152 ? (V + part - 1) / part : 0;
 }
 
 // Logits of the head form: as many rows at a time as fit these bytes. Their maxima add at most

@@ -25,3 +25,21 @@ def test_more_rows_than_a_grid_takes(V, dt):
         p = m.flce_sample(h[part].contiguous(), W, u[part].contiguous(),
                           temperature=T[part].contiguous(), top_k=5)
         assert torch.equal(p.tokens, r.tokens[part]) and torch.equal(p.logp, r.logp[part])
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [49151, 49152, 49153])
+def test_either_side_of_the_maxima(V, dt):
+    """Up to 64 rows from 49152 logits on have the maxima of their parts formed first: the
+    same rows among more than 64 have not."""
+    import lm_head_linear_amd as m
+    from tests.test_gpu_sample import compare, make, run
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    assert (m.flce_sample_logits_workspace_size(64, V, dt) > 256) == (V >= 49152)
+    assert m.flce_sample_logits_workspace_size(65, V, dt) == 256
+    z, u = make(65, V, dt, V, masked=0.2)
+    for kw in (dict(T=0.7, k=50, p=0.9), dict(T=0.0), dict(k=3, cap=20.0), dict(T=1.2, k=900)):
+        some, all_ = run(z[:64], u[:64], **kw), run(z, u, **kw)
+        assert torch.equal(some.tokens, all_.tokens[:64]) and torch.equal(some.logp, all_.logp[:64])
+        compare(run(z[:2], u[:2], **kw), z[:2], u[:2], **kw)
