@@ -4,9 +4,9 @@
 //
 // Bound by memory (2 or 3 rows of N x H). A thread takes a block of eight columns, the
 // generator's unit (16 bytes of bf16, 32 of float32), or four of them 256 blocks apart
-// where the grid is large. Rows of whole blocks (WHOLE) are loaded without conditions, all
-// before the first is used. 8192 x 4096 bf16: 41 us with the residual (201 MB, 5.0 TB/s), 26
-// without (134 MB); with conditional loads 45 and 32.
+// where the grid is large (kDropMany). Rows of whole blocks (WHOLE) are loaded without
+// conditions, all before the first is used. 8192 x 4096 bf16: 40 us with the residual (201 MB,
+// 5.0 TB/s), 26 without (134 MB); with conditional loads 45 and 32.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>

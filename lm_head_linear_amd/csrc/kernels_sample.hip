@@ -38,7 +38,7 @@
 // counts and three of masses, took 239. Keeping each logit's bin as a byte in LDS, so that
 // collecting reads no memory, gave 97, and 2 us more for rows of 32000: not kept. Top-k is
 // bound by latency: one row of 131072 18 us (4 of them the maxima), 128 bf16 rows of 32000
-// with settings of their own 22 to 28, by the settings drawn.
+// with settings of their own 22 to 30, by the settings drawn.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -56,7 +56,10 @@ constexpr int kThreads = 1024, kWaves = kThreads / 64;
 constexpr int kBins = 2048;                        // of a radix selection's digit
 constexpr int kMassBins = 384;                     // of weights: eighths of 2^-48 .. 1
 constexpr int kWaveList = 256;                     // candidates a wave collects
-constexpr int kSmallList = 256;                    // of a list ranked by counting
+// A list up to this long is ranked by counting, a longer one by digits (us, 1 row of 131072
+// and 256 of 32000 float32: top-50 18 and 24, 23 and 30; top-100 22 and 26, 27 and 31; top-150
+// 27 and 27, 31 and 31; top-250 38 and 29, 41 and 32).
+constexpr int kSmallList = 256;
 constexpr int kMaximaChunks = 4;                   // a thread of k_sample_maxima loads
 constexpr double kLog2eD = 1.4426950408889634074;
 

@@ -40,8 +40,10 @@ struct DropoutArgs {
   int dtype;
 };
 
-// Blocks of eight columns a thread takes, from kDropMany of them: below, the chip has more
-// lanes than blocks.
+// Blocks of eight columns a thread takes, from kDropMany of them, which keeps grids of
+// 2^34 blocks within what one holds. us with four and with one, bf16 with the residual, rows
+// that are in no cache: 2^18 blocks 5.3 and 4.4, 2^20 12.4 and 11.6, 2^21 21.8 and 20.2, 2^22
+// (8192 x 4096) 39.7 and 37.3, 2^23 80 and 73; float32 2^20 21.2 and 20.1, 2^22 78 and 70.
 constexpr int kDropBlocks = 4;
 constexpr int64_t kDropMany = int64_t(1) << 20;
 
@@ -123,16 +125,41 @@ struct LinearBwdArgs {
   int dtype;
 };
 
-// Tiles of 256 x 256 from which a bf16 product runs on the head's tiles.
+// Tiles of 256 x 256 from which a bf16 product runs on the head's tiles, most of a round of the
+// 256 CUs. us on these and on smaller ones, forward to 4096 columns (silu, bias, residual,
+// slope), by tiles:
+//   k  512: 160 44 39, 224 46 51, 256 47 53, 288 83 63, 384 85 77, 512 91 104
+//   k 1024: 160 53 51, 224 55 68, 256 57 70, 288 101 84, 384 103 103, 512 111 137
+//   k 4096: 128 101 90, 160 103 127, 256 120 172, 288 213 210, 384 219 258, 512 242 345
+// and both gradients of I = 2048, N = O: 128 64 55, 160 78 90, 224 114 154, 288 237 243, 384
+// 327 384. Little past a whole round a short k would do better on the smaller ones.
 constexpr int64_t kLinearLargeTiles = 192;
 
-// Rows up to which a forward takes the kernels that read W once, and W's rows from which
-// those are the head's (two workgroups of 64 rows for each CU).
+// Rows up to which a forward takes the kernels that read W once (k_linear_few), and W's rows
+// from which bf16 takes the head's (k_linear_wide, up to kFewTokens rows). us of the few rows'
+// kernel, the wide one and tiles, bf16, k 1024:
+//   W of  4096: 1 row 4.2 7.9 7.3,  16 5.0  8.1 7.7,  48  7.6 18.3  8.7,  64  8.3 20.6 7.4
+//   W of  8192: 1 row 5.4 8.3 7.4,  16 6.8  8.6 7.8,  48 11.8 18.3  8.9,  64 13.4 20.6 7.9
+//   W of 16384: 1 row 9.5 8.6 8.9,  16 12.7 8.8 9.5,  64 25.5 22.9 10.1, 128 - 37.8 12.9
+//   W of 32768: 1 row 20 16 14,     16 26 16 15,      64 46 25 16,       128 - 40 23
+//   W of 49152: 1 row 28 21 30,     16 36 22 32,      64 68 36 41,       128 - 50 51
+// float32 (no wide one): W of 4096 1 row 5.2 and 10.6 on tiles, 32 8.6 10.7, 64 12.7 11.2; W of
+// 16384 15.9 24.6, 32 25.4 26.2, 64 41.7 25.8. Between a W of about 8192 and 40000 rows, and
+// near 64 rows of x, tiles would do better.
 constexpr int64_t kLinearFew = 64, kLinearWide = 32768;
 
-// Tiles of 128 x 128 from which a product takes those (others: of 64 x 64).
+// Tiles of 128 x 128 from which a product takes those (others: of 64 x 64): one and a half
+// rounds of the CUs. us on tiles of 128 and of 64, to 2048 columns, by tiles of 128:
+//   bf16, k 512: 128 13.6 8.6, 256 15.5 15.8, 320 25.9 19.6, 448 27.3 24.7, 512 28.9 27.7
+//   bf16, k 2048: 128 26 19, 256 29 34, 320 49 42, 448 51 56, 512 55 61
+//   bf16, gradients of I = 1024: 128 25 16, 256 33 39, 320 62 58, 448 85 101, 512 102 131
+//   float32, k 512: 128 43 27, 256 45 47, 320 83 57, 448 84 76, 512 85 85
+//   float32, k 2048: 256 139 159, 320 271 186, 448 273 256, 512 274 289
 constexpr int64_t kLinearWholeTiles = 384;
-// ... and of float32, below which it takes tiles of 32 x 32.
+// ... and of float32, below which it takes tiles of 32 x 32. us on tiles of 64 and of 32, to
+// 512 columns, by tiles of 128: k 256: 16 9.2 5.3, 32 9.7 7.3, 48 10.1 9.2, 64 10.5 10.9, 128
+// 16.5 17.2; k 1024: 16 24 11, 48 25 21, 64 25 26, 128 42 47; gradients of I = 256: 32 26 23,
+// 48 44 38, 64 56 58, 128 188 209.
 constexpr int64_t kLinearQuarterTiles = 64;
 
 // A gradient's product of rows x cols over k: split along k into segments of `seg` (a multiple
