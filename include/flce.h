@@ -657,7 +657,8 @@ int flce_dropout_norm_backward(const void* dy, int64_t ld_dy, const void* ds, in
  *   z = x . weight^T + bias,  y = round(act(z) + residual)
  * for N rows of I values, weight [O,I], bias [O] and residual [N,O] (either may be NULL).
  * x, weight, bias and residual are of `dtype`; y is of `y_dtype`: `dtype`, or float32
- * with bf16 rows; slope is float32 with float32 rows and IEEE half (float16) with bf16. With z in float32, act is one of
+ * with bf16 rows; slope is float32 with float32 rows and IEEE half (float16) with bf16
+ * (slopes below 2^-14 are multiples of 2^-24). With z in float32, act is one of
  *   NONE z;  RELU max(z, 0);  GELU z Phi(z);  GELU_TANH z (1 + tanh(sqrt(2/pi) (z +
  *   0.044715 z^3))) / 2;  SILU z / (1 + exp(-z))
  * slope [N,O] (dense; NULL: not wanted) gets round(act'(z)), which the backward reads
@@ -756,7 +757,8 @@ int flce_sample_logits(const void* logits, int64_t ld_logits, int64_t N, int64_t
  * flce_sample -- flce_sample_logits of the logits z = h . W^T (float32) of the head W [V,H]
  * at N rows h [N,H] (dense, `dtype`). The logits live in the workspace, as many rows at a
  * time as fit 512 MiB with their maxima and one grid (2^22 - 1; N itself may be larger):
- * flce_sample_workspace_size bytes (0 for invalid sizes), 256-byte aligned. Errors as flce_sample_logits and flce_linear, and FLCE_ERR_WORKSPACE.
+ * flce_sample_workspace_size bytes (0 for invalid sizes), 256-byte aligned. Errors as
+ * flce_sample_logits and flce_linear, and FLCE_ERR_WORKSPACE.
  */
 size_t flce_sample_workspace_size(int64_t N, int64_t H, int64_t V, int dtype);
 int flce_sample_check_args(const void* h, const void* W, int64_t N, int64_t H, int64_t V,

@@ -40,8 +40,8 @@ def flce_linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tens
     """act(x weight^T + bias) + residual for x [N, I], weight [O, I]: (y, slope).
 
     ``slope`` is the activation's derivative (float32, or float16 with bf16 rows), which
-    :func:`flce_linear_backward` takes: formed with ``save_slope`` (or where a tensor for it is passed in), otherwise None, and
-    None without an activation. y has x's type, or float32 with ``y_dtype``; ``y`` may be
+    :func:`flce_linear_backward` takes: formed with ``save_slope`` (or where a tensor for it is
+    passed in), otherwise None, and None without an activation. y has x's type, or float32 with ``y_dtype``; ``y`` may be
     the residual (in place).
     """
     if x.dim() != 2 or weight.dim() != 2:

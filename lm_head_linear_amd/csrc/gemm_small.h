@@ -1,8 +1,9 @@
 // A matrix product on CDNA4 matrix cores (gfx950) for rows of any length, stride and
 // alignment, bf16 or float32: C[m][n] = sum_k B(m, k) A(n, k) in float32, tiles of TS x TS
 // (128, or 64 where those leave CUs without work, and 32 of float32, whose matrix
-// instruction is sixteen times slower than its loads are short). The head's product (gemm_bf16.h) takes 256 x 256 tiles of aligned bf16 rows; this
-// one serves what that does not: float32, odd rows, and outputs of too few such tiles.
+// instruction is sixteen times slower than its loads are short). The head's product
+// (gemm_bf16.h) takes 256 x 256 tiles of aligned bf16 rows; this one serves what that does
+// not: float32, odd rows, and outputs of too few such tiles.
 //
 // A's rows are C's columns, so that a lane of the matrix instruction's result holds four
 // consecutive columns of one row of C: bias, residual and output move 8 or 16 bytes a lane
